@@ -296,6 +296,170 @@ lla_status lla_decode_attn_decoupled(const lla_dims* dims, int loop_t, int d_rop
                                      float* out, float* lse,
                                      void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * RoPE as operators of its own, beside the rotation that the decode calls fuse.
+ *
+ * lla_rope_scaling — frequencies for contexts beyond the trained one; with
+ * theta_f = rope_base^(-2f/d_head), f < d_head/2:
+ *   LLA_ROPE_PLAIN     theta_f
+ *   LLA_ROPE_LINEAR    theta_f / factor                      (positions interpolated)
+ *   LLA_ROPE_BASE      rope_base scaled by factor^(d/(d-2))  (d_head >= 4)
+ *   LLA_ROPE_BY_PARTS  with r = original_len theta_f / 2 pi turns over the original
+ *                      context and g = clamp((r - slow) / (fast - slow), 0, 1):
+ *                      (1 - g) theta_f / factor + g theta_f; fast > slow >= 0,
+ *                      original_len >= 1
+ * factor > 0.  A field that the kind does not use is ignored.
+ */
+typedef enum {
+    LLA_ROPE_PLAIN = 0,
+    LLA_ROPE_LINEAR = 1,
+    LLA_ROPE_BASE = 2,
+    LLA_ROPE_BY_PARTS = 3
+} lla_rope_scaling_kind;
+
+typedef struct {
+    int kind;                   /* lla_rope_scaling_kind                   */
+    double factor;
+    int64_t original_len;
+    double fast, slow;
+} lla_rope_scaling;
+
+/*
+ * lla_rope_table_scaled — a RoPE table built on the GPU: row i gets cos and sin of
+ * (pos0 + i) theta_f for f < d_head/2.  Rows have the layout of lla_rope_table (whose
+ * values it equals to about 1 ulp with scaling NULL or LLA_ROPE_PLAIN), so with pos0 = 0
+ * the result serves every call that takes a RoPE table.  Angles are exact products in
+ * 64-bit fixed point: positions up to 2^31 lose no precision.
+ *   scaling              host; NULL: plain
+ *   rope_cos, rope_sin   device fp32 [n_pos][d_head/2], 16-byte aligned
+ * Of lla_dims only rope_base and d_head (even, 2..256) are used.  pos0 and n_pos are
+ * at most 2^31.  Asynchronous on `stream`.
+ */
+lla_status lla_rope_table_scaled(const lla_dims* dims, const lla_rope_scaling* scaling, int64_t pos0,
+                                 int64_t n_pos, float* rope_cos, float* rope_sin, void* stream);
+
+/*
+ * lla_rope_apply — rotate elements offset .. offset+d_rope-1 of every head's vector by
+ * its token's position and scale them; the other elements pass through:
+ *     out = scale * RoPE(x, pos)            (inverse == 0)
+ *     out = scale * RoPE(x, -pos)           (inverse != 0: the gradient of the former
+ *                                            with respect to x, given out's gradient as x)
+ * Pairs are those of lla_dims.rope_style within the d_rope elements.  `scale` is for the
+ * attention factor that some scalings put on the rotated part; 1 for a plain rotation.
+ *   x, out     device  element (n, h, e) at n*tok_stride + h*head_stride + e, e < d_x
+ *                      (strides in elements, so a slice of a fused projection is taken as it
+ *                      is); storage dtype; aligned to an element (16-byte alignment of
+ *                      bases, strides, offset, d_rope/2 and d_x is faster)
+ *   pos        device  int32 [N]; outside [0, rope_len) is clamped and records
+ *                      LLA_ERR_DEVICE_ARG
+ *   rope_cos/_sin      device fp32 [rope_len][d_rope/2]
+ *   workspace          device, >= 256 bytes: the status word
+ * out == x with the same strides rotates in place (only the rotated part is written);
+ * other overlaps return LLA_ERR_INVALID_ARG, but two slices of one buffer with equal strides
+ * whose rows lie apart within a token are no overlap.  Rows of `out` must not overlap each
+ * other.  Arithmetic in fp32, rounded once.  Of lla_dims only dtype and rope_style are used.
+ */
+lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_stride, int64_t x_head_stride,
+                          void* out, int64_t out_tok_stride, int64_t out_head_stride, int N, int heads,
+                          int d_x, int offset, int d_rope, const int32_t* pos, const float* rope_cos,
+                          const float* rope_sin, int64_t rope_len, float scale, int inverse,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * lla_page_plan — the block tables and slot maps of one step, built on the GPU from the
+ * requests' lengths and a list of free pages ("Enabling dynamic computation in Looped
+ * LMs", Appendix A.1).  Request b holds ctx_lens[b] cached tokens, in pages that its
+ * table row names already, and brings new_lens[b] more.  Its new tokens are numbered from
+ * tok_start[b] = sum of new_lens before b, the order in which the step's activations are
+ * packed.  A request is granted if its table row can hold all of its tokens
+ * (ctx + new <= max_pages * page_size), its tokens lie below n_tok, and the free pages
+ * reach it: pages are handed out in request order, and the first request that they do
+ * not suffice for ends the hand-out for every later one that needs a page (requests whose
+ * last page has room are still granted).
+ *   ctx_lens, new_lens  device int32 [B]       a negative value counts as 0 and records
+ *                                              LLA_ERR_DEVICE_ARG
+ *   free_pages          device int32 [n_free]  physical pages, taken from free_head on
+ *   free_head           device int32 [1] or NULL (0): entries already taken; outside
+ *                                              [0, n_free] counts as n_free, flagged
+ *   block_table         device int32 [B][max_pages], updated: the entries of the pages
+ *                                              that granted requests take; no other
+ *   seq_lens            device int32 [B]       out: ctx + new where granted, else ctx
+ *   tok_start           device int32 [B+1]     out; entry B is the sum (saturating)
+ *   granted             device int32 [B]       out: 1 or 0
+ *   seq_idx, pos        device int32 [n_tok]   out: request and position of token n, as
+ *                                              lla_encode_paged takes them
+ *   slots               device int64 [n_tok]   out: physical page * page_size + row, as
+ *                                              lla_q4_store takes them
+ *                                              (entries of no granted token: -1 in all three)
+ *   counts              device int32 [2]       out: the next call's free_head; tokens granted
+ *   workspace           device, >= 256 bytes: the status word
+ * A table or free-list entry outside [0, num_pages) that a token falls on records
+ * LLA_ERR_DEVICE_ARG and its slot is -1.  No output may overlap an input (a step's
+ * seq_lens become the next step's ctx_lens by alternating two arrays).  B <= 8192,
+ * max_pages * page_size <= 2^30; else LLA_ERR_UNSUPPORTED.
+ */
+lla_status lla_page_plan(int B, int page_size, int max_pages, int64_t num_pages, const int32_t* ctx_lens,
+                         const int32_t* new_lens, const int32_t* free_pages, int n_free,
+                         const int32_t* free_head, int32_t* block_table, int32_t* seq_lens,
+                         int32_t* tok_start, int32_t* granted, int n_tok, int32_t* seq_idx, int32_t* pos,
+                         int64_t* slots, int32_t* counts, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A paged per-head latent cache held in 4 bits (device): rows [num_pages][H][page_size]
+ * of lla_q4_row_bytes() bytes, one per token and head with its K and its V latent:
+ * K codes, V codes, one bf16 scale per 32 columns (the last group of a rank may have
+ * 16) of K, then of V, zero padding to 16 bytes.  Eight columns make a 32-bit word;
+ * column c of a word is bits 4(c/2) + 16(c mod 2) .. +3, holding code + 8 with code in
+ * [-7, 7]; the latent is code * scale.  At (r_k, r_v) = (96, 160) a row is 144 bytes
+ * against 512 in bf16, at (16, 32) 32 against 96.  block_table as in lla_paged_cache;
+ * lla_q4_store and lla_q4_load use only rows, page_size and num_pages.
+ */
+typedef struct {
+    void* rows;
+    const int32_t* block_table;
+    int B;
+    int max_pages;
+    int page_size;
+    int64_t num_pages;
+} lla_q4_cache;
+
+/* Bytes of a row (a multiple of 16); 0 for invalid dims and LLA_2D. */
+size_t lla_q4_row_bytes(const lla_dims* dims);
+
+/*
+ * lla_q4_store / lla_q4_load — round N tokens' latents into 4-bit rows, and read rows
+ * back as latents.  Per group of 32 columns scale = bf16(max|c| / 7) and
+ * code = round(c / scale), half to even, both divisions in fp32; a group of zeros has
+ * scale 0, a group with a value that is not finite reads back as NaN.
+ *   c_k, c_v   device  [N][H][r_k], [N][H][r_v] in the storage dtype: what lla_encode
+ *                      writes into a cache of B = N sequences and L_max = 1
+ *   slots      device  int64 [N]: physical page * page_size + row within it, as made by
+ *                      lla_page_plan; a negative slot is skipped (a load leaves that
+ *                      token's output as it is), one beyond the pool is skipped and
+ *                      records LLA_ERR_DEVICE_ARG; two tokens storing to one slot race
+ *   workspace  device, >= 256 bytes: the status word
+ * A load rounds code * scale to the storage dtype.  LLA_PER_HEAD only.
+ */
+lla_status lla_q4_store(const lla_dims* dims, const void* c_k, const void* c_v, int N, const int64_t* slots,
+                        const lla_q4_cache* cache, void* workspace, size_t ws_bytes, void* stream);
+lla_status lla_q4_load(const lla_dims* dims, const int64_t* slots, int N, const lla_q4_cache* cache,
+                       void* c_k, void* c_v, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * lla_decode_attn_q4 — lla_decode_attn_paged over a 4-bit cache: the same attention of the
+ * latents that the rows stand for.  `out` is [B][H][d] in the storage dtype (rounded
+ * once); `lse` may be NULL.  Everything else as lla_decode_attn_paged, with a workspace of
+ * lla_q4_workspace_size() bytes (L_max = max_pages * page_size), the first 256 zero.  A row
+ * with a NaN scale makes its sequence-head's result NaN.
+ */
+size_t lla_q4_workspace_size(const lla_dims* dims, int B, int64_t L_max);
+lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, const lla_q4_cache* cache,
+                              const int32_t* seq_lens, const int32_t* q_pos,
+                              const void* w_up_k, const void* w_up_v,
+                              const float* mu_k, const float* mu_v,
+                              const float* rope_cos, const float* rope_sin, int64_t rope_len,
+                              void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+
 /* Size of the fixed scratch array behind lla_decode_attn_noalloc (64 MiB). */
 #define LLA_NOALLOC_SCRATCH_BYTES (64u << 20)
 

@@ -168,6 +168,13 @@ int sm_count() {
 
 }  // namespace
 
+namespace lla {
+
+lla_status checked_dims(const lla_dims* dims) { return check_dims(dims); }
+int device_sm_count() { return sm_count(); }
+
+}  // namespace lla
+
 extern "C" {
 
 int lla_abi_version(void) { return LLA_ABI_VERSION; }

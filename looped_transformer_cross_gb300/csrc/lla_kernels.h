@@ -354,6 +354,11 @@ cudaError_t launch_encode_bf16(const EncodeArgs& a, const EncodePlan& plan, cons
                                cudaStream_t s);
 cudaError_t launch_encode_f32(const EncodeArgs& a, cudaStream_t s);
 
+// ----------------------------------------------------------------- host checks
+// (lla_api.cu) the checks of dims that every call makes, and the current device's SM count
+lla_status checked_dims(const lla_dims* dims);
+int device_sm_count();
+
 // ----------------------------------------------------------------- scratch without allocation
 
 // Device address of the library's fixed scratch array on the current device (looked

@@ -1,0 +1,64 @@
+// lla_q4.h — the 4-bit latent row shared by the kernels that write it (lla_q4.cu) and
+// the ones that attend over it (lla_q4.cu, lla_q4_decode.cu).
+//
+// A row holds one token of one head, K and V together, so that one bulk copy per page
+// brings a whole head-tile:
+//   [0, r_k/2)           K codes, 8 columns per 32-bit word
+//   [r_k/2, (r_k+r_v)/2) V codes
+//   then bf16 scales, one per 32 columns of K, then of V; zero padding to 16 bytes.
+// Column c of a word (c < 8) sits at bit 4(c/2) + 16(c mod 2) as code + 8: a word's two
+// halves hold its even and its odd columns, so one mask yields a pair of neighbouring
+// columns as two half-words.  Value = code * scale, code in [-7, 7].
+#pragma once
+
+#include "lla_kernels.h"
+
+namespace lla {
+
+constexpr int kQ4Group = 32;          // columns that share a scale
+
+__host__ __device__ inline int q4_groups(int r) { return (r + kQ4Group - 1) / kQ4Group; }
+__host__ __device__ inline int q4_scale_offset(int r_k, int r_v) { return (r_k + r_v) / 2; }
+__host__ __device__ inline int q4_row_bytes(int r_k, int r_v) {
+  return ((r_k + r_v) / 2 + 2 * (q4_groups(r_k) + q4_groups(r_v)) + 15) / 16 * 16;
+}
+
+struct Q4DecodeArgs {
+  int B, H, r_k, r_v, rope_style;
+  int row_bytes;
+  int64_t L_max, rope_len, mu_hstride;
+  const void* q;                     // [B][H][128] storage dtype
+  const uint8_t* rows;               // pool [num_pages][H][page_size][row_bytes]
+  const int32_t* block_table;        // [B][max_pages]
+  int page_size, max_pages;
+  int64_t num_pages;
+  const int32_t* seq_lens;           // [B]
+  const int32_t* q_pos;              // [B]
+  const void* w_up_k;                // loop-t slice [H][128][r_k]
+  const void* w_up_v;                // loop-t slice [H][128][r_v]
+  const float* mu_k;                 // loop-t slice: element (h, e) at mu_k[h*mu_hstride + e]
+  const float* mu_v;
+  const float* rope_cos;             // [rope_len][64]
+  const float* rope_sin;
+  void* out;                         // [B][H][128] storage dtype
+  float* lse;                        // [B][H], or nullptr
+  uint32_t* status;
+  float* records;                    // split records: {m (log2 units), l, -, -, acc[r_v]}
+  int64_t chunk;                     // plain kernel: tokens of a split
+  int splits;                        // plain kernel: splits of a (sequence, head)
+};
+
+// Tokens per split of the plain kernel: enough splits for two blocks per SM, whole tiles.
+int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms);
+cudaError_t launch_q4_plain(const Q4DecodeArgs& a, bool bf16, cudaStream_t s);
+
+// Opt the kernel in to `smem` bytes of dynamic shared memory on the current device.
+// Set at every launch: the attribute belongs to a device's copy of the kernel, and a
+// process may use several.
+template <typename K>
+cudaError_t allow_smem(K* kern, size_t smem) {
+  if (smem <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+}
+
+}  // namespace lla

@@ -25,6 +25,7 @@ LIB_PATH = os.path.join(_PKG, "lib", "liblla.so")
 LLA_BF16, LLA_F32 = 0, 1
 LLA_PER_HEAD, LLA_2D = 0, 1
 LLA_ROPE_HALF, LLA_ROPE_INTERLEAVED = 0, 1
+LLA_ROPE_PLAIN, LLA_ROPE_LINEAR, LLA_ROPE_BASE, LLA_ROPE_BY_PARTS = range(4)
 
 
 class Dims(ctypes.Structure):
@@ -42,6 +43,16 @@ class PagedCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("num_pages", ctypes.c_int64)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original_len", ctypes.c_int64),
+                ("fast", ctypes.c_double), ("slow", ctypes.c_double)]
+
+
+class Q4Cache(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int64)]
 
 
 class LLAError(RuntimeError):
@@ -95,6 +106,27 @@ def lib():
             L.lla_decode_attn_noalloc.restype = ctypes.c_int
             L.lla_evict_window.argtypes = [pd, Cache, i32p, ctypes.c_int, ctypes.c_int, vp, ctypes.c_size_t, vp]
             L.lla_evict_window.restype = ctypes.c_int
+            i32, i64, sz, i64p = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+            pq = ctypes.POINTER(Q4Cache)
+            L.lla_rope_table_scaled.argtypes = [pd, ctypes.POINTER(RopeScaling), i64, i64, fp, fp, vp]
+            L.lla_rope_table_scaled.restype = ctypes.c_int
+            L.lla_rope_apply.argtypes = [pd, vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, i32, i32p, fp, fp, i64,
+                                         ctypes.c_float, i32, vp, sz, vp]
+            L.lla_rope_apply.restype = ctypes.c_int
+            L.lla_page_plan.argtypes = [i32, i32, i32, i64, i32p, i32p, i32p, i32, i32p, i32p, i32p, i32p, i32p, i32,
+                                        i32p, i32p, i64p, i32p, vp, sz, vp]
+            L.lla_page_plan.restype = ctypes.c_int
+            L.lla_q4_row_bytes.argtypes = [pd]
+            L.lla_q4_row_bytes.restype = sz
+            L.lla_q4_store.argtypes = [pd, vp, vp, i32, i64p, pq, vp, sz, vp]
+            L.lla_q4_store.restype = ctypes.c_int
+            L.lla_q4_load.argtypes = [pd, i64p, i32, pq, vp, vp, vp, sz, vp]
+            L.lla_q4_load.restype = ctypes.c_int
+            L.lla_q4_workspace_size.argtypes = [pd, i32, i64]
+            L.lla_q4_workspace_size.restype = sz
+            L.lla_decode_attn_q4.argtypes = [pd, i32, vp, pq, i32p, i32p, vp, vp, fp, fp, fp, fp, i64, vp, fp,
+                                             vp, sz, vp]
+            L.lla_decode_attn_q4.restype = ctypes.c_int
             L.lla_decode_kernel.argtypes = [pd]
             L.lla_decode_kernel.restype = ctypes.c_char_p
             L.lla_decoupled_kernel.argtypes = [pd, ctypes.c_int]
@@ -319,3 +351,206 @@ def decode_attn_noalloc(dm: Dims, loop_t: int, q, cache_k, cache_v, seq_lens, q_
            _ptr(w_up_v), _ptr(mu_k), _ptr(mu_v), _ptr(rope_cos), _ptr(rope_sin),
            int(rope_cos.shape[0]), _ptr(out), _ptr(lse), _stream(stream))
     _check(st, "lla_decode_attn_noalloc")
+
+
+# ---------------------------------------------------------------- RoPE operators, page plans, the 4-bit cache
+#
+# These calls check what they are given (types, shapes, one device) before they pass
+# pointers on, and run on the tensors' own device: its current stream unless `stream` is given.
+
+def _need(cond: bool, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(name: str, t, dtype, device, shape=None):
+    """Check one argument tensor (None in ``shape``: any extent); returns its pointer."""
+    _need(isinstance(t, torch.Tensor), name + " must be a tensor")
+    _need(t.dtype == dtype, "%s must be %s, not %s" % (name, dtype, t.dtype))
+    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
+    if shape is not None:
+        _need(t.dim() == len(shape) and all(w is None or w == g for w, g in zip(shape, t.shape)),
+              "%s has shape %s, not %s" % (name, tuple(t.shape), tuple("*" if w is None else w for w in shape)))
+    return _ptr(t)
+
+
+def _workspace(t, device):
+    _need(t is not None and t.is_cuda and t.device == device, "the workspace must be on %s" % (device,))
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _storage(dm: Dims):
+    return torch.bfloat16 if dm.dtype == LLA_BF16 else torch.float32
+
+
+def _run(device, stream, f, *args):
+    """Call f(*args, stream) with ``device`` current."""
+    _need(device.type == "cuda", "the tensors must be on a CUDA device, not on %s" % (device,))
+    if stream is not None:
+        _need(stream.device == device, "the stream is of %s, not of %s" % (stream.device, device))
+    if device.index == torch.cuda.current_device():
+        return f(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return f(*args, _stream(stream))
+
+
+_SCALINGS = {"plain": LLA_ROPE_PLAIN, "linear": LLA_ROPE_LINEAR, "base": LLA_ROPE_BASE, "by_parts": LLA_ROPE_BY_PARTS}
+
+
+def rope_scaling(kind="plain", factor=1.0, original_len=0, fast=32.0, slow=1.0) -> RopeScaling:
+    """An lla_rope_scaling: ``kind`` is "plain", "linear", "base" or "by_parts"."""
+    _need(kind in _SCALINGS, "unknown scaling %r" % (kind,))
+    return RopeScaling(_SCALINGS[kind], float(factor), int(original_len), float(fast), float(slow))
+
+
+def rope_table_scaled(dm: Dims, n_pos: int, scaling: Optional[RopeScaling] = None, pos0: int = 0, cos=None, sin=None,
+                      device=None, stream=None):
+    """lla_rope_table_scaled: (cos, sin) fp32 [n_pos][d_head/2] built on the GPU, for positions
+    pos0 .. pos0 + n_pos - 1."""
+    shape = (int(n_pos), dm.d_head // 2)
+    _need((cos is None) == (sin is None), "give both outputs or neither")
+    if cos is None:
+        cos = torch.empty(shape, dtype=torch.float32, device="cuda" if device is None else device)
+        sin = torch.empty_like(cos)
+    pc = _tensor("cos", cos, torch.float32, cos.device, shape)
+    ps = _tensor("sin", sin, torch.float32, cos.device, shape)
+    st = _run(cos.device, stream, lib().lla_rope_table_scaled, ctypes.byref(dm),
+              None if scaling is None else ctypes.byref(scaling), int(pos0), int(n_pos), pc, ps)
+    _check(st, "lla_rope_table_scaled")
+    return cos, sin
+
+
+def rope_apply(dm: Dims, x, pos, rope_cos, rope_sin, out=None, offset: int = 0, scale: float = 1.0,
+               inverse: bool = False, workspace=None, stream=None):
+    """lla_rope_apply: rotate 2 * rope_cos.shape[1] elements of every head's vector of ``x``
+    [N][heads][d_x], from element ``offset`` on; ``out`` may be ``x`` (in place) and is
+    returned.  Token and head strides are free, a head's vector is contiguous."""
+    _need(x.dim() == 3, "x must be [N][heads][d_x]")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    sd, dev = _storage(dm), x.device
+    for name, t in (("x", x), ("out", out)):
+        _need(t.dtype == sd and t.device == dev and t.shape == x.shape,
+              "%s must be %s of shape %s on %s" % (name, sd, tuple(x.shape), dev))
+        _need(t.shape[2] <= 1 or t.stride(2) == 1, name + ": a head's vector must be contiguous")
+    N, heads, d_x = (int(n) for n in x.shape)
+    half = int(rope_cos.shape[1])
+    pc = _tensor("rope_cos", rope_cos, torch.float32, dev, (None, half))
+    ps = _tensor("rope_sin", rope_sin, torch.float32, dev, rope_cos.shape)
+    pp = _tensor("pos", pos, torch.int32, dev, (N,))
+    ws, wb = _workspace(workspace, dev)
+    st = _run(dev, stream, lib().lla_rope_apply, ctypes.byref(dm), x.data_ptr(), x.stride(0), x.stride(1),
+              out.data_ptr(), out.stride(0), out.stride(1), N, heads, d_x, int(offset), 2 * half, pp, pc, ps,
+              int(rope_cos.shape[0]), float(scale), 1 if inverse else 0, ws, wb)
+    _check(st, "lla_rope_apply")
+    return out
+
+
+class PagePlan:
+    """Output arrays and status word of lla_page_plan for B requests and at most ``n_tok``
+    new tokens; calling it plans one step into them (``block_table`` is updated in place).
+
+    ``seq_lens`` [B], ``tok_start`` [B + 1], ``granted`` [B], ``seq_idx``, ``pos``, ``slots``
+    (int64) [n_tok], ``counts`` [2] (the next call's ``free_head``; tokens granted).
+    """
+
+    def __init__(self, B: int, n_tok: int, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.B, self.n_tok = int(B), int(n_tok)
+        self.seq_lens, self.granted = torch.empty(self.B, **i32), torch.empty(self.B, **i32)
+        self.tok_start, self.counts = torch.empty(self.B + 1, **i32), torch.empty(2, **i32)
+        self.seq_idx, self.pos = torch.empty(self.n_tok, **i32), torch.empty(self.n_tok, **i32)
+        self.slots = torch.empty(self.n_tok, dtype=torch.int64, device=device)
+        self.workspace = torch.zeros(256, dtype=torch.uint8, device=device)
+        self._out = [_ptr(t) for t in (self.seq_lens, self.tok_start, self.granted)]
+        self._map = [_ptr(t) for t in (self.seq_idx, self.pos, self.slots, self.counts, self.workspace)]
+
+    def __call__(self, page_size: int, num_pages: int, ctx_lens, new_lens, free_pages, block_table, free_head=None,
+                 stream=None):
+        dev = self.counts.device
+        pc = _tensor("ctx_lens", ctx_lens, torch.int32, dev, (self.B,))
+        pn = _tensor("new_lens", new_lens, torch.int32, dev, (self.B,))
+        pf = _tensor("free_pages", free_pages, torch.int32, dev, (None,))
+        pt = _tensor("block_table", block_table, torch.int32, dev, (self.B, None))
+        ph = None if free_head is None else _tensor("free_head", free_head, torch.int32, dev, (1,))
+        st = _run(dev, stream, lib().lla_page_plan, self.B, int(page_size), int(block_table.shape[1]), int(num_pages),
+                  pc, pn, pf, int(free_pages.shape[0]), ph, pt, *self._out, self.n_tok, *self._map, 256)
+        _check(st, "lla_page_plan")
+        return self
+
+
+def q4_row_bytes(dm: Dims) -> int:
+    """Bytes of one token-head's row of the 4-bit cache."""
+    n = lib().lla_q4_row_bytes(ctypes.byref(dm))
+    if n == 0:
+        raise LLAError(LLA_ERR_UNSUPPORTED, "lla_q4_row_bytes")
+    return int(n)
+
+
+def q4_pool(dm: Dims, num_pages: int, page_size: int, device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit pool [num_pages][H][page_size][row bytes] (uint8)."""
+    return torch.zeros((int(num_pages), dm.H, int(page_size), q4_row_bytes(dm)), dtype=torch.uint8, device=device)
+
+
+def q4_workspace(dm: Dims, B: int, L_max: int, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for lla_decode_attn_q4 (L_max = max_pages * page_size)."""
+    with torch.cuda.device(device):
+        n = lib().lla_q4_workspace_size(ctypes.byref(dm), int(B), int(L_max))
+    if n == 0:
+        raise LLAError(LLA_ERR_INVALID_ARG, "lla_q4_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _q4_cache(dm: Dims, pool, block_table=None) -> Q4Cache:
+    rb = lib().lla_q4_row_bytes(ctypes.byref(dm))
+    rows = _tensor("pool", pool, torch.uint8, pool.device, (None, dm.H, None, rb))
+    c = Q4Cache(rows, None, 0, 1, int(pool.shape[2]), int(pool.shape[0]))
+    if block_table is not None:
+        c.block_table = _tensor("block_table", block_table, torch.int32, pool.device, (None, None))
+        c.B, c.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
+    return c
+
+
+def q4_store(dm: Dims, c_k, c_v, slots, pool, workspace, stream=None):
+    """lla_q4_store: latents c_k [N][H][r_k], c_v [N][H][r_v] rounded to 4 bits into the
+    pool's rows at ``slots`` [N] (int64, as lla_page_plan makes them)."""
+    dev, N = pool.device, int(slots.shape[0])
+    c = _q4_cache(dm, pool)
+    pk = _tensor("c_k", c_k, _storage(dm), dev, (N, dm.H, dm.r_k))
+    pv = _tensor("c_v", c_v, _storage(dm), dev, (N, dm.H, dm.r_v))
+    ws, wb = _workspace(workspace, dev)
+    st = _run(dev, stream, lib().lla_q4_store, ctypes.byref(dm), pk, pv, N,
+              _tensor("slots", slots, torch.int64, dev, (N,)), ctypes.byref(c), ws, wb)
+    _check(st, "lla_q4_store")
+
+
+def q4_load(dm: Dims, slots, pool, c_k, c_v, workspace, stream=None):
+    """lla_q4_load: the latents that the pool's rows at ``slots`` stand for, into c_k, c_v."""
+    dev, N = pool.device, int(slots.shape[0])
+    c = _q4_cache(dm, pool)
+    pk = _tensor("c_k", c_k, _storage(dm), dev, (N, dm.H, dm.r_k))
+    pv = _tensor("c_v", c_v, _storage(dm), dev, (N, dm.H, dm.r_v))
+    ws, wb = _workspace(workspace, dev)
+    st = _run(dev, stream, lib().lla_q4_load, ctypes.byref(dm), _tensor("slots", slots, torch.int64, dev, (N,)), N,
+              ctypes.byref(c), pk, pv, ws, wb)
+    _check(st, "lla_q4_load")
+
+
+def decode_attn_q4(dm: Dims, loop_t: int, q, pool, block_table, seq_lens, q_pos, w_up_k, w_up_v, mu_k, mu_v, rope_cos,
+                   rope_sin, out, lse, workspace, stream=None):
+    """lla_decode_attn_q4: latent-store decode attention over a 4-bit paged cache, into ``out``
+    [B][H][d] (storage dtype) and, unless None, ``lse`` [B][H] (fp32)."""
+    dev, sd, T, H, d = pool.device, _storage(dm), dm.T, dm.H, dm.d_head
+    c = _q4_cache(dm, pool, block_table)
+    B = c.B
+    f32, i32 = torch.float32, torch.int32
+    pl = None if lse is None else _tensor("lse", lse, f32, dev, (B, H))
+    ws, wb = _workspace(workspace, dev)
+    st = _run(dev, stream, lib().lla_decode_attn_q4, ctypes.byref(dm), int(loop_t), _tensor("q", q, sd, dev, (B, H, d)),
+              ctypes.byref(c), _tensor("seq_lens", seq_lens, i32, dev, (B,)), _tensor("q_pos", q_pos, i32, dev, (B,)),
+              _tensor("w_up_k", w_up_k, sd, dev, (T, H, d, dm.r_k)), _tensor("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)),
+              _tensor("mu_k", mu_k, f32, dev, (H, T * d)), _tensor("mu_v", mu_v, f32, dev, (H, T * d)),
+              _tensor("rope_cos", rope_cos, f32, dev, (None, d // 2)),
+              _tensor("rope_sin", rope_sin, f32, dev, rope_cos.shape), int(rope_cos.shape[0]),
+              _tensor("out", out, sd, dev, (B, H, d)), pl, ws, wb)
+    _check(st, "lla_decode_attn_q4")
