@@ -147,9 +147,9 @@ __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_consta
   store8(static_cast<T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col, v);
 }
 
-// ----------------------------------------------------------------- plain decode
+// ----------------------------------------------------------------- fp32 decode
 
-// Decode attention over 4-bit rows in fp32 arithmetic for either storage type: one block
+// Decode attention over 4-bit rows for fp32 storage, in fp32 arithmetic: one block
 // per (sequence, head, split of whole 128-token tiles), one token per thread.  The
 // score is Eq. (3) with RoPE after reconstruction, regrouped per frequency pair as in
 // lla_paged_generic.cu, with the folded query in fp32; one online softmax over the
@@ -157,16 +157,12 @@ __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_consta
 constexpr int kPlainThreads = 128;
 constexpr float kPlainScale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 
-__device__ __forceinline__ float as_f32(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float as_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   const int L = __ldg(a.seq_lens + b);
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kPlainThreads) q4_plain_kernel(const __grid_constant__ Q4DecodeArgs a) {
+__global__ void __launch_bounds__(kPlainThreads) q4_f32_kernel(const __grid_constant__ Q4DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float bc[64], bs[64], qr[kHeadDim], pw[kPlainThreads], red[4];
   const int rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
@@ -193,14 +189,14 @@ __global__ void __launch_bounds__(kPlainThreads) q4_plain_kernel(const __grid_co
     i0 = a.rope_style == 0 ? f : 2 * f;
     i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
   };
-  const T* q = static_cast<const T*>(a.q) + u * kHeadDim;
+  const float* q = static_cast<const float*>(a.q) + u * kHeadDim;
   const float* mk = a.mu_k + h * a.mu_hstride;
   if (tid < 64) {
     int i0, i1;
     pair_of(tid, i0, i1);
     const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + tid);
     const float s = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + tid);
-    const float x0 = as_f32(q + i0), x1 = as_f32(q + i1);
+    const float x0 = __ldg(q + i0), x1 = __ldg(q + i1);
     const float q0 = (x0 * c - x1 * s) * kPlainScale, q1 = (x0 * s + x1 * c) * kPlainScale;
     qr[i0] = q0;
     qr[i1] = q1;
@@ -208,12 +204,12 @@ __global__ void __launch_bounds__(kPlainThreads) q4_plain_kernel(const __grid_co
     bs[tid] = q1 * mk[i0] - q0 * mk[i1];
   }
   __syncthreads();
-  const T* W = static_cast<const T*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk;
+  const float* W = static_cast<const float*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk;
   for (int i = tid; i < 64 * rk; i += kPlainThreads) {
     const int f = i / rk, k = i - f * rk;
     int i0, i1;
     pair_of(f, i0, i1);
-    const float w0 = as_f32(W + static_cast<int64_t>(i0) * rk + k), w1 = as_f32(W + static_cast<int64_t>(i1) * rk + k);
+    const float w0 = __ldg(W + static_cast<int64_t>(i0) * rk + k), w1 = __ldg(W + static_cast<int64_t>(i1) * rk + k);
     zc[k * 64 + f] = qr[i0] * w0 + qr[i1] * w1;
     zs[k * 64 + f] = qr[i1] * w0 - qr[i0] * w1;
   }
@@ -309,15 +305,14 @@ __global__ void __launch_bounds__(kPlainThreads) q4_plain_kernel(const __grid_co
 
 // Merge a (sequence, head)'s split records by log-sum-exp, apply W_up,v once (Appendix J
 // "Absorbed attention") and normalise.  Block = (head, sequence), one output per thread.
-template <typename T>
-__global__ void __launch_bounds__(kPlainThreads) q4_plain_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
+__global__ void __launch_bounds__(kPlainThreads) q4_f32_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
   __shared__ float acc[kMaxRankPerHead];
   const int64_t u = blockIdx.x;
   const int b = static_cast<int>(u / a.H), h = static_cast<int>(u - static_cast<int64_t>(b) * a.H), tid = threadIdx.x;
   const int L = q4_len(a, b), rv = a.r_v;
-  T* out = static_cast<T*>(a.out) + u * kHeadDim;
+  float* out = static_cast<float*>(a.out) + u * kHeadDim;
   if (L == 0) {
-    out[tid] = T(0.f);
+    out[tid] = 0.f;
     if (tid == 0 && a.lse) a.lse[u] = -INFINITY;
     return;
   }
@@ -336,7 +331,7 @@ __global__ void __launch_bounds__(kPlainThreads) q4_plain_combine_kernel(const _
   for (int half = 0; half < 2; ++half)
     if (tid + half * kPlainThreads < rv) acc[tid + half * kPlainThreads] = v[half];
   __syncthreads();
-  const T* W = static_cast<const T*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * rv;
+  const float* W = static_cast<const float*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * rv;
   float o = 0.f;
   for (int k = 0; k < rv; k += 8) {
     float w8[8];
@@ -344,25 +339,22 @@ __global__ void __launch_bounds__(kPlainThreads) q4_plain_combine_kernel(const _
 #pragma unroll
     for (int e = 0; e < 8; ++e) o = fmaf(acc[k + e], w8[e], o);
   }
-  const float y = o / l + a.mu_v[h * a.mu_hstride + tid];
-  if constexpr (sizeof(T) == 2) out[tid] = __float2bfloat16_rn(y);
-  else out[tid] = y;
+  out[tid] = o / l + a.mu_v[h * a.mu_hstride + tid];
   if (tid == 0 && a.lse) a.lse[u] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <typename T>
-cudaError_t launch_plain(const Q4DecodeArgs& a, cudaStream_t s) {
+}  // namespace
+
+cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(a.r_k) * 512 + static_cast<size_t>(kPlainThreads) * (a.row_bytes + 16);
-  cudaError_t e = allow_smem(q4_plain_kernel<T>, smem);
+  cudaError_t e = allow_smem(q4_f32_kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * a.H;
-  q4_plain_kernel<T><<<static_cast<unsigned>(units * a.splits), kPlainThreads, smem, s>>>(a);
+  q4_f32_kernel<<<static_cast<unsigned>(units * a.splits), kPlainThreads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  q4_plain_combine_kernel<T><<<static_cast<unsigned>(units), kPlainThreads, 0, s>>>(a);
+  q4_f32_combine_kernel<<<static_cast<unsigned>(units), kPlainThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
-
-}  // namespace
 
 int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms) {
   const int64_t tiles = (L_max + kTile - 1) / kTile, units = static_cast<int64_t>(B) * H;
@@ -370,9 +362,6 @@ int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms) {
   return (tiles + std::min(want, tiles) - 1) / std::min(want, tiles) * kTile;
 }
 
-cudaError_t launch_q4_plain(const Q4DecodeArgs& a, bool bf16, cudaStream_t s) {
-  return bf16 ? launch_plain<__nv_bfloat16>(a, s) : launch_plain<float>(a, s);
-}
 
 }  // namespace lla
 
@@ -436,11 +425,31 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
   return LLA_OK;
 }
 
-size_t q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
-  const int64_t tiles = (L_max + kTile - 1) / kTile;
+// Workspace of a decode call: status word; tensor-core kernel: the CTA range of every
+// (sequence, head group), then a record per head of every (unit, CTA) of a run (at most
+// units + grid of them); fp32 kernel: a record per split.
+struct Q4Ws {
+  size_t ranges, records, total;
+  int grid;
+};
+Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
+  Q4Ws w{};
+  const int64_t tiles = std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
+  const size_t rec = static_cast<size_t>(d->r_v + kRecordHead) * 4;
+  w.ranges = 256;
+  if (d->dtype == LLA_BF16) {
+    Q4Plan p;
+    make_q4_plan(d->H, d->r_k, d->r_v, &p);
+    const int64_t units = static_cast<int64_t>(B) * p.ngroups;
+    w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), units * tiles)));
+    w.records = (256 + static_cast<size_t>(units) * 8 + 255) / 256 * 256;
+    w.total = w.records + (static_cast<size_t>(units) + w.grid) * p.nh * rec;
+    return w;
+  }
   const int64_t chunk = q4_plain_chunk(std::max(B, 1), d->H, std::max<int64_t>(L_max, 1), sms) / kTile;
-  const int64_t splits = (std::max<int64_t>(tiles, 1) + chunk - 1) / chunk;
-  return 256 + static_cast<size_t>(B) * d->H * splits * (d->r_v + kRecordHead) * 4;
+  w.records = 256;
+  w.total = 256 + static_cast<size_t>(B) * d->H * ((tiles + chunk - 1) / chunk) * rec;
+  return w;
 }
 
 }  // namespace
@@ -454,7 +463,7 @@ size_t lla_q4_row_bytes(const lla_dims* dims) {
 
 size_t lla_q4_workspace_size(const lla_dims* dims, int B, int64_t L_max) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || B < 0 || L_max < 0) return 0;
-  return q4_ws(dims, B, L_max, device_sm_count());
+  return q4_ws(dims, B, L_max, device_sm_count()).total;
 }
 
 lla_status lla_q4_store(const lla_dims* dims, const void* c_k, const void* c_v, int N, const int64_t* slots,
@@ -478,7 +487,8 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
   if (loop_t < 0 || loop_t >= dims->T || cache->max_pages < 1) return LLA_ERR_INVALID_ARG;
   const int64_t L_max = static_cast<int64_t>(cache->max_pages) * cache->page_size;
   if (L_max > (int64_t(1) << 30) || static_cast<int64_t>(cache->B) * cache->max_pages >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(cache->B) * dims->H > (int64_t(1) << 24))
+      static_cast<int64_t>(cache->B) * dims->H > (int64_t(1) << 24) ||
+      static_cast<int64_t>(cache->B) * ((L_max + kTile - 1) / kTile) >= (int64_t(1) << 31))
     return LLA_ERR_UNSUPPORTED;
   if (cache->B == 0) return LLA_OK;
   if (rope_len < L_max || rope_len < kTile) return LLA_ERR_INVALID_ARG;
@@ -490,7 +500,8 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
     return LLA_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
-  if (ws_bytes < q4_ws(dims, cache->B, L_max, sms)) return LLA_ERR_INVALID_ARG;
+  const Q4Ws w = q4_ws(dims, cache->B, L_max, sms);
+  if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   const size_t es = dims->dtype == LLA_BF16 ? 2 : 4;
   const size_t wk = static_cast<size_t>(dims->H) * kHeadDim * dims->r_k * es;
   const size_t wv = static_cast<size_t>(dims->H) * kHeadDim * dims->r_v * es;
@@ -521,11 +532,19 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
   a.out = out;
   a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
-  a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.records);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (dims->dtype == LLA_BF16) {
+    if (!make_q4_plan(a.H, a.r_k, a.r_v, &a.plan)) return LLA_ERR_UNSUPPORTED;
+    a.ranges = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.ranges);
+    a.grid = w.grid;
+    // sequences per combine block: W_up,v is read once for them; about four blocks per SM
+    a.combine_units = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, static_cast<int64_t>(a.B) * a.H / (4 * sms))));
+    return launch_q4_tile(a, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
+  }
   a.chunk = q4_plain_chunk(a.B, a.H, L_max, sms);
   a.splits = static_cast<int>((L_max + a.chunk - 1) / a.chunk);
-  return launch_q4_plain(a, dims->dtype == LLA_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? LLA_OK
-                                                                                                       : LLA_ERR_CUDA;
+  return launch_q4_f32(a, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -23,6 +23,17 @@ __host__ __device__ inline int q4_row_bytes(int r_k, int r_v) {
   return ((r_k + r_v) / 2 + 2 * (q4_groups(r_k) + q4_groups(r_v)) + 15) / 16 * 16;
 }
 
+// Shared-memory plan of the tensor-core decode kernel (byte offsets from a 1024-aligned base).
+struct Q4Plan {
+  int nh, ngroups;                   // heads of a group (1 or 2), groups of a sequence
+  int NS, NA;                        // ring stages, A operand buffers in TMEM
+  int z, z_stride, z_bias;           // query operands, one per head of the group; its bias chunk
+  int trig, acc, misc, ring, stage;
+  int bytes;                         // total dynamic smem incl. alignment slack
+};
+// False where no plan fits (never for ranks up to kMaxRankPerHead).
+bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p);
+
 struct Q4DecodeArgs {
   int B, H, r_k, r_v, rope_style;
   int row_bytes;
@@ -44,13 +55,18 @@ struct Q4DecodeArgs {
   float* lse;                        // [B][H], or nullptr
   uint32_t* status;
   float* records;                    // split records: {m (log2 units), l, -, -, acc[r_v]}
-  int64_t chunk;                     // plain kernel: tokens of a split
-  int splits;                        // plain kernel: splits of a (sequence, head)
+  int64_t chunk;                     // fp32 kernel: tokens of a split
+  int splits;                        // fp32 kernel: splits of a (sequence, head)
+  int32_t* ranges;                   // tensor-core kernel: first and last CTA of each (sequence, head group)
+  int grid;
+  int combine_units;                 // sequences per combine block (1..8)
+  Q4Plan plan;
 };
 
-// Tokens per split of the plain kernel: enough splits for two blocks per SM, whole tiles.
+// Tokens per split of the fp32 kernel: enough splits for two blocks per SM, whole tiles.
 int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms);
-cudaError_t launch_q4_plain(const Q4DecodeArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_q4_tile(const Q4DecodeArgs& a, cudaStream_t s);
 
 // Opt the kernel in to `smem` bytes of dynamic shared memory on the current device.
 // Set at every launch: the attribute belongs to a device's copy of the kernel, and a
