@@ -26,8 +26,9 @@ __host__ __device__ inline int q4_row_bytes(int r_k, int r_v) {
 // Shared-memory plan of the tensor-core decode kernel (byte offsets from a 1024-aligned base).
 struct Q4Plan {
   int nh, ngroups;                   // heads of a group (1 or 2), groups of a sequence
-  int NS, NA;                        // ring stages, A operand buffers in TMEM
-  int z, z_stride, z_bias;           // query operands, one per head of the group; its bias chunk
+  int NS, NG;                        // ring stages, G buffers in TMEM
+  int N;                             // rows of a query operand = columns of G: r_k + 16
+  int z, z_stride;                   // query operands, one per head of the group
   int trig, acc, misc, ring, stage;
   int bytes;                         // total dynamic smem incl. alignment slack
 };

@@ -1,35 +1,37 @@
 // lla_q4_decode.cu — latent decode attention over the 4-bit paged cache on the tensor
 // cores (bf16 storage; lla_q4.cu holds the fp32 kernel and the entry point).
 //
-// Score of Eq. (3) with RoPE after reconstruction, regrouped per frequency pair f as in
-// lla_decode.cu: with the folded query Z_f = sc (q'_i0 W_i0 + q'_i1 W_i1) and
-// Z_64+f = sc (q'_i1 W_i0 - q'_i0 W_i1), U = c_j Z^T + bias,
-//     s_j = sum_f cos(j th_f) U_f + sin(j th_f) U_64+f         (log2 units).
-// A 4-bit row is 144 bytes at (96, 160), 3.6 times less than in bf16, so at HBM speed an SM has about
-// 6 cycles per token-head: the contractions run on the tensor cores, and a code
-// costs about one ALU instruction on its way there.
-//   K  Each thread of the K warpgroup owns one token: codes become f16 pairs (two magic
-//      operations), are scaled by the group scale relative to the token's largest (a power of two,
-//      multiplied back in the epilogue, so latents of any size stay in f16 range) and go
-//      straight to TMEM as the A operand of U = c Z^T (M = 128 tokens, N = 128, K = r_k + 16:
-//      one more step carries the bias, f16 high and low parts against that power).
-//   s  Two epilogue warpgroups share a head-tile, 32 frequencies each.  A thread keeps its
-//      row's cos / sin in registers and turns them by one tile's angle (table row 128) from tile to
-//      tile: rows read from L2 (64 KB a tile) would be more traffic than the latents.  Partial
-//      scores meet in shared memory, and the groups take turns at the softmax.
-//   V  sum_j p_j c_v,j is a warp-level MMA: A = the codes themselves, as f16
-//      subnormals (code * 2^-24 and code * 2^-20: masking is the whole conversion), B = one
-//      column per scale group holding p_j scale_j,g, so that a group's scale is applied to a
-//      weight and never to a code; a row of ones gives the sum that takes the codes' offset of 8 back.  Every
-//      code is finite, so rows behind the last token only need weight 0.
+// Score of Eq. (3) with RoPE after reconstruction, regrouped as in lla_decode_small.cu: with the
+// query folded into W_up,k,t (Z_n over 128 rotary coordinates) and the position's rotary row
+// R_j = (cos(j th_0..63), sin(j th_0..63)),
+//     s_j = sum_n c_j,n G_j,n + bias,   G_j = R_j Z^T        (log2 units),
+// so G of a 128-token tile is one MMA chain (M = 128 tokens, N = r_k + 16, K = 128), and the codes
+// never enter it: a token's c_n = (code - 8) scale meets G in one thread's registers.
+// A 4-bit row is 144 bytes at (96, 160), 3.6 times less than in bf16: at HBM speed an SM has about
+// 6 cycles per token-head, and what bounds the kernel is instruction issue; the choices
+// below are for few instructions per code.
+//   G  A = the rotary rows, f16 in TMEM, shared by the heads of a position.  Their fp32 values stay in
+//      the registers of the two epilogue warpgroups (32 frequencies each), turned by one tile's
+//      angle (table row 128) from tile to tile: rows read from L2 (64 KB a tile) would be more
+//      traffic than the latents.  B = the head's Z rows (f16, resident for the whole run), two bias rows
+//      (f16 high and low part) and one row -8 sum Z per scale group, which takes the codes'
+//      offset back.
+//   s  One token per thread, the two warpgroups alternate head-tiles.  Codes are masked into f16
+//      subnormals (code * 2^-24, or * 2^-20 from the next nibble), converted, and summed per
+//      scale group in fp32; the group's scale multiplies the sum.
+//   V  sum_j p_j c_v,j is a warp-level MMA: A = the codes themselves, as f16 subnormals (masking is
+//      the whole conversion), B = one column per scale group holding p_j scale_j,g, so that a
+//      scale is applied to a weight and never to a code; a row of ones gives the sum that takes the offset of 8
+//      back.  Every code is finite, so rows behind the last token only need weight 0.
 //
 // Work: positions (sequence, head group, 128-token tile) in that order, cut into
 // equal contiguous ranges, one per CTA.  A run is a CTA's part of one (sequence, head
 // group); the query operand of its nh heads is built in shared memory at its start, and
 // one record {m, l, acc} per head is written at its end.  Warps: 0 producer (bulk
-// copies of page pieces into the ring), 1 MMA issuer, 4-7 K, 8-15 epilogue, 16-19 V.
+// copies of page pieces into the ring), 1 MMA issuer, 4-11 epilogue, 12-15 V.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "lla_q4.h"
 
@@ -37,37 +39,41 @@ namespace lla {
 
 namespace {
 
-constexpr int kQ4TileThreads = 640;
-constexpr int kWorkers = 512;                    // K, epilogue and V warpgroups
+constexpr int kQ4TileThreads = 512;
+constexpr int kWorkers = 384;                    // epilogue and V warpgroups
 constexpr int kQ4MaxNS = 16;
+constexpr int kMaxG = 4;                         // G buffers
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
 constexpr int kWBytes = 8 * kWStride * 2;
 constexpr int kStageTail = kWBytes + 64;         // weights, then the four references
-constexpr int kTrigRow = 20;                     // words of a staged row of 16 table values
+constexpr int kTrigRow = 12;                     // words of a staged row of 8 table values
 constexpr int kTrigBytes = 8 * 32 * kTrigRow * 4;
-constexpr int kUCol = 0;                         // TMEM: two U buffers of 128 columns
-constexpr int kACol = 256;                       // then the A operand buffers
+constexpr int kACol = 0;                         // TMEM: two buffers of rotary rows, 64 columns each
+constexpr int kGCol = 128;                       // then the G buffers
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr int kSeedTiles = 512;                  // tiles between reads of the table (a power of two)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
 constexpr int kNoRef = -(1 << 28);
-// named barriers: 1 workers + MMA warp, 2 workers, 3.. one per (quadrant, parity) of the epilogue
-enum { kBarRun = 1, kBarWork = 2, kBarPair = 3 };
+enum { kBarRun = 1, kBarWork = 2 };              // named barriers: workers + MMA warp; workers
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
-  uint64_t afull[2], aempty[2], ufull[2], uempty[2];
+  uint64_t afull[2], aempty[2], gfull[kMaxG], gempty[kMaxG];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
   int start_b, start_hg, start_t, count;
   int scan[kQ4TileThreads];
-  float2 ml[2][8];                               // run end: (m, l) per head and epilogue warp
+  float2 ml[8];                                  // run end: (m, l) of each epilogue warp
+  int head[2];                                   // run end: the head that each epilogue group held
   int vref[4];                                   // run end: reference of each V warp
   float qs[2][2][64];                            // rotated query, sc q'_i0 and sc q'_i1, per head
-  float tile_cos[64], tile_sin[64], tile_nsin[64];   // table row 128 (and - sin): one tile's angles
-  float part[2][128];                            // half scores of a head-tile, by parity
+  alignas(16) float tile_cos[64];                // table row 128: one tile's angles
+  float tile_sin[64];                            // (follows tile_cos: read by 16-byte loads)
 };
+
+static_assert(offsetof(Q4Misc, tile_cos) % 16 == 0 && offsetof(Q4Misc, tile_sin) == offsetof(Q4Misc, tile_cos) + 256,
+              "read as 16-byte vectors");
 
 struct Slot {
   int i;
@@ -111,31 +117,37 @@ struct RunWalker {
   }
 };
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
+// Shared-memory accesses by 32-bit address (the loops below are bound by instruction issue).
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
+__device__ __forceinline__ uint32_t lds16(uint32_t p) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(p));
+  return v;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+  return v;
 }
-__device__ __forceinline__ float sum2(uint64_t v) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-  return lo + hi;
+__device__ __forceinline__ float4 lds128f(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts64(uint32_t p, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t p, __half v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(__half_as_ushort(v)) : "memory");
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 __device__ __forceinline__ uint32_t h2_bits(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t v) { return *reinterpret_cast<__half2*>(&v); }
-__device__ __forceinline__ void pair_arrive(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
-
 // D[16 x 8] += A[16 x 16] B[16 x 8], f16 operands, fp32 accumulator (one warp).
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -145,34 +157,40 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+// 32 lanes x 32 bits, one column.
+__device__ __forceinline__ void tmem_ld_x1(uint32_t taddr, float (&v)[1]) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  v[0] = __uint_as_float(r);
 }
 
-// Exponent of the power of two that a token's K codes are scaled against, from the bits of
-// its largest scale.  Not below -14: 2^14 is the largest that multiplies the bias in f16, and
-// latents that small against it no longer move a score.
-__device__ __forceinline__ int k_exponent(uint32_t top) { return min(max(static_cast<int>(top >> 7) - 127, -14), 126); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
-__device__ __forceinline__ uint32_t scale_bits(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 
-// Register shares of the warpgroups: 56 + 72 + 2 x 120 + 112 = 480 = 5 x 96, what the
-// block is launched with (640 threads of 96).
+// Warp-collective bounded wait for a barrier phase: every lane tests it, so each makes its own
+// acquire; the clock and the abort flag are looked at now and then only, because a
+// waiting warp's instructions are taken from the warps that work.
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000))) return true;
+    const bool give_up = *abort != 0 || global_timer_ns() - t0 > kWaitLimitNs;
+    if (__any_sync(0xffffffffu, give_up)) {
+      record_status(status, LLA_ERR_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// Register shares of the warpgroups: 72 + 2 x 152 + 136 = 512 = 4 x 128, what the
+// block is launched with (512 threads of 128).
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// The eight f16 pairs of a 4-code-pair word: columns (2i, 2i + 1) as code - 8, exact, times `s`.
-// 0x6400 is 1024 in f16, whose unit in the last place is 1.
-__device__ __forceinline__ void k_word(uint32_t w, __half2 s, uint32_t (&o)[4]) {
-  const __half2 off = __half2half2(__ushort_as_half(0x6408));   // 1032
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o[i] = h2_bits(__hmul2(__hsub2(bits_h2(((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u), off), s));
-}
 
 // RV32 = ceil(r_v / 32): V columns in chunks of 64 (four MMAs of 16 rows) and at most
 // one of 32 (two).  Columns beyond r_v read the bytes behind the codes, and their rows
@@ -188,7 +206,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   Q4Misc* misc = reinterpret_cast<Q4Misc*>(sm + P.misc);
   volatile int* abort = &misc->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, NA = P.NA, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
+  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, NG = P.NG, N = P.N, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
   const int scale_at = q4_scale_offset(rk, rv), gk = q4_groups(rk);
 
   // ---------------------------------------------------------- work range
@@ -249,14 +267,16 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar(misc->full[s]), 1);
-      mbar_init(bar(misc->empty[s]), 4 + 4 / nh);   // K warps, the head's V warps
+      mbar_init(bar(misc->empty[s]), 4 / nh);       // the head's V warps, the last to read it
       mbar_init(bar(misc->wfull[s]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(misc->afull[i]), 4);
+      mbar_init(bar(misc->afull[i]), 8);
       mbar_init(bar(misc->aempty[i]), 1);
-      mbar_init(bar(misc->ufull[i]), 1);
-      mbar_init(bar(misc->uempty[i]), 8);
+    }
+    for (int i = 0; i < NG; ++i) {
+      mbar_init(bar(misc->gfull[i]), 1);
+      mbar_init(bar(misc->gempty[i]), 4);
     }
     mbar_init(bar(misc->mma_done), 1);
     fence_mbar_init();
@@ -265,7 +285,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     const int f = tid - 64;
     misc->tile_cos[f] = __ldg(a.rope_cos + kTile * 64 + f);
     misc->tile_sin[f] = __ldg(a.rope_sin + kTile * 64 + f);
-    misc->tile_nsin[f] = -misc->tile_sin[f];
   }
   if (warp == 1) {
     __syncwarp();
@@ -276,27 +295,30 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine waits for this grid
   const uint32_t tmem = misc->tmem_base;
-  const int acols = rk / 2 + 8;                  // TMEM columns of an A operand
   RunWalker walk = start;
   Run run{0, 0, 0, 0, 0};
   bool ok = true;
   // every role keeps its place in the loops when a wait has expired: the named barriers
   // below count on it
   auto wait = [&](const uint64_t& m, uint32_t parity) {
-    if (ok) ok = warp_wait(bar(m), parity, abort, a.status);
+    if (ok) ok = q4_wait(bar(m), parity, abort, a.status);
   };
   auto arrive = [&](const uint64_t& m) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(m));
   };
 
-  // Builds the run's query operands: Z rows of its heads in the K-major chunk layout, and
-  // the bias chunk {high, low, 0...}.  All workers; the previous run has ended.
+  // Builds the run's query operands, per head N rows of 128 rotary coordinates in two K-major
+  // chunks of 64 (128-byte swizzle): r_k Z rows, bias high and low, -8 sum Z of each scale
+  // group, zeros.  All workers; the previous run has ended.
   auto build = [&](int wtid) {
     const int nhg = min(nh, a.H - run.hg * nh);
     int qp = __ldg(a.q_pos + run.b);
     qp = qp < 0 ? 0 : (qp >= a.rope_len ? static_cast<int>(a.rope_len - 1) : qp);
     float amax = 0.f;
+    auto at = [&](int hi, int row, int coord) {   // address of 8-byte aligned coordinates of a row
+      return sbase + P.z + hi * P.z_stride + (coord >> 6) * N * 128 + swizzle_offset(row * 128 + 2 * (coord & 63), 128);
+    };
     for (int i = wtid; i < nhg * 64; i += kWorkers) {
       const int hi = i >> 6, f = i & 63, h = run.hg * nh + hi;
       const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
@@ -309,54 +331,67 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       misc->qs[hi][1][f] = q1;
       const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1);
       const float bias[2] = {q0 * m0 + q1 * m1, q1 * m0 - q0 * m1};
-      uint8_t* img = sm + P.z + hi * P.z_stride + P.z_bias;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
-        const float hi16 = __half2float(__float2half_rn(bias[part]));
+        const __half high = __float2half_rn(bias[part]);
         amax = fmaxf(amax, fabsf(bias[part]));
-        const uint32_t row = (64 * part + f) * 32;
-        *reinterpret_cast<uint4*>(img + swizzle_offset(row, 32)) =
-            make_uint4(h2_bits(__floats2half2_rn(hi16, bias[part] - hi16)), 0, 0, 0);
-        *reinterpret_cast<uint4*>(img + swizzle_offset(row + 16, 32)) = make_uint4(0, 0, 0, 0);
+        sts16(at(hi, rk, 64 * part + f), high);
+        sts16(at(hi, rk + 1, 64 * part + f), __float2half_rn(bias[part] - __half2float(high)));
+        for (int row = rk + 2 + gk; row < N; ++row) sts16(at(hi, row, 64 * part + f), __ushort_as_half(0));
       }
     }
     named_bar_sync(kBarWork, kWorkers);
-    const int k8 = rk / 8;
-    for (int i = wtid; i < nhg * 64 * k8; i += kWorkers) {
-      const int hf = i / k8, k = (i - hf * k8) * 8, hi = hf >> 6, f = hf & 63, h = run.hg * nh + hi;
-      const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
-      const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk + k;
-      float w0[8], w1[8], zc[8], zs[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0) * rk)), w0);
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1) * rk)), w1);
-      const float q0 = misc->qs[hi][0][f], q1 = misc->qs[hi][1][f];
+    // item = (head, scale group, 4 frequencies, 8 columns); the four of a scale group are neighbouring
+    // lanes (whole warps take part: 64 gk items per head)
+    for (int i = wtid; i < nhg * gk * 64; i += kWorkers) {
+      const int o = i & 3, f0 = (i >> 2 & 15) * 4, hg = i >> 6, hi = hg / gk, g = hg - hi * gk, n = 32 * g + 8 * o;
+      const int h = run.hg * nh + hi;
+      float sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
+      if (n < rk) {
+        const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk + n;
+        uint4 w0[4], w1[4];
+        float q0[4], q1[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        zc[e] = q0 * w0[e] + q1 * w1[e];
-        zs[e] = q1 * w0[e] - q0 * w1[e];
-        amax = fmaxf(amax, fmaxf(fabsf(zc[e]), fabsf(zs[e])));
-      }
-      // chunk of column k: 64-wide chunks first, then one of 32, then one of 16
-      const int c64 = rk / 64 * 64;
-      int width = 64, at = k / 64 * 16384, col = k & 63;
-      if (k >= c64) {
-        const int rest = rk - c64;
-        at = c64 / 64 * 16384;
-        col = k - c64;
-        width = 32;
-        if (rest < 32 || col >= 32) {
-          width = 16;
-          if (rest >= 32) { at += 8192; col -= 32; }
+        for (int e = 0; e < 4; ++e) {
+          const int f = f0 + e;
+          const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
+          w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0) * rk));
+          w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1) * rk));
+          q0[e] = misc->qs[hi][0][f];
+          q1[e] = misc->qs[hi][1][f];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          __half zc[4], zs[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t x0 = (&w0[e].x)[j >> 1], x1 = (&w1[e].x)[j >> 1];
+            const float u = __uint_as_float(j & 1 ? x0 & 0xFFFF0000u : x0 << 16);
+            const float v = __uint_as_float(j & 1 ? x1 & 0xFFFF0000u : x1 << 16);
+            zc[e] = __float2half_rn(q0[e] * u + q1[e] * v);
+            zs[e] = __float2half_rn(q1[e] * u - q0[e] * v);
+            const float cf = __half2float(zc[e]), sf = __half2float(zs[e]);
+            sum_c[e] += cf;
+            sum_s[e] += sf;
+            amax = fmaxf(amax, fmaxf(fabsf(cf), fabsf(sf)));
+          }
+          sts64(at(hi, n + j, f0), h2_bits(__halves2half2(zc[0], zc[1])), h2_bits(__halves2half2(zc[2], zc[3])));
+          sts64(at(hi, n + j, 64 + f0), h2_bits(__halves2half2(zs[0], zs[1])), h2_bits(__halves2half2(zs[2], zs[3])));
         }
       }
-      uint8_t* img = sm + P.z + hi * P.z_stride + at;
-      const int row_b = 2 * width;
-      *reinterpret_cast<uint4*>(img + swizzle_offset(f * row_b + 2 * col, row_b)) =
-          make_uint4(h2_bits(__floats2half2_rn(zc[0], zc[1])), h2_bits(__floats2half2_rn(zc[2], zc[3])),
-                     h2_bits(__floats2half2_rn(zc[4], zc[5])), h2_bits(__floats2half2_rn(zc[6], zc[7])));
-      *reinterpret_cast<uint4*>(img + swizzle_offset((64 + f) * row_b + 2 * col, row_b)) =
-          make_uint4(h2_bits(__floats2half2_rn(zs[0], zs[1])), h2_bits(__floats2half2_rn(zs[2], zs[3])),
-                     h2_bits(__floats2half2_rn(zs[4], zs[5])), h2_bits(__floats2half2_rn(zs[6], zs[7])));
+      // the codes' offset: -8 sum Z over the scale group's columns
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum_c[e] += __shfl_xor_sync(0xffffffffu, sum_c[e], 1);
+        sum_s[e] += __shfl_xor_sync(0xffffffffu, sum_s[e], 1);
+        sum_c[e] = -8.f * (sum_c[e] + __shfl_xor_sync(0xffffffffu, sum_c[e], 2));
+        sum_s[e] = -8.f * (sum_s[e] + __shfl_xor_sync(0xffffffffu, sum_s[e], 2));
+        amax = fmaxf(amax, fmaxf(fabsf(sum_c[e]), fabsf(sum_s[e])));
+      }
+      if (o == 0) {
+        sts64(at(hi, rk + 2 + g, f0), h2_bits(__floats2half2_rn(sum_c[0], sum_c[1])), h2_bits(__floats2half2_rn(sum_c[2], sum_c[3])));
+        sts64(at(hi, rk + 2 + g, 64 + f0), h2_bits(__floats2half2_rn(sum_s[0], sum_s[1])), h2_bits(__floats2half2_rn(sum_s[2], sum_s[3])));
+      }
     }
     if (amax > 65504.f) record_status(a.status, LLA_ERR_RANGE);   // NaN queries stay NaN
     fence_proxy_async_smem();
@@ -364,7 +399,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   };
 
   if (warp < 4) {
-    regs_dec<56>();
+    regs_dec<72>();
     if (warp == 0) {
       // ======================================================== producer
       // Per head-tile: the page pieces that its rows lie in, lane i copying piece i.
@@ -410,51 +445,37 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
     } else if (warp == 1) {
       // ======================================================== MMA issuer
-      // U = A Z^T per head-tile; the whole warp runs the loop, one elected lane issues
-      const uint32_t idesc = umma_idesc_f16(128, 128);
-      const int n64 = rk / 64, r32 = (rk & 63) >= 32, r16 = (rk & 31) >= 16;
-      Slot as{0, 0u};
-      uint32_t n = 0;
+      // G = R Z^T per head-tile; the whole warp runs the loop, one elected lane issues
+      const uint32_t idesc = umma_idesc_f16(128, min(N, 256)), tail_idesc = umma_idesc_f16(128, 16);
+      Slot as{0, 0u}, gs{0, 0u};
       while (walk.next(a, ngroups, run)) {
         const int nhg = min(nh, a.H - run.hg * nh);
         named_bar_sync(kBarRun, kWorkers + 32);   // operands built
-        for (int t = 0; t < run.n; ++t)
-          for (int hi = 0; hi < nhg; ++hi, ++n) {
-            wait(misc->afull[as.i], as.phase);
-            wait(misc->uempty[n & 1], ((n >> 1) & 1) ^ 1u);
+        for (int t = 0; t < run.n; ++t) {
+          wait(misc->afull[as.i], as.phase);
+          for (int hi = 0; hi < nhg; ++hi) {
+            wait(misc->gempty[gs.i], gs.phase ^ 1u);
             if (ok) {
               tc_fence_after();
-              const uint32_t d = tmem + kUCol + (n & 1) * 128;
-              uint32_t ac = tmem + kACol + as.i * acols;
-              uint32_t z = sbase + P.z + hi * P.z_stride;
-              uint32_t acc = 0;
-              for (int c = 0; c < n64; ++c, z += 16384) {
-                const uint64_t bd = umma_desc(z, 16, 1024, kSw128);
+              const uint32_t d = tmem + kGCol + gs.i * N, ac = tmem + kACol + 64 * as.i;
+              const uint32_t z = sbase + P.z + hi * P.z_stride;
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk, ac += 8) {
-                  umma_bf16_ts_warp(d, ac, bd + 2 * kk, idesc, acc);
-                  acc = 1;
-                }
-              }
-              if (r32) {
-                const uint64_t bd = umma_desc(z, 16, 512, kSw64);
-                umma_bf16_ts_warp(d, ac, bd, idesc, acc);
-                umma_bf16_ts_warp(d, ac + 8, bd + 2, idesc, 1);
-                acc = 1;
-                ac += 16;
-                z += 8192;
-              }
-              if (r16) {
-                umma_bf16_ts_warp(d, ac, umma_desc(z, 16, 256, kSw32), idesc, acc);
-                ac += 8;
-                z += 4096;
-              }
-              umma_bf16_ts_warp(d, ac, umma_desc(z, 16, 256, kSw32), idesc, 1);   // the bias step
-              umma_commit_warp(bar(misc->ufull[n & 1]));
-              umma_commit_warp(bar(misc->aempty[as.i]));
+              for (int kk = 0; kk < 8; ++kk)
+                umma_bf16_ts_warp(d, ac + 8 * kk, umma_desc(z + (kk >> 2) * N * 128, 16, 1024, kSw128) + 2 * (kk & 3), idesc,
+                                  kk > 0 ? 1u : 0u);
+              if (N > 256)   // r_k = 256: the last 16 rows are an MMA of their own
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  umma_bf16_ts_warp(d + 256, ac + 8 * kk,
+                                    umma_desc(z + (kk >> 2) * N * 128 + 256 * 128, 16, 1024, kSw128) + 2 * (kk & 3),
+                                    tail_idesc, kk > 0 ? 1u : 0u);
+              umma_commit_warp(bar(misc->gfull[gs.i]));
+              if (hi == nhg - 1) umma_commit_warp(bar(misc->aempty[as.i]));
             }
-            as.next(NA);
+            gs.next(NG);
           }
+          as.next(2);
+        }
         named_bar_sync(kBarRun, kWorkers + 32);   // run ended
       }
       // this warp's MMAs complete before TMEM is released
@@ -462,209 +483,163 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(bar(misc->mma_done), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
     }
-  } else if (warp < 8) {
-    regs_dec<72>();
-    // ======================================================== K: codes to the A operand
-    const int q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
+  } else if (warp < 12) {
+    regs_inc<152>();
+    // ======================================================== epilogue: rotary rows, scores, weights
+    const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    Slot st{0, 0u}, as{0, 0u};
-    while (walk.next(a, ngroups, run)) {
-      const int nhg = min(nh, a.H - run.hg * nh);
-      build(wtid);
-      for (int t = 0; t < run.n; ++t)
-        for (int hi = 0; hi < nhg; ++hi) {
-          wait(misc->full[st.i], st.phase);
-          wait(misc->aempty[as.i], as.phase ^ 1u);
-          tc_fence_after();
-          const uint8_t* r = sm + P.ring + st.i * P.stage + row * rb;
-          const uint32_t at = tmem + lane_base + kACol + as.i * acols;
-          // the token's power of two: that of its largest group scale
-          uint32_t top = 0;
-          for (int g = 0; g < gk; ++g) top = max(top, scale_bits(r + scale_at + 2 * g) & 0x7FFFu);
-          const float down = pow2(-k_exponent(top));
-          int c = 0;
-          for (; c + 32 <= rk; c += 32) {
-            const float s = __uint_as_float(scale_bits(r + scale_at + c / 16) << 16);
-            const __half2 s2 = __float2half2_rn(s * down);
-            uint32_t o[16], u[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              k_word(*reinterpret_cast<const uint32_t*>(r + c / 2 + 4 * i), s2, u);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[4 * i + j] = u[j];
-            }
-            tmem_st_x16(at + c / 2, o);
-          }
-          uint32_t o[8], u[4];
-          if (c < rk) {
-            const float s = __uint_as_float(scale_bits(r + scale_at + c / 16) << 16);
-            const __half2 s2 = __float2half2_rn(s * down);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              k_word(*reinterpret_cast<const uint32_t*>(r + c / 2 + 4 * i), s2, u);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[4 * i + j] = u[j];
-            }
-            tmem_st_x8(at + c / 2, o);
-          }
-          // the bias step: the power of two against the bias rows' high and low parts
-          o[0] = h2_bits(__float2half2_rn(down));
-#pragma unroll
-          for (int i = 1; i < 8; ++i) o[i] = 0;
-          tmem_st_x8(at + rk / 2, o);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(misc->afull[as.i]));
-            mbar_arrive(bar(misc->empty[st.i]));
-          }
-          st.next(NS);
-          as.next(NA);
-        }
-      named_bar_sync(kBarRun, kWorkers + 32);
-    }
-  } else if (warp < 16) {
-    regs_inc<120>();
-    // ======================================================== epilogue: scores and weights
-    const int grp = (warp - 8) >> 2, q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    float* stage = reinterpret_cast<float*>(sm + P.trig) + (warp - 8) * 32 * kTrigRow;
-    Slot st{0, 0u};
-    uint32_t n = 0;
-    uint64_t tc[16], ts[16];   // cos and sin of the own row, pairs of frequencies 32 grp + (2i, 2i + 1)
+    float* stage = reinterpret_cast<float*>(sm + P.trig) + (warp - 4) * 32 * kTrigRow;
+    Slot st{0, 0u}, as{0, 0u}, gs{0, 0u};
+    uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
+    float tc[32], ts[32];   // cos and sin of the own row, frequencies 32 grp + i
     // rows of tile t from the table, through shared memory (a thread's own row straight from
     // global memory would touch 32 lines per load)
     auto seed = [&](int t) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
+      for (int p = 0; p < 8; ++p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int64_t j = static_cast<int64_t>(t) * kTile + 32 * q + 8 * i + (lane >> 2);
+        for (int i = 0; i < 2; ++i) {
+          const int r = 16 * i + (lane >> 1);
+          int64_t j = static_cast<int64_t>(t) * kTile + 32 * q + r;
           j = j < a.rope_len ? j : a.rope_len - 1;    // behind the sequence's end: masked
-          *reinterpret_cast<float4*>(stage + (8 * i + (lane >> 2)) * kTrigRow + 4 * (lane & 3)) = __ldg(
-              reinterpret_cast<const float4*>((p < 2 ? a.rope_cos : a.rope_sin) + j * 64 + 32 * grp + 16 * (p & 1) + 4 * (lane & 3)));
+          *reinterpret_cast<float4*>(stage + r * kTrigRow + 4 * (lane & 1)) = __ldg(
+              reinterpret_cast<const float4*>((p < 4 ? a.rope_cos : a.rope_sin) + j * 64 + 32 * grp + 8 * (p & 3) + 4 * (lane & 1)));
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const float4 v = *reinterpret_cast<const float4*>(stage + lane * kTrigRow + 4 * i);
-          (p < 2 ? tc : ts)[8 * (p & 1) + 2 * i] = pack2(v.x, v.y);
-          (p < 2 ? tc : ts)[8 * (p & 1) + 2 * i + 1] = pack2(v.z, v.w);
+          float* o = (p < 4 ? tc : ts) + 8 * (p & 3) + 4 * i;
+          o[0] = v.x;
+          o[1] = v.y;
+          o[2] = v.z;
+          o[3] = v.w;
         }
         __syncwarp();
       }
     };
     // one tile further: by the angle sum with row 128
+    const uint32_t turn = smem_u32(&misc->tile_cos[32 * grp]);   // tile_sin follows
     auto step = [&]() {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const ulonglong2 C = *reinterpret_cast<const ulonglong2*>(&misc->tile_cos[32 * grp + 4 * i]);
-        const ulonglong2 S = *reinterpret_cast<const ulonglong2*>(&misc->tile_sin[32 * grp + 4 * i]);
-        const ulonglong2 N = *reinterpret_cast<const ulonglong2*>(&misc->tile_nsin[32 * grp + 4 * i]);
+        const float4 C = lds128f(turn + 16 * i), S = lds128f(turn + 256 + 16 * i);
+        const float cc[4] = {C.x, C.y, C.z, C.w}, ss[4] = {S.x, S.y, S.z, S.w};
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint64_t c = tc[2 * i + e], s = ts[2 * i + e], c1 = e ? C.y : C.x, s1 = e ? S.y : S.x, n1 = e ? N.y : N.x;
-          tc[2 * i + e] = fma2(c, c1, mul2(s, n1));
-          ts[2 * i + e] = fma2(c, s1, mul2(s, c1));
+        for (int e = 0; e < 4; ++e) {
+          const float c = tc[4 * i + e], s = ts[4 * i + e];
+          tc[4 * i + e] = fmaf(c, cc[e], -s * ss[e]);
+          ts[4 * i + e] = fmaf(c, ss[e], s * cc[e]);
         }
       }
+    };
+    // this group's half of the rotary rows into the next A buffer
+    auto put_rows = [&]() {
+      wait(misc->aempty[as.i], as.phase ^ 1u);
+      tc_fence_after();
+      uint32_t o[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = h2_bits(__floats2half2_rn(tc[2 * i], tc[2 * i + 1]));
+      tmem_st_x16(tmem + lane_base + kACol + 64 * as.i + 16 * grp, o);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[i] = h2_bits(__floats2half2_rn(ts[2 * i], ts[2 * i + 1]));
+      tmem_st_x16(tmem + lane_base + kACol + 64 * as.i + 32 + 16 * grp, o);
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(misc->afull[as.i]);
+      as.next(2);
     };
     while (walk.next(a, ngroups, run)) {
       const int nhg = min(nh, a.H - run.hg * nh);
       build(wtid);
-      float m0 = -INFINITY, l0 = 0.f, m1 = -INFINITY, l1 = 0.f;
+      seed(run.t0);
+      put_rows();
+      float m = -INFINITY, l = 0.f;
+      const int held = nhg == 2 ? static_cast<int>((n ^ grp) & 1) : 0;   // the head whose state (m, l) is
+#pragma unroll 1
       for (int t = 0; t < run.n; ++t) {
-        // each step adds about an fp32 rounding: seeded again before they add up
-        if ((t & (kSeedTiles - 1)) == 0) seed(run.t0 + t);
-        else step();
+        if (t + 1 < run.n) {   // the next position's rows, ahead of this one's scores
+          // each step adds about an fp32 rounding: seeded again before they add up
+          if (((t + 1) & (kSeedTiles - 1)) == 0) seed(run.t0 + t + 1);
+          else step();
+          put_rows();
+        }
         const bool valid = row < run.L - (run.t0 + t) * kTile;
-        // this group's half of a head-tile's scores
-        auto half_score = [&]() -> float {
-          const uint32_t par = n & 1;
-          wait(misc->ufull[par], (n >> 1) & 1);
+#pragma unroll 1
+        for (int hi = 0; hi < nhg; ++hi, ++n, st.next(NS), gs.next(NG)) {
+          if (grp != static_cast<int>(n & 1)) continue;
+          const uint32_t base = sbase + P.ring + st.i * P.stage, tail = base + kTile * rb, r = base + row * rb;
+          wait(misc->full[st.i], st.phase);
+          // ---- V scales; 2^E is above every one of the warp's tokens
+          uint32_t vtop = 0, vs[RV32];
+#pragma unroll
+          for (int g = 0; g < RV32; ++g) {
+            vs[g] = lds16(r + scale_at + 2 * (gk + g));
+            vtop = max(vtop, vs[g] & 0x7FFFu);
+          }
+          const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, valid ? vtop >> 7 : 0u)) - 126, 126);
+          const float ie = pow2(-E);
+          wait(misc->gfull[gs.i], gs.phase);
           tc_fence_after();
-          uint64_t s2 = 0, s3 = 0;
-          // 16 cosine and 16 sine columns at a time: the table rows hold half of the registers
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float u0[16], u1[16];
-            const uint32_t u = tmem + lane_base + kUCol + par * 128 + 32 * grp + 16 * c;
-            tmem_ld_x16(u, u0);
-            tmem_ld_x16(u + 64, u1);
+          const uint32_t gcol = tmem + lane_base + kGCol + gs.i * N;
+          float bias[2];
+          tmem_ld_x2(gcol + rk, bias);
+          float s = 0.f;
+          // ---- per scale group: 32 codes against G (a last group of 16: its other codes count as 0)
+#pragma unroll 1
+          for (int g = 0; g < gk; ++g) {
+            uint4 w = lds128(r + 16 * g);
+            const float sc = __uint_as_float(lds16(r + scale_at + 2 * g) << 16);
+            float G[32], off[1];
+            tmem_ld_x32(gcol + 32 * g, G);
+            tmem_ld_x1(gcol + rk + 2 + g, off);
+            if (32 * g + 32 > rk) w.z = w.w = 0;
             tmem_wait_ld();
-            if (c == 1) {
-              tc_fence_before();
-              arrive(misc->uempty[par]);
-            }
+            float lo0 = 0.f, lo1 = 0.f, hi0 = 0.f, hi1 = 0.f;
+            uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              s2 = fma2(tc[8 * c + i], pack2(u0[2 * i], u0[2 * i + 1]), s2);
-              s3 = fma2(ts[8 * c + i], pack2(u1[2 * i], u1[2 * i + 1]), s3);
-            }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float2 x = __half22float2(bits_h2(ww[i] & 0x000F000Fu)), y = __half22float2(bits_h2(ww[i] & 0x00F000F0u));
+                ww[i] >>= 8;
+                lo0 = fmaf(x.x, G[8 * i + 4 * j], lo0);
+                lo1 = fmaf(x.y, G[8 * i + 4 * j + 1], lo1);
+                hi0 = fmaf(y.x, G[8 * i + 4 * j + 2], hi0);
+                hi1 = fmaf(y.y, G[8 * i + 4 * j + 3], hi1);
+              }
+            s = fmaf(sc, fmaf(lo0 + lo1, 16777216.f, fmaf(hi0 + hi1, 1048576.f, off[0])), s);
           }
-          return sum2(s2) + sum2(s3);
-        };
-        // hand the half over, or take the other group's and finish the head-tile
-        auto finish = [&](float half, float& m, float& l) {
-          const uint32_t par = n & 1;
-          const int id = kBarPair + 2 * q + static_cast<int>(par);
-          if (grp != static_cast<int>(par)) {
-            misc->part[par][row] = half;
-            pair_arrive(id);
-          } else {
-            wait(misc->full[st.i], st.phase);   // the rows' scales (complete long since)
-            const uint8_t* r = sm + P.ring + st.i * P.stage + row * rb + scale_at;
-            uint32_t ktop = 0, vtop = 0;
-            for (int g = 0; g < gk; ++g) ktop = max(ktop, scale_bits(r + 2 * g) & 0x7FFFu);
-            uint32_t vs[RV32];
-#pragma unroll
-            for (int g = 0; g < RV32; ++g) {
-              vs[g] = scale_bits(r + 2 * (gk + g));
-              vtop = max(vtop, vs[g] & 0x7FFFu);
-            }
-            // 2^E: above every V scale of the warp's tokens
-            const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, valid ? vtop >> 7 : 0u)) - 126, 126);
-            const float up = pow2(k_exponent(ktop)), ie = pow2(-E);
-            named_bar_sync(id, 64);
-            const float s = valid ? (half + misc->part[par][row]) * up : -INFINITY;
-            // ---- softmax of the warp's 32 tokens: integer reference, raised lazily
-            const float mt = warp_max_redux(s);
-            if (mt > m + kRaise) {
-              const float mn = ceilf(mt);
-              l *= exp2f(m - mn);
-              m = mn;
-            }
-            const float p = s == -INFINITY ? 0.f : exp2f(s - m);
-            l += p;
-            // ---- weights p * scale of each V group, relative to 2^(m + E)
-            uint8_t* tail = sm + P.ring + st.i * P.stage + kTile * rb;
-            __half* w = reinterpret_cast<__half*>(tail) + row;
-#pragma unroll
-            for (int g = 0; g < RV32; ++g)
-              w[g * kWStride] = __float2half_rn(valid ? p * (__uint_as_float(vs[g] << 16) * ie) : 0.f);
-            if (lane == 0) reinterpret_cast<int*>(tail + kWBytes)[q] = m == -INFINITY ? kNoRef : static_cast<int>(m) + E;
-            arrive(misc->wfull[st.i]);
+          tc_fence_before();
+          arrive(misc->gempty[gs.i]);
+          s = valid ? s + (bias[0] + bias[1]) : -INFINITY;
+          // ---- softmax of the warp's 32 tokens: integer reference, raised lazily
+          const float mt = warp_max_redux(s);
+          if (mt > m + kRaise) {
+            const float mn = ceilf(mt);
+            l *= exp2f(m - mn);
+            m = mn;
           }
-          st.next(NS);
-          ++n;
-        };
-        if (nhg == 2) finish(half_score(), m0, l0);
-        finish(half_score(), m1, l1);
+          const float p = s == -INFINITY ? 0.f : exp2f(s - m);
+          l += p;
+          // ---- weights p * scale of each V group, relative to 2^(m + E)
+#pragma unroll
+          for (int g = 0; g < RV32; ++g)
+            sts16(tail + 2 * (g * kWStride + row), __float2half_rn(valid ? p * (__uint_as_float(vs[g] << 16) * ie) : 0.f));
+          if (lane == 0) sts32(tail + kWBytes + 4 * q, m == -INFINITY ? kNoRef : static_cast<int>(m) + E);
+          arrive(misc->wfull[st.i]);
+        }
       }
-      // ---- run end: (m, l) of each head
-      l0 = warp_sum(l0);
-      l1 = warp_sum(l1);
-      if (lane == 0) {
-        misc->ml[0][warp - 8] = make_float2(m0, l0);
-        misc->ml[nhg - 1][warp - 8] = make_float2(m1, l1);
-      }
+      // ---- run end: (m, l) of this warp's tokens
+      l = warp_sum(l);
+      if (lane == 0) misc->ml[warp - 4] = make_float2(m, l);
+      if (lane == 0 && q == 0) misc->head[grp] = held;
       named_bar_sync(kBarRun, kWorkers + 32);
     }
   } else {
-    regs_inc<112>();
+    regs_inc<136>();
     // ======================================================== V: sum_j p_j c_v,j
-    const int v = warp - 16, gid = lane >> 2, tig = lane & 3, wtid = tid - 128;
+    const int v = warp - 12, gid = lane >> 2, tig = lane & 3, wtid = tid - 128;
     const int mine = nh == 2 ? v >> 1 : 0;                        // head of the group
     const int tg0 = nh == 2 ? 2 * (v & 1) : v, ntg = nh == 2 ? 2 : 1;   // its 32-token groups
     float* accs = reinterpret_cast<float*>(sm + P.acc);            // [4][RV32 * 32]
@@ -685,12 +660,10 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         for (int hi = 0; hi < nhg; ++hi, st.next(NS)) {
           if (hi != mine) continue;
           wait(misc->wfull[st.i], st.phase);
-          wait(misc->full[st.i], st.phase);
-          const uint8_t* rows = sm + P.ring + st.i * P.stage;
-          const uint8_t* tail = rows + kTile * rb;
+          const uint32_t rows = sbase + P.ring + st.i * P.stage, tail = rows + kTile * rb;
 #pragma unroll 1
           for (int g = tg0; g < tg0 + ntg; ++g) {
-            const int r = reinterpret_cast<const int*>(tail + kWBytes)[g];
+            const int r = static_cast<int>(lds32(tail + kWBytes + 4 * g));
             if (r > ref) {
               const float f = exp2f(static_cast<float>(ref) - static_cast<float>(r));
 #pragma unroll
@@ -702,20 +675,14 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               ref = r;
             }
             const __half2 f2 = __float2half2_rn(exp2f(static_cast<float>(r) - static_cast<float>(ref)));
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-              const int t0 = 32 * g + 16 * ks + 2 * tig;
-              const __half* w = reinterpret_cast<const __half*>(tail) + gid * kWStride + t0;
-              const uint32_t b0 = h2_bits(__hmul2(*reinterpret_cast<const __half2*>(w), f2));
-              const uint32_t b1 = h2_bits(__hmul2(*reinterpret_cast<const __half2*>(w + 8), f2));
+            // tokens t0, t0 + 1 (k of the low half of B) and t0 + 8, t0 + 9 of each step of 16
+            const int t0 = 32 * g + 2 * tig;
+            uint32_t w = tail + 2 * (gid * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
+#pragma unroll 1
+            for (int ks = 0; ks < 2; ++ks, w += 32, p0 += 16 * rb) {
+              const uint32_t b0 = h2_bits(__hmul2(bits_h2(lds32(w)), f2)), b1 = h2_bits(__hmul2(bits_h2(lds32(w + 16)), f2));
+              const uint32_t p1 = p0 + rb, p8 = p0 + 8 * rb, p9 = p1 + 8 * rb;
               mma16816(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, b0, b1);
-              const uint8_t* p0 = rows + t0 * rb + rk / 2;
-              // code word `at` of tokens t0, t0 + 1 (k of the low half) and t0 + 8, t0 + 9
-              auto words = [&](int at, uint32_t sel, uint32_t& x, uint32_t& y) {
-                const uint8_t* c = p0 + 4 * at;
-                x = prmt(*reinterpret_cast<const uint32_t*>(c), *reinterpret_cast<const uint32_t*>(c + rb), sel);
-                y = prmt(*reinterpret_cast<const uint32_t*>(c + 8 * rb), *reinterpret_cast<const uint32_t*>(c + 9 * rb), sel);
-              };
               // a pair of half-words holds four columns: two MMAs of 8 + 8 rows
               auto two = [&](float (&d0)[4], float (&d1)[4], uint32_t x, uint32_t y) {
                 mma16816(d0, x & 0x000F000Fu, x & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u, b0, b1);
@@ -725,16 +692,15 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               };
 #pragma unroll
               for (int c = 0; c < F; ++c) {
-                const uint8_t* cp = p0 + 4 * (8 * c + gid);
-                const uint32_t w0 = *reinterpret_cast<const uint32_t*>(cp), w1 = *reinterpret_cast<const uint32_t*>(cp + rb);
-                const uint32_t w8 = *reinterpret_cast<const uint32_t*>(cp + 8 * rb), w9 = *reinterpret_cast<const uint32_t*>(cp + 9 * rb);
+                const uint32_t o = 4 * gid + 32 * c;
+                const uint32_t w0 = lds32(p0 + o), w1 = lds32(p1 + o), w8 = lds32(p8 + o), w9 = lds32(p9 + o);
                 two(d[4 * c], d[4 * c + 1], prmt(w0, w1, 0x5410), prmt(w8, w9, 0x5410));
                 two(d[4 * c + 2], d[4 * c + 3], prmt(w0, w1, 0x7632), prmt(w8, w9, 0x7632));
               }
               if constexpr (HF) {
-                uint32_t x, y;
-                words(8 * F + (gid >> 1), half_sel, x, y);
-                two(d[4 * F], d[4 * F + 1], x, y);
+                const uint32_t o = 4 * (gid >> 1) + 32 * F;
+                two(d[4 * F], d[4 * F + 1], prmt(lds32(p0 + o), lds32(p1 + o), half_sel),
+                    prmt(lds32(p8 + o), lds32(p9 + o), half_sel));
               }
             }
           }
@@ -772,11 +738,12 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       for (int hi = 0; hi < nhg; ++hi) {
         float M = -INFINITY, ls = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) M = fmaxf(M, misc->ml[hi][i].x);
+        for (int i = 0; i < 8; ++i)
+          if (misc->head[i >> 2] == hi) M = fmaxf(M, misc->ml[i].x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 x = misc->ml[hi][i];
-          ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // no maximum: every score was NaN
+          const float2 x = misc->ml[i];
+          if (misc->head[i >> 2] == hi) ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // (no maximum: all NaN)
         }
         float* rec = a.records + ((static_cast<int64_t>(u) + blockIdx.x) * nh + hi) * (rv + kRecordHead);
         for (int k = vt; k < rv; k += 128) {
@@ -879,9 +846,9 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     *p = Q4Plan{};
     p->nh = nh;
     p->ngroups = (H + nh - 1) / nh;
-    p->z_bias = make_chunk_plan(r_k, kTile).bytes;
-    p->z_stride = p->z_bias + 4096;
-    p->NA = 2 * (r_k / 2 + 8) <= 512 - kACol ? 2 : 1;
+    p->N = r_k + 16;
+    p->NG = std::min(kMaxG, (512 - kGCol) / p->N);
+    p->z_stride = (p->N * 256 + 1023) / 1024 * 1024;
     p->stage = al(kTile * rb + kStageTail, 128);
     int off = 0;
     p->z = off; off += nh * p->z_stride;
