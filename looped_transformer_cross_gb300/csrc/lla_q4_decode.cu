@@ -340,25 +340,34 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         for (int row = rk + 2 + gk; row < N; ++row) sts16(at(hi, row, 64 * part + f), __ushort_as_half(0));
       }
     }
-    named_bar_sync(kBarWork, kWorkers);
     // item = (head, scale group, 4 frequencies, 8 columns); the four of a scale group are neighbouring
-    // lanes (whole warps take part: 64 gk items per head)
+    // lanes (whole warps take part: 64 gk items per head).  A thread's first weights are
+    // requested before the barrier.
+    uint4 w0[4], w1[4];
+    auto fetch = [&](int i) {
+      const int o = i & 3, f0 = (i >> 2 & 15) * 4, hg = i >> 6, hi = hg / gk, g = hg - hi * gk, n = 32 * g + 8 * o;
+      if (i >= nhg * gk * 64 || n >= rk) return;
+      const __nv_bfloat16* W =
+          static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(run.hg * nh + hi) * kHeadDim * rk + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int f = f0 + e;
+        const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
+        w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0) * rk));
+        w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1) * rk));
+      }
+    };
+    fetch(wtid);
+    named_bar_sync(kBarWork, kWorkers);
     for (int i = wtid; i < nhg * gk * 64; i += kWorkers) {
       const int o = i & 3, f0 = (i >> 2 & 15) * 4, hg = i >> 6, hi = hg / gk, g = hg - hi * gk, n = 32 * g + 8 * o;
-      const int h = run.hg * nh + hi;
       float sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
       if (n < rk) {
-        const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk + n;
-        uint4 w0[4], w1[4];
         float q0[4], q1[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int f = f0 + e;
-          const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
-          w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0) * rk));
-          w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1) * rk));
-          q0[e] = misc->qs[hi][0][f];
-          q1[e] = misc->qs[hi][1][f];
+          q0[e] = misc->qs[hi][0][f0 + e];
+          q1[e] = misc->qs[hi][1][f0 + e];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -392,6 +401,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         sts64(at(hi, rk + 2 + g, f0), h2_bits(__floats2half2_rn(sum_c[0], sum_c[1])), h2_bits(__floats2half2_rn(sum_c[2], sum_c[3])));
         sts64(at(hi, rk + 2 + g, 64 + f0), h2_bits(__floats2half2_rn(sum_s[0], sum_s[1])), h2_bits(__floats2half2_rn(sum_s[2], sum_s[3])));
       }
+      fetch(i + kWorkers);
     }
     if (amax > 65504.f) record_status(a.status, LLA_ERR_RANGE);   // NaN queries stay NaN
     fence_proxy_async_smem();
@@ -493,18 +503,22 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
     float tc[32], ts[32];   // cos and sin of the own row, frequencies 32 grp + i
     // rows of tile t from the table, through shared memory (a thread's own row straight from
-    // global memory would touch 32 lines per load)
+    // global memory would touch 32 lines per load): every load first, then the exchange
     auto seed = [&](int t) {
+      float4 raw[16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int64_t j = static_cast<int64_t>(t) * kTile + 32 * q + 16 * i + (lane >> 1);
+        j = (j < a.rope_len ? j : a.rope_len - 1) * 64 + 32 * grp + 4 * (lane & 1);   // behind the sequence's end: masked
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          raw[2 * p + i] = __ldg(reinterpret_cast<const float4*>((p < 4 ? a.rope_cos : a.rope_sin) + j + 8 * (p & 3)));
+      }
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 16 * i + (lane >> 1);
-          int64_t j = static_cast<int64_t>(t) * kTile + 32 * q + r;
-          j = j < a.rope_len ? j : a.rope_len - 1;    // behind the sequence's end: masked
-          *reinterpret_cast<float4*>(stage + r * kTrigRow + 4 * (lane & 1)) = __ldg(
-              reinterpret_cast<const float4*>((p < 4 ? a.rope_cos : a.rope_sin) + j * 64 + 32 * grp + 8 * (p & 3) + 4 * (lane & 1)));
-        }
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float4*>(stage + (16 * i + (lane >> 1)) * kTrigRow + 4 * (lane & 1)) = raw[2 * p + i];
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -570,6 +584,11 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           if (grp != static_cast<int>(n & 1)) continue;
           const uint32_t base = sbase + P.ring + st.i * P.stage, tail = base + kTile * rb, r = base + row * rb;
           wait(misc->full[st.i], st.phase);
+          wait(misc->gfull[gs.i], gs.phase);
+          tc_fence_after();
+          const uint32_t gcol = tmem + lane_base + kGCol + gs.i * N;
+          float bias[2], s = 0.f;
+          tmem_ld_x2(gcol + rk, bias);
           // ---- V scales; 2^E is above every one of the warp's tokens
           uint32_t vtop = 0, vs[RV32];
 #pragma unroll
@@ -579,34 +598,28 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           }
           const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, valid ? vtop >> 7 : 0u)) - 126, 126);
           const float ie = pow2(-E);
-          wait(misc->gfull[gs.i], gs.phase);
-          tc_fence_after();
-          const uint32_t gcol = tmem + lane_base + kGCol + gs.i * N;
-          float bias[2];
-          tmem_ld_x2(gcol + rk, bias);
-          float s = 0.f;
           // ---- per scale group: 32 codes against G (a last group of 16: its other codes count as 0)
 #pragma unroll 1
           for (int g = 0; g < gk; ++g) {
-            uint4 w = lds128(r + 16 * g);
-            const float sc = __uint_as_float(lds16(r + scale_at + 2 * g) << 16);
             float G[32], off[1];
             tmem_ld_x32(gcol + 32 * g, G);
             tmem_ld_x1(gcol + rk + 2 + g, off);
-            if (32 * g + 32 > rk) w.z = w.w = 0;
+            uint4 w4 = lds128(r + 16 * g);
+            const float sc = __uint_as_float(lds16(r + scale_at + 2 * g) << 16);
+            if (32 * g + 32 > rk) w4.z = w4.w = 0;
             tmem_wait_ld();
             float lo0 = 0.f, lo1 = 0.f, hi0 = 0.f, hi1 = 0.f;
-            uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const float2 x = __half22float2(bits_h2(ww[i] & 0x000F000Fu)), y = __half22float2(bits_h2(ww[i] & 0x00F000F0u));
-                ww[i] >>= 8;
-                lo0 = fmaf(x.x, G[8 * i + 4 * j], lo0);
-                lo1 = fmaf(x.y, G[8 * i + 4 * j + 1], lo1);
-                hi0 = fmaf(y.x, G[8 * i + 4 * j + 2], hi0);
-                hi1 = fmaf(y.y, G[8 * i + 4 * j + 3], hi1);
+                const float2 c = __half22float2(bits_h2(w[i] & 0x000F000Fu)), d = __half22float2(bits_h2(w[i] & 0x00F000F0u));
+                w[i] >>= 8;
+                lo0 = fmaf(c.x, G[8 * i + 4 * j], lo0);
+                lo1 = fmaf(c.y, G[8 * i + 4 * j + 1], lo1);
+                hi0 = fmaf(d.x, G[8 * i + 4 * j + 2], hi0);
+                hi1 = fmaf(d.y, G[8 * i + 4 * j + 3], hi1);
               }
             s = fmaf(sc, fmaf(lo0 + lo1, 16777216.f, fmaf(hi0 + hi1, 1048576.f, off[0])), s);
           }
@@ -772,60 +785,71 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 }
 
 // Merge the records of each (sequence, head) by log-sum-exp, apply W_up,v once (Appendix J
-// "Absorbed attention") and normalise.  Block = (head, a.combine_units sequences).
-constexpr int kCombineThreads = 128;
+// "Absorbed attention") and normalise.  Block = (head, a.combine_units sequences), a warp
+// merging a sequence at a time, then two threads per output, each with half of its row of
+// W_up,v in registers: requested before the wait for the decode grid, they serve every sequence.
+constexpr int kCombineThreads = 256;
 constexpr int kMaxCombineUnits = 8;
+template <int RV32>
 __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
-  __shared__ float acc[kMaxCombineUnits][kMaxRankPerHead], inv[kMaxCombineUnits];
+  constexpr int kRegs = 2 * RV32;   // 16-byte loads of half a row, rounded up
+  __shared__ float acc[kMaxCombineUnits][RV32 * 32], inv[kMaxCombineUnits];
   const int h = blockIdx.x % a.H, b0 = static_cast<int>(blockIdx.x / a.H) * a.combine_units, tid = threadIdx.x;
-  const int rv = a.r_v, nh = a.plan.nh, nu = min(a.combine_units, a.B - b0);
+  const int rv = a.r_v, nh = a.plan.nh, nu = min(a.combine_units, a.B - b0), warp = tid >> 5, lane = tid & 31;
+  const int e = tid >> 1, half = tid & 1;   // output, and which 8-column pieces of its row: half, half + 2, ..
+  uint4 w[kRegs];
+  const uint4* W = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w_up_v) +
+                                                  (static_cast<int64_t>(h) * kHeadDim + e) * rv);
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) w[i] = 8 * (2 * i + half) < rv ? __ldg(W + 2 * i + half) : make_uint4(0, 0, 0, 0);
+  const float mu = __ldg(a.mu_v + h * a.mu_hstride + e);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = 0; i < nu; ++i) {
+  for (int i = warp; i < nu; i += kCombineThreads / 32) {
     const int b = b0 + i, u = b * a.plan.ngroups + h / nh;
-    const int L = tile_len(a, b);
-    float v0 = 0.f, v1 = 0.f, l = 1.f, m = -INFINITY;
-    if (L > 0) {
-      const int c0 = a.ranges[2 * u], c1 = a.ranges[2 * u + 1];
+    float v[RV32], l = 1.f, m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < RV32; ++k) v[k] = 0.f;
+    if (tile_len(a, b) > 0) {
+      const int2 c = *reinterpret_cast<const int2*>(a.ranges + 2 * u);
       const int64_t stride = static_cast<int64_t>(nh) * (rv + kRecordHead);
-      const float* rec = a.records + (static_cast<int64_t>(u) + c0) * stride + (h % nh) * (rv + kRecordHead);
-      for (int c = 0; c <= c1 - c0; ++c) m = fmaxf(m, rec[c * stride]);
+      const float* rec = a.records + (static_cast<int64_t>(u) + c.x) * stride + (h % nh) * (rv + kRecordHead);
+      const int n = c.y - c.x + 1;
+      for (int j = lane; j < n; j += 32) m = fmaxf(m, rec[j * stride]);
+      m = warp_max(m);
       l = 0.f;
-      for (int c = 0; c <= c1 - c0; ++c) {
-        const float* r = rec + c * stride;
-        const float w = m == -INFINITY ? 1.f : exp2f(r[0] - m);
-        l = fmaf(r[1], w, l);
-        if (tid < rv) v0 = fmaf(r[kRecordHead + tid], w, v0);
-        if (tid + 128 < rv) v1 = fmaf(r[kRecordHead + tid + 128], w, v1);
+      for (int j = 0; j < n; ++j) {
+        const float* r = rec + j * stride;
+        const float f = m == -INFINITY ? 1.f : exp2f(r[0] - m);   // no maximum: every score was NaN, and so is l
+        l = fmaf(r[1], f, l);
+#pragma unroll
+        for (int k = 0; k < RV32; ++k)
+          if (32 * k + lane < rv) v[k] = fmaf(r[kRecordHead + 32 * k + lane], f, v[k]);
       }
     }
-    if (tid < rv) acc[i][tid] = v0;
-    if (tid + 128 < rv) acc[i][tid + 128] = v1;
-    if (tid == 0) {
+#pragma unroll
+    for (int k = 0; k < RV32; ++k) acc[i][32 * k + lane] = v[k];
+    if (lane == 0) {
       inv[i] = 1.f / l;
-      if (a.lse) a.lse[static_cast<int64_t>(b) * a.H + h] = L > 0 ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (a.lse) a.lse[static_cast<int64_t>(b) * a.H + h] = m == -INFINITY && l == 1.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
   }
   __syncthreads();
-  const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * rv;
-  float o[kMaxCombineUnits];
+  for (int i = 0; i < nu; ++i) {
+    float o = 0.f;
 #pragma unroll
-  for (int i = 0; i < kMaxCombineUnits; ++i) o[i] = 0.f;
-  for (int k = 0; k < rv; k += 8) {
-    float w8[8];
-    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + k)), w8);
+    for (int k = 0; k < kRegs; ++k) {
+      const int c = 8 * (2 * k + half);
+      if (c >= rv) break;
+      float w8[8];
+      unpack_bf16x8(w[k], w8);
 #pragma unroll
-    for (int i = 0; i < kMaxCombineUnits; ++i) {
-      if (i >= nu) break;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[i] = fmaf(acc[i][k + e], w8[e], o[i]);
+      for (int j = 0; j < 8; ++j) o = fmaf(acc[i][c + j], w8[j], o);
     }
-  }
-  const float mu = __ldg(a.mu_v + h * a.mu_hstride + tid);
-#pragma unroll
-  for (int i = 0; i < kMaxCombineUnits; ++i) {
-    if (i >= nu) break;
-    const float y = tile_len(a, b0 + i) > 0 ? fmaf(o[i], inv[i], mu) : 0.f;
-    static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(b0 + i) * a.H + h) * kHeadDim + tid] = __float2bfloat16_rn(y);
+    o += __shfl_xor_sync(0xffffffffu, o, 1);
+    const int b = b0 + i;
+    if (half == 0)
+      static_cast<__nv_bfloat16*>(a.out)[(static_cast<int64_t>(b) * a.H + h) * kHeadDim + e] =
+          __float2bfloat16_rn(tile_len(a, b) > 0 ? fmaf(o, inv[i], mu) : 0.f);
   }
 }
 
@@ -834,7 +858,9 @@ cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem(q4_tile_kernel<RV32>, a.plan.bytes);
   if (e != cudaSuccess) return e;
   q4_tile_kernel<RV32><<<a.grid, kQ4TileThreads, a.plan.bytes, s>>>(a);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int blocks = a.H * ((a.B + a.combine_units - 1) / a.combine_units);
+  return launch_pdl(q4_combine_kernel<RV32>, dim3(blocks), dim3(kCombineThreads), 0, s, a);
 }
 
 }  // namespace
@@ -866,20 +892,16 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
 }
 
 cudaError_t launch_q4_tile(const Q4DecodeArgs& a, cudaStream_t s) {
-  cudaError_t e;
   switch ((a.r_v + 31) / 32) {
-    case 1: e = launch_tile<1>(a, s); break;
-    case 2: e = launch_tile<2>(a, s); break;
-    case 3: e = launch_tile<3>(a, s); break;
-    case 4: e = launch_tile<4>(a, s); break;
-    case 5: e = launch_tile<5>(a, s); break;
-    case 6: e = launch_tile<6>(a, s); break;
-    case 7: e = launch_tile<7>(a, s); break;
-    default: e = launch_tile<8>(a, s); break;
+    case 1: return launch_tile<1>(a, s);
+    case 2: return launch_tile<2>(a, s);
+    case 3: return launch_tile<3>(a, s);
+    case 4: return launch_tile<4>(a, s);
+    case 5: return launch_tile<5>(a, s);
+    case 6: return launch_tile<6>(a, s);
+    case 7: return launch_tile<7>(a, s);
+    default: return launch_tile<8>(a, s);
   }
-  if (e != cudaSuccess) return e;
-  const int blocks = a.H * ((a.B + a.combine_units - 1) / a.combine_units);
-  return launch_pdl(q4_combine_kernel, dim3(blocks), dim3(kCombineThreads), 0, s, a);
 }
 
 }  // namespace lla
