@@ -426,10 +426,10 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
 }
 
 // Workspace of a decode call: status word; tensor-core kernel: the CTA range of every
-// (sequence, head group), then a record per head of every (unit, CTA) of a run (at most
-// units + grid of them); fp32 kernel: a record per split.
+// (sequence, head group), a record per head of every (unit, CTA) of a run (at most
+// units + grid of them), the f16 rotary tiles of L_max positions; fp32 kernel: a record per split.
 struct Q4Ws {
-  size_t ranges, records, total;
+  size_t ranges, records, row_tiles, total;
   int grid;
 };
 Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
@@ -443,7 +443,8 @@ Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
     const int64_t units = static_cast<int64_t>(B) * p.ngroups;
     w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), units * tiles)));
     w.records = (256 + static_cast<size_t>(units) * 8 + 255) / 256 * 256;
-    w.total = w.records + (static_cast<size_t>(units) + w.grid) * p.nh * rec;
+    w.row_tiles = (w.records + (static_cast<size_t>(units) + w.grid) * p.nh * rec + 255) / 256 * 256;
+    w.total = w.row_tiles + static_cast<size_t>(tiles) * kTile * 256;
     return w;
   }
   const int64_t chunk = q4_plain_chunk(std::max(B, 1), d->H, std::max<int64_t>(L_max, 1), sms) / kTile;
@@ -538,6 +539,8 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
     if (!make_q4_plan(a.H, a.r_k, a.r_v, &a.plan)) return LLA_ERR_UNSUPPORTED;
     a.ranges = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.ranges);
     a.grid = w.grid;
+    a.row_tiles = static_cast<uint8_t*>(workspace) + w.row_tiles;
+    a.rows_grid = static_cast<int>(std::min<int64_t>((L_max + kTile - 1) / kTile, 4 * sms));
     // sequences per combine block: W_up,v is read once for them; about four blocks per SM
     a.combine_units = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, static_cast<int64_t>(a.B) * a.H / (4 * sms))));
     return launch_q4_tile(a, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;

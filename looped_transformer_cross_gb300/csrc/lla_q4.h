@@ -27,9 +27,11 @@ __host__ __device__ inline int q4_row_bytes(int r_k, int r_v) {
 struct Q4Plan {
   int nh, ngroups;                   // heads of a group (1 or 2), groups of a sequence
   int NS, NG;                        // ring stages, G buffers in TMEM
-  int N;                             // rows of a query operand = columns of G: r_k + 16
-  int z, z_stride;                   // query operands, one per head of the group
-  int trig, acc, misc, ring, stage;
+  int N;                             // rows of a head's query operand = columns of G: r_k + 16
+  int z, z_chunk;                    // query operands of the group's heads: two chunks of coordinates
+  int rows;                          // two rotary tiles
+  int misc, ring, stage;
+  int w_bytes;                       // V weights of a stage
   int bytes;                         // total dynamic smem incl. alignment slack
 };
 // False where no plan fits (never for ranks up to kMaxRankPerHead).
@@ -58,7 +60,9 @@ struct Q4DecodeArgs {
   float* records;                    // split records: {m (log2 units), l, -, -, acc[r_v]}
   int64_t chunk;                     // fp32 kernel: tokens of a split
   int splits;                        // fp32 kernel: splits of a (sequence, head)
-  int32_t* ranges;                   // tensor-core kernel: first and last CTA of each (sequence, head group)
+  uint8_t* row_tiles;                // tensor-core kernel: f16 rotary rows, 32 KB per 128 positions
+  int rows_grid;
+  int32_t* ranges;                   // first and last CTA of each (sequence, head group)
   int grid;
   int combine_units;                 // sequences per combine block (1..8)
   Q4Plan plan;

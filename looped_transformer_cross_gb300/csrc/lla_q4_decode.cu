@@ -10,13 +10,14 @@
 // A 4-bit row is 144 bytes at (96, 160), 3.6 times less than in bf16: at HBM speed an SM has about
 // 6 cycles per token-head, and what bounds the kernel is instruction issue; the choices
 // below are for few instructions per code.
-//   G  A = the rotary rows, f16 in TMEM, shared by the heads of a position.  Their fp32 values stay in
-//      the registers of the two epilogue warpgroups (32 frequencies each), turned by one tile's
-//      angle (table row 128) from tile to tile: rows read from L2 (64 KB a tile) would be more
-//      traffic than the latents.  B = the head's Z rows (f16, resident for the whole run), two bias rows
-//      (f16 high and low part) and one row -8 sum Z per scale group, which takes the codes'
-//      offset back.
-//   s  One token per thread, the two warpgroups alternate head-tiles.  Codes are masked into f16
+//   G  A = the rotary rows, f16, one 32 KB tile per position for all of its heads.  They are
+//      rounded once per call from the fp32 table into tiles in the layout that the MMA reads
+//      (q4_rows_kernel), so that one bulk copy brings a tile: an fp32 table read here would be
+//      more L2 traffic than the latents, and rows turned in registers from tile to tile cost a fifth of all
+//      instructions (measured: 144 us against the present time at 32 x 4096).
+//      B = the head's Z rows (f16, resident for the whole run), two bias rows (f16 high
+//      and low part) and one row -8 sum Z per scale group, which takes the codes' offset back.
+//   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
 //      subnormals (code * 2^-24, or * 2^-20 from the next nibble), converted, and summed per
 //      scale group in fp32; the group's scale multiplies the sum.
 //   V  sum_j p_j c_v,j is a warp-level MMA: A = the codes themselves, as f16 subnormals (masking is
@@ -28,7 +29,7 @@
 // equal contiguous ranges, one per CTA.  A run is a CTA's part of one (sequence, head
 // group); the query operand of its nh heads is built in shared memory at its start, and
 // one record {m, l, acc} per head is written at its end.  Warps: 0 producer (bulk
-// copies of page pieces into the ring), 1 MMA issuer, 4-11 epilogue, 12-15 V.
+// copies of page pieces and rotary tiles), 1 MMA issuer, 4-11 epilogue, 12-19 V.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -39,41 +40,29 @@ namespace lla {
 
 namespace {
 
-constexpr int kQ4TileThreads = 512;
-constexpr int kWorkers = 384;                    // epilogue and V warpgroups
+constexpr int kQ4TileThreads = 640;
+constexpr int kWorkers = 512;                    // epilogue and V warpgroups
 constexpr int kQ4MaxNS = 16;
 constexpr int kMaxG = 4;                         // G buffers
+constexpr int kRowTile = 32768;                  // rotary tile: two K-major chunks of 128 rows x 128 bytes
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
-constexpr int kWBytes = 8 * kWStride * 2;
-constexpr int kStageTail = kWBytes + 64;         // weights, then the four references
-constexpr int kTrigRow = 12;                     // words of a staged row of 8 table values
-constexpr int kTrigBytes = 8 * 32 * kTrigRow * 4;
-constexpr int kACol = 0;                         // TMEM: two buffers of rotary rows, 64 columns each
-constexpr int kGCol = 128;                       // then the G buffers
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
-constexpr int kSeedTiles = 512;                  // tiles between reads of the table (a power of two)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
 constexpr int kNoRef = -(1 << 28);
 enum { kBarRun = 1, kBarWork = 2 };              // named barriers: workers + MMA warp; workers
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
-  uint64_t afull[2], aempty[2], gfull[kMaxG], gempty[kMaxG];
+  uint64_t rfull[2], rempty[2], gfull[kMaxG], gempty[kMaxG];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
   int start_b, start_hg, start_t, count;
-  int scan[kQ4TileThreads];
   float2 ml[8];                                  // run end: (m, l) of each epilogue warp
   int head[2];                                   // run end: the head that each epilogue group held
-  int vref[4];                                   // run end: reference of each V warp
+  int vref[8];                                   // run end: reference of each V warp
   float qs[2][2][64];                            // rotated query, sc q'_i0 and sc q'_i1, per head
-  alignas(16) float tile_cos[64];                // table row 128: one tile's angles
-  float tile_sin[64];                            // (follows tile_cos: read by 16-byte loads)
 };
-
-static_assert(offsetof(Q4Misc, tile_cos) % 16 == 0 && offsetof(Q4Misc, tile_sin) == offsetof(Q4Misc, tile_cos) + 256,
-              "read as 16-byte vectors");
 
 struct Slot {
   int i;
@@ -185,8 +174,8 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
-// Register shares of the warpgroups: 72 + 2 x 152 + 136 = 512 = 4 x 128, what the
-// block is launched with (512 threads of 128).
+// Register shares of the warpgroups: 48 + 2 x 104 + 2 x 112 = 480 = 5 x 96, what the
+// block is launched with (640 threads of 96).
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -210,6 +199,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   const int scale_at = q4_scale_offset(rk, rv), gk = q4_groups(rk);
 
   // ---------------------------------------------------------- work range
+  int* scan = reinterpret_cast<int*>(sm + P.ring);   // (before any copy)
   RunWalker start{0, 0, 0, 0};
   {
     const int per_thr = (a.B + kQ4TileThreads - 1) / kQ4TileThreads;
@@ -220,13 +210,13 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       if (blockIdx.x == 0 && (L0 < 0 || L0 > a.L_max || qp < 0 || qp >= a.rope_len)) record_status(a.status, LLA_ERR_DEVICE_ARG);
       local += tiles_of(tile_len(a, b));
     }
-    misc->scan[tid] = static_cast<int>(local);
+    scan[tid] = static_cast<int>(local);
     if (tid == 0) { misc->abort = 0; misc->count = 0; }
     __syncthreads();
     if (warp == 0) {
       constexpr int kPer = kQ4TileThreads / 32;
       int s = 0;
-      for (int i = 0; i < kPer; ++i) s += misc->scan[lane * kPer + i];
+      for (int i = 0; i < kPer; ++i) s += scan[lane * kPer + i];
       int incl = s;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -235,8 +225,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       }
       int excl = incl - s;
       for (int i = 0; i < kPer; ++i) {
-        const int v = misc->scan[lane * kPer + i];
-        misc->scan[lane * kPer + i] = excl;
+        const int v = scan[lane * kPer + i];
+        scan[lane * kPer + i] = excl;
         excl += v;
       }
       if (lane == 31) misc->start_t = incl;   // total tiles, read below
@@ -245,7 +235,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     const long long total = static_cast<long long>(misc->start_t) * ngroups;
     const long long per = max(1LL, (total + a.grid - 1) / a.grid);
     const long long f0 = static_cast<long long>(blockIdx.x) * per, f1 = min(total, f0 + per);
-    long long p0 = static_cast<long long>(misc->scan[tid]) * ngroups;
+    long long p0 = static_cast<long long>(scan[tid]) * ngroups;
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
       const long long nb = static_cast<long long>(tiles_of(tile_len(a, b)));
@@ -267,12 +257,12 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar(misc->full[s]), 1);
-      mbar_init(bar(misc->empty[s]), 4 / nh);       // the head's V warps, the last to read it
+      mbar_init(bar(misc->empty[s]), 8 / nh);       // the head's V warps, the last to read it
       mbar_init(bar(misc->wfull[s]), 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(misc->afull[i]), 8);
-      mbar_init(bar(misc->aempty[i]), 1);
+      mbar_init(bar(misc->rfull[i]), 1);
+      mbar_init(bar(misc->rempty[i]), 1);
     }
     for (int i = 0; i < NG; ++i) {
       mbar_init(bar(misc->gfull[i]), 1);
@@ -280,11 +270,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     }
     mbar_init(bar(misc->mma_done), 1);
     fence_mbar_init();
-  }
-  if (tid >= 64 && tid < 128 && a.rope_len > kTile) {   // (at most 128 positions: one tile, no step)
-    const int f = tid - 64;
-    misc->tile_cos[f] = __ldg(a.rope_cos + kTile * 64 + f);
-    misc->tile_sin[f] = __ldg(a.rope_sin + kTile * 64 + f);
   }
   if (warp == 1) {
     __syncwarp();
@@ -308,17 +293,18 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     if (lane == 0) mbar_arrive(bar(m));
   };
 
-  // Builds the run's query operands, per head N rows of 128 rotary coordinates in two K-major
-  // chunks of 64 (128-byte swizzle): r_k Z rows, bias high and low, -8 sum Z of each scale
+  // Builds the run's query operands, N rows of 128 rotary coordinates per head, all heads' rows
+  // in two K-major chunks of 64 coordinates (128-byte swizzle); a head's are its r_k Z rows, bias high and low, -8 sum Z of each scale
   // group, zeros.  All workers; the previous run has ended.
   auto build = [&](int wtid) {
     const int nhg = min(nh, a.H - run.hg * nh);
     int qp = __ldg(a.q_pos + run.b);
     qp = qp < 0 ? 0 : (qp >= a.rope_len ? static_cast<int>(a.rope_len - 1) : qp);
-    float amax = 0.f;
+    __half2 top = __half2half2(__ushort_as_half(0));   // largest magnitude written (infinite: out of range)
     auto at = [&](int hi, int row, int coord) {   // address of 8-byte aligned coordinates of a row
-      return sbase + P.z + hi * P.z_stride + (coord >> 6) * N * 128 + swizzle_offset(row * 128 + 2 * (coord & 63), 128);
+      return sbase + P.z + (coord >> 6) * P.z_chunk + swizzle_offset((hi * N + row) * 128 + 2 * (coord & 63), 128);
     };
+    named_bar_sync(kBarWork, kWorkers);   // the last run's records are written: its sums lie in the rows' place
     for (int i = wtid; i < nhg * 64; i += kWorkers) {
       const int hi = i >> 6, f = i & 63, h = run.hg * nh + hi;
       const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
@@ -334,7 +320,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         const __half high = __float2half_rn(bias[part]);
-        amax = fmaxf(amax, fabsf(bias[part]));
+        top = __hmax2(top, __habs2(__half2half2(high)));
         sts16(at(hi, rk, 64 * part + f), high);
         sts16(at(hi, rk + 1, 64 * part + f), __float2half_rn(bias[part] - __half2float(high)));
         for (int row = rk + 2 + gk; row < N; ++row) sts16(at(hi, row, 64 * part + f), __ushort_as_half(0));
@@ -371,21 +357,24 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          __half zc[4], zs[4];
+          float zc[4], zs[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t x0 = (&w0[e].x)[j >> 1], x1 = (&w1[e].x)[j >> 1];
             const float u = __uint_as_float(j & 1 ? x0 & 0xFFFF0000u : x0 << 16);
             const float v = __uint_as_float(j & 1 ? x1 & 0xFFFF0000u : x1 << 16);
-            zc[e] = __float2half_rn(q0[e] * u + q1[e] * v);
-            zs[e] = __float2half_rn(q1[e] * u - q0[e] * v);
-            const float cf = __half2float(zc[e]), sf = __half2float(zs[e]);
-            sum_c[e] += cf;
-            sum_s[e] += sf;
-            amax = fmaxf(amax, fmaxf(fabsf(cf), fabsf(sf)));
+            zc[e] = fmaf(q0[e], u, q1[e] * v);
+            zs[e] = fmaf(q1[e], u, -q0[e] * v);
           }
-          sts64(at(hi, n + j, f0), h2_bits(__halves2half2(zc[0], zc[1])), h2_bits(__halves2half2(zc[2], zc[3])));
-          sts64(at(hi, n + j, 64 + f0), h2_bits(__halves2half2(zs[0], zs[1])), h2_bits(__halves2half2(zs[2], zs[3])));
+          const __half2 c0 = __floats2half2_rn(zc[0], zc[1]), c1 = __floats2half2_rn(zc[2], zc[3]);
+          const __half2 s0 = __floats2half2_rn(zs[0], zs[1]), s1 = __floats2half2_rn(zs[2], zs[3]);
+          top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
+          // (the sums of what the MMA reads: of the rounded values)
+          const float2 cf0 = __half22float2(c0), cf1 = __half22float2(c1), sf0 = __half22float2(s0), sf1 = __half22float2(s1);
+          sum_c[0] += cf0.x; sum_c[1] += cf0.y; sum_c[2] += cf1.x; sum_c[3] += cf1.y;
+          sum_s[0] += sf0.x; sum_s[1] += sf0.y; sum_s[2] += sf1.x; sum_s[3] += sf1.y;
+          sts64(at(hi, n + j, f0), h2_bits(c0), h2_bits(c1));
+          sts64(at(hi, n + j, 64 + f0), h2_bits(s0), h2_bits(s1));
         }
       }
       // the codes' offset: -8 sum Z over the scale group's columns
@@ -395,32 +384,45 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         sum_s[e] += __shfl_xor_sync(0xffffffffu, sum_s[e], 1);
         sum_c[e] = -8.f * (sum_c[e] + __shfl_xor_sync(0xffffffffu, sum_c[e], 2));
         sum_s[e] = -8.f * (sum_s[e] + __shfl_xor_sync(0xffffffffu, sum_s[e], 2));
-        amax = fmaxf(amax, fmaxf(fabsf(sum_c[e]), fabsf(sum_s[e])));
       }
       if (o == 0) {
-        sts64(at(hi, rk + 2 + g, f0), h2_bits(__floats2half2_rn(sum_c[0], sum_c[1])), h2_bits(__floats2half2_rn(sum_c[2], sum_c[3])));
-        sts64(at(hi, rk + 2 + g, 64 + f0), h2_bits(__floats2half2_rn(sum_s[0], sum_s[1])), h2_bits(__floats2half2_rn(sum_s[2], sum_s[3])));
+        const __half2 c0 = __floats2half2_rn(sum_c[0], sum_c[1]), c1 = __floats2half2_rn(sum_c[2], sum_c[3]);
+        const __half2 s0 = __floats2half2_rn(sum_s[0], sum_s[1]), s1 = __floats2half2_rn(sum_s[2], sum_s[3]);
+        top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
+        sts64(at(hi, rk + 2 + g, f0), h2_bits(c0), h2_bits(c1));
+        sts64(at(hi, rk + 2 + g, 64 + f0), h2_bits(s0), h2_bits(s1));
       }
       fetch(i + kWorkers);
     }
-    if (amax > 65504.f) record_status(a.status, LLA_ERR_RANGE);   // NaN queries stay NaN
+    if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) record_status(a.status, LLA_ERR_RANGE);   // (NaN queries stay NaN)
     fence_proxy_async_smem();
     named_bar_sync(kBarRun, kWorkers + 32);
   };
 
   if (warp < 4) {
-    regs_dec<72>();
+    regs_dec<48>();
     if (warp == 0) {
       // ======================================================== producer
-      // Per head-tile: the page pieces that its rows lie in, lane i copying piece i.
-      Slot st{0, 0u};
-      int issued = 0;
+      // Per position the rotary tile, per head-tile the page pieces that its rows lie in, lane i
+      // copying piece i.
+      Slot st{0, 0u}, rs{0, 0u};
+      int issued = 0, tiles = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotary tiles are written
       while (walk.next(a, ngroups, run)) {
         const int nhg = min(nh, a.H - run.hg * nh);
         for (int t = run.t0; t < run.t0 + run.n && ok; ++t) {
           const int y0 = t * kTile, y1 = min(y0 + kTile, run.L), pg = a.page_size;
           const int lp0 = y0 / pg, np = (y1 - 1) / pg - lp0 + 1;
           const int32_t* table = a.block_table + static_cast<int64_t>(run.b) * a.max_pages + lp0;
+          wait(misc->rempty[rs.i], rs.phase ^ 1u);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(misc->rfull[rs.i]), kRowTile);
+            bulk_load(sbase + P.rows + rs.i * kRowTile, a.row_tiles + static_cast<int64_t>(t) * kRowTile, kRowTile,
+                      bar(misc->rfull[rs.i]));
+          }
+          ++tiles;
+          rs.next(2);
           for (int hi = 0; hi < nhg && ok; ++hi) {
             wait(misc->empty[st.i], st.phase ^ 1u);
             if (!ok) break;
@@ -444,47 +446,59 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       }
       // let every copy land before the CTA can exit
-      // (st is the next stage: the oldest of the last NS copies, or not yet used)
-      if (lane == 0)
-        for (int i = min(issued, NS); i > 0; --i) {
-          if (issued < NS && i == issued) st = Slot{0, 0u};
-          const uint32_t phase = issued < NS ? 0u : st.phase ^ 1u;
+      // (the next slot holds the oldest of the last n copies, or was not yet used)
+      auto land = [&](uint64_t* full, Slot at, int n, int count) {
+        for (int i = min(count, n); i > 0; --i) {
+          if (count < n && i == count) at = Slot{0, 0u};
+          const uint32_t phase = count < n ? 0u : at.phase ^ 1u;
           const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(bar(misc->full[st.i]), phase) && global_timer_ns() - t0 < kWaitLimitNs) {}
-          st.next(NS);
+          while (!mbar_try_wait(bar(full[at.i]), phase) && global_timer_ns() - t0 < kWaitLimitNs) {}
+          at.next(n);
         }
+      };
+      if (lane == 0) {
+        land(misc->full, st, NS, issued);
+        land(misc->rfull, rs, 2, tiles);
+      }
     } else if (warp == 1) {
       // ======================================================== MMA issuer
-      // G = R Z^T per head-tile; the whole warp runs the loop, one elected lane issues
-      const uint32_t idesc = umma_idesc_f16(128, min(N, 256)), tail_idesc = umma_idesc_f16(128, 16);
-      Slot as{0, 0u}, gs{0, 0u};
+      // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
+      // step takes about as long for 256 columns as for 128, so the heads of a position share
+      // one chain where their rows fit; else each has its own (two where r_k = 256).
+      const bool together = 2 * N <= 256;
+      Slot rs{0, 0u}, gs{0, 0u};
       while (walk.next(a, ngroups, run)) {
         const int nhg = min(nh, a.H - run.hg * nh);
         named_bar_sync(kBarRun, kWorkers + 32);   // operands built
         for (int t = 0; t < run.n; ++t) {
-          wait(misc->afull[as.i], as.phase);
-          for (int hi = 0; hi < nhg; ++hi) {
+          wait(misc->rfull[rs.i], rs.phase);
+          const uint64_t ad = umma_desc(sbase + P.rows + rs.i * kRowTile, 16, 1024, kSw128);
+          for (int hi = 0, heads; hi < nhg; hi += heads) {
+            heads = together && nhg - hi == 2 && gs.i + 1 < NG ? 2 : 1;   // two: into neighbouring buffers
+            Slot last = gs;
             wait(misc->gempty[gs.i], gs.phase ^ 1u);
+            if (heads == 2) {
+              last.next(NG);
+              wait(misc->gempty[last.i], last.phase ^ 1u);
+            }
             if (ok) {
               tc_fence_after();
-              const uint32_t d = tmem + kGCol + gs.i * N, ac = tmem + kACol + 64 * as.i;
-              const uint32_t z = sbase + P.z + hi * P.z_stride;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16_ts_warp(d, ac + 8 * kk, umma_desc(z + (kk >> 2) * N * 128, 16, 1024, kSw128) + 2 * (kk & 3), idesc,
-                                  kk > 0 ? 1u : 0u);
-              if (N > 256)   // r_k = 256: the last 16 rows are an MMA of their own
+              for (int r0 = 0; r0 < heads * N; r0 += 256) {
+                const uint32_t idesc = umma_idesc_f16(128, min(heads * N - r0, 256));
+                const uint64_t bd = umma_desc(sbase + P.z + (hi * N + r0) * 128, 16, 1024, kSw128);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                  umma_bf16_ts_warp(d + 256, ac + 8 * kk,
-                                    umma_desc(z + (kk >> 2) * N * 128 + 256 * 128, 16, 1024, kSw128) + 2 * (kk & 3),
-                                    tail_idesc, kk > 0 ? 1u : 0u);
+                  umma_bf16_warp(tmem + gs.i * N + r0, ad + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3),
+                                 bd + (kk >> 2) * (P.z_chunk >> 4) + 2 * (kk & 3), idesc, kk > 0 ? 1u : 0u);
+              }
               umma_commit_warp(bar(misc->gfull[gs.i]));
-              if (hi == nhg - 1) umma_commit_warp(bar(misc->aempty[as.i]));
+              if (heads == 2) umma_commit_warp(bar(misc->gfull[last.i]));
+              if (hi + heads == nhg) umma_commit_warp(bar(misc->rempty[rs.i]));
             }
+            gs = last;
             gs.next(NG);
           }
-          as.next(2);
+          rs.next(2);
         }
         named_bar_sync(kBarRun, kWorkers + 32);   // run ended
       }
@@ -494,90 +508,19 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       while (!mbar_try_wait(bar(misc->mma_done), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
     }
   } else if (warp < 12) {
-    regs_inc<152>();
-    // ======================================================== epilogue: rotary rows, scores, weights
+    regs_inc<104>();
+    // ======================================================== epilogue: scores, weights
     const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    float* stage = reinterpret_cast<float*>(sm + P.trig) + (warp - 4) * 32 * kTrigRow;
-    Slot st{0, 0u}, as{0, 0u}, gs{0, 0u};
+    Slot st{0, 0u}, gs{0, 0u};
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
-    float tc[32], ts[32];   // cos and sin of the own row, frequencies 32 grp + i
-    // rows of tile t from the table, through shared memory (a thread's own row straight from
-    // global memory would touch 32 lines per load): every load first, then the exchange
-    auto seed = [&](int t) {
-      float4 raw[16];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int64_t j = static_cast<int64_t>(t) * kTile + 32 * q + 16 * i + (lane >> 1);
-        j = (j < a.rope_len ? j : a.rope_len - 1) * 64 + 32 * grp + 4 * (lane & 1);   // behind the sequence's end: masked
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-          raw[2 * p + i] = __ldg(reinterpret_cast<const float4*>((p < 4 ? a.rope_cos : a.rope_sin) + j + 8 * (p & 3)));
-      }
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<float4*>(stage + (16 * i + (lane >> 1)) * kTrigRow + 4 * (lane & 1)) = raw[2 * p + i];
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(stage + lane * kTrigRow + 4 * i);
-          float* o = (p < 4 ? tc : ts) + 8 * (p & 3) + 4 * i;
-          o[0] = v.x;
-          o[1] = v.y;
-          o[2] = v.z;
-          o[3] = v.w;
-        }
-        __syncwarp();
-      }
-    };
-    // one tile further: by the angle sum with row 128
-    const uint32_t turn = smem_u32(&misc->tile_cos[32 * grp]);   // tile_sin follows
-    auto step = [&]() {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 C = lds128f(turn + 16 * i), S = lds128f(turn + 256 + 16 * i);
-        const float cc[4] = {C.x, C.y, C.z, C.w}, ss[4] = {S.x, S.y, S.z, S.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float c = tc[4 * i + e], s = ts[4 * i + e];
-          tc[4 * i + e] = fmaf(c, cc[e], -s * ss[e]);
-          ts[4 * i + e] = fmaf(c, ss[e], s * cc[e]);
-        }
-      }
-    };
-    // this group's half of the rotary rows into the next A buffer
-    auto put_rows = [&]() {
-      wait(misc->aempty[as.i], as.phase ^ 1u);
-      tc_fence_after();
-      uint32_t o[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = h2_bits(__floats2half2_rn(tc[2 * i], tc[2 * i + 1]));
-      tmem_st_x16(tmem + lane_base + kACol + 64 * as.i + 16 * grp, o);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = h2_bits(__floats2half2_rn(ts[2 * i], ts[2 * i + 1]));
-      tmem_st_x16(tmem + lane_base + kACol + 64 * as.i + 32 + 16 * grp, o);
-      tmem_wait_st();
-      tc_fence_before();
-      arrive(misc->afull[as.i]);
-      as.next(2);
-    };
     while (walk.next(a, ngroups, run)) {
       const int nhg = min(nh, a.H - run.hg * nh);
       build(wtid);
-      seed(run.t0);
-      put_rows();
       float m = -INFINITY, l = 0.f;
       const int held = nhg == 2 ? static_cast<int>((n ^ grp) & 1) : 0;   // the head whose state (m, l) is
 #pragma unroll 1
       for (int t = 0; t < run.n; ++t) {
-        if (t + 1 < run.n) {   // the next position's rows, ahead of this one's scores
-          // each step adds about an fp32 rounding: seeded again before they add up
-          if (((t + 1) & (kSeedTiles - 1)) == 0) seed(run.t0 + t + 1);
-          else step();
-          put_rows();
-        }
         const bool valid = row < run.L - (run.t0 + t) * kTile;
 #pragma unroll 1
         for (int hi = 0; hi < nhg; ++hi, ++n, st.next(NS), gs.next(NG)) {
@@ -586,7 +529,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           wait(misc->full[st.i], st.phase);
           wait(misc->gfull[gs.i], gs.phase);
           tc_fence_after();
-          const uint32_t gcol = tmem + lane_base + kGCol + gs.i * N;
+          const uint32_t gcol = tmem + lane_base + gs.i * N;
           float bias[2], s = 0.f;
           tmem_ld_x2(gcol + rk, bias);
           // ---- V scales; 2^E is above every one of the warp's tokens
@@ -639,7 +582,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 #pragma unroll
           for (int g = 0; g < RV32; ++g)
             sts16(tail + 2 * (g * kWStride + row), __float2half_rn(valid ? p * (__uint_as_float(vs[g] << 16) * ie) : 0.f));
-          if (lane == 0) sts32(tail + kWBytes + 4 * q, m == -INFINITY ? kNoRef : static_cast<int>(m) + E);
+          if (lane == 0) sts32(tail + P.w_bytes + 4 * q, m == -INFINITY ? kNoRef : static_cast<int>(m) + E);
           arrive(misc->wfull[st.i]);
         }
       }
@@ -650,12 +593,14 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       named_bar_sync(kBarRun, kWorkers + 32);
     }
   } else {
-    regs_inc<136>();
+    regs_inc<112>();
     // ======================================================== V: sum_j p_j c_v,j
     const int v = warp - 12, gid = lane >> 2, tig = lane & 3, wtid = tid - 128;
-    const int mine = nh == 2 ? v >> 1 : 0;                        // head of the group
-    const int tg0 = nh == 2 ? 2 * (v & 1) : v, ntg = nh == 2 ? 2 : 1;   // its 32-token groups
-    float* accs = reinterpret_cast<float*>(sm + P.acc);            // [4][RV32 * 32]
+    const int mine = nh == 2 ? v >> 2 : 0;                        // head of the group
+    const int g = nh == 2 ? v & 3 : v >> 1;                       // its 32 tokens: all of them, or 16
+    const int ks0 = nh == 2 ? 0 : v & 1, ks1 = nh == 2 ? 2 : ks0 + 1;
+    // run-end sums, [8][RV32 * 32] in the rows of the warps' own head: read no more by then
+    float* accs = reinterpret_cast<float*>(sm + P.z);
     const uint32_t half_sel = (gid & 1) ? 0x7632u : 0x5410u;
     Slot st{0, 0u};
     while (walk.next(a, ngroups, run)) {
@@ -674,9 +619,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           if (hi != mine) continue;
           wait(misc->wfull[st.i], st.phase);
           const uint32_t rows = sbase + P.ring + st.i * P.stage, tail = rows + kTile * rb;
-#pragma unroll 1
-          for (int g = tg0; g < tg0 + ntg; ++g) {
-            const int r = static_cast<int>(lds32(tail + kWBytes + 4 * g));
+          {
+            const int r = static_cast<int>(lds32(tail + P.w_bytes + 4 * g));
             if (r > ref) {
               const float f = exp2f(static_cast<float>(ref) - static_cast<float>(r));
 #pragma unroll
@@ -689,10 +633,11 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             }
             const __half2 f2 = __float2half2_rn(exp2f(static_cast<float>(r) - static_cast<float>(ref)));
             // tokens t0, t0 + 1 (k of the low half of B) and t0 + 8, t0 + 9 of each step of 16
-            const int t0 = 32 * g + 2 * tig;
-            uint32_t w = tail + 2 * (gid * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
+            const int t0 = 32 * g + 16 * ks0 + 2 * tig;
+            // (columns without a scale group repeat the last one's weights: never read from D)
+            uint32_t w = tail + 2 * (min(gid, RV32 - 1) * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
 #pragma unroll 1
-            for (int ks = 0; ks < 2; ++ks, w += 32, p0 += 16 * rb) {
+            for (int ks = ks0; ks < ks1; ++ks, w += 32, p0 += 16 * rb) {
               const uint32_t b0 = h2_bits(__hmul2(bits_h2(lds32(w)), f2)), b1 = h2_bits(__hmul2(bits_h2(lds32(w + 16)), f2));
               const uint32_t p1 = p0 + rb, p8 = p0 + 8 * rb, p9 = p1 + 8 * rb;
               mma16816(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, b0, b1);
@@ -721,7 +666,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       // ---- run end: the thread whose accumulator columns are a chunk's groups holds its
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
-      float* acc = accs + v * RV32 * 32;
+      float* acc = accs + (mine * N * 32 + (nh == 2 ? v & 3 : v) * RV32 * 32);
 #pragma unroll
       for (int c = 0; c < F; ++c) {
         if (tig != c) continue;
@@ -747,7 +692,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       if (lane == 0) misc->vref[v] = ref;
       named_bar_sync(kBarRun, kWorkers + 32);
       // ---- one record per head: {m, l, -, -, acc[r_v]}
-      const int u = run.b * ngroups + run.hg, vt = tid - (kQ4TileThreads - 128);
+      const int u = run.b * ngroups + run.hg, vt = tid - (kQ4TileThreads - 256);
       for (int hi = 0; hi < nhg; ++hi) {
         float M = -INFINITY, ls = 0.f;
 #pragma unroll
@@ -759,13 +704,11 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           if (misc->head[i >> 2] == hi) ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // (no maximum: all NaN)
         }
         float* rec = a.records + ((static_cast<int64_t>(u) + blockIdx.x) * nh + hi) * (rv + kRecordHead);
-        for (int k = vt; k < rv; k += 128) {
+        if (vt < rv) {
           float s = 0.f;
-          for (int i = 0; i < 4 / nh; ++i) {
-            const int vv = hi * (4 / nh) + i;
-            s = fmaf(accs[vv * RV32 * 32 + k], exp2f(static_cast<float>(misc->vref[vv]) - M), s);
-          }
-          rec[kRecordHead + k] = s;
+          for (int i = 0; i < 8 / nh; ++i)
+            s = fmaf(accs[hi * N * 32 + i * RV32 * 32 + vt], exp2f(static_cast<float>(misc->vref[hi * (8 / nh) + i]) - M), s);
+          rec[kRecordHead + vt] = s;
         }
         if (vt == 0) { rec[0] = M; rec[1] = ls; }
       }
@@ -781,6 +724,38 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// The f16 rotary rows of every position below the longest length, in tiles of 128 positions
+// as the MMA reads them: chunk 0 the cosines, chunk 1 the sines, 128 bytes a row, 128-byte
+// swizzle.  Reads 512 bytes and writes 256 per position; the decode grid's set-up overlaps it.
+constexpr int kRowsThreads = 256;
+__global__ void __launch_bounds__(kRowsThreads) q4_rows_kernel(const __grid_constant__ Q4DecodeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int longest[kRowsThreads / 32];
+  const int tid = threadIdx.x;
+  int L = 0;
+  for (int b = tid; b < a.B; b += kRowsThreads) L = max(L, tile_len(a, b));
+  L = __reduce_max_sync(0xffffffffu, L);
+  if ((tid & 31) == 0) longest[tid >> 5] = L;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRowsThreads / 32; ++i) L = max(L, longest[i]);
+  const int tiles = tiles_of(L);
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    uint8_t* out = a.row_tiles + static_cast<int64_t>(t) * kRowTile;
+#pragma unroll
+    for (int i = 0; i < kTile * 16 / kRowsThreads; ++i) {
+      const int at = tid + i * kRowsThreads, row = at >> 4, c = at & 15;   // 8 coordinates: 8 c ..
+      int64_t j = static_cast<int64_t>(t) * kTile + row;
+      j = j < a.rope_len ? j : a.rope_len - 1;   // behind the sequence's end: masked
+      const float4* src = reinterpret_cast<const float4*>((c < 8 ? a.rope_cos : a.rope_sin) + j * 64 + 8 * (c & 7));
+      const float4 x = __ldg(src), y = __ldg(src + 1);
+      *reinterpret_cast<uint4*>(out + (c >> 3) * 16384 + swizzle_offset(row * 128 + 16 * (c & 7), 128)) =
+          make_uint4(h2_bits(__floats2half2_rn(x.x, x.y)), h2_bits(__floats2half2_rn(x.z, x.w)),
+                     h2_bits(__floats2half2_rn(y.x, y.y)), h2_bits(__floats2half2_rn(y.z, y.w)));
+    }
   }
 }
 
@@ -857,8 +832,10 @@ template <int RV32>
 cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem(q4_tile_kernel<RV32>, a.plan.bytes);
   if (e != cudaSuccess) return e;
-  q4_tile_kernel<RV32><<<a.grid, kQ4TileThreads, a.plan.bytes, s>>>(a);
+  q4_rows_kernel<<<a.rows_grid, kRowsThreads, 0, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // programmatic dependents: each grid's set-up overlaps the one before
+  if ((e = launch_pdl(q4_tile_kernel<RV32>, dim3(a.grid), dim3(kQ4TileThreads), a.plan.bytes, s, a)) != cudaSuccess) return e;
   const int blocks = a.H * ((a.B + a.combine_units - 1) / a.combine_units);
   return launch_pdl(q4_combine_kernel<RV32>, dim3(blocks), dim3(kCombineThreads), 0, s, a);
 }
@@ -873,13 +850,13 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     p->nh = nh;
     p->ngroups = (H + nh - 1) / nh;
     p->N = r_k + 16;
-    p->NG = std::min(kMaxG, (512 - kGCol) / p->N);
-    p->z_stride = (p->N * 256 + 1023) / 1024 * 1024;
-    p->stage = al(kTile * rb + kStageTail, 128);
+    p->NG = std::min(kMaxG, 512 / p->N);
+    p->z_chunk = nh * p->N * 128;
+    p->w_bytes = rv32 * kWStride * 2;
+    p->stage = al(kTile * rb + p->w_bytes + 64, 128);
     int off = 0;
-    p->z = off; off += nh * p->z_stride;
-    p->trig = off; off += kTrigBytes;
-    p->acc = off; off += 4 * rv32 * 32 * 4;
+    p->z = off; off += 2 * p->z_chunk;
+    p->rows = off = al(off, 1024); off += 2 * kRowTile;
     p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 128);
     p->ring = off;
     p->NS = std::min((kSmemLimit - 1024 - off) / p->stage, kQ4MaxNS);
