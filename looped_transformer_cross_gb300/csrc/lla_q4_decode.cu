@@ -28,8 +28,8 @@
 // Work: positions (sequence, head group, 128-token tile) in that order, cut into
 // equal contiguous ranges, one per CTA.  A run is a CTA's part of one (sequence, head
 // group); the query operand of its nh heads is built in shared memory at its start, and
-// one record {m, l, acc} per head is written at its end.  Warps: 0 producer (bulk
-// copies of page pieces and rotary tiles), 1 MMA issuer, 4-11 epilogue, 12-19 V.
+// one record {m, l, acc} per head is written at its end.  Warps: 0 copies rows (bulk
+// copies of page pieces), 1 issues MMAs, 2 copies rotary tiles, 4-11 epilogue, 12-19 V.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -399,67 +399,105 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     named_bar_sync(kBarRun, kWorkers + 32);
   };
 
+  // Waits (bounded) for the last `count` copies of a ring of n slots to land: none may be in
+  // flight when the CTA exits.  (`at`, the next slot, holds the oldest of the last n, or none yet.)
+  auto land = [&](uint64_t* full, Slot at, int n, int count) {
+    for (int i = min(count, n); i > 0; --i) {
+      if (count < n && i == count) at = Slot{0, 0u};
+      const uint32_t phase = count < n ? 0u : at.phase ^ 1u;
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(bar(full[at.i]), phase) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      at.next(n);
+    }
+  };
   if (warp < 4) {
     regs_dec<48>();
     if (warp == 0) {
-      // ======================================================== producer
-      // Per position the rotary tile, per head-tile the page pieces that its rows lie in, lane i
-      // copying piece i.
-      Slot st{0, 0u}, rs{0, 0u};
-      int issued = 0, tiles = 0;
-      asm volatile("griddepcontrol.wait;" ::: "memory");   // the rotary tiles are written
-      while (walk.next(a, ngroups, run)) {
-        const int nhg = min(nh, a.H - run.hg * nh);
+      // ======================================================== producer of rows
+      // Per head-tile the page pieces that its rows lie in, lane i copying piece i.  A position's page ids are
+      // requested one position ahead: read when needed, their latency would pace the ring.
+      struct Pos {
+        int b, hg, y0, y1, lp0, np, page;
+      };
+      Slot st{0, 0u};
+      int issued = 0, left = 0, t = 0;
+      const int pg = a.page_size;
+      const int64_t head_bytes = static_cast<int64_t>(pg) * rb;
+      auto next = [&](Pos& x) -> bool {
+        if (left == 0) {
+          if (!walk.next(a, ngroups, run)) return false;
+          left = run.n;
+          t = run.t0;
+        }
+        x.b = run.b;
+        x.hg = run.hg;
+        x.y0 = t * kTile;
+        x.y1 = min(x.y0 + kTile, run.L);
+        x.lp0 = x.y0 / pg;
+        x.np = (x.y1 - 1) / pg - x.lp0 + 1;
+        if (lane < x.np) x.page = __ldg(a.block_table + static_cast<int64_t>(x.b) * a.max_pages + x.lp0 + lane);
+        --left;
+        ++t;
+        return true;
+      };
+      // piece i of a position: bytes, offset in the stage, address of the first head's rows
+      struct Piece {
+        uint32_t bytes, to;
+        const uint8_t* from;
+      };
+      auto piece = [&](const Pos& x, int i, int page) -> Piece {
+        const int p0 = (x.lp0 + i) * pg, t0 = max(x.y0, p0), t1 = i + 1 < x.np ? p0 + pg : x.y1;
+        if (page < 0 || page >= a.num_pages) {
+          record_status(a.status, LLA_ERR_DEVICE_ARG);
+          page = 0;
+        }
+        return Piece{static_cast<uint32_t>((t1 - t0) * rb), static_cast<uint32_t>((t0 - x.y0) * rb),
+                     a.rows + (static_cast<int64_t>(page) * a.H + x.hg * nh) * head_bytes + (t0 - p0) * rb};
+      };
+      Pos x{}, y{};
+      bool more = next(y);
+      while (more && ok) {
+        x = y;
+        more = next(y);
+        const int nhg = min(nh, a.H - x.hg * nh);
+        Piece mine{};
+        if (lane < x.np) mine = piece(x, lane, x.page);
+        for (int hi = 0; hi < nhg && ok; ++hi) {
+          wait(misc->empty[st.i], st.phase ^ 1u);
+          if (!ok) break;
+          const uint32_t fb = bar(misc->full[st.i]), dst = sbase + P.ring + st.i * P.stage;
+          if (lane == 0) mbar_arrive_expect_tx(fb, (x.y1 - x.y0) * rb);
+          __syncwarp();
+          if (lane < x.np) bulk_load(dst + mine.to, mine.from + hi * head_bytes, mine.bytes, fb);
+          for (int i = lane + 32; i < x.np; i += 32) {   // pages of fewer than four tokens
+            const Piece z = piece(x, i, __ldg(a.block_table + static_cast<int64_t>(x.b) * a.max_pages + x.lp0 + i));
+            bulk_load(dst + z.to, z.from + hi * head_bytes, z.bytes, fb);
+          }
+          __syncwarp();
+          ++issued;
+          st.next(NS);
+        }
+      }
+      if (lane == 0) land(misc->full, st, NS, issued);
+    } else if (warp == 2) {
+      // ======================================================== producer of rotary tiles
+      Slot rs{0, 0u};
+      int issued = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // they are written
+      while (walk.next(a, ngroups, run))
         for (int t = run.t0; t < run.t0 + run.n && ok; ++t) {
-          const int y0 = t * kTile, y1 = min(y0 + kTile, run.L), pg = a.page_size;
-          const int lp0 = y0 / pg, np = (y1 - 1) / pg - lp0 + 1;
-          const int32_t* table = a.block_table + static_cast<int64_t>(run.b) * a.max_pages + lp0;
           wait(misc->rempty[rs.i], rs.phase ^ 1u);
           if (!ok) break;
           if (lane == 0) {
-            mbar_arrive_expect_tx(bar(misc->rfull[rs.i]), kRowTile);
-            bulk_load(sbase + P.rows + rs.i * kRowTile, a.row_tiles + static_cast<int64_t>(t) * kRowTile, kRowTile,
-                      bar(misc->rfull[rs.i]));
+            const uint32_t fb = bar(misc->rfull[rs.i]);
+            mbar_arrive_expect_tx(fb, kRowTile);
+            bulk_load(sbase + P.rows + rs.i * kRowTile, a.row_tiles + static_cast<int64_t>(t) * kRowTile, kRowTile, fb);
           }
-          ++tiles;
+          __syncwarp();
+          ++issued;
           rs.next(2);
-          for (int hi = 0; hi < nhg && ok; ++hi) {
-            wait(misc->empty[st.i], st.phase ^ 1u);
-            if (!ok) break;
-            const uint32_t fb = bar(misc->full[st.i]), dst = sbase + P.ring + st.i * P.stage;
-            if (lane == 0) mbar_arrive_expect_tx(fb, (y1 - y0) * rb);
-            __syncwarp();
-            for (int i = lane; i < np; i += 32) {
-              const int p0 = (lp0 + i) * pg, t0 = max(y0, p0), t1 = i + 1 < np ? p0 + pg : y1;
-              int page = __ldg(table + i);
-              if (page < 0 || page >= a.num_pages) {
-                record_status(a.status, LLA_ERR_DEVICE_ARG);
-                page = 0;
-              }
-              const int64_t r0 = static_cast<int64_t>(page * a.H + run.hg * nh + hi) * pg + (t0 - p0);
-              bulk_load(dst + (t0 - y0) * rb, a.rows + r0 * rb, (t1 - t0) * rb, fb);
-            }
-            __syncwarp();
-            ++issued;
-            st.next(NS);
-          }
         }
-      }
-      // let every copy land before the CTA can exit
-      // (the next slot holds the oldest of the last n copies, or was not yet used)
-      auto land = [&](uint64_t* full, Slot at, int n, int count) {
-        for (int i = min(count, n); i > 0; --i) {
-          if (count < n && i == count) at = Slot{0, 0u};
-          const uint32_t phase = count < n ? 0u : at.phase ^ 1u;
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(bar(full[at.i]), phase) && global_timer_ns() - t0 < kWaitLimitNs) {}
-          at.next(n);
-        }
-      };
-      if (lane == 0) {
-        land(misc->full, st, NS, issued);
-        land(misc->rfull, rs, 2, tiles);
-      }
+      if (lane == 0) land(misc->rfull, rs, 2, issued);
     } else if (warp == 1) {
       // ======================================================== MMA issuer
       // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
