@@ -68,6 +68,8 @@ _lock = threading.Lock()
 def lib():
     """Load liblla.so (raises OSError if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             L = ctypes.CDLL(LIB_PATH)
@@ -356,42 +358,68 @@ def decode_attn_noalloc(dm: Dims, loop_t: int, q, cache_k, cache_v, seq_lens, q_
 # ---------------------------------------------------------------- RoPE operators, page plans, the 4-bit cache
 #
 # These calls check what they are given (types, shapes, one device) before they pass
-# pointers on, and run on the tensors' own device: its current stream unless `stream` is given.
+# pointers on, and run on the tensors' own device: its current stream unless `stream` is
+# given.  A step's calls are short, so the checks that pass cost little: one comparison
+# per property, and the wording of an error only once something does not fit.
 
 def _need(cond: bool, what: str):
     if not cond:
         raise ValueError(what)
 
 
-def _tensor(name: str, t, dtype, device, shape=None):
-    """Check one argument tensor (None in ``shape``: any extent); returns its pointer."""
+def _misfit(name: str, t, dtype, index, shape):
+    """Raise the error that names what does not fit of an argument tensor."""
     _need(isinstance(t, torch.Tensor), name + " must be a tensor")
     _need(t.dtype == dtype, "%s must be %s, not %s" % (name, dtype, t.dtype))
-    _need(t.device == device, "%s is on %s, not on %s" % (name, t.device, device))
-    if shape is not None:
-        _need(t.dim() == len(shape) and all(w is None or w == g for w, g in zip(shape, t.shape)),
-              "%s has shape %s, not %s" % (name, tuple(t.shape), tuple("*" if w is None else w for w in shape)))
-    return _ptr(t)
+    _need(t.is_cuda, "%s is on %s: a CUDA device is needed" % (name, t.device))
+    _need(t.get_device() == index, "%s is on %s, not on cuda:%d" % (name, t.device, index))
+    _need(shape is None or t.shape == shape, "%s has shape %s, not %s" % (name, tuple(t.shape), shape))
+    _need(t.is_contiguous(), name + " must be contiguous")
+    raise ValueError(name + " does not fit")
 
 
-def _workspace(t, device):
-    _need(t is not None and t.is_cuda and t.device == device, "the workspace must be on %s" % (device,))
-    return _ptr(t), t.numel() * t.element_size()
+def _arg(name: str, t, dtype, index: int, shape):
+    """Address of an argument tensor of this type, device, shape and contiguous."""
+    try:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _misfit(name, t, dtype, index, shape)
+
+
+def _device_of(name: str, t) -> int:
+    _need(isinstance(t, torch.Tensor), name + " must be a tensor")
+    index = t.get_device()
+    _need(index >= 0, "%s is on %s: a CUDA device is needed" % (name, t.device))
+    return index
+
+
+def _space(t, index: int):
+    """Address and bytes of a workspace."""
+    _need(isinstance(t, torch.Tensor) and t.get_device() == index and t.is_contiguous(),
+          "the workspace must be a contiguous tensor on cuda:%d" % index)
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _storage(dm: Dims):
     return torch.bfloat16 if dm.dtype == LLA_BF16 else torch.float32
 
 
-def _run(device, stream, f, *args):
-    """Call f(*args, stream) with ``device`` current."""
-    _need(device.type == "cuda", "the tensors must be on a CUDA device, not on %s" % (device,))
-    if stream is not None:
-        _need(stream.device == device, "the stream is of %s, not of %s" % (stream.device, device))
-    if device.index == torch.cuda.current_device():
-        return f(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return f(*args, _stream(stream))
+def _run(what: str, f, index: int, stream, *args):
+    """Call f(*args, stream) with device ``index`` current; raise for a status that is not ok."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        _need(stream.device.index == index, "the stream is of %s, not of cuda:%d" % (stream.device, index))
+        raw = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        status = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, raw)
+    if status != LLA_OK:
+        raise LLAError(status, what)
 
 
 _SCALINGS = {"plain": LLA_ROPE_PLAIN, "linear": LLA_ROPE_LINEAR, "base": LLA_ROPE_BASE, "by_parts": LLA_ROPE_BY_PARTS}
@@ -412,11 +440,10 @@ def rope_table_scaled(dm: Dims, n_pos: int, scaling: Optional[RopeScaling] = Non
     if cos is None:
         cos = torch.empty(shape, dtype=torch.float32, device="cuda" if device is None else device)
         sin = torch.empty_like(cos)
-    pc = _tensor("cos", cos, torch.float32, cos.device, shape)
-    ps = _tensor("sin", sin, torch.float32, cos.device, shape)
-    st = _run(cos.device, stream, lib().lla_rope_table_scaled, ctypes.byref(dm),
-              None if scaling is None else ctypes.byref(scaling), int(pos0), int(n_pos), pc, ps)
-    _check(st, "lla_rope_table_scaled")
+    dev = _device_of("cos", cos)
+    _run("lla_rope_table_scaled", lib().lla_rope_table_scaled, dev, stream, ctypes.byref(dm),
+         None if scaling is None else ctypes.byref(scaling), pos0, n_pos, _arg("cos", cos, torch.float32, dev, shape),
+         _arg("sin", sin, torch.float32, dev, shape))
     return cos, sin
 
 
@@ -425,24 +452,23 @@ def rope_apply(dm: Dims, x, pos, rope_cos, rope_sin, out=None, offset: int = 0, 
     """lla_rope_apply: rotate 2 * rope_cos.shape[1] elements of every head's vector of ``x``
     [N][heads][d_x], from element ``offset`` on; ``out`` may be ``x`` (in place) and is
     returned.  Token and head strides are free, a head's vector is contiguous."""
+    dev = _device_of("x", x)
     _need(x.dim() == 3, "x must be [N][heads][d_x]")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    sd, dev = _storage(dm), x.device
-    for name, t in (("x", x), ("out", out)):
-        _need(t.dtype == sd and t.device == dev and t.shape == x.shape,
-              "%s must be %s of shape %s on %s" % (name, sd, tuple(x.shape), dev))
-        _need(t.shape[2] <= 1 or t.stride(2) == 1, name + ": a head's vector must be contiguous")
-    N, heads, d_x = (int(n) for n in x.shape)
-    half = int(rope_cos.shape[1])
-    pc = _tensor("rope_cos", rope_cos, torch.float32, dev, (None, half))
-    ps = _tensor("rope_sin", rope_sin, torch.float32, dev, rope_cos.shape)
-    pp = _tensor("pos", pos, torch.int32, dev, (N,))
-    ws, wb = _workspace(workspace, dev)
-    st = _run(dev, stream, lib().lla_rope_apply, ctypes.byref(dm), x.data_ptr(), x.stride(0), x.stride(1),
-              out.data_ptr(), out.stride(0), out.stride(1), N, heads, d_x, int(offset), 2 * half, pp, pc, ps,
-              int(rope_cos.shape[0]), float(scale), 1 if inverse else 0, ws, wb)
-    _check(st, "lla_rope_apply")
+    sd, shape = _storage(dm), x.shape
+    N, heads, d_x = shape
+    xs, os = x.stride(), out.stride()
+    if not (x.dtype is sd and out.dtype is sd and out.get_device() == dev and out.shape == shape and
+            (d_x <= 1 or xs[2] == 1 and os[2] == 1)):
+        raise ValueError("x and out must be %s of one shape on one device, each head's vector contiguous" % (sd,))
+    table = rope_cos.shape
+    _need(len(table) == 2, "rope_cos must be [rope_len][d_rope / 2]")
+    ws, wb = _space(workspace, dev)
+    _run("lla_rope_apply", lib().lla_rope_apply, dev, stream, ctypes.byref(dm), x.data_ptr(), xs[0], xs[1], out.data_ptr(),
+         os[0], os[1], N, heads, d_x, offset, 2 * table[1], _arg("pos", pos, torch.int32, dev, (N,)),
+         _arg("rope_cos", rope_cos, torch.float32, dev, table), _arg("rope_sin", rope_sin, torch.float32, dev, table),
+         table[0], scale, 1 if inverse else 0, ws, wb)
     return out
 
 
@@ -462,20 +488,21 @@ class PagePlan:
         self.seq_idx, self.pos = torch.empty(self.n_tok, **i32), torch.empty(self.n_tok, **i32)
         self.slots = torch.empty(self.n_tok, dtype=torch.int64, device=device)
         self.workspace = torch.zeros(256, dtype=torch.uint8, device=device)
-        self._out = [_ptr(t) for t in (self.seq_lens, self.tok_start, self.granted)]
-        self._map = [_ptr(t) for t in (self.seq_idx, self.pos, self.slots, self.counts, self.workspace)]
 
     def __call__(self, page_size: int, num_pages: int, ctx_lens, new_lens, free_pages, block_table, free_head=None,
                  stream=None):
-        dev = self.counts.device
-        pc = _tensor("ctx_lens", ctx_lens, torch.int32, dev, (self.B,))
-        pn = _tensor("new_lens", new_lens, torch.int32, dev, (self.B,))
-        pf = _tensor("free_pages", free_pages, torch.int32, dev, (None,))
-        pt = _tensor("block_table", block_table, torch.int32, dev, (self.B, None))
-        ph = None if free_head is None else _tensor("free_head", free_head, torch.int32, dev, (1,))
-        st = _run(dev, stream, lib().lla_page_plan, self.B, int(page_size), int(block_table.shape[1]), int(num_pages),
-                  pc, pn, pf, int(free_pages.shape[0]), ph, pt, *self._out, self.n_tok, *self._map, 256)
-        _check(st, "lla_page_plan")
+        dev, B, i32 = self.counts.get_device(), self.B, torch.int32
+        table = block_table.shape
+        _need(len(table) == 2 and table[0] == B, "block_table must be [%d][max_pages]" % B)
+        free = free_pages.shape
+        _need(len(free) == 1, "free_pages must be one-dimensional")
+        _run("lla_page_plan", lib().lla_page_plan, dev, stream, B, page_size, table[1], num_pages,
+             _arg("ctx_lens", ctx_lens, i32, dev, (B,)), _arg("new_lens", new_lens, i32, dev, (B,)),
+             _arg("free_pages", free_pages, i32, dev, free), free[0],
+             None if free_head is None else _arg("free_head", free_head, i32, dev, (1,)),
+             _arg("block_table", block_table, i32, dev, table), self.seq_lens.data_ptr(), self.tok_start.data_ptr(),
+             self.granted.data_ptr(), self.n_tok, self.seq_idx.data_ptr(), self.pos.data_ptr(), self.slots.data_ptr(),
+             self.counts.data_ptr(), self.workspace.data_ptr(), 256)
         return self
 
 
@@ -501,56 +528,58 @@ def q4_workspace(dm: Dims, B: int, L_max: int, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _q4_cache(dm: Dims, pool, block_table=None) -> Q4Cache:
-    rb = lib().lla_q4_row_bytes(ctypes.byref(dm))
-    rows = _tensor("pool", pool, torch.uint8, pool.device, (None, dm.H, None, rb))
-    c = Q4Cache(rows, None, 0, 1, int(pool.shape[2]), int(pool.shape[0]))
-    if block_table is not None:
-        c.block_table = _tensor("block_table", block_table, torch.int32, pool.device, (None, None))
-        c.B, c.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
-    return c
+def _q4_cache(L, dm: Dims, pool, dev: int, block_table=None) -> Q4Cache:
+    shape = pool.shape
+    _need(len(shape) == 4 and shape[1] == dm.H and shape[3] == L.lla_q4_row_bytes(ctypes.byref(dm)),
+          "the pool must be [num_pages][%d][page_size][row bytes], not %s" % (dm.H, tuple(shape)))
+    rows = _arg("pool", pool, torch.uint8, dev, shape)
+    if block_table is None:
+        return Q4Cache(rows, None, 0, 1, shape[2], shape[0])
+    table = block_table.shape
+    _need(len(table) == 2, "block_table must be [B][max_pages]")
+    return Q4Cache(rows, _arg("block_table", block_table, torch.int32, dev, table), table[0], table[1], shape[2], shape[0])
+
+
+def _q4_latents(dm: Dims, c_k, c_v, slots, dev: int):
+    """Addresses of c_k [N][H][r_k], c_v [N][H][r_v] and slots [N], and N."""
+    N, sd = slots.shape[0], _storage(dm)
+    return (_arg("c_k", c_k, sd, dev, (N, dm.H, dm.r_k)), _arg("c_v", c_v, sd, dev, (N, dm.H, dm.r_v)),
+            _arg("slots", slots, torch.int64, dev, (N,)), N)
 
 
 def q4_store(dm: Dims, c_k, c_v, slots, pool, workspace, stream=None):
     """lla_q4_store: latents c_k [N][H][r_k], c_v [N][H][r_v] rounded to 4 bits into the
     pool's rows at ``slots`` [N] (int64, as lla_page_plan makes them)."""
-    dev, N = pool.device, int(slots.shape[0])
-    c = _q4_cache(dm, pool)
-    pk = _tensor("c_k", c_k, _storage(dm), dev, (N, dm.H, dm.r_k))
-    pv = _tensor("c_v", c_v, _storage(dm), dev, (N, dm.H, dm.r_v))
-    ws, wb = _workspace(workspace, dev)
-    st = _run(dev, stream, lib().lla_q4_store, ctypes.byref(dm), pk, pv, N,
-              _tensor("slots", slots, torch.int64, dev, (N,)), ctypes.byref(c), ws, wb)
-    _check(st, "lla_q4_store")
+    dev, L = _device_of("pool", pool), lib()
+    c = _q4_cache(L, dm, pool, dev)
+    pk, pv, ps, N = _q4_latents(dm, c_k, c_v, slots, dev)
+    ws, wb = _space(workspace, dev)
+    _run("lla_q4_store", L.lla_q4_store, dev, stream, ctypes.byref(dm), pk, pv, N, ps, ctypes.byref(c), ws, wb)
 
 
 def q4_load(dm: Dims, slots, pool, c_k, c_v, workspace, stream=None):
     """lla_q4_load: the latents that the pool's rows at ``slots`` stand for, into c_k, c_v."""
-    dev, N = pool.device, int(slots.shape[0])
-    c = _q4_cache(dm, pool)
-    pk = _tensor("c_k", c_k, _storage(dm), dev, (N, dm.H, dm.r_k))
-    pv = _tensor("c_v", c_v, _storage(dm), dev, (N, dm.H, dm.r_v))
-    ws, wb = _workspace(workspace, dev)
-    st = _run(dev, stream, lib().lla_q4_load, ctypes.byref(dm), _tensor("slots", slots, torch.int64, dev, (N,)), N,
-              ctypes.byref(c), pk, pv, ws, wb)
-    _check(st, "lla_q4_load")
+    dev, L = _device_of("pool", pool), lib()
+    c = _q4_cache(L, dm, pool, dev)
+    pk, pv, ps, N = _q4_latents(dm, c_k, c_v, slots, dev)
+    ws, wb = _space(workspace, dev)
+    _run("lla_q4_load", L.lla_q4_load, dev, stream, ctypes.byref(dm), ps, N, ctypes.byref(c), pk, pv, ws, wb)
 
 
 def decode_attn_q4(dm: Dims, loop_t: int, q, pool, block_table, seq_lens, q_pos, w_up_k, w_up_v, mu_k, mu_v, rope_cos,
                    rope_sin, out, lse, workspace, stream=None):
     """lla_decode_attn_q4: latent-store decode attention over a 4-bit paged cache, into ``out``
     [B][H][d] (storage dtype) and, unless None, ``lse`` [B][H] (fp32)."""
-    dev, sd, T, H, d = pool.device, _storage(dm), dm.T, dm.H, dm.d_head
-    c = _q4_cache(dm, pool, block_table)
-    B = c.B
-    f32, i32 = torch.float32, torch.int32
-    pl = None if lse is None else _tensor("lse", lse, f32, dev, (B, H))
-    ws, wb = _workspace(workspace, dev)
-    st = _run(dev, stream, lib().lla_decode_attn_q4, ctypes.byref(dm), int(loop_t), _tensor("q", q, sd, dev, (B, H, d)),
-              ctypes.byref(c), _tensor("seq_lens", seq_lens, i32, dev, (B,)), _tensor("q_pos", q_pos, i32, dev, (B,)),
-              _tensor("w_up_k", w_up_k, sd, dev, (T, H, d, dm.r_k)), _tensor("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)),
-              _tensor("mu_k", mu_k, f32, dev, (H, T * d)), _tensor("mu_v", mu_v, f32, dev, (H, T * d)),
-              _tensor("rope_cos", rope_cos, f32, dev, (None, d // 2)),
-              _tensor("rope_sin", rope_sin, f32, dev, rope_cos.shape), int(rope_cos.shape[0]),
-              _tensor("out", out, sd, dev, (B, H, d)), pl, ws, wb)
-    _check(st, "lla_decode_attn_q4")
+    dev, L = _device_of("pool", pool), lib()
+    c = _q4_cache(L, dm, pool, dev, block_table)
+    sd, T, H, d, f32, i32 = _storage(dm), dm.T, dm.H, dm.d_head, torch.float32, torch.int32
+    vec, one = (c.B, H, d), (c.B,)
+    table = rope_cos.shape
+    _need(len(table) == 2 and table[1] == d // 2, "rope_cos must be [rope_len][%d]" % (d // 2))
+    ws, wb = _space(workspace, dev)
+    _run("lla_decode_attn_q4", L.lla_decode_attn_q4, dev, stream, ctypes.byref(dm), loop_t, _arg("q", q, sd, dev, vec),
+         ctypes.byref(c), _arg("seq_lens", seq_lens, i32, dev, one), _arg("q_pos", q_pos, i32, dev, one),
+         _arg("w_up_k", w_up_k, sd, dev, (T, H, d, dm.r_k)), _arg("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)),
+         _arg("mu_k", mu_k, f32, dev, (H, T * d)), _arg("mu_v", mu_v, f32, dev, (H, T * d)),
+         _arg("rope_cos", rope_cos, f32, dev, table), _arg("rope_sin", rope_sin, f32, dev, table), table[0],
+         _arg("out", out, sd, dev, vec), None if lse is None else _arg("lse", lse, f32, dev, (c.B, H)), ws, wb)
