@@ -354,6 +354,25 @@ cudaError_t launch_encode_bf16(const EncodeArgs& a, const EncodePlan& plan, cons
                                cudaStream_t s);
 cudaError_t launch_encode_f32(const EncodeArgs& a, cudaStream_t s);
 
+// ----------------------------------------------------------------- division by a launch constant
+
+// n / d for n < 2^31 by one multiplication: with p = 31 + ceil(log2 d) and m = ceil(2^p / d), the
+// excess e = m d - 2^p is below d <= 2^(p - 31), so n m / 2^p = n / d + n e / (d 2^p) stays below
+// the next integer.
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    uint32_t lg = 0;
+    while ((uint64_t(1) << lg) < div) ++lg;
+    if (lg > 0) {
+      m = static_cast<uint32_t>(((uint64_t(1) << (31 + lg)) + div - 1) / div);
+      s = lg - 1;
+    }
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> s; }
+};
+
 // ----------------------------------------------------------------- host checks
 // (lla_api.cu) the checks of dims that every call makes, and the current device's SM count
 lla_status checked_dims(const lla_dims* dims);

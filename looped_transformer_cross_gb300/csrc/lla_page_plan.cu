@@ -3,12 +3,12 @@
 // step take, made without the host seeing a length ("Enabling dynamic computation in
 // Looped LMs", App. A.1: a logical-to-physical page table per sequence).
 //
-// One launch.  Every block scans all B requests by itself (a few KB from L2, a few
-// microseconds), so no block waits for another, and then writes its own stretch of the
-// token maps and its own requests' table rows; a slot never depends on a table entry
-// that this call writes, because pages taken now are read from the free list.
+// One launch.  Every block scans all B requests by itself (a few KB from L2, held in shared
+// memory), so no block waits for another, and then writes its own stretch of the token maps and of
+// the new table entries, each found by a binary search of the scan; a slot never depends on a
+// table entry that this call writes, because pages taken now are read from the free list.
+// Latency-bound: the lengths are read once, the rest runs out of shared memory.
 #include <algorithm>
-#include <atomic>
 
 #include "lla_kernels.h"
 
@@ -18,11 +18,11 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;        // requests of a plan (shared memory: 16 bytes each)
-constexpr int kTokPerThread = 8;
 
 struct PlanArgs {
   int B, page_size, max_pages, n_free, n_tok;
   int64_t num_pages;
+  int per_thread;                    // token entries of a thread
   const int32_t* ctx;
   const int32_t* fresh;
   const int32_t* free_pages;
@@ -57,15 +57,30 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& b, int64_t (*tot
 
 __device__ __forceinline__ int64_t pages_of(int64_t tokens, int P) { return (tokens + P - 1) / P; }
 
+// The last of n ascending starts that is at or before i (starts[0] <= i).
+__device__ __forceinline__ int owner(const int32_t* starts, int n, int64_t i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int32_t clamp32(int64_t x) { return static_cast<int32_t>(min(x, static_cast<int64_t>(INT32_MAX))); }
+
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PlanArgs a) {
-  // per request: first token (requested), cached length, first page taken, 1 if granted
+  // per request: first token (requested), cached length, first page taken (counted from the list's
+  // head), tokens brought; -1 - tokens where it is not granted
   extern __shared__ int32_t sh[];
   int32_t* start = sh;
   int32_t* len0 = sh + a.B;
   int32_t* page0 = sh + 2 * a.B;
-  int32_t* ok = sh + 3 * a.B;
+  int32_t* fresh = sh + 3 * a.B;
   __shared__ int64_t tot[kPlanThreads / 32][2];
-  const int tid = threadIdx.x;
+  __shared__ int64_t total[2];           // tokens requested, pages taken
+  const int tid = threadIdx.x, P = a.page_size;
   const bool first = blockIdx.x == 0;
   int64_t head = a.free_head ? static_cast<int64_t>(__ldg(a.free_head)) : 0;
   if (head < 0 || head > a.n_free) {
@@ -73,43 +88,45 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     head = a.n_free;   // nothing to take
   }
   const int64_t avail = a.n_free - head;
-  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page_size;
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * P;
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const int c = __ldg(a.ctx + b), n = __ldg(a.fresh + b);
+    if ((c < 0 || n < 0) && first) record_status(a.status, LLA_ERR_DEVICE_ARG);
+    len0[b] = max(c, 0);
+    fresh[b] = max(n, 0);
+  }
+  __syncthreads();
   // a thread's requests: a contiguous stretch, so that one block scan serves them all
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int64_t toks = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int c = __ldg(a.ctx + b), n = __ldg(a.fresh + b);
-    if ((c < 0 || n < 0) && first) record_status(a.status, LLA_ERR_DEVICE_ARG);
-    toks += max(n, 0);
-  }
-  int64_t tok_end = toks, zero = 0;
+  int64_t toks = 0, zero = 0;
+  for (int b = b0; b < b1; ++b) toks += fresh[b];
+  int64_t tok_end = toks;
   block_scan(tok_end, zero, tot);
   // pages: a request that cannot hold its tokens (table too short, maps too short) takes none
-  int64_t need_sum = 0;
-  int64_t t = tok_end - toks;
+  auto fits = [&](int64_t c, int64_t n, int64_t before) { return c + n <= cap && before + n <= a.n_tok; };
+  auto need_of = [&](int64_t c, int64_t n) { return pages_of(c + n, P) - pages_of(c, P); };
+  int64_t need_sum = 0, t = tok_end - toks;
   for (int b = b0; b < b1; ++b) {
-    const int64_t c = max(__ldg(a.ctx + b), 0), n = max(__ldg(a.fresh + b), 0);
+    const int64_t c = len0[b], n = fresh[b];
+    if (fits(c, n, t)) need_sum += need_of(c, n);
     t += n;
-    if (c + n <= cap && t <= a.n_tok) need_sum += pages_of(c + n, a.page_size) - pages_of(c, a.page_size);
   }
   int64_t page_end = need_sum;
   zero = 0;
   block_scan(page_end, zero, tot);
-  int64_t taken = 0, live = 0;
+  int64_t taken = 0, live = 0, pg = page_end - need_sum;
   t = tok_end - toks;
-  int64_t pg = page_end - need_sum;
   for (int b = b0; b < b1; ++b) {
-    const int64_t c = max(__ldg(a.ctx + b), 0), n = max(__ldg(a.fresh + b), 0);
-    const bool fits = c + n <= cap && t + n <= a.n_tok;
-    const int64_t need = fits ? pages_of(c + n, a.page_size) - pages_of(c, a.page_size) : 0;
+    const int64_t c = len0[b], n = fresh[b];
+    const bool f = fits(c, n, t);
+    const int64_t need = f ? need_of(c, n) : 0;
     // the free list serves requests in order: the first that it cannot fill ends it for
     // every later one that needs a page
-    const bool g = fits && (need == 0 || pg + need <= avail);
-    start[b] = static_cast<int32_t>(min(t, static_cast<int64_t>(INT32_MAX)));
-    len0[b] = static_cast<int32_t>(c);
-    page0[b] = static_cast<int32_t>(min(head + pg, static_cast<int64_t>(INT32_MAX)));
-    ok[b] = g ? 1 : 0;
+    const bool g = f && (need == 0 || pg + need <= avail);
+    start[b] = clamp32(t);
+    page0[b] = clamp32(pg);
+    if (!g) fresh[b] = -1 - static_cast<int32_t>(n);
     if (first) {
       a.seq_lens[b] = static_cast<int32_t>(g ? c + n : c);
       a.tok_start[b] = start[b];
@@ -119,58 +136,43 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     t += n;
     pg += need;
   }
-  if (first) {
-    if (tid == kPlanThreads - 1) a.tok_start[a.B] = static_cast<int32_t>(min(tok_end, static_cast<int64_t>(INT32_MAX)));
-    block_scan(taken, live, tot);
-    if (tid == kPlanThreads - 1) {
+  block_scan(taken, live, tot);
+  if (tid == kPlanThreads - 1) {
+    total[0] = tok_end;
+    total[1] = taken;
+    if (first) {
+      a.tok_start[a.B] = clamp32(tok_end);
       a.counts[0] = static_cast<int32_t>(head + taken);
       a.counts[1] = static_cast<int32_t>(live);
     }
   }
   __syncthreads();
 
-  // ---- table rows: one warp per request, its new pages in order off the free list
-  const int warps = kPlanThreads / 32, lane = tid & 31;
-  for (int b = blockIdx.x * warps + (tid >> 5); b < a.B; b += gridDim.x * warps) {
-    if (!ok[b]) continue;
-    const int64_t c = len0[b], n = max(__ldg(a.fresh + b), 0);
-    const int held = static_cast<int>(pages_of(c, a.page_size)), need = static_cast<int>(pages_of(c + n, a.page_size)) - held;
-    for (int i = lane; i < need; i += 32) {
-      const int p = __ldg(a.free_pages + page0[b] + i);
-      if (p < 0 || p >= a.num_pages) record_status(a.status, LLA_ERR_DEVICE_ARG);
-      a.table[static_cast<int64_t>(b) * a.max_pages + held + i] = p;
-    }
+  // ---- new table entries: page k of those taken belongs to the last request that starts at or before it
+  // (the granted requests that take pages come before every other that needs one)
+  for (int64_t k = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; k < total[1]; k += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
+    const int b = owner(page0, a.B, k), p = __ldg(a.free_pages + head + k);
+    if (p < 0 || p >= a.num_pages) record_status(a.status, LLA_ERR_DEVICE_ARG);
+    a.table[static_cast<int64_t>(b) * a.max_pages + pages_of(len0[b], P) + (k - page0[b])] = p;
   }
 
-  // ---- token maps: entry i belongs to the last request that starts at or before it
-  const int64_t total = min(tok_end, static_cast<int64_t>(INT32_MAX));   // of the last thread only: broadcast
-  __shared__ int64_t all;
-  if (tid == kPlanThreads - 1) all = total;
-  __syncthreads();
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kPlanThreads * kTokPerThread;
+  // ---- token maps
+  int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads * a.per_thread + tid;
 #pragma unroll 1
-  for (int k = 0; k < kTokPerThread; ++k) {
-    const int64_t i = i0 + k * kPlanThreads + tid;
-    if (i >= a.n_tok) break;
+  for (int k = 0; k < a.per_thread && i < a.n_tok; ++k, i += kPlanThreads) {
     int sb = -1, sp = -1;
     int64_t slot = -1;
-    if (i < all) {
-      int lo = 0, hi = a.B;   // the last b with start[b] <= i
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= i) lo = mid;
-        else hi = mid;
-      }
-      if (ok[lo]) {
-        const int p = len0[lo] + static_cast<int>(i - start[lo]);
-        const int lp = p / a.page_size;
-        const int held = static_cast<int>(pages_of(len0[lo], a.page_size));
-        const int page = lp < held ? __ldg(a.table + static_cast<int64_t>(lo) * a.max_pages + lp)
-                                   : __ldg(a.free_pages + page0[lo] + lp - held);
-        sb = lo;
+    if (i < total[0]) {
+      const int b = owner(start, a.B, i);
+      if (fresh[b] >= 0) {
+        const int p = len0[b] + static_cast<int>(i - start[b]), lp = p / P;
+        const int held = static_cast<int>(pages_of(len0[b], P));
+        const int page = lp < held ? __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + lp)
+                                   : __ldg(a.free_pages + head + page0[b] + lp - held);
+        sb = b;
         sp = p;
         if (page < 0 || page >= a.num_pages) record_status(a.status, LLA_ERR_DEVICE_ARG);
-        else slot = static_cast<int64_t>(page) * a.page_size + (p - lp * a.page_size);
+        else slot = static_cast<int64_t>(page) * P + (p - lp * P);
       }
     }
     a.seq_idx[i] = sb;
@@ -210,14 +212,20 @@ extern "C" lla_status lla_page_plan(int B, int page_size, int max_pages, int64_t
       const uintptr_t x = reinterpret_cast<uintptr_t>(i.p), y = reinterpret_cast<uintptr_t>(o.p);
       if (x && y && x < y + o.bytes && y < x + i.bytes) return LLA_ERR_INVALID_ARG;
     }
-  PlanArgs a{B, page_size, max_pages, n_free, n_tok, num_pages, ctx_lens, new_lens, free_pages, free_head, block_table,
-             seq_lens, tok_start, granted, seq_idx, pos, slots, counts, static_cast<uint32_t*>(workspace)};
+  const int sms = device_sm_count();
+  if (sms <= 0) return LLA_ERR_CUDA;
+  // two blocks per SM at most: each repeats the scan
+  const int64_t stretch = static_cast<int64_t>(kPlanThreads) * 2 * sms;
+  PlanArgs a{B, page_size, max_pages, n_free, n_tok, num_pages, static_cast<int>((n_tok + stretch - 1) / stretch), ctx_lens,
+             new_lens, free_pages, free_head, block_table, seq_lens, tok_start, granted, seq_idx, pos, slots, counts,
+             static_cast<uint32_t*>(workspace)};
+  a.per_thread = std::max(a.per_thread, 1);
   const size_t smem = static_cast<size_t>(B) * 16;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxB * 16) != cudaSuccess)
     return LLA_ERR_CUDA;
-  const int64_t tok_blocks = (static_cast<int64_t>(n_tok) + kPlanThreads * kTokPerThread - 1) / (kPlanThreads * kTokPerThread);
-  const unsigned blocks = static_cast<unsigned>(std::max<int64_t>(1, tok_blocks));
+  const int64_t per_block = static_cast<int64_t>(kPlanThreads) * a.per_thread;
+  const unsigned blocks = static_cast<unsigned>(std::max<int64_t>(1, (n_tok + per_block - 1) / per_block));
   page_plan_kernel<<<blocks, kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(a);
   return cudaGetLastError() == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }

@@ -16,33 +16,13 @@ namespace lla {
 namespace {
 
 constexpr int kQ4Threads = 256;
-
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(p)), v);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 w;
-  __nv_bfloat162 h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  w.x = *reinterpret_cast<uint32_t*>(&h[0]); w.y = *reinterpret_cast<uint32_t*>(&h[1]);
-  w.z = *reinterpret_cast<uint32_t*>(&h[2]); w.w = *reinterpret_cast<uint32_t*>(&h[3]);
-  *reinterpret_cast<uint4*>(p) = w;
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
+constexpr float kQ4Normal = 1.17549435e-38f;   // 2^-126: scales below it have no finite reciprocal, or few bits
 
 struct Q4CopyArgs {
-  int H, r_k, r_v, row_bytes, page_size;
+  int H, r_k, r_v, row_bytes;
+  FastDiv groups, heads, page;       // scale groups of a row, heads, rows of a page
   int64_t num_slots;                 // num_pages * page_size
-  uint32_t n_items;                  // token-heads * 4 (groups of K + groups of V)
+  uint32_t n_items;                  // token-heads * 2 (groups of K + groups of V)
   uint32_t tok0;
   const int64_t* slots;
   void* k;                           // [N][H][r_k] storage dtype
@@ -58,13 +38,15 @@ __device__ __forceinline__ int64_t q4_row(const Q4CopyArgs& a, int64_t slot, int
     if (report) record_status(a.status, LLA_ERR_DEVICE_ARG);
     return -1;
   }
-  const int64_t page = slot / a.page_size;
-  return (page * a.H + h) * a.page_size + (slot - page * a.page_size);
+  const int64_t P = a.page.d, page = slot < (int64_t(1) << 31) ? a.page.div(static_cast<uint32_t>(slot)) : slot / P;
+  return (page * a.H + h) * P + (slot - page * P);
 }
 
-// Four neighbouring threads hold one group of 32 columns, eight columns each (the last
-// group may have 16: two of the four idle).  Both directions are HBM-bound: the
-// store reads 2 (r_k + r_v) bytes (bf16) and writes a row per token-head.
+// Two neighbouring threads hold one group of 32 columns, sixteen each (the last group of a
+// rank may have 16: the second is idle).  Both directions move 2 (r_k + r_v) bytes (bf16)
+// and a row per token-head and should be bound by HBM, so the work per column is kept to a
+// few instructions: what eight columns a thread, conversions by int and true divisions took
+// was 299 us (store) and 210 us (load) for 65536 tokens of 16 heads at (96, 160).
 struct Q4Item {
   int sub, col, r, code_at, scale_at;
   bool k_axis, active;
@@ -72,37 +54,61 @@ struct Q4Item {
 };
 __device__ __forceinline__ Q4Item q4_item(const Q4CopyArgs& a, uint32_t i) {
   Q4Item it;
-  const uint32_t gk = q4_groups(a.r_k), ng = gk + q4_groups(a.r_v);
-  const uint32_t g_all = i >> 2, th = g_all / ng, g = g_all - th * ng;
-  it.sub = i & 3;
-  it.n = th / a.H;
-  it.h = th - it.n * a.H;
+  const uint32_t gk = q4_groups(a.r_k), g_all = i >> 1, th = a.groups.div(g_all), g = g_all - th * a.groups.d;
+  it.sub = i & 1;
+  it.n = a.heads.div(th);
+  it.h = th - it.n * a.heads.d;
   it.k_axis = g < gk;
   it.r = it.k_axis ? a.r_k : a.r_v;
-  it.col = (it.k_axis ? g : g - gk) * kQ4Group + 8 * it.sub;
+  it.col = (it.k_axis ? g : g - gk) * kQ4Group + 16 * it.sub;
   it.active = it.col < it.r;
   it.code_at = (it.k_axis ? 0 : a.r_k / 2) + it.col / 2;
   it.scale_at = q4_scale_offset(a.r_k, a.r_v) + 2 * g;
   return it;
 }
 
+// Sixteen latents, and the bits of the largest |c| among them (NaN sorts above infinity).
+__device__ __forceinline__ uint32_t load16(const __nv_bfloat16* p, float (&v)[16]) {
+  const uint4 x = __ldg(reinterpret_cast<const uint4*>(p)), y = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+  }
+  return max(top << 16, top & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t load16(const float* p, float (&v)[16]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
+    v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return top;
+}
+
+// Bit of column e of a code word.
+__host__ __device__ constexpr int q4_bit(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
+
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_store_kernel(const __grid_constant__ Q4CopyArgs a) {
   const uint32_t i = blockIdx.x * kQ4Threads + threadIdx.x;
-  // whole warps: every lane takes part in the shuffles below
+  // whole warps: every lane takes part in the shuffle below
   const bool live = i < a.n_items;
   const Q4Item it = q4_item(a, live ? i : a.n_items - 1);
   const int64_t n = static_cast<int64_t>(a.tok0) + it.n;
-  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const T* src = static_cast<const T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col;
-  if (live && it.active) load8(src, v);
-  const int64_t row = live ? q4_row(a, __ldg(a.slots + n), it.h, true) : -1;
-  // max |c| over the group, on the bits of |c|: NaN sorts above infinity, so either shows
+  float v[16];
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+  for (int e = 0; e < 16; ++e) v[e] = 0.f;
+  if (live && it.active) top = load16(static_cast<const T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col, v);
+  const int64_t row = live ? q4_row(a, __ldg(a.slots + n), it.h, true) : -1;
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   if (row < 0) return;
   uint8_t* dst = a.rows + row * a.row_bytes;
   const bool finite = top < 0x7f800000u;
@@ -110,25 +116,68 @@ __global__ void __launch_bounds__(kQ4Threads) q4_store_kernel(const __grid_const
   const __nv_bfloat16 s16 =
       finite ? __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f)) : __ushort_as_bfloat16(0x7fc0);
   const float s = __bfloat162float(s16);
-  const bool some = finite && s > 0.f;
-  uint32_t w = 0;
+  uint32_t w[2];
+  if (sizeof(T) == 2 && finite && s >= kQ4Normal) {
+    // bf16 values: c / s has 8-bit numerator and denominator, so it is half an integer exactly or off
+    // by 2^-10 at least (for |c / s| >= 1/4).  c * (1 / s), 2^-22 off at most, rounded to multiples of
+    // 2^-11 is therefore on the same side or on the same tie, and rounds to the same code as
+    // the quotient.  |c / s| <= 7.03: no clamp.  1.5 * 2^23 + 8 leaves code + 8 in the low bits;
+    // a multiply-add per code packs the words, and the constant parts are taken off once.
+    const float inv = __frcp_rn(s);
+    constexpr uint32_t kBase = 0x4B400000u;   // bits of 1.5 * 2^23
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int code = some ? min(max(__float2int_rn(__fdiv_rn(v[e], s)), -7), 7) : 0;
-    w |= static_cast<uint32_t>(code + 8) << (4 * (e >> 1) + 16 * (e & 1));
+    for (int j = 0; j < 2; ++j) {
+      uint32_t sum = 0, base = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = __fadd_rn(__fmaf_rn(v[8 * j + e], inv, 6144.f), -6144.f);
+        sum += __float_as_uint(__fadd_rn(t, 12582920.f)) * (1u << q4_bit(e));
+        base += kBase * (1u << q4_bit(e));
+      }
+      w[j] = sum - base;
+    }
+  } else {
+    const bool some = finite && s > 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w[j] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int code = some ? min(max(__float2int_rn(__fdiv_rn(v[8 * j + e], s)), -7), 7) : 0;
+        w[j] |= static_cast<uint32_t>(code + 8) << q4_bit(e);
+      }
+    }
   }
-  if (it.active) *reinterpret_cast<uint32_t*>(dst + it.code_at) = w;
+  if (it.active) *reinterpret_cast<uint2*>(dst + it.code_at) = make_uint2(w[0], w[1]);
   if (it.sub == 0) *reinterpret_cast<__nv_bfloat16*>(dst + it.scale_at) = s16;
   // the row's padding, by the last group's threads: rows are fully defined
-  if (!it.k_axis && it.scale_at + 2 == q4_scale_offset(a.r_k, a.r_v) + 2 * (q4_groups(a.r_k) + q4_groups(a.r_v)))
-    for (int p = it.scale_at + 2 + 2 * it.sub; p < a.row_bytes; p += 8) *reinterpret_cast<uint16_t*>(dst + p) = 0;
+  if (!it.k_axis && it.scale_at + 2 == q4_scale_offset(a.r_k, a.r_v) + 2 * static_cast<int>(a.groups.d))
+    for (int p = it.scale_at + 2 + 2 * it.sub; p < a.row_bytes; p += 4) *reinterpret_cast<uint16_t*>(dst + p) = 0;
 }
 
-// Eight values of a code word.
-__device__ __forceinline__ void q4_unpack8(uint32_t w, float s, float (&v)[8]) {
+// Eight values of a code word: code * scale, rounded once to the storage type.
+__device__ __forceinline__ void put8(__nv_bfloat16* p, uint32_t w, __nv_bfloat16 s) {
+  // 128 + code + 8 has unit 1 in bf16; the difference is exact, the product rounds once
+  const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(0x4308)), s2 = __bfloat162bfloat162(s);   // 136
+  uint32_t o[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    v[e] = static_cast<float>(static_cast<int>((w >> (4 * (e >> 1) + 16 * (e & 1))) & 15u) - 8) * s;
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 y = __hmul2(__hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), off), s2);
+    o[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void q4_unpack8(uint32_t w, float s, float (&v)[8]) {
+  // 2^23 + code + 8 has unit 1 in fp32
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (__uint_as_float(((w >> q4_bit(e)) & 15u) | 0x4B000000u) - 8388616.f) * s;
+}
+__device__ __forceinline__ void put8(float* p, uint32_t w, __nv_bfloat16 s) {
+  float v[8];
+  q4_unpack8(w, __bfloat162float(s), v);
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 template <typename T>
@@ -141,33 +190,38 @@ __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_consta
   const int64_t row = q4_row(a, __ldg(a.slots + n), it.h, true);
   if (row < 0) return;
   const uint8_t* src = a.rows + row * a.row_bytes;
-  const float s = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(src + it.scale_at));
-  float v[8];
-  q4_unpack8(*reinterpret_cast<const uint32_t*>(src + it.code_at), s, v);
-  store8(static_cast<T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col, v);
+  const __nv_bfloat16 s = *reinterpret_cast<const __nv_bfloat16*>(src + it.scale_at);
+  const uint2 w = *reinterpret_cast<const uint2*>(src + it.code_at);
+  T* dst = static_cast<T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col;
+  put8(dst, w.x, s);
+  put8(dst + 8, w.y, s);
 }
 
 // ----------------------------------------------------------------- fp32 decode
 
 // Decode attention over 4-bit rows for fp32 storage, in fp32 arithmetic: one block
-// per (sequence, head, split of whole 128-token tiles), one token per thread.  The
-// score is Eq. (3) with RoPE after reconstruction, regrouped per frequency pair as in
-// lla_paged_generic.cu, with the folded query in fp32; one online softmax over the
-// split's tiles, the value path absorbed; a record per split, merged by the combine.
-constexpr int kPlainThreads = 128;
-constexpr float kPlainScale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
+// per (sequence, head, split of whole 128-token tiles).  The score is Eq. (3) with RoPE
+// after reconstruction, regrouped per frequency pair as in lla_paged_generic.cu, with the
+// folded query in fp32: four neighbouring threads share a token, each with a quarter of the 128
+// rotary coordinates (shared-memory reads of the folded query bound it: one 16-byte read per
+// four multiply-adds, whatever the split, and a small call wants many threads).  One online
+// softmax over the split's tiles, the value path absorbed; a record per split, merged by the combine.
+constexpr int kF32Threads = 512;
+constexpr int kParts = 4;             // threads of a token
+constexpr int kCols = 128 / kParts;   // rotary coordinates of a thread
+constexpr float kQ4ScoreScale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   const int L = __ldg(a.seq_lens + b);
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
-__global__ void __launch_bounds__(kPlainThreads) q4_f32_kernel(const __grid_constant__ Q4DecodeArgs a) {
+__global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_constant__ Q4DecodeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine waits for this grid
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float bc[64], bs[64], qr[kHeadDim], pw[kPlainThreads], red[4];
+  __shared__ float bias[128], qr[kHeadDim], pw[kTile], red[kF32Threads / 32], sums[kF32Threads];
   const int rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
-  float* zc = reinterpret_cast<float*>(smem);                        // [rk][64] cosine part
-  float* zs = zc + rk * 64;                                          // [rk][64] sine part
+  float* z = reinterpret_cast<float*>(smem);                         // [rk][128]: cosine, then sine coordinates
   uint8_t* tile = smem + static_cast<size_t>(rk) * 512;              // [128][rb + 16]
   const int ts = rb + 16;
   const int64_t id = blockIdx.x;
@@ -178,17 +232,27 @@ __global__ void __launch_bounds__(kPlainThreads) q4_f32_kernel(const __grid_cons
   const int L0 = __ldg(a.seq_lens + b);
   if (sp == 0 && (L0 < 0 || L0 > a.L_max) && tid == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
   const int L = q4_len(a, b);
-  const int64_t j_lo = sp * a.chunk, j_hi = min(static_cast<int64_t>(L), j_lo + a.chunk);
-  if (j_lo >= j_hi) return;
   int qp = __ldg(a.q_pos + b);
   if (qp < 0 || qp >= a.rope_len) {
     if (tid == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
     qp = qp < 0 ? 0 : static_cast<int>(a.rope_len - 1);
   }
+  const int64_t j_lo = sp * a.chunk, j_hi = min(static_cast<int64_t>(L), j_lo + a.chunk);
+  if (j_lo >= j_hi) return;
   auto pair_of = [&](int f, int& i0, int& i1) {
     i0 = a.rope_style == 0 ? f : 2 * f;
     i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
   };
+  // the split's first rows are requested before the folded query is formed
+  auto fetch = [&](int64_t j0) {
+    const int64_t j = j0 + tid / kParts;
+    if (j >= j_hi) return;
+    const int64_t row = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, j, a.status);
+    const uint4* src = reinterpret_cast<const uint4*>(a.rows + row * rb);
+    uint4* dst = reinterpret_cast<uint4*>(tile + static_cast<size_t>(tid / kParts) * ts);
+    for (int i = tid % kParts; i < rb / 16; i += kParts) dst[i] = __ldg(src + i);
+  };
+  fetch(j_lo);
   const float* q = static_cast<const float*>(a.q) + u * kHeadDim;
   const float* mk = a.mu_k + h * a.mu_hstride;
   if (tid < 64) {
@@ -197,122 +261,143 @@ __global__ void __launch_bounds__(kPlainThreads) q4_f32_kernel(const __grid_cons
     const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + tid);
     const float s = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + tid);
     const float x0 = __ldg(q + i0), x1 = __ldg(q + i1);
-    const float q0 = (x0 * c - x1 * s) * kPlainScale, q1 = (x0 * s + x1 * c) * kPlainScale;
+    const float q0 = (x0 * c - x1 * s) * kQ4ScoreScale, q1 = (x0 * s + x1 * c) * kQ4ScoreScale;
     qr[i0] = q0;
     qr[i1] = q1;
-    bc[tid] = q0 * mk[i0] + q1 * mk[i1];
-    bs[tid] = q1 * mk[i0] - q0 * mk[i1];
+    bias[tid] = q0 * mk[i0] + q1 * mk[i1];
+    bias[64 + tid] = q1 * mk[i0] - q0 * mk[i1];
   }
   __syncthreads();
   const float* W = static_cast<const float*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk;
-  for (int i = tid; i < 64 * rk; i += kPlainThreads) {
-    const int f = i / rk, k = i - f * rk;
+  // four columns of one frequency per item: 16-byte loads, several in flight; 4 x 8 (columns,
+  // frequencies) per warp
+#pragma unroll 3
+  for (int i = tid; i < 16 * rk; i += kF32Threads) {
+    const int q4 = i & 3, f = (i >> 2) & 63, k = (i >> 8) * 16 + 4 * q4;   // rk is a multiple of 16
     int i0, i1;
     pair_of(f, i0, i1);
-    const float w0 = __ldg(W + static_cast<int64_t>(i0) * rk + k), w1 = __ldg(W + static_cast<int64_t>(i1) * rk + k);
-    zc[k * 64 + f] = qr[i0] * w0 + qr[i1] * w1;
-    zs[k * 64 + f] = qr[i1] * w0 - qr[i0] * w1;
+    const float4 w0 = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(i0) * rk + k));
+    const float4 w1 = __ldg(reinterpret_cast<const float4*>(W + static_cast<int64_t>(i1) * rk + k));
+    const float q0 = qr[i0], q1 = qr[i1];
+    const float u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[(k + e) * 128 + f] = q0 * u0[e] + q1 * u1[e];
+      z[(k + e) * 128 + 64 + f] = q1 * u0[e] - q0 * u1[e];
+    }
   }
-  float acc[2] = {0.f, 0.f};
-  float m_run = -INFINITY, l_run = 0.f;
+  // V: a thread's column, and which share of a tile's tokens it adds up
+  const int shares = rv <= 128 ? 4 : 2, width = kF32Threads / shares, col = tid % width, share = tid / width;
+  const int v_at = rk / 2 + 4 * (col / 8), v_bit = 4 * ((col & 7) >> 1) + 16 * (col & 1);
+  const int v_scale = q4_scale_offset(rk, rv) + 2 * (q4_groups(rk) + col / kQ4Group);
+  float acc = 0.f, m_run = -INFINITY, l_run = 0.f;
   __syncthreads();
-  for (int64_t j0 = j_lo; j0 < j_hi; j0 += kPlainThreads) {
-    const int64_t j = j0 + tid;
+  const int token = tid / kParts, part = tid % kParts;
+  for (int64_t j0 = j_lo; j0 < j_hi; j0 += kTile) {
+    const int64_t j = j0 + token;
     const bool valid = j < j_hi;
-    const int nt = static_cast<int>(min(static_cast<int64_t>(kPlainThreads), j_hi - j0));
-    uint8_t* mine = tile + static_cast<size_t>(tid) * ts;
-    float s = -INFINITY;
+    const int nt = static_cast<int>(min(static_cast<int64_t>(kTile), j_hi - j0));
+    const uint8_t* mine = tile + static_cast<size_t>(token) * ts;
+    float s = 0.f;
     if (valid) {
-      const int64_t row = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, j, a.status);
-      const uint4* src = reinterpret_cast<const uint4*>(a.rows + row * rb);
-      for (int i = 0; i < rb / 16; ++i) reinterpret_cast<uint4*>(mine)[i] = __ldg(src + i);
-      float A[64];
-      const float* cr = a.rope_cos + j * 64;
-      const float* sr = a.rope_sin + j * 64;
-      s = 0.f;
-      // the cosine part, then the sine part: 64 running sums each
+      // this part's coordinates: four of every sixteen, so that a token's four reads are neighbours
+      float A[kCols];
+#pragma unroll
+      for (int f = 0; f < kCols; ++f) A[f] = bias[16 * (f / 4) + 4 * part + f % 4];
+      const float* zp = z + 4 * part;
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const float* z = part == 0 ? zc : zs;
-        const float* bias = part == 0 ? bc : bs;
+      for (int k0 = 0; k0 < rk; k0 += 8) {
+        float c8[8];
+        const float sc = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+            mine + q4_scale_offset(rk, rv) + 2 * (k0 / kQ4Group)));
+        q4_unpack8(*reinterpret_cast<const uint32_t*>(mine + k0 / 2), sc, c8);
 #pragma unroll
-        for (int f = 0; f < 64; ++f) A[f] = bias[f];
-#pragma unroll 1
-        for (int k0 = 0; k0 < rk; k0 += 8) {
-          float c8[8];
-          const float sc = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-              mine + q4_scale_offset(rk, rv) + 2 * (k0 / kQ4Group)));
-          q4_unpack8(*reinterpret_cast<const uint32_t*>(mine + k0 / 2), sc, c8);
+        for (int e = 0; e < 8; ++e) {
+          const float4* zr = reinterpret_cast<const float4*>(zp + (k0 + e) * 128);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4* zr = reinterpret_cast<const float4*>(z + (k0 + e) * 64);
-#pragma unroll
-            for (int g = 0; g < 16; ++g) {
-              const float4 z4 = zr[g];
-              A[4 * g] = fmaf(c8[e], z4.x, A[4 * g]);
-              A[4 * g + 1] = fmaf(c8[e], z4.y, A[4 * g + 1]);
-              A[4 * g + 2] = fmaf(c8[e], z4.z, A[4 * g + 2]);
-              A[4 * g + 3] = fmaf(c8[e], z4.w, A[4 * g + 3]);
-            }
+          for (int g = 0; g < kCols / 4; ++g) {
+            const float4 z4 = zr[4 * g];
+            A[4 * g] = fmaf(c8[e], z4.x, A[4 * g]);
+            A[4 * g + 1] = fmaf(c8[e], z4.y, A[4 * g + 1]);
+            A[4 * g + 2] = fmaf(c8[e], z4.z, A[4 * g + 2]);
+            A[4 * g + 3] = fmaf(c8[e], z4.w, A[4 * g + 3]);
           }
         }
-        const float* t = part == 0 ? cr : sr;
+      }
 #pragma unroll
-        for (int f = 0; f < 64; f += 4) {
-          const float4 t4 = __ldg(reinterpret_cast<const float4*>(t + f));
-          s = fmaf(t4.x, A[f], fmaf(t4.y, A[f + 1], fmaf(t4.z, A[f + 2], fmaf(t4.w, A[f + 3], s))));
-        }
+      for (int f = 0; f < kCols; f += 4) {
+        const float* t = (f < kCols / 2 ? a.rope_cos : a.rope_sin) + j * 64 + 16 * (f / 4 % 4) + 4 * part;
+        const float4 t4 = __ldg(reinterpret_cast<const float4*>(t));
+        s = fmaf(t4.x, A[f], fmaf(t4.y, A[f + 1], fmaf(t4.z, A[f + 2], fmaf(t4.w, A[f + 3], s))));
       }
     }
+#pragma unroll
+    for (int o = 1; o < kParts; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (!valid) s = -INFINITY;
     // ---- online softmax over the tile (log2 units)
-    float mt = warp_max(s);
-    if (lane == 0) red[wid] = mt;
+    const float mw = warp_max(s);
+    if (lane == 0) red[wid] = mw;
     __syncthreads();
-    const float m_new = fmaxf(m_run, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+    float m_new = m_run;
+#pragma unroll
+    for (int i = 0; i < kF32Threads / 32; ++i) m_new = fmaxf(m_new, red[i]);
     const float scale = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);   // the first tile: 0
     const float p = valid ? (m_new == -INFINITY ? s - s : exp2f(s - m_new)) : 0.f;   // all NaN: stays NaN
-    pw[tid] = p;
-    __syncthreads();   // pw and the tile's rows are complete; red is free again
-    const float ps = warp_sum(p);
+    if (part == 0) pw[token] = p;
+    const float ps = warp_sum(part == 0 ? p : 0.f);
+    __syncthreads();   // pw complete; red is read
     if (lane == 0) red[wid] = ps;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int k = tid + half * kPlainThreads;
-      if (k >= rv) break;
-      const int at = rk / 2 + 4 * (k / 8) , bit = 4 * ((k & 7) >> 1) + 16 * (k & 1);
-      const int sat = q4_scale_offset(rk, rv) + 2 * (q4_groups(rk) + k / kQ4Group);
+    if (col < rv) {
       float v = 0.f;
-      for (int i = 0; i < nt; ++i) {
+#pragma unroll 4
+      for (int i = share; i < nt; i += shares) {
         const uint8_t* r = tile + static_cast<size_t>(i) * ts;
-        const float c = static_cast<float>(static_cast<int>((*reinterpret_cast<const uint32_t*>(r + at) >> bit) & 15u) - 8);
-        v = fmaf(pw[i], c * __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(r + sat)), v);
+        const float c = static_cast<float>(static_cast<int>((*reinterpret_cast<const uint32_t*>(r + v_at) >> v_bit) & 15u) - 8);
+        v = fmaf(pw[i], c * __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(r + v_scale)), v);
       }
-      acc[half] = fmaf(acc[half], scale, v);
+      acc = fmaf(acc, scale, v);
     }
-    __syncthreads();   // sums complete; the rows are free for the next tile
-    l_run = l_run * scale + (red[0] + red[1] + red[2] + red[3]);
+    __syncthreads();   // red holds the sums; the rows are free for the next tile
+    if (j0 + kTile < j_hi) fetch(j0 + kTile);
+    float ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < kF32Threads / 32; ++i) ls += red[i];
+    l_run = l_run * scale + ls;
     m_run = m_new;
-    __syncthreads();   // everyone has read red
+    __syncthreads();   // the next rows are in place; everyone has read red
   }
+  sums[tid] = acc;
+  __syncthreads();
   float* rec = a.records + id * (rv + kRecordHead);
   if (tid == 0) {
     rec[0] = m_run;
     rec[1] = l_run;
   }
-  for (int half = 0; half < 2; ++half)
-    if (tid + half * kPlainThreads < rv) rec[kRecordHead + tid + half * kPlainThreads] = acc[half];
+  if (tid < rv) {   // rv <= width
+    float v = sums[tid];
+    for (int i = 1; i < shares; ++i) v += sums[i * width + tid];
+    rec[kRecordHead + tid] = v;
+  }
 }
 
 // Merge a (sequence, head)'s split records by log-sum-exp, apply W_up,v once (Appendix J
-// "Absorbed attention") and normalise.  Block = (head, sequence), one output per thread.
-__global__ void __launch_bounds__(kPlainThreads) q4_f32_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
+// "Absorbed attention") and normalise.  Block = (head, sequence), two threads per output, their halves of
+// its row requested before the wait for the decode grid.
+constexpr int kF32CombineThreads = 256;
+__global__ void __launch_bounds__(kF32CombineThreads) q4_f32_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
+  constexpr int kRegs = kMaxRankPerHead / 8;   // 16-byte loads of half a row
   __shared__ float acc[kMaxRankPerHead];
   const int64_t u = blockIdx.x;
   const int b = static_cast<int>(u / a.H), h = static_cast<int>(u - static_cast<int64_t>(b) * a.H), tid = threadIdx.x;
-  const int L = q4_len(a, b), rv = a.r_v;
+  const int L = q4_len(a, b), rv = a.r_v, e = tid >> 1, half = tid & 1;
+  const float4* W = reinterpret_cast<const float4*>(static_cast<const float*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + e) * rv);
+  float4 w[kRegs];
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) w[i] = 4 * (2 * i + half) < rv ? __ldg(W + 2 * i + half) : make_float4(0.f, 0.f, 0.f, 0.f);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float* out = static_cast<float*>(a.out) + u * kHeadDim;
   if (L == 0) {
-    out[tid] = 0.f;
+    if (half == 0) out[e] = 0.f;
     if (tid == 0 && a.lse) a.lse[u] = -INFINITY;
     return;
   }
@@ -320,40 +405,36 @@ __global__ void __launch_bounds__(kPlainThreads) q4_f32_combine_kernel(const __g
   const float* rec = a.records + u * a.splits * (rv + kRecordHead);
   float m = -INFINITY;
   for (int i = 0; i < n; ++i) m = fmaxf(m, rec[static_cast<int64_t>(i) * (rv + kRecordHead)]);
-  float l = 0.f, v[2] = {0.f, 0.f};
+  float l = 0.f, v = 0.f;
   for (int i = 0; i < n; ++i) {
     const float* r = rec + static_cast<int64_t>(i) * (rv + kRecordHead);
-    const float w = m == -INFINITY ? 1.f : exp2f(r[0] - m);   // no maximum: every score was NaN, and so is l
-    l = fmaf(r[1], w, l);
-    for (int half = 0; half < 2; ++half)
-      if (tid + half * kPlainThreads < rv) v[half] = fmaf(r[kRecordHead + tid + half * kPlainThreads], w, v[half]);
+    const float f = m == -INFINITY ? 1.f : exp2f(r[0] - m);   // no maximum: every score was NaN, and so is l
+    l = fmaf(r[1], f, l);
+    if (tid < rv) v = fmaf(r[kRecordHead + tid], f, v);
   }
-  for (int half = 0; half < 2; ++half)
-    if (tid + half * kPlainThreads < rv) acc[tid + half * kPlainThreads] = v[half];
+  if (tid < rv) acc[tid] = v;
   __syncthreads();
-  const float* W = static_cast<const float*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * rv;
   float o = 0.f;
-  for (int k = 0; k < rv; k += 8) {
-    float w8[8];
-    load8(W + k, w8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o = fmaf(acc[k + e], w8[e], o);
+  for (int i = 0; i < kRegs; ++i) {
+    const int k = 4 * (2 * i + half);
+    if (k < rv) o = fmaf(acc[k], w[i].x, fmaf(acc[k + 1], w[i].y, fmaf(acc[k + 2], w[i].z, fmaf(acc[k + 3], w[i].w, o))));
   }
-  out[tid] = o / l + a.mu_v[h * a.mu_hstride + tid];
+  o += __shfl_xor_sync(0xffffffffu, o, 1);
+  if (half == 0) out[e] = o / l + a.mu_v[h * a.mu_hstride + e];
   if (tid == 0 && a.lse) a.lse[u] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace
 
 cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(a.r_k) * 512 + static_cast<size_t>(kPlainThreads) * (a.row_bytes + 16);
+  const size_t smem = static_cast<size_t>(a.r_k) * 512 + static_cast<size_t>(kTile) * (a.row_bytes + 16);
   cudaError_t e = allow_smem(q4_f32_kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * a.H;
-  q4_f32_kernel<<<static_cast<unsigned>(units * a.splits), kPlainThreads, smem, s>>>(a);
+  q4_f32_kernel<<<static_cast<unsigned>(units * a.splits), kF32Threads, smem, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  q4_f32_combine_kernel<<<static_cast<unsigned>(units), kPlainThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(q4_f32_combine_kernel, dim3(static_cast<unsigned>(units)), dim3(kF32CombineThreads), 0, s, a);
 }
 
 int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms) {
@@ -396,7 +477,9 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
   a.r_k = dims->r_k;
   a.r_v = dims->r_v;
   a.row_bytes = q4_row_bytes(dims->r_k, dims->r_v);
-  a.page_size = cache->page_size;
+  a.groups = FastDiv(q4_groups(dims->r_k) + q4_groups(dims->r_v));
+  a.heads = FastDiv(dims->H);
+  a.page = FastDiv(cache->page_size);
   a.num_slots = cache->num_pages * cache->page_size;
   a.slots = slots;
   a.k = k;
@@ -405,7 +488,7 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // launches of at most 2^30 items keep the item arithmetic in 32 bits
-  const int64_t per_tok = static_cast<int64_t>(dims->H) * 4 * (q4_groups(dims->r_k) + q4_groups(dims->r_v));
+  const int64_t per_tok = static_cast<int64_t>(dims->H) * 2 * (q4_groups(dims->r_k) + q4_groups(dims->r_v));
   if (per_tok > (int64_t(1) << 30)) return LLA_ERR_UNSUPPORTED;
   const int64_t chunk = (int64_t(1) << 30) / per_tok;
   for (int64_t t = 0; t < N; t += chunk) {

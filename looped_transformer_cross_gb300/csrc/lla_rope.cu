@@ -6,6 +6,7 @@
 // decode kernels fuse; these calls serve what runs beside them: the exact attention of
 // a prefill, the consumers of the window's keys, and the codec's training, whose
 // gradient is the inverse rotation.
+#include <algorithm>
 #include <cmath>
 
 #include "lla_kernels.h"
@@ -18,7 +19,7 @@ namespace {
 
 constexpr int kMaxHalf = 128;         // frequencies of a row
 constexpr int kTableThreads = 256;
-constexpr int kTableRows = 16;        // rows of a thread
+constexpr int kTableRows = 16;        // rows of a thread at most
 
 // Angular steps per position in turns, as 64-bit fixed-point fractions: position p
 // sits at p * turn mod 2^64, an exact integer product, so a far position loses
@@ -27,6 +28,7 @@ struct TurnArgs {
   uint64_t turn[kMaxHalf];
   int half;
   int64_t pos0, n_pos;
+  int rows;                           // rows of a thread
   float* cos_out;
   float* sin_out;
 };
@@ -51,7 +53,7 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
   const int rows = kTableThreads / per_row;               // rows of the block at a time
   const int r = threadIdx.x / per_row, f = (threadIdx.x % per_row) * VEC;
   if (r >= rows) return;
-  int64_t p = static_cast<int64_t>(blockIdx.x) * rows * kTableRows + r;
+  int64_t p = static_cast<int64_t>(blockIdx.x) * rows * a.rows + r;
   uint64_t phase[VEC], step[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -59,7 +61,7 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
     phase[e] = static_cast<uint64_t>(a.pos0 + p) * t;
     step[e] = static_cast<uint64_t>(rows) * t;
   }
-  for (int i = 0; i < kTableRows && p < a.n_pos; ++i, p += rows) {
+  for (int i = 0; i < a.rows && p < a.n_pos; ++i, p += rows) {
     float c[VEC], s[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
@@ -112,8 +114,9 @@ struct ApplyArgs {
   const void* x;
   void* out;
   int64_t x_tok, x_head, out_tok, out_head;   // strides in elements
-  int heads, d_x, offset, half;
-  int rot_items, items;                       // per token-head: rotated items, then copied ones
+  int offset, half;
+  int rot_items;                              // per token-head: rotated items, then copied ones
+  FastDiv items, per_head;                    // items of a token-head; heads
   int64_t tok0;                               // first token of this launch
   uint32_t n_items;                           // items of this launch
   const int32_t* pos;
@@ -151,8 +154,8 @@ template <typename T, int VEC, int kStyle>
 __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const __grid_constant__ ApplyArgs a) {
   const uint32_t i = blockIdx.x * kApplyThreads + threadIdx.x;
   if (i >= a.n_items) return;
-  const uint32_t row = i / static_cast<uint32_t>(a.items), item = i - row * a.items;
-  const uint32_t t = row / static_cast<uint32_t>(a.heads), h = row - t * a.heads;
+  const uint32_t row = a.items.div(i), item = i - row * a.items.d;
+  const uint32_t t = a.per_head.div(row), h = row - t * a.per_head.d;
   const int64_t n = a.tok0 + t;
   const T* x = static_cast<const T*>(a.x) + n * a.x_tok + h * a.x_head;
   T* out = static_cast<T*>(a.out) + n * a.out_tok + h * a.out_head;
@@ -242,8 +245,11 @@ lla_status lla_rope_table_scaled(const lla_dims* dims, const lla_rope_scaling* s
   a.sin_out = rope_sin;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int vec = a.half % 4 == 0 ? 4 : 1;
-  const int64_t rows = kTableThreads / (a.half / vec) * kTableRows;
-  const unsigned blocks = static_cast<unsigned>((n_pos + rows - 1) / rows);
+  // a thread's frequencies are set up once for several rows, as long as every SM has four blocks
+  const int64_t at_once = kTableThreads / (a.half / vec), sms = device_sm_count();
+  if (sms <= 0) return LLA_ERR_CUDA;
+  a.rows = static_cast<int>(std::min<int64_t>(kTableRows, std::max<int64_t>(1, n_pos / (at_once * 4 * sms))));
+  const unsigned blocks = static_cast<unsigned>((n_pos + at_once * a.rows - 1) / (at_once * a.rows));
   if (vec == 4) rope_table_kernel<4><<<blocks, kTableThreads, 0, s>>>(a);
   else rope_table_kernel<1><<<blocks, kTableThreads, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
@@ -297,8 +303,6 @@ lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_str
   a.x_head = x_head_stride;
   a.out_tok = out_tok_stride;
   a.out_head = out_head_stride;
-  a.heads = heads;
-  a.d_x = d_x;
   a.offset = offset;
   a.half = d_rope / 2;
   a.pos = pos;
@@ -317,10 +321,11 @@ lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_str
                    all % wide == 0;
   const int V = vec ? wide : 1;
   a.rot_items = a.half / V;
-  a.items = a.rot_items + (in_place ? 0 : (d_x - d_rope) / V);
+  a.items = FastDiv(a.rot_items + (in_place ? 0 : (d_x - d_rope) / V));
+  a.per_head = FastDiv(heads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // launches of at most 2^30 items keep the item arithmetic in 32 bits
-  const int64_t per_tok = static_cast<int64_t>(heads) * a.items;
+  const int64_t per_tok = static_cast<int64_t>(heads) * a.items.d;
   if (per_tok > (int64_t(1) << 30)) return LLA_ERR_UNSUPPORTED;
   const int64_t chunk = (int64_t(1) << 30) / per_tok;
   for (int64_t t = 0; t < N; t += chunk) {
