@@ -15,7 +15,7 @@
 //      (q4_rows_kernel), so that one bulk copy brings a tile: an fp32 table read here would be
 //      more L2 traffic than the latents, and rows turned in registers from tile to tile cost a fifth of all
 //      instructions (measured: 144 us against the present time at 32 x 4096).
-//      B = the head's Z rows (f16, resident for the whole run), two bias rows (f16 high
+//      (All heads of a group share one chain where their rows fit.)  B = a head's Z rows (f16, resident for the whole run), two bias rows (f16 high
 //      and low part) and one row -8 sum Z per scale group, which takes the codes' offset back.
 //   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
 //      subnormals (code * 2^-24, or * 2^-20 from the next nibble), converted, and summed per
@@ -43,8 +43,11 @@ namespace {
 constexpr int kQ4TileThreads = 640;
 constexpr int kWorkers = 512;                    // epilogue and V warpgroups
 constexpr int kQ4MaxNS = 16;
-constexpr int kMaxG = 4;                         // G buffers
-constexpr int kRowTile = 32768;                  // rotary tile: two K-major chunks of 128 rows x 128 bytes
+constexpr int kMaxG = 16;                        // G buffers
+constexpr int kMaxNh = 8;                        // heads of a group
+constexpr int kRowChunk = 16384;                 // half a rotary tile: a K-major chunk of 128 rows x 128 bytes
+constexpr int kRowTile = 2 * kRowChunk;
+constexpr int kNR = 3;                           // chunks of rotary tiles in shared memory
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
@@ -53,15 +56,13 @@ enum { kBarRun = 1, kBarWork = 2 };              // named barriers: workers + MM
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
-  uint64_t rfull[2], rempty[2], gfull[kMaxG], gempty[kMaxG];
+  uint64_t rfull[kNR], rempty[kNR], gfull[kMaxG], gempty[kMaxG];
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
   int start_b, start_hg, start_t, count;
-  float2 ml[8];                                  // run end: (m, l) of each epilogue warp
-  int head[2];                                   // run end: the head that each epilogue group held
+  float2 ml[kMaxNh][8];                          // run end: (m, l) of each head and epilogue warp
   int vref[8];                                   // run end: reference of each V warp
-  float qs[2][2][64];                            // rotated query, sc q'_i0 and sc q'_i1, per head
 };
 
 struct Slot {
@@ -122,9 +123,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
   return v;
 }
-__device__ __forceinline__ float4 lds128f(uint32_t p) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p));
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
   return v;
 }
 __device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
@@ -174,7 +175,7 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
-// Register shares of the warpgroups: 48 + 2 x 104 + 2 x 112 = 480 = 5 x 96, what the
+// Register shares of the warpgroups: 64 + 2 x 96 + 2 x 112 = 480 = 5 x 96, what the
 // block is launched with (640 threads of 96).
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       mbar_init(bar(misc->empty[s]), 8 / nh);       // the head's V warps, the last to read it
       mbar_init(bar(misc->wfull[s]), 4);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kNR; ++i) {
       mbar_init(bar(misc->rfull[i]), 1);
       mbar_init(bar(misc->rempty[i]), 1);
     }
@@ -293,6 +294,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     if (lane == 0) mbar_arrive(bar(m));
   };
 
+  float* qs = reinterpret_cast<float*>(sm + P.qs);   // rotated query, sc q'_i0 and sc q'_i1: [nh][2][64]
   // Builds the run's query operands, N rows of 128 rotary coordinates per head, all heads' rows
   // in two K-major chunks of 64 coordinates (128-byte swizzle); a head's are its r_k Z rows, bias high and low, -8 sum Z of each scale
   // group, zeros.  All workers; the previous run has ended.
@@ -313,8 +315,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       const float s = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + f);
       const float x0 = __bfloat162float(q[i0]), x1 = __bfloat162float(q[i1]);
       const float q0 = (x0 * c - x1 * s) * kQ4Scale, q1 = (x0 * s + x1 * c) * kQ4Scale;
-      misc->qs[hi][0][f] = q0;
-      misc->qs[hi][1][f] = q1;
+      qs[hi * 128 + f] = q0;
+      qs[hi * 128 + 64 + f] = q1;
       const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1);
       const float bias[2] = {q0 * m0 + q1 * m1, q1 * m0 - q0 * m1};
 #pragma unroll
@@ -352,8 +354,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         float q0[4], q1[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          q0[e] = misc->qs[hi][0][f0 + e];
-          q1[e] = misc->qs[hi][1][f0 + e];
+          q0[e] = qs[hi * 128 + f0 + e];
+          q1[e] = qs[hi * 128 + 64 + f0 + e];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     }
   };
   if (warp < 4) {
-    regs_dec<48>();
+    regs_dec<64>();
     if (warp == 0) {
       // ======================================================== producer of rows
       // Per head-tile the page pieces that its rows lie in, lane i copying piece i.  A position's page ids are
@@ -485,58 +487,61 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       int issued = 0;
       asm volatile("griddepcontrol.wait;" ::: "memory");   // they are written
       while (walk.next(a, ngroups, run))
-        for (int t = run.t0; t < run.t0 + run.n && ok; ++t) {
+        for (int c = 2 * run.t0; c < 2 * (run.t0 + run.n) && ok; ++c) {
           wait(misc->rempty[rs.i], rs.phase ^ 1u);
           if (!ok) break;
           if (lane == 0) {
             const uint32_t fb = bar(misc->rfull[rs.i]);
-            mbar_arrive_expect_tx(fb, kRowTile);
-            bulk_load(sbase + P.rows + rs.i * kRowTile, a.row_tiles + static_cast<int64_t>(t) * kRowTile, kRowTile, fb);
+            mbar_arrive_expect_tx(fb, kRowChunk);
+            bulk_load(sbase + P.rows + rs.i * kRowChunk, a.row_tiles + static_cast<int64_t>(c) * kRowChunk, kRowChunk, fb);
           }
           __syncwarp();
           ++issued;
-          rs.next(2);
+          rs.next(kNR);
         }
-      if (lane == 0) land(misc->rfull, rs, 2, issued);
+      if (lane == 0) land(misc->rfull, rs, kNR, issued);
     } else if (warp == 1) {
       // ======================================================== MMA issuer
       // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
       // step takes about as long for 256 columns as for 128, so the heads of a position share
-      // one chain where their rows fit; else each has its own (two where r_k = 256).
-      const bool together = 2 * N <= 256;
+      // one chain while their rows fit and their buffers are neighbours (r_k = 256: two chains a head).
+      const int together = max(1, 256 / N);
       Slot rs{0, 0u}, gs{0, 0u};
       while (walk.next(a, ngroups, run)) {
         const int nhg = min(nh, a.H - run.hg * nh);
         named_bar_sync(kBarRun, kWorkers + 32);   // operands built
         for (int t = 0; t < run.n; ++t) {
-          wait(misc->rfull[rs.i], rs.phase);
-          const uint64_t ad = umma_desc(sbase + P.rows + rs.i * kRowTile, 16, 1024, kSw128);
+          // the position's chunks: cosines, sines
+          Slot half[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            half[c] = rs;
+            rs.next(kNR);
+          }
           for (int hi = 0, heads; hi < nhg; hi += heads) {
-            heads = together && nhg - hi == 2 && gs.i + 1 < NG ? 2 : 1;   // two: into neighbouring buffers
-            Slot last = gs;
-            wait(misc->gempty[gs.i], gs.phase ^ 1u);
-            if (heads == 2) {
-              last.next(NG);
-              wait(misc->gempty[last.i], last.phase ^ 1u);
-            }
-            if (ok) {
-              tc_fence_after();
+            heads = min(together, min(nhg - hi, NG - gs.i));
+            for (int i = 0; i < heads; ++i) wait(misc->gempty[gs.i + i], gs.phase ^ 1u);
+            tc_fence_after();
+            const bool last = hi + heads == nhg;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              if (hi == 0) wait(misc->rfull[half[c].i], half[c].phase);
+              if (!ok) continue;
+              const uint64_t ad = umma_desc(sbase + P.rows + half[c].i * kRowChunk, 16, 1024, kSw128);
               for (int r0 = 0; r0 < heads * N; r0 += 256) {
                 const uint32_t idesc = umma_idesc_f16(128, min(heads * N - r0, 256));
-                const uint64_t bd = umma_desc(sbase + P.z + (hi * N + r0) * 128, 16, 1024, kSw128);
+                const uint64_t bd = umma_desc(sbase + P.z + c * P.z_chunk + (hi * N + r0) * 128, 16, 1024, kSw128);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                  umma_bf16_warp(tmem + gs.i * N + r0, ad + (kk >> 2) * (16384 >> 4) + 2 * (kk & 3),
-                                 bd + (kk >> 2) * (P.z_chunk >> 4) + 2 * (kk & 3), idesc, kk > 0 ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_warp(tmem + gs.i * N + r0, ad + 2 * kk, bd + 2 * kk, idesc, c + kk > 0 ? 1u : 0u);
               }
-              umma_commit_warp(bar(misc->gfull[gs.i]));
-              if (heads == 2) umma_commit_warp(bar(misc->gfull[last.i]));
-              if (hi + heads == nhg) umma_commit_warp(bar(misc->rempty[rs.i]));
+              if (last) umma_commit_warp(bar(misc->rempty[half[c].i]));
             }
-            gs = last;
-            gs.next(NG);
+            for (int i = 0; i < heads; ++i) {
+              if (ok) umma_commit_warp(bar(misc->gfull[gs.i]));
+              gs.next(NG);
+            }
           }
-          rs.next(2);
         }
         named_bar_sync(kBarRun, kWorkers + 32);   // run ended
       }
@@ -546,17 +551,21 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       while (!mbar_try_wait(bar(misc->mma_done), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
     }
   } else if (warp < 12) {
-    regs_inc<104>();
     // ======================================================== epilogue: scores, weights
     const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     Slot st{0, 0u}, gs{0, 0u};
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
+    // per head the warp's reference and each thread's own sum
+    float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * 33;
     while (walk.next(a, ngroups, run)) {
       const int nhg = min(nh, a.H - run.hg * nh);
       build(wtid);
-      float m = -INFINITY, l = 0.f;
-      const int held = nhg == 2 ? static_cast<int>((n ^ grp) & 1) : 0;   // the head whose state (m, l) is
+      for (int hi = 0; hi < nhg; ++hi) {
+        state[hi * 33 + lane] = 0.f;
+        if (lane == 0) state[hi * 33 + 32] = -INFINITY;
+      }
+      __syncwarp();
 #pragma unroll 1
       for (int t = 0; t < run.n; ++t) {
         const bool valid = row < run.L - (run.t0 + t) * kTile;
@@ -574,69 +583,92 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           uint32_t vtop = 0, vs[RV32];
 #pragma unroll
           for (int g = 0; g < RV32; ++g) {
-            vs[g] = lds16(r + scale_at + 2 * (gk + g));
+            vs[g] = 0;
+            if (valid) vs[g] = lds16(r + scale_at + 2 * (gk + g));   // (a row that holds no token may hold anything)
             vtop = max(vtop, vs[g] & 0x7FFFu);
           }
-          const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, valid ? vtop >> 7 : 0u)) - 126, 126);
-          const float ie = pow2(-E);
-          // ---- per scale group: 32 codes against G (a last group of 16: its other codes count as 0)
+          const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, vtop >> 7)) - 126, 126);
+          // ---- per scale group its codes against G: 32 columns, or 16 in a last group
+          auto sum8 = [&](uint32_t w, const float* G, float& lo, float& hi) {   // columns of one code word
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 c = __half22float2(bits_h2(w & 0x000F000Fu)), d = __half22float2(bits_h2(w & 0x00F000F0u));
+              w >>= 8;
+              lo = fmaf(c.x, G[4 * j], lo);
+              lo = fmaf(c.y, G[4 * j + 1], lo);
+              hi = fmaf(d.x, G[4 * j + 2], hi);
+              hi = fmaf(d.y, G[4 * j + 3], hi);
+            }
+          };
+          auto scaled = [&](uint32_t sc, float lo, float hi, float off) {
+            s = fmaf(__uint_as_float(sc << 16), fmaf(lo, 16777216.f, fmaf(hi, 1048576.f, off)), s);
+          };
+          const int whole = rk / kQ4Group;
 #pragma unroll 1
-          for (int g = 0; g < gk; ++g) {
+          for (int g = 0; g < whole; ++g) {
             float G[32], off[1];
             tmem_ld_x32(gcol + 32 * g, G);
             tmem_ld_x1(gcol + rk + 2 + g, off);
-            uint4 w4 = lds128(r + 16 * g);
-            const float sc = __uint_as_float(lds16(r + scale_at + 2 * g) << 16);
-            if (32 * g + 32 > rk) w4.z = w4.w = 0;
+            const uint4 w = lds128(r + 16 * g);
+            const uint32_t sc = lds16(r + scale_at + 2 * g);
             tmem_wait_ld();
-            float lo0 = 0.f, lo1 = 0.f, hi0 = 0.f, hi1 = 0.f;
-            uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const float2 c = __half22float2(bits_h2(w[i] & 0x000F000Fu)), d = __half22float2(bits_h2(w[i] & 0x00F000F0u));
-                w[i] >>= 8;
-                lo0 = fmaf(c.x, G[8 * i + 4 * j], lo0);
-                lo1 = fmaf(c.y, G[8 * i + 4 * j + 1], lo1);
-                hi0 = fmaf(d.x, G[8 * i + 4 * j + 2], hi0);
-                hi1 = fmaf(d.y, G[8 * i + 4 * j + 3], hi1);
-              }
-            s = fmaf(sc, fmaf(lo0 + lo1, 16777216.f, fmaf(hi0 + hi1, 1048576.f, off[0])), s);
+            float lo[2] = {0.f, 0.f}, hi2[2] = {0.f, 0.f};
+            sum8(w.x, G, lo[0], hi2[0]);
+            sum8(w.y, G + 8, lo[1], hi2[1]);
+            sum8(w.z, G + 16, lo[0], hi2[0]);
+            sum8(w.w, G + 24, lo[1], hi2[1]);
+            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0]);
+          }
+          if (whole < gk) {
+            float G[16], off[1];
+            tmem_ld_x16(gcol + 32 * whole, G);
+            tmem_ld_x1(gcol + rk + 2 + whole, off);
+            const uint2 w = lds64(r + 16 * whole);
+            const uint32_t sc = lds16(r + scale_at + 2 * whole);
+            tmem_wait_ld();
+            float lo[2] = {0.f, 0.f}, hi2[2] = {0.f, 0.f};
+            sum8(w.x, G, lo[0], hi2[0]);
+            sum8(w.y, G + 8, lo[1], hi2[1]);
+            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0]);
           }
           tc_fence_before();
           arrive(misc->gempty[gs.i]);
           s = valid ? s + (bias[0] + bias[1]) : -INFINITY;
           // ---- softmax of the warp's 32 tokens: integer reference, raised lazily
           const float mt = warp_max_redux(s);
+          float m = state[hi * 33 + 32], l = state[hi * 33 + lane];
           if (mt > m + kRaise) {
             const float mn = ceilf(mt);
             l *= exp2f(m - mn);
             m = mn;
+            __syncwarp();
+            if (lane == 0) state[hi * 33 + 32] = m;
           }
           const float p = s == -INFINITY ? 0.f : exp2f(s - m);
-          l += p;
+          state[hi * 33 + lane] = l + p;
           // ---- weights p * scale of each V group, relative to 2^(m + E)
+          // (scale / 2^E is below one and p at most 2^8: f16 holds the product; p / 2^E might not be finite)
+          const uint32_t out = tail + 2 * row;
+          const float ie = pow2(-E);
 #pragma unroll
-          for (int g = 0; g < RV32; ++g)
-            sts16(tail + 2 * (g * kWStride + row), __float2half_rn(valid ? p * (__uint_as_float(vs[g] << 16) * ie) : 0.f));
+          for (int g = 0; g < RV32; ++g) sts16(out + 2 * g * kWStride, __float2half_rn(__uint_as_float(vs[g] << 16) * ie * p));
           if (lane == 0) sts32(tail + P.w_bytes + 4 * q, m == -INFINITY ? kNoRef : static_cast<int>(m) + E);
           arrive(misc->wfull[st.i]);
         }
       }
       // ---- run end: (m, l) of this warp's tokens
-      l = warp_sum(l);
-      if (lane == 0) misc->ml[warp - 4] = make_float2(m, l);
-      if (lane == 0 && q == 0) misc->head[grp] = held;
+      for (int hi = 0; hi < nhg; ++hi) {
+        const float l = warp_sum(state[hi * 33 + lane]);
+        if (lane == 0) misc->ml[hi][warp - 4] = make_float2(state[hi * 33 + 32], l);
+      }
       named_bar_sync(kBarRun, kWorkers + 32);
     }
   } else {
     regs_inc<112>();
     // ======================================================== V: sum_j p_j c_v,j
     const int v = warp - 12, gid = lane >> 2, tig = lane & 3, wtid = tid - 128;
-    const int mine = nh == 2 ? v >> 2 : 0;                        // head of the group
-    const int g = nh == 2 ? v & 3 : v >> 1;                       // its 32 tokens: all of them, or 16
-    const int ks0 = nh == 2 ? 0 : v & 1, ks1 = nh == 2 ? 2 : ks0 + 1;
+    // a head has 8 / nh warps, each with 16 nh of a tile's tokens
+    const int per = 8 / nh, mine = v / per, ks_first = v % per * nh;
     // run-end sums, [8][RV32 * 32] in the rows of the warps' own head: read no more by then
     float* accs = reinterpret_cast<float*>(sm + P.z);
     const uint32_t half_sel = (gid & 1) ? 0x7632u : 0x5410u;
@@ -657,7 +689,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           if (hi != mine) continue;
           wait(misc->wfull[st.i], st.phase);
           const uint32_t rows = sbase + P.ring + st.i * P.stage, tail = rows + kTile * rb;
-          {
+#pragma unroll 1
+          for (int g = ks_first >> 1; 2 * g < ks_first + nh; ++g) {
+            // the reference of these 32 tokens' weights: the sums are rescaled when it rises
             const int r = static_cast<int>(lds32(tail + P.w_bytes + 4 * g));
             if (r > ref) {
               const float f = exp2f(static_cast<float>(ref) - static_cast<float>(r));
@@ -669,13 +703,15 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               for (int j = 0; j < 4; ++j) one[j] *= f;
               ref = r;
             }
-            const __half2 f2 = __float2half2_rn(exp2f(static_cast<float>(r) - static_cast<float>(ref)));
-            // tokens t0, t0 + 1 (k of the low half of B) and t0 + 8, t0 + 9 of each step of 16
-            const int t0 = 32 * g + 16 * ks0 + 2 * tig;
-            // (columns without a scale group repeat the last one's weights: never read from D)
-            uint32_t w = tail + 2 * (min(gid, RV32 - 1) * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
+            // 2^(r - ref) in f16 (0 below 2^-14: such weights no longer count)
+            const __half2 f2 = bits_h2(r - ref >= -14 ? static_cast<uint32_t>(r - ref + 15) * 0x04000400u : 0u);
+            const int ks_end = min(2 * g + 2, ks_first + nh);
 #pragma unroll 1
-            for (int ks = ks0; ks < ks1; ++ks, w += 32, p0 += 16 * rb) {
+            for (int ks = max(2 * g, ks_first); ks < ks_end; ++ks) {
+              // tokens t0, t0 + 1 (k of the low half of B) and t0 + 8, t0 + 9
+              // (columns without a scale group repeat the last one's weights: never read from D)
+              const int t0 = 16 * ks + 2 * tig;
+              const uint32_t w = tail + 2 * (min(gid, RV32 - 1) * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
               const uint32_t b0 = h2_bits(__hmul2(bits_h2(lds32(w)), f2)), b1 = h2_bits(__hmul2(bits_h2(lds32(w + 16)), f2));
               const uint32_t p1 = p0 + rb, p8 = p0 + 8 * rb, p9 = p1 + 8 * rb;
               mma16816(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, b0, b1);
@@ -704,7 +740,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       // ---- run end: the thread whose accumulator columns are a chunk's groups holds its
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
-      float* acc = accs + (mine * N * 32 + (nh == 2 ? v & 3 : v) * RV32 * 32);
+      float* acc = accs + (mine * N * 32 + v % per * RV32 * 32);
 #pragma unroll
       for (int c = 0; c < F; ++c) {
         if (tig != c) continue;
@@ -734,18 +770,17 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       for (int hi = 0; hi < nhg; ++hi) {
         float M = -INFINITY, ls = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (misc->head[i >> 2] == hi) M = fmaxf(M, misc->ml[i].x);
+        for (int i = 0; i < 8; ++i) M = fmaxf(M, misc->ml[hi][i].x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float2 x = misc->ml[i];
-          if (misc->head[i >> 2] == hi) ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // (no maximum: all NaN)
+          const float2 x = misc->ml[hi][i];
+          ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // (no maximum: every score was NaN)
         }
         float* rec = a.records + ((static_cast<int64_t>(u) + blockIdx.x) * nh + hi) * (rv + kRecordHead);
         if (vt < rv) {
           float s = 0.f;
-          for (int i = 0; i < 8 / nh; ++i)
-            s = fmaf(accs[hi * N * 32 + i * RV32 * 32 + vt], exp2f(static_cast<float>(misc->vref[hi * (8 / nh) + i]) - M), s);
+          for (int i = 0; i < per; ++i)
+            s = fmaf(accs[hi * N * 32 + i * RV32 * 32 + vt], exp2f(static_cast<float>(misc->vref[hi * per + i]) - M), s);
           rec[kRecordHead + vt] = s;
         }
         if (vt == 0) { rec[0] = M; rec[1] = ls; }
@@ -883,7 +918,13 @@ cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
 bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
   const int rb = q4_row_bytes(r_k, r_v), rv32 = (r_v + 31) / 32;
   auto al = [](int x, int a) { return (x + a - 1) / a * a; };
-  for (int nh = H >= 2 ? 2 : 1; nh >= 1; --nh) {
+  // Heads of a group: they share a position's rotary tile and, up to 256 operand rows, its MMA
+  // chain, which takes as long for one head as for all.  Eight or four only where they divide
+  // the heads (positions are dealt out as if all groups were alike) and their rows fit a
+  // chain; a head-tile stays in the ring while scores and V take their turns, so groups of several
+  // heads need room for copies ahead.
+  for (int nh = kMaxNh; nh >= 1; nh /= 2) {
+    if (nh > H || (nh > 2 && (H % nh || nh * (r_k + 16) > 256))) continue;
     *p = Q4Plan{};
     p->nh = nh;
     p->ngroups = (H + nh - 1) / nh;
@@ -891,17 +932,17 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     p->NG = std::min(kMaxG, 512 / p->N);
     p->z_chunk = nh * p->N * 128;
     p->w_bytes = rv32 * kWStride * 2;
-    p->stage = al(kTile * rb + p->w_bytes + 64, 128);
+    p->stage = kTile * rb + p->w_bytes + 16;
     int off = 0;
     p->z = off; off += 2 * p->z_chunk;
-    p->rows = off = al(off, 1024); off += 2 * kRowTile;
-    p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 128);
+    p->rows = off = al(off, 1024); off += kNR * kRowChunk;
+    p->qs = off; off += nh * 512;
+    p->state = off; off = al(off + 8 * nh * 33 * 4, 16);
+    p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 16);
     p->ring = off;
     p->NS = std::min((kSmemLimit - 1024 - off) / p->stage, kQ4MaxNS);
     p->bytes = off + p->NS * p->stage + 1024;
-    // a head-tile stays in the ring while K, scores and V take their turns: two heads
-    // per group (they share a position's table rows) only with room for copies ahead
-    if (p->NS >= (nh == 2 ? 4 : 2)) return true;
+    if (p->NS >= (nh == 1 ? 2 : std::max(4, nh))) return true;
   }
   return false;
 }
