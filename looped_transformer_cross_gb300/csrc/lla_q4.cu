@@ -623,9 +623,9 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
     a.ranges = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.ranges);
     a.grid = w.grid;
     a.row_tiles = static_cast<uint8_t*>(workspace) + w.row_tiles;
-    a.rows_grid = static_cast<int>(std::min<int64_t>((L_max + kTile - 1) / kTile, 4 * sms));
-    // sequences per combine block: W_up,v is read once for them; about four blocks per SM
-    a.combine_units = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, static_cast<int64_t>(a.B) * a.H / (4 * sms))));
+    a.rows_grid = static_cast<int>(std::min<int64_t>((L_max + 15) / 16, 8 * sms));
+    // sequences per combine block: W_up,v is read once for them, and two blocks per SM run at a time
+    a.combine_units = static_cast<int>(std::min<int64_t>(8, (static_cast<int64_t>(a.B) * a.H + 2 * sms - 1) / (2 * sms)));
     return launch_q4_tile(a, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
   }
   a.chunk = q4_plain_chunk(a.B, a.H, L_max, sms);

@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           q0[e] = qs[hi * 128 + f0 + e];
           q1[e] = qs[hi * 128 + 64 + f0 + e];
         }
+        // (rows n + j, n a multiple of 8: j alone makes the swizzle, so an address is one exclusive or)
+        const uint32_t z0 = sbase + P.z + (hi * N + n) * 128 + 2 * f0, z1 = z0 + P.z_chunk;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           float zc[4], zs[4];
@@ -368,15 +370,18 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             zc[e] = fmaf(q0[e], u, q1[e] * v);
             zs[e] = fmaf(q1[e], u, -q0[e] * v);
           }
+          // (-8 sum Z takes the codes' offset back: of the unrounded values, whose rounding errors, half
+          // a step of f16 each, add up to no more than the rounding of the sum itself)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum_c[e] += zc[e];
+            sum_s[e] += zs[e];
+          }
           const __half2 c0 = __floats2half2_rn(zc[0], zc[1]), c1 = __floats2half2_rn(zc[2], zc[3]);
           const __half2 s0 = __floats2half2_rn(zs[0], zs[1]), s1 = __floats2half2_rn(zs[2], zs[3]);
           top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
-          // (the sums of what the MMA reads: of the rounded values)
-          const float2 cf0 = __half22float2(c0), cf1 = __half22float2(c1), sf0 = __half22float2(s0), sf1 = __half22float2(s1);
-          sum_c[0] += cf0.x; sum_c[1] += cf0.y; sum_c[2] += cf1.x; sum_c[3] += cf1.y;
-          sum_s[0] += sf0.x; sum_s[1] += sf0.y; sum_s[2] += sf1.x; sum_s[3] += sf1.y;
-          sts64(at(hi, n + j, f0), h2_bits(c0), h2_bits(c1));
-          sts64(at(hi, n + j, 64 + f0), h2_bits(s0), h2_bits(s1));
+          sts64((z0 ^ (j << 4)) + 128 * j, h2_bits(c0), h2_bits(c1));
+          sts64((z1 ^ (j << 4)) + 128 * j, h2_bits(s0), h2_bits(s1));
         }
       }
       // the codes' offset: -8 sum Z over the scale group's columns
@@ -804,6 +809,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 // as the MMA reads them: chunk 0 the cosines, chunk 1 the sines, 128 bytes a row, 128-byte
 // swizzle.  Reads 512 bytes and writes 256 per position; the decode grid's set-up overlaps it.
 constexpr int kRowsThreads = 256;
+constexpr int kRowsPart = 16;        // positions of a block: short contexts want many blocks
 __global__ void __launch_bounds__(kRowsThreads) q4_rows_kernel(const __grid_constant__ Q4DecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int longest[kRowsThreads / 32];
@@ -816,19 +822,17 @@ __global__ void __launch_bounds__(kRowsThreads) q4_rows_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < kRowsThreads / 32; ++i) L = max(L, longest[i]);
   const int tiles = tiles_of(L);
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    uint8_t* out = a.row_tiles + static_cast<int64_t>(t) * kRowTile;
-#pragma unroll
-    for (int i = 0; i < kTile * 16 / kRowsThreads; ++i) {
-      const int at = tid + i * kRowsThreads, row = at >> 4, c = at & 15;   // 8 coordinates: 8 c ..
-      int64_t j = static_cast<int64_t>(t) * kTile + row;
-      j = j < a.rope_len ? j : a.rope_len - 1;   // behind the sequence's end: masked
-      const float4* src = reinterpret_cast<const float4*>((c < 8 ? a.rope_cos : a.rope_sin) + j * 64 + 8 * (c & 7));
-      const float4 x = __ldg(src), y = __ldg(src + 1);
-      *reinterpret_cast<uint4*>(out + (c >> 3) * 16384 + swizzle_offset(row * 128 + 16 * (c & 7), 128)) =
-          make_uint4(h2_bits(__floats2half2_rn(x.x, x.y)), h2_bits(__floats2half2_rn(x.z, x.w)),
-                     h2_bits(__floats2half2_rn(y.x, y.y)), h2_bits(__floats2half2_rn(y.z, y.w)));
-    }
+  const int row0 = tid >> 4, c = tid & 15;   // 16 positions x 16 pieces of 8 coordinates
+  for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * kRowsPart; p0 < static_cast<int64_t>(tiles) * kTile;
+       p0 += static_cast<int64_t>(gridDim.x) * kRowsPart) {
+    const int64_t p = p0 + row0, j = p < a.rope_len ? p : a.rope_len - 1;   // behind the sequence's end: masked
+    const int row = static_cast<int>(p & (kTile - 1));
+    const float4* src = reinterpret_cast<const float4*>((c < 8 ? a.rope_cos : a.rope_sin) + j * 64 + 8 * (c & 7));
+    const float4 x = __ldg(src), y = __ldg(src + 1);
+    *reinterpret_cast<uint4*>(a.row_tiles + p / kTile * kRowTile + (c >> 3) * kRowChunk +
+                              swizzle_offset(row * 128 + 16 * (c & 7), 128)) =
+        make_uint4(h2_bits(__floats2half2_rn(x.x, x.y)), h2_bits(__floats2half2_rn(x.z, x.w)),
+                   h2_bits(__floats2half2_rn(y.x, y.y)), h2_bits(__floats2half2_rn(y.z, y.w)));
   }
 }
 
