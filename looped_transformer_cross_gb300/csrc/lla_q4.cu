@@ -510,9 +510,10 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
 
 // Workspace of a decode call: status word; tensor-core kernel: the CTA range of every
 // (sequence, head group), a record per head of every (unit, CTA) of a run (at most
-// units + grid of them), the f16 rotary tiles of L_max positions; fp32 kernel: a record per split.
+// units + grid of them), the query operands of every (sequence, head group), the f16 rotary tiles of
+// L_max positions; fp32 kernel: a record per split.
 struct Q4Ws {
-  size_t ranges, records, row_tiles, total;
+  size_t ranges, records, zimg, row_tiles, total;
   int grid;
 };
 Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
@@ -526,7 +527,8 @@ Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
     const int64_t units = static_cast<int64_t>(B) * p.ngroups;
     w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), units * tiles)));
     w.records = (256 + static_cast<size_t>(units) * 8 + 255) / 256 * 256;
-    w.row_tiles = (w.records + (static_cast<size_t>(units) + w.grid) * p.nh * rec + 255) / 256 * 256;
+    w.zimg = (w.records + (static_cast<size_t>(units) + w.grid) * p.nh * q4_record_floats(p.nh, d->r_v) * 4 + 255) / 256 * 256;
+    w.row_tiles = w.zimg + static_cast<size_t>(units) * 2 * p.z_chunk;
     w.total = w.row_tiles + static_cast<size_t>(tiles) * kTile * 256;
     return w;
   }
@@ -623,6 +625,9 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
     a.ranges = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.ranges);
     a.grid = w.grid;
     a.row_tiles = static_cast<uint8_t*>(workspace) + w.row_tiles;
+    a.zimg = static_cast<uint8_t*>(workspace) + w.zimg;
+    a.rec_stride = q4_record_floats(a.plan.nh, a.r_v);
+    a.z_blocks = a.H * ((a.B + kQ4PrepSeqs - 1) / kQ4PrepSeqs);
     a.rows_grid = static_cast<int>(std::min<int64_t>((L_max + 15) / 16, 8 * sms));
     // sequences per combine block: W_up,v is read once for them, and two blocks per SM run at a time
     a.combine_units = static_cast<int>(std::min<int64_t>(8, (static_cast<int64_t>(a.B) * a.H + 2 * sms - 1) / (2 * sms)));

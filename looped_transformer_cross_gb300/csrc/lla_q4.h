@@ -16,6 +16,7 @@
 namespace lla {
 
 constexpr int kQ4Group = 32;          // columns that share a scale
+constexpr int kQ4PrepSeqs = 4;        // sequences of a block that forms query operands
 
 __host__ __device__ inline int q4_groups(int r) { return (r + kQ4Group - 1) / kQ4Group; }
 __host__ __device__ inline int q4_scale_offset(int r_k, int r_v) { return (r_k + r_v) / 2; }
@@ -30,12 +31,15 @@ struct Q4Plan {
   int N;                             // rows of a head's query operand = columns of G: r_k + 16
   int z, z_chunk;                    // query operands of the group's heads: two chunks of coordinates
   int rows;                          // rotary tiles
-  int qs, state, misc, ring, stage;  // rotated query; softmax state of the epilogue; barriers; head-tiles
+  int state, misc, ring, stage;      // softmax state of the epilogue; barriers; head-tiles
   int w_bytes;                       // V weights of a stage
   int bytes;                         // total dynamic smem incl. alignment slack
 };
 // False where no plan fits (never for ranks up to kMaxRankPerHead).
 bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p);
+// Floats of a record of one head: 8 (m, l), 8 references, 8 / nh sums of r_v (even, so that records are
+// 8-byte aligned).
+inline int q4_record_floats(int nh, int r_v) { return 24 + 8 / nh * r_v; }
 
 struct Q4DecodeArgs {
   int B, H, r_k, r_v, rope_style;
@@ -57,11 +61,13 @@ struct Q4DecodeArgs {
   void* out;                         // [B][H][128] storage dtype
   float* lse;                        // [B][H], or nullptr
   uint32_t* status;
-  float* records;                    // split records: {m (log2 units), l, -, -, acc[r_v]}
+  float* records;                    // split records (fp32 kernel: {m (log2 units), l, -, -, acc[r_v]})
+  int rec_stride;                    // tensor-core kernel: floats of a record
   int64_t chunk;                     // fp32 kernel: tokens of a split
   int splits;                        // fp32 kernel: splits of a (sequence, head)
   uint8_t* row_tiles;                // tensor-core kernel: f16 rotary rows, 32 KB per 128 positions
-  int rows_grid;
+  uint8_t* zimg;                     // query operands of every (sequence, head group)
+  int z_blocks, rows_grid;           // blocks that form the operands, and the rotary tiles
   int32_t* ranges;                   // first and last CTA of each (sequence, head group)
   int grid;
   int combine_units;                 // sequences per combine block (1..8)

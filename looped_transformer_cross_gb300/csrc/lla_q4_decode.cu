@@ -11,12 +11,13 @@
 // 6 cycles per token-head, and what bounds the kernel is instruction issue; the choices
 // below are for few instructions per code.
 //   G  A = the rotary rows, f16, one 32 KB tile per position for all of its heads.  They are
-//      rounded once per call from the fp32 table into tiles in the layout that the MMA reads
-//      (q4_rows_kernel), so that one bulk copy brings a tile: an fp32 table read here would be
-//      more L2 traffic than the latents, and rows turned in registers from tile to tile cost a fifth of all
-//      instructions (measured: 144 us against the present time at 32 x 4096).
-//      (All heads of a group share one chain where their rows fit.)  B = a head's Z rows (f16, resident for the whole run), two bias rows (f16 high
-//      and low part) and one row -8 sum Z per scale group, which takes the codes' offset back.
+//      rounded once per call from the fp32 table into tiles in the layout that the MMA reads, so that a
+//      bulk copy brings a tile: an fp32 table read here would be more L2 traffic than
+//      the latents, and rows turned in registers from tile to tile took a fifth of all
+//      instructions.  B = a head's Z rows (f16), two bias rows (f16 high and low part) and one row
+//      -8 sum Z per scale group, which takes the codes' offset back.  (All heads of a group
+//      share one chain where their rows fit.)  Both operands are formed by q4_prepare_kernel: formed here
+//      at the start of each run they stopped every role for 7 us, a seventh of the call at 32 x 4096.
 //   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
 //      subnormals (code * 2^-24, or * 2^-20 from the next nibble), converted, and summed per
 //      scale group in fp32; the group's scale multiplies the sum.
@@ -27,9 +28,9 @@
 //
 // Work: positions (sequence, head group, 128-token tile) in that order, cut into
 // equal contiguous ranges, one per CTA.  A run is a CTA's part of one (sequence, head
-// group); the query operand of its nh heads is built in shared memory at its start, and
-// one record {m, l, acc} per head is written at its end.  Warps: 0 copies rows (bulk
-// copies of page pieces), 1 issues MMAs, 2 copies rotary tiles, 4-11 epilogue, 12-19 V.
+// group).  Roles meet only at mbarriers, at run ends too: each epilogue and V warp writes its own
+// part of the run's records, which the combine merges.  Warps: 0 copies rows (bulk copies of page
+// pieces), 1 copies query operands and issues MMAs, 2 copies rotary tiles, 4-11 epilogue, 12-19 V.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -41,7 +42,6 @@ namespace lla {
 namespace {
 
 constexpr int kQ4TileThreads = 640;
-constexpr int kWorkers = 512;                    // epilogue and V warpgroups
 constexpr int kQ4MaxNS = 16;
 constexpr int kMaxG = 16;                        // G buffers
 constexpr int kMaxNh = 8;                        // heads of a group
@@ -52,17 +52,16 @@ constexpr int kWStride = 136;                    // halves between the groups of
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
 constexpr int kNoRef = -(1 << 28);
-enum { kBarRun = 1, kBarWork = 2 };              // named barriers: workers + MMA warp; workers
+// a record per (unit, CTA) and head: (m, l) of each epilogue warp, the reference of each V warp, their sums
+constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 24;
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
   uint64_t rfull[kNR], rempty[kNR], gfull[kMaxG], gempty[kMaxG];
-  uint64_t mma_done;
+  uint64_t zfull, zdone;                         // query operands: copied; no longer read
   uint32_t tmem_base;
   int abort;
   int start_b, start_hg, start_t, count;
-  float2 ml[kMaxNh][8];                          // run end: (m, l) of each head and epilogue warp
-  int vref[8];                                   // run end: reference of each V warp
 };
 
 struct Slot {
@@ -207,8 +206,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     const int b0 = min(a.B, tid * per_thr), b1 = min(a.B, b0 + per_thr);
     long long local = 0;
     for (int b = b0; b < b1; ++b) {
-      const int L0 = __ldg(a.seq_lens + b), qp = __ldg(a.q_pos + b);
-      if (blockIdx.x == 0 && (L0 < 0 || L0 > a.L_max || qp < 0 || qp >= a.rope_len)) record_status(a.status, LLA_ERR_DEVICE_ARG);
+      const int L0 = __ldg(a.seq_lens + b);
+      if (blockIdx.x == 0 && (L0 < 0 || L0 > a.L_max)) record_status(a.status, LLA_ERR_DEVICE_ARG);
       local += tiles_of(tile_len(a, b));
     }
     scan[tid] = static_cast<int>(local);
@@ -269,7 +268,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       mbar_init(bar(misc->gfull[i]), 1);
       mbar_init(bar(misc->gempty[i]), 4);
     }
-    mbar_init(bar(misc->mma_done), 1);
+    mbar_init(bar(misc->zfull), 1);
+    mbar_init(bar(misc->zdone), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -284,8 +284,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   RunWalker walk = start;
   Run run{0, 0, 0, 0, 0};
   bool ok = true;
-  // every role keeps its place in the loops when a wait has expired: the named barriers
-  // below count on it
   auto wait = [&](const uint64_t& m, uint32_t parity) {
     if (ok) ok = q4_wait(bar(m), parity, abort, a.status);
   };
@@ -294,118 +292,10 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     if (lane == 0) mbar_arrive(bar(m));
   };
 
-  float* qs = reinterpret_cast<float*>(sm + P.qs);   // rotated query, sc q'_i0 and sc q'_i1: [nh][2][64]
-  // Builds the run's query operands, N rows of 128 rotary coordinates per head, all heads' rows
-  // in two K-major chunks of 64 coordinates (128-byte swizzle); a head's are its r_k Z rows, bias high and low, -8 sum Z of each scale
-  // group, zeros.  All workers; the previous run has ended.
-  auto build = [&](int wtid) {
-    const int nhg = min(nh, a.H - run.hg * nh);
-    int qp = __ldg(a.q_pos + run.b);
-    qp = qp < 0 ? 0 : (qp >= a.rope_len ? static_cast<int>(a.rope_len - 1) : qp);
-    __half2 top = __half2half2(__ushort_as_half(0));   // largest magnitude written (infinite: out of range)
-    auto at = [&](int hi, int row, int coord) {   // address of 8-byte aligned coordinates of a row
-      return sbase + P.z + (coord >> 6) * P.z_chunk + swizzle_offset((hi * N + row) * 128 + 2 * (coord & 63), 128);
-    };
-    named_bar_sync(kBarWork, kWorkers);   // the last run's records are written: its sums lie in the rows' place
-    for (int i = wtid; i < nhg * 64; i += kWorkers) {
-      const int hi = i >> 6, f = i & 63, h = run.hg * nh + hi;
-      const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(run.b) * a.H + h) * kHeadDim;
-      const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + f);
-      const float s = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + f);
-      const float x0 = __bfloat162float(q[i0]), x1 = __bfloat162float(q[i1]);
-      const float q0 = (x0 * c - x1 * s) * kQ4Scale, q1 = (x0 * s + x1 * c) * kQ4Scale;
-      qs[hi * 128 + f] = q0;
-      qs[hi * 128 + 64 + f] = q1;
-      const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1);
-      const float bias[2] = {q0 * m0 + q1 * m1, q1 * m0 - q0 * m1};
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const __half high = __float2half_rn(bias[part]);
-        top = __hmax2(top, __habs2(__half2half2(high)));
-        sts16(at(hi, rk, 64 * part + f), high);
-        sts16(at(hi, rk + 1, 64 * part + f), __float2half_rn(bias[part] - __half2float(high)));
-        for (int row = rk + 2 + gk; row < N; ++row) sts16(at(hi, row, 64 * part + f), __ushort_as_half(0));
-      }
-    }
-    // item = (head, scale group, 4 frequencies, 8 columns); the four of a scale group are neighbouring
-    // lanes (whole warps take part: 64 gk items per head).  A thread's first weights are
-    // requested before the barrier.
-    uint4 w0[4], w1[4];
-    auto fetch = [&](int i) {
-      const int o = i & 3, f0 = (i >> 2 & 15) * 4, hg = i >> 6, hi = hg / gk, g = hg - hi * gk, n = 32 * g + 8 * o;
-      if (i >= nhg * gk * 64 || n >= rk) return;
-      const __nv_bfloat16* W =
-          static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(run.hg * nh + hi) * kHeadDim * rk + n;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int f = f0 + e;
-        const int i0 = a.rope_style == 0 ? f : 2 * f, i1 = a.rope_style == 0 ? f + 64 : 2 * f + 1;
-        w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0) * rk));
-        w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1) * rk));
-      }
-    };
-    fetch(wtid);
-    named_bar_sync(kBarWork, kWorkers);
-    for (int i = wtid; i < nhg * gk * 64; i += kWorkers) {
-      const int o = i & 3, f0 = (i >> 2 & 15) * 4, hg = i >> 6, hi = hg / gk, g = hg - hi * gk, n = 32 * g + 8 * o;
-      float sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
-      if (n < rk) {
-        float q0[4], q1[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q0[e] = qs[hi * 128 + f0 + e];
-          q1[e] = qs[hi * 128 + 64 + f0 + e];
-        }
-        // (rows n + j, n a multiple of 8: j alone makes the swizzle, so an address is one exclusive or)
-        const uint32_t z0 = sbase + P.z + (hi * N + n) * 128 + 2 * f0, z1 = z0 + P.z_chunk;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float zc[4], zs[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t x0 = (&w0[e].x)[j >> 1], x1 = (&w1[e].x)[j >> 1];
-            const float u = __uint_as_float(j & 1 ? x0 & 0xFFFF0000u : x0 << 16);
-            const float v = __uint_as_float(j & 1 ? x1 & 0xFFFF0000u : x1 << 16);
-            zc[e] = fmaf(q0[e], u, q1[e] * v);
-            zs[e] = fmaf(q1[e], u, -q0[e] * v);
-          }
-          // (-8 sum Z takes the codes' offset back: of the unrounded values, whose rounding errors, half
-          // a step of f16 each, add up to no more than the rounding of the sum itself)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sum_c[e] += zc[e];
-            sum_s[e] += zs[e];
-          }
-          const __half2 c0 = __floats2half2_rn(zc[0], zc[1]), c1 = __floats2half2_rn(zc[2], zc[3]);
-          const __half2 s0 = __floats2half2_rn(zs[0], zs[1]), s1 = __floats2half2_rn(zs[2], zs[3]);
-          top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
-          sts64((z0 ^ (j << 4)) + 128 * j, h2_bits(c0), h2_bits(c1));
-          sts64((z1 ^ (j << 4)) + 128 * j, h2_bits(s0), h2_bits(s1));
-        }
-      }
-      // the codes' offset: -8 sum Z over the scale group's columns
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum_c[e] += __shfl_xor_sync(0xffffffffu, sum_c[e], 1);
-        sum_s[e] += __shfl_xor_sync(0xffffffffu, sum_s[e], 1);
-        sum_c[e] = -8.f * (sum_c[e] + __shfl_xor_sync(0xffffffffu, sum_c[e], 2));
-        sum_s[e] = -8.f * (sum_s[e] + __shfl_xor_sync(0xffffffffu, sum_s[e], 2));
-      }
-      if (o == 0) {
-        const __half2 c0 = __floats2half2_rn(sum_c[0], sum_c[1]), c1 = __floats2half2_rn(sum_c[2], sum_c[3]);
-        const __half2 s0 = __floats2half2_rn(sum_s[0], sum_s[1]), s1 = __floats2half2_rn(sum_s[2], sum_s[3]);
-        top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
-        sts64(at(hi, rk + 2 + g, f0), h2_bits(c0), h2_bits(c1));
-        sts64(at(hi, rk + 2 + g, 64 + f0), h2_bits(s0), h2_bits(s1));
-      }
-      fetch(i + kWorkers);
-    }
-    if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) record_status(a.status, LLA_ERR_RANGE);   // (NaN queries stay NaN)
-    fence_proxy_async_smem();
-    named_bar_sync(kBarRun, kWorkers + 32);
+  // record of head hi of the run in this CTA
+  auto record = [&](int hi) {
+    return a.records + ((static_cast<int64_t>(run.b) * ngroups + run.hg + blockIdx.x) * nh + hi) * a.rec_stride;
   };
-
   // Waits (bounded) for the last `count` copies of a ring of n slots to land: none may be in
   // flight when the CTA exits.  (`at`, the next slot, holds the oldest of the last n, or none yet.)
   auto land = [&](uint64_t* full, Slot at, int n, int count) {
@@ -511,10 +401,27 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // step takes about as long for 256 columns as for 128, so the heads of a position share
       // one chain while their rows fit and their buffers are neighbours (r_k = 256: two chains a head).
       const int together = max(1, 256 / N);
+      // A run's query operands come by two bulk copies once the last run's MMAs are done; the epilogue
+      // still has up to NG head-tiles of that run to go.
       Slot rs{0, 0u}, gs{0, 0u};
+      uint32_t runs = 0;
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // the operands are written
       while (walk.next(a, ngroups, run)) {
         const int nhg = min(nh, a.H - run.hg * nh);
-        named_bar_sync(kBarRun, kWorkers + 32);   // operands built
+        if (runs > 0) {
+          if (ok) umma_commit_warp(bar(misc->zdone));
+          wait(misc->zdone, (runs - 1) & 1);
+        }
+        if (ok && lane == 0) {
+          const uint32_t bytes = nhg * N * 128;
+          const uint8_t* src = a.zimg + (static_cast<int64_t>(run.b) * ngroups + run.hg) * 2 * P.z_chunk;
+          mbar_arrive_expect_tx(bar(misc->zfull), 2 * bytes);
+          bulk_load(sbase + P.z, src, bytes, bar(misc->zfull));
+          bulk_load(sbase + P.z + P.z_chunk, src + P.z_chunk, bytes, bar(misc->zfull));
+        }
+        __syncwarp();
+        wait(misc->zfull, runs & 1);
+        if (ok) ++runs;
         for (int t = 0; t < run.n; ++t) {
           // the position's chunks: cosines, sines
           Slot half[2];
@@ -548,16 +455,19 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             }
           }
         }
-        named_bar_sync(kBarRun, kWorkers + 32);   // run ended
       }
-      // this warp's MMAs complete before TMEM is released
-      umma_commit_warp(bar(misc->mma_done));
+      // this warp's copies and MMAs complete before shared memory and TMEM are released
+      if (!ok && lane == 0) {
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar(misc->zfull), runs & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      }
+      umma_commit_warp(bar(misc->zdone));
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bar(misc->mma_done), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+      while (!mbar_try_wait(bar(misc->zdone), (runs + 1) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
     }
   } else if (warp < 12) {
     // ======================================================== epilogue: scores, weights
-    const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane, wtid = tid - 128;
+    const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     Slot st{0, 0u}, gs{0, 0u};
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
@@ -565,7 +475,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * 33;
     while (walk.next(a, ngroups, run)) {
       const int nhg = min(nh, a.H - run.hg * nh);
-      build(wtid);
       for (int hi = 0; hi < nhg; ++hi) {
         state[hi * 33 + lane] = 0.f;
         if (lane == 0) state[hi * 33 + 32] = -INFINITY;
@@ -664,23 +573,20 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // ---- run end: (m, l) of this warp's tokens
       for (int hi = 0; hi < nhg; ++hi) {
         const float l = warp_sum(state[hi * 33 + lane]);
-        if (lane == 0) misc->ml[hi][warp - 4] = make_float2(state[hi * 33 + 32], l);
+        if (lane == 0) *reinterpret_cast<float2*>(record(hi) + kRecMl + 2 * (warp - 4)) = make_float2(state[hi * 33 + 32], l);
       }
-      named_bar_sync(kBarRun, kWorkers + 32);
+      __syncwarp();
     }
   } else {
     regs_inc<112>();
     // ======================================================== V: sum_j p_j c_v,j
-    const int v = warp - 12, gid = lane >> 2, tig = lane & 3, wtid = tid - 128;
+    const int v = warp - 12, gid = lane >> 2, tig = lane & 3;
     // a head has 8 / nh warps, each with 16 nh of a tile's tokens
     const int per = 8 / nh, mine = v / per, ks_first = v % per * nh;
-    // run-end sums, [8][RV32 * 32] in the rows of the warps' own head: read no more by then
-    float* accs = reinterpret_cast<float*>(sm + P.z);
     const uint32_t half_sel = (gid & 1) ? 0x7632u : 0x5410u;
     Slot st{0, 0u};
     while (walk.next(a, ngroups, run)) {
       const int nhg = min(nh, a.H - run.hg * nh);
-      build(wtid);
       float d[NM][4], one[4];
 #pragma unroll
       for (int i = 0; i < NM; ++i)
@@ -745,54 +651,40 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       // ---- run end: the thread whose accumulator columns are a chunk's groups holds its
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
-      float* acc = accs + (mine * N * 32 + v % per * RV32 * 32);
+      if (mine < nhg) {
+        float* rec = record(mine);
+        float* acc = rec + kRecAcc + v % per * rv;
+        if (lane == 0) rec[kRecRef + v % per] = static_cast<float>(ref);
+        auto put = [&](int col, float x) {
+          if (col < rv) acc[col] = x;
+        };
 #pragma unroll
-      for (int c = 0; c < F; ++c) {
-        if (tig != c) continue;
-        const int jj = gid >> 2;
-        const float o8 = 8.f * (jj ? one[1] : one[0]);
+        for (int c = 0; c < F; ++c) {
+          if (tig != c) continue;
+          const int jj = gid >> 2;
+          const float o8 = 8.f * (jj ? one[1] : one[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = 64 * c + 8 * gid + 4 * (i & 1) + (i >> 1);   // low half: even columns, high half: odd
-          acc[col] = (jj ? d[4 * c + i][1] : d[4 * c + i][0]) * 16777216.f - o8;
-          acc[col + 2] = (jj ? d[4 * c + i][3] : d[4 * c + i][2]) * 1048576.f - o8;
+          for (int i = 0; i < 4; ++i) {
+            const int col = 64 * c + 8 * gid + 4 * (i & 1) + (i >> 1);   // low half: even columns, high half: odd
+            put(col, (jj ? d[4 * c + i][1] : d[4 * c + i][0]) * 16777216.f - o8);
+            put(col + 2, (jj ? d[4 * c + i][3] : d[4 * c + i][2]) * 1048576.f - o8);
+          }
         }
-      }
-      if constexpr (HF) {
-        if (tig == F) {
+        if constexpr (HF) {
+          if (tig == F) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int col = 64 * F + 8 * (gid >> 1) + 4 * i + (gid & 1);
-            acc[col] = d[4 * F + i][0] * 16777216.f - 8.f * one[0];
-            acc[col + 2] = d[4 * F + i][2] * 1048576.f - 8.f * one[0];
+            for (int i = 0; i < 2; ++i) {
+              const int col = 64 * F + 8 * (gid >> 1) + 4 * i + (gid & 1);
+              put(col, d[4 * F + i][0] * 16777216.f - 8.f * one[0]);
+              put(col + 2, d[4 * F + i][2] * 1048576.f - 8.f * one[0]);
+            }
           }
         }
       }
-      if (lane == 0) misc->vref[v] = ref;
-      named_bar_sync(kBarRun, kWorkers + 32);
-      // ---- one record per head: {m, l, -, -, acc[r_v]}
-      const int u = run.b * ngroups + run.hg, vt = tid - (kQ4TileThreads - 256);
-      for (int hi = 0; hi < nhg; ++hi) {
-        float M = -INFINITY, ls = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) M = fmaxf(M, misc->ml[hi][i].x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 x = misc->ml[hi][i];
-          ls = fmaf(x.y, M == -INFINITY ? 1.f : exp2f(x.x - M), ls);   // (no maximum: every score was NaN)
-        }
-        float* rec = a.records + ((static_cast<int64_t>(u) + blockIdx.x) * nh + hi) * (rv + kRecordHead);
-        if (vt < rv) {
-          float s = 0.f;
-          for (int i = 0; i < per; ++i)
-            s = fmaf(accs[hi * N * 32 + i * RV32 * 32 + vt], exp2f(static_cast<float>(misc->vref[hi * per + i]) - M), s);
-          rec[kRecordHead + vt] = s;
-        }
-        if (vt == 0) { rec[0] = M; rec[1] = ls; }
-      }
       // which CTAs hold records of this unit
-      if (vt == 0 && run.t0 == 0) a.ranges[2 * u] = blockIdx.x;
-      if (vt == 0 && run.t0 + run.n == tiles_of(run.L)) a.ranges[2 * u + 1] = blockIdx.x;
+      const int u = run.b * ngroups + run.hg;
+      if (v == 0 && lane == 0 && run.t0 == 0) a.ranges[2 * u] = blockIdx.x;
+      if (v == 0 && lane == 0 && run.t0 + run.n == tiles_of(run.L)) a.ranges[2 * u + 1] = blockIdx.x;
     }
   }
 
@@ -805,35 +697,147 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   }
 }
 
-// The f16 rotary rows of every position below the longest length, in tiles of 128 positions
-// as the MMA reads them: chunk 0 the cosines, chunk 1 the sines, 128 bytes a row, 128-byte
-// swizzle.  Reads 512 bytes and writes 256 per position; the decode grid's set-up overlaps it.
-constexpr int kRowsThreads = 256;
+// The operands of the decode grid's MMAs, in the layouts that they are read in.
+// Blocks below a.z_blocks: the query operands of one head and up to kQ4PrepSeqs sequences.  Per (sequence,
+// head group) two K-major chunks (cosine, then sine coordinates) of nh N rows of 128 bytes,
+// 128-byte swizzle; a head's N rows are its r_k rows Z_n, bias high and low, -8 sum Z of each scale
+// group, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
+//     Z_n,f = sc (q'_i0 W_i0,n + q'_i1 W_i1,n),  Z_n,64+f = sc (q'_i1 W_i0,n - q'_i0 W_i1,n),
+// the bias rows the same over mu.  A warp holds the weights of 32 columns and 32 frequencies in
+// registers and serves the block's sequences with them.
+// The other blocks: the f16 rotary rows of every position below the longest length, as
+// tiles of 128 positions (chunk 0 cosines, chunk 1 sines); 512 bytes read and 256 written
+// per position.  The decode grid's set-up overlaps this kernel.
+constexpr int kPrepThreads = 256;
+
 constexpr int kRowsPart = 16;        // positions of a block: short contexts want many blocks
-__global__ void __launch_bounds__(kRowsThreads) q4_rows_kernel(const __grid_constant__ Q4DecodeArgs a) {
+__global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_constant__ Q4DecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ int longest[kRowsThreads / 32];
-  const int tid = threadIdx.x;
-  int L = 0;
-  for (int b = tid; b < a.B; b += kRowsThreads) L = max(L, tile_len(a, b));
-  L = __reduce_max_sync(0xffffffffu, L);
-  if ((tid & 31) == 0) longest[tid >> 5] = L;
-  __syncthreads();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (static_cast<int>(blockIdx.x) >= a.z_blocks) {
+    __shared__ int longest[kPrepThreads / 32];
+    int L = 0;
+    for (int b = tid; b < a.B; b += kPrepThreads) L = max(L, tile_len(a, b));
+    L = __reduce_max_sync(0xffffffffu, L);
+    if (lane == 0) longest[warp] = L;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kRowsThreads / 32; ++i) L = max(L, longest[i]);
-  const int tiles = tiles_of(L);
-  const int row0 = tid >> 4, c = tid & 15;   // 16 positions x 16 pieces of 8 coordinates
-  for (int64_t p0 = static_cast<int64_t>(blockIdx.x) * kRowsPart; p0 < static_cast<int64_t>(tiles) * kTile;
-       p0 += static_cast<int64_t>(gridDim.x) * kRowsPart) {
-    const int64_t p = p0 + row0, j = p < a.rope_len ? p : a.rope_len - 1;   // behind the sequence's end: masked
-    const int row = static_cast<int>(p & (kTile - 1));
-    const float4* src = reinterpret_cast<const float4*>((c < 8 ? a.rope_cos : a.rope_sin) + j * 64 + 8 * (c & 7));
-    const float4 x = __ldg(src), y = __ldg(src + 1);
-    *reinterpret_cast<uint4*>(a.row_tiles + p / kTile * kRowTile + (c >> 3) * kRowChunk +
-                              swizzle_offset(row * 128 + 16 * (c & 7), 128)) =
-        make_uint4(h2_bits(__floats2half2_rn(x.x, x.y)), h2_bits(__floats2half2_rn(x.z, x.w)),
-                   h2_bits(__floats2half2_rn(y.x, y.y)), h2_bits(__floats2half2_rn(y.z, y.w)));
+    for (int i = 0; i < kPrepThreads / 32; ++i) L = max(L, longest[i]);
+    const int64_t end = static_cast<int64_t>(tiles_of(L)) * kTile;
+    const int row0 = tid >> 4, c = tid & 15;   // 16 positions x 16 pieces of 8 coordinates
+    const int64_t step = static_cast<int64_t>(gridDim.x - a.z_blocks) * kRowsPart;
+    for (int64_t p = static_cast<int64_t>(blockIdx.x - a.z_blocks) * kRowsPart + row0; p < end; p += step) {
+      const int64_t j = p < a.rope_len ? p : a.rope_len - 1;   // behind the sequence's end: masked
+      const int row = static_cast<int>(p & (kTile - 1));
+      const float4* src = reinterpret_cast<const float4*>((c < 8 ? a.rope_cos : a.rope_sin) + j * 64 + 8 * (c & 7));
+      const float4 x = __ldg(src), y = __ldg(src + 1);
+      *reinterpret_cast<uint4*>(a.row_tiles + p / kTile * kRowTile + (c >> 3) * kRowChunk +
+                                swizzle_offset(row * 128 + 16 * (c & 7), 128)) =
+          make_uint4(h2_bits(__floats2half2_rn(x.x, x.y)), h2_bits(__floats2half2_rn(x.z, x.w)),
+                     h2_bits(__floats2half2_rn(y.x, y.y)), h2_bits(__floats2half2_rn(y.z, y.w)));
+    }
+    return;
   }
+  __shared__ float qs[kQ4PrepSeqs][2][64];   // sc q'_i0 and sc q'_i1
+  const int h = blockIdx.x % a.H, b0 = blockIdx.x / a.H * kQ4PrepSeqs, seqs = min(kQ4PrepSeqs, a.B - b0);
+  const Q4Plan& P = a.plan;
+  const int N = P.N, rk = a.r_k, gk = q4_groups(rk), nh = P.nh, hi = h % nh;
+  auto i0_of = [&](int f) { return a.rope_style == 0 ? f : 2 * f; };
+  auto i1_of = [&](int f) { return a.rope_style == 0 ? f + 64 : 2 * f + 1; };
+  // rows of (sequence s of the block, this head): 8-byte aligned coordinates of a row
+  auto at = [&](int s, int row, int coord) {
+    return a.zimg + (static_cast<int64_t>(b0 + s) * P.ngroups + h / nh) * 2 * P.z_chunk + (coord >> 6) * P.z_chunk +
+           swizzle_offset((hi * N + row) * 128 + 2 * (coord & 63), 128);
+  };
+  __half2 top = __half2half2(__ushort_as_half(0));   // largest magnitude written (infinite: out of range)
+  for (int i = tid; i < seqs * 64; i += kPrepThreads) {
+    const int s = i >> 6, f = i & 63, b = b0 + s;
+    int qp = __ldg(a.q_pos + b);
+    if (qp < 0 || qp >= a.rope_len) {
+      if (f == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
+      qp = qp < 0 ? 0 : static_cast<int>(a.rope_len - 1);
+    }
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h) * kHeadDim;
+    const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + f);
+    const float sn = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + f);
+    const float x0 = __bfloat162float(q[i0_of(f)]), x1 = __bfloat162float(q[i1_of(f)]);
+    const float q0 = (x0 * c - x1 * sn) * kQ4Scale, q1 = (x0 * sn + x1 * c) * kQ4Scale;
+    qs[s][0][f] = q0;
+    qs[s][1][f] = q1;
+    const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0_of(f)), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1_of(f));
+    const float bias[2] = {q0 * m0 + q1 * m1, q1 * m0 - q0 * m1};
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const __half high = __float2half_rn(bias[part]);
+      top = __hmax2(top, __habs2(__half2half2(high)));
+      *reinterpret_cast<__half*>(at(s, rk, 64 * part + f)) = high;
+      *reinterpret_cast<__half*>(at(s, rk + 1, 64 * part + f)) = __float2half_rn(bias[part] - __half2float(high));
+      for (int row = rk + 2 + gk; row < N; ++row) *reinterpret_cast<__half*>(at(s, row, 64 * part + f)) = __ushort_as_half(0);
+    }
+  }
+  __syncthreads();
+  // item of a warp = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies)
+  for (int it = warp; it < 2 * gk; it += kPrepThreads / 32) {
+    const int g = it >> 1, n = 32 * g + 8 * (lane >> 3), f0 = 32 * (it & 1) + 4 * (lane & 7);
+    const bool live = n < rk;
+    uint4 w0[4], w1[4];
+    const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w0[e] = w1[e] = make_uint4(0, 0, 0, 0);
+      if (live) w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0_of(f0 + e)) * rk));
+      if (live) w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1_of(f0 + e)) * rk));
+    }
+    for (int s = 0; s < seqs; ++s) {
+      float q0[4], q1[4], sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
+      uint8_t* z0 = at(s, n, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        q0[e] = qs[s][0][f0 + e];
+        q1[e] = qs[s][1][f0 + e];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float zc[4], zs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x0 = (&w0[e].x)[j >> 1], x1 = (&w1[e].x)[j >> 1];
+          const float u = __uint_as_float(j & 1 ? x0 & 0xFFFF0000u : x0 << 16);
+          const float v = __uint_as_float(j & 1 ? x1 & 0xFFFF0000u : x1 << 16);
+          zc[e] = fmaf(q0[e], u, q1[e] * v);
+          zs[e] = fmaf(q1[e], u, -q0[e] * v);
+        }
+        const __half2 c0 = __floats2half2_rn(zc[0], zc[1]), c1 = __floats2half2_rn(zc[2], zc[3]);
+        const __half2 s0 = __floats2half2_rn(zs[0], zs[1]), s1 = __floats2half2_rn(zs[2], zs[3]);
+        top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
+        // (the sums of what the MMA reads: of the rounded values)
+        const float2 cf0 = __half22float2(c0), cf1 = __half22float2(c1), sf0 = __half22float2(s0), sf1 = __half22float2(s1);
+        sum_c[0] += cf0.x; sum_c[1] += cf0.y; sum_c[2] += cf1.x; sum_c[3] += cf1.y;
+        sum_s[0] += sf0.x; sum_s[1] += sf0.y; sum_s[2] += sf1.x; sum_s[3] += sf1.y;
+        if (live) {   // (row n + j, n a multiple of 8: j alone makes the swizzle)
+          uint8_t* z = z0 + ((2 * f0) ^ (j << 4)) + 128 * j;
+          *reinterpret_cast<uint2*>(z) = make_uint2(h2_bits(c0), h2_bits(c1));
+          *reinterpret_cast<uint2*>(z + P.z_chunk) = make_uint2(h2_bits(s0), h2_bits(s1));
+        }
+      }
+      // the codes' offset: -8 sum Z over the scale group's columns
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum_c[e] += __shfl_xor_sync(0xffffffffu, sum_c[e], 8);
+        sum_s[e] += __shfl_xor_sync(0xffffffffu, sum_s[e], 8);
+        sum_c[e] = -8.f * (sum_c[e] + __shfl_xor_sync(0xffffffffu, sum_c[e], 16));
+        sum_s[e] = -8.f * (sum_s[e] + __shfl_xor_sync(0xffffffffu, sum_s[e], 16));
+      }
+      if (lane < 8) {
+        const __half2 c0 = __floats2half2_rn(sum_c[0], sum_c[1]), c1 = __floats2half2_rn(sum_c[2], sum_c[3]);
+        const __half2 s0 = __floats2half2_rn(sum_s[0], sum_s[1]), s1 = __floats2half2_rn(sum_s[2], sum_s[3]);
+        top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
+        *reinterpret_cast<uint2*>(at(s, rk + 2 + g, f0)) = make_uint2(h2_bits(c0), h2_bits(c1));
+        *reinterpret_cast<uint2*>(at(s, rk + 2 + g, 64 + f0)) = make_uint2(h2_bits(s0), h2_bits(s1));
+      }
+    }
+  }
+  if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) record_status(a.status, LLA_ERR_RANGE);   // (NaN queries stay NaN)
 }
 
 // Merge the records of each (sequence, head) by log-sum-exp, apply W_up,v once (Appendix J
@@ -863,20 +867,26 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __gri
     for (int k = 0; k < RV32; ++k) v[k] = 0.f;
     if (tile_len(a, b) > 0) {
       const int2 c = *reinterpret_cast<const int2*>(a.ranges + 2 * u);
-      const int64_t stride = static_cast<int64_t>(nh) * (rv + kRecordHead);
-      const float* rec = a.records + (static_cast<int64_t>(u) + c.x) * stride + (h % nh) * (rv + kRecordHead);
-      const int n = c.y - c.x + 1;
-      for (int j = lane; j < n; j += 32) m = fmaxf(m, rec[j * stride]);
+      const int64_t stride = static_cast<int64_t>(nh) * a.rec_stride;
+      const float* rec = a.records + (static_cast<int64_t>(u) + c.x) * stride + (h % nh) * a.rec_stride;
+      const int n = c.y - c.x + 1, per = 8 / nh;
+      // references and sums: 8 epilogue warps per record, four records a step
+      for (int j = lane >> 3; j < n; j += 4) m = fmaxf(m, rec[j * stride + kRecMl + 2 * (lane & 7)]);
       m = warp_max(m);
       l = 0.f;
-      for (int j = 0; j < n; ++j) {
-        const float* r = rec + j * stride;
-        const float f = m == -INFINITY ? 1.f : exp2f(r[0] - m);   // no maximum: every score was NaN, and so is l
-        l = fmaf(r[1], f, l);
-#pragma unroll
-        for (int k = 0; k < RV32; ++k)
-          if (32 * k + lane < rv) v[k] = fmaf(r[kRecordHead + 32 * k + lane], f, v[k]);
+      for (int j = lane >> 3; j < n; j += 4) {
+        const float2 x = *reinterpret_cast<const float2*>(rec + j * stride + kRecMl + 2 * (lane & 7));
+        l = fmaf(x.y, m == -INFINITY ? 1.f : exp2f(x.x - m), l);   // (no maximum: every score was NaN)
       }
+      l = warp_sum(l);
+      for (int j = 0; j < n; ++j)
+        for (int p = 0; p < per; ++p) {
+          const float* r = rec + j * stride;
+          const float f = exp2f(r[kRecRef + p] - m);
+#pragma unroll
+          for (int k = 0; k < RV32; ++k)
+            if (32 * k + lane < rv) v[k] = fmaf(r[kRecAcc + p * rv + 32 * k + lane], f, v[k]);
+        }
     }
 #pragma unroll
     for (int k = 0; k < RV32; ++k) acc[i][32 * k + lane] = v[k];
@@ -909,7 +919,7 @@ template <int RV32>
 cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
   cudaError_t e = allow_smem(q4_tile_kernel<RV32>, a.plan.bytes);
   if (e != cudaSuccess) return e;
-  q4_rows_kernel<<<a.rows_grid, kRowsThreads, 0, s>>>(a);
+  q4_prepare_kernel<<<a.z_blocks + a.rows_grid, kPrepThreads, 0, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   // programmatic dependents: each grid's set-up overlaps the one before
   if ((e = launch_pdl(q4_tile_kernel<RV32>, dim3(a.grid), dim3(kQ4TileThreads), a.plan.bytes, s, a)) != cudaSuccess) return e;
@@ -940,7 +950,6 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     int off = 0;
     p->z = off; off += 2 * p->z_chunk;
     p->rows = off = al(off, 1024); off += kNR * kRowChunk;
-    p->qs = off; off += nh * 512;
     p->state = off; off = al(off + 8 * nh * 33 * 4, 16);
     p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 16);
     p->ring = off;
