@@ -64,6 +64,11 @@ struct alignas(16) Q4Misc {
   int start_b, start_hg, start_t, count;
 };
 
+// Position of a ring with its barriers' phase.  A wait tells a phase from the one before it only, so no
+// warp may leave out phases of a barrier that it waits on.  Every ring that several groups take
+// turns at therefore has a multiple of their number of barriers, which gives each barrier one
+// waiting group: the head-tiles of the two epilogue groups (NS and NB even), the heads of the V warps
+// (NS a multiple of nh, and so is H).
 struct Slot {
   int i;
   uint32_t phase;
@@ -128,9 +133,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
   return v;
 }
 __device__ __forceinline__ void sts32(uint32_t p, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
-__device__ __forceinline__ void sts64(uint32_t p, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(p), "r"(x), "r"(y) : "memory");
-}
 __device__ __forceinline__ void sts16(uint32_t p, __half v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(p), "h"(__half_as_ushort(v)) : "memory");
 }
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   Q4Misc* misc = reinterpret_cast<Q4Misc*>(sm + P.misc);
   volatile int* abort = &misc->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, NG = P.NG, N = P.N, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
+  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, NG = P.NG, NB = P.NB, N = P.N, gstep = P.gstep, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
   const int scale_at = q4_scale_offset(rk, rv), gk = q4_groups(rk);
 
   // ---------------------------------------------------------- work range
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       mbar_init(bar(misc->rfull[i]), 1);
       mbar_init(bar(misc->rempty[i]), 1);
     }
-    for (int i = 0; i < NG; ++i) {
+    for (int i = 0; i < NB; ++i) {
       mbar_init(bar(misc->gfull[i]), 1);
       mbar_init(bar(misc->gempty[i]), 4);
     }
@@ -356,10 +358,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       while (more && ok) {
         x = y;
         more = next(y);
-        const int nhg = min(nh, a.H - x.hg * nh);
         Piece mine{};
         if (lane < x.np) mine = piece(x, lane, x.page);
-        for (int hi = 0; hi < nhg && ok; ++hi) {
+        for (int hi = 0; hi < nh && ok; ++hi) {
           wait(misc->empty[st.i], st.phase ^ 1u);
           if (!ok) break;
           const uint32_t fb = bar(misc->full[st.i]), dst = sbase + P.ring + st.i * P.stage;
@@ -407,13 +408,12 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       uint32_t runs = 0;
       asm volatile("griddepcontrol.wait;" ::: "memory");   // the operands are written
       while (walk.next(a, ngroups, run)) {
-        const int nhg = min(nh, a.H - run.hg * nh);
         if (runs > 0) {
           if (ok) umma_commit_warp(bar(misc->zdone));
           wait(misc->zdone, (runs - 1) & 1);
         }
         if (ok && lane == 0) {
-          const uint32_t bytes = nhg * N * 128;
+          const uint32_t bytes = nh * N * 128;
           const uint8_t* src = a.zimg + (static_cast<int64_t>(run.b) * ngroups + run.hg) * 2 * P.z_chunk;
           mbar_arrive_expect_tx(bar(misc->zfull), 2 * bytes);
           bulk_load(sbase + P.z, src, bytes, bar(misc->zfull));
@@ -430,11 +430,14 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             half[c] = rs;
             rs.next(kNR);
           }
-          for (int hi = 0, heads; hi < nhg; hi += heads) {
-            heads = min(together, min(nhg - hi, NG - gs.i));
-            for (int i = 0; i < heads; ++i) wait(misc->gempty[gs.i + i], gs.phase ^ 1u);
+          for (int hi = 0, heads; hi < nh; hi += heads) {
+            heads = min(together, min(nh - hi, NB - gs.i));
+            if (NG > 1)
+              for (int i = 0; i < heads; ++i) wait(misc->gempty[gs.i + i], gs.phase ^ 1u);
+            else
+              wait(misc->gempty[gs.i ^ 1], gs.phase ^ static_cast<uint32_t>(gs.i ^ 1));   // the tile before
             tc_fence_after();
-            const bool last = hi + heads == nhg;
+            const bool last = hi + heads == nh;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               if (hi == 0) wait(misc->rfull[half[c].i], half[c].phase);
@@ -445,13 +448,13 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
                 const uint64_t bd = umma_desc(sbase + P.z + c * P.z_chunk + (hi * N + r0) * 128, 16, 1024, kSw128);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_warp(tmem + gs.i * N + r0, ad + 2 * kk, bd + 2 * kk, idesc, c + kk > 0 ? 1u : 0u);
+                  umma_bf16_warp(tmem + gs.i * gstep + r0, ad + 2 * kk, bd + 2 * kk, idesc, c + kk > 0 ? 1u : 0u);
               }
               if (last) umma_commit_warp(bar(misc->rempty[half[c].i]));
             }
             for (int i = 0; i < heads; ++i) {
               if (ok) umma_commit_warp(bar(misc->gfull[gs.i]));
-              gs.next(NG);
+              gs.next(NB);
             }
           }
         }
@@ -474,8 +477,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     // per head the warp's reference and each thread's own sum
     float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * 33;
     while (walk.next(a, ngroups, run)) {
-      const int nhg = min(nh, a.H - run.hg * nh);
-      for (int hi = 0; hi < nhg; ++hi) {
+      for (int hi = 0; hi < nh; ++hi) {
         state[hi * 33 + lane] = 0.f;
         if (lane == 0) state[hi * 33 + 32] = -INFINITY;
       }
@@ -484,13 +486,13 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       for (int t = 0; t < run.n; ++t) {
         const bool valid = row < run.L - (run.t0 + t) * kTile;
 #pragma unroll 1
-        for (int hi = 0; hi < nhg; ++hi, ++n, st.next(NS), gs.next(NG)) {
+        for (int hi = 0; hi < nh; ++hi, ++n, st.next(NS), gs.next(NB)) {
           if (grp != static_cast<int>(n & 1)) continue;
           const uint32_t base = sbase + P.ring + st.i * P.stage, tail = base + kTile * rb, r = base + row * rb;
           wait(misc->full[st.i], st.phase);
           wait(misc->gfull[gs.i], gs.phase);
           tc_fence_after();
-          const uint32_t gcol = tmem + lane_base + gs.i * N;
+          const uint32_t gcol = tmem + lane_base + gs.i * gstep;
           float bias[2], s = 0.f;
           tmem_ld_x2(gcol + rk, bias);
           // ---- V scales; 2^E is above every one of the warp's tokens
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       }
       // ---- run end: (m, l) of this warp's tokens
-      for (int hi = 0; hi < nhg; ++hi) {
+      for (int hi = 0; hi < nh; ++hi) {
         const float l = warp_sum(state[hi * 33 + lane]);
         if (lane == 0) *reinterpret_cast<float2*>(record(hi) + kRecMl + 2 * (warp - 4)) = make_float2(state[hi * 33 + 32], l);
       }
@@ -586,7 +588,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     const uint32_t half_sel = (gid & 1) ? 0x7632u : 0x5410u;
     Slot st{0, 0u};
     while (walk.next(a, ngroups, run)) {
-      const int nhg = min(nh, a.H - run.hg * nh);
       float d[NM][4], one[4];
 #pragma unroll
       for (int i = 0; i < NM; ++i)
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       for (int j = 0; j < 4; ++j) one[j] = 0.f;
       int ref = kNoRef;
       for (int t = 0; t < run.n; ++t)
-        for (int hi = 0; hi < nhg; ++hi, st.next(NS)) {
+        for (int hi = 0; hi < nh; ++hi, st.next(NS)) {
           if (hi != mine) continue;
           wait(misc->wfull[st.i], st.phase);
           const uint32_t rows = sbase + P.ring + st.i * P.stage, tail = rows + kTile * rb;
@@ -651,33 +652,31 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         }
       // ---- run end: the thread whose accumulator columns are a chunk's groups holds its
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
-      if (mine < nhg) {
-        float* rec = record(mine);
-        float* acc = rec + kRecAcc + v % per * rv;
-        if (lane == 0) rec[kRecRef + v % per] = static_cast<float>(ref);
-        auto put = [&](int col, float x) {
-          if (col < rv) acc[col] = x;
-        };
+      float* rec = record(mine);
+      float* acc = rec + kRecAcc + v % per * rv;
+      if (lane == 0) rec[kRecRef + v % per] = static_cast<float>(ref);
+      auto put = [&](int col, float x) {
+        if (col < rv) acc[col] = x;
+      };
 #pragma unroll
-        for (int c = 0; c < F; ++c) {
-          if (tig != c) continue;
-          const int jj = gid >> 2;
-          const float o8 = 8.f * (jj ? one[1] : one[0]);
+      for (int c = 0; c < F; ++c) {
+        if (tig != c) continue;
+        const int jj = gid >> 2;
+        const float o8 = 8.f * (jj ? one[1] : one[0]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int col = 64 * c + 8 * gid + 4 * (i & 1) + (i >> 1);   // low half: even columns, high half: odd
-            put(col, (jj ? d[4 * c + i][1] : d[4 * c + i][0]) * 16777216.f - o8);
-            put(col + 2, (jj ? d[4 * c + i][3] : d[4 * c + i][2]) * 1048576.f - o8);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const int col = 64 * c + 8 * gid + 4 * (i & 1) + (i >> 1);   // low half: even columns, high half: odd
+          put(col, (jj ? d[4 * c + i][1] : d[4 * c + i][0]) * 16777216.f - o8);
+          put(col + 2, (jj ? d[4 * c + i][3] : d[4 * c + i][2]) * 1048576.f - o8);
         }
-        if constexpr (HF) {
-          if (tig == F) {
+      }
+      if constexpr (HF) {
+        if (tig == F) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int col = 64 * F + 8 * (gid >> 1) + 4 * i + (gid & 1);
-              put(col, d[4 * F + i][0] * 16777216.f - 8.f * one[0]);
-              put(col + 2, d[4 * F + i][2] * 1048576.f - 8.f * one[0]);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int col = 64 * F + 8 * (gid >> 1) + 4 * i + (gid & 1);
+            put(col, d[4 * F + i][0] * 16777216.f - 8.f * one[0]);
+            put(col + 2, d[4 * F + i][2] * 1048576.f - 8.f * one[0]);
           }
         }
       }
@@ -933,17 +932,19 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
   const int rb = q4_row_bytes(r_k, r_v), rv32 = (r_v + 31) / 32;
   auto al = [](int x, int a) { return (x + a - 1) / a * a; };
   // Heads of a group: they share a position's rotary tile and, up to 256 operand rows, its MMA
-  // chain, which takes as long for one head as for all.  Eight or four only where they divide
-  // the heads (positions are dealt out as if all groups were alike) and their rows fit a
-  // chain; a head-tile stays in the ring while scores and V take their turns, so groups of several
+  // chain, which takes as long for one head as for all.  Only as many as divide the heads, eight or
+  // four only where their rows fit a chain; a head-tile stays in the ring while scores and V take their turns, so groups of several
   // heads need room for copies ahead.
   for (int nh = kMaxNh; nh >= 1; nh /= 2) {
-    if (nh > H || (nh > 2 && (H % nh || nh * (r_k + 16) > 256))) continue;
+    if (H % nh || (nh > 2 && nh * (r_k + 16) > 256)) continue;
     *p = Q4Plan{};
     p->nh = nh;
-    p->ngroups = (H + nh - 1) / nh;
+    p->ngroups = H / nh;
     p->N = r_k + 16;
     p->NG = std::min(kMaxG, 512 / p->N);
+    if (p->NG > 1) p->NG -= p->NG % 2;
+    p->NB = std::max(2, p->NG);
+    p->gstep = p->NG > 1 ? p->N : 0;
     p->z_chunk = nh * p->N * 128;
     p->w_bytes = rv32 * kWStride * 2;
     p->stage = kTile * rb + p->w_bytes + 16;
@@ -954,6 +955,7 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 16);
     p->ring = off;
     p->NS = std::min((kSmemLimit - 1024 - off) / p->stage, kQ4MaxNS);
+    p->NS -= p->NS % std::max(2, nh);
     p->bytes = off + p->NS * p->stage + 1024;
     if (p->NS >= (nh == 1 ? 2 : std::max(4, nh))) return true;
   }

@@ -228,6 +228,20 @@ def test_decode_many_short_sequences(dtype):
     _check(_inputs(list(g.integers(0, 150, 300)), 4, 32, 48, 16, dtype, 11), 1, bsel=range(0, 300, 17))
 
 
+@pytest.mark.parametrize("rk,rv,H,lens", [(240, 240, 1, [60000, 0, 40001]), (256, 256, 3, [20000, 13333]), (96, 160, 5, [1, 20001]),
+                                          (96, 160, 4, [50001]), (176, 64, 2, [99999]), (48, 80, 4, [100001]),
+                                          (16, 32, 8, [60000, 40001])])
+def test_decode_long_runs(rk, rv, H, lens):
+    """Blocks with several positions of a sequence, at every number of heads that share one: each
+    buffer and barrier is used again, by either of the groups that take turns."""
+    x = _inputs(lens, H, rk, rv, 128, "bf16", 500 + rk + H, T=1)
+    first, _, _ = _gpu(x, 0)
+    _check(x, 0)
+    for _ in range(3):                                         # and always with the same bits
+        again, _, _ = _gpu(x, 0)
+        assert torch.equal(first, again)
+
+
 def test_decode_full_size_sampled():
     """The serving shape (32 x 4096 tokens, 16 heads, 96 / 160) on sampled sequences."""
     g = np.random.default_rng(2)
