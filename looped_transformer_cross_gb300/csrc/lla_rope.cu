@@ -108,17 +108,19 @@ bool turns_of(const lla_dims* dims, const lla_rope_scaling* sc, TurnArgs* a) {
 
 // ----------------------------------------------------------------- rotation
 
-constexpr int kApplyThreads = 256;
+constexpr int kApplyThreads = 128;
+constexpr int kApplyHeads = 4;                // heads of a thread whose loads are in flight together
 
 struct ApplyArgs {
   const void* x;
   void* out;
   int64_t x_tok, x_head, out_tok, out_head;   // strides in elements
   int offset, half;
-  int rot_items;                              // per token-head: rotated items, then copied ones
-  FastDiv items, per_head;                    // items of a token-head; heads
-  int64_t tok0;                               // first token of this launch
-  uint32_t n_items;                           // items of this launch
+  int rot_items, n_items;                     // per token-head: rotated items, then copied ones; all
+  int first;                                  // column of the first item (interleaved vectors)
+  FastDiv items, strips;                      // a block's items of a token-head; threads that share a token's heads
+  int heads, toks;                            // heads; tokens of a block
+  int64_t N;
   const int32_t* pos;
   const float* rope_cos;                      // [rope_len][half]
   const float* rope_sin;
@@ -128,7 +130,7 @@ struct ApplyArgs {
 };
 
 template <typename T, int N>
-struct alignas(N * sizeof(T)) Vec {
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Vec {
   T v[N];
 };
 
@@ -145,72 +147,101 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// x is read once: evicted first, so that L2 keeps what was written (82 -> 77 us of the
+// gradient of 32768 x 16 vectors of 192).
+template <typename V>
+__device__ __forceinline__ V load_once(const void* p) {
+  if constexpr (sizeof(V) == 16) {
+    const uint4 x = __ldcs(static_cast<const uint4*>(p));
+    return *reinterpret_cast<const V*>(&x);
+  } else {
+    return *static_cast<const V*>(p);
+  }
+}
+
 // One item = VEC rotation pairs of a token-head (two 16-byte loads and stores where
 // VEC * sizeof(T) == 16), or VEC elements outside the rotated part, copied when the call
-// is not in place.  HBM-bound: each element is read and written once, and a token's
-// cos / sin row comes from L1 or L2 for all of its heads but the first.  fp32
-// arithmetic, one rounding to the storage type.
+// is not in place.  Interleaved pairs lie within 16 bytes: there an item is one such vector, rotated or
+// copied, in the order of the columns.  A thread keeps its item and token, and with them its
+// position, cosines and sines, for up to kApplyHeads heads at a time, whose loads are all
+// under way before the first is used.  (One item a thread, with its divisions and
+// addresses, took 177 instructions per warp and was bound by issuing them.)  HBM-bound:
+// each element is read and written once.  fp32 arithmetic, one rounding to the storage type.
 template <typename T, int VEC, int kStyle>
 __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const __grid_constant__ ApplyArgs a) {
-  const uint32_t i = blockIdx.x * kApplyThreads + threadIdx.x;
-  if (i >= a.n_items) return;
-  const uint32_t row = a.items.div(i), item = i - row * a.items.d;
-  const uint32_t t = a.per_head.div(row), h = row - t * a.per_head.d;
-  const int64_t n = a.tok0 + t;
-  const T* x = static_cast<const T*>(a.x) + n * a.x_tok + h * a.x_head;
-  T* out = static_cast<T*>(a.out) + n * a.out_tok + h * a.out_head;
+  constexpr bool kWhole = kStyle == 1 && VEC > 1;          // an item's pairs are one vector's
+  constexpr int kPairs = kWhole ? VEC / 2 : VEC;
   using V = Vec<T, VEC>;
-  if (static_cast<int>(item) >= a.rot_items) {
-    int c = (static_cast<int>(item) - a.rot_items) * VEC;
-    if (c >= a.offset) c += 2 * a.half;
-    *reinterpret_cast<V*>(out + c) = *reinterpret_cast<const V*>(x + c);
-    return;
-  }
-  int p = __ldg(a.pos + n);
-  if (p < 0 || p >= a.rope_len) {
-    record_status(a.status, LLA_ERR_DEVICE_ARG);
-    p = p < 0 ? 0 : static_cast<int>(a.rope_len - 1);
-  }
-  const int f = static_cast<int>(item) * VEC;
-  const float* cr = a.rope_cos + static_cast<int64_t>(p) * a.half + f;
-  const float* sr = a.rope_sin + static_cast<int64_t>(p) * a.half + f;
-  float c[VEC], s[VEC];
-  if constexpr (VEC % 4 == 0) {
-#pragma unroll
-    for (int e = 0; e < VEC; e += 4) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cr + e));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(sr + e));
-      c[e] = c4.x; c[e + 1] = c4.y; c[e + 2] = c4.z; c[e + 3] = c4.w;
-      s[e] = s4.x; s[e + 1] = s4.y; s[e + 2] = s4.z; s[e + 3] = s4.w;
-    }
+  using F = Vec<float, kPairs>;
+  const uint32_t slot = a.items.div(threadIdx.x), ts = a.strips.div(slot);
+  const int item = static_cast<int>(blockIdx.y * a.items.d + threadIdx.x - slot * a.items.d);
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * a.toks + ts;
+  if (static_cast<int>(ts) >= a.toks || n >= a.N || item >= a.n_items) return;
+  // the item's columns: i0, and of a split pair i1
+  int i0, i1 = 0, f = -1;
+  if constexpr (kWhole) {
+    i0 = a.first + item * VEC;
+    if (i0 >= a.offset && i0 < a.offset + 2 * a.half) f = (i0 - a.offset) / 2;
+  } else if (item < a.rot_items) {
+    f = item * VEC;
+    i0 = a.offset + (kStyle == 0 ? f : 2 * f);
+    i1 = kStyle == 0 ? i0 + a.half : i0 + 1;
   } else {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) { c[e] = __ldg(cr + e); s[e] = __ldg(sr + e); }
+    i0 = (item - a.rot_items) * VEC;
+    if (i0 >= a.offset) i0 += 2 * a.half;
   }
-  // the pair (i0, i1) of frequency f: (f, f + half) or (2f, 2f + 1)
-  const int i0 = a.offset + (kStyle == 0 ? f : 2 * f), i1 = kStyle == 0 ? i0 + a.half : i0 + VEC;
-  const V u = *reinterpret_cast<const V*>(x + i0), w = *reinterpret_cast<const V*>(x + i1);
-  V yu, yw;
-  T* yp[2] = {yu.v, yw.v};
-  const T* xp[2] = {u.v, w.v};
+  F c, s;
+  if (f >= 0) {
+    int p = __ldg(a.pos + n);
+    if (p < 0 || p >= a.rope_len) {
+      record_status(a.status, LLA_ERR_DEVICE_ARG);
+      p = p < 0 ? 0 : static_cast<int>(a.rope_len - 1);
+    }
+    c = *reinterpret_cast<const F*>(a.rope_cos + static_cast<int64_t>(p) * a.half + f);
+    s = *reinterpret_cast<const F*>(a.rope_sin + static_cast<int64_t>(p) * a.half + f);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    // members of pair e: half layout u[e], w[e]; interleaved layout elements 2e, 2e + 1 of (u, w)
-    const int k0 = kStyle == 0 ? e : 2 * e, k1 = kStyle == 0 ? e + VEC : 2 * e + 1;
-    const float x0 = to_f32<T>(xp[k0 / VEC][k0 % VEC]), x1 = to_f32<T>(xp[k1 / VEC][k1 % VEC]);
-    const float sn = s[e] * a.sign;
-    yp[k0 / VEC][k0 % VEC] = from_f32<T>((x0 * c[e] - x1 * sn) * a.scale);
-    yp[k1 / VEC][k1 % VEC] = from_f32<T>((x0 * sn + x1 * c[e]) * a.scale);
+    for (int e = 0; e < kPairs; ++e) s.v[e] *= a.sign;
   }
-  *reinterpret_cast<V*>(out + i0) = yu;
-  *reinterpret_cast<V*>(out + i1) = yw;
+  int h = static_cast<int>(slot - ts * a.strips.d);
+  const T* x = static_cast<const T*>(a.x) + n * a.x_tok + h * a.x_head + i0;
+  T* out = static_cast<T*>(a.out) + n * a.out_tok + h * a.out_head + i0;
+  const int strips = static_cast<int>(a.strips.d);
+  const int64_t x_step = strips * a.x_head, out_step = strips * a.out_head;
+  for (; h < a.heads; h += kApplyHeads * strips) {
+    V u[kApplyHeads], w[kApplyHeads];
+#pragma unroll
+    for (int k = 0; k < kApplyHeads; ++k) {
+      if (h + k * strips >= a.heads) continue;
+      u[k] = load_once<V>(x + k * x_step);
+      if (!kWhole && f >= 0) w[k] = load_once<V>(x + k * x_step + (i1 - i0));
+    }
+#pragma unroll
+    for (int k = 0; k < kApplyHeads; ++k) {
+      if (h + k * strips >= a.heads) continue;
+      if (f >= 0) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          T& y0 = u[k].v[kWhole ? 2 * e : e];
+          T& y1 = kWhole ? u[k].v[2 * e + 1] : w[k].v[e];
+          const float x0 = to_f32<T>(y0), x1 = to_f32<T>(y1);
+          y0 = from_f32<T>((x0 * c.v[e] - x1 * s.v[e]) * a.scale);
+          y1 = from_f32<T>((x0 * s.v[e] + x1 * c.v[e]) * a.scale);
+        }
+        if (!kWhole) *reinterpret_cast<V*>(out + k * out_step + (i1 - i0)) = w[k];
+      }
+      *reinterpret_cast<V*>(out + k * out_step) = u[k];
+    }
+    x += kApplyHeads * x_step;
+    out += kApplyHeads * out_step;
+  }
 }
 
 template <typename T, int VEC>
 cudaError_t launch_apply(const ApplyArgs& a, int style, cudaStream_t s) {
-  const unsigned blocks = (a.n_items + kApplyThreads - 1) / kApplyThreads;
-  if (style == LLA_ROPE_HALF) rope_apply_kernel<T, VEC, 0><<<blocks, kApplyThreads, 0, s>>>(a);
-  else rope_apply_kernel<T, VEC, 1><<<blocks, kApplyThreads, 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>((a.N + a.toks - 1) / a.toks), (a.n_items + a.items.d - 1) / a.items.d);
+  const unsigned threads = (a.items.d * a.strips.d * a.toks + 31) / 32 * 32;
+  if (style == LLA_ROPE_HALF) rope_apply_kernel<T, VEC, 0><<<grid, threads, 0, s>>>(a);
+  else rope_apply_kernel<T, VEC, 1><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -321,25 +352,26 @@ lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_str
                    all % wide == 0;
   const int V = vec ? wide : 1;
   a.rot_items = a.half / V;
-  a.items = FastDiv(a.rot_items + (in_place ? 0 : (d_x - d_rope) / V));
-  a.per_head = FastDiv(heads);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // launches of at most 2^30 items keep the item arithmetic in 32 bits
-  const int64_t per_tok = static_cast<int64_t>(heads) * a.items.d;
-  if (per_tok > (int64_t(1) << 30)) return LLA_ERR_UNSUPPORTED;
-  const int64_t chunk = (int64_t(1) << 30) / per_tok;
-  for (int64_t t = 0; t < N; t += chunk) {
-    const int64_t n = N - t < chunk ? N - t : chunk;
-    a.tok0 = t;
-    a.n_items = static_cast<uint32_t>(n * per_tok);
-    cudaError_t e;
-    if (dims->dtype == LLA_BF16)
-      e = vec ? launch_apply<__nv_bfloat16, 8>(a, dims->rope_style, s) : launch_apply<__nv_bfloat16, 1>(a, dims->rope_style, s);
-    else
-      e = vec ? launch_apply<float, 4>(a, dims->rope_style, s) : launch_apply<float, 1>(a, dims->rope_style, s);
-    if (e != cudaSuccess) return LLA_ERR_CUDA;
+  a.n_items = a.rot_items + (in_place ? 0 : (d_x - d_rope) / V);
+  if (vec && dims->rope_style == LLA_ROPE_INTERLEAVED) {
+    a.first = in_place ? offset : 0;
+    a.n_items = (in_place ? d_rope : d_x) / V;
   }
-  return LLA_OK;
+  // a block: items of a token-head x threads for kApplyHeads heads each x tokens
+  a.heads = heads;
+  a.N = N;
+  const int items = std::min(a.n_items, kApplyThreads), at_once = kApplyThreads / items;
+  const int strips = std::min((heads + kApplyHeads - 1) / kApplyHeads, at_once);
+  a.items = FastDiv(items);
+  a.strips = FastDiv(strips);
+  a.toks = at_once / strips;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dims->dtype == LLA_BF16)
+    e = vec ? launch_apply<__nv_bfloat16, 8>(a, dims->rope_style, s) : launch_apply<__nv_bfloat16, 1>(a, dims->rope_style, s);
+  else
+    e = vec ? launch_apply<float, 4>(a, dims->rope_style, s) : launch_apply<float, 1>(a, dims->rope_style, s);
+  return e == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }
 
 }  // extern "C"

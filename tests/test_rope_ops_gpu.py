@@ -106,6 +106,26 @@ def test_apply(style, dtype, N, heads, d_x, off, d_rope):
     assert lla.device_status(ws) == lla.LLA_OK
 
 
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,heads,d_x,off,d_rope", [(3, 71, 64, 0, 32), (2, 530, 16, 0, 16), (9, 2, 2100, 4, 2080),
+                                                    (2, 3, 1031, 5, 1020), (1000, 1, 32, 16, 16)])
+def test_apply_many_heads_and_wide_rows(style, dtype, N, heads, d_x, off, d_rope):
+    """More heads than a block's threads take at once, rows of more than a block's threads; table
+    rows that begin on a 16-byte boundary and no wider one."""
+    dm = lla.dims(1, heads, 16, 16, dtype=lla.LLA_BF16 if dtype == "bf16" else lla.LLA_F32, rope_style=style)
+    sd = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(N + d_x)
+    x = torch.randn(N, heads, d_x, generator=g).to(sd).cuda()
+    pos = torch.randint(0, 300, (N,), generator=g, dtype=torch.int32).cuda()
+    cos, sin = (torch.cat([t.new_zeros(4), t.flatten()])[4:].view_as(t) for t in _tables(d_rope))
+    ws = _ws()
+    y = lla.rope_apply(dm, x, pos, cos, sin, offset=off, workspace=ws)
+    _check(y, x, pos, cos, sin, off, style, 1.0, False)
+    lla.rope_apply(dm, x, pos, cos, sin, out=x, offset=off, workspace=ws)
+    assert torch.equal(x, y) and lla.device_status(ws) == lla.LLA_OK
+
+
 def test_apply_strided_slices():
     """q and k as slices of one fused projection, rotated in place and into each other's buffer."""
     dm = lla.dims(1, 4, 16, 16)
