@@ -8,6 +8,7 @@
 // than 7.03, which still rounds to 7).
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "lla_q4.h"
 
@@ -15,15 +16,14 @@ namespace lla {
 
 namespace {
 
-constexpr int kQ4Threads = 256;
+constexpr int kQ4Threads = 32;       // copies: small blocks, a token's heads in few steps of one warp
 constexpr float kQ4Normal = 1.17549435e-38f;   // 2^-126: scales below it have no finite reciprocal, or few bits
 
 struct Q4CopyArgs {
   int H, r_k, r_v, row_bytes;
-  FastDiv groups, heads, page;       // scale groups of a row, heads, rows of a page
-  int64_t num_slots;                 // num_pages * page_size
-  uint32_t n_items;                  // token-heads * 2 (groups of K + groups of V)
-  uint32_t tok0;
+  FastDiv items, strips, page;       // halves of a row's scale groups, threads that share a token's heads, rows of a page
+  int toks;                          // tokens of a block
+  int64_t N, num_slots;              // num_pages * page_size
   const int64_t* slots;
   void* k;                           // [N][H][r_k] storage dtype
   void* v;
@@ -31,86 +31,92 @@ struct Q4CopyArgs {
   uint32_t* status;
 };
 
-// Row of (slot, head); -1 for a slot that holds no token (negative) or lies outside.
-__device__ __forceinline__ int64_t q4_row(const Q4CopyArgs& a, int64_t slot, int h, bool report) {
-  if (slot < 0) return -1;
-  if (slot >= a.num_slots) {
-    if (report) record_status(a.status, LLA_ERR_DEVICE_ARG);
-    return -1;
-  }
-  const int64_t P = a.page.d, page = slot < (int64_t(1) << 31) ? a.page.div(static_cast<uint32_t>(slot)) : slot / P;
-  return (page * a.H + h) * P + (slot - page * P);
-}
-
 // Two neighbouring threads hold one group of 32 columns, sixteen each (the last group of a
-// rank may have 16: the second is idle).  Both directions move 2 (r_k + r_v) bytes (bf16)
-// and a row per token-head and should be bound by HBM, so the work per column is kept to a
-// few instructions: what eight columns a thread, conversions by int and true divisions took
-// was 299 us (store) and 210 us (load) for 65536 tokens of 16 heads at (96, 160).
+// rank may have 16: the second is idle), of one token and up to kQ4Heads of its heads at a
+// time, whose loads go out together.  Both directions move 2 (r_k + r_v) bytes (bf16) and a
+// row per token-head and should be bound by HBM, so the work per column is kept to a few
+// instructions, and divisions and addresses to once per thread.  65536 tokens of 16 heads at
+// (96, 160), store and load: 299 + 210 us with eight columns a thread, conversions by int
+// and true divisions, 188 + 143 with sixteen columns of one head, 267 together as here (310 with
+// four heads and 128 threads).
+constexpr int kQ4Heads = 2;
 struct Q4Item {
   int sub, col, r, code_at, scale_at;
-  bool k_axis, active;
-  uint32_t n, h;
+  bool k_axis, active, last;
+  int64_t n, row;                    // token; its row of head 0, -1: the thread has nothing to do
+  int h;                             // first head
 };
-__device__ __forceinline__ Q4Item q4_item(const Q4CopyArgs& a, uint32_t i) {
+__device__ __forceinline__ Q4Item q4_item(const Q4CopyArgs& a) {
   Q4Item it;
-  const uint32_t gk = q4_groups(a.r_k), g_all = i >> 1, th = a.groups.div(g_all), g = g_all - th * a.groups.d;
-  it.sub = i & 1;
-  it.n = a.heads.div(th);
-  it.h = th - it.n * a.heads.d;
+  const uint32_t team = a.items.div(threadIdx.x), ts = a.strips.div(team);
+  const int item = static_cast<int>(threadIdx.x - team * a.items.d), g = item >> 1, gk = q4_groups(a.r_k);
+  it.sub = item & 1;
+  it.n = static_cast<int64_t>(blockIdx.x) * a.toks + ts;
+  it.h = static_cast<int>(team - ts * a.strips.d);
   it.k_axis = g < gk;
   it.r = it.k_axis ? a.r_k : a.r_v;
   it.col = (it.k_axis ? g : g - gk) * kQ4Group + 16 * it.sub;
   it.active = it.col < it.r;
+  it.last = (item | 1) == static_cast<int>(a.items.d) - 1;
   it.code_at = (it.k_axis ? 0 : a.r_k / 2) + it.col / 2;
   it.scale_at = q4_scale_offset(a.r_k, a.r_v) + 2 * g;
+  it.row = -1;
+  if (static_cast<int>(ts) >= a.toks || it.n >= a.N) return it;
+  const int64_t slot = __ldg(a.slots + it.n);
+  if (slot < 0) return it;           // holds no token
+  if (slot >= a.num_slots) {
+    record_status(a.status, LLA_ERR_DEVICE_ARG);
+    return it;
+  }
+  const int64_t P = a.page.d, page = slot < (int64_t(1) << 31) ? a.page.div(static_cast<uint32_t>(slot)) : slot / P;
+  it.row = page * a.H * P + (slot - page * P);
   return it;
 }
 
-// Sixteen latents, and the bits of the largest |c| among them (NaN sorts above infinity).
-__device__ __forceinline__ uint32_t load16(const __nv_bfloat16* p, float (&v)[16]) {
-  const uint4 x = __ldg(reinterpret_cast<const uint4*>(p)), y = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+// Sixteen latents as they are stored, and the bits of the largest |c| among them
+// (NaN sorts above infinity).
+struct Half16 {
+  uint4 x[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   }
-  return max(top << 16, top & 0xFFFF0000u);
-}
-__device__ __forceinline__ uint32_t load16(const float* p, float (&v)[16]) {
-  uint32_t top = 0;
+  __device__ __forceinline__ uint32_t get(float (&v)[16]) const {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p) + i);
-    v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    }
+    return max(top << 16, top & 0xFFFF0000u);
   }
+};
+struct Full16 {
+  float4 x[4];
+  __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  return top;
-}
+    for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ uint32_t get(float (&v)[16]) const {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[4 * i] = x[i].x; v[4 * i + 1] = x[i].y; v[4 * i + 2] = x[i].z; v[4 * i + 3] = x[i].w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    return top;
+  }
+};
 
 // Bit of column e of a code word.
 __host__ __device__ constexpr int q4_bit(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
 
+// The sixteen columns' codes and scale, at their place in the row `dst`.
 template <typename T>
-__global__ void __launch_bounds__(kQ4Threads) q4_store_kernel(const __grid_constant__ Q4CopyArgs a) {
-  const uint32_t i = blockIdx.x * kQ4Threads + threadIdx.x;
-  // whole warps: every lane takes part in the shuffle below
-  const bool live = i < a.n_items;
-  const Q4Item it = q4_item(a, live ? i : a.n_items - 1);
-  const int64_t n = static_cast<int64_t>(a.tok0) + it.n;
-  float v[16];
-  uint32_t top = 0;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = 0.f;
-  if (live && it.active) top = load16(static_cast<const T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col, v);
-  const int64_t row = live ? q4_row(a, __ldg(a.slots + n), it.h, true) : -1;
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  if (row < 0) return;
-  uint8_t* dst = a.rows + row * a.row_bytes;
+__device__ __forceinline__ void q4_put(const Q4CopyArgs& a, const Q4Item& it, uint8_t* dst, uint32_t top, const float (&v)[16]) {
   const bool finite = top < 0x7f800000u;
   // a group with a value that is not finite stores a NaN scale: all of it reads as NaN
   const __nv_bfloat16 s16 =
@@ -151,8 +157,35 @@ __global__ void __launch_bounds__(kQ4Threads) q4_store_kernel(const __grid_const
   if (it.active) *reinterpret_cast<uint2*>(dst + it.code_at) = make_uint2(w[0], w[1]);
   if (it.sub == 0) *reinterpret_cast<__nv_bfloat16*>(dst + it.scale_at) = s16;
   // the row's padding, by the last group's threads: rows are fully defined
-  if (!it.k_axis && it.scale_at + 2 == q4_scale_offset(a.r_k, a.r_v) + 2 * static_cast<int>(a.groups.d))
+  if (it.last)
     for (int p = it.scale_at + 2 + 2 * it.sub; p < a.row_bytes; p += 4) *reinterpret_cast<uint16_t*>(dst + p) = 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQ4Threads) q4_store_kernel(const __grid_constant__ Q4CopyArgs a) {
+  const Q4Item it = q4_item(a);
+  if (it.row < 0) return;            // (both threads of a group, or neither)
+  const uint32_t pair = 3u << (threadIdx.x & 30);
+  const int strips = static_cast<int>(a.strips.d);
+  const T* src = static_cast<const T*>(it.k_axis ? a.k : a.v) + (it.n * a.H + it.h) * it.r + it.col;
+  const int64_t head = static_cast<int64_t>(a.page.d) * a.row_bytes;   // bytes between a token's heads
+  uint8_t* dst = a.rows + it.row * a.row_bytes + it.h * head;
+  for (int h = it.h; h < a.H; h += kQ4Heads * strips) {
+    std::conditional_t<sizeof(T) == 2, Half16, Full16> c[kQ4Heads] = {};
+#pragma unroll
+    for (int i = 0; i < kQ4Heads; ++i)
+      if (h + i * strips < a.H && it.active) c[i].load(src + i * strips * it.r);
+#pragma unroll
+    for (int i = 0; i < kQ4Heads; ++i) {
+      if (h + i * strips >= a.H) break;
+      float v[16];
+      uint32_t top = c[i].get(v);
+      top = max(top, __shfl_xor_sync(pair, top, 1));
+      q4_put<T>(a, it, dst + i * strips * head, top, v);
+    }
+    src += kQ4Heads * strips * it.r;
+    dst += kQ4Heads * strips * head;
+  }
 }
 
 // Eight values of a code word: code * scale, rounded once to the storage type.
@@ -182,19 +215,30 @@ __device__ __forceinline__ void put8(float* p, uint32_t w, __nv_bfloat16 s) {
 
 template <typename T>
 __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_constant__ Q4CopyArgs a) {
-  const uint32_t i = blockIdx.x * kQ4Threads + threadIdx.x;
-  if (i >= a.n_items) return;
-  const Q4Item it = q4_item(a, i);
-  if (!it.active) return;
-  const int64_t n = static_cast<int64_t>(a.tok0) + it.n;
-  const int64_t row = q4_row(a, __ldg(a.slots + n), it.h, true);
-  if (row < 0) return;
-  const uint8_t* src = a.rows + row * a.row_bytes;
-  const __nv_bfloat16 s = *reinterpret_cast<const __nv_bfloat16*>(src + it.scale_at);
-  const uint2 w = *reinterpret_cast<const uint2*>(src + it.code_at);
-  T* dst = static_cast<T*>(it.k_axis ? a.k : a.v) + (n * a.H + it.h) * it.r + it.col;
-  put8(dst, w.x, s);
-  put8(dst + 8, w.y, s);
+  const Q4Item it = q4_item(a);
+  if (it.row < 0 || !it.active) return;
+  const int strips = static_cast<int>(a.strips.d);
+  const int64_t head = static_cast<int64_t>(a.page.d) * a.row_bytes;
+  const uint8_t* src = a.rows + it.row * a.row_bytes + it.h * head;
+  T* dst = static_cast<T*>(it.k_axis ? a.k : a.v) + (it.n * a.H + it.h) * it.r + it.col;
+  for (int h = it.h; h < a.H; h += kQ4Heads * strips) {
+    __nv_bfloat16 sc[kQ4Heads];
+    uint2 w[kQ4Heads];
+#pragma unroll
+    for (int i = 0; i < kQ4Heads; ++i) {
+      if (h + i * strips >= a.H) break;
+      sc[i] = *reinterpret_cast<const __nv_bfloat16*>(src + i * strips * head + it.scale_at);
+      w[i] = *reinterpret_cast<const uint2*>(src + i * strips * head + it.code_at);
+    }
+#pragma unroll
+    for (int i = 0; i < kQ4Heads; ++i) {
+      if (h + i * strips >= a.H) break;
+      put8(dst + i * strips * it.r, w[i].x, sc[i]);
+      put8(dst + i * strips * it.r + 8, w[i].y, sc[i]);
+    }
+    src += kQ4Heads * strips * head;
+    dst += kQ4Heads * strips * it.r;
+  }
 }
 
 // ----------------------------------------------------------------- fp32 decode
@@ -477,8 +521,13 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
   a.r_k = dims->r_k;
   a.r_v = dims->r_v;
   a.row_bytes = q4_row_bytes(dims->r_k, dims->r_v);
-  a.groups = FastDiv(q4_groups(dims->r_k) + q4_groups(dims->r_v));
-  a.heads = FastDiv(dims->H);
+  // a block: the halves of a row's groups x threads for kQ4Heads heads each x tokens
+  const int items = 2 * (q4_groups(dims->r_k) + q4_groups(dims->r_v)), at_once = kQ4Threads / items;
+  const int strips = std::min((dims->H + kQ4Heads - 1) / kQ4Heads, at_once);
+  a.items = FastDiv(items);
+  a.strips = FastDiv(strips);
+  a.toks = at_once / strips;
+  a.N = N;
   a.page = FastDiv(cache->page_size);
   a.num_slots = cache->num_pages * cache->page_size;
   a.slots = slots;
@@ -487,25 +536,15 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
   a.rows = static_cast<uint8_t*>(cache->rows);
   a.status = static_cast<uint32_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // launches of at most 2^30 items keep the item arithmetic in 32 bits
-  const int64_t per_tok = static_cast<int64_t>(dims->H) * 2 * (q4_groups(dims->r_k) + q4_groups(dims->r_v));
-  if (per_tok > (int64_t(1) << 30)) return LLA_ERR_UNSUPPORTED;
-  const int64_t chunk = (int64_t(1) << 30) / per_tok;
-  for (int64_t t = 0; t < N; t += chunk) {
-    const int64_t n = std::min<int64_t>(chunk, N - t);
-    a.tok0 = static_cast<uint32_t>(t);
-    a.n_items = static_cast<uint32_t>(n * per_tok);
-    const unsigned blocks = (a.n_items + kQ4Threads - 1) / kQ4Threads;
-    if (store) {
-      if (dims->dtype == LLA_BF16) q4_store_kernel<__nv_bfloat16><<<blocks, kQ4Threads, 0, s>>>(a);
-      else q4_store_kernel<float><<<blocks, kQ4Threads, 0, s>>>(a);
-    } else {
-      if (dims->dtype == LLA_BF16) q4_load_kernel<__nv_bfloat16><<<blocks, kQ4Threads, 0, s>>>(a);
-      else q4_load_kernel<float><<<blocks, kQ4Threads, 0, s>>>(a);
-    }
-    if (cudaGetLastError() != cudaSuccess) return LLA_ERR_CUDA;
+  const unsigned blocks = static_cast<unsigned>((a.N + a.toks - 1) / a.toks);
+  if (store) {
+    if (dims->dtype == LLA_BF16) q4_store_kernel<__nv_bfloat16><<<blocks, kQ4Threads, 0, s>>>(a);
+    else q4_store_kernel<float><<<blocks, kQ4Threads, 0, s>>>(a);
+  } else {
+    if (dims->dtype == LLA_BF16) q4_load_kernel<__nv_bfloat16><<<blocks, kQ4Threads, 0, s>>>(a);
+    else q4_load_kernel<float><<<blocks, kQ4Threads, 0, s>>>(a);
   }
-  return LLA_OK;
+  return cudaGetLastError() == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
 }
 
 // Workspace of a decode call: status word; tensor-core kernel: the CTA range of every

@@ -67,6 +67,13 @@ def test_store_writes_the_oracle_rows(dtype, N, H, rk, rv, P):
     assert lla.device_status(ws) == lla.LLA_OK
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,H,rk,rv,P", [(3, 37, 112, 240, 16), (2, 130, 16, 16, 3), (1, 9, 256, 240, 1)])
+def test_store_many_heads(dtype, N, H, rk, rv, P):
+    """More heads than a block's threads hold at a time, and the last step of them not full."""
+    test_store_writes_the_oracle_rows(dtype, N, H, rk, rv, P)
+
+
 def test_store_values_that_are_not_finite():
     """A group with an infinity or a NaN reads as NaN, its neighbours as themselves; the largest
     and the smallest finite values keep their group."""
