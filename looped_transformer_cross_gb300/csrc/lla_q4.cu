@@ -201,16 +201,16 @@ __device__ __forceinline__ void put8(__nv_bfloat16* p, uint32_t w, __nv_bfloat16
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ void q4_unpack8(uint32_t w, float s, float (&v)[8]) {
-  // 2^23 + code + 8 has unit 1 in fp32
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (__uint_as_float(((w >> q4_bit(e)) & 15u) | 0x4B000000u) - 8388616.f) * s;
+// Code of column e of a word: 2^23 + code + 8 has unit 1 in fp32.
+__device__ __forceinline__ float q4_code(uint32_t w, int e) {
+  return __uint_as_float(((w >> q4_bit(e)) & 15u) | 0x4B000000u) - 8388616.f;
 }
 __device__ __forceinline__ void put8(float* p, uint32_t w, __nv_bfloat16 s) {
-  float v[8];
-  q4_unpack8(w, __bfloat162float(s), v);
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  const float f = __bfloat162float(s);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(q4_code(w, 4 * i) * f, q4_code(w, 4 * i + 1) * f, q4_code(w, 4 * i + 2) * f,
+                                                  q4_code(w, 4 * i + 3) * f);
 }
 
 template <typename T>
@@ -246,13 +246,13 @@ __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_consta
 // Decode attention over 4-bit rows for fp32 storage, in fp32 arithmetic: one block
 // per (sequence, head, split of whole 128-token tiles).  The score is Eq. (3) with RoPE
 // after reconstruction, regrouped per frequency pair as in lla_paged_generic.cu, with the
-// folded query in fp32: four neighbouring threads share a token, each with a quarter of the 128
-// rotary coordinates (shared-memory reads of the folded query bound it: one 16-byte read per
-// four multiply-adds, whatever the split, and a small call wants many threads).  One online
-// softmax over the split's tiles, the value path absorbed; a record per split, merged by the combine.
+// folded query in fp32.  A warp has eight of a tile's tokens, a thread four of them and eight of
+// the 128 rotary coordinates (cosine and sine of four frequencies): two 16-byte reads of the
+// folded query serve 32 multiply-adds.  (With 32 coordinates of one token a thread needed
+// eight, and those reads bound the kernel: 34 us for 3 x 333 tokens of 2 heads, now 23.)  One online softmax over
+// the split's tiles, the value path absorbed; a record per split, merged by the combine.
 constexpr int kF32Threads = 512;
-constexpr int kParts = 4;             // threads of a token
-constexpr int kCols = 128 / kParts;   // rotary coordinates of a thread
+constexpr int kParts = 4;             // threads that fetch a token's row
 constexpr float kQ4ScoreScale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
@@ -336,48 +336,67 @@ __global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_consta
   const int v_scale = q4_scale_offset(rk, rv) + 2 * (q4_groups(rk) + col / kQ4Group);
   float acc = 0.f, m_run = -INFINITY, l_run = 0.f;
   __syncthreads();
-  const int token = tid / kParts, part = tid % kParts;
+  const int t0 = 8 * wid + 4 * (lane >> 4), f4 = 4 * (lane & 15);   // the thread's tokens and frequencies
+  const bool owner = (lane & 12) == 0;                                // of one token's weight
+  const int token = t0 + (lane & 3);
   for (int64_t j0 = j_lo; j0 < j_hi; j0 += kTile) {
-    const int64_t j = j0 + token;
-    const bool valid = j < j_hi;
+    const bool valid = owner && j0 + token < j_hi;
     const int nt = static_cast<int>(min(static_cast<int64_t>(kTile), j_hi - j0));
-    const uint8_t* mine = tile + static_cast<size_t>(token) * ts;
-    float s = 0.f;
-    if (valid) {
-      // this part's coordinates: four of every sixteen, so that a token's four reads are neighbours
-      float A[kCols];
+    const uint8_t* mine = tile + static_cast<size_t>(t0) * ts;
+    float s4[4];
+    {
+      float A[4][8];
 #pragma unroll
-      for (int f = 0; f < kCols; ++f) A[f] = bias[16 * (f / 4) + 4 * part + f % 4];
-      const float* zp = z + 4 * part;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) A[i][e] = bias[64 * (e >> 2) + f4 + (e & 3)];
+      const float* zp = z + f4;
 #pragma unroll 1
       for (int k0 = 0; k0 < rk; k0 += 8) {
-        float c8[8];
-        const float sc = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-            mine + q4_scale_offset(rk, rv) + 2 * (k0 / kQ4Group)));
-        q4_unpack8(*reinterpret_cast<const uint32_t*>(mine + k0 / 2), sc, c8);
+        float sc[4];
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // (a token behind the split's last may hold anything: its score is not used)
+          sc[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+              mine + i * ts + q4_scale_offset(rk, rv) + 2 * (k0 / kQ4Group)));
+          w[i] = *reinterpret_cast<const uint32_t*>(mine + i * ts + k0 / 2);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float4* zr = reinterpret_cast<const float4*>(zp + (k0 + e) * 128);
+          const float4 zc = *reinterpret_cast<const float4*>(zp + (k0 + e) * 128);
+          const float4 zs = *reinterpret_cast<const float4*>(zp + (k0 + e) * 128 + 64);
 #pragma unroll
-          for (int g = 0; g < kCols / 4; ++g) {
-            const float4 z4 = zr[4 * g];
-            A[4 * g] = fmaf(c8[e], z4.x, A[4 * g]);
-            A[4 * g + 1] = fmaf(c8[e], z4.y, A[4 * g + 1]);
-            A[4 * g + 2] = fmaf(c8[e], z4.z, A[4 * g + 2]);
-            A[4 * g + 3] = fmaf(c8[e], z4.w, A[4 * g + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const float c = q4_code(w[i], e) * sc[i];
+            A[i][0] = fmaf(c, zc.x, A[i][0]);
+            A[i][1] = fmaf(c, zc.y, A[i][1]);
+            A[i][2] = fmaf(c, zc.z, A[i][2]);
+            A[i][3] = fmaf(c, zc.w, A[i][3]);
+            A[i][4] = fmaf(c, zs.x, A[i][4]);
+            A[i][5] = fmaf(c, zs.y, A[i][5]);
+            A[i][6] = fmaf(c, zs.z, A[i][6]);
+            A[i][7] = fmaf(c, zs.w, A[i][7]);
           }
         }
       }
 #pragma unroll
-      for (int f = 0; f < kCols; f += 4) {
-        const float* t = (f < kCols / 2 ? a.rope_cos : a.rope_sin) + j * 64 + 16 * (f / 4 % 4) + 4 * part;
-        const float4 t4 = __ldg(reinterpret_cast<const float4*>(t));
-        s = fmaf(t4.x, A[f], fmaf(t4.y, A[f + 1], fmaf(t4.z, A[f + 2], fmaf(t4.w, A[f + 3], s))));
+      for (int i = 0; i < 4; ++i) {
+        const int64_t j = min(j0 + t0 + i, j_hi - 1);
+        const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + j * 64 + f4));
+        const float4 n = __ldg(reinterpret_cast<const float4*>(a.rope_sin + j * 64 + f4));
+        float s = c.x * A[i][0];
+        s = fmaf(c.y, A[i][1], fmaf(c.z, A[i][2], fmaf(c.w, A[i][3], s)));
+        s4[i] = fmaf(n.x, A[i][4], fmaf(n.y, A[i][5], fmaf(n.z, A[i][6], fmaf(n.w, A[i][7], s))));
       }
     }
 #pragma unroll
-    for (int o = 1; o < kParts; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (!valid) s = -INFINITY;
+    for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s4[i] += __shfl_xor_sync(0xffffffffu, s4[i], o);
+    float s = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (valid && (lane & 3) == i) s = s4[i];
     // ---- online softmax over the tile (log2 units)
     const float mw = warp_max(s);
     if (lane == 0) red[wid] = mw;
@@ -387,8 +406,8 @@ __global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_consta
     for (int i = 0; i < kF32Threads / 32; ++i) m_new = fmaxf(m_new, red[i]);
     const float scale = m_new == -INFINITY ? 1.f : exp2f(m_run - m_new);   // the first tile: 0
     const float p = valid ? (m_new == -INFINITY ? s - s : exp2f(s - m_new)) : 0.f;   // all NaN: stays NaN
-    if (part == 0) pw[token] = p;
-    const float ps = warp_sum(part == 0 ? p : 0.f);
+    if (owner) pw[token] = p;
+    const float ps = warp_sum(p);
     __syncthreads();   // pw complete; red is read
     if (lane == 0) red[wid] = ps;
     if (col < rv) {
