@@ -567,11 +567,11 @@ lla_status q4_copy(const lla_dims* dims, void* k, void* v, int N, const int64_t*
 }
 
 // Workspace of a decode call: status word; tensor-core kernel: the CTA range of every
-// (sequence, head group), a record per head of every (unit, CTA) of a run (at most
+// (sequence, head group), the units of every folded query, a record per head of every (unit, CTA) of a run (at most
 // units + grid of them), the query operands of every (sequence, head group), the f16 rotary tiles of
 // L_max positions; fp32 kernel: a record per split.
 struct Q4Ws {
-  size_t ranges, records, zimg, row_tiles, total;
+  size_t ranges, z_unit, records, zimg, row_tiles, total;
   int grid;
 };
 Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
@@ -584,7 +584,8 @@ Q4Ws q4_ws(const lla_dims* d, int B, int64_t L_max, int sms) {
     make_q4_plan(d->H, d->r_k, d->r_v, &p);
     const int64_t units = static_cast<int64_t>(B) * p.ngroups;
     w.grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min(sms, kMaxGrid), units * tiles)));
-    w.records = (256 + static_cast<size_t>(units) * 8 + 255) / 256 * 256;
+    w.z_unit = 256 + static_cast<size_t>(units) * 8;
+    w.records = (w.z_unit + static_cast<size_t>(B) * d->H * 8 + 255) / 256 * 256;
     w.zimg = (w.records + (static_cast<size_t>(units) + w.grid) * p.nh * q4_record_floats(p.nh, d->r_v) * 4 + 255) / 256 * 256;
     w.row_tiles = w.zimg + static_cast<size_t>(units) * 2 * p.z_chunk;
     w.total = w.row_tiles + static_cast<size_t>(tiles) * kTile * 256;
@@ -681,6 +682,7 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
   if (dims->dtype == LLA_BF16) {
     if (!make_q4_plan(a.H, a.r_k, a.r_v, &a.plan)) return LLA_ERR_UNSUPPORTED;
     a.ranges = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + w.ranges);
+    a.z_unit = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.z_unit);
     a.grid = w.grid;
     a.row_tiles = static_cast<uint8_t*>(workspace) + w.row_tiles;
     a.zimg = static_cast<uint8_t*>(workspace) + w.zimg;

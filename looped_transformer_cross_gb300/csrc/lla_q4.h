@@ -67,6 +67,7 @@ struct Q4DecodeArgs {
   int splits;                        // fp32 kernel: splits of a (sequence, head)
   uint8_t* row_tiles;                // tensor-core kernel: f16 rotary rows, 32 KB per 128 positions
   uint8_t* zimg;                     // query operands of every (sequence, head group)
+  float2* z_unit;                    // [B][H]: units of the folded query's f16 values, and of its bias's
   int z_blocks, rows_grid;           // blocks that form the operands, and the rotary tiles
   int32_t* ranges;                   // first and last CTA of each (sequence, head group)
   int grid;

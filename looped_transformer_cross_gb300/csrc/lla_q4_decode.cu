@@ -48,6 +48,7 @@ constexpr int kMaxNh = 8;                        // heads of a group
 constexpr int kRowChunk = 16384;                 // half a rotary tile: a K-major chunk of 128 rows x 128 bytes
 constexpr int kRowTile = 2 * kRowChunk;
 constexpr int kNR = 3;                           // chunks of rotary tiles in shared memory
+constexpr int kState = 36;                        // floats of a (warp, head)'s state
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
@@ -474,12 +475,16 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
     Slot st{0, 0u}, gs{0, 0u};
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
-    // per head the warp's reference and each thread's own sum
-    float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * 33;
+    // per head each thread's own sum, the warp's reference, and the units of its query operands
+    float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * kState;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the units are written
     while (walk.next(a, ngroups, run)) {
       for (int hi = 0; hi < nh; ++hi) {
-        state[hi * 33 + lane] = 0.f;
-        if (lane == 0) state[hi * 33 + 32] = -INFINITY;
+        state[hi * kState + lane] = 0.f;
+        if (lane == 0) state[hi * kState + 32] = -INFINITY;
+        if (lane == 0)
+          *reinterpret_cast<float2*>(state + hi * kState + 34) =
+              __ldcg(a.z_unit + static_cast<int64_t>(run.b) * a.H + run.hg * nh + hi);
       }
       __syncwarp();
 #pragma unroll 1
@@ -549,19 +554,20 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           }
           tc_fence_before();
           arrive(misc->gempty[gs.i]);
-          s = valid ? s + (bias[0] + bias[1]) : -INFINITY;
+          const float2 unit = *reinterpret_cast<const float2*>(state + hi * kState + 34);
+          s = valid ? fmaf(s, unit.x, (bias[0] + bias[1]) * unit.y) : -INFINITY;
           // ---- softmax of the warp's 32 tokens: integer reference, raised lazily
           const float mt = warp_max_redux(s);
-          float m = state[hi * 33 + 32], l = state[hi * 33 + lane];
+          float m = state[hi * kState + 32], l = state[hi * kState + lane];
           if (mt > m + kRaise) {
             const float mn = ceilf(mt);
             l *= exp2f(m - mn);
             m = mn;
             __syncwarp();
-            if (lane == 0) state[hi * 33 + 32] = m;
+            if (lane == 0) state[hi * kState + 32] = m;
           }
           const float p = s == -INFINITY ? 0.f : exp2f(s - m);
-          state[hi * 33 + lane] = l + p;
+          state[hi * kState + lane] = l + p;
           // ---- weights p * scale of each V group, relative to 2^(m + E)
           // (scale / 2^E is below one and p at most 2^8: f16 holds the product; p / 2^E might not be finite)
           const uint32_t out = tail + 2 * row;
@@ -574,8 +580,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       }
       // ---- run end: (m, l) of this warp's tokens
       for (int hi = 0; hi < nh; ++hi) {
-        const float l = warp_sum(state[hi * 33 + lane]);
-        if (lane == 0) *reinterpret_cast<float2*>(record(hi) + kRecMl + 2 * (warp - 4)) = make_float2(state[hi * 33 + 32], l);
+        const float l = warp_sum(state[hi * kState + lane]);
+        if (lane == 0) *reinterpret_cast<float2*>(record(hi) + kRecMl + 2 * (warp - 4)) = make_float2(state[hi * kState + 32], l);
       }
       __syncwarp();
     }
@@ -702,7 +708,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 // 128-byte swizzle; a head's N rows are its r_k rows Z_n, bias high and low, -8 sum Z of each scale
 // group, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
 //     Z_n,f = sc (q'_i0 W_i0,n + q'_i1 W_i1,n),  Z_n,64+f = sc (q'_i1 W_i0,n - q'_i0 W_i1,n),
-// the bias rows the same over mu.  A warp holds the weights of 32 columns and 32 frequencies in
+// the bias rows the same over mu; either times a power of two that brings the largest (for Z a
+// bound of it) to 2^7, because f16 has no range to spare for queries and weights of any size.  The
+// inverses, the units, are multiplied back into the score.  A warp holds the weights of 32 columns and 32 frequencies in
 // registers and serves the block's sequences with them.
 // The other blocks: the f16 rotary rows of every position below the longest length, as
 // tiles of 128 positions (chunk 0 cosines, chunk 1 sines); 512 bytes read and 256 written
@@ -737,7 +745,9 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
     }
     return;
   }
+  static_assert(kPrepThreads == 64 * kQ4PrepSeqs, "a thread per sequence and frequency");
   __shared__ float qs[kQ4PrepSeqs][2][64];   // sc q'_i0 and sc q'_i1
+  __shared__ uint32_t tops[3][kPrepThreads / 32];   // bits of the largest |q'|, |bias|, |W| of each warp
   const int h = blockIdx.x % a.H, b0 = blockIdx.x / a.H * kQ4PrepSeqs, seqs = min(kQ4PrepSeqs, a.B - b0);
   const Q4Plan& P = a.plan;
   const int N = P.N, rk = a.r_k, gk = q4_groups(rk), nh = P.nh, hi = h % nh;
@@ -749,32 +759,70 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
            swizzle_offset((hi * N + row) * 128 + 2 * (coord & 63), 128);
   };
   __half2 top = __half2half2(__ushort_as_half(0));   // largest magnitude written (infinite: out of range)
-  for (int i = tid; i < seqs * 64; i += kPrepThreads) {
-    const int s = i >> 6, f = i & 63, b = b0 + s;
-    int qp = __ldg(a.q_pos + b);
-    if (qp < 0 || qp >= a.rope_len) {
-      if (f == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
-      qp = qp < 0 ? 0 : static_cast<int>(a.rope_len - 1);
+  const int ms = tid >> 6, mf = tid & 63;    // the thread's sequence and frequency
+  float bias[2] = {0.f, 0.f};
+  {
+    uint32_t w_top = 0;
+    const uint4* W = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk);
+#pragma unroll 4
+    for (int i = tid; i < kHeadDim * rk / 8; i += kPrepThreads) {
+      const uint4 x = __ldg(W + i);
+      w_top = __vmaxu2(w_top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
     }
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h) * kHeadDim;
-    const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + f);
-    const float sn = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + f);
-    const float x0 = __bfloat162float(q[i0_of(f)]), x1 = __bfloat162float(q[i1_of(f)]);
-    const float q0 = (x0 * c - x1 * sn) * kQ4Scale, q1 = (x0 * sn + x1 * c) * kQ4Scale;
-    qs[s][0][f] = q0;
-    qs[s][1][f] = q1;
-    const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0_of(f)), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1_of(f));
-    const float bias[2] = {q0 * m0 + q1 * m1, q1 * m0 - q0 * m1};
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const __half high = __float2half_rn(bias[part]);
-      top = __hmax2(top, __habs2(__half2half2(high)));
-      *reinterpret_cast<__half*>(at(s, rk, 64 * part + f)) = high;
-      *reinterpret_cast<__half*>(at(s, rk + 1, 64 * part + f)) = __float2half_rn(bias[part] - __half2float(high));
-      for (int row = rk + 2 + gk; row < N; ++row) *reinterpret_cast<__half*>(at(s, row, 64 * part + f)) = __ushort_as_half(0);
+    float q0 = 0.f, q1 = 0.f;
+    if (ms < seqs) {
+      const int b = b0 + ms;
+      int qp = __ldg(a.q_pos + b);
+      if (qp < 0 || qp >= a.rope_len) {
+        if (mf == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
+        qp = qp < 0 ? 0 : static_cast<int>(a.rope_len - 1);
+      }
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<int64_t>(b) * a.H + h) * kHeadDim;
+      const float c = __ldg(a.rope_cos + static_cast<int64_t>(qp) * 64 + mf);
+      const float sn = __ldg(a.rope_sin + static_cast<int64_t>(qp) * 64 + mf);
+      const float x0 = __bfloat162float(q[i0_of(mf)]), x1 = __bfloat162float(q[i1_of(mf)]);
+      q0 = (x0 * c - x1 * sn) * kQ4Scale;
+      q1 = (x0 * sn + x1 * c) * kQ4Scale;
+      const float m0 = __ldg(a.mu_k + h * a.mu_hstride + i0_of(mf)), m1 = __ldg(a.mu_k + h * a.mu_hstride + i1_of(mf));
+      bias[0] = q0 * m0 + q1 * m1;
+      bias[1] = q1 * m0 - q0 * m1;
+    }
+    qs[ms][0][mf] = q0;
+    qs[ms][1][mf] = q1;
+    auto bits = [](float x) { return __float_as_uint(x) & 0x7FFFFFFFu; };   // (NaN sorts above infinity)
+    w_top = __reduce_max_sync(0xffffffffu, max(w_top << 16, w_top & 0xFFFF0000u));
+    const uint32_t q_top = __reduce_max_sync(0xffffffffu, max(bits(q0), bits(q1)));
+    const uint32_t b_top = __reduce_max_sync(0xffffffffu, max(bits(bias[0]), bits(bias[1])));
+    if (lane == 0) {
+      tops[0][warp] = q_top;
+      tops[1][warp] = b_top;
+      tops[2][warp] = w_top;
     }
   }
   __syncthreads();
+  uint32_t w_top = 0;
+#pragma unroll
+  for (int i = 0; i < kPrepThreads / 32; ++i) w_top = max(w_top, tops[2][i]);
+  // the exponent that brings a value of these bits to 2^7 at most; 0 if not finite: nor is the result
+  auto lift = [](uint32_t bits) {
+    return bits >= 0x7F800000u ? 0 : max(-100, min(100, 133 - static_cast<int>(bits >> 23)));
+  };
+  auto z_lift = [&](int s) {   // of sequence s: |Z| <= 2 max|q'| max|W|
+    return lift(__float_as_uint(2.f * __uint_as_float(max(tops[0][2 * s], tops[0][2 * s + 1])) * __uint_as_float(w_top)));
+  };
+  if (ms < seqs) {
+    const int e = lift(max(tops[1][2 * ms], tops[1][2 * ms + 1]));
+    if (mf == 0) a.z_unit[static_cast<int64_t>(b0 + ms) * a.H + h] = make_float2(pow2(-z_lift(ms)), pow2(-e));
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      const float x = bias[part] * pow2(e);
+      const __half high = __float2half_rn(x);
+      top = __hmax2(top, __habs2(__half2half2(high)));
+      *reinterpret_cast<__half*>(at(ms, rk, 64 * part + mf)) = high;
+      *reinterpret_cast<__half*>(at(ms, rk + 1, 64 * part + mf)) = __float2half_rn(x - __half2float(high));
+      for (int row = rk + 2 + gk; row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
+    }
+  }
   // item of a warp = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies)
   for (int it = warp; it < 2 * gk; it += kPrepThreads / 32) {
     const int g = it >> 1, n = 32 * g + 8 * (lane >> 3), f0 = 32 * (it & 1) + 4 * (lane & 7);
@@ -790,10 +838,11 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
     for (int s = 0; s < seqs; ++s) {
       float q0[4], q1[4], sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
       uint8_t* z0 = at(s, n, 0);
+      const float up = pow2(z_lift(s));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        q0[e] = qs[s][0][f0 + e];
-        q1[e] = qs[s][1][f0 + e];
+        q0[e] = qs[s][0][f0 + e] * up;
+        q1[e] = qs[s][1][f0 + e] * up;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -951,7 +1000,7 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
     int off = 0;
     p->z = off; off += 2 * p->z_chunk;
     p->rows = off = al(off, 1024); off += kNR * kRowChunk;
-    p->state = off; off = al(off + 8 * nh * 33 * 4, 16);
+    p->state = off; off = al(off + 8 * nh * kState * 4, 16);
     p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 16);
     p->ring = off;
     p->NS = std::min((kSmemLimit - 1024 - off) / p->stage, kQ4MaxNS);

@@ -271,6 +271,17 @@ def test_decode_scales_of_any_size(dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rk,rv", [(96, 160), (16, 32)])
+@pytest.mark.parametrize("wide,mean", [(2.0 ** -30, 1.0), (2.0 ** 24, 1.0), (2.0 ** -18, 0.0), (2.0 ** 30, 2.0 ** -20)])
+def test_decode_weights_of_any_size(dtype, rk, rv, wide, mean):
+    """Small weights over large latents and the reverse are the same keys: the folded query keeps its
+    digits whatever its size."""
+    x = _inputs([150, 700, 1], 4, rk, rv, 16, dtype, 33, scale=1.0 / wide)
+    x = dict(x, wk=(x["wk"].double() * wide).to(_sd(dtype)), mk=x["mk"] * mean)
+    _check(x, 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decode_nan_stays_in_its_sequence_head(dtype):
     """A row whose scale is NaN makes its own (sequence, head) NaN and no other."""
     x = _inputs([200, 130, 64], 2, 96, 160, 16, dtype, 8)
