@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           page = 0;
         }
         return Piece{static_cast<uint32_t>((t1 - t0) * rb), static_cast<uint32_t>((t0 - x.y0) * rb),
-                     a.rows + (static_cast<int64_t>(page) * a.H + x.hg * nh) * head_bytes + (t0 - p0) * rb};
+                     a.rows + (static_cast<int64_t>(page) * a.H + x.hg * nh) * head_bytes + static_cast<int64_t>(t0 - p0) * rb};
       };
       Pos x{}, y{};
       bool more = next(y);

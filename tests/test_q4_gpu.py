@@ -385,6 +385,36 @@ def test_decode_pool_past_32_bits():
     assert rel_err(out.double().cpu().numpy(), _oracle(x, 1)[0]) <= TOL["bf16"]
 
 
+def test_decode_page_past_32_bits():
+    """One page of more than 2^31 bytes: rows of zeros (score and value 0 without means) but for the
+    last token, whose score outweighs all of them, so its value is the result."""
+    rk = rv = 256
+    L = (1 << 31) // q4.row_bytes(rk, rv) + 1000
+    dm = _dims(1, 1, rk, rv)
+    g = np.random.default_rng(3)
+    q, wk, wv = (torch.from_numpy(g.standard_normal(s) * f).bfloat16()
+                 for s, f in (((1, 1, 128), 1.0), ((1, 1, 128, rk), 1 / 16), ((1, 1, 128, rv), 1 / 16)))
+    # the query and the token share a position, so the score is q . W c / sqrt(128): 60 for this c
+    u = widen(q)[0, 0] @ widen(wk)[0, 0]
+    ck, cv = u * (60 * math.sqrt(128) / (u @ u)), g.standard_normal(rv)
+    row = np.frombuffer(q4.row_of(ck.astype(np.float32), cv.astype(np.float32)), np.uint8)
+    pool = torch.zeros((1, 1, L, q4.row_bytes(rk, rv)), dtype=torch.uint8, device="cuda")
+    pool[0, 0, L - 1] = torch.from_numpy(row.copy()).cuda()
+    cos, sin = lla.rope_table_scaled(dm, L)
+    ws = lla.q4_workspace(dm, 1, L)
+    out, lse = torch.empty(1, 1, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 1, device="cuda")
+    i = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    zero = torch.zeros(1, 128, device="cuda")
+    lla.decode_attn_q4(dm, 0, q.cuda(), pool, i([[0]]), i([L]), i([L - 1]), wk.cuda(), wv.cuda(), zero, zero, cos, sin,
+                       out, lse, ws)
+    assert lla.device_status(ws) == lla.LLA_OK
+    vk, vv = q4.values(row[None], rk, rv)
+    s = float(u @ vk[0]) / math.sqrt(128)
+    assert s > 40                                              # exp(-40) of 7.5e6 zeros is 3e-11
+    assert abs(float(lse) - s) <= TOL["bf16"] * s
+    assert rel_err(out.double().cpu().numpy()[0, 0], widen(wv)[0, 0] @ vv[0]) <= TOL["bf16"]
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("dtype,rk,rv,P", [("bf16", 96, 160, 16), ("f32", 48, 80, 24), ("bf16", 16, 32, 64)])
