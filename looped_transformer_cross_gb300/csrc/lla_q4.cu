@@ -517,7 +517,7 @@ namespace {
 lla_status q4_pool_checks(const lla_dims* dims, const lla_q4_cache* c) {
   if (!c || c->B < 0 || c->page_size < 1 || c->num_pages < 1) return LLA_ERR_INVALID_ARG;
   if (dims->variant != LLA_PER_HEAD) return LLA_ERR_UNSUPPORTED;
-  if (c->num_pages * static_cast<int64_t>(dims->H) >= (int64_t(1) << 31) ||
+  if (c->num_pages >= (int64_t(1) << 31) || c->num_pages * static_cast<int64_t>(dims->H) >= (int64_t(1) << 31) ||
       c->num_pages * static_cast<int64_t>(c->page_size) >= (int64_t(1) << 40))
     return LLA_ERR_UNSUPPORTED;
   return LLA_OK;

@@ -178,6 +178,17 @@ def test_q4_copy_and_decode_refusals(L, mem):
         assert dec(**bad) == UNS, bad
 
 
+@pytest.mark.parametrize("num", [1 << 62, (1 << 63) - 1, (1 << 60) + 1])
+def test_pool_sizes_past_64_bits(L, mem, num):
+    """Page counts whose products with the heads or the page size do not fit 64 bits are refused."""
+    dm, p = lla.dims(4, 16, 96, 160), mem()
+    c = lla.Q4Cache(p, p, 1, 4, 16, num)
+    assert L.lla_q4_store(ctypes.byref(dm), p, p, 2, p, ctypes.byref(c), p, 256, None) == UNS
+    assert L.lla_q4_load(ctypes.byref(dm), p, 2, ctypes.byref(c), p, p, p, 256, None) == UNS
+    assert L.lla_decode_attn_q4(ctypes.byref(dm), 0, p, ctypes.byref(c), p, p, p, p, p, p, p, p, 128, p, None, p, 1 << 30,
+                                None) == UNS
+
+
 def test_binding_argument_checks(L):
     """The binding names the argument that does not fit before it passes a pointer on."""
     dm = lla.dims(4, 2, 96, 160)
