@@ -16,6 +16,7 @@
 namespace lla {
 
 constexpr int kQ4Group = 32;          // columns that share a scale
+constexpr int kQ4CombineUnits = 4;    // most sequences of a combine block
 constexpr int kQ4PrepSeqs = 4;        // sequences of a block that forms query operands
 
 __host__ __device__ inline int q4_groups(int r) { return (r + kQ4Group - 1) / kQ4Group; }
@@ -71,7 +72,7 @@ struct Q4DecodeArgs {
   int z_blocks, rows_grid;           // blocks that form the operands, and the rotary tiles
   int32_t* ranges;                   // first and last CTA of each (sequence, head group)
   int grid;
-  int combine_units;                 // sequences per combine block (1..8)
+  int combine_units;                 // sequences per combine block (1..kQ4CombineUnits)
   Q4Plan plan;
 };
 

@@ -823,9 +823,12 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
       for (int row = rk + 2 + gk; row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
     }
   }
-  // item of a warp = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies)
-  for (int it = warp; it < 2 * gk; it += kPrepThreads / 32) {
-    const int g = it >> 1, n = 32 * g + 8 * (lane >> 3), f0 = 32 * (it & 1) + 4 * (lane & 7);
+  // item = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies).  The (item,
+  // sequence) pairs are dealt out evenly, a warp's in a row so that its weights serve several
+  const int pairs = 2 * gk * seqs, share = (pairs + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
+  const int last = min(pairs, (warp + 1) * share);
+  for (int pair = warp * share, s; pair < last;) {
+    const int it = pair / seqs, g = it >> 1, n = 32 * g + 8 * (lane >> 3), f0 = 32 * (it & 1) + 4 * (lane & 7);
     const bool live = n < rk;
     uint4 w0[4], w1[4];
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * rk + n;
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
       if (live) w0[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i0_of(f0 + e)) * rk));
       if (live) w1[e] = __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(i1_of(f0 + e)) * rk));
     }
-    for (int s = 0; s < seqs; ++s) {
+    for (s = pair - it * seqs; s < seqs && pair < last; ++s, ++pair) {
       float q0[4], q1[4], sum_c[4] = {0.f, 0.f, 0.f, 0.f}, sum_s[4] = {0.f, 0.f, 0.f, 0.f};
       uint8_t* z0 = at(s, n, 0);
       const float up = pow2(z_lift(s));
@@ -893,11 +896,10 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
 // merging a sequence at a time, then two threads per output, each with half of its row of
 // W_up,v in registers: requested before the wait for the decode grid, they serve every sequence.
 constexpr int kCombineThreads = 256;
-constexpr int kMaxCombineUnits = 8;
 template <int RV32>
 __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __grid_constant__ Q4DecodeArgs a) {
   constexpr int kRegs = 2 * RV32;   // 16-byte loads of half a row, rounded up
-  __shared__ float acc[kMaxCombineUnits][RV32 * 32], inv[kMaxCombineUnits];
+  __shared__ float acc[kQ4CombineUnits][RV32 * 32], inv[kQ4CombineUnits];
   const int h = blockIdx.x % a.H, b0 = static_cast<int>(blockIdx.x / a.H) * a.combine_units, tid = threadIdx.x;
   const int rv = a.r_v, nh = a.plan.nh, nu = min(a.combine_units, a.B - b0), warp = tid >> 5, lane = tid & 31;
   const int e = tid >> 1, half = tid & 1;   // output, and which 8-column pieces of its row: half, half + 2, ..
