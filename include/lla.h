@@ -70,7 +70,8 @@ typedef enum {
     LLA_ERR_DEVICE_ARG = 5,    /* out-of-range seq_lens/q_pos/seq_idx/pos seen
                                   by a kernel (device word)                       */
     LLA_ERR_RANGE = 6          /* a folded query operand left the f16 range of
-                                  the small-rank decode path (device word)        */
+                                  the small-rank decode path, or is infinite in
+                                  the 4-bit one (device word)                     */
 } lla_status;
 
 typedef enum { LLA_BF16 = 0, LLA_F32 = 1 } lla_dtype;
@@ -450,7 +451,9 @@ lla_status lla_q4_load(const lla_dims* dims, const int64_t* slots, int N, const 
  * latents that the rows stand for.  `out` is [B][H][d] in the storage dtype (rounded
  * once); `lse` may be NULL.  Everything else as lla_decode_attn_paged, with a workspace of
  * lla_q4_workspace_size() bytes (L_max = max_pages * page_size), the first 256 zero.  A row
- * with a NaN scale makes its sequence-head's result NaN.
+ * with a NaN scale makes its sequence-head's result NaN.  bf16 storage: scores carry one f16
+ * rounding of the folded query and one of the table's rows (|cos|, |sin| below 65504), weights one of
+ * p * scale; sums are fp32.  fp32 storage: fp32 throughout.
  */
 size_t lla_q4_workspace_size(const lla_dims* dims, int B, int64_t L_max);
 lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, const lla_q4_cache* cache,
