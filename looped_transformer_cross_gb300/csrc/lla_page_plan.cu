@@ -20,7 +20,8 @@ constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 8192;        // requests of a plan (shared memory: 16 bytes each)
 
 struct PlanArgs {
-  int B, page_size, max_pages, n_free, n_tok;
+  int B, max_pages, n_free, n_tok;
+  FastDiv page;                      // page size
   int64_t num_pages;
   int per_thread;                    // token entries of a thread
   const int32_t* ctx;
@@ -55,7 +56,11 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& b, int64_t (*tot
   __syncthreads();
 }
 
-__device__ __forceinline__ int64_t pages_of(int64_t tokens, int P) { return (tokens + P - 1) / P; }
+// (lengths are below 2^31: 64-bit divisions took a tenth of the kernel's time)
+__device__ __forceinline__ int pages_of(int tokens, const FastDiv& P) {
+  const uint32_t whole = P.div(static_cast<uint32_t>(tokens));
+  return static_cast<int>(whole + (whole * P.d != static_cast<uint32_t>(tokens)));
+}
 
 // The last of n ascending starts that is at or before i (starts[0] <= i).
 __device__ __forceinline__ int owner(const int32_t* starts, int n, int64_t i) {
@@ -80,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   int32_t* fresh = sh + 3 * a.B;
   __shared__ int64_t tot[kPlanThreads / 32][2];
   __shared__ int64_t total[2];           // tokens requested, pages taken
-  const int tid = threadIdx.x, P = a.page_size;
+  const int tid = threadIdx.x, P = static_cast<int>(a.page.d);
   const bool first = blockIdx.x == 0;
   int64_t head = a.free_head ? static_cast<int64_t>(__ldg(a.free_head)) : 0;
   if (head < 0 || head > a.n_free) {
@@ -105,7 +110,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   block_scan(tok_end, zero, tot);
   // pages: a request that cannot hold its tokens (table too short, maps too short) takes none
   auto fits = [&](int64_t c, int64_t n, int64_t before) { return c + n <= cap && before + n <= a.n_tok; };
-  auto need_of = [&](int64_t c, int64_t n) { return pages_of(c + n, P) - pages_of(c, P); };
+  auto need_of = [&](int64_t c, int64_t n) {   // (fits: below 2^30)
+    return pages_of(static_cast<int>(c + n), a.page) - pages_of(static_cast<int>(c), a.page);
+  };
   int64_t need_sum = 0, t = tok_end - toks;
   for (int b = b0; b < b1; ++b) {
     const int64_t c = len0[b], n = fresh[b];
@@ -153,7 +160,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
   for (int64_t k = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; k < total[1]; k += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
     const int b = owner(page0, a.B, k), p = __ldg(a.free_pages + head + k);
     if (p < 0 || p >= a.num_pages) record_status(a.status, LLA_ERR_DEVICE_ARG);
-    a.table[static_cast<int64_t>(b) * a.max_pages + pages_of(len0[b], P) + (k - page0[b])] = p;
+    a.table[static_cast<int64_t>(b) * a.max_pages + pages_of(len0[b], a.page) + (k - page0[b])] = p;
   }
 
   // ---- token maps
@@ -165,8 +172,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     if (i < total[0]) {
       const int b = owner(start, a.B, i);
       if (fresh[b] >= 0) {
-        const int p = len0[b] + static_cast<int>(i - start[b]), lp = p / P;
-        const int held = static_cast<int>(pages_of(len0[b], P));
+        const int p = len0[b] + static_cast<int>(i - start[b]), lp = static_cast<int>(a.page.div(static_cast<uint32_t>(p)));
+        const int held = pages_of(len0[b], a.page);
         const int page = lp < held ? __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + lp)
                                    : __ldg(a.free_pages + head + page0[b] + lp - held);
         sb = b;
@@ -216,7 +223,7 @@ extern "C" lla_status lla_page_plan(int B, int page_size, int max_pages, int64_t
   if (sms <= 0) return LLA_ERR_CUDA;
   // two blocks per SM at most: each repeats the scan
   const int64_t stretch = static_cast<int64_t>(kPlanThreads) * 2 * sms;
-  PlanArgs a{B, page_size, max_pages, n_free, n_tok, num_pages, static_cast<int>((n_tok + stretch - 1) / stretch), ctx_lens,
+  PlanArgs a{B, max_pages, n_free, n_tok, FastDiv(page_size), num_pages, static_cast<int>((n_tok + stretch - 1) / stretch), ctx_lens,
              new_lens, free_pages, free_head, block_table, seq_lens, tok_start, granted, seq_idx, pos, slots, counts,
              static_cast<uint32_t*>(workspace)};
   a.per_thread = std::max(a.per_thread, 1);
