@@ -52,7 +52,6 @@ constexpr int kState = 36;                        // floats of a (warp, head)'s 
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
-constexpr int kNoRef = -(1 << 28);
 // a record per (unit, CTA) and head: (m, l) of each epilogue warp, the reference of each V warp, their sums
 constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 24;
 
@@ -574,7 +573,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           const float ie = pow2(-E);
 #pragma unroll
           for (int g = 0; g < RV32; ++g) sts16(out + 2 * g * kWStride, __float2half_rn(__uint_as_float(vs[g] << 16) * ie * p));
-          if (lane == 0) sts32(tail + P.w_bytes + 4 * q, m == -INFINITY ? kNoRef : static_cast<int>(m) + E);
+          if (lane == 0) sts32(tail + P.w_bytes + 4 * q, __float_as_uint(m + static_cast<float>(E)));   // (-inf: none)
           arrive(misc->wfull[st.i]);
         }
       }
@@ -601,7 +600,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) one[j] = 0.f;
-      int ref = kNoRef;
+      float ref = -INFINITY;
       for (int t = 0; t < run.n; ++t)
         for (int hi = 0; hi < nh; ++hi, st.next(NS)) {
           if (hi != mine) continue;
@@ -610,9 +609,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 #pragma unroll 1
           for (int g = ks_first >> 1; 2 * g < ks_first + nh; ++g) {
             // the reference of these 32 tokens' weights: the sums are rescaled when it rises
-            const int r = static_cast<int>(lds32(tail + P.w_bytes + 4 * g));
+            const float r = __uint_as_float(lds32(tail + P.w_bytes + 4 * g));
             if (r > ref) {
-              const float f = exp2f(static_cast<float>(ref) - static_cast<float>(r));
+              const float f = exp2f(ref - r);
 #pragma unroll
               for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -622,7 +621,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               ref = r;
             }
             // 2^(r - ref) in f16 (0 below 2^-14: such weights no longer count)
-            const __half2 f2 = bits_h2(r - ref >= -14 ? static_cast<uint32_t>(r - ref + 15) * 0x04000400u : 0u);
+            const __half2 f2 = bits_h2(r - ref >= -14.f ? static_cast<uint32_t>(static_cast<int>(r - ref) + 15) * 0x04000400u : 0u);
             const int ks_end = min(2 * g + 2, ks_first + nh);
 #pragma unroll 1
             for (int ks = max(2 * g, ks_first); ks < ks_end; ++ks) {
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
       float* rec = record(mine);
       float* acc = rec + kRecAcc + v % per * rv;
-      if (lane == 0) rec[kRecRef + v % per] = static_cast<float>(ref);
+      if (lane == 0) rec[kRecRef + v % per] = ref;
       auto put = [&](int col, float x) {
         if (col < rv) acc[col] = x;
       };

@@ -282,6 +282,43 @@ def test_decode_weights_of_any_size(dtype, rk, rv, wide, mean):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("wide", [2.0 ** 12, 2.0 ** 20, 2.0 ** 32])
+def test_decode_scores_of_any_size(dtype, sign, wide):
+    """Scores of thousands to 10^10: the largest takes all of the weight.  Keys are one mean per head,
+    its share by a latent, so the scores have one sign; the two best are a tenth apart at least."""
+    L, rk, rv = 700, 32, 48
+    x = _inputs([L], 2, rk, rv, 16, dtype, 35, T=1)
+    # one rotation angle for all positions (a table of one row), a key of length c_0 along the query
+    q, rows = widen(x["q"])[0], x["pool"][x["table"][0, np.arange(L) // 16], :, np.arange(L) % 16]
+    order = np.random.default_rng(4).permutation(L)
+    for h in range(2):
+        ck = np.zeros((L, rk), np.float32)
+        ck[:, 0] = np.where(order == 0, 1.0, 0.5 + 0.4 * order / L) if sign > 0 else np.where(order == 0, 0.5, 0.6 + 0.4 * order / L)
+        for j in range(L):
+            row = np.frombuffer(q4.row_of(ck[j], q4.values_of(rows[j, h].tobytes(), rk, rv)[1].astype(np.float32)), np.uint8)
+            x["pool"][x["table"][0, j // 16], h, j % 16] = row
+    wk = np.zeros((1, 2, 128, rk))
+    wk[0, :, :, 0] = sign * wide * np.sign(q)
+    x = dict(x, wk=torch.from_numpy(wk).to(_sd(dtype)), mk=torch.zeros(2, 128))
+    dm = _dims(1, 2, rk, rv, dtype)
+    cos, sin = torch.ones(704, 64, device="cuda"), torch.zeros(704, 64, device="cuda")
+    ws = lla.q4_workspace(dm, 1, 704)
+    out, lse = torch.empty(1, 2, 128, dtype=_sd(dtype), device="cuda"), torch.empty(1, 2, device="cuda")
+    c = lambda v: torch.as_tensor(v).cuda()  # noqa: E731
+    lla.decode_attn_q4(dm, 0, c(x["q"]), c(x["pool"]), c(x["table"]), c(x["lens"]), c(x["q_pos"]), c(x["wk"]), c(x["wv"]),
+                       c(x["mk"]), c(x["mv"]), cos, sin, out, lse, ws)
+    assert lla.device_status(ws) == lla.LLA_OK
+    best = int(np.flatnonzero(order == 0)[0])
+    for h in range(2):
+        vk, vv = q4.values_of(x["pool"][x["table"][0, best // 16], h, best % 16].tobytes(), rk, rv)
+        want = widen(x["wv"])[0, h] @ vv + widen(x["mv"])[h]
+        assert rel_err(out.double().cpu().numpy()[0, h], want) <= TOL[dtype]
+        score = q[h] @ (widen(x["wk"])[0, h] @ vk) / math.sqrt(128)
+        assert abs(float(lse[0, h]) - score) <= TOL[dtype] * abs(score)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decode_nan_stays_in_its_sequence_head(dtype):
     """A row whose scale is NaN makes its own (sequence, head) NaN and no other."""
     x = _inputs([200, 130, 64], 2, 96, 160, 16, dtype, 8)
