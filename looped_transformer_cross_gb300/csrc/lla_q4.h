@@ -28,7 +28,8 @@ __host__ __device__ inline int q4_row_bytes(int r_k, int r_v) {
 // Shared-memory plan of the tensor-core decode kernel (byte offsets from a 1024-aligned base).
 struct Q4Plan {
   int nh, ngroups;                   // heads of a group (1, 2, 4 or 8), groups of a sequence
-  int NS, NG, NB, gstep;             // ring stages, G buffers in TMEM, their barriers and columns apart
+  int NS, NR;                        // stages of head-tiles, chunks (half tiles) of rotary rows
+  int PG, PB, gstep;                 // positions with G in TMEM, their barriers, columns apart
   int N;                             // rows of a head's query operand = columns of G: r_k + 16
   int z, z_chunk;                    // query operands of the group's heads: two chunks of coordinates
   int rows;                          // rotary tiles

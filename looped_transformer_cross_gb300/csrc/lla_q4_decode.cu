@@ -30,7 +30,7 @@
 // equal contiguous ranges, one per CTA.  A run is a CTA's part of one (sequence, head
 // group).  Roles meet only at mbarriers, at run ends too: each epilogue and V warp writes its own
 // part of the run's records, which the combine merges.  Warps: 0 copies rows (bulk copies of page
-// pieces), 1 copies query operands and issues MMAs, 2 copies rotary tiles, 4-11 epilogue, 12-19 V.
+// pieces), 1 copies query operands and issues MMAs, 2 copies rotary tiles, 3 gives them back, 4-11 epilogue, 12-19 V.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -43,11 +43,11 @@ namespace {
 
 constexpr int kQ4TileThreads = 640;
 constexpr int kQ4MaxNS = 16;
-constexpr int kMaxG = 16;                        // G buffers
+constexpr int kMaxG = 16;                        // positions whose G is in TMEM
 constexpr int kMaxNh = 8;                        // heads of a group
 constexpr int kRowChunk = 16384;                 // half a rotary tile: a K-major chunk of 128 rows x 128 bytes
 constexpr int kRowTile = 2 * kRowChunk;
-constexpr int kNR = 3;                           // chunks of rotary tiles in shared memory
+constexpr int kMinNR = 3, kMaxNR = 8;             // chunks of rotary tiles in shared memory
 constexpr int kState = 36;                        // floats of a (warp, head)'s state
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
@@ -57,7 +57,7 @@ constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 24;
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
-  uint64_t rfull[kNR], rempty[kNR], gfull[kMaxG], gempty[kMaxG];
+  uint64_t rfull[kMaxNR], rempty[kMaxNR], gfull[kMaxG], gempty[kMaxG];
   uint64_t zfull, zdone;                         // query operands: copied; no longer read
   uint32_t tmem_base;
   int abort;
@@ -67,8 +67,8 @@ struct alignas(16) Q4Misc {
 // Position of a ring with its barriers' phase.  A wait tells a phase from the one before it only, so no
 // warp may leave out phases of a barrier that it waits on.  Every ring that several groups take
 // turns at therefore has a multiple of their number of barriers, which gives each barrier one
-// waiting group: the head-tiles of the two epilogue groups (NS and NB even), the heads of the V warps
-// (NS a multiple of nh, and so is H).
+// waiting group: the head-tiles of the two epilogue groups (NS even; with one head PB too), the heads of
+// the V warps (NS a multiple of nh, and so is H).
 struct Slot {
   int i;
   uint32_t phase;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
   Q4Misc* misc = reinterpret_cast<Q4Misc*>(sm + P.misc);
   volatile int* abort = &misc->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, NG = P.NG, NB = P.NB, N = P.N, gstep = P.gstep, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
+  const int nh = P.nh, ngroups = P.ngroups, NS = P.NS, PG = P.PG, PB = P.PB, NR = P.NR, N = P.N, gstep = P.gstep, rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
   const int scale_at = q4_scale_offset(rk, rv), gk = q4_groups(rk);
 
   // ---------------------------------------------------------- work range
@@ -262,13 +262,13 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       mbar_init(bar(misc->empty[s]), 8 / nh);       // the head's V warps, the last to read it
       mbar_init(bar(misc->wfull[s]), 4);
     }
-    for (int i = 0; i < kNR; ++i) {
+    for (int i = 0; i < NR; ++i) {
       mbar_init(bar(misc->rfull[i]), 1);
       mbar_init(bar(misc->rempty[i]), 1);
     }
-    for (int i = 0; i < NB; ++i) {
+    for (int i = 0; i < PB; ++i) {
       mbar_init(bar(misc->gfull[i]), 1);
-      mbar_init(bar(misc->gempty[i]), 4);
+      mbar_init(bar(misc->gempty[i]), 4 * nh);
     }
     mbar_init(bar(misc->zfull), 1);
     mbar_init(bar(misc->zdone), 1);
@@ -393,18 +393,32 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           }
           __syncwarp();
           ++issued;
-          rs.next(kNR);
+          rs.next(NR);
         }
-      if (lane == 0) land(misc->rfull, rs, kNR, issued);
+      if (lane == 0) land(misc->rfull, rs, NR, issued);
+    } else if (warp == 3) {
+      // ======================================================== rotary chunks of finished MMAs
+      // (gfull cannot come round twice unseen: NR <= 2 PB + 1 chunks, and position t + PB needs one of t's)
+      Slot rs{0, 0u}, gp{0, 0u};
+      while (walk.next(a, ngroups, run))
+        for (int t = 0; t < run.n; ++t) {
+          wait(misc->gfull[gp.i], gp.phase);
+          gp.next(PB);
+          for (int c = 0; c < 2; ++c) {
+            if (ok && lane == 0) mbar_arrive(bar(misc->rempty[rs.i]));
+            rs.next(NR);
+          }
+        }
     } else if (warp == 1) {
       // ======================================================== MMA issuer
       // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
-      // step takes about as long for 256 columns as for 128, so the heads of a position share
-      // one chain while their rows fit and their buffers are neighbours (r_k = 256: two chains a head).
-      const int together = max(1, 256 / N);
+      // step takes about as long for 256 columns as for 128, so the heads of a group share one chain
+      // (r_k = 256: two chains).  A commit takes this warp 570 cycles, more than it takes to issue
+      // the eight MMAs, so there is one per position: of all heads' buffers and, passed on by
+      // warp 3, of the rotary chunks.  (One per head and chunk bound the kernel: 122 us at 32 x 4096.)
       // A run's query operands come by two bulk copies once the last run's MMAs are done; the epilogue
-      // still has up to NG head-tiles of that run to go.
-      Slot rs{0, 0u}, gs{0, 0u};
+      // still has up to PG positions of that run to go.
+      Slot rs{0, 0u}, gp{0, 0u};
       uint32_t runs = 0;
       asm volatile("griddepcontrol.wait;" ::: "memory");   // the operands are written
       while (walk.next(a, ngroups, run)) {
@@ -423,40 +437,31 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         wait(misc->zfull, runs & 1);
         if (ok) ++runs;
         for (int t = 0; t < run.n; ++t) {
-          // the position's chunks: cosines, sines
-          Slot half[2];
+          // the position's buffers (PG = 1: two barriers take turns at one), then its chunks: cosines, sines
+          if (PG > 1) wait(misc->gempty[gp.i], gp.phase ^ 1u);
+          else wait(misc->gempty[gp.i ^ 1], gp.phase ^ static_cast<uint32_t>(gp.i ^ 1));
+          uint64_t ad[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            half[c] = rs;
-            rs.next(kNR);
+            wait(misc->rfull[rs.i], rs.phase);
+            ad[c] = umma_desc(sbase + P.rows + rs.i * kRowChunk, 16, 1024, kSw128);
+            rs.next(NR);
           }
-          for (int hi = 0, heads; hi < nh; hi += heads) {
-            heads = min(together, min(nh - hi, NB - gs.i));
-            if (NG > 1)
-              for (int i = 0; i < heads; ++i) wait(misc->gempty[gs.i + i], gs.phase ^ 1u);
-            else
-              wait(misc->gempty[gs.i ^ 1], gs.phase ^ static_cast<uint32_t>(gs.i ^ 1));   // the tile before
-            tc_fence_after();
-            const bool last = hi + heads == nh;
+          tc_fence_after();
+          if (ok) {
+            for (int r0 = 0; r0 < nh * N; r0 += 256) {
+              const uint32_t idesc = umma_idesc_f16(128, min(nh * N - r0, 256));
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (hi == 0) wait(misc->rfull[half[c].i], half[c].phase);
-              if (!ok) continue;
-              const uint64_t ad = umma_desc(sbase + P.rows + half[c].i * kRowChunk, 16, 1024, kSw128);
-              for (int r0 = 0; r0 < heads * N; r0 += 256) {
-                const uint32_t idesc = umma_idesc_f16(128, min(heads * N - r0, 256));
-                const uint64_t bd = umma_desc(sbase + P.z + c * P.z_chunk + (hi * N + r0) * 128, 16, 1024, kSw128);
+              for (int c = 0; c < 2; ++c) {
+                const uint64_t bd = umma_desc(sbase + P.z + c * P.z_chunk + r0 * 128, 16, 1024, kSw128);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_warp(tmem + gs.i * gstep + r0, ad + 2 * kk, bd + 2 * kk, idesc, c + kk > 0 ? 1u : 0u);
+                  umma_bf16_warp(tmem + gp.i * gstep + r0, ad[c] + 2 * kk, bd + 2 * kk, idesc, c + kk > 0 ? 1u : 0u);
               }
-              if (last) umma_commit_warp(bar(misc->rempty[half[c].i]));
             }
-            for (int i = 0; i < heads; ++i) {
-              if (ok) umma_commit_warp(bar(misc->gfull[gs.i]));
-              gs.next(NB);
-            }
+            umma_commit_warp(bar(misc->gfull[gp.i]));
           }
+          gp.next(PB);
         }
       }
       // this warp's copies and MMAs complete before shared memory and TMEM are released
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     // ======================================================== epilogue: scores, weights
     const int grp = (warp - 4) >> 2, q = warp & 3, row = 32 * q + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
-    Slot st{0, 0u}, gs{0, 0u};
+    Slot st{0, 0u}, gp{0, 0u};
     uint32_t n = 0;         // head-tiles so far: group n & 1 takes the n-th
     // per head each thread's own sum, the warp's reference, and the units of its query operands
     float* state = reinterpret_cast<float*>(sm + P.state) + (warp - 4) * nh * kState;
@@ -490,13 +495,13 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       for (int t = 0; t < run.n; ++t) {
         const bool valid = row < run.L - (run.t0 + t) * kTile;
 #pragma unroll 1
-        for (int hi = 0; hi < nh; ++hi, ++n, st.next(NS), gs.next(NB)) {
+        for (int hi = 0; hi < nh; ++hi, ++n, st.next(NS)) {
           if (grp != static_cast<int>(n & 1)) continue;
           const uint32_t base = sbase + P.ring + st.i * P.stage, tail = base + kTile * rb, r = base + row * rb;
           wait(misc->full[st.i], st.phase);
-          wait(misc->gfull[gs.i], gs.phase);
+          wait(misc->gfull[gp.i], gp.phase);
           tc_fence_after();
-          const uint32_t gcol = tmem + lane_base + gs.i * gstep;
+          const uint32_t gcol = tmem + lane_base + gp.i * gstep + hi * N;
           float bias[2], s = 0.f;
           tmem_ld_x2(gcol + rk, bias);
           // ---- V scales; 2^E is above every one of the warp's tokens
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0]);
           }
           tc_fence_before();
-          arrive(misc->gempty[gs.i]);
+          arrive(misc->gempty[gp.i]);
           const float2 unit = *reinterpret_cast<const float2*>(state + hi * kState + 34);
           s = valid ? fmaf(s, unit.x, (bias[0] + bias[1]) * unit.y) : -INFINITY;
           // ---- softmax of the warp's 32 tokens: integer reference, raised lazily
@@ -576,6 +581,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           if (lane == 0) sts32(tail + P.w_bytes + 4 * q, __float_as_uint(m + static_cast<float>(E)));   // (-inf: none)
           arrive(misc->wfull[st.i]);
         }
+        gp.next(PB);
       }
       // ---- run end: (m, l) of this warp's tokens
       for (int hi = 0; hi < nh; ++hi) {
@@ -981,32 +987,34 @@ cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
 bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
   const int rb = q4_row_bytes(r_k, r_v), rv32 = (r_v + 31) / 32;
   auto al = [](int x, int a) { return (x + a - 1) / a * a; };
-  // Heads of a group: they share a position's rotary tile and, up to 256 operand rows, its MMA
-  // chain, which takes as long for one head as for all.  Only as many as divide the heads, eight or
-  // four only where their rows fit a chain; a head-tile stays in the ring while scores and V take their turns, so groups of several
-  // heads need room for copies ahead.
+  // Heads of a group: they share a position's rotary tile and MMA chain, which takes as long for
+  // one head as for all.  Only as many as divide the heads and fit a chain; a head-tile stays in the ring while scores and V take
+  // their turns, so groups of several heads need room for copies ahead.  What the head-tiles leave
+  // goes to rotary chunks: with few heads a position is over before the next tile has come.
   for (int nh = kMaxNh; nh >= 1; nh /= 2) {
-    if (H % nh || (nh > 2 && nh * (r_k + 16) > 256)) continue;
+    if (H % nh || (nh > 1 && nh * (r_k + 16) > 256)) continue;
     *p = Q4Plan{};
     p->nh = nh;
     p->ngroups = H / nh;
     p->N = r_k + 16;
-    p->NG = std::min(kMaxG, 512 / p->N);
-    if (p->NG > 1) p->NG -= p->NG % 2;
-    p->NB = std::max(2, p->NG);
-    p->gstep = p->NG > 1 ? p->N : 0;
+    p->PG = std::min(kMaxG, 512 / p->N / nh);
+    if (nh == 1 && p->PG > 1) p->PG -= p->PG % 2;
+    p->PB = nh == 1 ? std::max(2, p->PG) : p->PG;
+    p->gstep = p->PG > 1 ? nh * p->N : 0;
     p->z_chunk = nh * p->N * 128;
     p->w_bytes = rv32 * kWStride * 2;
     p->stage = kTile * rb + p->w_bytes + 16;
-    int off = 0;
-    p->z = off; off += 2 * p->z_chunk;
-    p->rows = off = al(off, 1024); off += kNR * kRowChunk;
-    p->state = off; off = al(off + 8 * nh * kState * 4, 16);
-    p->misc = off; off += al(static_cast<int>(sizeof(Q4Misc)), 16);
-    p->ring = off;
-    p->NS = std::min((kSmemLimit - 1024 - off) / p->stage, kQ4MaxNS);
+    const int state = al(8 * nh * kState * 4, 16), misc = al(static_cast<int>(sizeof(Q4Misc)), 16);
+    p->z = 0;
+    p->rows = al(2 * p->z_chunk, 1024);
+    const int room = kSmemLimit - 1024 - p->rows - state - misc;
+    p->NS = std::min((room - kMinNR * kRowChunk) / p->stage, kQ4MaxNS);
     p->NS -= p->NS % std::max(2, nh);
-    p->bytes = off + p->NS * p->stage + 1024;
+    p->NR = std::min((room - p->NS * p->stage) / kRowChunk, std::min(kMaxNR, 2 * p->PB + 1));
+    p->state = p->rows + p->NR * kRowChunk;
+    p->misc = p->state + state;
+    p->ring = p->misc + misc;
+    p->bytes = p->ring + p->NS * p->stage + 1024;
     if (p->NS >= (nh == 1 ? 2 : std::max(4, nh))) return true;
   }
   return false;
