@@ -123,6 +123,7 @@ __device__ __forceinline__ void q4_put(const Q4CopyArgs& a, const Q4Item& it, ui
       finite ? __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.f)) : __ushort_as_bfloat16(0x7fc0);
   const float s = __bfloat162float(s16);
   uint32_t w[2];
+  bool done = false;
   if (sizeof(T) == 2 && finite && s >= kQ4Normal) {
     // bf16 values: c / s has 8-bit numerator and denominator, so it is half an integer exactly or off
     // by 2^-10 at least (for |c / s| >= 1/4).  c * (1 / s), 2^-22 off at most, rounded to multiples of
@@ -142,7 +143,30 @@ __device__ __forceinline__ void q4_put(const Q4CopyArgs& a, const Q4Item& it, ui
       }
       w[j] = sum - base;
     }
-  } else {
+    done = true;
+  }
+  if (sizeof(T) == 4 && finite && s >= kQ4Normal) {
+    // fp32 values: c * (1 / s) is within 2^-23 of the quotient (8.4e-7 of up to 7.03), which fp32 division
+    // moves by 2.4e-7 more: only next to a tie could either matter, and that group is divided.  (A
+    // division for every value took four times as long as the bytes.)
+    const float inv = __frcp_rn(s);
+    constexpr uint32_t kBase = 0x4B400000u;
+    float off = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      uint32_t sum = 0, base = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float q = __fmul_rn(v[8 * j + e], inv), t = __fadd_rn(q, 12582920.f);
+        off = fmaxf(off, fabsf(__fsub_rn(q, __fadd_rn(t, -12582920.f))));
+        sum += __float_as_uint(t) * (1u << q4_bit(e));
+        base += kBase * (1u << q4_bit(e));
+      }
+      w[j] = sum - base;
+    }
+    done = off < 0.5f - 2e-6f;
+  }
+  if (!done) {
     const bool some = finite && s > 0.f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {

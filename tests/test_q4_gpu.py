@@ -74,6 +74,30 @@ def test_store_many_heads(dtype, N, H, rk, rv, P):
     test_store_writes_the_oracle_rows(dtype, N, H, rk, rv, P)
 
 
+def test_store_fp32_next_to_ties():
+    """fp32 latents at, just above and just below the half-way points of their group's grid, for scales
+    of any mantissa and size: the codes of the fp32 quotients."""
+    dm, g = _dims(1, 1, 256, 16, "f32"), np.random.default_rng(6)
+    N = 400
+    ck = np.zeros((N, 1, 256), np.float32)
+    for n in range(N):
+        for a in range(0, 256, 32):
+            amax = np.float32(g.uniform(1, 2) * 2.0 ** int(g.integers(-100, 100)))
+            bits = (np.array([amax / np.float32(7)], np.float32).view(np.uint32) + 0x7FFF + 0) & 0xFFFF0000
+            sc = bits.view(np.float32)[0]
+            c = (g.integers(-7, 7, 32) + 0.5).astype(np.float32) * sc
+            step = g.integers(-2, 3, 32)
+            c = np.where(step > 0, np.nextafter(c, np.float32(np.inf)), np.where(step < 0, np.nextafter(c, np.float32(-np.inf)), c))
+            c = np.clip(c, -amax, amax)
+            c[g.integers(32)] = amax
+            ck[n, 0, a:a + 32] = c
+    cv = g.standard_normal((N, 1, 16)).astype(np.float32)
+    pool, ws = lla.q4_pool(dm, 1, N), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    lla.q4_store(dm, torch.from_numpy(ck).cuda(), torch.from_numpy(cv).cuda(), torch.arange(N, device="cuda"), pool, ws)
+    want = np.stack([np.frombuffer(q4.row_of(ck[n, 0], cv[n, 0]), np.uint8) for n in range(N)])
+    np.testing.assert_array_equal(pool.cpu().numpy()[0, 0], want)
+
+
 def test_store_values_that_are_not_finite():
     """A group with an infinity or a NaN reads as NaN, its neighbours as themselves; the largest
     and the smallest finite values keep their group."""
