@@ -124,17 +124,24 @@ bool turns_of(const lla_dims* dims, const lla_rope_scaling* sc, TurnArgs* a) {
 // ----------------------------------------------------------------- rotation
 
 constexpr int kApplyThreads = 128;
-constexpr int kApplyHeads = 4;                // heads of a thread whose loads are in flight together
+// Heads of a thread whose loads are in flight together (two 16-byte loads, 16 cosines and sines a head
+// take the registers of two).
+constexpr int kCopyHeads = 4;
+__host__ __device__ constexpr int apply_heads(int vec, int style) { return style == 0 && vec == 8 ? 2 : 4; }
 
 struct ApplyArgs {
   const void* x;
   void* out;
   int64_t x_tok, x_head, out_tok, out_head;   // strides in elements
   int offset, half;
-  int rot_items, n_items;                     // per token-head: rotated items, then copied ones; all
+  struct Deal {                               // a block's share: items of a token-head x strips x tokens
+    FastDiv items, strips;                    // strips: threads that share a token's heads
+    int toks;
+  } deal[2];                                  // of rotated items, of copied ones
+  int rot_items, n_items;                     // per token-head: rotated items, all
+  unsigned rot_blocks;                        // blocks (x) of rotated items; copied ones follow
   int first;                                  // column of the first item (interleaved vectors)
-  FastDiv items, strips;                      // a block's items of a token-head; threads that share a token's heads
-  int heads, toks;                            // heads; tokens of a block
+  int heads;
   int64_t N;
   const int32_t* pos;
   const float* rope_cos;                      // [rope_len][half]
@@ -178,26 +185,32 @@ __device__ __forceinline__ V load_once(const void* p) {
 // VEC * sizeof(T) == 16), or VEC elements outside the rotated part, copied when the call
 // is not in place.  Interleaved pairs lie within 16 bytes: there an item is one such vector, rotated or
 // copied, in the order of the columns.  A thread keeps its item and token, and with them its
-// position, cosines and sines, for up to kApplyHeads heads at a time, whose loads are all
+// position, cosines and sines, for two or four heads at a time, whose loads are all
 // under way before the first is used.  (One item a thread, with its divisions and
-// addresses, took 177 instructions per warp and was bound by issuing them.)  HBM-bound:
+// addresses, took 177 instructions per warp and was bound by issuing them; rotated and copied
+// items in one warp take turns: 32768 x 16 vectors of 192, last 64 in half layout: 182 us, in blocks
+// of their own and with 64 registers a thread 75.)  HBM-bound:
 // each element is read and written once.  fp32 arithmetic, one rounding to the storage type.
 template <typename T, int VEC, int kStyle>
-__global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const __grid_constant__ ApplyArgs a) {
+__global__ void __launch_bounds__(kApplyThreads, 8) rope_apply_kernel(const __grid_constant__ ApplyArgs a) {
   constexpr bool kWhole = kStyle == 1 && VEC > 1;          // an item's pairs are one vector's
+  constexpr int kHeads = apply_heads(VEC, kStyle);
   constexpr int kPairs = kWhole ? VEC / 2 : VEC;
   using V = Vec<T, VEC>;
   using F = Vec<float, kPairs>;
-  const uint32_t slot = a.items.div(threadIdx.x), ts = a.strips.div(slot);
-  const int item = static_cast<int>(blockIdx.y * a.items.d + threadIdx.x - slot * a.items.d);
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * a.toks + ts;
-  if (static_cast<int>(ts) >= a.toks || n >= a.N || item >= a.n_items) return;
+  // (rotated and copied items in blocks of their own: no warp has both)
+  const bool copy = !kWhole && blockIdx.x >= a.rot_blocks;
+  const ApplyArgs::Deal& D = a.deal[copy];
+  const uint32_t slot = D.items.div(threadIdx.x), ts = D.strips.div(slot);
+  const int item = (copy ? a.rot_items : 0) + static_cast<int>(blockIdx.y * D.items.d + threadIdx.x - slot * D.items.d);
+  const int64_t n = static_cast<int64_t>(copy ? blockIdx.x - a.rot_blocks : blockIdx.x) * D.toks + ts;
+  if (static_cast<int>(ts) >= D.toks || n >= a.N || item >= (kWhole || copy ? a.n_items : a.rot_items)) return;
   // the item's columns: i0, and of a split pair i1
   int i0, i1 = 0, f = -1;
   if constexpr (kWhole) {
     i0 = a.first + item * VEC;
     if (i0 >= a.offset && i0 < a.offset + 2 * a.half) f = (i0 - a.offset) / 2;
-  } else if (item < a.rot_items) {
+  } else if (!copy) {
     f = item * VEC;
     i0 = a.offset + (kStyle == 0 ? f : 2 * f);
     i1 = kStyle == 0 ? i0 + a.half : i0 + 1;
@@ -217,21 +230,33 @@ __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const __grid_
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) s.v[e] *= a.sign;
   }
-  int h = static_cast<int>(slot - ts * a.strips.d);
+  int h = static_cast<int>(slot - ts * D.strips.d);
   const T* x = static_cast<const T*>(a.x) + n * a.x_tok + h * a.x_head + i0;
   T* out = static_cast<T*>(a.out) + n * a.out_tok + h * a.out_head + i0;
-  const int strips = static_cast<int>(a.strips.d);
+  const int strips = static_cast<int>(D.strips.d);
   const int64_t x_step = strips * a.x_head, out_step = strips * a.out_head;
-  for (; h < a.heads; h += kApplyHeads * strips) {
-    V u[kApplyHeads], w[kApplyHeads];
+  if (copy) {
+    for (; h < a.heads; h += kCopyHeads * strips, x += kCopyHeads * x_step, out += kCopyHeads * out_step) {
+      V u[kCopyHeads];
 #pragma unroll
-    for (int k = 0; k < kApplyHeads; ++k) {
+      for (int k = 0; k < kCopyHeads; ++k)
+        if (h + k * strips < a.heads) u[k] = load_once<V>(x + k * x_step);
+#pragma unroll
+      for (int k = 0; k < kCopyHeads; ++k)
+        if (h + k * strips < a.heads) *reinterpret_cast<V*>(out + k * out_step) = u[k];
+    }
+    return;
+  }
+  for (; h < a.heads; h += kHeads * strips) {
+    V u[kHeads], w[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
       if (h + k * strips >= a.heads) continue;
       u[k] = load_once<V>(x + k * x_step);
       if (!kWhole && f >= 0) w[k] = load_once<V>(x + k * x_step + (i1 - i0));
     }
 #pragma unroll
-    for (int k = 0; k < kApplyHeads; ++k) {
+    for (int k = 0; k < kHeads; ++k) {
       if (h + k * strips >= a.heads) continue;
       if (f >= 0) {
 #pragma unroll
@@ -246,17 +271,22 @@ __global__ void __launch_bounds__(kApplyThreads) rope_apply_kernel(const __grid_
       }
       *reinterpret_cast<V*>(out + k * out_step) = u[k];
     }
-    x += kApplyHeads * x_step;
-    out += kApplyHeads * out_step;
+    x += kHeads * x_step;
+    out += kHeads * out_step;
   }
 }
 
 template <typename T, int VEC>
-cudaError_t launch_apply(const ApplyArgs& a, int style, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((a.N + a.toks - 1) / a.toks), (a.n_items + a.items.d - 1) / a.items.d);
-  const unsigned threads = (a.items.d * a.strips.d * a.toks + 31) / 32 * 32;
-  if (style == LLA_ROPE_HALF) rope_apply_kernel<T, VEC, 0><<<grid, threads, 0, s>>>(a);
-  else rope_apply_kernel<T, VEC, 1><<<grid, threads, 0, s>>>(a);
+cudaError_t launch_apply(ApplyArgs a, int style, cudaStream_t s) {
+  const int copied = style != LLA_ROPE_HALF && VEC > 1 ? 0 : a.n_items - a.rot_items;
+  auto blocks = [&](const ApplyArgs::Deal& d) { return static_cast<unsigned>((a.N + d.toks - 1) / d.toks); };
+  a.rot_blocks = blocks(a.deal[0]);
+  auto chunks = [](int n, const ApplyArgs::Deal& d) { return (n + d.items.d - 1) / d.items.d; };
+  const int turned = a.n_items - copied;
+  const dim3 grid(a.rot_blocks + (copied ? blocks(a.deal[1]) : 0),
+                  std::max(chunks(turned, a.deal[0]), copied ? chunks(copied, a.deal[1]) : 0));
+  if (style == LLA_ROPE_HALF) rope_apply_kernel<T, VEC, 0><<<grid, kApplyThreads, 0, s>>>(a);
+  else rope_apply_kernel<T, VEC, 1><<<grid, kApplyThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -372,14 +402,16 @@ lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_str
     a.first = in_place ? offset : 0;
     a.n_items = (in_place ? d_rope : d_x) / V;
   }
-  // a block: items of a token-head x threads for kApplyHeads heads each x tokens
   a.heads = heads;
   a.N = N;
-  const int items = std::min(a.n_items, kApplyThreads), at_once = kApplyThreads / items;
-  const int strips = std::min((heads + kApplyHeads - 1) / kApplyHeads, at_once);
-  a.items = FastDiv(items);
-  a.strips = FastDiv(strips);
-  a.toks = at_once / strips;
+  const bool whole = vec && dims->rope_style == LLA_ROPE_INTERLEAVED;
+  auto deal = [&](int n, int per) {   // n items of a token-head, per heads of a thread at a time
+    const int items = std::min(n, kApplyThreads), at_once = kApplyThreads / items;
+    const int strips = std::min((heads + per - 1) / per, at_once);
+    return ApplyArgs::Deal{FastDiv(items), FastDiv(strips), at_once / strips};
+  };
+  a.deal[0] = deal(whole ? a.n_items : a.rot_items, apply_heads(V, dims->rope_style == LLA_ROPE_HALF ? 0 : 1));
+  a.deal[1] = deal(std::max(1, a.n_items - a.rot_items), kCopyHeads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (dims->dtype == LLA_BF16)
