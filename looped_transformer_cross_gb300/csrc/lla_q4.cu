@@ -279,15 +279,26 @@ constexpr int kF32Threads = 512;
 constexpr int kParts = 4;             // threads that fetch a token's row
 constexpr float kQ4ScoreScale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 
+// d += (a, a) * b: two fp32 multiply-adds in one instruction
+__device__ __forceinline__ void fma2(float2& d, float a, float2 b) {
+  uint64_t x, y, z;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(x) : "f"(a));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(d.x), "f"(d.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(z) : "l"(x), "l"(y));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(z));
+}
+
 __device__ __forceinline__ int q4_len(const Q4DecodeArgs& a, int b) {
   const int L = __ldg(a.seq_lens + b);
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
-__global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_constant__ Q4DecodeArgs a) {
+__global__ void __launch_bounds__(kF32Threads, 2) q4_f32_kernel(const __grid_constant__ Q4DecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the combine waits for this grid
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float bias[128], qr[kHeadDim], pw[kTile], red[kF32Threads / 32], sums[kF32Threads];
+  __shared__ __align__(8) float bias[128];
+  __shared__ float qr[kHeadDim], pw[kTile], red[kF32Threads / 32], sums[kF32Threads];
   const int rk = a.r_k, rv = a.r_v, rb = a.row_bytes;
   float* z = reinterpret_cast<float*>(smem);                         // [rk][128]: cosine, then sine coordinates
   uint8_t* tile = smem + static_cast<size_t>(rk) * 512;              // [128][rb + 16]
@@ -369,11 +380,11 @@ __global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_consta
     const uint8_t* mine = tile + static_cast<size_t>(t0) * ts;
     float s4[4];
     {
-      float A[4][8];
+      float2 A[4][4];   // cosines, then sines of the four frequencies
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) A[i][e] = bias[64 * (e >> 2) + f4 + (e & 3)];
+        for (int e = 0; e < 4; ++e) A[i][e] = *reinterpret_cast<const float2*>(bias + 64 * (e >> 1) + f4 + 2 * (e & 1));
       const float* zp = z + f4;
 #pragma unroll 1
       for (int k0 = 0; k0 < rk; k0 += 8) {
@@ -392,14 +403,10 @@ __global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float c = q4_code(w[i], e) * sc[i];
-            A[i][0] = fmaf(c, zc.x, A[i][0]);
-            A[i][1] = fmaf(c, zc.y, A[i][1]);
-            A[i][2] = fmaf(c, zc.z, A[i][2]);
-            A[i][3] = fmaf(c, zc.w, A[i][3]);
-            A[i][4] = fmaf(c, zs.x, A[i][4]);
-            A[i][5] = fmaf(c, zs.y, A[i][5]);
-            A[i][6] = fmaf(c, zs.z, A[i][6]);
-            A[i][7] = fmaf(c, zs.w, A[i][7]);
+            fma2(A[i][0], c, make_float2(zc.x, zc.y));
+            fma2(A[i][1], c, make_float2(zc.z, zc.w));
+            fma2(A[i][2], c, make_float2(zs.x, zs.y));
+            fma2(A[i][3], c, make_float2(zs.z, zs.w));
           }
         }
       }
@@ -408,9 +415,9 @@ __global__ void __launch_bounds__(kF32Threads) q4_f32_kernel(const __grid_consta
         const int64_t j = min(j0 + t0 + i, j_hi - 1);
         const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + j * 64 + f4));
         const float4 n = __ldg(reinterpret_cast<const float4*>(a.rope_sin + j * 64 + f4));
-        float s = c.x * A[i][0];
-        s = fmaf(c.y, A[i][1], fmaf(c.z, A[i][2], fmaf(c.w, A[i][3], s)));
-        s4[i] = fmaf(n.x, A[i][4], fmaf(n.y, A[i][5], fmaf(n.z, A[i][6], fmaf(n.w, A[i][7], s))));
+        float s = c.x * A[i][0].x;
+        s = fmaf(c.y, A[i][0].y, fmaf(c.z, A[i][1].x, fmaf(c.w, A[i][1].y, s)));
+        s4[i] = fmaf(n.x, A[i][2].x, fmaf(n.y, A[i][2].y, fmaf(n.z, A[i][3].x, fmaf(n.w, A[i][3].y, s))));
       }
     }
 #pragma unroll
