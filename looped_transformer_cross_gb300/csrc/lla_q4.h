@@ -39,9 +39,9 @@ struct Q4Plan {
 };
 // False where no plan fits (never for ranks up to kMaxRankPerHead).
 bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p);
-// Floats of a record of one head: 8 (m, l), 8 references, 8 / nh sums of r_v (even, so that records are
-// 8-byte aligned).
-inline int q4_record_floats(int nh, int r_v) { return 24 + 8 / nh * r_v; }
+// Floats of a record of one head: 8 (m, l), 8 references (m, E), 8 / nh sums of r_v (even, so that records
+// are 8-byte aligned).
+inline int q4_record_floats(int nh, int r_v) { return 32 + 8 / nh * r_v; }
 
 struct Q4DecodeArgs {
   int B, H, r_k, r_v, rope_style;

@@ -52,10 +52,11 @@ constexpr int kRowTile = 2 * kRowChunk;
 constexpr int kMinNR = 3, kMaxNR = 8;             // chunks of rotary tiles in shared memory
 constexpr int kState = 36;                        // floats of a (warp, head)'s state
 constexpr int kWStride = 136;                    // halves between the groups of a weight tile
+constexpr int kWExp = 2 * kTile;                 // bytes into it: behind the first group's weights, four exponents
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
-// a record per (unit, CTA) and head: (m, l) of each epilogue warp, the reference of each V warp, their sums
-constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 24;
+// a record per (unit, CTA) and head: (m, l) of each epilogue warp, the reference (m, E) of each V warp, their sums
+constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 32;
 
 struct alignas(16) Q4Misc {
   uint64_t full[kQ4MaxNS], empty[kQ4MaxNS], wfull[kQ4MaxNS];
@@ -580,7 +581,11 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           const float ie = pow2(-E);
 #pragma unroll
           for (int g = 0; g < RV32; ++g) sts16(out + 2 * g * kWStride, __float2half_rn(__uint_as_float(vs[g] << 16) * ie * p));
-          if (lane == 0) sts32(tail + P.w_bytes + 4 * q, __float_as_uint(m + static_cast<float>(E)));   // (-inf: none)
+          // (two numbers: from 2^24 on m + E would lose E; m of -inf: none)
+          if (lane == 0) {
+            sts32(tail + P.w_bytes + 4 * q, __float_as_uint(m));
+            sts32(tail + kWExp + 4 * q, __float_as_uint(static_cast<float>(E)));
+          }
           arrive(misc->wfull[st.i]);
         }
         gp.next(PB);
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) one[j] = 0.f;
-      float ref = -INFINITY;
+      float ref_m = -INFINITY, ref_e = 0.f;
       for (int t = 0; t < run.n; ++t)
         for (int hi = 0; hi < nh; ++hi, st.next(NS)) {
           if (hi != mine) continue;
@@ -617,19 +622,22 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 #pragma unroll 1
           for (int g = ks_first >> 1; 2 * g < ks_first + nh; ++g) {
             // the reference of these 32 tokens' weights: the sums are rescaled when it rises
-            const float r = __uint_as_float(lds32(tail + P.w_bytes + 4 * g));
-            if (r > ref) {
-              const float f = exp2f(ref - r);
+            const float r_m = __uint_as_float(lds32(tail + P.w_bytes + 4 * g)), r_e = __uint_as_float(lds32(tail + kWExp + 4 * g));
+            float gap = r_m == -INFINITY ? -INFINITY : (r_m - ref_m) + (r_e - ref_e);
+            if (gap > 0.f) {
+              const float f = exp2f(-gap);
 #pragma unroll
               for (int i = 0; i < NM; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) d[i][j] *= f;
 #pragma unroll
               for (int j = 0; j < 4; ++j) one[j] *= f;
-              ref = r;
+              ref_m = r_m;
+              ref_e = r_e;
+              gap = 0.f;
             }
-            // 2^(r - ref) in f16 (0 below 2^-14: such weights no longer count)
-            const __half2 f2 = bits_h2(r - ref >= -14.f ? static_cast<uint32_t>(static_cast<int>(r - ref) + 15) * 0x04000400u : 0u);
+            // 2^gap in f16 (0 below 2^-14: such weights no longer count)
+            const __half2 f2 = bits_h2(gap >= -14.f ? static_cast<uint32_t>(static_cast<int>(gap) + 15) * 0x04000400u : 0u);
             const int ks_end = min(2 * g + 2, ks_first + nh);
 #pragma unroll 1
             for (int ks = max(2 * g, ks_first); ks < ks_end; ++ks) {
@@ -667,7 +675,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // sums; column of (chunk, word gid, MMA i, row half): see `two`
       float* rec = record(mine);
       float* acc = rec + kRecAcc + v % per * rv;
-      if (lane == 0) rec[kRecRef + v % per] = ref;
+      if (lane == 0) *reinterpret_cast<float2*>(rec + kRecRef + 2 * (v % per)) = make_float2(ref_m, ref_e);
       auto put = [&](int col, float x) {
         if (col < rv) acc[col] = x;
       };
@@ -939,7 +947,8 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __gri
       for (int j = 0; j < n; ++j)
         for (int p = 0; p < per; ++p) {
           const float* r = rec + j * stride;
-          const float f = exp2f(r[kRecRef + p] - m);
+          const float2 ref = *reinterpret_cast<const float2*>(r + kRecRef + 2 * p);
+          const float f = exp2f((ref.x - m) + ref.y);
 #pragma unroll
           for (int k = 0; k < RV32; ++k)
             if (32 * k + lane < rv) v[k] = fmaf(r[kRecAcc + p * rv + 32 * k + lane], f, v[k]);

@@ -1,0 +1,129 @@
+"""The 4-bit decode where softmax weights, V scales and score sizes are far apart: attention
+sinks above long tails, V outliers, scores of any size, scale groups of different size, keys
+whose weights share a sign.
+
+A table of cos = 1, sin = 0 leaves keys unrotated, so every score is set by its latent: with
+W_up,k's column 0 along the query, score_j = g_h c_j,0 / sqrt(128).  The expected results are
+written out in 64 bits on the values that the rows hold.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from lla_cases import TOL, rel_err, widen
+from looped_transformer_cross_gb300 import lla
+from oracle import q4
+
+pytestmark = pytest.mark.gpu
+
+LOG2 = math.log2(math.e)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from looped_transformer_cross_gb300 import build
+    build.build()
+
+
+def _bf16(x):
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).bfloat16()
+
+
+def _row_parts(codes, scales):
+    """Bytes of signed codes [..., r] and of the bf16 scales [..., groups]."""
+    r = codes.shape[-1]
+    c = np.arange(r)
+    w = ((codes + 8).astype(np.uint64) << (4 * ((c % 8) // 2) + 16 * (c % 2)).astype(np.uint64))
+    w = w.reshape(*codes.shape[:-1], r // 8, 8).sum(-1).astype(np.uint32)
+    return w.view(np.uint8), _bf16(scales).view(torch.uint8).numpy()
+
+
+class Cache:
+    """One sequence's rows [L][H], as pages of 64 tokens, and the values that they stand for."""
+
+    def __init__(self, kc, ks, vc, vs, P=64):
+        L, H, self.rk = kc.shape
+        self.rv, self.H, self.L, self.P = vc.shape[-1], H, L, P
+        (k, sk), (v, sv) = _row_parts(kc, ks), _row_parts(vc, vs)
+        rows = np.concatenate([k, v, sk, sv], -1)
+        rows = np.pad(rows, ((0, 0), (0, 0), (0, q4.row_bytes(self.rk, self.rv) - rows.shape[-1])))
+        self.pages = -(-L // P)
+        pool = np.full((self.pages * P,) + rows.shape[1:], 0xFF, np.uint8)
+        pool[:L] = rows
+        self.pool = np.ascontiguousarray(pool.reshape(self.pages, P, H, -1).transpose(0, 2, 1, 3))
+        wide = lambda s, r: widen(_bf16(s)).repeat(32, -1)[..., :r]  # noqa: E731
+        self.k, self.v = kc * wide(ks, self.rk), vc * wide(vs, self.rv)          # [L][H][r], fp64
+
+
+def _decode(c, q, wk, wv, dtype, B):
+    """B sequences that name the same rows, all with the query q [H][128]; their common result."""
+    sd = torch.bfloat16 if dtype == "bf16" else torch.float32
+    dm = lla.dims(1, c.H, c.rk, c.rv, dtype=lla.LLA_BF16 if dtype == "bf16" else lla.LLA_F32)
+    cap = c.pages * c.P
+    n = max(cap, 128)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.arange(c.pages, **i32).repeat(B, 1)
+    lens, q_pos = torch.full((B,), c.L, **i32), torch.full((B,), c.L - 1, **i32)
+    out, lse = torch.empty(B, c.H, 128, dtype=sd, device="cuda"), torch.empty(B, c.H, device="cuda")
+    ws, mu = lla.q4_workspace(dm, B, cap), torch.zeros(c.H, 128, device="cuda")
+    lla.decode_attn_q4(dm, 0, q.to(sd).cuda().repeat(B, 1, 1), torch.from_numpy(c.pool).cuda(), table, lens, q_pos,
+                       wk.to(sd).cuda()[None], wv.to(sd).cuda()[None], mu, mu, torch.ones(n, 64, device="cuda"),
+                       torch.zeros(n, 64, device="cuda"), out, lse, ws)
+    assert lla.device_status(ws) == lla.LLA_OK
+    # (sequences are cut into runs at different places: the order of the sums differs, not more)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def _expect(c, q, wk, wv):
+    out, lse = np.empty((c.H, 128)), np.empty(c.H)
+    for h in range(c.H):
+        s = c.k[:, h] @ (widen(wk)[h].T @ widen(q)[h]) / math.sqrt(128)
+        m = s.max()
+        p = np.exp(s - m)
+        lse[h] = m + math.log(p.sum())
+        out[h] = widen(wv)[h] @ (p @ c.v[:, h]) / p.sum()
+    return out, lse
+
+
+def _problem(scores, H, rk, rv, seed, v_scale=0.25, v_codes=None, gain=1.0):
+    """Rows whose scores are close to `scores` [L] (log2 units) in every head, q, W_up,k and W_up,v.
+    v_scale: [L] or [L][groups] or a number."""
+    g = np.random.default_rng(seed)
+    scores = np.asarray(scores, np.float64)
+    L = len(scores)
+    q = torch.from_numpy(g.standard_normal((H, 128))).bfloat16()
+    wk = np.zeros((H, 128, rk))
+    wk[:, :, 0] = gain * np.sign(widen(q))
+    wk = torch.from_numpy(wk).bfloat16()
+    wv = torch.from_numpy(g.standard_normal((H, 128, rv)) / math.sqrt(rv)).bfloat16()
+    kc, ks = np.zeros((L, H, rk), np.int64), np.zeros((L, H, q4.groups(rk)))
+    for h in range(H):
+        unit = gain * np.abs(widen(q)[h]).sum() / math.sqrt(128) * LOG2      # score (log2) of a latent of 1
+        kc[:, h, 0] = np.where(scores < 0, -7, 7)
+        ks[:, h, 0] = np.abs(scores) / unit / 7
+    vc = g.integers(1, 8, (L, H, rv)) if v_codes is None else v_codes        # a mean that is not zero
+    vs = np.broadcast_to(np.asarray(v_scale, np.float64).reshape(-1, 1, 1) if np.ndim(v_scale) < 2 else
+                         np.asarray(v_scale, np.float64)[:, None, :], (L, H, q4.groups(rv)))
+    return Cache(kc, ks, vc, vs), q, wk, wv
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("v_scale", [2.0 ** -20, 0.1, 0.3, 0.6, 3.0, 2.0 ** 20])
+@pytest.mark.parametrize("size", [2.0 ** 22, 2.0 ** 26, 2.0 ** 30, 2.0 ** 35])
+def test_large_scores_and_any_v_scale(dtype, v_scale, size):
+    """Scores of 2^22 to 2^35: the best token's V is the result, whatever its scale."""
+    L = 300
+    g = np.random.default_rng(5)
+    for sign in (1.0, -1.0):
+        s = sign * size * (0.5 + 0.4 * g.permutation(L) / L)
+        best = int(np.argmin(np.abs(s)) if sign < 0 else np.argmax(np.abs(s)))
+        s[best] *= 1.2 if sign > 0 else 0.8
+        p = _problem(s, 3, 32, 48, 6, v_scale=v_scale, gain=2.0 ** 20)
+        got, lse = _decode(*p, dtype, 2)
+        want, wl = _expect(*p)
+        assert rel_err(got[0], want) <= TOL[dtype] and rel_err(got[1], want) <= TOL[dtype]
+        assert (np.abs(lse[0] - wl) <= TOL[dtype] * np.abs(wl)).all()
