@@ -55,6 +55,7 @@ constexpr int kWStride = 136;                    // halves between the groups of
 constexpr int kWExp = 2 * kTile;                 // bytes into it: behind the first group's weights, four exponents
 constexpr float kQ4Scale = 0.08838834764831845f * 1.4426950408889634f;   // log2(e) / sqrt(128)
 constexpr float kRaise = 8.f;                    // lazy maximum: raised when passed by 2^8
+constexpr float kBelow = 64.f;                   // V weights count down to 2^-64 of the largest
 // a record per (unit, CTA) and head: (m, l) of each epilogue warp, the reference (m, E) of each V warp, their sums
 constexpr int kRecMl = 0, kRecRef = 16, kRecAcc = 32;
 
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
         for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) one[j] = 0.f;
-      float ref_m = -INFINITY, ref_e = 0.f;
+      float ref_m = -INFINITY, ref_e = 0.f, below = 0.f;   // the sums are relative to 2^(ref_m + ref_e); the highest reference is 2^below above
       for (int t = 0; t < run.n; ++t)
         for (int hi = 0; hi < nh; ++hi, st.next(NS)) {
           if (hi != mine) continue;
@@ -621,11 +622,16 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           const uint32_t rows = sbase + P.ring + st.i * P.stage, tail = rows + kTile * rb;
 #pragma unroll 1
           for (int g = ks_first >> 1; 2 * g < ks_first + nh; ++g) {
-            // the reference of these 32 tokens' weights: the sums are rescaled when it rises
+            // The reference of these 32 tokens' weights.  The sums follow it up and down: f16 has no room for
+            // weights relative to another one, and the tokens that it leaves out may be thousands (a
+            // sink's followers).  fp32 sums of weights up to 2^8 hold the 2^64 above the reference
+            // that this may need; what lies further below the highest one is less than their last bit.
             const float r_m = __uint_as_float(lds32(tail + P.w_bytes + 4 * g)), r_e = __uint_as_float(lds32(tail + kWExp + 4 * g));
-            float gap = r_m == -INFINITY ? -INFINITY : (r_m - ref_m) + (r_e - ref_e);
-            if (gap > 0.f) {
-              const float f = exp2f(-gap);
+            if (r_m == -INFINITY) continue;   // no token has a weight (scores that are NaN: so is the sum of the weights)
+            const float gap = (ref_m - r_m) + (ref_e - r_e);
+            if (gap != 0.f) {
+              if (below + gap > kBelow) continue;
+              const float f = gap < -126.f ? 0.f : pow2(static_cast<int>(gap));
 #pragma unroll
               for (int i = 0; i < NM; ++i)
 #pragma unroll
@@ -634,10 +640,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               for (int j = 0; j < 4; ++j) one[j] *= f;
               ref_m = r_m;
               ref_e = r_e;
-              gap = 0.f;
+              below = fmaxf(below + gap, 0.f);
             }
-            // 2^gap in f16 (0 below 2^-14: such weights no longer count)
-            const __half2 f2 = bits_h2(gap >= -14.f ? static_cast<uint32_t>(static_cast<int>(gap) + 15) * 0x04000400u : 0u);
             const int ks_end = min(2 * g + 2, ks_first + nh);
 #pragma unroll 1
             for (int ks = max(2 * g, ks_first); ks < ks_end; ++ks) {
@@ -645,7 +649,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
               // (columns without a scale group repeat the last one's weights: never read from D)
               const int t0 = 16 * ks + 2 * tig;
               const uint32_t w = tail + 2 * (min(gid, RV32 - 1) * kWStride + t0), p0 = rows + t0 * rb + rk / 2;
-              const uint32_t b0 = h2_bits(__hmul2(bits_h2(lds32(w)), f2)), b1 = h2_bits(__hmul2(bits_h2(lds32(w + 16)), f2));
+              const uint32_t b0 = lds32(w), b1 = lds32(w + 16);
               const uint32_t p1 = p0 + rb, p8 = p0 + 8 * rb, p9 = p1 + 8 * rb;
               mma16816(one, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, b0, b1);
               // a pair of half-words holds four columns: two MMAs of 8 + 8 rows

@@ -111,6 +111,70 @@ def _problem(scores, H, rk, rv, seed, v_scale=0.25, v_codes=None, gain=1.0):
     return Cache(kc, ks, vc, vs), q, wk, wv
 
 
+# (r_k, r_v, H): 8, 8, 4, 2, 1 and 1 heads share a position's tile in the tensor-core kernel
+GROUPS = [(16, 32, 8), (16, 256, 8), (48, 80, 4), (96, 160, 2), (96, 160, 1), (240, 64, 1)]
+
+
+# Tolerance 2e-2 of the largest output (bf16), as for every decode.  What moves an output here: the
+# sink's score, below 14 nats, by one f16 half step of Z and of nothing else (the table is exact):
+# 14 * 2^-11 = 0.7 %; the output's own rounding 2^-9, the weights' 2^-11.
+def _check(problem, dtype="bf16", B=160, lse_tol=None):
+    got, lse = _decode(*problem, dtype, B)
+    want, wl = _expect(*problem)
+    assert np.isfinite(got).all()
+    for b in (0, B // 3, B - 1):
+        assert rel_err(got[b], want) <= TOL[dtype], (b, rel_err(got[b], want))
+        assert np.abs(lse[b] - wl).max() <= (TOL[dtype] if lse_tol is None else lse_tol)
+
+
+@pytest.mark.parametrize("rk,rv,H", GROUPS)
+@pytest.mark.parametrize("above,L", [(12.0, 2500), (16.0, 4096), (18.0, 9000), (20.0, 4096)])
+def test_sink_over_a_long_tail(rk, rv, H, above, L):
+    """Token 0 far above thousands of others, its V zero: the result is the tail's."""
+    g = np.random.default_rng(int(above) + rk)
+    s = 0.3 * g.standard_normal(L)
+    s[0] = above
+    v = np.full(L, 0.25)
+    v[0] = 0.0
+    _check(_problem(s, H, rk, rv, rk + H, v_scale=v), B=160 if H > 1 else 40)
+
+
+@pytest.mark.parametrize("rk,rv,H", GROUPS)
+def test_sink_and_scores_that_rise_later(rk, rv, H):
+    """The tail rises by eight bits after the first tile: weights far above their own warp's
+    first maximum, far below the sink's."""
+    L = 4096
+    g = np.random.default_rng(rk + H)
+    s = 12.5 + 0.2 * g.standard_normal(L)
+    s[:128] = 4.5
+    s[0] = 20.0
+    v = np.full(L, 0.25)
+    v[0] = 0.0
+    _check(_problem(s, H, rk, rv, rk + H, v_scale=v))
+
+
+@pytest.mark.parametrize("rk,rv,H", GROUPS[:1] + GROUPS[2:])
+@pytest.mark.parametrize("at", [0, 2000, 4095])
+def test_sink_anywhere(rk, rv, H, at):
+    """The far token first, in the middle, last; its V as the others'."""
+    s = 0.3 * np.random.default_rng(at).standard_normal(4096)
+    s[at] = 15.0
+    _check(_problem(s, H, rk, rv, rk + at))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_falling_scores(dtype):
+    """Every tile's scores lie ten bits below the last one's, and the other way round."""
+    L = 1500
+    for sign in (1.0, -1.0):
+        s = sign * (np.arange(L) // 128 * 10.0 - 50.0)
+        # scores reach 50 log2 = 35 nats: a Z half step moves them by 35 * 2^-11 = 0.017 each
+        p = _problem(s, 2, 32, 64, 3)
+        got, lse = _decode(*p, dtype, 9)
+        want, wl = _expect(*p)
+        assert rel_err(got[0], want) <= TOL[dtype] and np.abs(lse[0] - wl).max() <= max(TOL[dtype], 35 * 2.0 ** -20)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("v_scale", [2.0 ** -20, 0.1, 0.3, 0.6, 3.0, 2.0 ** 20])
 @pytest.mark.parametrize("size", [2.0 ** 22, 2.0 ** 26, 2.0 ** 30, 2.0 ** 35])
