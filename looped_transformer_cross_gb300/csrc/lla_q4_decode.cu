@@ -181,7 +181,8 @@ __device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, volatile 
 }
 
 // Register shares of the warpgroups: 64 + 2 x 96 + 2 x 112 = 480 = 5 x 96, what the
-// block is launched with (640 threads of 96).
+// block is launched with (640 threads of 96); up to 192 V columns 72 + 2 x 96 + 2 x 104 (at 160 the
+// producers spill with 64: 32 x 4096 takes 112 us, else 109).
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -314,7 +315,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
     }
   };
   if (warp < 4) {
-    regs_dec<64>();
+    regs_dec<RV32 <= 6 ? 72 : 64>();
     if (warp == 0) {
       // ======================================================== producer of rows
       // Per head-tile the page pieces that its rows lie in, lane i copying piece i.  A position's page ids are
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           const uint32_t gcol = tmem + lane_base + gp.i * gstep + hi * N;
           float bias[2], s = 0.f;
           tmem_ld_x2(gcol + rk, bias);
-          // ---- V scales; 2^E is above every one of the warp's tokens
+          // ---- V scales
           uint32_t vtop = 0, vs[RV32];
 #pragma unroll
           for (int g = 0; g < RV32; ++g) {
@@ -516,7 +517,6 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             if (valid) vs[g] = lds16(r + scale_at + 2 * (gk + g));   // (a row that holds no token may hold anything)
             vtop = max(vtop, vs[g] & 0x7FFFu);
           }
-          const int E = min(static_cast<int>(__reduce_max_sync(0xffffffffu, vtop >> 7)) - 126, 126);
           // ---- per scale group its codes against G: 32 columns, or 16 in a last group
           auto sum8 = [&](uint32_t w, const float* G, float& lo, float& hi) {   // columns of one code word
 #pragma unroll
@@ -576,15 +576,20 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           }
           const float p = s == -INFINITY ? 0.f : exp2f(s - m);
           state[hi * kState + lane] = l + p;
-          // ---- weights p * scale of each V group, relative to 2^(m + E)
-          // (scale / 2^E is below one and p at most 2^8: f16 holds the product; p / 2^E might not be finite)
+          // ---- weights p * scale of each V group, relative to 2^(m + E): the largest of the warp's comes to
+          // 2^7 .. 2^15, so f16 keeps all its digits down to 2^21 below it.  m + E is a multiple of 8 less 7,
+          // which makes it the same for most tiles, whichever warp they come from.
+          const float p9 = p * 0.001953125f;   // (2^-9: p is at most 2^8, the products stay finite)
+          const uint32_t wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(p9 * __uint_as_float(vtop << 16)) & 0x7FFFFFFFu);
+          const int m8 = __float2int_rz(m) & 7;   // (m past 2^31 saturates: any fixed value serves)
+          const int E = max(((static_cast<int>(wtop >> 23) - 118 + m8) & ~7) - m8 - 7, -118);
           const uint32_t out = tail + 2 * row;
-          const float ie = pow2(-E);
+          const float ie = pow2(9 - E);
 #pragma unroll
-          for (int g = 0; g < RV32; ++g) sts16(out + 2 * g * kWStride, __float2half_rn(__uint_as_float(vs[g] << 16) * ie * p));
-          // (two numbers: from 2^24 on m + E would lose E; m of -inf: none)
+          for (int g = 0; g < RV32; ++g) sts16(out + 2 * g * kWStride, __float2half_rn(p9 * __uint_as_float(vs[g] << 16) * ie));
+          // (two numbers: from 2^24 on m + E would lose E; m of -inf: no token with a weight)
           if (lane == 0) {
-            sts32(tail + P.w_bytes + 4 * q, __float_as_uint(m));
+            sts32(tail + P.w_bytes + 4 * q, __float_as_uint(wtop != 0 ? m : -INFINITY));
             sts32(tail + kWExp + 4 * q, __float_as_uint(static_cast<float>(E)));
           }
           arrive(misc->wfull[st.i]);
@@ -599,7 +604,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       __syncwarp();
     }
   } else {
-    regs_inc<112>();
+    regs_inc<RV32 <= 6 ? 104 : 112>();
     // ======================================================== V: sum_j p_j c_v,j
     const int v = warp - 12, gid = lane >> 2, tig = lane & 3;
     // a head has 8 / nh warps, each with 16 nh of a tile's tokens
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           for (int g = ks_first >> 1; 2 * g < ks_first + nh; ++g) {
             // The reference of these 32 tokens' weights.  The sums follow it up and down: f16 has no room for
             // weights relative to another one, and the tokens that it leaves out may be thousands (a
-            // sink's followers).  fp32 sums of weights up to 2^8 hold the 2^64 above the reference
+            // sink's followers).  fp32 sums of weights up to 2^15 hold the 2^64 above the reference
             // that this may need; what lies further below the highest one is less than their last bit.
             const float r_m = __uint_as_float(lds32(tail + P.w_bytes + 4 * g)), r_e = __uint_as_float(lds32(tail + kWExp + 4 * g));
             if (r_m == -INFINITY) continue;   // no token has a weight (scores that are NaN: so is the sum of the weights)
@@ -952,10 +957,11 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __gri
         for (int p = 0; p < per; ++p) {
           const float* r = rec + j * stride;
           const float2 ref = *reinterpret_cast<const float2*>(r + kRecRef + 2 * p);
-          const float f = exp2f((ref.x - m) + ref.y);
+          // (2^E alone may leave fp32's range: half of it each)
+          const float e2 = floorf(0.5f * ref.y), f = exp2f((ref.x - m) + e2), f2 = exp2f(ref.y - e2);
 #pragma unroll
           for (int k = 0; k < RV32; ++k)
-            if (32 * k + lane < rv) v[k] = fmaf(r[kRecAcc + p * rv + 32 * k + lane], f, v[k]);
+            if (32 * k + lane < rv) v[k] = fmaf(r[kRecAcc + p * rv + 32 * k + lane] * f, f2, v[k]);
         }
     }
 #pragma unroll

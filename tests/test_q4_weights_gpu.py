@@ -176,6 +176,19 @@ def test_falling_scores(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rk,rv,H", GROUPS)
+@pytest.mark.parametrize("size,below,L", [(14, 40.0, 2500), (16, 40.0, 2500), (30, 80.0, 700), (30, 80.0, 30), (60, 110.0, 40)])
+def test_v_outlier_without_weight(dtype, rk, rv, H, size, below, L):
+    """One early token with V 2^size above the others' and no weight to speak of."""
+    s = 0.3 * np.random.default_rng(size).standard_normal(L)
+    s[3] = -below
+    v = np.full(L, 0.25)
+    v[3] = 0.25 * 2.0 ** size
+    # (the outlier adds 2^(size - below) <= 2^-24 of one token's share)
+    _check(_problem(s, H, rk, rv, size, v_scale=v), dtype, B=40 if dtype == "bf16" else 2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("v_scale", [2.0 ** -20, 0.1, 0.3, 0.6, 3.0, 2.0 ** 20])
 @pytest.mark.parametrize("size", [2.0 ** 22, 2.0 ** 26, 2.0 ** 30, 2.0 ** 35])
 def test_large_scores_and_any_v_scale(dtype, v_scale, size):
@@ -191,3 +204,23 @@ def test_large_scores_and_any_v_scale(dtype, v_scale, size):
         want, wl = _expect(*p)
         assert rel_err(got[0], want) <= TOL[dtype] and rel_err(got[1], want) <= TOL[dtype]
         assert (np.abs(lse[0] - wl) <= TOL[dtype] * np.abs(wl)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [1, 2, 8])
+@pytest.mark.parametrize("L", [1, 3, 40])
+@pytest.mark.parametrize("step", [10.0, 21.0])
+def test_v_groups_of_different_size(dtype, H, L, step):
+    """Scale groups of V 2^step apart, each read by outputs of its own: every group keeps its
+    digits.  (f16 keeps 11 bits down to 2^-14, the weights' largest is 2^7 at least.)"""
+    rk, rv = 16, 64
+    g = np.random.default_rng(L + H)
+    vs = np.array([[0.3, 0.3 * 2.0 ** -step]]) * np.exp(0.3 * g.standard_normal((L, 2)))
+    c, q, wk, wv = _problem(0.5 * g.standard_normal(L), H, rk, rv, 7, v_scale=vs)
+    wv = wv.clone()
+    wv[:, :64, 32:] = 0.0                                      # outputs 0..63 of group 0, 64..127 of group 1
+    wv[:, 64:, :32] = 0.0
+    got, _ = _decode(c, q, wk, wv, dtype, 3)
+    want, _ = _expect(c, q, wk, wv)
+    for part in (slice(0, 64), slice(64, 128)):
+        assert rel_err(got[0][:, part], want[:, part]) <= TOL[dtype], part
