@@ -5,7 +5,7 @@
 // query folded into W_up,k,t (Z_n over 128 rotary coordinates) and the position's rotary row
 // R_j = (cos(j th_0..63), sin(j th_0..63)),
 //     s_j = sum_n c_j,n G_j,n + bias,   G_j = R_j Z^T        (log2 units),
-// so G of a 128-token tile is one MMA chain (M = 128 tokens, N = r_k + 16, K = 128), and the codes
+// so G of a 128-token tile is one MMA chain (M = 128 tokens, N = r_k + 16 or 32, K = 128), and the codes
 // never enter it: a token's c_n = (code - 8) scale meets G in one thread's registers.
 // A 4-bit row is 144 bytes at (96, 160), 3.6 times less than in bf16: at HBM speed an SM has about
 // 6 cycles per token-head, and what bounds the kernel is the work per code and the chain of scores,
@@ -16,8 +16,9 @@
 //      rounded once per call from the fp32 table into tiles in the layout that the MMA reads, so that a
 //      bulk copy brings a tile: an fp32 table read here would be more L2 traffic than
 //      the latents, and rows turned in registers from tile to tile took a fifth of all
-//      instructions.  B = a head's Z rows (f16), two bias rows (f16 high and low part) and one row
-//      -8 sum Z per scale group, which takes the codes' offset back.  All heads of a group
+//      instructions.  B = a head's Z rows (f16), two bias rows (f16 high and low part) and two rows
+//      -8 sum Z per scale group, which take the codes' offset back (high and low part as well: up to 256
+//      times a Z of its own, a single f16 would be off by more than all of the Z).  All heads of a group
 //      share one chain.  Both operands are formed by q4_prepare_kernel: formed here
 //      at the start of each run they stopped every role for 7 us, a seventh of the call at 32 x 4096.
 //   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
@@ -150,13 +151,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                "{%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// 32 lanes x 32 bits, one column.
-__device__ __forceinline__ void tmem_ld_x1(uint32_t taddr, float (&v)[1]) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  v[0] = __uint_as_float(r);
 }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
@@ -418,7 +412,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // ======================================================== MMA issuer
       // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
       // step takes about as long for 256 columns as for 128, so the heads of a group share one chain
-      // (r_k = 256: two chains).  Commits took this warp 570 cycles each, more than
+      // (r_k of 240 and 256: two chains).  Commits took this warp 570 cycles each, more than
       // issuing the eight MMAs, so there is one per position: of all heads' buffers and, passed on by
       // warp 3, of the rotary chunks.  (One per head and chunk bound the kernel: 122 us at 32 x 4096.)
       // A run's query operands come by two bulk copies once the last run's MMAs are done; the epilogue
@@ -535,9 +529,9 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
           const int whole = rk / kQ4Group;
 #pragma unroll 1
           for (int g = 0; g < whole; ++g) {
-            float G[32], off[1];
+            float G[32], off[2];
             tmem_ld_x32(gcol + 32 * g, G);
-            tmem_ld_x1(gcol + rk + 2 + g, off);
+            tmem_ld_x2(gcol + rk + 2 + 2 * g, off);
             const uint4 w = lds128(r + 16 * g);
             const uint32_t sc = lds16(r + scale_at + 2 * g);
             tmem_wait_ld();
@@ -546,19 +540,19 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             sum8(w.y, G + 8, lo[1], hi2[1]);
             sum8(w.z, G + 16, lo[0], hi2[0]);
             sum8(w.w, G + 24, lo[1], hi2[1]);
-            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0]);
+            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0] + off[1]);
           }
           if (whole < gk) {
-            float G[16], off[1];
+            float G[16], off[2];
             tmem_ld_x16(gcol + 32 * whole, G);
-            tmem_ld_x1(gcol + rk + 2 + whole, off);
+            tmem_ld_x2(gcol + rk + 2 + 2 * whole, off);
             const uint2 w = lds64(r + 16 * whole);
             const uint32_t sc = lds16(r + scale_at + 2 * whole);
             tmem_wait_ld();
             float lo[2] = {0.f, 0.f}, hi2[2] = {0.f, 0.f};
             sum8(w.x, G, lo[0], hi2[0]);
             sum8(w.y, G + 8, lo[1], hi2[1]);
-            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0]);
+            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0] + off[1]);
           }
           tc_fence_before();
           arrive(misc->gempty[gp.i]);
@@ -729,8 +723,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 // The operands of the decode grid's MMAs, in the layouts that they are read in.
 // Blocks below a.z_blocks: the query operands of one head and up to kQ4PrepSeqs sequences.  Per (sequence,
 // head group) two K-major chunks (cosine, then sine coordinates) of nh N rows of 128 bytes,
-// 128-byte swizzle; a head's N rows are its r_k rows Z_n, bias high and low, -8 sum Z of each scale
-// group, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
+// 128-byte swizzle; a head's N rows are its r_k rows Z_n, bias high and low, -8 sum Z high and low of each
+// scale group, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
 //     Z_n,f = sc (q'_i0 W_i0,n + q'_i1 W_i1,n),  Z_n,64+f = sc (q'_i1 W_i0,n - q'_i0 W_i1,n),
 // the bias rows the same over mu; either times a power of two that brings the largest (for Z a
 // bound of it) to 2^7, because f16 has no range to spare for queries and weights of any size.  The
@@ -844,7 +838,7 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
       top = __hmax2(top, __habs2(__half2half2(high)));
       *reinterpret_cast<__half*>(at(ms, rk, 64 * part + mf)) = high;
       *reinterpret_cast<__half*>(at(ms, rk + 1, 64 * part + mf)) = __float2half_rn(x - __half2float(high));
-      for (int row = rk + 2 + gk; row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
+      for (int row = rk + 2 + 2 * gk; row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
     }
   }
   // item = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies).  The (item,
@@ -904,11 +898,18 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
         sum_s[e] = -8.f * (sum_s[e] + __shfl_xor_sync(0xffffffffu, sum_s[e], 16));
       }
       if (lane < 8) {
-        const __half2 c0 = __floats2half2_rn(sum_c[0], sum_c[1]), c1 = __floats2half2_rn(sum_c[2], sum_c[3]);
-        const __half2 s0 = __floats2half2_rn(sum_s[0], sum_s[1]), s1 = __floats2half2_rn(sum_s[2], sum_s[3]);
-        top = __hmax2(__hmax2(top, __habs2(c0)), __hmax2(__habs2(c1), __hmax2(__habs2(s0), __habs2(s1))));
-        *reinterpret_cast<uint2*>(at(s, rk + 2 + g, f0)) = make_uint2(h2_bits(c0), h2_bits(c1));
-        *reinterpret_cast<uint2*>(at(s, rk + 2 + g, 64 + f0)) = make_uint2(h2_bits(s0), h2_bits(s1));
+        // (high and low part; row rk + 2 + 2 g and the next)
+        auto put = [&](int coord, const float (&sum)[4]) {
+          const __half2 h0 = __floats2half2_rn(sum[0], sum[1]), h1 = __floats2half2_rn(sum[2], sum[3]);
+          const float2 r0 = __half22float2(h0), r1 = __half22float2(h1);
+          top = __hmax2(top, __hmax2(__habs2(h0), __habs2(h1)));
+          *reinterpret_cast<uint2*>(at(s, rk + 2 + 2 * g, coord)) = make_uint2(h2_bits(h0), h2_bits(h1));
+          *reinterpret_cast<uint2*>(at(s, rk + 3 + 2 * g, coord)) =
+              make_uint2(h2_bits(__floats2half2_rn(sum[0] - r0.x, sum[1] - r0.y)),
+                         h2_bits(__floats2half2_rn(sum[2] - r1.x, sum[3] - r1.y)));
+        };
+        put(f0, sum_c);
+        put(64 + f0, sum_s);
       }
     }
   }
@@ -1013,11 +1014,12 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
   // their turns, so groups of several heads need room for copies ahead.  What the head-tiles leave
   // goes to rotary chunks: with few heads a position is over before the next tile has come.
   for (int nh = kMaxNh; nh >= 1; nh /= 2) {
-    if (H % nh || (nh > 1 && nh * (r_k + 16) > 256)) continue;
+    const int N = r_k + al(2 + 2 * q4_groups(r_k), 16);
+    if (H % nh || (nh > 1 && nh * N > 256)) continue;
     *p = Q4Plan{};
     p->nh = nh;
     p->ngroups = H / nh;
-    p->N = r_k + 16;
+    p->N = N;
     p->PG = std::min(kMaxG, 512 / p->N / nh);
     if (nh == 1 && p->PG > 1) p->PG -= p->PG % 2;
     p->PB = nh == 1 ? std::max(2, p->PG) : p->PG;

@@ -224,3 +224,27 @@ def test_v_groups_of_different_size(dtype, H, L, step):
     want, _ = _expect(c, q, wk, wv)
     for part in (slice(0, 64), slice(64, 128)):
         assert rel_err(got[0][:, part], want[:, part]) <= TOL[dtype], part
+
+
+@pytest.mark.parametrize("rk", [16, 32, 96, 160, 224, 240, 256])
+def test_offset_of_columns_that_share_a_sign(rk):
+    """Columns of W_up,k of one sign under codes of zero leave no trace in the score.
+
+    One token, so lse is its score: code 1 in column 0 of every scale group, 7 in a column whose
+    weights are zero, zeros elsewhere.  The score's terms have one sign and each carries one f16 half
+    step of Z, 2^-11; sums with the codes' offset are up to 256 / 1 times larger in fp32
+    (2^-23 a step): 2^-12 more covers four of them."""
+    H, rv = 4, 32
+    g = np.random.default_rng(rk)
+    q = torch.from_numpy(g.standard_normal((H, 128))).bfloat16()
+    wk = torch.from_numpy(np.sign(widen(q))[:, :, None] * (1.0 + 0.4 * g.random((H, 128, rk)))).bfloat16()
+    kc = np.zeros((1, H, rk), np.int64)
+    kc[..., 0::32] = 1
+    kc[..., 15::32] = 7
+    wk[:, :, 15::32] = 0.0
+    wv = torch.from_numpy(g.standard_normal((H, 128, rv))).bfloat16()
+    c = Cache(kc, np.full((1, H, q4.groups(rk)), 0.5), g.integers(-7, 8, (1, H, rv)), np.full((1, H, 1), 0.25))
+    got, lse = _decode(c, q, wk, wv, "bf16", 2)
+    want, wl = _expect(c, q, wk, wv)
+    assert (np.abs(lse - wl) <= np.abs(wl) * (2.0 ** -11 + 2.0 ** -12)).all(), np.abs(lse / wl - 1).max()
+    assert rel_err(got[0], want) <= TOL["bf16"]
