@@ -82,12 +82,12 @@ int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms);
 cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_q4_tile(const Q4DecodeArgs& a, cudaStream_t s);
 
-// Opt the kernel in to `smem` bytes of dynamic shared memory on the current device.
+// Opt the kernel in to `smem` bytes of dynamic shared memory on the current device, whatever the size:
+// what needs no opt-in is 48 KB less the kernel's own static part.
 // Set at every launch: the attribute belongs to a device's copy of the kernel, and a
 // process may use several.
 template <typename K>
 cudaError_t allow_smem(K* kern, size_t smem) {
-  if (smem <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
 }
 

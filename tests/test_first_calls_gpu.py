@@ -1,0 +1,76 @@
+"""Calls whose shared memory lies near the size that needs an opt-in, as the first ones of a process:
+a launch must not depend on what ran before.
+"""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+from looped_transformer_cross_gb300 import lla
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from looped_transformer_cross_gb300 import build
+    build.build()
+
+
+def _in_new_process(code):
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return r.stdout
+
+
+def fp32_decode(rk, rv, stream=None, B=2, L=40):
+    """A closure that makes one fp32 4-bit decode call; its output tensor."""
+    dm = lla.dims(1, 1, rk, rv, dtype=lla.LLA_F32)
+    g = torch.Generator(device="cuda").manual_seed(rk + rv)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    pool, ws = lla.q4_pool(dm, B, 64), lla.q4_workspace(dm, B, 64)
+    lla.q4_store(dm, rnd(B * 64, 1, rk), rnd(B * 64, 1, rv), torch.arange(B * 64, device="cuda"), pool, ws)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    args = (rnd(B, 1, 128), pool, torch.arange(B, **i32)[:, None].contiguous(), torch.full((B,), L, **i32),
+            torch.full((B,), L - 1, **i32), rnd(1, 1, 128, rk), rnd(1, 1, 128, rv), rnd(1, 128), rnd(1, 128))
+    cos, sin = lla.rope_table_scaled(lla.dims(1, 1, 16, 16), 128)
+    out = torch.empty(B, 1, 128, device="cuda")
+    torch.cuda.synchronize()
+
+    def call():
+        lla.decode_attn_q4(dm, 0, *args, cos, sin, out, None, ws, stream)
+    return call, out
+
+
+def test_fp32_decode_of_any_rank_first():
+    """Ranks around the size at which shared memory has to be asked for, smallest first."""
+    code = """
+import sys
+sys.path.insert(0, "tests")
+import torch
+from test_first_calls_gpu import fp32_decode
+ranks = sorted(((k, v) for k in range(16, 129, 16) for v in range(16, 257, 16) if k * 512 + 128 * v < 60000), key=lambda r: 512 * r[0] + 64 * r[1])
+for rk, rv in ranks:
+    call, out = fp32_decode(rk, rv)
+    call()
+    assert out.isfinite().all()
+print(len(ranks))
+"""
+    assert int(_in_new_process(code)) > 40
+
+
+@pytest.mark.parametrize("rk,rv", [(64, 128), (48, 256)])
+def test_fp32_decode_first_call(rk, rv):
+    _in_new_process("""
+import sys
+sys.path.insert(0, "tests")
+from test_first_calls_gpu import fp32_decode
+call, out = fp32_decode(%d, %d)
+call()
+assert out.isfinite().all()
+""" % (rk, rv))
