@@ -228,8 +228,8 @@ extern "C" lla_status lla_page_plan(int B, int page_size, int max_pages, int64_t
              static_cast<uint32_t*>(workspace)};
   a.per_thread = std::max(a.per_thread, 1);
   const size_t smem = static_cast<size_t>(B) * 16;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxB * 16) != cudaSuccess)
+  // (the most any call takes, at every call: what needs no opt-in is 48 KB less the kernel's static part)
+  if (cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxB * 16) != cudaSuccess)
     return LLA_ERR_CUDA;
   const int64_t per_block = static_cast<int64_t>(kPlanThreads) * a.per_thread;
   const unsigned blocks = static_cast<unsigned>(std::max<int64_t>(1, (n_tok + per_block - 1) / per_block));

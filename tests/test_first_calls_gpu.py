@@ -74,3 +74,19 @@ call, out = fp32_decode(%d, %d)
 call()
 assert out.isfinite().all()
 """ % (rk, rv))
+
+
+def test_page_plan_of_any_number_of_requests_first():
+    """Request counts around the size at which shared memory has to be asked for, in rising order."""
+    _in_new_process("""
+import torch
+from looped_transformer_cross_gb300 import lla
+for B in (3000, 3050, 3055, 3056, 3060, 3065, 3071, 3080, 4000, 8192):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = lla.PagePlan(B, B)
+    table = torch.full((B, 1), -1, **i32)
+    plan(4, B, torch.zeros(B, **i32), torch.ones(B, **i32), torch.arange(B, **i32), table)
+    assert torch.equal(plan.slots, 4 * torch.arange(B, device="cuda")), B
+    assert torch.equal(table[:, 0], torch.arange(B, **i32)) and plan.counts.tolist() == [B, B]
+    assert lla.device_status(plan.workspace) == lla.LLA_OK
+""")
