@@ -522,8 +522,9 @@ __global__ void __launch_bounds__(kF32CombineThreads) q4_f32_combine_kernel(cons
 }  // namespace
 
 cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(a.r_k) * 512 + static_cast<size_t>(kTile) * (a.row_bytes + 16);
-  cudaError_t e = allow_smem(q4_f32_kernel, smem);
+  auto bytes = [](int r_k, int row_bytes) { return static_cast<size_t>(r_k) * 512 + static_cast<size_t>(kTile) * (row_bytes + 16); };
+  const size_t smem = bytes(a.r_k, a.row_bytes);
+  cudaError_t e = allow_smem(q4_f32_kernel, bytes(kMaxRankPerHead, q4_row_bytes(kMaxRankPerHead, kMaxRankPerHead)));
   if (e != cudaSuccess) return e;
   const int64_t units = static_cast<int64_t>(a.B) * a.H;
   q4_f32_kernel<<<static_cast<unsigned>(units * a.splits), kF32Threads, smem, s>>>(a);

@@ -82,13 +82,14 @@ int64_t q4_plain_chunk(int B, int H, int64_t L_max, int sms);
 cudaError_t launch_q4_f32(const Q4DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_q4_tile(const Q4DecodeArgs& a, cudaStream_t s);
 
-// Opt the kernel in to `smem` bytes of dynamic shared memory on the current device, whatever the size:
-// what needs no opt-in is 48 KB less the kernel's own static part.
+// Opt the kernel in to `most` bytes of dynamic shared memory on the current device: the most that any
+// call takes, so that two host threads with calls of different sizes set the same; whatever
+// the size, because what needs no opt-in is 48 KB less the kernel's own static part.
 // Set at every launch: the attribute belongs to a device's copy of the kernel, and a
 // process may use several.
 template <typename K>
-cudaError_t allow_smem(K* kern, size_t smem) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+cudaError_t allow_smem(K* kern, size_t most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
 }
 
 }  // namespace lla

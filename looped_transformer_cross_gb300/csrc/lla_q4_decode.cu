@@ -994,7 +994,7 @@ __global__ void __launch_bounds__(kCombineThreads) q4_combine_kernel(const __gri
 
 template <int RV32>
 cudaError_t launch_tile(const Q4DecodeArgs& a, cudaStream_t s) {
-  cudaError_t e = allow_smem(q4_tile_kernel<RV32>, a.plan.bytes);
+  cudaError_t e = allow_smem(q4_tile_kernel<RV32>, kSmemLimit);
   if (e != cudaSuccess) return e;
   q4_prepare_kernel<<<a.z_blocks + a.rows_grid, kPrepThreads, 0, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

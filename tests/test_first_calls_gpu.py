@@ -1,9 +1,10 @@
-"""Calls whose shared memory lies near the size that needs an opt-in, as the first ones of a process:
-a launch must not depend on what ran before.
+"""Calls whose shared memory lies near the size that needs an opt-in, as the first ones of a process,
+and calls of two host threads at once: a launch must not depend on what ran before or beside it.
 """
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -90,3 +91,33 @@ for B in (3000, 3050, 3055, 3056, 3060, 3065, 3071, 3080, 4000, 8192):
     assert torch.equal(table[:, 0], torch.arange(B, **i32)) and plan.counts.tolist() == [B, B]
     assert lla.device_status(plan.workspace) == lla.LLA_OK
 """)
+
+
+def test_two_threads_with_different_ranks(monkeypatch):
+    """Three host threads call the same kernel with different shared memory at once (the C call itself,
+    which runs without Python's lock)."""
+    calls, kept, fails = [], [], []
+    ranks = ((256, 256), (112, 64), (256, 16))
+    for rk, rv in ranks:
+        stream = torch.cuda.Stream()
+        call, out = fp32_decode(rk, rv, stream)
+        kept.append(call)                                      # (and with it the tensors that the addresses belong to)
+        call()
+        torch.cuda.synchronize()
+        with monkeypatch.context() as m:
+            m.setattr(lla, "_run", lambda what, f, index, s, *args: calls.append((f, args, s, out, out.clone())))
+            call()
+    torch.cuda.synchronize()
+
+    def work(f, args, stream, out, want):
+        status = {f(*args, stream.cuda_stream) for _ in range(20000)}
+        stream.synchronize()
+        if status != {lla.LLA_OK} or not torch.equal(out, want):
+            fails.append(status)
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not fails, fails
