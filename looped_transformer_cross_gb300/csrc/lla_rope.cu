@@ -8,6 +8,8 @@
 // gradient is the inverse rotation.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <utility>
 
 #include "lla_kernels.h"
 
@@ -290,6 +292,21 @@ cudaError_t launch_apply(ApplyArgs a, int style, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Whether rows of d elements at i s + j t (i < n, j < m) keep clear of the same rows `gap` >= 0 elements on.  The
+// rows of either set keep clear of each other (checked before), so with s <= t all rows of one j lie
+// within t - d of its first, and only the two j around gap / t can come near; of these the two i.
+bool rows_apart(int64_t gap, int64_t s, int64_t n, int64_t t, int64_t m, int64_t d) {
+  if (n == 1) { s = t; n = m; m = 1; }
+  if (m > 1 && s > t) { std::swap(s, t); std::swap(n, m); }
+  const int64_t j0 = m > 1 ? std::min(gap / t, m - 1) : 0;
+  for (int64_t j = j0; j < std::min(j0 + 2, m); ++j) {
+    const int64_t r = std::abs(gap - (m > 1 ? j * t : 0)), i0 = n > 1 ? std::min(r / s, n - 1) : 0;
+    for (int64_t i = i0; i < std::min(i0 + 2, n); ++i)
+      if (std::abs(r - (n > 1 ? i * s : 0)) < d) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -365,11 +382,10 @@ lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_str
     const uintptr_t xe = xa + es * ((N - 1) * x_tok_stride + (heads - 1) * x_head_stride + d_x);
     const uintptr_t oe = oa + es * ((N - 1) * out_tok_stride + (heads - 1) * out_head_stride + d_x);
     // interleaved slices of one buffer (q and k of a fused projection) overlap as ranges but
-    // not as rows: allowed when both have the same strides and the rows lie apart
-    const bool same = x_tok_stride == out_tok_stride && x_head_stride == out_head_stride;
-    const uintptr_t gap = (xa > oa ? xa - oa : oa - xa) / es;
-    if (xa < oe && oa < xe && !(same && gap >= static_cast<uintptr_t>((heads - 1) * x_head_stride + d_x) &&
-                                gap + (heads - 1) * x_head_stride + d_x <= static_cast<uintptr_t>(x_tok_stride)))
+    // not as rows: allowed when both have the same strides and no row meets another
+    const bool same = (N == 1 || x_tok_stride == out_tok_stride) && (heads == 1 || x_head_stride == out_head_stride);
+    const int64_t gap = static_cast<int64_t>((xa > oa ? xa - oa : oa - xa) / es);
+    if (xa < oe && oa < xe && !(same && rows_apart(gap, out_tok_stride, N, out_head_stride, heads, d_x)))
       return LLA_ERR_INVALID_ARG;
   }
   ApplyArgs a{};
