@@ -329,8 +329,10 @@ typedef struct {
  * lla_rope_table_scaled — a RoPE table built on the GPU: row i gets cos and sin of
  * (pos0 + i) theta_f for f < d_head/2.  Rows have the layout of lla_rope_table (whose
  * values it equals to about 1 ulp with scaling NULL or LLA_ROPE_PLAIN), so with pos0 = 0
- * the result serves every call that takes a RoPE table.  Angles are exact products in
- * 64-bit fixed point: positions up to 2^31 lose no precision.
+ * the result serves every call that takes a RoPE table.  Angles are exact products, in
+ * 64-bit fixed point, of the position and a frequency held in fp64, so what a far position
+ * loses is the frequency's own rounding: 2^-52 of the angle at most (an fp32 half step
+ * from 2^28 radians on, 5e-7 at 2^31).
  *   scaling              host; NULL: plain
  *   rope_cos, rope_sin   device fp32 [n_pos][d_head/2], 16-byte aligned
  * Of lla_dims only rope_base and d_head (even, 2..256) are used.  pos0 and n_pos are

@@ -24,8 +24,8 @@ constexpr int kTableThreads = 256;
 constexpr int kTableRows = 16;        // rows of a thread at most
 
 // Angular steps per position in turns, as 64-bit fixed-point fractions: position p
-// sits at p * turn mod 2^64, an exact integer product, so a far position loses
-// nothing to the size of its angle (an fp32 angle would, and fp64 arithmetic is slow here).
+// sits at p * turn mod 2^64, an exact integer product, so a far position loses no more
+// than p times the rounding of its frequency in fp64 (an fp32 angle would, and fp64 arithmetic is slow here).
 struct TurnArgs {
   uint64_t turn[kMaxHalf];
   int half;
