@@ -30,7 +30,7 @@ struct Q4Plan {
   int nh, ngroups;                   // heads of a group (1, 2, 4 or 8), groups of a sequence
   int NS, NR;                        // stages of head-tiles, chunks (half tiles) of rotary rows
   int PG, PB, gstep;                 // positions with G in TMEM, their barriers, columns apart
-  int N;                             // rows of a head's query operand = columns of G: r_k + 2 (1 + scale groups), in 16s
+  int N;                             // rows of a head's query operand = columns of G: r_k + 2 (1 + scale groups of 32), in 16s
   int z, z_chunk;                    // query operands of the group's heads: two chunks of coordinates
   int rows;                          // rotary tiles
   int state, misc, ring, stage;      // softmax state of the epilogue; barriers; head-tiles

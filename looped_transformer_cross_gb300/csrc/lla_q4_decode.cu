@@ -17,8 +17,10 @@
 //      bulk copy brings a tile: an fp32 table read here would be more L2 traffic than
 //      the latents, and rows turned in registers from tile to tile took a fifth of all
 //      instructions.  B = a head's Z rows (f16), two bias rows (f16 high and low part) and two rows
-//      -8 sum Z per scale group, which take the codes' offset back (high and low part as well: up to 256
-//      times a Z of its own, a single f16 would be off by more than all of the Z).  All heads of a group
+//      -8 sum Z per scale group of 32, which take the codes' offset back (high and low part as well: up to 256
+//      times a Z of its own, a single f16 would be off by more than all of the Z).  A last group of 16 has
+//      none: its codes lose their offset in f16 (so r_k = 240 stays at one MMA chain: 161 us at 32 x 4096
+//      of 15 heads and r_v = 112, with rows for it and two chains 236).  All heads of a group
 //      share one chain.  Both operands are formed by q4_prepare_kernel: formed here
 //      at the start of each run they stopped every role for 7 us, a seventh of the call at 32 x 4096.
 //   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
@@ -37,6 +39,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
+#include <type_traits>
 
 #include "lla_q4.h"
 
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // ======================================================== MMA issuer
       // G = R Z^T; the whole warp runs the loop, one elected lane issues.  With A in shared memory a
       // step takes about as long for 256 columns as for 128, so the heads of a group share one chain
-      // (r_k of 240 and 256: two chains).  Commits took this warp 570 cycles each, more than
+      // (r_k = 256: two chains).  Commits took this warp 570 cycles each, more than
       // issuing the eight MMAs, so there is one per position: of all heads' buffers and, passed on by
       // warp 3, of the rotary chunks.  (One per head and chunk bound the kernel: 122 us at 32 x 4096.)
       // A run's query operands come by two bulk copies once the last run's MMAs are done; the epilogue
@@ -512,10 +515,15 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             vtop = max(vtop, vs[g] & 0x7FFFu);
           }
           // ---- per scale group its codes against G: 32 columns, or 16 in a last group
-          auto sum8 = [&](uint32_t w, const float* G, float& lo, float& hi) {   // columns of one code word
+          auto sum8 = [&](uint32_t w, const float* G, float& lo, float& hi, auto centred) {   // columns of one code word
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float2 c = __half22float2(bits_h2(w & 0x000F000Fu)), d = __half22float2(bits_h2(w & 0x00F000F0u));
+              __half2 x = bits_h2(w & 0x000F000Fu), y = bits_h2(w & 0x00F000F0u);
+              if constexpr (centred.value) {   // (code + 8) - 8, exact
+                x = __hsub2(x, bits_h2(0x00080008u));
+                y = __hsub2(y, bits_h2(0x00800080u));
+              }
+              const float2 c = __half22float2(x), d = __half22float2(y);
               w >>= 8;
               lo = fmaf(c.x, G[4 * j], lo);
               lo = fmaf(c.y, G[4 * j + 1], lo);
@@ -536,23 +544,22 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
             const uint32_t sc = lds16(r + scale_at + 2 * g);
             tmem_wait_ld();
             float lo[2] = {0.f, 0.f}, hi2[2] = {0.f, 0.f};
-            sum8(w.x, G, lo[0], hi2[0]);
-            sum8(w.y, G + 8, lo[1], hi2[1]);
-            sum8(w.z, G + 16, lo[0], hi2[0]);
-            sum8(w.w, G + 24, lo[1], hi2[1]);
+            sum8(w.x, G, lo[0], hi2[0], std::false_type{});
+            sum8(w.y, G + 8, lo[1], hi2[1], std::false_type{});
+            sum8(w.z, G + 16, lo[0], hi2[0], std::false_type{});
+            sum8(w.w, G + 24, lo[1], hi2[1], std::false_type{});
             scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0] + off[1]);
           }
           if (whole < gk) {
-            float G[16], off[2];
+            float G[16];
             tmem_ld_x16(gcol + 32 * whole, G);
-            tmem_ld_x2(gcol + rk + 2 + 2 * whole, off);
             const uint2 w = lds64(r + 16 * whole);
             const uint32_t sc = lds16(r + scale_at + 2 * whole);
             tmem_wait_ld();
             float lo[2] = {0.f, 0.f}, hi2[2] = {0.f, 0.f};
-            sum8(w.x, G, lo[0], hi2[0]);
-            sum8(w.y, G + 8, lo[1], hi2[1]);
-            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], off[0] + off[1]);
+            sum8(w.x, G, lo[0], hi2[0], std::true_type{});
+            sum8(w.y, G + 8, lo[1], hi2[1], std::true_type{});
+            scaled(sc, lo[0] + lo[1], hi2[0] + hi2[1], 0.f);
           }
           tc_fence_before();
           arrive(misc->gempty[gp.i]);
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
 // Blocks below a.z_blocks: the query operands of one head and up to kQ4PrepSeqs sequences.  Per (sequence,
 // head group) two K-major chunks (cosine, then sine coordinates) of nh N rows of 128 bytes,
 // 128-byte swizzle; a head's N rows are its r_k rows Z_n, bias high and low, -8 sum Z high and low of each
-// scale group, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
+// scale group of 32, zeros.  With q' = RoPE(q, q_pos) and the frequency pair (i0, i1) of f:
 //     Z_n,f = sc (q'_i0 W_i0,n + q'_i1 W_i1,n),  Z_n,64+f = sc (q'_i1 W_i0,n - q'_i0 W_i1,n),
 // the bias rows the same over mu; either times a power of two that brings the largest (for Z a
 // bound of it) to 2^7, because f16 has no range to spare for queries and weights of any size.  The
@@ -838,7 +845,7 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
       top = __hmax2(top, __habs2(__half2half2(high)));
       *reinterpret_cast<__half*>(at(ms, rk, 64 * part + mf)) = high;
       *reinterpret_cast<__half*>(at(ms, rk + 1, 64 * part + mf)) = __float2half_rn(x - __half2float(high));
-      for (int row = rk + 2 + 2 * gk; row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
+      for (int row = rk + 2 + 2 * (rk / kQ4Group); row < N; ++row) *reinterpret_cast<__half*>(at(ms, row, 64 * part + mf)) = __ushort_as_half(0);
     }
   }
   // item = (scale group, half of the frequencies); lane = (8 columns, 4 frequencies).  The (item,
@@ -889,7 +896,8 @@ __global__ void __launch_bounds__(kPrepThreads) q4_prepare_kernel(const __grid_c
           *reinterpret_cast<uint2*>(z + P.z_chunk) = make_uint2(h2_bits(s0), h2_bits(s1));
         }
       }
-      // the codes' offset: -8 sum Z over the scale group's columns
+      // the codes' offset: -8 sum Z over the scale group's columns (groups of 32)
+      if (32 * g + 32 > rk) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         sum_c[e] += __shfl_xor_sync(0xffffffffu, sum_c[e], 8);
@@ -1014,7 +1022,7 @@ bool make_q4_plan(int H, int r_k, int r_v, Q4Plan* p) {
   // their turns, so groups of several heads need room for copies ahead.  What the head-tiles leave
   // goes to rotary chunks: with few heads a position is over before the next tile has come.
   for (int nh = kMaxNh; nh >= 1; nh /= 2) {
-    const int N = r_k + al(2 + 2 * q4_groups(r_k), 16);
+    const int N = r_k + al(2 + 2 * (r_k / kQ4Group), 16);
     if (H % nh || (nh > 1 && nh * N > 256)) continue;
     *p = Q4Plan{};
     p->nh = nh;
