@@ -171,18 +171,6 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// x is read once: evicted first, so that L2 keeps what was written (82 -> 77 us of the
-// gradient of 32768 x 16 vectors of 192).
-template <typename V>
-__device__ __forceinline__ V load_once(const void* p) {
-  if constexpr (sizeof(V) == 16) {
-    const uint4 x = __ldcs(static_cast<const uint4*>(p));
-    return *reinterpret_cast<const V*>(&x);
-  } else {
-    return *static_cast<const V*>(p);
-  }
-}
-
 // One item = VEC rotation pairs of a token-head (two 16-byte loads and stores where
 // VEC * sizeof(T) == 16), or VEC elements outside the rotated part, copied when the call
 // is not in place.  Interleaved pairs lie within 16 bytes: there an item is one such vector, rotated or
@@ -191,7 +179,7 @@ __device__ __forceinline__ V load_once(const void* p) {
 // under way before the first is used.  (One item a thread, with its divisions and
 // addresses, took 177 instructions per warp and was bound by issuing them; rotated and copied
 // items in one warp take turns: 32768 x 16 vectors of 192, last 64 in half layout: 182 us, in blocks
-// of their own and with 64 registers a thread 75.)  HBM-bound:
+// of their own and with 64 registers a thread 70.  An evict-first hint on the loads: 74.)  HBM-bound:
 // each element is read and written once.  fp32 arithmetic, one rounding to the storage type.
 template <typename T, int VEC, int kStyle>
 __global__ void __launch_bounds__(kApplyThreads, 8) rope_apply_kernel(const __grid_constant__ ApplyArgs a) {
@@ -242,7 +230,7 @@ __global__ void __launch_bounds__(kApplyThreads, 8) rope_apply_kernel(const __gr
       V u[kCopyHeads];
 #pragma unroll
       for (int k = 0; k < kCopyHeads; ++k)
-        if (h + k * strips < a.heads) u[k] = load_once<V>(x + k * x_step);
+        if (h + k * strips < a.heads) u[k] = *reinterpret_cast<const V*>(x + k * x_step);
 #pragma unroll
       for (int k = 0; k < kCopyHeads; ++k)
         if (h + k * strips < a.heads) *reinterpret_cast<V*>(out + k * out_step) = u[k];
@@ -254,8 +242,8 @@ __global__ void __launch_bounds__(kApplyThreads, 8) rope_apply_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       if (h + k * strips >= a.heads) continue;
-      u[k] = load_once<V>(x + k * x_step);
-      if (!kWhole && f >= 0) w[k] = load_once<V>(x + k * x_step + (i1 - i0));
+      u[k] = *reinterpret_cast<const V*>(x + k * x_step);
+      if (!kWhole && f >= 0) w[k] = *reinterpret_cast<const V*>(x + k * x_step + (i1 - i0));
     }
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
