@@ -455,7 +455,13 @@ lla_status lla_q4_load(const lla_dims* dims, const int64_t* slots, int N, const 
  * lla_q4_workspace_size() bytes (L_max = max_pages * page_size), the first 256 zero.  A row
  * with a NaN scale makes its sequence-head's result NaN.  bf16 storage: scores carry one f16
  * rounding of the folded query and one of the table's rows (|cos|, |sin| below 65504), weights one of
- * p * scale; sums are fp32.  fp32 storage: fp32 throughout.
+ * p * scale (11 bits down to 2^-21 of the largest p * scale among 32 tokens, one bit fewer per power of
+ * two below); sums are fp32 and leave out what lies 2^64 below the largest.  fp32 storage: fp32 throughout.
+ * An attention factor f that a scaling puts on rotated queries and keys: rows of a table multiplied by
+ * f, which the query and the keys both take (scores times f^2).
+ * lla_encode writes latents in the storage dtype only (lla_q4_store rounds them).  The decoupled and
+ * eviction calls do not take a 4-bit cache; lla_window_attn merges into an fp32 `out`, which this call
+ * writes in fp32 storage.
  */
 size_t lla_q4_workspace_size(const lla_dims* dims, int B, int64_t L_max);
 lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, const lla_q4_cache* cache,

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kQ4Threads) q4_load_kernel(const __grid_consta
 // folded query in fp32.  A warp has eight of a tile's tokens, a thread four of them and eight of
 // the 128 rotary coordinates (cosine and sine of four frequencies): two 16-byte reads of the
 // folded query serve 32 multiply-adds.  (With 32 coordinates of one token a thread needed
-// eight, and those reads bound the kernel: 34 us for 3 x 333 tokens of 2 heads, now 23.)  One online softmax over
+// eight, and those reads bound the kernel: 34 us for 3 x 333 tokens of 2 heads, 24.5 as here.)  One online softmax over
 // the split's tiles, the value path absorbed; a record per split, merged by the combine.
 constexpr int kF32Threads = 512;
 constexpr int kParts = 4;             // threads that fetch a token's row
@@ -722,7 +722,8 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
     a.z_blocks = a.H * ((a.B + kQ4PrepSeqs - 1) / kQ4PrepSeqs);
     a.rows_grid = static_cast<int>(std::min<int64_t>((L_max + 15) / 16, 8 * sms));
     // sequences per combine block: W_up,v is read once for them while there are two blocks per SM (up to
-    // four: 128 x 4096 at (16, 32) takes 158 us, with seven 161)
+    // four: 128 x 4096 at (16, 32) takes 150 us, with one 152, with seven 153; 64 x 1000 at (96, 160)
+    // 70, with one 81)
     a.combine_units = static_cast<int>(std::min<int64_t>(kQ4CombineUnits, (static_cast<int64_t>(a.B) * a.H + 2 * sms - 1) / (2 * sms)));
     return launch_q4_tile(a, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
   }

@@ -10,8 +10,8 @@
 // A 4-bit row is 144 bytes at (96, 160), 3.6 times less than in bf16: at HBM speed an SM has about
 // 6 cycles per token-head, and what bounds the kernel is the work per code and the chain of scores,
 // softmax and weights in the epilogue warps; the choices below are for few instructions per code.
-// 32 x 4096 tokens of 16 heads at (96, 160) take 106 us (43 for the bytes), 128 x 2048..4096 at
-// (16, 32) 144 (31).
+// 32 x 4096 tokens of 16 heads at (96, 160) take 109 us (43 for the bytes), 128 x 2048..4096 at
+// (16, 32) 150 (31).
 //   G  A = the rotary rows, f16, one 32 KB tile per position for all of its heads.  They are
 //      rounded once per call from the fp32 table into tiles in the layout that the MMA reads, so that a
 //      bulk copy brings a tile: an fp32 table read here would be more L2 traffic than
@@ -22,7 +22,7 @@
 //      none: its codes lose their offset in f16 (so r_k = 240 stays at one MMA chain: 161 us at 32 x 4096
 //      of 15 heads and r_v = 112, with rows for it and two chains 236).  All heads of a group
 //      share one chain.  Both operands are formed by q4_prepare_kernel: formed here
-//      at the start of each run they stopped every role for 7 us, a seventh of the call at 32 x 4096.
+//      at the start of each run they stopped every role for 7 us.
 //   s  One token per thread, two warpgroups alternate head-tiles.  Codes are masked into f16
 //      subnormals (code * 2^-24, or * 2^-20 from the next nibble), converted, and summed per
 //      scale group in fp32; the group's scale multiplies the sum.
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kQ4TileThreads, 1) q4_tile_kernel(const __grid
       // step takes about as long for 256 columns as for 128, so the heads of a group share one chain
       // (r_k = 256: two chains).  Commits took this warp 570 cycles each, more than
       // issuing the eight MMAs, so there is one per position: of all heads' buffers and, passed on by
-      // warp 3, of the rotary chunks.  (One per head and chunk bound the kernel: 122 us at 32 x 4096.)
+      // warp 3, of the rotary chunks.  (One per head and chunk bound the kernel: 122 us at 32 x 4096, one per
+      // position 106.)
       // A run's query operands come by two bulk copies once the last run's MMAs are done; the epilogue
       // still has up to PG positions of that run to go.
       Slot rs{0, 0u}, gp{0, 0u};
