@@ -360,7 +360,8 @@ lla_status lla_rope_table_scaled(const lla_dims* dims, const lla_rope_scaling* s
  * out == x with the same strides rotates in place (only the rotated part is written);
  * other overlaps return LLA_ERR_INVALID_ARG, but two slices of one buffer with equal strides
  * whose rows lie apart (q and k next to each other per token, per head or head-major) are no
- * overlap.  Rows of `out` must not overlap each other.  Arithmetic in fp32, rounded once.  Of lla_dims only dtype and rope_style are used.
+ * overlap.  Rows of `out` must not overlap each other.  Arithmetic in fp32, rounded once.
+ * Of lla_dims only dtype and rope_style are used.
  */
 lla_status lla_rope_apply(const lla_dims* dims, const void* x, int64_t x_tok_stride, int64_t x_head_stride,
                           void* out, int64_t out_tok_stride, int64_t out_head_stride, int N, int heads,
