@@ -472,6 +472,147 @@ lla_status lla_decode_attn_q4(const lla_dims* dims, int loop_t, const void* q, c
                               const float* rope_cos, const float* rope_sin, int64_t rope_len,
                               void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * A step that verifies drafted tokens (speculative decoding).  Every sequence brings a
+ * tree of drafted tokens, its nodes; all of them go through the model in one step, each
+ * attending to the cached tokens and to the nodes on its own path (itself and its
+ * ancestors).  lla_tree_attn is that attention, lla_logits_adjust prepares each node's
+ * logits and names its best token, lla_tree_accept walks down the tree along the chosen
+ * tokens and says which nodes stay and where lla_encode writes them.
+ *
+ * lla_tree — the nodes of B sequences, packed in sequence order: those of sequence b are
+ * the token entries tok_start[b] .. tok_start[b+1]-1.  A sequence may have none; entries
+ * from tok_start[B] on are padding, and no output of theirs is written.
+ *   n_tok       entries of the arrays that have one per token
+ *   max_nodes   most nodes of a sequence, 1..LLA_TREE_MAX_NODES
+ *   tok_start   device int32 [B+1]   as made by lla_page_plan; a sequence whose entries are
+ *                                    not 0 <= start <= end <= n_tok with at most max_nodes
+ *                                    between counts as one without nodes
+ *   parent      device int32 [n_tok] the parent's index among the sequence's nodes, below
+ *                                    the node's own; -1 for a root (anything else counts
+ *                                    as -1).  A chain has parent i-1.
+ *   pos         device int32 [n_tok] positions of the nodes, as a rule cached tokens + depth
+ *                                    (lla_tree_attn only; else it may be NULL); outside
+ *                                    [0, rope_len) is clamped
+ * Everything that "counts as" something else or is clamped records LLA_ERR_DEVICE_ARG.
+ */
+#define LLA_TREE_MAX_NODES 128
+
+typedef struct {
+    int B;
+    int n_tok;
+    int max_nodes;
+    const int32_t* tok_start;
+    const int32_t* parent;
+    const int32_t* pos;
+} lla_tree;
+
+/*
+ * lla_tree_attn / lla_tree_attn_paged — one layer, one loop t, all heads: attention of every
+ * node i over its sequence's L = seq_lens[b] cached tokens, whose keys and values are
+ * reconstructed from their latents as in lla_decode_attn, and over the exact keys and values
+ * of the nodes on its path:
+ *     s_j = RoPE(q_i, pos_i) . RoPE(k_j, j) / sqrt(d)       k_j of Eq. (3), j < L
+ *     s_a = RoPE(q_i, pos_i) . RoPE(k_a, pos_a) / sqrt(d)   a on the path of i
+ *     out = softmax over both, times v_j and v_a;  lse = ln of the sum of exponentials
+ * A node sees itself, so L = 0 is an ordinary case.  Drafted tokens are not in the cache:
+ * once they are accepted, lla_encode writes their latents.
+ *   q, k, v   device  [n_tok][H][d] of loop t, before RoPE, storage dtype: element (n, h, e)
+ *                     at n*stride + h*d + e (strides in elements, multiples of 16 bytes of
+ *                     at least H*d: slices of one fused projection are taken as they are)
+ *   out       device  [n_tok][H][d] in the storage dtype, rounded once; no input may overlap it
+ *   lse       device  fp32 [n_tok][H] or NULL
+ *   workspace device  >= lla_tree_workspace_size() bytes (L_max: that of the cache, or
+ *                     max_pages * page_size), the first 256 zero
+ * cache.B is the tree's B.  seq_lens, w_up, mu, rope tables and the paged cache as for
+ * lla_decode_attn and lla_decode_attn_paged; rope_len >= max(L_max, 128) and past every pos.
+ * bf16 storage, shapes and pages that lla_tree_kernel names "tensor": fp32 sums; keys (after
+ * their rotation), queries (after rotation and scale) and weights are rounded to bf16 for the
+ * matrix instructions, as exact attention over a bf16 cache of keys does, and the table's rows
+ * have to be those of a plain rotation, cos and sin of j theta_f (rows of any scaling; no factor
+ * on them).  Otherwise ("plain") fp32 arithmetic throughout.  LLA_ERR_UNSUPPORTED: LLA-2D.
+ */
+size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max);
+lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, lla_cache cache,
+                         const int32_t* seq_lens, const void* w_up_k, const void* w_up_v, const float* mu_k,
+                         const float* mu_v, const float* rope_cos, const float* rope_sin, int64_t rope_len,
+                         void* out, float* lse, void* workspace, size_t ws_bytes, void* stream);
+lla_status lla_tree_attn_paged(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               lla_paged_cache cache, const int32_t* seq_lens, const void* w_up_k,
+                               const void* w_up_v, const float* mu_k, const float* mu_v, const float* rope_cos,
+                               const float* rope_sin, int64_t rope_len, void* out, float* lse, void* workspace,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * lla_logits_adjust — penalties, biases and grammar masks on the logits of every node, and
+ * each row's best token and log-sum-exp.  Row n holds what the model predicts after node n of
+ * request b; its context is the request's history and the tokens of the nodes on n's path
+ * (itself among them; a step without drafting has one node a request, its newest token).  With
+ * c = occurrences of the token in the output part of the history (from prompt_len on) and on
+ * the path, and seen = c > 0 or it occurs in the prompt part, in fp32, each step rounded:
+ *     x = seen ? (x > 0 ? x / repetition : x * repetition) : x
+ *     x = x - frequency * c;  x = x - presence if c > 0;  x = x + bias
+ *     x = -inf unless the row's mask allows the token
+ *     best = the lowest index of the largest x (a NaN is never the largest; -1 if no x is above
+ *     -inf),  lse = ln sum exp(x) (-inf if nothing is allowed)
+ *   token       device int32 [n_tok]   token of each node
+ *   logits      device [n_tok] rows of `vocab` elements, row n at n*row_stride elements; dtype
+ *                                      LLA_BF16 or LLA_F32, aligned to an element
+ *   out         the same layout with out_stride, rounded once; out == logits with equal strides
+ *               is in place, any other overlap LLA_ERR_INVALID_ARG; NULL: not written
+ *   best        device int32 [n_tok] or NULL: from x before `out` rounds it
+ *   lse         device fp32 [n_tok] or NULL; at least one of out, best, lse
+ *   workspace   device, >= lla_logits_workspace_size() bytes, the first 256 zero
+ * Tokens outside [0, vocab) count nowhere and record LLA_ERR_DEVICE_ARG.
+ */
+typedef struct {
+    const int32_t* history;     /* device [B][max_history]: tokens, prompt then output           */
+    const int32_t* hist_len;    /* device [B], 0..max_history (clamped, flagged)                  */
+    const int32_t* prompt_len;  /* device [B], 0..hist_len (clamped, flagged); NULL: 0            */
+    int max_history;            /* 0: no history (the three above may be NULL)                    */
+    const float* repetition;    /* device [B]; NULL: 1                                            */
+    const float* presence;      /* device [B]; NULL: 0                                            */
+    const float* frequency;     /* device [B]; NULL: 0                                            */
+    const int32_t* bias_token;  /* device [B][max_bias]: a negative entry is unused; a token      */
+    const float* bias;          /*        listed more than once gets the sum, in list order       */
+    int max_bias;               /* 0: no biases                                                   */
+    const uint32_t* allowed;    /* device [n_masks][ceil(vocab/32)]: bit v%32 of word v/32        */
+    const int32_t* allowed_row; /* device [n_tok]: the row's mask, negative: none (beyond         */
+    int n_masks;                /* n_masks: none, flagged).  n_masks 0: no masks                  */
+} lla_logit_rules;
+
+size_t lla_logits_workspace_size(int n_tok, int vocab);
+lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dtype, const void* logits,
+                             int64_t row_stride, int vocab, const lla_logit_rules* rules, void* out,
+                             int64_t out_stride, int32_t* best, float* lse, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * lla_tree_accept — which drafted tokens stay.  Node 0 of a sequence is accepted (it is the
+ * token that the step before chose); from an accepted node the walk goes on to its lowest child
+ * whose token is the one chosen after that node, until there is none.
+ *   token, chosen  device int32 [n_tok]  token of each node; token that the model chose after it
+ *                                        (lla_logits_adjust's best, or a sample)
+ *   ctx_lens       device int32 [B]      cached tokens of each sequence
+ *   count          device int32 [B]      out: accepted nodes (0 for a sequence without nodes)
+ *   next_token     device int32 [B]      out: the token chosen after the last of them (-1 likewise)
+ *   seq_lens       device int32 [B]      out: ctx_lens + count
+ *   path           device int32 [n_tok]  out: entries of the accepted nodes in path order, from
+ *                                        each sequence's first entry on, then -1
+ *   seq_idx, pos   device int32 [n_tok]  out: as lla_encode takes them: accepted nodes go to slots
+ *                                        ctx_lens .. seq_lens-1 in path order, the others behind
+ *                                        them in node order (every entry has a slot of its own; what
+ *                                        lies behind seq_lens is overwritten by the next step)
+ *   workspace      device, >= 256 bytes: the status word
+ * A negative ctx_lens counts as 0 and records LLA_ERR_DEVICE_ARG.  No output may overlap an input.
+ */
+lla_status lla_tree_accept(const lla_tree* tree, const int32_t* token, const int32_t* chosen,
+                           const int32_t* ctx_lens, int32_t* count, int32_t* next_token, int32_t* seq_lens,
+                           int32_t* path, int32_t* seq_idx, int32_t* pos, void* workspace, size_t ws_bytes,
+                           void* stream);
+
 /* Size of the fixed scratch array behind lla_decode_attn_noalloc (64 MiB). */
 #define LLA_NOALLOC_SCRATCH_BYTES (64u << 20)
 
@@ -526,6 +667,13 @@ const char* lla_decode_kernel(const lla_dims* dims);
  * tiles over (sequence, head), the same tensor-core score, V read from L2), or
  * NULL for invalid or unsupported dims (LLA_2D, d_rope != 64, larger ranks). */
 const char* lla_decoupled_kernel(const lla_dims* dims, int d_rope);
+
+/* Name of the kernel family lla_tree_attn (page_size 0) or lla_tree_attn_paged runs for
+ * `dims` (host-only, no launch): "tensor" (LLA_BF16 whose operands fit in shared memory, dense or
+ * with pages of a multiple of 128 tokens or of 8, 16, 32 or 64), "plain" (LLA_F32, larger
+ * ranks, other page sizes: fp32 arithmetic, not tuned for bf16), or NULL for invalid or
+ * unsupported dims (LLA_2D). */
+const char* lla_tree_kernel(const lla_dims* dims, int page_size);
 
 /* Workspace bytes for calls with at most B sequences of L_max slots and
  * encode batches of at most max_N tokens, on the current CUDA device.

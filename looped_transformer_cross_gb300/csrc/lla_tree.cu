@@ -1,0 +1,494 @@
+// lla_tree.cu — attention of drafted tokens over a latent cache (lla_tree_attn): entry points,
+// the plain kernel (fp32 arithmetic, either storage type) and the finish kernel.
+//
+// A node's softmax runs over the cached tokens, whose keys are reconstructed from their
+// latents, and over the nodes on its path, whose keys are exact.  The first part is split along
+// the cache; each split leaves, per node, its running maximum m, sum l and latent sum
+// acc = sum_j 2^(s_j - m) c_v,j, because sum_j p_j (W c_j + mu) = W (sum_j p_j c_j) + mu sum_j p_j:
+// V is never reconstructed per token.  The finish kernel merges the splits, adds the path's
+// part and applies W_up,v once per node.
+#include <algorithm>
+#include <cmath>
+
+#include "lla_tree.h"
+
+namespace lla {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
+constexpr int kPlainThreads = 256;
+constexpr int kKeyStride = kHeadDim + 4;            // floats between rows of keys and queries in shared memory
+constexpr int kFinishThreads = 128;
+constexpr int kFinishRows = 8;                      // nodes of a finish block
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float x, float* p) { *p = x; }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16* p) { *p = __float2bfloat16_rn(x); }
+
+// Four consecutive elements (aligned to four) as floats.
+__device__ __forceinline__ float4 ld4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+// First and second member of frequency pair f.
+__device__ __forceinline__ int pair0(int style, int f) { return style == 0 ? f : 2 * f; }
+__device__ __forceinline__ int pair1(int style, int f) { return style == 0 ? f + 64 : 2 * f + 1; }
+
+__device__ __forceinline__ int64_t node_pos(const TreeArgs& a, int entry, bool flag) {
+  const int p = __ldg(a.pos + entry);
+  if (p >= 0 && p < a.rope_len) return p;
+  if (flag) record_status(a.status, LLA_ERR_DEVICE_ARG);
+  return p < 0 ? 0 : a.rope_len - 1;
+}
+
+// Block = (unit, split of the cache) x 32 nodes.  32 tokens at a time: their K latents in
+// shared memory, keys by a thread per (dimension, 16 tokens), rotated in place, then eight
+// threads a node take its scores, its softmax and r_v / 8 columns of its latent sum each.
+// Bound by its multiply-adds (2 * 128 * r_k a token for the keys, repeated for every 32 nodes).
+template <typename T>
+__global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_constant__ TreeArgs a) {
+  extern __shared__ float4 sh4[];
+  float* qs = reinterpret_cast<float*>(sh4);                    // [32][kKeyStride]
+  float* ks = qs + kTreePlainRows * kKeyStride;                 // [32][kKeyStride]
+  float* cs = ks + kTreePlainTile * kKeyStride;                 // [32][r_k]
+  float* vs = cs + kTreePlainTile * a.r_k;                      // [32][r_v]
+  float* ps = vs + kTreePlainTile * a.r_v;                      // [32][33]
+  const int tid = threadIdx.x;
+  const int64_t unit = blockIdx.x / a.splits;
+  const int split = static_cast<int>(blockIdx.x - unit * a.splits);
+  const int b = static_cast<int>(unit / a.H), h = static_cast<int>(unit - static_cast<int64_t>(b) * a.H);
+  const int row0 = blockIdx.y * kTreePlainRows;
+  int first;
+  const int n = tree_nodes(a, b, first, false);
+  const int L = tree_cached(a, b, false);
+  const int64_t j0 = split * a.chunk, j1 = min(static_cast<int64_t>(L), j0 + a.chunk);
+  if (row0 >= n || j0 >= j1) return;
+  const int rows = min(kTreePlainRows, n - row0);
+
+  // ---- queries: rotated, scaled to log2 units; rows past the last node are zeros
+  for (int i = tid; i < kTreePlainRows * 64; i += kPlainThreads) {
+    const int r = i >> 6, f = i & 63;
+    float y0 = 0.f, y1 = 0.f;
+    if (r < rows) {
+      const int entry = first + row0 + r;
+      const T* qv = static_cast<const T*>(a.q) + entry * a.q_stride + h * kHeadDim;
+      const int64_t p = node_pos(a, entry, false);
+      const float c = __ldg(a.rope_cos + p * 64 + f), s = __ldg(a.rope_sin + p * 64 + f);
+      const float x0 = to_f(qv[pair0(a.rope_style, f)]), x1 = to_f(qv[pair1(a.rope_style, f)]);
+      const float sc = kLog2e * kInvSqrtD;
+      y0 = (x0 * c - x1 * s) * sc;
+      y1 = (x0 * s + x1 * c) * sc;
+    }
+    qs[r * kKeyStride + f] = y0;          // pairs (f, f + 64), like the keys below
+    qs[r * kKeyStride + 64 + f] = y1;
+  }
+
+  const int row = tid >> 3, part = tid & 7;     // eight threads a node
+  const int nv = a.r_v >> 3;                    // columns of its latent sum a thread keeps
+  float acc[kMaxRankPerHead / 8];
+#pragma unroll
+  for (int i = 0; i < kMaxRankPerHead / 8; ++i) acc[i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const T* W = static_cast<const T*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * a.r_k;
+  const int e = tid & 127, half = tid >> 7;     // key dimension and token half of a thread
+  // dimension e of the paired layout is dimension src of W and mu
+  const int src = e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64);
+  const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
+
+  for (int64_t t0 = j0; t0 < j1; t0 += kTreePlainTile) {
+    const int cnt = static_cast<int>(min(static_cast<int64_t>(kTreePlainTile), j1 - t0));
+    __syncthreads();
+    // ---- latents of the tile; zeros past its last token
+    const int gk = a.r_k >> 2, gv = a.r_v >> 2, g = gk + gv;
+    for (int i = tid; i < kTreePlainTile * g; i += kPlainThreads) {
+      const int t = i / g, c = i - t * g;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < cnt) {
+        const int64_t at = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, t0 + t, a.status);
+        x = c < gk ? ld4(static_cast<const T*>(a.cache_k) + at * a.r_k + 4 * c)
+                   : ld4(static_cast<const T*>(a.cache_v) + at * a.r_v + 4 * (c - gk));
+      }
+      *reinterpret_cast<float4*>(c < gk ? cs + t * a.r_k + 4 * c : vs + t * a.r_v + 4 * (c - gk)) = x;
+    }
+    __syncthreads();
+    // ---- keys before rotation
+    float k[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) k[t] = mu;
+    for (int r = 0; r < a.r_k; r += 4) {
+      const float4 w = ld4(W + static_cast<int64_t>(src) * a.r_k + r);
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + (16 * half + t) * a.r_k + r);
+        k[t] = fmaf(w.x, c.x, fmaf(w.y, c.y, fmaf(w.z, c.z, fmaf(w.w, c.w, k[t]))));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 16; ++t) ks[(16 * half + t) * kKeyStride + e] = k[t];
+    __syncthreads();
+    // ---- rotation by each token's row of the table
+    for (int i = tid; i < kTreePlainTile * 64; i += kPlainThreads) {
+      const int t = i >> 6, f = i & 63;
+      if (t < cnt) {
+        const float c = __ldg(a.rope_cos + (t0 + t) * 64 + f), s = __ldg(a.rope_sin + (t0 + t) * 64 + f);
+        const float x0 = ks[t * kKeyStride + f], x1 = ks[t * kKeyStride + 64 + f];
+        ks[t * kKeyStride + f] = x0 * c - x1 * s;
+        ks[t * kKeyStride + 64 + f] = x0 * s + x1 * c;
+      }
+    }
+    __syncthreads();
+    // ---- scores of the thread's four tokens (part, part + 8, ..), softmax over the node's eight threads
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < kHeadDim; d += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(qs + row * kKeyStride + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 kk = *reinterpret_cast<const float4*>(ks + (part + 8 * i) * kKeyStride + d);
+        s[i] = fmaf(q.x, kk.x, fmaf(q.y, kk.y, fmaf(q.z, kk.z, fmaf(q.w, kk.w, s[i]))));
+      }
+    }
+    float mt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (part + 8 * i >= cnt) s[i] = -INFINITY;
+      mt = fmaxf(mt, s[i]);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+    const float m_new = fmaxf(m, mt);
+    const float alpha = m == -INFINITY ? 0.f : exp2f(m - m_new);
+    m = m_new;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = part + 8 * i < cnt ? exp2f(s[i] - m) : 0.f;
+      ps[row * 33 + part + 8 * i] = p;
+      sum += p;
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * alpha + sum;
+    __syncwarp();
+    // ---- latent sum: columns part, part + 8, ..
+#pragma unroll
+    for (int i = 0; i < kMaxRankPerHead / 8; ++i) {
+      if (i < nv) {
+        float x = acc[i] * alpha;
+        for (int t = 0; t < kTreePlainTile; ++t) x = fmaf(ps[row * 33 + t], vs[t * a.r_v + part + 8 * i], x);
+        acc[i] = x;
+      }
+    }
+  }
+  if (row < rows) {
+    float* rec = a.records + ((unit * a.splits + split) * a.max_nodes + row0 + row) * (a.r_v + kRecordHead);
+    if (part == 0) { rec[0] = m; rec[1] = l; }
+#pragma unroll
+    for (int i = 0; i < kMaxRankPerHead / 8; ++i)
+      if (i < nv) rec[kRecordHead + part + 8 * i] = acc[i];
+  }
+}
+
+// Block = (unit, eight nodes), one node at a time: scores of the nodes on its path (a warp each),
+// merge of the unit's records, then thread e forms out_e = (W_e . A + mu_e P + sum_a p_a v_a,e) / l.
+template <typename T>
+__global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ int32_t par[kTreeMaxNodes];
+  __shared__ int32_t chain[kTreeMaxNodes];
+  __shared__ int depth;
+  __shared__ float sc[kTreeMaxNodes];
+  __shared__ float qrow[kHeadDim];
+  __shared__ float A[kMaxRankPerHead];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t unit = blockIdx.x;
+  const int b = static_cast<int>(unit / a.H), h = static_cast<int>(unit - static_cast<int64_t>(b) * a.H);
+  const bool flag = h == 0 && blockIdx.y == 0;
+  int first;
+  const int n = tree_nodes(a, b, first, flag);
+  const int L = tree_cached(a, b, flag);
+  if (blockIdx.y * kFinishRows >= n) return;
+  for (int i = tid; i < n; i += kFinishThreads) {
+    int p = __ldg(a.parent + first + i);
+    if (p < -1 || p >= i) {
+      if (flag) record_status(a.status, LLA_ERR_DEVICE_ARG);
+      p = -1;
+    }
+    par[i] = p;
+    if (flag) node_pos(a, first + i, true);
+  }
+  __syncthreads();
+  const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
+  const int stride = a.r_v + kRecordHead;
+
+  for (int row = blockIdx.y * kFinishRows; row < min(n, (static_cast<int>(blockIdx.y) + 1) * kFinishRows); ++row) {
+    const int entry = first + row;
+    __syncthreads();
+    if (tid == 0) {
+      int d = 0;
+      for (int i = row; i >= 0; i = par[i]) chain[d++] = i;
+      depth = d;
+    }
+    if (tid < 64) {
+      const T* qv = static_cast<const T*>(a.q) + entry * a.q_stride + h * kHeadDim;
+      const int64_t p = node_pos(a, entry, false);
+      const float c = __ldg(a.rope_cos + p * 64 + tid), s = __ldg(a.rope_sin + p * 64 + tid);
+      const float x0 = to_f(qv[pair0(a.rope_style, tid)]), x1 = to_f(qv[pair1(a.rope_style, tid)]);
+      qrow[tid] = (x0 * c - x1 * s) * (kLog2e * kInvSqrtD);
+      qrow[64 + tid] = (x0 * s + x1 * c) * (kLog2e * kInvSqrtD);
+    }
+    __syncthreads();
+    const int nd = depth;
+    for (int i = warp; i < nd; i += kFinishThreads / 32) {
+      const int ke = first + chain[i];
+      const T* kv = static_cast<const T*>(a.k) + ke * a.k_stride + h * kHeadDim;
+      const int64_t p = node_pos(a, ke, false);
+      float dot = 0.f;
+#pragma unroll
+      for (int f = lane; f < 64; f += 32) {
+        const float c = __ldg(a.rope_cos + p * 64 + f), s = __ldg(a.rope_sin + p * 64 + f);
+        const float x0 = to_f(kv[pair0(a.rope_style, f)]), x1 = to_f(kv[pair1(a.rope_style, f)]);
+        dot = fmaf(qrow[f], x0 * c - x1 * s, fmaf(qrow[64 + f], x0 * s + x1 * c, dot));
+      }
+      dot = warp_sum(dot);
+      if (lane == 0) sc[i] = dot;
+    }
+    __syncthreads();
+    // the largest of the path's scores and of the records' maxima
+    float m = -INFINITY;
+    for (int i = 0; i < nd; ++i) m = fmaxf(m, sc[i]);
+    const float* rec0 = a.records + (unit * a.splits * a.max_nodes + row) * stride;
+    const int64_t next = static_cast<int64_t>(a.max_nodes) * stride;
+    for (int i = 0; i < nsplit; ++i) m = fmaxf(m, rec0[i * next]);
+    float held = 0.f;
+    for (int i = 0; i < nsplit; ++i) held = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + 1], held);
+    for (int c = tid; c < a.r_v; c += kFinishThreads) {
+      float x = 0.f;
+      for (int i = 0; i < nsplit; ++i) x = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + kRecordHead + c], x);
+      A[c] = x;
+    }
+    __syncthreads();
+    float l = held, o = held * __ldg(a.mu_v + h * a.mu_hstride + tid);
+    if (nsplit == 0) o = 0.f;
+    for (int i = 0; i < nd; ++i) {
+      const float p = exp2f(sc[i] - m);
+      l += p;
+      o = fmaf(p, to_f(static_cast<const T*>(a.v)[(first + chain[i]) * a.v_stride + h * kHeadDim + tid]), o);
+    }
+    if (nsplit > 0) {
+      const T* wrow = static_cast<const T*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * a.r_v;
+      for (int r = 0; r < a.r_v; r += 4) {
+        const float4 w = ld4(wrow + r);
+        o = fmaf(w.x, A[r], fmaf(w.y, A[r + 1], fmaf(w.z, A[r + 2], fmaf(w.w, A[r + 3], o))));
+      }
+    }
+    const int64_t at = static_cast<int64_t>(entry) * a.H + h;
+    from_f(o / l, static_cast<T*>(a.out) + at * kHeadDim + tid);
+    if (tid == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kLn2;
+  }
+}
+
+size_t plain_smem(int r_k, int r_v) {
+  return sizeof(float) * ((kTreePlainRows + kTreePlainTile) * kKeyStride + kTreePlainTile * (r_k + r_v) + kTreePlainRows * 33);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H * a.splits),
+                  (a.max_nodes + kTreePlainRows - 1) / kTreePlainRows);
+  auto kern = bf16 ? tree_plain_kernel<__nv_bfloat16> : tree_plain_kernel<float>;
+  // (the most any shape takes, at every call)
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(plain_smem(kMaxRankPerHead, kMaxRankPerHead)));
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kPlainThreads, plain_smem(a.r_k, a.r_v), s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_tree_finish(const TreeArgs& a, bool bf16, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H), (a.max_nodes + kFinishRows - 1) / kFinishRows);
+  if (bf16) tree_finish_kernel<__nv_bfloat16><<<grid, kFinishThreads, 0, s>>>(a);
+  else tree_finish_kernel<float><<<grid, kFinishThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace lla
+
+using namespace lla;
+
+namespace {
+
+bool at16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool at4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The cache of a call: dense, or a page pool with a block table.
+struct View {
+  const void* k;
+  const void* v;
+  int B;
+  int64_t L_max;
+  const int32_t* bt;
+  int page_size, max_pages;
+  int64_t num_pages;
+};
+
+// Workspace: status word, then the records.
+struct TreeWs {
+  int64_t chunk;
+  int splits;
+  size_t records, total;
+};
+
+TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms) {
+  TreeWs w{};
+  // plain kernel: about four blocks an SM, splits of whole tiles
+  const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * d->H);
+  const int64_t tiles = std::max<int64_t>(1, (L_max + kTreePlainTile - 1) / kTreePlainTile);
+  const int64_t want = std::min(tiles, std::max<int64_t>(1, 4 * sms / units));
+  const int64_t per = (tiles + want - 1) / want;
+  w.chunk = per * kTreePlainTile;
+  w.splits = static_cast<int>((tiles + per - 1) / per);
+  w.records = 256;
+  w.total = 256 + static_cast<size_t>(units) * w.splits * max_nodes * (d->r_v + kRecordHead) * 4;
+  return w;
+}
+
+lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const View& cache, const int32_t* seq_lens,
+                     const void* w_up_k, const void* w_up_v, const float* mu_k, const float* mu_v, const float* rope_cos,
+                     const float* rope_sin, int64_t rope_len, void* out, float* lse, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  if (!tree || loop_t < 0 || loop_t >= dims->T || tree->B < 0 || tree->n_tok < 0 || tree->max_nodes < 1 ||
+      cache.B != tree->B || cache.L_max < 1)
+    return LLA_ERR_INVALID_ARG;
+  if (tree->max_nodes > kTreeMaxNodes || cache.L_max > (int64_t(1) << 30) ||
+      static_cast<int64_t>(tree->B) * dims->H > (int64_t(1) << 24) ||
+      static_cast<int64_t>(tree->n_tok) * dims->H >= (int64_t(1) << 31))
+    return LLA_ERR_UNSUPPORTED;
+  if (tree->B == 0 || tree->n_tok == 0) return LLA_OK;
+  if (rope_len < cache.L_max || rope_len < kTile) return LLA_ERR_INVALID_ARG;
+  const int64_t es = dims->dtype == LLA_BF16 ? 2 : 4, width = static_cast<int64_t>(dims->H) * kHeadDim;
+  const int64_t strides[] = {q_stride, k_stride, v_stride};
+  for (int64_t x : strides)
+    if (x < width || x * es % 16 || x > (int64_t(1) << 40)) return LLA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, k, v, cache.k, cache.v, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, out, workspace};
+  for (const void* p : ptrs)
+    if (!at16(p)) return LLA_ERR_INVALID_ARG;
+  const void* words[] = {tree->tok_start, tree->parent, tree->pos, seq_lens};
+  for (const void* p : words)
+    if (!at4(p)) return LLA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) || ws_bytes < 256) return LLA_ERR_INVALID_ARG;
+  // blocks read q, k and v of other nodes while they write out: no overlap
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + tree->n_tok * width * es;
+  const void* in[] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(in[i]);
+    if (p < o1 && o0 < p + ((tree->n_tok - 1) * strides[i] + width) * es) return LLA_ERR_INVALID_ARG;
+  }
+  const int sms = device_sm_count();
+  if (sms <= 0) return LLA_ERR_CUDA;
+  const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms);
+  if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
+  TreeArgs a{};
+  a.B = tree->B;
+  a.H = dims->H;
+  a.r_k = dims->r_k;
+  a.r_v = dims->r_v;
+  a.rope_style = dims->rope_style;
+  a.n_tok = tree->n_tok;
+  a.max_nodes = tree->max_nodes;
+  a.L_max = cache.L_max;
+  a.rope_len = rope_len;
+  a.mu_hstride = static_cast<int64_t>(dims->T) * kHeadDim;
+  a.tok_start = tree->tok_start;
+  a.parent = tree->parent;
+  a.pos = tree->pos;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.seq_lens = seq_lens;
+  a.cache_k = cache.k;
+  a.cache_v = cache.v;
+  a.block_table = cache.bt;
+  a.page_size = cache.page_size;
+  a.max_pages = cache.max_pages;
+  a.num_pages = cache.num_pages;
+  a.w_up_k = static_cast<const uint8_t*>(w_up_k) + static_cast<size_t>(loop_t) * width * dims->r_k * es;
+  a.w_up_v = static_cast<const uint8_t*>(w_up_v) + static_cast<size_t>(loop_t) * width * dims->r_v * es;
+  a.mu_k = mu_k + static_cast<size_t>(loop_t) * kHeadDim;
+  a.mu_v = mu_v + static_cast<size_t>(loop_t) * kHeadDim;
+  a.rope_cos = rope_cos;
+  a.rope_sin = rope_sin;
+  a.out = out;
+  a.lse = lse;
+  a.status = static_cast<uint32_t*>(workspace);
+  a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.records);
+  a.splits = w.splits;
+  a.chunk = w.chunk;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf16 = dims->dtype == LLA_BF16;
+  if (launch_tree_plain(a, bf16, s) != cudaSuccess || launch_tree_finish(a, bf16, s) != cudaSuccess) return LLA_ERR_CUDA;
+  return LLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* lla_tree_kernel(const lla_dims* dims, int page_size) {
+  if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || page_size < 0) return nullptr;
+  return "plain";
+}
+
+size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max) {
+  if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || B < 0 || max_nodes < 1 ||
+      max_nodes > kTreeMaxNodes || L_max < 0)
+    return 0;
+  return tree_ws(dims, B, max_nodes, L_max, std::max(1, device_sm_count())).total;
+}
+
+lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, lla_cache cache,
+                         const int32_t* seq_lens, const void* w_up_k, const void* w_up_v, const float* mu_k,
+                         const float* mu_v, const float* rope_cos, const float* rope_sin, int64_t rope_len,
+                         void* out, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  const lla_status st = checked_dims(dims);
+  if (st != LLA_OK) return st;
+  if (dims->variant != LLA_PER_HEAD) return LLA_ERR_UNSUPPORTED;
+  return tree_attn(dims, loop_t, tree, q, q_stride, k, k_stride, v, v_stride,
+                   View{cache.k, cache.v, cache.B, cache.L_max, nullptr, 0, 0, 0}, seq_lens, w_up_k, w_up_v, mu_k, mu_v,
+                   rope_cos, rope_sin, rope_len, out, lse, workspace, ws_bytes, stream);
+}
+
+lla_status lla_tree_attn_paged(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q,
+                               int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               lla_paged_cache cache, const int32_t* seq_lens, const void* w_up_k,
+                               const void* w_up_v, const float* mu_k, const float* mu_v, const float* rope_cos,
+                               const float* rope_sin, int64_t rope_len, void* out, float* lse, void* workspace,
+                               size_t ws_bytes, void* stream) {
+  const lla_status st = checked_dims(dims);
+  if (st != LLA_OK) return st;
+  if (dims->variant != LLA_PER_HEAD) return LLA_ERR_UNSUPPORTED;
+  if (cache.B < 0 || cache.max_pages < 1 || cache.page_size < 1 || cache.num_pages < 1) return LLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(cache.max_pages) * cache.page_size > (int64_t(1) << 30) || cache.num_pages >= (int64_t(1) << 31) ||
+      cache.num_pages * static_cast<int64_t>(dims->H) >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(cache.B) * cache.max_pages >= (int64_t(1) << 31))
+    return LLA_ERR_UNSUPPORTED;
+  if (cache.B > 0 && !at4(cache.block_table)) return LLA_ERR_INVALID_ARG;
+  return tree_attn(dims, loop_t, tree, q, q_stride, k, k_stride, v, v_stride,
+                   View{cache.k, cache.v, cache.B, static_cast<int64_t>(cache.max_pages) * cache.page_size, cache.block_table,
+                        cache.page_size, cache.max_pages, cache.num_pages},
+                   seq_lens, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, rope_len, out, lse, workspace, ws_bytes,
+                   stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,69 @@
+// lla_tree.h — parameter block and launchers of the attention over drafted trees
+// (lla_tree_attn), shared by lla_tree.cu (entry points, plain and finish kernels) and
+// lla_tree_tc.cu (tensor-core kernel).
+#pragma once
+
+#include "lla_kernels.h"
+
+namespace lla {
+
+constexpr int kTreeMaxNodes = LLA_TREE_MAX_NODES;
+constexpr int kTreePlainRows = 32;      // nodes of a plain block
+constexpr int kTreePlainTile = 32;      // cached tokens it takes at a time
+
+struct TreeArgs {
+  int B, H, r_k, r_v, rope_style, n_tok, max_nodes;
+  int64_t L_max, rope_len, mu_hstride;
+  const int32_t* tok_start;          // [B + 1]
+  const int32_t* parent;             // [n_tok]
+  const int32_t* pos;                // [n_tok]
+  const void* q;                     // element (n, h, e) at n * stride + h * 128 + e
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* seq_lens;           // [B]
+  const void* cache_k;               // dense [B][H][L_max][r] or pools [num_pages][H][page_size][r]
+  const void* cache_v;
+  const int32_t* block_table;        // [B][max_pages], or nullptr (dense)
+  int page_size, max_pages;
+  int64_t num_pages;
+  const void* w_up_k;                // loop-t slice [H][128][r_k]
+  const void* w_up_v;                // loop-t slice [H][128][r_v]
+  const float* mu_k;                 // loop-t slice: element (h, e) at h * mu_hstride + e
+  const float* mu_v;
+  const float* rope_cos;             // [rope_len][64]
+  const float* rope_sin;
+  void* out;                         // [n_tok][H][128]
+  float* lse;                        // [n_tok][H] or nullptr
+  uint32_t* status;
+  // Partial results of the cached tokens: a record holds max_nodes rows of {m, l, -, -, acc[r_v]}
+  // (m in log2 units).  Plain kernel: record unit * splits + s covers tokens s * chunk ..; a unit
+  // is b H + h.
+  float* records;
+  int splits;
+  int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
+};
+
+// Nodes of sequence b: its first entry, and how many (0 for entries that do not describe a
+// sequence, which `flag` records).
+__device__ __forceinline__ int tree_nodes(const TreeArgs& a, int b, int& first, bool flag) {
+  const int s0 = __ldg(a.tok_start + b), s1 = __ldg(a.tok_start + b + 1);
+  first = s0;
+  if (s0 < 0 || s1 < s0 || s1 > a.n_tok || s1 - s0 > a.max_nodes) {
+    if (flag) record_status(a.status, LLA_ERR_DEVICE_ARG);
+    return 0;
+  }
+  return s1 - s0;
+}
+
+// Cached tokens of sequence b, clamped to what the cache can hold.
+__device__ __forceinline__ int tree_cached(const TreeArgs& a, int b, bool flag) {
+  const int L = __ldg(a.seq_lens + b);
+  if (flag && (L < 0 || L > a.L_max)) record_status(a.status, LLA_ERR_DEVICE_ARG);
+  return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
+}
+
+cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_tree_finish(const TreeArgs& a, bool bf16, cudaStream_t s);
+
+}  // namespace lla

@@ -26,6 +26,7 @@ LLA_BF16, LLA_F32 = 0, 1
 LLA_PER_HEAD, LLA_2D = 0, 1
 LLA_ROPE_HALF, LLA_ROPE_INTERLEAVED = 0, 1
 LLA_ROPE_PLAIN, LLA_ROPE_LINEAR, LLA_ROPE_BASE, LLA_ROPE_BY_PARTS = range(4)
+LLA_TREE_MAX_NODES = 128
 
 
 class Dims(ctypes.Structure):
@@ -53,6 +54,19 @@ class RopeScaling(ctypes.Structure):
 class Q4Cache(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("B", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int64)]
+
+
+class Tree(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("n_tok", ctypes.c_int), ("max_nodes", ctypes.c_int),
+                ("tok_start", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("pos", ctypes.c_void_p)]
+
+
+class LogitRulesC(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("hist_len", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p),
+                ("max_history", ctypes.c_int), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("bias_token", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("max_bias", ctypes.c_int), ("allowed", ctypes.c_void_p), ("allowed_row", ctypes.c_void_p),
+                ("n_masks", ctypes.c_int)]
 
 
 class LLAError(RuntimeError):
@@ -129,6 +143,22 @@ def lib():
             L.lla_decode_attn_q4.argtypes = [pd, i32, vp, pq, i32p, i32p, vp, vp, fp, fp, fp, fp, i64, vp, fp,
                                              vp, sz, vp]
             L.lla_decode_attn_q4.restype = ctypes.c_int
+            pt, pr = ctypes.POINTER(Tree), ctypes.POINTER(LogitRulesC)
+            after = [i32p, vp, vp, fp, fp, fp, fp, i64, vp, fp, vp, sz, vp]
+            L.lla_tree_workspace_size.argtypes = [pd, i32, i32, i64]
+            L.lla_tree_workspace_size.restype = sz
+            L.lla_tree_attn.argtypes = [pd, i32, pt, vp, i64, vp, i64, vp, i64, Cache] + after
+            L.lla_tree_attn.restype = ctypes.c_int
+            L.lla_tree_attn_paged.argtypes = [pd, i32, pt, vp, i64, vp, i64, vp, i64, PagedCache] + after
+            L.lla_tree_attn_paged.restype = ctypes.c_int
+            L.lla_tree_kernel.argtypes = [pd, i32]
+            L.lla_tree_kernel.restype = ctypes.c_char_p
+            L.lla_logits_workspace_size.argtypes = [i32, i32]
+            L.lla_logits_workspace_size.restype = sz
+            L.lla_logits_adjust.argtypes = [pt, i32p, i32, vp, i64, i32, pr, vp, i64, i32p, fp, vp, sz, vp]
+            L.lla_logits_adjust.restype = ctypes.c_int
+            L.lla_tree_accept.argtypes = [pt, i32p, i32p, i32p, i32p, i32p, i32p, i32p, i32p, i32p, vp, sz, vp]
+            L.lla_tree_accept.restype = ctypes.c_int
             L.lla_decode_kernel.argtypes = [pd]
             L.lla_decode_kernel.restype = ctypes.c_char_p
             L.lla_decoupled_kernel.argtypes = [pd, ctypes.c_int]
@@ -583,3 +613,200 @@ def decode_attn_q4(dm: Dims, loop_t: int, q, pool, block_table, seq_lens, q_pos,
          _arg("mu_k", mu_k, f32, dev, (H, T * d)), _arg("mu_v", mu_v, f32, dev, (H, T * d)),
          _arg("rope_cos", rope_cos, f32, dev, table), _arg("rope_sin", rope_sin, f32, dev, table), table[0],
          _arg("out", out, sd, dev, vec), None if lse is None else _arg("lse", lse, f32, dev, (c.B, H)), ws, wb)
+
+
+# ---------------------------------------------------------------- verifying drafted tokens
+
+class DraftTree:
+    """An lla_tree: the drafted tokens (nodes) of B sequences.
+
+    ``tok_start`` [B + 1], ``parent`` [n_tok] and, for tree_attn, ``pos`` [n_tok] are int32
+    tensors on one device, kept alive (and read at every call) here; ``max_nodes`` is the most
+    nodes that a sequence has, at most LLA_TREE_MAX_NODES."""
+
+    def __init__(self, tok_start, parent, max_nodes: int, pos=None):
+        dev = self.dev = _device_of("tok_start", tok_start)
+        _need(tok_start.dim() == 1 and tok_start.shape[0] >= 1, "tok_start must be [B + 1]")
+        _need(isinstance(parent, torch.Tensor) and parent.dim() == 1, "parent must be [n_tok]")
+        self.B, self.n_tok, self.max_nodes = tok_start.shape[0] - 1, parent.shape[0], int(max_nodes)
+        _need(1 <= self.max_nodes <= LLA_TREE_MAX_NODES, "max_nodes must be in 1..%d" % LLA_TREE_MAX_NODES)
+        self.tok_start, self.parent, self.pos = tok_start, parent, pos
+        one = (self.n_tok,)
+        self.c = Tree(self.B, self.n_tok, self.max_nodes, _arg("tok_start", tok_start, torch.int32, dev, (self.B + 1,)),
+                      _arg("parent", parent, torch.int32, dev, one),
+                      None if pos is None else _arg("pos", pos, torch.int32, dev, one))
+        self.ref = ctypes.byref(self.c)
+
+
+def tree_kernel(dm: Dims, page_size: int = 0) -> Optional[str]:
+    """Kernel family of tree_attn (page_size 0) and tree_attn_paged for these dims ("tensor",
+    "plain"), or None if they are invalid or unsupported."""
+    r = lib().lla_tree_kernel(ctypes.byref(dm), int(page_size))
+    return None if r is None else r.decode()
+
+
+def tree_workspace(dm: Dims, tree: DraftTree, L_max: int) -> torch.Tensor:
+    """A zeroed workspace for lla_tree_attn (L_max: the cache's, or max_pages * page_size)."""
+    with torch.cuda.device(tree.dev):
+        n = lib().lla_tree_workspace_size(ctypes.byref(dm), tree.B, tree.max_nodes, int(L_max))
+    if n == 0:
+        raise LLAError(LLA_ERR_UNSUPPORTED, "lla_tree_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=tree.tok_start.device)
+
+
+def _node_vectors(name: str, t, dtype, dev: int, shape):
+    """Address and token stride of q, k or v [n_tok][H][d], each token's [H][d] contiguous."""
+    _need(isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape,
+          "%s must be %s of shape %s on cuda:%d" % (name, dtype, tuple(shape), dev))
+    n, H, d = shape
+    st = t.stride()
+    _need((d <= 1 or st[2] == 1) and (H <= 1 or st[1] == d), "each token's vectors of %s must be contiguous" % name)
+    # (torch leaves the stride of a single token open)
+    return t.data_ptr(), st[0] if n > 1 else H * d
+
+
+def _tree_attn(what, f, dm, loop_t, tree, q, k, v, cache, B, seq_lens, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin,
+               out, lse, workspace, stream):
+    dev, sd, T, H, d, f32 = tree.dev, _storage(dm), dm.T, dm.H, dm.d_head, torch.float32
+    _need(tree.pos is not None, "the tree has no positions")
+    _need(B == tree.B, "the cache is for %d sequences, the tree for %d" % (B, tree.B))
+    vec, table = (tree.n_tok, H, d), rope_cos.shape
+    _need(len(table) == 2 and table[1] == d // 2, "rope_cos must be [rope_len][%d]" % (d // 2))
+    ws, wb = _space(workspace, dev)
+    _run(what, f, dev, stream, ctypes.byref(dm), loop_t, tree.ref, *_node_vectors("q", q, sd, dev, vec),
+         *_node_vectors("k", k, sd, dev, vec), *_node_vectors("v", v, sd, dev, vec), cache,
+         _arg("seq_lens", seq_lens, torch.int32, dev, (B,)), _arg("w_up_k", w_up_k, sd, dev, (T, H, d, dm.r_k)),
+         _arg("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)), _arg("mu_k", mu_k, f32, dev, (H, T * d)),
+         _arg("mu_v", mu_v, f32, dev, (H, T * d)), _arg("rope_cos", rope_cos, f32, dev, table),
+         _arg("rope_sin", rope_sin, f32, dev, table), table[0], _arg("out", out, sd, dev, vec),
+         None if lse is None else _arg("lse", lse, f32, dev, (tree.n_tok, H)), ws, wb)
+
+
+def tree_attn(dm: Dims, loop_t: int, tree: DraftTree, q, k, v, cache_k, cache_v, seq_lens, w_up_k, w_up_v, mu_k, mu_v,
+              rope_cos, rope_sin, out, lse, workspace, stream=None):
+    """lla_tree_attn: every node of ``tree`` attends to its sequence's cached latents and to the nodes
+    on its path.  q, k, v [n_tok][H][d] (token stride free) of loop ``loop_t``, before RoPE; ``out``
+    [n_tok][H][d] (storage dtype), ``lse`` [n_tok][H] (fp32) or None."""
+    sd, dev = _storage(dm), tree.dev
+    _need(cache_k.dim() == 4, "cache_k must be [B][H][L_max][r_k]")
+    B, L_max = cache_k.shape[0], cache_k.shape[2]
+    cache = Cache(_arg("cache_k", cache_k, sd, dev, (B, dm.H, L_max, dm.r_k)),
+                  _arg("cache_v", cache_v, sd, dev, (B, dm.H, L_max, dm.r_v)), B, L_max)
+    _tree_attn("lla_tree_attn", lib().lla_tree_attn, dm, loop_t, tree, q, k, v, cache, B, seq_lens, w_up_k, w_up_v, mu_k,
+               mu_v, rope_cos, rope_sin, out, lse, workspace, stream)
+
+
+def tree_attn_paged(dm: Dims, loop_t: int, tree: DraftTree, q, k, v, pool_k, pool_v, block_table, page_size: int,
+                    seq_lens, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, out, lse, workspace, stream=None):
+    """lla_tree_attn_paged: tree_attn over pools [num_pages][H][page_size][r] and a block table
+    [B][max_pages]."""
+    sd, dev = _storage(dm), tree.dev
+    _need(pool_k.dim() == 4 and pool_k.shape[2] == page_size, "pool_k must be [num_pages][H][%d][r_k]" % page_size)
+    num, table = pool_k.shape[0], block_table.shape
+    _need(len(table) == 2, "block_table must be [B][max_pages]")
+    cache = PagedCache(_arg("pool_k", pool_k, sd, dev, (num, dm.H, page_size, dm.r_k)),
+                       _arg("pool_v", pool_v, sd, dev, (num, dm.H, page_size, dm.r_v)),
+                       _arg("block_table", block_table, torch.int32, dev, table), table[0], table[1], page_size, num)
+    _tree_attn("lla_tree_attn_paged", lib().lla_tree_attn_paged, dm, loop_t, tree, q, k, v, cache, table[0], seq_lens,
+               w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, out, lse, workspace, stream)
+
+
+class LogitRules:
+    """An lla_logit_rules: what the requests of a step impose on their logits.  Tensors are kept
+    alive (and read at every call) here.
+
+    ``history`` [B][max_history], ``hist_len``, ``prompt_len`` [B] (int32; prompt_len None: no
+    prompt part), ``repetition``, ``presence``, ``frequency`` [B] (fp32 or None), ``bias_token``
+    (int32, negative: unused) and ``bias`` (fp32) [B][max_bias], ``allowed`` [n_masks][ceil(vocab / 32)]
+    (int32 words of bits) with ``allowed_row`` [n_tok] (int32, negative: no mask)."""
+
+    def __init__(self, history=None, hist_len=None, prompt_len=None, repetition=None, presence=None, frequency=None,
+                 bias_token=None, bias=None, allowed=None, allowed_row=None):
+        given = (history, hist_len, prompt_len, repetition, presence, frequency, bias_token, bias, allowed, allowed_row)
+        self.keep = given
+        self.dev = next((_device_of("a rule", t) for t in given if t is not None), None)
+        _need((history is None) == (hist_len is None), "give history and hist_len or neither")
+        _need(history is not None or prompt_len is None, "prompt_len needs a history")
+        _need((bias_token is None) == (bias is None), "give bias_token and bias or neither")
+        _need((allowed is None) == (allowed_row is None), "give allowed and allowed_row or neither")
+        for name, t in (("history", history), ("bias_token", bias_token), ("allowed", allowed)):
+            _need(t is None or t.dim() == 2, name + " must have two dimensions")
+        i32, f32 = torch.int32, torch.float32
+        per = next((t.shape[0] for t in (history, repetition, presence, frequency, bias_token) if t is not None), None)
+        self.B = per
+        self.n_tok = None if allowed_row is None else allowed_row.shape[0]
+        self.words = None if allowed is None else allowed.shape[1]
+
+        def p(name, t, dtype, shape):
+            return None if t is None else _arg(name, t, dtype, self.dev, shape)
+
+        cols = lambda t: 0 if t is None else t.shape[1]  # noqa: E731
+        self.c = LogitRulesC(p("history", history, i32, (per, cols(history))), p("hist_len", hist_len, i32, (per,)),
+                             p("prompt_len", prompt_len, i32, (per,)), cols(history), p("repetition", repetition, f32, (per,)),
+                             p("presence", presence, f32, (per,)), p("frequency", frequency, f32, (per,)),
+                             p("bias_token", bias_token, i32, (per, cols(bias_token))),
+                             p("bias", bias, f32, (per, cols(bias_token))), cols(bias_token),
+                             None if allowed is None else p("allowed", allowed, i32, tuple(allowed.shape)),
+                             p("allowed_row", allowed_row, i32, (self.n_tok,)), 0 if allowed is None else allowed.shape[0])
+        self.ref = ctypes.byref(self.c)
+
+
+def logits_workspace(tree: DraftTree, vocab: int) -> torch.Tensor:
+    """A zeroed workspace for lla_logits_adjust."""
+    n = lib().lla_logits_workspace_size(tree.n_tok, int(vocab))
+    if n == 0:
+        raise LLAError(LLA_ERR_UNSUPPORTED, "lla_logits_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=tree.tok_start.device)
+
+
+_LOGIT_TYPES = {torch.bfloat16: LLA_BF16, torch.float32: LLA_F32}
+
+
+def logits_adjust(tree: DraftTree, token, logits, rules: LogitRules, out=None, best=None, lse=None, workspace=None,
+                  stream=None):
+    """lla_logits_adjust: ``rules`` on the rows of ``logits`` [n_tok][vocab] (bf16 or fp32, row
+    stride free), into ``out`` (may be ``logits``), each row's best token into ``best`` [n_tok] (int32)
+    and its log-sum-exp into ``lse`` [n_tok] (fp32); at least one of the three.  ``token`` [n_tok]
+    (int32) are the nodes' tokens."""
+    dev, n = tree.dev, tree.n_tok
+    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.shape[0] == n and logits.get_device() == dev,
+          "logits must be [%d][vocab] on cuda:%d" % (n, dev))
+    dtype, V = logits.dtype, logits.shape[1]
+    _need(dtype in _LOGIT_TYPES, "logits must be bfloat16 or float32, not %s" % (dtype,))
+    _need(V <= 1 or logits.stride(1) == 1, "each row of logits must be contiguous")
+    if out is not None:
+        _need(out.dtype is dtype and out.get_device() == dev and out.shape == logits.shape and
+              (V <= 1 or out.stride(1) == 1), "out must be like logits")
+    _need(rules.dev in (None, dev), "the rules are on cuda:%s, not on cuda:%d" % (rules.dev, dev))
+    _need(rules.B in (None, tree.B), "the rules are for %s sequences, the tree for %d" % (rules.B, tree.B))
+    _need(rules.n_tok in (None, n), "allowed_row has %s entries, the tree %d" % (rules.n_tok, n))
+    _need(rules.words in (None, (V + 31) // 32), "a mask has %s words, %d tokens need %d" % (rules.words, V, (V + 31) // 32))
+    row = lambda t: t.stride(0) if n > 1 else V  # noqa: E731
+    ws, wb = _space(workspace, dev)
+    _run("lla_logits_adjust", lib().lla_logits_adjust, dev, stream, tree.ref, _arg("token", token, torch.int32, dev, (n,)),
+         _LOGIT_TYPES[dtype], logits.data_ptr(), row(logits), V, rules.ref, None if out is None else out.data_ptr(),
+         0 if out is None else row(out), None if best is None else _arg("best", best, torch.int32, dev, (n,)),
+         None if lse is None else _arg("lse", lse, torch.float32, dev, (n,)), ws, wb)
+
+
+class TreeAccept:
+    """Output arrays and status word of lla_tree_accept for ``tree``; calling it walks down the tree.
+
+    ``count``, ``next_token``, ``seq_lens`` [B], ``path``, ``seq_idx``, ``pos`` [n_tok] (int32; the
+    last two as lla_encode takes them)."""
+
+    def __init__(self, tree: DraftTree):
+        i32 = dict(dtype=torch.int32, device=tree.tok_start.device)
+        self.tree = tree
+        self.count, self.next_token, self.seq_lens = (torch.empty(tree.B, **i32) for _ in range(3))
+        self.path, self.seq_idx, self.pos = (torch.empty(tree.n_tok, **i32) for _ in range(3))
+        self.workspace = torch.zeros(256, dtype=torch.uint8, device=tree.tok_start.device)
+
+    def __call__(self, token, chosen, ctx_lens, stream=None):
+        t, i32 = self.tree, torch.int32
+        one = (t.n_tok,)
+        _run("lla_tree_accept", lib().lla_tree_accept, t.dev, stream, t.ref, _arg("token", token, i32, t.dev, one),
+             _arg("chosen", chosen, i32, t.dev, one), _arg("ctx_lens", ctx_lens, i32, t.dev, (t.B,)),
+             self.count.data_ptr(), self.next_token.data_ptr(), self.seq_lens.data_ptr(), self.path.data_ptr(),
+             self.seq_idx.data_ptr(), self.pos.data_ptr(), self.workspace.data_ptr(), 256)
+        return self

@@ -1,0 +1,289 @@
+"""lla_tree_attn and lla_tree_attn_paged against the 64-bit oracle.
+
+Cache rows that hold no token of a call, and entries that belong to no sequence, are NaN: a result
+that touched one shows it.  Tolerances: fp32 storage 1e-5 of the largest value of an output
+vector, as everywhere; bf16 storage the oracle's bound of the roundings to bf16 (six standard
+deviations) and half a step of the result, 2^-8 of its value."""
+import numpy as np
+import pytest
+import torch
+
+from lla_cases import widen
+from looped_transformer_cross_gb300 import lla
+from oracle import tree as otree
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from looped_transformer_cross_gb300 import build
+    build.build()
+
+
+def make(lens, nodes, H, rk, rv, page=0, style=0, dtype="bf16", branch=2, T=2, t=1, seed=0, pad=3, device="cuda", scale=1.0,
+         fused=True, roots=False, cap=None):
+    """A call's tensors: sequences of the given cached lengths and node counts."""
+    g = torch.Generator().manual_seed(1000 * seed + 7 * rk + rv + sum(lens) + 31 * sum(nodes))
+    sd = torch.bfloat16 if dtype == "bf16" else torch.float32
+    rnd = lambda std, *s: torch.randn(*s, generator=g) * std  # noqa: E731
+    B, n = len(lens), sum(nodes)
+    parent, pos = [], []
+    for L, m in zip(lens, nodes):
+        depth = []
+        for i in range(m):
+            p = -1 if i == 0 or (roots and i % 5 == 4) else max(0, i - 1 - int(torch.randint(0, branch, (1,), generator=g)))
+            depth.append(0 if p < 0 else depth[p] + 1)
+            parent.append(p)
+            pos.append(L + depth[-1])
+    c = dict(H=H, T=T, t=t, style=style, page=page, lens=list(lens), nodes=list(nodes), dtype=dtype)
+    c["dm"] = lla.dims(T, H, rk, rv, dtype=lla.LLA_BF16 if dtype == "bf16" else lla.LLA_F32, rope_style=style)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=device)  # noqa: E731
+    c["tok_start"] = i32([0] + list(np.cumsum(nodes)))
+    c["parent"], c["pos"] = i32(parent + [-1] * pad), i32(pos + [0] * pad)
+    c["seq_lens"] = i32(list(lens))
+    qkv = rnd(scale, n + pad, 3 * H, D).to(sd)
+    qkv[n:] = float("nan")
+    c["qkv"] = qkv.to(device)
+    cap = max([1, *lens]) if cap is None else cap
+    if page == 0:
+        ck, cv = rnd(1.0, B, H, cap, rk).to(sd), rnd(1.0, B, H, cap, rv).to(sd)
+        for b, L in enumerate(lens):
+            ck[b, :, L:], cv[b, :, L:] = float("nan"), float("nan")
+    else:
+        mp = (cap + page - 1) // page
+        held = [(L + page - 1) // page for L in lens]
+        num = sum(held) + 2
+        ck, cv = rnd(1.0, num, H, page, rk).to(sd), rnd(1.0, num, H, page, rv).to(sd)
+        perm, used = torch.randperm(num, generator=g).tolist(), 0
+        table = np.full((B, mp), -7, np.int32)
+        for b, L in enumerate(lens):
+            table[b, :held[b]] = perm[used:used + held[b]]
+            used += held[b]
+            if L % page:
+                ck[table[b, held[b] - 1], :, L % page:] = float("nan")
+                cv[table[b, held[b] - 1], :, L % page:] = float("nan")
+        for p in perm[used:]:
+            ck[p], cv[p] = float("nan"), float("nan")
+        c["table"] = torch.from_numpy(table).to(device)
+        cap = mp * page
+    c["cap"], c["ck"], c["cv"] = cap, ck.to(device), cv.to(device)
+    c["wk"], c["wv"] = rnd(rk ** -0.5, T, H, D, rk).to(sd).to(device), rnd(rv ** -0.5, T, H, D, rv).to(sd).to(device)
+    c["mk"], c["mv"] = rnd(0.3, H, T * D).to(device), rnd(0.3, H, T * D).to(device)
+    ang = torch.arange(max(128, cap + 130), dtype=torch.float64)[:, None] * 10000.0 ** (-2.0 * torch.arange(64, dtype=torch.float64) / D)
+    c["cos"], c["sin"] = ang.cos().float().to(device), ang.sin().float().to(device)
+    c["max_nodes"] = max([1, *nodes])
+    c["out"] = torch.full((n + pad, H, D), 77.0, dtype=sd, device=device)
+    c["lse"] = torch.full((n + pad, H), 77.0, device=device)
+    return c
+
+
+def tree_of(c, max_nodes=None):
+    return lla.DraftTree(c["tok_start"], c["parent"], c["max_nodes"] if max_nodes is None else max_nodes, pos=c["pos"])
+
+
+def call(c, ws=None, tree=None, out="out", lse="lse", stream=None):
+    tree = tree_of(c) if tree is None else tree
+    ws = lla.tree_workspace(c["dm"], tree, c["cap"]) if ws is None else ws
+    H = c["H"]
+    q, k, v = (c["qkv"][:, i * H:(i + 1) * H] for i in range(3))
+    rest = (c["seq_lens"], c["wk"], c["wv"], c["mk"], c["mv"], c["cos"], c["sin"], c[out], None if lse is None else c[lse], ws)
+    if c["page"]:
+        lla.tree_attn_paged(c["dm"], c["t"], tree, q, k, v, c["ck"], c["cv"], c["table"], c["page"], *rest, stream=stream)
+    else:
+        lla.tree_attn(c["dm"], c["t"], tree, q, k, v, c["ck"], c["cv"], *rest, stream=stream)
+    return ws
+
+
+def want(c):
+    ck, cv = widen(c["ck"]), widen(c["cv"])
+
+    def latents(b, h):
+        L, P = c["lens"][b], c["page"]
+        if not P:
+            return ck[b, h, :L], cv[b, h, :L]
+        pages = c["table"][b, :(L + P - 1) // P].tolist()
+        return tuple(np.concatenate([x[p, h] for p in pages] + [np.zeros((0, x.shape[3]))])[:L] for x in (ck, cv))
+
+    H, t = c["H"], c["t"]
+    qkv = widen(c["qkv"])
+    sl = slice(t * D, (t + 1) * D)
+    return otree.tree_attn(qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:], c["tok_start"].tolist(), c["parent"].tolist(), c["pos"].tolist(),
+                           latents, widen(c["wk"])[t], widen(c["wv"])[t], widen(c["mk"])[:, sl], widen(c["mv"])[:, sl],
+                           widen(c["cos"]), widen(c["sin"]), c["style"])
+
+
+def check(c, ws, lse=True):
+    assert lla.device_status(ws) == lla.LLA_OK
+    o, s, tol, tol_s = want(c)
+    n = sum(c["nodes"])
+    got, got_s = widen(c["out"]), widen(c["lse"])
+    top = np.abs(o[:n]).max(-1, keepdims=True) if n else np.zeros((0, c["H"], 1))
+    if c["dtype"] == "f32":
+        tol, tol_s = 1e-5 * top, np.full_like(s[:n], 1e-5)
+    else:
+        # (fp32 sums, and what a bound to first order leaves out: 1e-4 of the largest value)
+        tol, tol_s = tol[:n] + 2.0 ** -8 * np.abs(o[:n]) + 1e-4 * top, tol_s[:n] + 1e-4
+    err = np.abs(got[:n] - o[:n])
+    assert np.isfinite(got[:n]).all() and (err <= tol).all(), float((err / tol).max())
+    if lse:
+        assert (np.abs(got_s[:n] - s[:n]) <= tol_s).all(), float((np.abs(got_s[:n] - s[:n]) / tol_s).max())
+    assert (got[n:] == 77.0).all() and (got_s[n:] == 77.0).all()
+
+
+CASES = [
+    # lens, nodes, H, r_k, r_v, page
+    ([1], [1], 1, 16, 16, 0),
+    ([0], [1], 2, 96, 160, 0),
+    ([0, 130, 0], [3, 0, 0], 1, 96, 160, 0),
+    ([127, 128, 129], [1, 2, 3], 2, 96, 160, 0),
+    ([300, 7, 0, 256], [9, 16, 5, 0], 3, 96, 160, 0),
+    ([513], [33], 2, 64, 128, 0),
+    ([260, 90], [64, 31], 2, 96, 160, 64),
+    ([385], [128], 1, 96, 160, 0),
+    ([200, 70], [65, 127], 1, 32, 64, 16),
+    ([700, 3, 511], [4, 8, 2], 4, 16, 32, 0),
+    ([700, 3, 511], [4, 8, 2], 4, 16, 32, 8),
+    ([257, 100], [7, 5], 2, 16, 32, 32),
+    ([150, 49], [5, 6], 2, 96, 160, 24),
+    ([150, 49], [5, 6], 2, 96, 160, 1),
+    ([301, 64], [5, 6], 2, 96, 160, 100),
+    ([301, 600], [17, 6], 2, 96, 160, 128),
+    ([301, 600], [17, 6], 2, 80, 48, 256),
+    ([301], [40], 2, 112, 112, 0),
+    ([140], [6], 2, 256, 256, 0),
+    ([140], [6], 1, 240, 16, 64),
+    ([129], [12], 2, 16, 256, 0),
+    ([2100], [10], 3, 128, 208, 0),
+    ([1300, 1, 40], [3, 20, 50], 5, 48, 80, 0),
+]
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("lens,nodes,H,rk,rv,page", CASES)
+def test_tree_attn_bf16(lens, nodes, H, rk, rv, page, style):
+    c = make(lens, nodes, H, rk, rv, page, style, "bf16")
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("lens,nodes,H,rk,rv,page", CASES)
+def test_tree_attn_f32(lens, nodes, H, rk, rv, page):
+    c = make(lens, nodes, H, rk, rv, page, len(lens) % 2, "f32")
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("branch,roots", [(1, False), (8, False), (2, True)])
+def test_tree_shapes(dtype, branch, roots):
+    """Chains, bushy trees and forests."""
+    c = make([130, 20, 0], [20, 33, 64], 2, 96, 160, 0, 0, dtype, branch=branch, roots=roots)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_sequences_and_long_ones(dtype):
+    """More units than multiprocessors, lengths far apart, none of a unit's tiles in one block only."""
+    lens = [5000, 1, 0, 127, 640, 130] + [100] * 30
+    c = make(lens, [3, 1, 2, 4, 1, 0] + [2] * 30, 6, 32, 64, 0, 0, dtype)
+    check(c, call(c))
+
+
+def test_large_scores():
+    """Queries and keys of 4 standard deviations: weights far apart, a running maximum that rises."""
+    c = make([900], [12], 2, 96, 160, 0, 0, "f32", scale=4.0)
+    check(c, call(c))
+    c = make([900], [12], 2, 96, 160, 0, 0, "bf16", scale=4.0)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_without_lse_and_on_another_stream(dtype):
+    c = make([300, 40], [4, 9], 2, 96, 160, 64, 0, dtype)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = lla.tree_workspace(c["dm"], tree_of(c), c["cap"])
+    torch.cuda.synchronize()
+    call(c, ws, lse=None, stream=s)
+    s.synchronize()
+    check(c, ws, lse=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_separate_tensors_and_room_for_more_nodes(dtype):
+    """q, k, v as tensors of their own; max_nodes above what any sequence has."""
+    c = make([300, 40], [4, 9], 2, 96, 160, 0, 0, dtype)
+    tree = tree_of(c, 100)
+    ws = lla.tree_workspace(c["dm"], tree, c["cap"])
+    q, k, v = (c["qkv"][:, 2 * i:2 * i + 2].contiguous() for i in range(3))
+    lla.tree_attn(c["dm"], c["t"], tree, q, k, v, c["ck"], c["cv"], c["seq_lens"], c["wk"], c["wv"], c["mk"], c["mv"], c["cos"], c["sin"],
+                  c["out"], c["lse"], ws)
+    check(c, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_repeats_bit_for_bit_and_replays(dtype):
+    """The same call gives the same bits, and so does a captured graph after its inputs changed."""
+    c = make([700, 333], [20, 5], 3, 96, 160, 64, 0, dtype)
+    ws = call(c)
+    first = c["out"].clone()
+    call(c, ws)
+    assert torch.equal(first, c["out"])
+    tree = tree_of(c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c, ws, tree)
+    c["qkv"].neg_()
+    c["seq_lens"] -= 1
+    c["pos"] -= 1
+    c["lens"] = [x - 1 for x in c["lens"]]
+    c["out"].fill_(77.0)
+    c["lse"].fill_(77.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_device_values(dtype):
+    """Values that the host cannot see: recorded, and read as the documentation says."""
+    base = lambda: make([200, 100], [5, 4], 2, 96, 160, 64, 0, dtype)  # noqa: E731
+
+    def flagged(c, ws):
+        assert lla.device_status(ws) == lla.LLA_ERR_DEVICE_ARG
+        return ws
+
+    c = base()                                       # a parent that does not come before its node: a root
+    c["parent"][2] = 2
+    c["parent"][7] = -3
+    check(c, flagged(c, call(c)))
+    c = base()                                       # a sequence with more nodes than there is room for: none
+    n0 = c["nodes"][0]
+    ws = flagged(c, call(c, tree=tree_of(c, 4)))
+    assert (c["out"][:n0] == 77.0).all() and torch.isfinite(c["out"][n0:9].float()).all()
+    c = base()                                       # starts that descend, or leave the array
+    c["tok_start"][1] = 50
+    ws = flagged(c, call(c))
+    assert (c["out"] == 77.0).all()
+    c = base()                                       # lengths and positions out of range: clamped
+    c["seq_lens"][0], c["pos"][6] = -1, 1 << 30
+    ws = call(c)
+    flagged(c, ws)
+    c["lens"][0] = 0
+    c["pos"][6] = c["cos"].shape[0] - 1
+    check(c, ws)
+    c = base()                                       # a page outside the pool: read as one inside, flagged
+    c["table"][1, 0] = 1 << 20
+    flagged(c, call(c))
+    assert torch.isfinite(c["out"][:5].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_pages(dtype):
+    """Two sequences whose tables name the same pages (a shared prefix)."""
+    c = make([128, 128], [3, 4], 2, 96, 160, 64, 0, dtype)
+    c["table"][1] = c["table"][0]
+    check(c, call(c))
