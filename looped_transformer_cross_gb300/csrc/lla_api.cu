@@ -12,7 +12,7 @@
 
 using namespace lla;
 
-namespace {
+namespace lla {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -27,6 +27,10 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   });
   return fn;
 }
+
+}  // namespace lla
+
+namespace {
 
 // 3-D tiled map over a dense row-major tensor [d2][d1][d0] of `esize`-byte elements.
 // Swizzle = the atom matching the box row bytes (128 / 64 / 32 B).

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 #include <cstdint>
 
 #include "lla_sm103.cuh"
@@ -377,6 +378,8 @@ struct FastDiv {
 // (lla_api.cu) the checks of dims that every call makes, and the current device's SM count
 lla_status checked_dims(const lla_dims* dims);
 int device_sm_count();
+// the driver's cuTensorMapEncodeTiled, or nullptr
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // ----------------------------------------------------------------- scratch without allocation
 

@@ -223,7 +223,17 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     if (flag) node_pos(a, first + i, true);
   }
   __syncthreads();
-  const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
+  // the unit's records: consecutive, each max_nodes rows
+  int64_t rec_at = unit * a.splits;
+  int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
+  if (a.copies > 0) {
+    const int64_t t0 = a.tile_start[b], nb = a.tile_start[b + 1] - t0;
+    const int64_t share = max(static_cast<int64_t>(1), (static_cast<int64_t>(a.tile_start[a.B]) * a.H + a.grid - 1) / a.grid);
+    const int64_t f0 = t0 * a.H + h * nb;
+    const int64_t c0 = f0 / share, c1 = nb > 0 ? (f0 + nb - 1) / share + 1 : c0;
+    rec_at = (unit + c0) * a.copies;
+    nsplit = static_cast<int>(c1 - c0) * a.copies;
+  }
   const int stride = a.r_v + kRecordHead;
 
   for (int row = blockIdx.y * kFinishRows; row < min(n, (static_cast<int>(blockIdx.y) + 1) * kFinishRows); ++row) {
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     // the largest of the path's scores and of the records' maxima
     float m = -INFINITY;
     for (int i = 0; i < nd; ++i) m = fmaxf(m, sc[i]);
-    const float* rec0 = a.records + (unit * a.splits * a.max_nodes + row) * stride;
+    const float* rec0 = a.records + (rec_at * a.max_nodes + row) * stride;
     const int64_t next = static_cast<int64_t>(a.max_nodes) * stride;
     for (int i = 0; i < nsplit; ++i) m = fmaxf(m, rec0[i * next]);
     float held = 0.f;
@@ -338,25 +348,83 @@ struct View {
   int64_t num_pages;
 };
 
-// Workspace: status word, then the records.
+// Pages that the tensor-core kernel's copies take (0: dense).
+bool tensor_pages(int page_size) { return page_size == 0 || (page_size >= 8 && tile_kernel_page_size(page_size)); }
+
+// Workspace: status word; tensor-core kernel: the plan, the mu and the query operands; the records.
 struct TreeWs {
   int64_t chunk;
-  int splits;
-  size_t records, total;
+  int splits, grid;
+  size_t tile_start, cta_start, bias, qimg, records, total;
 };
 
-TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms) {
+TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
   TreeWs w{};
-  // plain kernel: about four blocks an SM, splits of whole tiles
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * d->H);
+  const size_t rec = static_cast<size_t>(max_nodes) * (d->r_v + kRecordHead) * 4;
+  auto al = [](size_t x) { return (x + 255) / 256 * 256; };
+  if (tensor) {
+    const int copies = tree_copies(max_nodes);
+    const int64_t most = units * std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
+    w.grid = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxGrid), most));
+    w.tile_start = 256;
+    w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
+    w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
+    w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
+    w.records = w.qimg + static_cast<size_t>(units) * (32768 / copies);
+    w.total = w.records + static_cast<size_t>(units + w.grid) * copies * rec;
+    return w;
+  }
+  // plain kernel: about four blocks an SM, splits of whole tiles
   const int64_t tiles = std::max<int64_t>(1, (L_max + kTreePlainTile - 1) / kTreePlainTile);
   const int64_t want = std::min(tiles, std::max<int64_t>(1, 4 * sms / units));
   const int64_t per = (tiles + want - 1) / want;
   w.chunk = per * kTreePlainTile;
   w.splits = static_cast<int>((tiles + per - 1) / per);
   w.records = 256;
-  w.total = 256 + static_cast<size_t>(units) * w.splits * max_nodes * (d->r_v + kRecordHead) * 4;
+  w.total = 256 + static_cast<size_t>(units) * w.splits * rec;
   return w;
+}
+
+// bf16 tensor of up to four dimensions as a map; strides in bytes of dimensions 1.., swizzle of the box's rows.
+bool map_4d(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) st[i - 1] = strides[i - 1];
+  }
+  const CUtensorMapSwizzle sw = box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : box[0] == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tree_maps(const TreeArgs& a, TreeMaps* m) {
+  *m = TreeMaps{};
+  // rows of one (sequence or page, head): L_max or page_size of them
+  const uint64_t rows = static_cast<uint64_t>(a.block_table ? a.page_size : a.L_max);
+  const uint64_t outer = static_cast<uint64_t>(a.block_table ? a.num_pages : a.B) * a.H;
+  const uint32_t box_rows = a.block_table && a.page_size < kTile ? a.page_size : kTile;
+  const uint64_t rk = a.r_k, rv = a.r_v;
+  auto latents = [&](CUtensorMap* map, const void* base, uint64_t r, uint32_t width) {
+    const uint64_t d[3] = {r, rows, outer}, st[2] = {2 * r, 2 * r * rows};
+    const uint32_t box[3] = {width, box_rows, 1};
+    return map_4d(map, base, 3, d, st, box);
+  };
+  for (int c = 0; c < a.plan.kplan.n; ++c) {
+    const uint32_t width = a.plan.kplan.width[c];
+    const int i = chunk_map_index(width);
+    if (!latents(&m->k[i], a.cache_k, rk, width)) return false;
+    // row pair_index of member 0 or 1: f and f + 64, or 2 f and 2 f + 1
+    const uint64_t step = a.rope_style == 0 ? 1 : 2, member = a.rope_style == 0 ? 64 : 1;
+    const uint64_t d[4] = {rk, 64, 2, static_cast<uint64_t>(a.H)}, st[3] = {2 * rk * step, 2 * rk * member, 2 * rk * kHeadDim};
+    const uint32_t box[4] = {width, 64, 2, 1};
+    if (!map_4d(&m->w[i], a.w_up_k, 4, d, st, box)) return false;
+  }
+  return latents(&m->v, a.cache_v, rv, 32);
 }
 
 lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride, const void* k,
@@ -369,7 +437,8 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     return LLA_ERR_INVALID_ARG;
   if (tree->max_nodes > kTreeMaxNodes || cache.L_max > (int64_t(1) << 30) ||
       static_cast<int64_t>(tree->B) * dims->H > (int64_t(1) << 24) ||
-      static_cast<int64_t>(tree->n_tok) * dims->H >= (int64_t(1) << 31))
+      static_cast<int64_t>(tree->n_tok) * dims->H >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(tree->B) * dims->H * ((cache.L_max + kTile - 1) / kTile) >= (int64_t(1) << 31))
     return LLA_ERR_UNSUPPORTED;
   if (tree->B == 0 || tree->n_tok == 0) return LLA_OK;
   if (rope_len < cache.L_max || rope_len < kTile) return LLA_ERR_INVALID_ARG;
@@ -393,9 +462,10 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   }
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
-  const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms);
-  if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   TreeArgs a{};
+  const bool tensor = dims->dtype == LLA_BF16 && tensor_pages(cache.page_size) && make_tree_plan(dims->r_k, dims->r_v, &a.plan);
+  const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms, tensor);
+  if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   a.B = tree->B;
   a.H = dims->H;
   a.r_k = dims->r_k;
@@ -436,6 +506,20 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   a.chunk = w.chunk;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dims->dtype == LLA_BF16;
+  if (tensor) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.copies = tree_copies(a.max_nodes);
+    a.rows = kTile / a.copies;
+    a.grid = w.grid;
+    a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);
+    a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
+    a.bias = ws + w.bias;
+    a.qimg = ws + w.qimg;
+    TreeMaps maps;
+    if (!tree_maps(a, &maps)) return LLA_ERR_CUDA;
+    if (launch_tree_tensor(a, maps, s) != cudaSuccess || launch_tree_finish(a, true, s) != cudaSuccess) return LLA_ERR_CUDA;
+    return LLA_OK;
+  }
   if (launch_tree_plain(a, bf16, s) != cudaSuccess || launch_tree_finish(a, bf16, s) != cudaSuccess) return LLA_ERR_CUDA;
   return LLA_OK;
 }
@@ -446,14 +530,19 @@ extern "C" {
 
 const char* lla_tree_kernel(const lla_dims* dims, int page_size) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || page_size < 0) return nullptr;
-  return "plain";
+  TreePlan p;
+  return dims->dtype == LLA_BF16 && tensor_pages(page_size) && make_tree_plan(dims->r_k, dims->r_v, &p) ? "tensor" : "plain";
 }
 
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || B < 0 || max_nodes < 1 ||
       max_nodes > kTreeMaxNodes || L_max < 0)
     return 0;
-  return tree_ws(dims, B, max_nodes, L_max, std::max(1, device_sm_count())).total;
+  // either kernel: which one a call takes depends on its page size too
+  const int sms = std::max(1, device_sm_count());
+  TreePlan p;
+  const bool tensor = dims->dtype == LLA_BF16 && make_tree_plan(dims->r_k, dims->r_v, &p);
+  return std::max(tree_ws(dims, B, max_nodes, L_max, sms, false).total, tensor ? tree_ws(dims, B, max_nodes, L_max, sms, true).total : 0);
 }
 
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,

@@ -11,6 +11,20 @@ constexpr int kTreeMaxNodes = LLA_TREE_MAX_NODES;
 constexpr int kTreePlainRows = 32;      // nodes of a plain block
 constexpr int kTreePlainTile = 32;      // cached tokens it takes at a time
 
+// Shared-memory and TMEM plan of the tensor-core kernel (byte offsets from a 1024-aligned base).
+struct TreePlan {
+  ChunkPlan kplan, vplan;            // K latents and W (64/32/16 wide); V latents (32 wide)
+  int SK, SV, k_stage, v_stage;      // rings of K and V tiles
+  int v_ring, k_ring, w, q, rot, ones, mu, base, misc, bytes;
+  int p_col, d_col;                  // TMEM columns of the weights and of the latent sums
+};
+
+struct TreeMaps {
+  CUtensorMap k[3];                  // K latents, boxes 64 / 32 / 16 wide
+  CUtensorMap v;                     // V latents, boxes 32 wide
+  CUtensorMap w[3];                  // W_up,k of the loop as (r_k, pair, member, head), boxes 64 / 32 / 16 wide
+};
+
 struct TreeArgs {
   int B, H, r_k, r_v, rope_style, n_tok, max_nodes;
   int64_t L_max, rope_len, mu_hstride;
@@ -42,6 +56,14 @@ struct TreeArgs {
   float* records;
   int splits;
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
+  // Tensor-core kernel (copies > 0): record ((unit + CTA) * copies + c) of every (unit, CTA) that
+  // share a tile
+  int copies, rows, grid;            // copies of the queries in S, rows of a copy, CTAs
+  int32_t* tile_start;               // [B + 1]: tiles of one head before sequence b
+  int4* cta_start;                   // [grid]: first (sequence, head, tile), number of tiles
+  uint8_t* qimg;                     // [B H][rows * 256] query operands
+  uint8_t* bias;                     // [H][4096] mu operands
+  TreePlan plan;
 };
 
 // Nodes of sequence b: its first entry, and how many (0 for entries that do not describe a
@@ -63,6 +85,11 @@ __device__ __forceinline__ int tree_cached(const TreeArgs& a, int b, bool flag) 
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
+// False where the operands do not fit in shared memory.
+bool make_tree_plan(int r_k, int r_v, TreePlan* p);
+// Copies of the queries for calls of up to max_nodes nodes a sequence.
+inline int tree_copies(int max_nodes) { return max_nodes <= 32 ? 4 : max_nodes <= 64 ? 2 : 1; }
+cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);
 cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_tree_finish(const TreeArgs& a, bool bf16, cudaStream_t s);
 
