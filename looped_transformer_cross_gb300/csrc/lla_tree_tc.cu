@@ -86,6 +86,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Two fp32 lanes in one 64-bit register, and packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+// The two lanes rounded to bf16, the lower one in the low half.
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+  return pack_bf16(lo, hi);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Store 8 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ int page_at(const TreeArgs& a, int b, int lp) {
   const int pg = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + lp);
   return min(max(pg, 0), static_cast<int>(a.num_pages) - 1);
@@ -440,7 +474,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         // S(j - 1) read; where P lies in S's columns, also P(j - 1)
         if (j > 0 && !(ok = agree(mbar_wait(P.p_col == kSCol ? bar(misc->vdone) : bar(misc->pfull), (j - 1) & 1, abort, a.status)))) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 8; ++k)
           umma_bf16_warp(tmem + kSCol, d_q + (k >> 2) * 1024 + (k & 3) * 2, d_r + (k >> 2) * 1024 + (k & 3) * 2, idesc, k > 0);
         umma_commit_warp(bar(misc->sfull));
@@ -491,14 +525,15 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== rotation: U -> K^ in shared memory
     const int quad = warp & 3, row = 32 * quad + lane, f0 = 32 * ((warp - 4) >> 2);
     const uint32_t t_u = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kUCol + f0;
-    float cl[32], sl[32];                             // the lane's own row of the table
+    uint64_t cl[16], sl[16];                          // the lane's own row of the table, by twos
 #pragma unroll
-    for (int f = 0; f < 32; f += 4) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + row * 64 + f0 + f));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(a.rope_sin + row * 64 + f0 + f));
-      cl[f] = c.x; cl[f + 1] = c.y; cl[f + 2] = c.z; cl[f + 3] = c.w;
-      sl[f] = s.x; sl[f + 1] = s.y; sl[f + 2] = s.z; sl[f + 3] = s.w;
+    for (int f = 0; f < 16; f += 2) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + row * 64 + f0 + 2 * f));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(a.rope_sin + row * 64 + f0 + 2 * f));
+      cl[f] = pair2(c.x, c.y); cl[f + 1] = pair2(c.z, c.w);
+      sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
     }
+    const uint64_t minus = pair2(-1.f, -1.f);
     uint8_t* rot = sm + P.rot;
     Ring br;
     for (int i = 0; i < count; ++i, br.next(P.SK + 1)) {
@@ -517,20 +552,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         tmem_wait_ld();
         uint32_t y0[8], y1[8];
 #pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const float4 c4 = *reinterpret_cast<const float4*>(base + 16 * g + k);
-          const float4 s4 = *reinterpret_cast<const float4*>(base + 64 + 16 * g + k);
-          const float cb[4] = {c4.x, c4.y, c4.z, c4.w}, sb[4] = {s4.x, s4.y, s4.z, s4.w};
-          float z0[4], z1[4];
+        for (int k = 0; k < 8; k += 2) {
+          const float4 c4 = *reinterpret_cast<const float4*>(base + 16 * g + 2 * k);
+          const float4 s4 = *reinterpret_cast<const float4*>(base + 64 + 16 * g + 2 * k);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int f = 16 * g + k + e;
-            const float c = fmaf(cb[e], cl[f], -sb[e] * sl[f]), s = fmaf(sb[e], cl[f], cb[e] * sl[f]);
-            z0[e] = fmaf(u0[k + e], c, -u1[k + e] * s);
-            z1[e] = fmaf(u0[k + e], s, u1[k + e] * c);
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t cb = e == 0 ? pair2(c4.x, c4.y) : pair2(c4.z, c4.w), sb = e == 0 ? pair2(s4.x, s4.y) : pair2(s4.z, s4.w);
+            const int f = 8 * g + k + e;
+            const uint64_t c = fma2(mul2(sb, sl[f]), minus, mul2(cb, cl[f])), sn = fma2(sb, cl[f], mul2(cb, sl[f]));
+            const uint64_t x0 = pair2(u0[2 * (k + e)], u0[2 * (k + e) + 1]), x1 = pair2(u1[2 * (k + e)], u1[2 * (k + e) + 1]);
+            y0[k + e] = pack2(fma2(mul2(x1, sn), minus, mul2(x0, c)));
+            y1[k + e] = pack2(fma2(x0, sn, mul2(x1, c)));
           }
-          y0[k / 2] = pack_bf16(z0[0], z0[1]); y0[k / 2 + 1] = pack_bf16(z0[2], z0[3]);
-          y1[k / 2] = pack_bf16(z1[0], z1[1]); y1[k / 2 + 1] = pack_bf16(z1[2], z1[3]);
         }
         if (g == 1) {                                 // U and the base row have been read
           tc_fence_before();
@@ -556,13 +589,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
     const uint32_t t_s = tmem + lane_base + kSCol + tok0, t_p = tmem + lane_base + P.p_col, t_d = tmem + lane_base + P.d_col;
     const bool overlay = P.p_col == kSCol;
-    const uint32_t zeros[16] = {};
-    auto zero_p = [&]() {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st_x16(t_p + 16 * c, zeros);
-    };
-    if (kCopies > 1 && !overlay) {
-      zero_p();                                       // the other copies' tokens stay zero
+    const uint32_t zeros[8] = {};
+    if (kCopies > 1 && !overlay) {                    // the other copies' tokens stay zero
+      for (int c = 0; c < 64; c += 8) tmem_st_x8(t_p + c, zeros);
       tmem_wait_st();
     }
     float m_ref = -INFINITY, l = 0.f;
@@ -598,20 +627,20 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!(ok = warp_wait(bar(misc->sfull), i & 1, abort, a.status))) break;
       tc_fence_after();
       const int valid = w.L - w.t * kTile - tok0;     // of this copy's tokens
+      // (16 columns at a time, in loops: the code of all roles has to stay in the instruction caches)
       float m_tile = -INFINITY;
-      float s[32];
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        tmem_ld_x32(t_s + c, s);
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 16) {
+        float s[16];
+        tmem_ld_x16(t_s + c, s);
         tmem_wait_ld();
-        if (c + 32 <= valid) {
+        if (c + 16 > valid) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) m_tile = fmaxf(m_tile, s[k]);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (c + k < valid) m_tile = fmaxf(m_tile, s[k]);
+          for (int k = 0; k < 16; ++k)
+            if (c + k >= valid) s[k] = -INFINITY;
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) m_tile = fmaxf(m_tile, s[k]);
       }
       const bool move = m_tile > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_tile > -INFINITY);
       // P and (where it is rescaled) D are at rest once the product of tile i - 1 is done
@@ -631,34 +660,34 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         l *= alpha;
       }
       if (move) m_ref = m_tile;
-      if (kCopies > 1 && overlay) {
-        // (P over S: every warp of this row's lanes has S in registers or reads its own columns below)
-        tmem_wait_st();
-      }
       const float ref = m_ref == -INFINITY ? 0.f : m_ref;   // (nothing above -inf yet: weights of 0)
-      uint32_t packed[kCols / 2];
+      // weights, in bf16 as the product takes them; l adds up what was rounded.  Where P lies over S, the
+      // weights of 16 columns go to 8 that lie before or among them and have been read.
+      float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 16) {
+        float s[16];
+        tmem_ld_x16(t_s + c, s);
+        tmem_wait_ld();
+        if (c + 16 > valid) {
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        if (kCols > 32) {
-          tmem_ld_x32(t_s + c, s);
-          tmem_wait_ld();
+          for (int k = 0; k < 16; ++k)
+            if (c + k >= valid) s[k] = -INFINITY;
         }
+        uint32_t x[8];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          const float p0 = c + k < valid ? exp2f(s[k] - ref) : 0.f, p1 = c + k + 1 < valid ? exp2f(s[k + 1] - ref) : 0.f;
-          const uint32_t x = pack_bf16(p0, p1);
-          packed[(c + k) / 2] = x;
-          l += __uint_as_float(x << 16) + __uint_as_float(x & 0xFFFF0000u);
+        for (int k = 0; k < 8; ++k) {
+          x[k] = pack_bf16(exp2_fast(s[2 * k] - ref), exp2_fast(s[2 * k + 1] - ref));
+          l0 += __uint_as_float(x[k] << 16);
+          l1 += __uint_as_float(x[k] & 0xFFFF0000u);
         }
+        tmem_st_x8(t_p + (tok0 + c) / 2, x);
       }
-      if (kCopies > 1 && overlay) zero_p();
-      if (kCopies > 1 && overlay) tmem_wait_st();
-#pragma unroll
-      for (int c = 0; c < kCols / 2; c += 16) {
-        uint32_t x[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = packed[c + k];
-        tmem_st_x16(t_p + tok0 / 2 + c, x);
+      l += l0 + l1;
+      if (kCopies > 1 && overlay) {                   // S of the other copies' tokens makes way for zeros
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 8)
+          if (c < tok0 / 2 || c >= (tok0 + kCols) / 2) tmem_st_x8(t_p + c, zeros);
       }
       tmem_wait_st();
       tc_fence_before();
