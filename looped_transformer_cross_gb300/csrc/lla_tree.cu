@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_
     }
   }
   if (row < rows) {
-    float* rec = a.records + ((unit * a.splits + split) * a.max_nodes + row0 + row) * (a.r_v + kRecordHead);
-    if (part == 0) { rec[0] = m; rec[1] = l; }
+    float* rec = a.records + ((unit * a.splits + split) * a.rec_rows + row0 + row) * (a.r_v + kTreeHead);
+    if (part == 0) { rec[0] = m; rec[1] = l; rec[2] = rec[3] = rec[4] = 0.f; }
 #pragma unroll
     for (int i = 0; i < kMaxRankPerHead / 8; ++i)
-      if (i < nv) rec[kRecordHead + part + 8 * i] = acc[i];
+      if (i < nv) rec[kTreeHead + part + 8 * i] = acc[i];
   }
 }
 
@@ -223,20 +223,23 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     if (flag) node_pos(a, first + i, true);
   }
   __syncthreads();
-  // the unit's records: consecutive, each max_nodes rows
+  // the records of this block's nodes are consecutive (a block of nodes lies in one group of 64)
+  const int row_first = blockIdx.y * kFinishRows;
   int64_t rec_at = unit * a.splits;
-  int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
-  if (a.copies > 0) {
-    const int64_t t0 = a.tile_start[b], nb = a.tile_start[b + 1] - t0;
+  int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk), rec_row0 = 0;
+  if (a.groups > 0) {
+    const int g = row_first / kTreeGroup, ng = (n + kTreeGroup - 1) / kTreeGroup;
+    rec_row0 = g * kTreeGroup;
+    const int64_t t0 = a.tile_start[b], nb = (a.tile_start[b + 1] - t0) / ng;
     const int64_t share = max(static_cast<int64_t>(1), (static_cast<int64_t>(a.tile_start[a.B]) * a.H + a.grid - 1) / a.grid);
-    const int64_t f0 = t0 * a.H + h * nb;
+    const int64_t f0 = t0 * a.H + (h * ng + g) * nb;
     const int64_t c0 = f0 / share, c1 = nb > 0 ? (f0 + nb - 1) / share + 1 : c0;
-    rec_at = (unit + c0) * a.copies;
-    nsplit = static_cast<int>(c1 - c0) * a.copies;
+    rec_at = unit * a.groups + g + c0;
+    nsplit = static_cast<int>(c1 - c0);
   }
-  const int stride = a.r_v + kRecordHead;
+  const int stride = a.r_v + kTreeHead;
 
-  for (int row = blockIdx.y * kFinishRows; row < min(n, (static_cast<int>(blockIdx.y) + 1) * kFinishRows); ++row) {
+  for (int row = row_first; row < min(n, row_first + kFinishRows); ++row) {
     const int entry = first + row;
     __syncthreads();
     if (tid == 0) {
@@ -272,14 +275,17 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     // the largest of the path's scores and of the records' maxima
     float m = -INFINITY;
     for (int i = 0; i < nd; ++i) m = fmaxf(m, sc[i]);
-    const float* rec0 = a.records + (rec_at * a.max_nodes + row) * stride;
-    const int64_t next = static_cast<int64_t>(a.max_nodes) * stride;
+    const float* rec0 = a.records + (rec_at * a.rec_rows + row - rec_row0) * stride;
+    const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
     for (int i = 0; i < nsplit; ++i) m = fmaxf(m, rec0[i * next]);
     float held = 0.f;
-    for (int i = 0; i < nsplit; ++i) held = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + 1], held);
+    for (int i = 0; i < nsplit; ++i) {
+      const float* r = rec0 + i * next;
+      held = fmaf(exp2f(r[0] - m), (r[1] + r[2]) + (r[3] + r[4]), held);
+    }
     for (int c = tid; c < a.r_v; c += kFinishThreads) {
       float x = 0.f;
-      for (int i = 0; i < nsplit; ++i) x = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + kRecordHead + c], x);
+      for (int i = 0; i < nsplit; ++i) x = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + kTreeHead + c], x);
       A[c] = x;
     }
     __syncthreads();
@@ -351,6 +357,12 @@ struct View {
 // Pages that the tensor-core kernel's copies take (0: dense).
 bool tensor_pages(int page_size) { return page_size == 0 || (page_size >= 8 && tile_kernel_page_size(page_size)); }
 
+// Shapes of the tensor-core kernel: those whose operands fit for any number of nodes.
+bool tensor_path(const lla_dims* d) {
+  TreePlan p;
+  return d->dtype == LLA_BF16 && make_tree_plan(d->r_k, d->r_v, kTreeGroup, &p);
+}
+
 // Workspace: status word; tensor-core kernel: the plan, the mu and the query operands; the records.
 struct TreeWs {
   int64_t chunk;
@@ -361,18 +373,19 @@ struct TreeWs {
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
   TreeWs w{};
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * d->H);
-  const size_t rec = static_cast<size_t>(max_nodes) * (d->r_v + kRecordHead) * 4;
+  const int groups = (max_nodes + kTreeGroup - 1) / kTreeGroup;
+  const size_t rec = static_cast<size_t>(tensor ? std::min(max_nodes, kTreeGroup) : max_nodes) * (d->r_v + kTreeHead) * 4;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   if (tensor) {
-    const int copies = tree_copies(max_nodes);
-    const int64_t most = units * std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
+    const int64_t most = units * groups * std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
     w.grid = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxGrid), most));
+    w.chunk = w.splits = 1;
     w.tile_start = 256;
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
     w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
-    w.records = w.qimg + static_cast<size_t>(units) * (32768 / copies);
-    w.total = w.records + static_cast<size_t>(units + w.grid) * copies * rec;
+    w.records = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 256;
+    w.total = w.records + static_cast<size_t>(units * groups + w.grid) * rec;
     return w;
   }
   // plain kernel: about four blocks an SM, splits of whole tiles
@@ -438,7 +451,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   if (tree->max_nodes > kTreeMaxNodes || cache.L_max > (int64_t(1) << 30) ||
       static_cast<int64_t>(tree->B) * dims->H > (int64_t(1) << 24) ||
       static_cast<int64_t>(tree->n_tok) * dims->H >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(tree->B) * dims->H * ((cache.L_max + kTile - 1) / kTile) >= (int64_t(1) << 31))
+      static_cast<int64_t>(tree->B) * dims->H * ((cache.L_max + kTile - 1) / kTile) >= (int64_t(1) << 30))
     return LLA_ERR_UNSUPPORTED;
   if (tree->B == 0 || tree->n_tok == 0) return LLA_OK;
   if (rope_len < cache.L_max || rope_len < kTile) return LLA_ERR_INVALID_ARG;
@@ -463,7 +476,8 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
   TreeArgs a{};
-  const bool tensor = dims->dtype == LLA_BF16 && tensor_pages(cache.page_size) && make_tree_plan(dims->r_k, dims->r_v, &a.plan);
+  const bool tensor = tensor_path(dims) && tensor_pages(cache.page_size) &&
+                      make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes), &a.plan);
   const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms, tensor);
   if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   a.B = tree->B;
@@ -502,14 +516,16 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   a.lse = lse;
   a.status = static_cast<uint32_t*>(workspace);
   a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.records);
+  a.rec_rows = a.max_nodes;
   a.splits = w.splits;
   a.chunk = w.chunk;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dims->dtype == LLA_BF16;
   if (tensor) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.copies = tree_copies(a.max_nodes);
-    a.rows = kTile / a.copies;
+    a.groups = (a.max_nodes + kTreeGroup - 1) / kTreeGroup;
+    a.rows = tree_rows(a.max_nodes);
+    a.rec_rows = std::min(a.max_nodes, kTreeGroup);
     a.grid = w.grid;
     a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
@@ -530,8 +546,7 @@ extern "C" {
 
 const char* lla_tree_kernel(const lla_dims* dims, int page_size) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || page_size < 0) return nullptr;
-  TreePlan p;
-  return dims->dtype == LLA_BF16 && tensor_pages(page_size) && make_tree_plan(dims->r_k, dims->r_v, &p) ? "tensor" : "plain";
+  return tensor_path(dims) && tensor_pages(page_size) ? "tensor" : "plain";
 }
 
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max) {
@@ -540,9 +555,7 @@ size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64
     return 0;
   // either kernel: which one a call takes depends on its page size too
   const int sms = std::max(1, device_sm_count());
-  TreePlan p;
-  const bool tensor = dims->dtype == LLA_BF16 && make_tree_plan(dims->r_k, dims->r_v, &p);
-  return std::max(tree_ws(dims, B, max_nodes, L_max, sms, false).total, tensor ? tree_ws(dims, B, max_nodes, L_max, sms, true).total : 0);
+  return std::max(tree_ws(dims, B, max_nodes, L_max, sms, false).total, tensor_path(dims) ? tree_ws(dims, B, max_nodes, L_max, sms, true).total : 0);
 }
 
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,

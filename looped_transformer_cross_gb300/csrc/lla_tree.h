@@ -8,6 +8,8 @@
 namespace lla {
 
 constexpr int kTreeMaxNodes = LLA_TREE_MAX_NODES;
+constexpr int kTreeGroup = 64;          // nodes of a unit of the tensor-core kernel
+constexpr int kTreeHead = 8;            // a record row: {reference, up to four sums, -, -, -, acc[r_v]}
 constexpr int kTreePlainRows = 32;      // nodes of a plain block
 constexpr int kTreePlainTile = 32;      // cached tokens it takes at a time
 
@@ -15,8 +17,8 @@ constexpr int kTreePlainTile = 32;      // cached tokens it takes at a time
 struct TreePlan {
   ChunkPlan kplan, vplan;            // K latents and W (64/32/16 wide); V latents (32 wide)
   int SK, SV, k_stage, v_stage;      // rings of K and V tiles
-  int v_ring, k_ring, w, q, rot, ones, mu, base, misc, bytes;
-  int p_col, d_col;                  // TMEM columns of the weights and of the latent sums
+  int blocks;                        // blocks of 128 V columns
+  int v_ring, k_ring, w, q, p, ones, mu, base, refs, misc, bytes;
 };
 
 struct TreeMaps {
@@ -50,18 +52,17 @@ struct TreeArgs {
   void* out;                         // [n_tok][H][128]
   float* lse;                        // [n_tok][H] or nullptr
   uint32_t* status;
-  // Partial results of the cached tokens: a record holds max_nodes rows of {m, l, -, -, acc[r_v]}
-  // (m in log2 units).  Plain kernel: record unit * splits + s covers tokens s * chunk ..; a unit
-  // is b H + h.
+  // Partial results of the cached tokens: a record holds rec_rows rows of {m, l's, acc[r_v]}, acc and
+  // l relative to 2^m.  Plain kernel: record (b H + h) * splits + s covers tokens s * chunk ..
   float* records;
-  int splits;
+  int rec_rows, splits;
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
-  // Tensor-core kernel (copies > 0): record ((unit + CTA) * copies + c) of every (unit, CTA) that
-  // share a tile
-  int copies, rows, grid;            // copies of the queries in S, rows of a copy, CTAs
+  // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of 64 nodes, and record
+  // unit + CTA belongs to every (unit, CTA) that share a tile
+  int groups, rows, grid;            // blocks of nodes a sequence may have, nodes S has room for, CTAs
   int32_t* tile_start;               // [B + 1]: tiles of one head before sequence b
   int4* cta_start;                   // [grid]: first (sequence, head, tile), number of tiles
-  uint8_t* qimg;                     // [B H][rows * 256] query operands
+  uint8_t* qimg;                     // [units][rows * 256] query operands
   uint8_t* bias;                     // [H][4096] mu operands
   TreePlan plan;
 };
@@ -85,10 +86,10 @@ __device__ __forceinline__ int tree_cached(const TreeArgs& a, int b, bool flag) 
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
+// Nodes that S has room for in calls of up to max_nodes a sequence.
+inline int tree_rows(int max_nodes) { return max_nodes <= 16 ? 16 : max_nodes <= 32 ? 32 : 64; }
 // False where the operands do not fit in shared memory.
-bool make_tree_plan(int r_k, int r_v, TreePlan* p);
-// Copies of the queries for calls of up to max_nodes nodes a sequence.
-inline int tree_copies(int max_nodes) { return max_nodes <= 32 ? 4 : max_nodes <= 64 ? 2 : 1; }
+bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p);
 cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);
 cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_tree_finish(const TreeArgs& a, bool bf16, cudaStream_t s);

@@ -1,22 +1,26 @@
 // lla_tree_tc.cu — lla_tree_attn over bf16 latents on the tensor cores: the cached tokens'
 // part of every node's softmax, one record (m, l, latent sum) per (unit, CTA, node).
 //
-// A unit is one (sequence, head); the flat list of its 128-token tiles over all units is cut into
-// equal contiguous ranges, one persistent CTA per SM.  Per tile, three matrix products:
-//   U = C_k W^T + mu          128 tokens x 128 dimensions, tcgen05, latents by TMA
-//   S = Q^ K^^T               queries x 128 tokens; Q^ (rotated, scaled to log2 units) comes from
-//                             tree_prepare_kernel, K^ is U rotated by the epilogue below
-//   D += P C_v                queries x r_v, P from TMEM, V latents as the MN-major operand
-// so a key is reconstructed and rotated once for all nodes of its sequence, and V never is.
-// The rows of S are nodes: a softmax row is one thread's own, with no exchange between lanes.
-// S always has 128 rows; with at most 64 (32) nodes they are two (four) copies of the queries,
-// and each copy's warps take every second (fourth) stretch of tokens, leaving zeros in P elsewhere, so
-// that all four softmax warps have work and the copies' sums are merged like any other records.
+// A unit is (sequence, head, block of up to 64 nodes); the flat list of the units' 128-token tiles is
+// cut into equal contiguous ranges, one persistent CTA per SM.  Per tile, three matrix products,
+// tokens in the rows of the first two:
+//   U = C_k W^T + mu          128 tokens x 128 dimensions, latents by TMA
+//   S = K^ Q^^T               128 tokens x nodes: K^ is U rotated and rounded to bf16 by the warps below,
+//                             read from TMEM; Q^ (rotated, scaled to log2 units) from tree_prepare_kernel
+//   D += C_v^T P              r_v x nodes, both operands MN-major from shared memory
+// so a key is reconstructed and rotated once for all nodes of its sequence, V never is, and the
+// products and exponentials of S and D are made for 16, 32 or 64 nodes, not for a full 128 rows.
+// Weights are 2^(s - ref) with one reference per node and unit: the largest score of the unit's first
+// tile.  Scores further on only have to stay below ref + 32 (bf16 keeps its digits at any size, and
+// fp32 sums have the range); the softmax warps vote on that for every tile, and a tile that breaks it
+// moves the references and rescales D.
 //
-// Roles: warp 0 copies K and V tiles, warp 1 issues U and S, warp 2 issues D, warp 3 copies each
-// unit's W and Q^; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies each, one token
-// per lane), warps 12..15 do the softmax.  cos/sin of a token's angle are the angle sum of the tile's
-// base row (shared memory) and the lane's own row (registers).
+// Roles: warp 0 copies K and V tiles and RoPE rows, warp 1 issues U (and copies W), warp 2 issues S
+// (and copies Q^), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
+// each, one token per lane), warps 12..15 do the softmax, one token per lane.  cos/sin of a token's
+// angle are the angle sum of the tile's base row (shared memory) and the lane's own row (registers).
+// The roles' loops are kept short on purpose: with bodies unrolled all the way, instruction fetch took
+// more time than anything else.
 #include <algorithm>
 #include <cmath>
 
@@ -28,29 +32,31 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
-constexpr float kRescaleLog2 = 8.f;                 // the reference moves when the maximum passes it by 2^8
+constexpr float kHeadroom = 32.f;                   // a score this far above its reference (log2 units) moves it
 constexpr int kPrepThreads = 256;
 constexpr int kRotWarps = 8;
 constexpr int kSoftWarp0 = 4 + kRotWarps;
 constexpr int kTreeThreads = 32 * (kSoftWarp0 + 4);
-constexpr int kUCol = 0, kSCol = 128;               // TMEM columns
+constexpr int kKhatCol = 256;                       // TMEM columns: U 0..255 (two), K^, S, D
 
 struct alignas(16) TreeMisc {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages];
-  uint64_t bfull[kMaxStages + 1];                   // a tile's base row of the RoPE table
+  uint64_t bfull[kMaxStages + 2];                   // a tile's base row of the RoPE table
   uint64_t wfull, wfree, qfull, qfree;              // the unit's W and bias; its queries
-  uint64_t ufull, ufree;                            // U computed; read by the rotating warps
-  uint64_t rfull;                                   // rotated keys in shared memory
-  uint64_t sfull;                                   // S computed (and the rotated keys read)
-  uint64_t pfull, vdone;                            // P written (and S read); D += P C_v done
-  uint64_t done[2];
+  uint64_t ufull[2], ufree[2];                      // U computed; read by the rotating warps
+  uint64_t rfull[2];                                // K^ written
+  uint64_t sfull[2], sfree[2];                      // S computed (and K^ read); S read
+  uint64_t pfull[2], vdone[2];                      // P written; D += C_v^T P done
+  uint64_t vote;                                    // the four softmax warps
+  uint64_t done[3];
   uint32_t tmem_base;
   int abort;
+  int over[2];                                      // tile + 1 in which a score passed its headroom
 };
-static_assert(sizeof(TreeMisc) <= 512, "misc region");
+static_assert(sizeof(TreeMisc) <= 1024, "misc region");
 
 struct Walk {
-  int b, h, t, nb, L;
+  int b, h, g, t, ng, nb, L;        // block g of ng of the sequence's nodes; tile t of nb
 };
 
 // Tiles of sequence b: none without nodes.
@@ -58,12 +64,15 @@ __device__ __forceinline__ void walk_load(Walk& w, const TreeArgs& a) {
   int first;
   const int n = tree_nodes(a, w.b, first, false);
   w.L = tree_cached(a, w.b, false);
+  w.ng = (n + kTreeGroup - 1) / kTreeGroup;
   w.nb = n > 0 ? (w.L + kTile - 1) / kTile : 0;
 }
 
 __device__ __forceinline__ void walk_next(Walk& w, const TreeArgs& a) {
   if (++w.t < w.nb) return;
   w.t = 0;
+  if (++w.g < w.ng) return;
+  w.g = 0;
   if (++w.h < a.H) return;
   w.h = 0;
   while (true) {
@@ -166,14 +175,16 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
-  const int units = a.B * a.H;
+  const int units = a.B * a.H * a.groups;
   if (blockIdx.x < units) {
-    const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H;
+    const int bh = blockIdx.x / a.groups, g = blockIdx.x - bh * a.groups;
+    const int b = bh / a.H, h = bh - b * a.H;
     int first;
-    const int n = tree_nodes(a, b, first, false);
+    const int n = tree_nodes(a, b, first, false) - g * kTreeGroup;
     const int L = tree_cached(a, b, false);
-    if (n == 0 || L == 0) return;
-    if (a.block_table && h == 0) {
+    if (n <= 0 || L == 0) return;
+    first += g * kTreeGroup;
+    if (a.block_table && h == 0 && g == 0) {
       const int used = (L + a.page_size - 1) / a.page_size;
       for (int lp = tid; lp < used; lp += kPrepThreads) {
         const int pg = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + lp);
@@ -243,11 +254,11 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
   __shared__ int starts[kHeld];
   const int per = (a.B + kPrepThreads - 1) / kPrepThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  auto tiles = [&](int b) {
+  auto tiles = [&](int b) {          // of one head
     Walk w;
     w.b = b;
     walk_load(w, a);
-    return w.nb;
+    return w.nb * w.ng;
   };
   int sum = 0;
   for (int b = b0; b < b1; ++b) sum += tiles(b);
@@ -282,8 +293,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
         else hi = mid;
       }
       const int64_t rem = f0 - static_cast<int64_t>(lo < kHeld ? starts[lo] : __ldcg(a.tile_start + lo)) * a.H;
-      const int nb = tiles(lo);
-      s = make_int4(lo, static_cast<int>(rem / nb), static_cast<int>(rem % nb), static_cast<int>(min(share, total - f0)));
+      // (z: the tile among the head's, over all its blocks of nodes)
+      const int nt = tiles(lo);
+      s = make_int4(lo, static_cast<int>(rem / nt), static_cast<int>(rem % nt), static_cast<int>(min(share, total - f0)));
     }
     a.cta_start[c] = s;
   }
@@ -291,11 +303,15 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
 
 // ---------------------------------------------------------------- the cached tokens
 
-// kPage: 0 dense, 1 pages of a multiple of 128 tokens, 2 pages of 8..64 tokens.  kCopies: copies of
-// the queries in S's rows (4: at most 32 nodes, 2: 64, 1: 128).
-template <int kPage, int kCopies>
+// kPage: 0 dense, 1 pages of a multiple of 128 tokens, 2 pages of 8..64 tokens.  kRows: nodes that S
+// and D have room for (16, 32 or 64).
+template <int kPage, int kRows>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
+  constexpr int kBuf = kRows <= 32 ? 2 : 1;           // buffers of K^ and of S (TMEM has 512 columns)
+  constexpr int kSCol = kKhatCol + 64 * kBuf, kDCol = kSCol + kRows * kBuf;
+  static_assert(kDCol + 2 * kRows <= 512, "TMEM columns");
+  constexpr uint32_t kPRow = kRows * 2;               // bytes of a token's weights
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const TreePlan& P = a.plan;
@@ -304,21 +320,26 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   volatile int* abort = &misc->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](const uint64_t& m) { return smem_u32(&m); };
+  auto wait = [&](const uint64_t& m, uint32_t parity) { return warp_wait(smem_u32(&m), parity & 1u, abort, a.status); };
 
   if (tid == 0) {
     misc->abort = 0;
-    for (int s = 0; s <= kMaxStages; ++s) mbar_init(bar(misc->bfull[s]), 1);
+    misc->over[0] = misc->over[1] = 0;
+    for (int s = 0; s < kMaxStages + 2; ++s) mbar_init(bar(misc->bfull[s]), 1);
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(bar(misc->kfull[s]), 1); mbar_init(bar(misc->kempty[s]), 1);
       mbar_init(bar(misc->vfull[s]), 1); mbar_init(bar(misc->vempty[s]), 1);
     }
     mbar_init(bar(misc->wfull), 1); mbar_init(bar(misc->wfree), 1);
     mbar_init(bar(misc->qfull), 1); mbar_init(bar(misc->qfree), 1);
-    mbar_init(bar(misc->ufull), 1); mbar_init(bar(misc->ufree), kRotWarps);
-    mbar_init(bar(misc->rfull), kRotWarps);
-    mbar_init(bar(misc->sfull), 1);
-    mbar_init(bar(misc->pfull), 4); mbar_init(bar(misc->vdone), 1);
-    mbar_init(bar(misc->done[0]), 1); mbar_init(bar(misc->done[1]), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(misc->ufull[s]), 1); mbar_init(bar(misc->ufree[s]), kRotWarps);
+      mbar_init(bar(misc->rfull[s]), kRotWarps);
+      mbar_init(bar(misc->sfull[s]), 1); mbar_init(bar(misc->sfree[s]), 4);
+      mbar_init(bar(misc->pfull[s]), 4); mbar_init(bar(misc->vdone[s]), 1);
+    }
+    mbar_init(bar(misc->vote), 4);
+    for (int s = 0; s < 3; ++s) mbar_init(bar(misc->done[s]), 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -343,23 +364,36 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   Walk w;
   w.b = first_tile.x;
   w.h = first_tile.y;
-  w.t = first_tile.z;
-  if (count > 0) walk_load(w, a);
-  auto agree = [](bool r) { return __all_sync(0xffffffffu, r); };
+  w.g = w.t = 0;
+  if (count > 0) {
+    walk_load(w, a);
+    w.g = first_tile.z / w.nb;
+    w.t = first_tile.z - w.g * w.nb;
+  }
+  // this warp's products complete before TMEM is released
+  auto products_done = [&](uint64_t& m) {
+    umma_commit_warp(bar(m));
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar(m), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  };
+  // the copy that completes phase `phase` (from 0 on; below 0: none) of a barrier lands before the CTA can exit
+  auto landed = [&](uint64_t& m, int phase) {
+    const uint64_t t0 = global_timer_ns();
+    while (phase >= 0 && !mbar_try_wait(bar(m), phase & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
+  };
 
   if (warp == 0) {
-    // ======================================================== K and V tiles
-    // (V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.)  Tile i's base row
-    // goes to slot i mod SK + 1: K tile i + SK + 1 is requested once U(i + 1) is computed, for which
-    // every rotating warp has read the base row of tile i.
+    // ======================================================== K and V tiles, RoPE rows
+    // V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.  Tile i's base row goes
+    // to slot i mod SK + 2: K tile i + SK + 2 is requested once U(i + 2) is computed, for which every
+    // rotating warp has read U(i) and, before that, the base row of tile i.
     Walk wv = w;
     Ring kr, vr, br;
     int issued_k = 0, issued_v = 0;
     for (int i = 0; i <= count && count > 0; ++i) {
       if (i < count) {
-        if (!warp_wait(bar(misc->kempty[kr.slot]), kr.phase ^ 1u, abort, a.status)) break;
-        const uint32_t kb = bar(misc->kfull[kr.slot]);
-        load_tile<kPage>(a, w, sbase + P.k_ring + kr.slot * P.k_stage, kb, P.kplan,
+        if (!wait(misc->kempty[kr.slot], kr.phase ^ 1u)) break;
+        load_tile<kPage>(a, w, sbase + P.k_ring + kr.slot * P.k_stage, bar(misc->kfull[kr.slot]), P.kplan,
                          [&](int c) { return &maps.k[chunk_map_index(P.kplan.width[c])]; });
         if (lane == 0) {
           const uint32_t bb = bar(misc->bfull[br.slot]), dst = sbase + P.base + br.slot * 512;
@@ -369,11 +403,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         }
         issued_k = i + 1;
         kr.next(P.SK);
-        br.next(P.SK + 1);
+        br.next(P.SK + 2);
         walk_next(w, a);
       }
       if (i > 0) {
-        if (!warp_wait(bar(misc->vempty[vr.slot]), vr.phase ^ 1u, abort, a.status)) break;
+        if (!wait(misc->vempty[vr.slot], vr.phase ^ 1u)) break;
         load_tile<kPage>(a, wv, sbase + P.v_ring + vr.slot * P.v_stage, bar(misc->vfull[vr.slot]), P.vplan,
                          [&](int) { return &maps.v; });
         issued_v = i;
@@ -381,120 +415,97 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         walk_next(wv, a);
       }
     }
-    // every copy lands before the CTA can exit
-    auto drain = [&](uint64_t* full, int n, int issued) {
-      for (int i = max(0, issued - n); i < issued; ++i) {
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(bar(full[i % n]), (i / n) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
-      }
-    };
     if (lane == 0) {
-      drain(misc->kfull, P.SK, issued_k);
-      drain(misc->vfull, P.SV, issued_v);
-      drain(misc->bfull, P.SK + 1, issued_k);
-    }
-  } else if (warp == 3) {
-    // ======================================================== a unit's weights and queries
-    if (lane == 0) {
-      int unit = 0, issued_w = 0, issued_q = 0;
-      for (int i = 0; i < count; ++unit) {
-        const int left = min(w.nb - w.t, count - i);
-        if (unit > 0 && !mbar_wait(bar(misc->wfree), (unit - 1) & 1, abort, a.status)) break;
-        const uint32_t wf = bar(misc->wfull);
-        mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
-        for (int c = 0; c < P.kplan.n; ++c)
-          tma_load_4d(sbase + P.w + P.kplan.off[c], &maps.w[chunk_map_index(P.kplan.width[c])], wf, P.kplan.start[c], 0, 0, w.h);
-        bulk_load(sbase + P.mu, a.bias + static_cast<int64_t>(w.h) * 4096, 4096, wf);
-        issued_w = unit + 1;
-        if (unit > 0 && !mbar_wait(bar(misc->qfree), (unit - 1) & 1, abort, a.status)) break;
-        const uint32_t qf = bar(misc->qfull);
-        mbar_arrive_expect_tx(qf, 32768);
-        const uint8_t* img = a.qimg + static_cast<int64_t>(w.b * a.H + w.h) * (32768 / kCopies);
-        constexpr uint32_t part = 16384 / kCopies;       // a copy's rows of one chunk
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int c = 0; c < kCopies; ++c) bulk_load(sbase + P.q + k * 16384 + c * part, img + k * part, part, qf);
-        issued_q = unit + 1;
-        i += left;
-        w.t += left - 1;
-        walk_next(w, a);
-      }
-      auto drain = [&](const uint64_t& full, int issued) {
-        const uint64_t t0 = global_timer_ns();
-        while (issued > 0 && !mbar_try_wait(bar(full), (issued - 1) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {}
-      };
-      drain(misc->wfull, issued_w);
-      drain(misc->qfull, issued_q);
+      for (int i = max(0, issued_k - P.SK); i < issued_k; ++i) landed(misc->kfull[i % P.SK], i / P.SK);
+      for (int i = max(0, issued_k - P.SK - 2); i < issued_k; ++i) landed(misc->bfull[i % (P.SK + 2)], i / (P.SK + 2));
+      for (int i = max(0, issued_v - P.SV); i < issued_v; ++i) landed(misc->vfull[i % P.SV], i / P.SV);
     }
   } else if (warp == 1) {
-    // ======================================================== U(i + 1), then S(i)
+    // ======================================================== U = C_k W^T + mu
     const uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
     const uint64_t d_ones = umma_desc(sbase + P.ones, 16, 256, kSw32), d_mu = umma_desc(sbase + P.mu, 16, 256, kSw32);
-    const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128), d_r = umma_desc(sbase + P.rot, 16, 1024, kSw128);
-    Walk ws = w;
     Ring kr;
-    int unit_u = -1, unit_s = -1;
-    bool ok = true;
-    for (int i = 0; i <= count && count > 0 && ok; ++i) {
-      if (i < count) {
-        if (i == 0 || w.t == 0) {
-          ++unit_u;
-          if (!(ok = agree(mbar_wait(bar(misc->wfull), unit_u & 1, abort, a.status)))) break;
+    int unit = -1;
+    for (int i = 0; i < count; ++i) {
+      if (i == 0 || w.t == 0) {
+        if (unit >= 0 && !wait(misc->wfree, unit)) break;
+        ++unit;
+        if (lane == 0) {
+          const uint32_t wf = bar(misc->wfull);
+          mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
+          for (int c = 0; c < P.kplan.n; ++c)
+            tma_load_4d(sbase + P.w + P.kplan.off[c], &maps.w[chunk_map_index(P.kplan.width[c])], wf, P.kplan.start[c], 0, 0, w.h);
+          bulk_load(sbase + P.mu, a.bias + static_cast<int64_t>(w.h) * 4096, 4096, wf);
         }
-        if (!(ok = agree(mbar_wait(bar(misc->kfull[kr.slot]), kr.phase, abort, a.status)))) break;
-        if (i > 0 && !(ok = agree(mbar_wait(bar(misc->ufree), (i - 1) & 1, abort, a.status)))) break;
-        tc_fence_after();
-        const uint32_t ka = sbase + P.k_ring + kr.slot * P.k_stage;
-        uint32_t acc = 0;
-        for (int c = 0; c < P.kplan.n; ++c) {
-          const int rb = P.kplan.width[c] * 2;
-          const uint32_t lay = sw_mode_for_row_bytes(rb);
-          const uint64_t a0 = umma_desc(ka + P.kplan.off[c], 16, 8 * rb, lay);
-          const uint64_t b0 = umma_desc(sbase + P.w + P.kplan.off[c], 16, 8 * rb, lay);
-          for (int k = 0; k < P.kplan.width[c] / 16; ++k) {
-            umma_bf16_warp(tmem + kUCol, a0 + 2 * k, b0 + 2 * k, idesc, acc);
-            acc = 1;
-          }
-        }
-        umma_bf16_warp(tmem + kUCol, d_ones, d_mu, idesc, 1);
-        umma_commit_warp(bar(misc->kempty[kr.slot]));
-        umma_commit_warp(bar(misc->ufull));
-        if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
-        kr.next(P.SK);
-        walk_next(w, a);
+        __syncwarp();
+        if (!wait(misc->wfull, unit)) break;
       }
-      if (i > 0) {
-        const int j = i - 1;
-        if (j == 0 || ws.t == 0) {
-          ++unit_s;
-          if (!(ok = agree(mbar_wait(bar(misc->qfull), unit_s & 1, abort, a.status)))) break;
+      if (!wait(misc->kfull[kr.slot], kr.phase)) break;
+      if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;
+      tc_fence_after();
+      const uint32_t ka = sbase + P.k_ring + kr.slot * P.k_stage, d = tmem + (i & 1) * 128;
+      uint32_t acc = 0;
+      for (int c = 0; c < P.kplan.n; ++c) {
+        const int rb = P.kplan.width[c] * 2;
+        const uint32_t lay = sw_mode_for_row_bytes(rb);
+        const uint64_t a0 = umma_desc(ka + P.kplan.off[c], 16, 8 * rb, lay);
+        const uint64_t b0 = umma_desc(sbase + P.w + P.kplan.off[c], 16, 8 * rb, lay);
+        for (int k = 0; k < P.kplan.width[c] / 16; ++k) {
+          umma_bf16_warp(d, a0 + 2 * k, b0 + 2 * k, idesc, acc);
+          acc = 1;
         }
-        if (!(ok = agree(mbar_wait(bar(misc->rfull), j & 1, abort, a.status)))) break;
-        // S(j - 1) read; where P lies in S's columns, also P(j - 1)
-        if (j > 0 && !(ok = agree(mbar_wait(P.p_col == kSCol ? bar(misc->vdone) : bar(misc->pfull), (j - 1) & 1, abort, a.status)))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int k = 0; k < 8; ++k)
-          umma_bf16_warp(tmem + kSCol, d_q + (k >> 2) * 1024 + (k & 3) * 2, d_r + (k >> 2) * 1024 + (k & 3) * 2, idesc, k > 0);
-        umma_commit_warp(bar(misc->sfull));
-        if (ws.t == ws.nb - 1) umma_commit_warp(bar(misc->qfree));
-        walk_next(ws, a);
       }
+      umma_bf16_warp(d, d_ones, d_mu, idesc, 1);
+      umma_commit_warp(bar(misc->ufull[i & 1]));
+      umma_commit_warp(bar(misc->kempty[kr.slot]));
+      if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
+      kr.next(P.SK);
+      walk_next(w, a);
     }
-    // this warp's products complete before TMEM is released
-    umma_commit_warp(bar(misc->done[0]));
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar(misc->done[0]), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+    products_done(misc->done[0]);
+    landed(misc->wfull, unit);
   } else if (warp == 2) {
-    // ======================================================== D += P C_v
-    const uint32_t idesc = umma_idesc_bf16(128, a.r_v, false, true);
+    // ======================================================== S = K^ Q^^T
+    const uint32_t idesc = umma_idesc_bf16(128, kRows, false, false);
+    const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128);
+    int unit = -1;
+    for (int i = 0; i < count; ++i) {
+      const int sb = i % kBuf;
+      if (i == 0 || w.t == 0) {
+        if (unit >= 0 && !wait(misc->qfree, unit)) break;
+        ++unit;
+        if (lane == 0) {
+          const uint32_t qf = bar(misc->qfull);
+          mbar_arrive_expect_tx(qf, kRows * 256);
+          bulk_load(sbase + P.q, a.qimg + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * (kRows * 256), kRows * 256, qf);
+        }
+        __syncwarp();
+        if (!wait(misc->qfull, unit)) break;
+      }
+      if (!wait(misc->rfull[sb], i / kBuf)) break;
+      if (i >= kBuf && !wait(misc->sfree[sb], (i - kBuf) / kBuf)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k)
+        umma_bf16_ts_warp(tmem + kSCol + sb * kRows, tmem + kKhatCol + sb * 64 + 8 * k, d_q + (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2,
+                          idesc, k > 0);
+      umma_commit_warp(bar(misc->sfull[sb]));
+      if (w.t == w.nb - 1) umma_commit_warp(bar(misc->qfree));
+      walk_next(w, a);
+    }
+    products_done(misc->done[1]);
+    landed(misc->qfull, unit);
+  } else if (warp == 3) {
+    // ======================================================== D += C_v^T P
+    // (two blocks of 128 rows of r_v; rows past r_v read whatever follows the tile in shared memory and
+    // are not looked at)
+    const uint32_t idesc = umma_idesc_bf16(128, kRows, true, true);
     const uint64_t d_v = umma_desc(sbase + P.v_ring, kTile * 64, 512, kSw64);
+    const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));
     const uint32_t vst = static_cast<uint32_t>(P.v_stage) >> 4;
     Ring vr;
     for (int j = 0; j < count; ++j, vr.next(P.SV)) {
-      if (!agree(mbar_wait(bar(misc->vfull[vr.slot]), vr.phase, abort, a.status))) break;
-      if (!agree(mbar_wait(bar(misc->pfull), j & 1, abort, a.status))) break;
+      if (!wait(misc->vfull[vr.slot], vr.phase)) break;
       // rows past the sequence's end: whole steps of 16 tokens are left out, the rest of a partial step
       // is zeroed (it may hold anything; its weights are 0 and 0 * x stays 0)
       const int valid = min(kTile, w.L - w.t * kTile);
@@ -509,22 +520,22 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         fence_proxy_async_smem();
         __syncwarp();
       }
+      if (!wait(misc->pfull[j & 1], j >> 1)) break;
       tc_fence_after();
-      const uint64_t b0 = d_v + vr.slot * vst;
-      const uint32_t fresh = j == 0 || w.t == 0;      // a unit's first product starts the sum
-      for (int k = 0; k < steps; ++k)
-        umma_bf16_ts_warp(tmem + P.d_col, tmem + P.p_col + 8 * k, b0 + 64 * k, idesc, k > 0 || !fresh);
+      const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j & 1) * (kTile * kPRow / 16);
+      const uint32_t sum = !(j == 0 || w.t == 0);     // a unit's first product starts the sum
+      for (int blk = 0; blk < P.blocks; ++blk)
+        for (int k = 0; k < steps; ++k)
+          umma_bf16_warp(tmem + kDCol + blk * kRows, a0 + blk * (4 * kTile * 64 / 16) + 64 * k, b0 + k * kPRow, idesc, k > 0 || sum);
+      umma_commit_warp(bar(misc->vdone[j & 1]));
       umma_commit_warp(bar(misc->vempty[vr.slot]));
-      umma_commit_warp(bar(misc->vdone));
       walk_next(w, a);
     }
-    umma_commit_warp(bar(misc->done[1]));
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(bar(misc->done[1]), 0) && global_timer_ns() - t0 < kWaitLimitNs) {}
+    products_done(misc->done[2]);
   } else if (warp < kSoftWarp0) {
-    // ======================================================== rotation: U -> K^ in shared memory
+    // ======================================================== rotation: U -> K^
     const int quad = warp & 3, row = 32 * quad + lane, f0 = 32 * ((warp - 4) >> 2);
-    const uint32_t t_u = tmem + (static_cast<uint32_t>(32 * quad) << 16) + kUCol + f0;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
     uint64_t cl[16], sl[16];                          // the lane's own row of the table, by twos
 #pragma unroll
     for (int f = 0; f < 16; f += 2) {
@@ -534,15 +545,15 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
     }
     const uint64_t minus = pair2(-1.f, -1.f);
-    uint8_t* rot = sm + P.rot;
     Ring br;
-    for (int i = 0; i < count; ++i, br.next(P.SK + 1)) {
+    for (int i = 0; i < count; ++i, br.next(P.SK + 2)) {
+      const int kb = i % kBuf;
+      const uint32_t t_u = lanes + (i & 1) * 128 + f0, t_k = lanes + kKhatCol + kb * 64 + f0 / 2;
       // the tile's base row: cos, then sin
       const float* base = reinterpret_cast<const float*>(sm + P.base + br.slot * 512) + f0;
-      if (!warp_wait(bar(misc->bfull[br.slot]), br.phase, abort, a.status)) break;
-      if (!warp_wait(bar(misc->ufull), i & 1, abort, a.status)) break;
-      // K^(i - 1) has been read
-      if (i > 0 && !warp_wait(bar(misc->sfull), (i - 1) & 1, abort, a.status)) break;
+      if (!wait(misc->bfull[br.slot], br.phase)) break;
+      if (!wait(misc->ufull[i & 1], i >> 1)) break;
+      if (i >= kBuf && !wait(misc->sfull[kb], (i - kBuf) / kBuf)) break;   // the buffer's last K^ has been read
       tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -565,137 +576,190 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             y1[k + e] = pack2(fma2(x0, sn, mul2(x1, c)));
           }
         }
-        if (g == 1) {                                 // U and the base row have been read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(misc->ufree));
-        }
-        const uint32_t o = row * 128 + (f0 + 16 * g) * 2;
-        *reinterpret_cast<uint4*>(rot + swizzle_offset(o, 128)) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
-        *reinterpret_cast<uint4*>(rot + swizzle_offset(o + 16, 128)) = make_uint4(y0[4], y0[5], y0[6], y0[7]);
-        *reinterpret_cast<uint4*>(rot + 16384 + swizzle_offset(o, 128)) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
-        *reinterpret_cast<uint4*>(rot + 16384 + swizzle_offset(o + 16, 128)) = make_uint4(y1[4], y1[5], y1[6], y1[7]);
+        tmem_st_x8(t_k + 8 * g, y0);
+        tmem_st_x8(t_k + 32 + 8 * g, y1);
       }
-      fence_proxy_async_smem();
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(misc->rfull));
+      if (lane == 0) {
+        mbar_arrive(bar(misc->rfull[kb]));
+        mbar_arrive(bar(misc->ufree[i & 1]));
+      }
     }
   } else {
     // ======================================================== softmax: S -> P, records
-    constexpr int kRows = kTile / kCopies, kCols = kTile / kCopies;   // a copy's rows; its tokens of a tile
     const int quad = warp & 3, row = 32 * quad + lane;
-    const int copy = row / kRows, node = row - copy * kRows;
-    const int tok0 = copy * kCols;                    // (uniform in a warp)
-    const uint32_t lane_base = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t t_s = tmem + lane_base + kSCol + tok0, t_p = tmem + lane_base + P.p_col, t_d = tmem + lane_base + P.d_col;
-    const bool overlay = P.p_col == kSCol;
-    const uint32_t zeros[8] = {};
-    if (kCopies > 1 && !overlay) {                    // the other copies' tokens stay zero
-      for (int c = 0; c < 64; c += 8) tmem_st_x8(t_p + c, zeros);
-      tmem_wait_st();
-    }
-    float m_ref = -INFINITY, l = 0.f;
-    bool ok = true;
-    int cur_b = w.b, cur_h = w.h;
-    // the finished unit's rows (its last product was tile `last`)
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+    // references of this unit (each warp its own copy) and what they were multiplied by when they moved;
+    // the warps' maxima (two sets in turn)
+    float* ref = reinterpret_cast<float*>(sm + P.refs) + quad * kRows;
+    float* factor = reinterpret_cast<float*>(sm + P.refs) + (4 + quad) * kRows;
+    float* maxima = reinterpret_cast<float*>(sm + P.refs) + 8 * kRows;
+    int votes = 0, moves = 0;
+    auto vote = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(misc->vote));
+      return wait(misc->vote, votes++);
+    };
+    uint64_t l[kRows / 2];
+    int cur_b = w.b, cur_h = w.h, cur_g = w.g;
+    // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
+    // is higher, or if it is the unit's first
+    auto move = [&](uint32_t t_s, bool live, bool fresh) -> bool {
+      float* mine = maxima + ((moves & 1) * 4 + quad) * kRows;
+#pragma unroll 1
+      for (int c = 0; c < kRows; c += 16) {
+        float s[16];
+        tmem_ld_x16(t_s + c, s);
+        tmem_wait_ld();
+        float keep = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float m = warp_max_redux(live ? s[k] : -INFINITY);
+          if (lane == k) keep = m;
+        }
+        if (lane < 16) mine[c + lane] = keep;
+      }
+      if (!vote()) return false;
+      for (int c = lane; c < kRows; c += 32) {
+        const float* m = maxima + (moves & 1) * 4 * kRows + c;
+        float top = fmaxf(fmaxf(m[0], m[kRows]), fmaxf(m[2 * kRows], m[3 * kRows]));
+        if (fresh) top = top == -INFINITY ? 0.f : top;
+        else top = fmaxf(top, ref[c]);
+        factor[c] = exp2f(ref[c] - top);               // (not looked at for a new unit)
+        ref[c] = top;
+      }
+      ++moves;
+      __syncwarp();
+      return true;
+    };
+    // the finished unit's sums (its last product was tile `last`): D's lanes are columns of the latent
     auto finish = [&](int last) -> bool {
-      if (!warp_wait(bar(misc->vdone), last & 1, abort, a.status)) return false;
+      if (!wait(misc->vdone[last & 1], last >> 1)) return false;
       tc_fence_after();
       int first;
-      const int n = tree_nodes(a, cur_b, first, false);
-      const int64_t slot = static_cast<int64_t>(cur_b) * a.H + cur_h + blockIdx.x;
-      float* rec = a.records + ((slot * kCopies + copy) * a.max_nodes + node) * (a.r_v + kRecordHead);
-      if (node < n) *reinterpret_cast<float4*>(rec) = make_float4(m_ref, l, 0.f, 0.f);
-      for (int c = 0; c < a.r_v; c += 16) {
-        float v[16];
-        tmem_ld_x16(t_d + c, v);
-        tmem_wait_ld();
-        if (node < n) {
+      const int n = min(kTreeGroup, tree_nodes(a, cur_b, first, false) - cur_g * kTreeGroup);
+      const int64_t slot = (static_cast<int64_t>(cur_b) * a.H + cur_h) * a.groups + cur_g + blockIdx.x;
+      const int stride = a.r_v + kTreeHead;
+      float* rec = a.records + slot * a.rec_rows * stride;
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(rec + kRecordHead + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      for (int c = 0; c < kRows; c += 32) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float x = 0.f, y = 0.f;
+          if (c / 2 + k < kRows / 2) asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(l[c / 2 + k < kRows / 2 ? c / 2 + k : 0]));
+          v[2 * k] = x;
+          v[2 * k + 1] = y;
+        }
+        const float sum = warp_column_sum32(v);
+        if (c + lane < n) {
+          if (quad == 0) rec[(c + lane) * stride] = ref[c + lane];
+          rec[(c + lane) * stride + 1 + quad] = sum;
+        }
+      }
+      for (int blk = 0; blk < P.blocks; ++blk) {
+        const int r = blk * 128 + row;
+#pragma unroll 1
+        for (int c = 0; c < n; c += 16) {
+          float v[16];
+          tmem_ld_x16(lanes + kDCol + blk * kRows + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (c + k < n && r < a.r_v) rec[(c + k) * stride + kTreeHead + r] = v[k];
         }
       }
       tc_fence_before();
       return true;
     };
-    for (int i = 0; i < count; ++i) {
-      if (i > 0 && w.t == 0) {
-        if (!(ok = finish(i - 1))) break;
-        cur_b = w.b; cur_h = w.h;
-        m_ref = -INFINITY; l = 0.f;
+    for (int i = 0; i <= count && count > 0; ++i) {
+      const int sb = i % kBuf;
+      const uint32_t t_s = lanes + kSCol + sb * kRows;
+      const bool fresh = i == 0 || w.t == 0;
+      if (i > 0 && (fresh || i == count)) {
+        if (!finish(i - 1)) break;
+        cur_b = w.b; cur_h = w.h; cur_g = w.g;
       }
-      if (!(ok = warp_wait(bar(misc->sfull), i & 1, abort, a.status))) break;
+      if (i == count || !wait(misc->sfull[sb], i / kBuf)) break;
       tc_fence_after();
-      const int valid = w.L - w.t * kTile - tok0;     // of this copy's tokens
-      // (16 columns at a time, in loops: the code of all roles has to stay in the instruction caches)
-      float m_tile = -INFINITY;
+      const bool live = w.t * kTile + row < w.L;
+      bool moved = fresh;
+      if (!fresh) {
+        float top = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 16) {
-        float s[16];
-        tmem_ld_x16(t_s + c, s);
-        tmem_wait_ld();
-        if (c + 16 > valid) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (c + k >= valid) s[k] = -INFINITY;
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) m_tile = fmaxf(m_tile, s[k]);
-      }
-      const bool move = m_tile > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_tile > -INFINITY);
-      // P and (where it is rescaled) D are at rest once the product of tile i - 1 is done
-      if (i > 0 && !(ok = warp_wait(bar(misc->vdone), (i - 1) & 1, abort, a.status))) break;
-      tc_fence_after();
-      if (__any_sync(0xffffffffu, move && m_ref != -INFINITY)) {
-        const float alpha = move ? exp2f(m_ref - m_tile) : 1.f;   // (0 from a reference of -inf)
-        for (int c = 0; c < a.r_v; c += 16) {
-          float v[16];
-          tmem_ld_x16(t_d + c, v);
+        for (int c = 0; c < kRows; c += 16) {
+          float s[16];
+          tmem_ld_x16(t_s + c, s);
           tmem_wait_ld();
-          uint32_t x[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(v[k] * alpha);
-          tmem_st_x16(t_d + c, x);
+          for (int k = 0; k < 16; k += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(ref + c + k);
+            top = fmaxf(top, fmaxf(fmaxf(s[k] - m.x, s[k + 1] - m.y), fmaxf(s[k + 2] - m.z, s[k + 3] - m.w)));
+          }
         }
-        l *= alpha;
+        if (__any_sync(0xffffffffu, live && top > kHeadroom) && lane == 0) misc->over[i & 1] = i + 1;
+        if (!vote()) break;
+        moved = *const_cast<volatile int*>(&misc->over[i & 1]) == i + 1;
       }
-      if (move) m_ref = m_tile;
-      const float ref = m_ref == -INFINITY ? 0.f : m_ref;   // (nothing above -inf yet: weights of 0)
-      // weights, in bf16 as the product takes them; l adds up what was rounded.  Where P lies over S, the
-      // weights of 16 columns go to 8 that lie before or among them and have been read.
-      float l0 = 0.f, l1 = 0.f;
+      if (moved) {
+        if (!move(t_s, live, fresh)) break;
+        if (!fresh) {
+          // D is at rest once the product of tile i - 1 is done
+          if (!wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;
+          tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 16) {
+          for (int c = 0; c < P.blocks * kRows; c += 8) {
+            float v[8];
+            tmem_ld_x8(lanes + kDCol + c, v);
+            tmem_wait_ld();
+            uint32_t x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(v[k] * factor[(c + k) % kRows]);
+            tmem_st_x8(lanes + kDCol + c, x);
+          }
+          tmem_wait_st();
+        }
+#pragma unroll
+        for (int k = 0; k < kRows / 2; ++k) l[k] = fresh ? 0 : mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
+      }
+      // the buffer's last weights have been read
+      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
+      // weights, in bf16 as the product takes them; l adds up what was rounded.  A token past the end has none.
+      uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
+      const uint64_t minus = pair2(-1.f, -1.f);
+#pragma unroll
+      for (int c = 0; c < kRows; c += 16) {
         float s[16];
         tmem_ld_x16(t_s + c, s);
         tmem_wait_ld();
-        if (c + 16 > valid) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (c + k >= valid) s[k] = -INFINITY;
-        }
         uint32_t x[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[k] = pack_bf16(exp2_fast(s[2 * k] - ref), exp2_fast(s[2 * k + 1] - ref));
-          l0 += __uint_as_float(x[k] << 16);
-          l1 += __uint_as_float(x[k] & 0xFFFF0000u);
+        for (int k = 0; k < 8; k += 2) {
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(ref + c + 2 * k);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float d0, d1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(fma2(e == 0 ? m.x : m.y, minus, pair2(s[2 * (k + e)], s[2 * (k + e) + 1]))));
+            const uint32_t y = live ? pack_bf16(exp2_fast(d0), exp2_fast(d1)) : 0u;
+            x[k + e] = y;
+            uint64_t& sum = l[c / 2 + k + e];
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(pair2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u))));
+          }
         }
-        tmem_st_x8(t_p + (tok0 + c) / 2, x);
+        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + 16, kPRow)) = make_uint4(x[4], x[5], x[6], x[7]);
       }
-      l += l0 + l1;
-      if (kCopies > 1 && overlay) {                   // S of the other copies' tokens makes way for zeros
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 8)
-          if (c < tok0 / 2 || c >= (tok0 + kCols) / 2) tmem_st_x8(t_p + c, zeros);
-      }
-      tmem_wait_st();
       tc_fence_before();
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(misc->pfull));
+      if (lane == 0) {
+        mbar_arrive(bar(misc->pfull[i & 1]));
+        mbar_arrive(bar(misc->sfree[sb]));
+      }
       walk_next(w, a);
     }
-    if (ok && count > 0) finish(count - 1);
   }
 
   tc_fence_before();
@@ -709,16 +773,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 
 }  // namespace
 
-bool make_tree_plan(int r_k, int r_v, TreePlan* p) {
+bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   *p = TreePlan{};
   p->kplan = make_chunk_plan(r_k, kTile);
   p->vplan = make_chunk_plan_32(r_v, kTile);
+  p->blocks = (r_v + 127) / 128;
   auto al = [](int x) { return (x + 1023) / 1024 * 1024; };
   p->k_stage = al(p->kplan.bytes);
   p->v_stage = al(p->vplan.bytes);
-  // W, two 4 KB bias operands, queries, rotated keys, base rows, barriers, alignment
-  const int fixed = al(p->kplan.bytes) + 8192 + 32768 + 32768 + 512 + 1024;
-  auto fits = [&](int sk, int sv) { return fixed + (sk + 1) * 512 + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
+  // queries, W, two 4 KB bias operands, two buffers of weights, references, barriers, alignment
+  const int refs = 16 * rows * 4;
+  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 1024 + 1024;
+  auto fits = [&](int sk, int sv) { return fixed + al((sk + 2) * 512) + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
   while (true) {
@@ -727,26 +793,25 @@ bool make_tree_plan(int r_k, int r_v, TreePlan* p) {
     if (p->SK < kMaxStages && fits(p->SK + 1, p->SV)) { ++p->SK; continue; }
     break;
   }
+  // (the V ring first: the last stage's products may read up to 128 columns, 32 KB, past it)
   int off = 0;
   p->v_ring = off; off += p->SV * p->v_stage;
   p->k_ring = off; off += p->SK * p->k_stage;
   p->w = off;      off += al(p->kplan.bytes);
-  p->q = off;      off += 32768;
-  p->rot = off;    off += 32768;
+  p->q = off;      off += rows * 256;
+  p->p = off;      off += 2 * kTile * rows * 2;
   p->ones = off;   off += 4096;
   p->mu = off;     off += 4096;
-  p->base = off;   off += (p->SK + 1) * 512;
-  p->misc = off;   off += 512;
+  p->base = off;   off += al((p->SK + 2) * 512);
+  p->refs = off;   off += refs;
+  p->misc = off;   off += 1024;
   p->bytes = off + 1024;
-  // TMEM: U 0..127, S 128..255, then P (64 columns) and D; P shares S's columns where D needs the room
-  p->p_col = r_v <= 192 ? 256 : kSCol;
-  p->d_col = r_v <= 192 ? 320 : 256;
   return true;
 }
 
 template <int kPage>
 static cudaError_t launch_tiles(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s) {
-  auto kern = a.copies == 4 ? tree_tile_kernel<kPage, 4> : a.copies == 2 ? tree_tile_kernel<kPage, 2> : tree_tile_kernel<kPage, 1>;
+  auto kern = a.rows == 16 ? tree_tile_kernel<kPage, 16> : a.rows == 32 ? tree_tile_kernel<kPage, 32> : tree_tile_kernel<kPage, 64>;
   // (the most any shape takes, at every call)
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
@@ -754,7 +819,7 @@ static cudaError_t launch_tiles(const TreeArgs& a, const TreeMaps& maps, cudaStr
 }
 
 cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H + a.H + 1), dim3(kPrepThreads), 0, s, a);
+  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H * a.groups + a.H + 1), dim3(kPrepThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   if (!a.block_table) return launch_tiles<0>(a, maps, s);
   return a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s) : launch_tiles<2>(a, maps, s);

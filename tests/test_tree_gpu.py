@@ -199,6 +199,17 @@ def test_large_scores():
     check(c, call(c))
 
 
+@pytest.mark.parametrize("n", [3, 20, 50, 100])
+def test_scores_that_rise(n):
+    """Latents that grow along the cache: scores 2^30 and more above the first tile's, twice, and
+    falling again (a reference taken early has to move, and the sums with it)."""
+    c = make([700, 380, 129], [n, 1, 2], 2, 96, 160, 0, 0, "bf16", scale=12.0)
+    c["ck"][:, :, :128] *= 0.05
+    c["ck"][:, :, 128:256] *= 0.5
+    c["ck"][:, :, 400:] *= 0.1
+    check(c, call(c))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_without_lse_and_on_another_stream(dtype):
     c = make([300, 40], [4, 9], 2, 96, 160, 64, 0, dtype)
