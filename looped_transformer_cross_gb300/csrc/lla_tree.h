@@ -18,7 +18,7 @@ struct TreePlan {
   ChunkPlan kplan, vplan;            // K latents and W (64/32/16 wide); V latents (32 wide)
   int SK, SV, k_stage, v_stage;      // rings of K and V tiles
   int blocks;                        // blocks of 128 V columns
-  int v_ring, k_ring, w, q, p, ones, mu, base, refs, misc, bytes;
+  int v_ring, k_ring, w, q, p, ones, mu, base, refs, chunks, misc, bytes;
 };
 
 struct TreeMaps {

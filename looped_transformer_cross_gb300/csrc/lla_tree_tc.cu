@@ -53,7 +53,7 @@ struct alignas(16) TreeMisc {
   int abort;
   int over[2];                                      // tile + 1 in which a score passed its headroom
 };
-static_assert(sizeof(TreeMisc) <= 1024, "misc region");
+static_assert(sizeof(TreeMisc) <= 768, "misc region");
 
 struct Walk {
   int b, h, g, t, ng, nb, L;        // block g of ng of the sequence's nodes; tile t of nb
@@ -134,32 +134,46 @@ __device__ __forceinline__ int page_at(const TreeArgs& a, int b, int lp) {
   return min(max(pg, 0), static_cast<int>(a.num_pages) - 1);
 }
 
-// One latent tile (chunk plan cp, map of chunk c from map_of) into dst, completing on fb: a box per
-// chunk, or with pages of 8..64 tokens a box per chunk and page that holds tokens (lane i issues page
-// i; the whole warp calls it).
-template <int kPage, typename MapOf>
-__device__ __forceinline__ void load_tile(const TreeArgs& a, const Walk& w, uint32_t dst, uint32_t fb, const ChunkPlan& cp, MapOf map_of) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (kPage != 2) {
-    if (lane == 0) {
-      mbar_arrive_expect_tx(fb, cp.bytes);
-      int y = w.t * kTile, z = w.b * a.H + w.h;
-      if constexpr (kPage == 1) {
-        const int lp = y / a.page_size;
-        z = page_at(a, w.b, lp) * a.H + w.h;
-        y -= lp * a.page_size;
-      }
-      for (int c = 0; c < cp.n; ++c) tma_load_3d(dst + cp.off[c], map_of(c), fb, cp.start[c], y, z);
-    }
-  } else {
-    const int pg = a.page_size;
-    const int np = (min(kTile, w.L - w.t * kTile) + pg - 1) / pg;
-    if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(cp.bytes / kTile * pg * np));
-    __syncwarp();
-    const int lp0 = w.t * (kTile / pg);
-    if (lane < np) {
-      const int z = page_at(a, w.b, lp0 + lane) * a.H + w.h;
-      for (int c = 0; c < cp.n; ++c) tma_load_3d(dst + cp.off[c] + lane * pg * cp.width[c] * 2, map_of(c), fb, cp.start[c], 0, z);
+// A chunk of a latent tile as the copying warp needs it (in shared memory: reading the plan's arrays
+// out of the launch parameters for every copy cost more than the copies).
+struct Chunk {
+  int off, start, row, map;          // byte offset in a tile, first column, bytes of a row, tensor map
+};
+
+// Where the latents of a tile lie: the lane's page (pages of 8..64 tokens: lane mod pages of a tile) or
+// the sequence, as the maps' outer coordinate, and the first row in it.
+struct Place {
+  int y, z;
+};
+template <int kPage>
+__device__ __forceinline__ Place place_of(const TreeArgs& a, const Walk& w, int my_page) {
+  Place p{w.t * kTile, w.b * a.H + w.h};
+  if constexpr (kPage == 1) {
+    const int lp = p.y / a.page_size;
+    p.z = page_at(a, w.b, lp) * a.H + w.h;
+    p.y -= lp * a.page_size;
+  }
+  if constexpr (kPage == 2) {
+    const int lp = w.t * (kTile / a.page_size) + my_page;
+    p.z = lp * a.page_size < w.L ? page_at(a, w.b, lp) * a.H + w.h : 0;
+    p.y = 0;
+  }
+  return p;
+}
+
+// One latent tile into dst, completing on fb (the whole warp calls it).  A lane issues the boxes of one
+// page (pages of 8..64 tokens, those that hold tokens) or of the tile, every `every`-th chunk from its first on.
+template <int kPage>
+__device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32_t dst, uint32_t fb, const Chunk* chunks, int n, int bytes,
+                                          const CUtensorMap* maps, int page_size, int my_page, int first, int every) {
+  int np = 1;
+  if constexpr (kPage == 2) np = (min(kTile, w.L - w.t * kTile) + page_size - 1) / page_size;
+  if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(fb, kPage == 2 ? bytes / kTile * page_size * np : bytes);
+  __syncwarp();
+  if (my_page < np) {
+    for (int c = first; c < n; c += every) {
+      const Chunk k = chunks[c];
+      tma_load_3d(dst + k.off + (kPage == 2 ? my_page * page_size * k.row : 0), maps + k.map, fb, k.start, at.y, at.z);
     }
   }
 }
@@ -342,6 +356,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     for (int s = 0; s < 3; ++s) mbar_init(bar(misc->done[s]), 1);
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 16) {
+    const ChunkPlan& c = lane < 8 ? P.kplan : P.vplan;
+    const int k = lane & 7;
+    reinterpret_cast<Chunk*>(sm + P.chunks)[lane] = Chunk{c.off[k], c.start[k], c.width[k] * 2, lane < 8 ? chunk_map_index(c.width[k]) : 0};
+  }
   if (warp == 1) {
     __syncwarp();
     tmem_alloc(smem_u32(&misc->tmem_base), 512);
@@ -386,34 +405,47 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== K and V tiles, RoPE rows
     // V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.  Tile i's base row goes
     // to slot i mod SK + 2: K tile i + SK + 2 is requested once U(i + 2) is computed, for which every
-    // rotating warp has read U(i) and, before that, the base row of tile i.
+    // rotating warp has read U(i) and, before that, the base row of tile i.  Page ids are read one tile ahead.
+    const int page_size = a.page_size, pages = kPage == 2 ? kTile / page_size : 1;
+    const int my_page = lane % pages, first = lane / pages, every = 32 / pages;
+    const Chunk* kc = reinterpret_cast<const Chunk*>(sm + P.chunks);
+    const Chunk* vc = kc + 8;
+    const int SK = P.SK, SV = P.SV, nk = P.kplan.n, nv = P.vplan.n, k_bytes = P.kplan.bytes, v_bytes = P.vplan.bytes;
+    const uint32_t k_ring = sbase + P.k_ring, v_ring = sbase + P.v_ring, rows = sbase + P.base;
+    const uint32_t k_stage = P.k_stage, v_stage = P.v_stage;
     Walk wv = w;
     Ring kr, vr, br;
     int issued_k = 0, issued_v = 0;
+    Place at = {}, at_v = {};
+    if (count > 0) at = place_of<kPage>(a, w, my_page);
     for (int i = 0; i <= count && count > 0; ++i) {
+      const Walk wt = w;
+      Place at_k = at;
       if (i < count) {
         if (!wait(misc->kempty[kr.slot], kr.phase ^ 1u)) break;
-        load_tile<kPage>(a, w, sbase + P.k_ring + kr.slot * P.k_stage, bar(misc->kfull[kr.slot]), P.kplan,
-                         [&](int c) { return &maps.k[chunk_map_index(P.kplan.width[c])]; });
-        if (lane == 0) {
-          const uint32_t bb = bar(misc->bfull[br.slot]), dst = sbase + P.base + br.slot * 512;
-          mbar_arrive_expect_tx(bb, 512);
-          bulk_load(dst, a.rope_cos + static_cast<int64_t>(w.t) * kTile * 64, 256, bb);
-          bulk_load(dst + 256, a.rope_sin + static_cast<int64_t>(w.t) * kTile * 64, 256, bb);
-        }
+        load_tile<kPage>(w, at, k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, page_size, my_page,
+                         first, every);
+        // (the base row's cos and sin: the last two lanes)
+        if (lane == 0) mbar_arrive_expect_tx(bar(misc->bfull[br.slot]), 512);
+        __syncwarp();
+        if (lane >= 30)
+          bulk_load(rows + br.slot * 512 + (lane - 30) * 256, (lane == 30 ? a.rope_cos : a.rope_sin) + static_cast<int64_t>(w.t) * kTile * 64,
+                    256, bar(misc->bfull[br.slot]));
         issued_k = i + 1;
-        kr.next(P.SK);
-        br.next(P.SK + 2);
+        kr.next(SK);
+        br.next(SK + 2);
         walk_next(w, a);
+        if (i + 1 < count) at = place_of<kPage>(a, w, my_page);
       }
       if (i > 0) {
         if (!wait(misc->vempty[vr.slot], vr.phase ^ 1u)) break;
-        load_tile<kPage>(a, wv, sbase + P.v_ring + vr.slot * P.v_stage, bar(misc->vfull[vr.slot]), P.vplan,
-                         [&](int) { return &maps.v; });
+        load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, page_size, my_page,
+                         first, every);
         issued_v = i;
-        vr.next(P.SV);
-        walk_next(wv, a);
+        vr.next(SV);
       }
+      wv = wt;
+      at_v = at_k;
     }
     if (lane == 0) {
       for (int i = max(0, issued_k - P.SK); i < issued_k; ++i) landed(misc->kfull[i % P.SK], i / P.SK);
@@ -424,6 +456,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== U = C_k W^T + mu
     const uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
     const uint64_t d_ones = umma_desc(sbase + P.ones, 16, 256, kSw32), d_mu = umma_desc(sbase + P.mu, 16, 256, kSw32);
+    const int r_k = a.r_k, k64 = r_k / 64 * 4, k32 = (r_k & 32) / 16, k16 = r_k & 16;
+    const int o32 = r_k / 64 * 16384, o16 = o32 + (r_k & 32) * 256;
+    const uint32_t k_ring = sbase + P.k_ring, wb = sbase + P.w, kst = static_cast<uint32_t>(P.k_stage) >> 4;
+    const uint64_t a64 = umma_desc(k_ring, 16, 1024, kSw128), b64 = umma_desc(wb, 16, 1024, kSw128);
+    const uint64_t a32 = umma_desc(k_ring + o32, 16, 512, kSw64), b32 = umma_desc(wb + o32, 16, 512, kSw64);
+    const uint64_t a16 = umma_desc(k_ring + o16, 16, 256, kSw32), b16 = umma_desc(wb + o16, 16, 256, kSw32);
+    const int SK = P.SK;
     Ring kr;
     int unit = -1;
     for (int i = 0; i < count; ++i) {
@@ -443,23 +482,26 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
       if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
-      const uint32_t ka = sbase + P.k_ring + kr.slot * P.k_stage, d = tmem + (i & 1) * 128;
+      // (chunks of 64 columns, then one of 32, then one of 16)
+      const uint32_t d = tmem + (i & 1) * 128, so = kr.slot * kst;
       uint32_t acc = 0;
-      for (int c = 0; c < P.kplan.n; ++c) {
-        const int rb = P.kplan.width[c] * 2;
-        const uint32_t lay = sw_mode_for_row_bytes(rb);
-        const uint64_t a0 = umma_desc(ka + P.kplan.off[c], 16, 8 * rb, lay);
-        const uint64_t b0 = umma_desc(sbase + P.w + P.kplan.off[c], 16, 8 * rb, lay);
-        for (int k = 0; k < P.kplan.width[c] / 16; ++k) {
-          umma_bf16_warp(d, a0 + 2 * k, b0 + 2 * k, idesc, acc);
-          acc = 1;
-        }
+#pragma unroll 1
+      for (int k = 0; k < k64; ++k) {
+        const uint32_t o = (k >> 2) * 1024 + (k & 3) * 2;
+        umma_bf16_warp(d, a64 + so + o, b64 + o, idesc, acc);
+        acc = 1;
       }
+#pragma unroll 1
+      for (int k = 0; k < k32; ++k) {
+        umma_bf16_warp(d, a32 + so + 2 * k, b32 + 2 * k, idesc, acc);
+        acc = 1;
+      }
+      if (k16) umma_bf16_warp(d, a16 + so, b16, idesc, acc);
       umma_bf16_warp(d, d_ones, d_mu, idesc, 1);
       umma_commit_warp(bar(misc->ufull[i & 1]));
       umma_commit_warp(bar(misc->kempty[kr.slot]));
       if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
-      kr.next(P.SK);
+      kr.next(SK);
       walk_next(w, a);
     }
     products_done(misc->done[0]);
@@ -503,8 +545,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint64_t d_v = umma_desc(sbase + P.v_ring, kTile * 64, 512, kSw64);
     const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));
     const uint32_t vst = static_cast<uint32_t>(P.v_stage) >> 4;
+    const int SV = P.SV, blocks = P.blocks;
     Ring vr;
-    for (int j = 0; j < count; ++j, vr.next(P.SV)) {
+    for (int j = 0; j < count; ++j, vr.next(SV)) {
       if (!wait(misc->vfull[vr.slot], vr.phase)) break;
       // rows past the sequence's end: whole steps of 16 tokens are left out, the rest of a partial step
       // is zeroed (it may hold anything; its weights are 0 and 0 * x stays 0)
@@ -524,7 +567,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       tc_fence_after();
       const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j & 1) * (kTile * kPRow / 16);
       const uint32_t sum = !(j == 0 || w.t == 0);     // a unit's first product starts the sum
-      for (int blk = 0; blk < P.blocks; ++blk)
+#pragma unroll 1
+      for (int blk = 0; blk < blocks; ++blk)
+#pragma unroll 1
         for (int k = 0; k < steps; ++k)
           umma_bf16_warp(tmem + kDCol + blk * kRows, a0 + blk * (4 * kTile * 64 / 16) + 64 * k, b0 + k * kPRow, idesc, k > 0 || sum);
       umma_commit_warp(bar(misc->vdone[j & 1]));
@@ -545,12 +590,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
     }
     const uint64_t minus = pair2(-1.f, -1.f);
+    const int slots = P.SK + 2;
+    const float* rows = reinterpret_cast<const float*>(sm + P.base) + f0;
     Ring br;
-    for (int i = 0; i < count; ++i, br.next(P.SK + 2)) {
+    for (int i = 0; i < count; ++i, br.next(slots)) {
       const int kb = i % kBuf;
       const uint32_t t_u = lanes + (i & 1) * 128 + f0, t_k = lanes + kKhatCol + kb * 64 + f0 / 2;
       // the tile's base row: cos, then sin
-      const float* base = reinterpret_cast<const float*>(sm + P.base + br.slot * 512) + f0;
+      const float* base = rows + br.slot * 128;
       if (!wait(misc->bfull[br.slot], br.phase)) break;
       if (!wait(misc->ufull[i & 1], i >> 1)) break;
       if (i >= kBuf && !wait(misc->sfull[kb], (i - kBuf) / kBuf)) break;   // the buffer's last K^ has been read
@@ -596,12 +643,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     float* ref = reinterpret_cast<float*>(sm + P.refs) + quad * kRows;
     float* factor = reinterpret_cast<float*>(sm + P.refs) + (4 + quad) * kRows;
     float* maxima = reinterpret_cast<float*>(sm + P.refs) + 8 * kRows;
+    const int blocks = P.blocks;
     int votes = 0, moves = 0;
     auto vote = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(misc->vote));
       return wait(misc->vote, votes++);
     };
+    const uint64_t minus = pair2(-1.f, -1.f);
     uint64_t l[kRows / 2];
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
@@ -659,7 +708,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           rec[(c + lane) * stride + 1 + quad] = sum;
         }
       }
-      for (int blk = 0; blk < P.blocks; ++blk) {
+      for (int blk = 0; blk < blocks; ++blk) {
         const int r = blk * 128 + row;
 #pragma unroll 1
         for (int c = 0; c < n; c += 16) {
@@ -685,78 +734,80 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (i == count || !wait(misc->sfull[sb], i / kBuf)) break;
       tc_fence_after();
       const bool live = w.t * kTile + row < w.L;
-      bool moved = fresh;
-      if (!fresh) {
+      // the buffer's last weights have been read
+      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
+      uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
+      if (fresh) {
+        if (!move(t_s, live, true)) break;
+#pragma unroll
+        for (int k = 0; k < kRows / 2; ++k) l[k] = 0;
+      }
+      // Weights, in bf16 as the product takes them (a token past the end has none).  Where a score is too
+      // far above its reference, the references move and the weights are made again.
+      bool settled = fresh, ok = true;
+      while (true) {
         float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < kRows; c += 16) {
           float s[16];
           tmem_ld_x16(t_s + c, s);
           tmem_wait_ld();
+          uint32_t x[8];
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(ref + c + k);
-            top = fmaxf(top, fmaxf(fmaxf(s[k] - m.x, s[k + 1] - m.y), fmaxf(s[k + 2] - m.z, s[k + 3] - m.w)));
+          for (int k = 0; k < 8; k += 2) {
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(ref + c + 2 * k);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float d0, d1;
+              asm("mov.b64 {%0, %1}, %2;"
+                  : "=f"(d0), "=f"(d1)
+                  : "l"(fma2(e == 0 ? m.x : m.y, minus, pair2(s[2 * (k + e)], s[2 * (k + e) + 1]))));
+              top = fmaxf(top, fmaxf(d0, d1));
+              x[k + e] = live ? pack_bf16(exp2_fast(d0), exp2_fast(d1)) : 0u;
+            }
           }
+          *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + 16, kPRow)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
+        if (settled) break;
         if (__any_sync(0xffffffffu, live && top > kHeadroom) && lane == 0) misc->over[i & 1] = i + 1;
-        if (!vote()) break;
-        moved = *const_cast<volatile int*>(&misc->over[i & 1]) == i + 1;
-      }
-      if (moved) {
-        if (!move(t_s, live, fresh)) break;
-        if (!fresh) {
-          // D is at rest once the product of tile i - 1 is done
-          if (!wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;
-          tc_fence_after();
+        ok = vote();
+        if (!ok || *const_cast<volatile int*>(&misc->over[i & 1]) != i + 1) break;
+        settled = true;
+        // (D is at rest once the product of tile i - 1 is done)
+        ok = move(t_s, live, false) && wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < P.blocks * kRows; c += 8) {
-            float v[8];
-            tmem_ld_x8(lanes + kDCol + c, v);
-            tmem_wait_ld();
-            uint32_t x[8];
+        for (int c = 0; c < blocks * kRows; c += 8) {
+          float v[8];
+          tmem_ld_x8(lanes + kDCol + c, v);
+          tmem_wait_ld();
+          uint32_t x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(v[k] * factor[(c + k) % kRows]);
-            tmem_st_x8(lanes + kDCol + c, x);
-          }
-          tmem_wait_st();
+          for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(v[k] * factor[(c + k) % kRows]);
+          tmem_st_x8(lanes + kDCol + c, x);
         }
+        tmem_wait_st();
 #pragma unroll
-        for (int k = 0; k < kRows / 2; ++k) l[k] = fresh ? 0 : mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
+        for (int k = 0; k < kRows / 2; ++k) l[k] = mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
       }
-      // the buffer's last weights have been read
-      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
-      // weights, in bf16 as the product takes them; l adds up what was rounded.  A token past the end has none.
-      uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
-      const uint64_t minus = pair2(-1.f, -1.f);
-#pragma unroll
-      for (int c = 0; c < kRows; c += 16) {
-        float s[16];
-        tmem_ld_x16(t_s + c, s);
-        tmem_wait_ld();
-        uint32_t x[8];
-#pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(ref + c + 2 * k);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float d0, d1;
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(fma2(e == 0 ? m.x : m.y, minus, pair2(s[2 * (k + e)], s[2 * (k + e) + 1]))));
-            const uint32_t y = live ? pack_bf16(exp2_fast(d0), exp2_fast(d1)) : 0u;
-            x[k + e] = y;
-            uint64_t& sum = l[c / 2 + k + e];
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(pair2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u))));
-          }
-        }
-        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + 16, kPRow)) = make_uint4(x[4], x[5], x[6], x[7]);
-      }
+      if (!ok) break;
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(misc->pfull[i & 1]));
         mbar_arrive(bar(misc->sfree[sb]));
+      }
+      // the sums add up what was rounded, once the products have it
+#pragma unroll
+      for (int c = 0; c < kRows; c += 8) {
+        const uint4 x4 = *reinterpret_cast<const uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow));
+        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l[c / 2 + k]) : "l"(pair2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u))));
       }
       walk_next(w, a);
     }
@@ -783,7 +834,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->v_stage = al(p->vplan.bytes);
   // queries, W, two 4 KB bias operands, two buffers of weights, references, barriers, alignment
   const int refs = 16 * rows * 4;
-  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 1024 + 1024;
+  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 256 + 768 + 1024;
   auto fits = [&](int sk, int sv) { return fixed + al((sk + 2) * 512) + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
@@ -804,7 +855,8 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->mu = off;     off += 4096;
   p->base = off;   off += al((p->SK + 2) * 512);
   p->refs = off;   off += refs;
-  p->misc = off;   off += 1024;
+  p->chunks = off; off += 256;
+  p->misc = off;   off += 768;
   p->bytes = off + 1024;
   return true;
 }
