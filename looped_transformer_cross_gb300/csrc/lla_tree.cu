@@ -437,6 +437,11 @@ bool tree_maps(const TreeArgs& a, TreeMaps* m) {
     const uint32_t box[4] = {width, 64, 2, 1};
     if (!map_4d(&m->w[i], a.w_up_k, 4, d, st, box)) return false;
   }
+  if (rv % 32 == 0) {
+    const uint64_t d[4] = {32, rows, rv / 32, outer}, st[3] = {2 * rv, 64, 2 * rv * rows};
+    const uint32_t box[4] = {32, box_rows, static_cast<uint32_t>(rv / 32), 1};
+    if (!map_4d(&m->v4, a.cache_v, 4, d, st, box)) return false;
+  }
   return latents(&m->v, a.cache_v, rv, 32);
 }
 
@@ -525,6 +530,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.groups = (a.max_nodes + kTreeGroup - 1) / kTreeGroup;
     a.rows = tree_rows(a.max_nodes);
+    a.v_whole = a.r_v % 32 == 0;
     a.rec_rows = std::min(a.max_nodes, kTreeGroup);
     a.grid = w.grid;
     a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);

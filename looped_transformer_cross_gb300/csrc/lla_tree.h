@@ -18,12 +18,13 @@ struct TreePlan {
   ChunkPlan kplan, vplan;            // K latents and W (64/32/16 wide); V latents (32 wide)
   int SK, SV, k_stage, v_stage;      // rings of K and V tiles
   int blocks;                        // blocks of 128 V columns
-  int v_ring, k_ring, w, q, p, ones, mu, base, refs, chunks, misc, bytes;
+  int v_ring, k_ring, w, q, p, ones, mu, refs, base, chunks, misc, bytes;
 };
 
 struct TreeMaps {
   CUtensorMap k[3];                  // K latents, boxes 64 / 32 / 16 wide
   CUtensorMap v;                     // V latents, boxes 32 wide
+  CUtensorMap v4;                    // the same as (32, row, chunk, ..), a box all of a tile's or page's chunks
   CUtensorMap w[3];                  // W_up,k of the loop as (r_k, pair, member, head), boxes 64 / 32 / 16 wide
 };
 
@@ -59,6 +60,7 @@ struct TreeArgs {
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
   // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of 64 nodes, and record
   // unit + CTA belongs to every (unit, CTA) that share a tile
+  int v_whole;                       // r_v a multiple of 32: V by maps.v4
   int groups, rows, grid;            // blocks of nodes a sequence may have, nodes S has room for, CTAs
   int32_t* tile_start;               // [B + 1]: tiles of one head before sequence b
   int4* cta_start;                   // [grid]: first (sequence, head, tile), number of tiles

@@ -15,8 +15,8 @@
 // fp32 sums have the range); the softmax warps vote on that for every tile, and a tile that breaks it
 // moves the references and rescales D.
 //
-// Roles: warp 0 copies K and V tiles and RoPE rows, warp 1 issues U (and copies W), warp 2 issues S
-// (and copies Q^), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
+// Roles: warp 0 copies K and V tiles, warp 1 issues U (and copies W), warp 2 issues S
+// (and copies Q^ and RoPE rows), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
 // each, one token per lane), warps 12..15 do the softmax, one token per lane.  cos/sin of a token's
 // angle are the angle sum of the tile's base row (shared memory) and the lane's own row (registers).
 // The roles' loops are kept short on purpose: with bodies unrolled all the way, instruction fetch took
@@ -41,7 +41,7 @@ constexpr int kKhatCol = 256;                       // TMEM columns: U 0..255 (t
 
 struct alignas(16) TreeMisc {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages];
-  uint64_t bfull[kMaxStages + 2];                   // a tile's base row of the RoPE table
+  uint64_t bfull[4];                                // a tile's base row of the RoPE table
   uint64_t wfull, wfree, qfull, qfree;              // the unit's W and bias; its queries
   uint64_t ufull[2], ufree[2];                      // U computed; read by the rotating warps
   uint64_t rfull[2];                                // K^ written
@@ -121,6 +121,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// acc += ones (16 x 16) times a 16 x 8 block of bf16 values: every row of acc gets the columns' sums.
+__device__ __forceinline__ void add_columns(float (&acc)[4], uint32_t b0, uint32_t b1) {
+  const uint32_t ones = 0x3F803F80u;
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %4, %4, %4}, {%5, %6}, {%0, %1, %2, %3};"
+      : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+      : "r"(ones), "r"(b0), "r"(b1));
 }
 // Store 8 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -339,7 +346,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   if (tid == 0) {
     misc->abort = 0;
     misc->over[0] = misc->over[1] = 0;
-    for (int s = 0; s < kMaxStages + 2; ++s) mbar_init(bar(misc->bfull[s]), 1);
+    for (int s = 0; s < 4; ++s) mbar_init(bar(misc->bfull[s]), 1);
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(bar(misc->kfull[s]), 1); mbar_init(bar(misc->kempty[s]), 1);
       mbar_init(bar(misc->vfull[s]), 1); mbar_init(bar(misc->vempty[s]), 1);
@@ -402,19 +409,19 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   };
 
   if (warp == 0) {
-    // ======================================================== K and V tiles, RoPE rows
-    // V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.  Tile i's base row goes
-    // to slot i mod SK + 2: K tile i + SK + 2 is requested once U(i + 2) is computed, for which every
-    // rotating warp has read U(i) and, before that, the base row of tile i.  Page ids are read one tile ahead.
+    // ======================================================== K and V tiles
+    // V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.  Page ids are read one
+    // tile ahead.  (A copy costs this warp some hundred cycles: the fewer the better.)
     const int page_size = a.page_size, pages = kPage == 2 ? kTile / page_size : 1;
     const int my_page = lane % pages, first = lane / pages, every = 32 / pages;
     const Chunk* kc = reinterpret_cast<const Chunk*>(sm + P.chunks);
     const Chunk* vc = kc + 8;
     const int SK = P.SK, SV = P.SV, nk = P.kplan.n, nv = P.vplan.n, k_bytes = P.kplan.bytes, v_bytes = P.vplan.bytes;
-    const uint32_t k_ring = sbase + P.k_ring, v_ring = sbase + P.v_ring, rows = sbase + P.base;
+    const uint32_t k_ring = sbase + P.k_ring, v_ring = sbase + P.v_ring;
     const uint32_t k_stage = P.k_stage, v_stage = P.v_stage;
+    const bool v_whole = a.v_whole;
     Walk wv = w;
-    Ring kr, vr, br;
+    Ring kr, vr;
     int issued_k = 0, issued_v = 0;
     Place at = {}, at_v = {};
     if (count > 0) at = place_of<kPage>(a, w, my_page);
@@ -425,22 +432,23 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!wait(misc->kempty[kr.slot], kr.phase ^ 1u)) break;
         load_tile<kPage>(w, at, k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, page_size, my_page,
                          first, every);
-        // (the base row's cos and sin: the last two lanes)
-        if (lane == 0) mbar_arrive_expect_tx(bar(misc->bfull[br.slot]), 512);
-        __syncwarp();
-        if (lane >= 30)
-          bulk_load(rows + br.slot * 512 + (lane - 30) * 256, (lane == 30 ? a.rope_cos : a.rope_sin) + static_cast<int64_t>(w.t) * kTile * 64,
-                    256, bar(misc->bfull[br.slot]));
         issued_k = i + 1;
         kr.next(SK);
-        br.next(SK + 2);
         walk_next(w, a);
         if (i + 1 < count) at = place_of<kPage>(a, w, my_page);
       }
       if (i > 0) {
         if (!wait(misc->vempty[vr.slot], vr.phase ^ 1u)) break;
-        load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, page_size, my_page,
-                         first, every);
+        if (v_whole) {                                // all of a tile's, or a page's, columns in one copy
+          const int np = kPage == 2 ? (min(kTile, wv.L - wv.t * kTile) + page_size - 1) / page_size : 1;
+          const uint32_t vb = bar(misc->vfull[vr.slot]), region = kPage == 2 ? page_size * nv * 64 : v_bytes;
+          if (lane == 0) mbar_arrive_expect_tx(vb, region * np);
+          __syncwarp();
+          if (lane < np) tma_load_4d(v_ring + vr.slot * v_stage + lane * region, &maps.v4, vb, 0, at_v.y, 0, at_v.z);
+        } else {
+          load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, page_size, my_page,
+                           first, every);
+        }
         issued_v = i;
         vr.next(SV);
       }
@@ -449,14 +457,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     }
     if (lane == 0) {
       for (int i = max(0, issued_k - P.SK); i < issued_k; ++i) landed(misc->kfull[i % P.SK], i / P.SK);
-      for (int i = max(0, issued_k - P.SK - 2); i < issued_k; ++i) landed(misc->bfull[i % (P.SK + 2)], i / (P.SK + 2));
       for (int i = max(0, issued_v - P.SV); i < issued_v; ++i) landed(misc->vfull[i % P.SV], i / P.SV);
     }
   } else if (warp == 1) {
     // ======================================================== U = C_k W^T + mu
     const uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
     const uint64_t d_ones = umma_desc(sbase + P.ones, 16, 256, kSw32), d_mu = umma_desc(sbase + P.mu, 16, 256, kSw32);
-    const int r_k = a.r_k, k64 = r_k / 64 * 4, k32 = (r_k & 32) / 16, k16 = r_k & 16;
+    const int r_k = a.r_k, n64 = r_k / 64, k32 = r_k & 32, k16 = r_k & 16;
     const int o32 = r_k / 64 * 16384, o16 = o32 + (r_k & 32) * 256;
     const uint32_t k_ring = sbase + P.k_ring, wb = sbase + P.w, kst = static_cast<uint32_t>(P.k_stage) >> 4;
     const uint64_t a64 = umma_desc(k_ring, 16, 1024, kSw128), b64 = umma_desc(wb, 16, 1024, kSw128);
@@ -484,20 +491,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       tc_fence_after();
       // (chunks of 64 columns, then one of 32, then one of 16)
       const uint32_t d = tmem + (i & 1) * 128, so = kr.slot * kst;
-      uint32_t acc = 0;
+      umma_bf16_warp(d, d_ones, d_mu, idesc, 0);
 #pragma unroll 1
-      for (int k = 0; k < k64; ++k) {
-        const uint32_t o = (k >> 2) * 1024 + (k & 3) * 2;
-        umma_bf16_warp(d, a64 + so + o, b64 + o, idesc, acc);
-        acc = 1;
-      }
+      for (int c = 0; c < n64; ++c) {
+        const uint64_t ac = a64 + so + c * 1024, bc = b64 + c * 1024;
 #pragma unroll 1
-      for (int k = 0; k < k32; ++k) {
-        umma_bf16_warp(d, a32 + so + 2 * k, b32 + 2 * k, idesc, acc);
-        acc = 1;
+        for (int k = 0; k < 4; ++k) umma_bf16_warp(d, ac + 2 * k, bc + 2 * k, idesc, 1);
       }
-      if (k16) umma_bf16_warp(d, a16 + so, b16, idesc, acc);
-      umma_bf16_warp(d, d_ones, d_mu, idesc, 1);
+      if (k32) {
+        umma_bf16_warp(d, a32 + so, b32, idesc, 1);
+        umma_bf16_warp(d, a32 + so + 2, b32 + 2, idesc, 1);
+      }
+      if (k16) umma_bf16_warp(d, a16 + so, b16, idesc, 1);
       umma_commit_warp(bar(misc->ufull[i & 1]));
       umma_commit_warp(bar(misc->kempty[kr.slot]));
       if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
@@ -511,8 +516,28 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint32_t idesc = umma_idesc_bf16(128, kRows, false, false);
     const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128);
     int unit = -1;
+    // The tiles' base rows of the RoPE table too: a lane takes four cosines or sines, read three tiles
+    // ahead and stored two ahead, to slot i mod 4 (K^(i - 1), and with it every reader of the slot's last
+    // row, is done before tile i + 2's is stored).
+    Walk wr = w;
+    const float* table = lane < 16 ? a.rope_cos + 4 * lane : a.rope_sin + 4 * (lane - 16);
+    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto fetch = [&]() { ahead = __ldg(reinterpret_cast<const float4*>(table + static_cast<int64_t>(wr.t) * kTile * 64)); };
+    auto store = [&](int i) {
+      reinterpret_cast<float4*>(sm + P.base + (i & 3) * 512)[lane] = ahead;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(misc->bfull[i & 3]));
+      walk_next(wr, a);
+      if (i + 1 < count) fetch();
+    };
+    if (count > 0) {
+      fetch();
+      store(0);
+    }
+    if (count > 1) store(1);
     for (int i = 0; i < count; ++i) {
       const int sb = i % kBuf;
+      if (i + 2 < count) store(i + 2);
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->qfree, unit)) break;
         ++unit;
@@ -542,7 +567,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // (two blocks of 128 rows of r_v; rows past r_v read whatever follows the tile in shared memory and
     // are not looked at)
     const uint32_t idesc = umma_idesc_bf16(128, kRows, true, true);
-    const uint64_t d_v = umma_desc(sbase + P.v_ring, kTile * 64, 512, kSw64);
+    // V: chunks of 32 columns, their 128 token rows of 64 bytes one after the other; with pages of 8..64
+    // tokens and one copy per page, page by page, each [chunk][page_size rows]
+    const bool by_page = kPage == 2 && a.v_whole;
+    const int nv = P.vplan.n, rows = by_page ? a.page_size : kTile;          // rows of a chunk that lie together
+    const uint32_t region = rows * nv * 64;
+    const uint64_t d_v = umma_desc(sbase + P.v_ring, rows * 64, rows >= 16 ? 512 : region, kSw64);
+    const uint32_t block_step = 4 * rows * 64 / 16;
+    const int log_rows = 31 - __clz(rows);
     const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));
     const uint32_t vst = static_cast<uint32_t>(P.v_stage) >> 4;
     const int SV = P.SV, blocks = P.blocks;
@@ -556,9 +588,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (valid < steps * 16) {
         uint8_t* vs = sm + P.v_ring + vr.slot * P.v_stage;
         const int per = (steps * 16 - valid) * 4;
-        for (int x = lane; x < P.vplan.n * per; x += 32) {
+        for (int x = lane; x < nv * per; x += 32) {
           const int c = x / per, r = valid + (x - c * per) / 4, g = x & 3;
-          *reinterpret_cast<uint4*>(vs + P.vplan.off[c] + swizzle_offset(r * 64 + g * 16, 64)) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(vs + (r >> log_rows) * region + c * rows * 64 + swizzle_offset((r & (rows - 1)) * 64 + g * 16, 64)) =
+              make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -570,8 +603,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll 1
       for (int blk = 0; blk < blocks; ++blk)
 #pragma unroll 1
-        for (int k = 0; k < steps; ++k)
-          umma_bf16_warp(tmem + kDCol + blk * kRows, a0 + blk * (4 * kTile * 64 / 16) + 64 * k, b0 + k * kPRow, idesc, k > 0 || sum);
+        for (int k = 0; k < steps; ++k) {
+          // (rows is a power of two; a whole tile is one region)
+          const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
+          umma_bf16_warp(tmem + kDCol + blk * kRows, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
+        }
       umma_commit_warp(bar(misc->vdone[j & 1]));
       umma_commit_warp(bar(misc->vempty[vr.slot]));
       walk_next(w, a);
@@ -590,15 +626,12 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
     }
     const uint64_t minus = pair2(-1.f, -1.f);
-    const int slots = P.SK + 2;
     const float* rows = reinterpret_cast<const float*>(sm + P.base) + f0;
-    Ring br;
-    for (int i = 0; i < count; ++i, br.next(slots)) {
+    for (int i = 0; i < count; ++i) {
       const int kb = i % kBuf;
       const uint32_t t_u = lanes + (i & 1) * 128 + f0, t_k = lanes + kKhatCol + kb * 64 + f0 / 2;
-      // the tile's base row: cos, then sin
-      const float* base = rows + br.slot * 128;
-      if (!wait(misc->bfull[br.slot], br.phase)) break;
+      const float* base = rows + (i & 3) * 128;       // cos, then sin
+      if (!wait(misc->bfull[i & 3], i >> 2)) break;
       if (!wait(misc->ufull[i & 1], i >> 1)) break;
       if (i >= kBuf && !wait(misc->sfull[kb], (i - kBuf) / kBuf)) break;   // the buffer's last K^ has been read
       tc_fence_after();
@@ -651,7 +684,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return wait(misc->vote, votes++);
     };
     const uint64_t minus = pair2(-1.f, -1.f);
-    uint64_t l[kRows / 2];
+    // sums of the weights over this warp's tokens, as the accumulators of ones (16 x 16) times P (16 tokens x
+    // 8 nodes): l[t][0..1] is nodes 8 t + 2 (lane mod 4) and the next
+    float l[kRows / 8][4];
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
     // is higher, or if it is the unit's first
@@ -692,22 +727,15 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       const int64_t slot = (static_cast<int64_t>(cur_b) * a.H + cur_h) * a.groups + cur_g + blockIdx.x;
       const int stride = a.r_v + kTreeHead;
       float* rec = a.records + slot * a.rec_rows * stride;
+      for (int c = lane; c < n; c += 32)
+        if (quad == 0) rec[c * stride] = ref[c];
 #pragma unroll
-      for (int c = 0; c < kRows; c += 32) {
-        float v[32];
+      for (int t = 0; t < kRows / 8; ++t)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x = 0.f, y = 0.f;
-          if (c / 2 + k < kRows / 2) asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(l[c / 2 + k < kRows / 2 ? c / 2 + k : 0]));
-          v[2 * k] = x;
-          v[2 * k + 1] = y;
+        for (int e = 0; e < 2; ++e) {
+          const int c = 8 * t + 2 * (lane & 3) + e;
+          if (lane < 4 && c < n) rec[c * stride + 1 + quad] = l[t][e];
         }
-        const float sum = warp_column_sum32(v);
-        if (c + lane < n) {
-          if (quad == 0) rec[(c + lane) * stride] = ref[c + lane];
-          rec[(c + lane) * stride + 1 + quad] = sum;
-        }
-      }
       for (int blk = 0; blk < blocks; ++blk) {
         const int r = blk * 128 + row;
 #pragma unroll 1
@@ -733,28 +761,30 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       if (i == count || !wait(misc->sfull[sb], i / kBuf)) break;
       tc_fence_after();
-      const bool live = w.t * kTile + row < w.L;
+      const bool live = w.t * kTile + row < w.L, partial = (w.t + 1) * kTile > w.L;
       // the buffer's last weights have been read
       if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
       if (fresh) {
         if (!move(t_s, live, true)) break;
 #pragma unroll
-        for (int k = 0; k < kRows / 2; ++k) l[k] = 0;
+        for (int t = 0; t < kRows / 8; ++t) l[t][0] = l[t][1] = l[t][2] = l[t][3] = 0.f;
       }
       // Weights, in bf16 as the product takes them (a token past the end has none).  Where a score is too
       // far above its reference, the references move and the weights are made again.
       bool settled = fresh, ok = true;
       while (true) {
         float top = -INFINITY;
+        constexpr int kCols = kRows < 32 ? kRows : 32;  // columns at a time
 #pragma unroll
-        for (int c = 0; c < kRows; c += 16) {
-          float s[16];
-          tmem_ld_x16(t_s + c, s);
+        for (int c = 0; c < kRows; c += kCols) {
+          float s[kCols];
+          if constexpr (kCols == 32) tmem_ld_x32(t_s + c, s);
+          else tmem_ld_x16(t_s + c, s);
           tmem_wait_ld();
-          uint32_t x[8];
+          uint32_t x[kCols / 2];
 #pragma unroll
-          for (int k = 0; k < 8; k += 2) {
+          for (int k = 0; k < kCols / 2; k += 2) {
             const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(ref + c + 2 * k);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -763,11 +793,17 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
                   : "=f"(d0), "=f"(d1)
                   : "l"(fma2(e == 0 ? m.x : m.y, minus, pair2(s[2 * (k + e)], s[2 * (k + e) + 1]))));
               top = fmaxf(top, fmaxf(d0, d1));
-              x[k + e] = live ? pack_bf16(exp2_fast(d0), exp2_fast(d1)) : 0u;
+              x[k + e] = pack_bf16(exp2_fast(d0), exp2_fast(d1));
             }
           }
-          *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + 16, kPRow)) = make_uint4(x[4], x[5], x[6], x[7]);
+#pragma unroll
+          for (int k = 0; k < kCols / 2; k += 4)
+            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + (c + 2 * k) * 2, kPRow)) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        }
+        if (partial && !live) {
+#pragma unroll 1
+          for (int c = 0; c < kRows; c += 8)
+            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(0, 0, 0, 0);
         }
         if (settled) break;
         if (__any_sync(0xffffffffu, live && top > kHeadroom) && lane == 0) misc->over[i & 1] = i + 1;
@@ -790,7 +826,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         }
         tmem_wait_st();
 #pragma unroll
-        for (int k = 0; k < kRows / 2; ++k) l[k] = mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
+        for (int t = 0; t < kRows / 8; ++t) {
+          const float2 f = *reinterpret_cast<const float2*>(factor + 8 * t + 2 * (lane & 3));
+          l[t][0] *= f.x;
+          l[t][1] *= f.y;
+        }
       }
       if (!ok) break;
       tc_fence_before();
@@ -802,13 +842,19 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       // the sums add up what was rounded, once the products have it
 #pragma unroll
-      for (int c = 0; c < kRows; c += 8) {
-        const uint4 x4 = *reinterpret_cast<const uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow));
-        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w};
+      for (int t = 0; t < kRows / 16; ++t)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm("add.rn.f32x2 %0, %0, %1;" : "+l"(l[c / 2 + k]) : "l"(pair2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xFFFF0000u))));
-      }
+        for (int half = 0; half < 2; ++half) {
+          // four 8 x 8 blocks: tokens 0..7 and 8..15 of 16 by nodes 0..7 and 8..15, lane = block * 8 + token
+          const int tok = 32 * quad + 16 * half + (lane & 15), col = 16 * t + 8 * (lane >> 4);
+          uint32_t b0, b1, b2, b3;
+          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                       : "r"(smem_u32(p) + swizzle_offset(tok * kPRow + col * 2, kPRow))
+                       : "memory");
+          add_columns(l[2 * t], b0, b1);
+          add_columns(l[2 * t + 1], b2, b3);
+        }
       walk_next(w, a);
     }
   }
@@ -834,8 +880,8 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->v_stage = al(p->vplan.bytes);
   // queries, W, two 4 KB bias operands, two buffers of weights, references, barriers, alignment
   const int refs = 16 * rows * 4;
-  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 256 + 768 + 1024;
-  auto fits = [&](int sk, int sv) { return fixed + al((sk + 2) * 512) + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
+  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 2048 + 256 + 768 + 1024;
+  auto fits = [&](int sk, int sv) { return fixed + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
   while (true) {
@@ -853,8 +899,8 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->p = off;      off += 2 * kTile * rows * 2;
   p->ones = off;   off += 4096;
   p->mu = off;     off += 4096;
-  p->base = off;   off += al((p->SK + 2) * 512);
   p->refs = off;   off += refs;
+  p->base = off;   off += 2048;
   p->chunks = off; off += 256;
   p->misc = off;   off += 768;
   p->bytes = off + 1024;
