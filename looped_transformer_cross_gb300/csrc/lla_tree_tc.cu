@@ -90,6 +90,19 @@ struct Ring {
   }
 };
 
+// warp_wait with everything past the first test out of line: one copy of that code instead of one for
+// each place that waits (instruction fetch bounds this kernel).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, status);
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+__device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, abort, status);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -341,7 +354,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   volatile int* abort = &misc->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](const uint64_t& m) { return smem_u32(&m); };
-  auto wait = [&](const uint64_t& m, uint32_t parity) { return warp_wait(smem_u32(&m), parity & 1u, abort, a.status); };
+  auto wait = [&](const uint64_t& m, uint32_t parity) { return tile_wait(smem_u32(&m), parity & 1u, abort, a.status); };
 
   if (tid == 0) {
     misc->abort = 0;
