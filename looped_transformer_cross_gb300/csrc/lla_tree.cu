@@ -223,20 +223,8 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     if (flag) node_pos(a, first + i, true);
   }
   __syncthreads();
-  // the records of this block's nodes are consecutive (a block of nodes lies in one group of 64)
   const int row_first = blockIdx.y * kFinishRows;
-  int64_t rec_at = unit * a.splits;
-  int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk), rec_row0 = 0;
-  if (a.groups > 0) {
-    const int g = row_first / kTreeGroup, ng = (n + kTreeGroup - 1) / kTreeGroup;
-    rec_row0 = g * kTreeGroup;
-    const int64_t t0 = a.tile_start[b], nb = (a.tile_start[b + 1] - t0) / ng;
-    const int64_t share = max(static_cast<int64_t>(1), (static_cast<int64_t>(a.tile_start[a.B]) * a.H + a.grid - 1) / a.grid);
-    const int64_t f0 = t0 * a.H + (h * ng + g) * nb;
-    const int64_t c0 = f0 / share, c1 = nb > 0 ? (f0 + nb - 1) / share + 1 : c0;
-    rec_at = unit * a.groups + g + c0;
-    nsplit = static_cast<int>(c1 - c0);
-  }
+  const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
   const int stride = a.r_v + kTreeHead;
 
   for (int row = row_first; row < min(n, row_first + kFinishRows); ++row) {
@@ -275,7 +263,7 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     // the largest of the path's scores and of the records' maxima
     float m = -INFINITY;
     for (int i = 0; i < nd; ++i) m = fmaxf(m, sc[i]);
-    const float* rec0 = a.records + (rec_at * a.rec_rows + row - rec_row0) * stride;
+    const float* rec0 = a.records + (unit * a.splits * a.rec_rows + row) * stride;
     const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
     for (int i = 0; i < nsplit; ++i) m = fmaxf(m, rec0[i * next]);
     float held = 0.f;
@@ -367,7 +355,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t tile_start, cta_start, bias, qimg, records, total;
+  size_t tile_start, cta_start, bias, qimg, khat, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -379,12 +367,13 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
   if (tensor) {
     const int64_t most = units * groups * std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
     w.grid = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxGrid), most));
-    w.chunk = w.splits = 1;
     w.tile_start = 256;
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
     w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
-    w.records = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 256;
+    w.khat = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 256;
+    w.paths = w.khat + static_cast<size_t>(units) * max_nodes * 256;
+    w.records = al(w.paths + static_cast<size_t>(std::max(B, 1)) * max_nodes * 16);
     w.total = w.records + static_cast<size_t>(units * groups + w.grid) * rec;
     return w;
   }
@@ -537,10 +526,11 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
     a.bias = ws + w.bias;
     a.qimg = ws + w.qimg;
+    a.khat = ws + w.khat;
+    a.paths = reinterpret_cast<uint4*>(ws + w.paths);
     TreeMaps maps;
     if (!tree_maps(a, &maps)) return LLA_ERR_CUDA;
-    if (launch_tree_tensor(a, maps, s) != cudaSuccess || launch_tree_finish(a, true, s) != cudaSuccess) return LLA_ERR_CUDA;
-    return LLA_OK;
+    return launch_tree_tensor(a, maps, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
   }
   if (launch_tree_plain(a, bf16, s) != cudaSuccess || launch_tree_finish(a, bf16, s) != cudaSuccess) return LLA_ERR_CUDA;
   return LLA_OK;

@@ -31,6 +31,7 @@ namespace lla {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
 constexpr float kHeadroom = 32.f;                   // a score this far above its reference (log2 units) moves it
 constexpr int kPrepThreads = 256;
@@ -200,11 +201,47 @@ __device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32
 
 // ---------------------------------------------------------------- preparation
 
+// Eight frequency pairs of a vector: first and second members, from f0 on.
+__device__ __forceinline__ void load_pairs8(const __nv_bfloat16* v, int style, int f0, float (&x0)[8], float (&x1)[8]) {
+  if (style == 0) {
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(v + f0)), x0);
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(v + 64 + f0)), x1);
+  } else {
+    float lo[8], hi[8];
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(v + 2 * f0)), lo);
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(v + 2 * f0 + 8)), hi);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x0[k] = lo[2 * k]; x1[k] = lo[2 * k + 1];
+      x0[4 + k] = hi[2 * k]; x1[4 + k] = hi[2 * k + 1];
+    }
+  }
+}
+
+// The pairs rotated, times `scale`, in bf16.
+__device__ __forceinline__ void turn_pairs8(const float (&x0)[8], const float (&x1)[8], const float* c, const float* s, float scale,
+                                            uint4& y0, uint4& y1) {
+  float z0[8], z1[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + k)), s4 = __ldg(reinterpret_cast<const float4*>(s + k));
+    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z0[k + e] = (x0[k + e] * cc[e] - x1[k + e] * ss[e]) * scale;
+      z1[k + e] = (x0[k + e] * ss[e] + x1[k + e] * cc[e]) * scale;
+    }
+  }
+  y0 = make_uint4(pack_bf16(z0[0], z0[1]), pack_bf16(z0[2], z0[3]), pack_bf16(z0[4], z0[5]), pack_bf16(z0[6], z0[7]));
+  y1 = make_uint4(pack_bf16(z1[0], z1[1]), pack_bf16(z1[2], z1[3]), pack_bf16(z1[4], z1[5]), pack_bf16(z1[6], z1[7]));
+}
+
 // Blocks 0 .. units-1: the unit's query operand, RoPE(q, pos) log2(e)/sqrt(d) in bf16, as the
-// shared-memory image (two chunks of 64 columns, 128-byte rows, swizzled); dimensions in the order
-// first members of the pairs, then second members, as U's.  Blocks units .. units+H-1: mu of a head
-// as an operand that ones multiply, in three bf16 parts (24 bits).  The last block: tiles per
-// sequence, and every CTA's first tile.
+// shared-memory image (two chunks of 64 columns, 128-byte rows, swizzled), and its drafted keys, RoPE(k, pos)
+// in bf16, row by row; dimensions in the order first members of the pairs, then second members, as U's.
+// Then B blocks: the nodes on each node's path as bits, and the checks of a sequence's values.  Then H
+// blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits).  The last
+// block: tiles per sequence, and every CTA's first tile.
 __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid_constant__ TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -215,62 +252,80 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     const int b = bh / a.H, h = bh - b * a.H;
     int first;
     const int n = tree_nodes(a, b, first, false) - g * kTreeGroup;
-    const int L = tree_cached(a, b, false);
-    if (n <= 0 || L == 0) return;
+    if (n <= 0) return;
     first += g * kTreeGroup;
-    if (a.block_table && h == 0 && g == 0) {
+    uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 256;
+    uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup) * 256;
+    for (int i = tid; i < a.rows * 16; i += kPrepThreads) {
+      const bool key = i >= a.rows * 8;
+      const int it = key ? i - a.rows * 8 : i, r = it >> 3, f0 = (it & 7) * 8;
+      uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
+      if (r < n) {
+        const int64_t entry = first + r;
+        const __nv_bfloat16* v = key ? static_cast<const __nv_bfloat16*>(a.k) + entry * a.k_stride
+                                     : static_cast<const __nv_bfloat16*>(a.q) + entry * a.q_stride;
+        float x0[8], x1[8];
+        load_pairs8(v + h * kHeadDim, a.rope_style, f0, x0, x1);
+        int p = __ldg(a.pos + entry);
+        p = p < 0 ? 0 : (p >= a.rope_len ? static_cast<int>(a.rope_len - 1) : p);
+        const int64_t at = static_cast<int64_t>(p) * 64 + f0;
+        turn_pairs8(x0, x1, a.rope_cos + at, a.rope_sin + at, key ? 1.f : kLog2e * kInvSqrtD, y0, y1);
+      }
+      if (!key) {
+        const uint32_t o = swizzle_offset(r * 128 + f0 * 2, 128);
+        *reinterpret_cast<uint4*>(img + o) = y0;
+        *reinterpret_cast<uint4*>(img + a.rows * 128 + o) = y1;
+      } else if (r < n) {
+        *reinterpret_cast<uint4*>(keys + r * 256 + f0 * 2) = y0;
+        *reinterpret_cast<uint4*>(keys + r * 256 + 128 + f0 * 2) = y1;
+      }
+    }
+    return;
+  }
+  if (blockIdx.x < units + a.B) {
+    const int b = blockIdx.x - units;
+    __shared__ int32_t jump[2][kTreeMaxNodes];
+    __shared__ uint4 path[2][kTreeMaxNodes];
+    int first;
+    const int n = tree_nodes(a, b, first, true), L = tree_cached(a, b, true);
+    if (n == 0) return;
+    if (a.block_table) {
       const int used = (L + a.page_size - 1) / a.page_size;
       for (int lp = tid; lp < used; lp += kPrepThreads) {
         const int pg = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + lp);
         if (pg < 0 || pg >= a.num_pages) record_status(a.status, LLA_ERR_DEVICE_ARG);
       }
     }
-    uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 256;
-    for (int i = tid; i < a.rows * 8; i += kPrepThreads) {
-      const int r = i >> 3, f0 = (i & 7) * 8;
-      uint32_t y0[4] = {0, 0, 0, 0}, y1[4] = {0, 0, 0, 0};
-      if (r < n) {
-        const __nv_bfloat16* qv = static_cast<const __nv_bfloat16*>(a.q) + (first + r) * a.q_stride + h * kHeadDim;
-        float x0[8], x1[8];
-        if (a.rope_style == 0) {
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(qv + f0)), x0);
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(qv + 64 + f0)), x1);
-        } else {
-          float lo[8], hi[8];
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(qv + 2 * f0)), lo);
-          unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(qv + 2 * f0 + 8)), hi);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x0[k] = lo[2 * k]; x1[k] = lo[2 * k + 1];
-            x0[4 + k] = hi[2 * k]; x1[4 + k] = hi[2 * k + 1];
-          }
-        }
-        int p = __ldg(a.pos + first + r);
-        p = p < 0 ? 0 : (p >= a.rope_len ? static_cast<int>(a.rope_len - 1) : p);
-        const float* c = a.rope_cos + static_cast<int64_t>(p) * 64 + f0;
-        const float* s = a.rope_sin + static_cast<int64_t>(p) * 64 + f0;
-        const float sc = kLog2e * kInvSqrtD;
-        float z0[8], z1[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float cc = __ldg(c + k), ss = __ldg(s + k);
-          z0[k] = (x0[k] * cc - x1[k] * ss) * sc;
-          z1[k] = (x0[k] * ss + x1[k] * cc) * sc;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          y0[k] = pack_bf16(z0[2 * k], z0[2 * k + 1]);
-          y1[k] = pack_bf16(z1[2 * k], z1[2 * k + 1]);
-        }
-      }
-      const uint32_t o = swizzle_offset(r * 128 + f0 * 2, 128);
-      *reinterpret_cast<uint4*>(img + o) = make_uint4(y0[0], y0[1], y0[2], y0[3]);
-      *reinterpret_cast<uint4*>(img + a.rows * 128 + o) = make_uint4(y1[0], y1[1], y1[2], y1[3]);
+    if (tid < n) {
+      int p = __ldg(a.parent + first + tid);
+      const int at = __ldg(a.pos + first + tid);
+      if (p < -1 || p >= tid || at < 0 || at >= a.rope_len) record_status(a.status, LLA_ERR_DEVICE_ARG);
+      if (p < -1 || p >= tid) p = -1;
+      jump[0][tid] = p;
+      const uint32_t bit = 1u << (tid & 31), w = tid >> 5;
+      path[0][tid] = make_uint4(w == 0 ? bit : 0, w == 1 ? bit : 0, w == 2 ? bit : 0, w == 3 ? bit : 0);
     }
+    __syncthreads();
+    // by pointer doubling
+    int cur = 0;
+    for (int reach = 1; reach < n; reach *= 2, cur ^= 1) {
+      if (tid < n) {
+        const int j = jump[cur][tid];
+        uint4 m = path[cur][tid];
+        if (j >= 0) {
+          const uint4 o = path[cur][j];
+          m = make_uint4(m.x | o.x, m.y | o.y, m.z | o.z, m.w | o.w);
+        }
+        path[cur ^ 1][tid] = m;
+        jump[cur ^ 1][tid] = j >= 0 ? jump[cur][j] : -1;
+      }
+      __syncthreads();
+    }
+    if (tid < n) a.paths[static_cast<int64_t>(b) * a.max_nodes + tid] = path[cur][tid];
     return;
   }
-  if (blockIdx.x < units + a.H) {
-    const int h = blockIdx.x - units;
+  if (blockIdx.x < units + a.B + a.H) {
+    const int h = blockIdx.x - units - a.B;
     if (tid < kHeadDim) {
       const int src = tid < 64 ? (a.rope_style == 0 ? tid : 2 * tid) : (a.rope_style == 0 ? tid : 2 * (tid - 64) + 1);
       const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
@@ -881,6 +936,237 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   }
 }
 
+// ---------------------------------------------------------------- joining the parts
+
+constexpr int kJoinThreads = 128;
+
+// acc (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.
+__device__ __forceinline__ void mma16816(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two steps over 32 values of K: a lane's 16 bytes of a row of A (rows g and g + 8) and of B are K values
+// 8 q .. 8 q + 7 (q = lane mod 4); both operands give them to the same places of the two steps, so the
+// order of K is another one and the sum the same.
+__device__ __forceinline__ void mma_k32(float (&acc)[4], const uint4& lo, const uint4& hi, const uint4& b) {
+  mma16816(acc, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+  mma16816(acc, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+}
+
+// Shared memory of a join block (bytes): V rows of the keys, scores or the two parts of the latent
+// sums, weights, per row {reference, cached sum, 1 / sum}.
+struct JoinPlan {
+  int rows, keys, s_pitch, p_pitch, a_pitch;         // pitches in elements
+  int v, s, p, row, bytes;
+};
+__host__ __device__ inline JoinPlan join_plan(int rows, int max_nodes, int r_v) {
+  JoinPlan j{};
+  j.rows = rows;
+  j.keys = (max_nodes + 15) / 16 * 16;
+  j.s_pitch = j.keys + 4;
+  j.p_pitch = j.keys + 8;
+  j.a_pitch = (r_v + 31) / 32 * 32 + 8;
+  int off = 0;
+  j.v = off;   off += j.keys * (kHeadDim + 8) * 2;
+  j.s = off;   off += rows * j.s_pitch * 4 > 2 * rows * j.a_pitch * 2 ? rows * j.s_pitch * 4 : 2 * rows * j.a_pitch * 2;
+  j.p = off;   off += rows * j.p_pitch * 2;
+  j.row = off; off += rows * 16;
+  j.bytes = off;
+  return j;
+}
+
+// Block = (unit): up to 16, 32 or 64 nodes of a (sequence, head), 4 warps = row tiles of 16 nodes x kSplit
+// parts of the output's dimensions (of the keys, for the scores).
+//   S = Q^ K^^T over the nodes' keys, masked to each node's path; reference M over S and the records
+//   P = 2^(S - M), A = sum of the records' latent sums times 2^(m - M) (in two bf16 parts, 16 bits)
+//   out = (A W_up,v^T + P V + held mu_v) / l
+// by warp-level products whose operands come straight from global memory (L2) where they are read
+// along K.  Bound by the latency of its few steps.
+template <int kSplit>
+__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  extern __shared__ uint4 shared[];
+  constexpr int kRows = 64 / kSplit, kTiles = 16 / kSplit;      // nodes of the block; 8-dimension tiles of a warp
+  uint8_t* sm = reinterpret_cast<uint8_t*>(shared);
+  const JoinPlan J = join_plan(kRows, a.max_nodes, a.r_v);
+  __nv_bfloat16* sv = reinterpret_cast<__nv_bfloat16*>(sm + J.v);
+  float* ss = reinterpret_cast<float*>(sm + J.s);
+  __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(sm + J.s);          // (over the scores once they are weights)
+  __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
+  float4* srow = reinterpret_cast<float4*>(sm + J.row);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int rt = warp / kSplit, part = warp % kSplit;
+  const int64_t bh = blockIdx.x;
+  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H), grp = blockIdx.y;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int first;
+  const int n = tree_nodes(a, b, first, false), row0 = grp * kTreeGroup;
+  if (row0 >= n) return;
+  const int nr = min(kRows, n - row0), nk = min(n, row0 + kRows), nk16 = (nk + 15) & ~15;
+
+  // ---- values of the keys
+  for (int i = tid; i < nk16 * 16; i += kJoinThreads) {
+    const int r = i >> 4, c = (i & 15) * 8;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < nk) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + (first + r) * a.v_stride + h * kHeadDim + c));
+    *reinterpret_cast<uint4*>(sv + r * (kHeadDim + 8) + c) = x;
+  }
+  // ---- scores of this warp's 16 nodes against every kSplit-th tile of eight keys
+  {
+    const uint8_t* img = a.qimg + (bh * a.groups + grp) * (kRows * 256);
+    uint4 lo[4], hi[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {                     // K values 32 c + 8 q .. of chunk c / 2
+      const uint32_t o = (c & 1) * 64 + q * 16;
+      const uint8_t* chunk = img + (c >> 1) * kRows * 128;
+      lo[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((16 * rt + g) * 128 + o, 128)));
+      hi[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((16 * rt + g + 8) * 128 + o, 128)));
+    }
+    const uint8_t* keys = a.khat + bh * a.max_nodes * 256;
+    uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
+    const int r0 = row0 + 16 * rt + g;
+    if (r0 < n) m0 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0);
+    if (r0 + 8 < n) m1 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0 + 8);
+    for (int kt = part; kt < nk16 / 8; kt += kSplit) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      uint4 x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        x[c] = 8 * kt + g < nk ? __ldcg(reinterpret_cast<const uint4*>(keys + (8 * kt + g) * 256 + c * 64 + q * 16)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mma_k32(acc, lo[c], hi[c], x[c]);
+      const int col = 8 * kt + 2 * q, wd = col >> 5, bit = col & 31;
+      const uint32_t b0 = (wd == 0 ? m0.x : wd == 1 ? m0.y : wd == 2 ? m0.z : m0.w) >> bit;
+      const uint32_t b1 = (wd == 0 ? m1.x : wd == 1 ? m1.y : wd == 2 ? m1.z : m1.w) >> bit;
+      float* s0 = ss + (16 * rt + g) * J.s_pitch + col;
+      float* s1 = s0 + 8 * J.s_pitch;
+      s0[0] = b0 & 1 ? acc[0] : -INFINITY;
+      s0[1] = b0 & 2 ? acc[1] : -INFINITY;
+      s1[0] = b1 & 1 ? acc[2] : -INFINITY;
+      s1[1] = b1 & 2 ? acc[3] : -INFINITY;
+    }
+  }
+  // the unit's records: consecutive
+  const int ng = (n + kTreeGroup - 1) / kTreeGroup, stride = a.r_v + kTreeHead;
+  const int64_t t0 = __ldcg(a.tile_start + b), nb = (__ldcg(a.tile_start + b + 1) - t0) / ng;
+  const int64_t share = max(static_cast<int64_t>(1), (static_cast<int64_t>(__ldcg(a.tile_start + a.B)) * a.H + a.grid - 1) / a.grid);
+  const int64_t f0 = t0 * a.H + (h * ng + grp) * nb;
+  const int64_t c0 = f0 / share;
+  const int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
+  const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
+  const float* recs = a.records + (bh * a.groups + grp + c0) * next;
+  __syncthreads();
+
+  // ---- reference, weights and sums: eight lanes a row
+  for (int r = tid >> 3; r < kRows; r += kJoinThreads / 8) {
+    const int x = tid & 7;
+    const bool row = r < nr;
+    const float* rec = recs + r * stride;
+    float m = -INFINITY;
+    for (int c = x; c < nk && row; c += 8) m = fmaxf(m, ss[r * J.s_pitch + c]);
+    for (int i = x; i < nrec && row; i += 8) m = fmaxf(m, __ldcg(rec + i * next));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, held = 0.f;
+    for (int c = x; c < nk16; c += 8) {
+      const __nv_bfloat16 p = __float2bfloat16_rn(row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f);
+      sp[r * J.p_pitch + c] = p;
+      l += __bfloat162float(p);
+    }
+    for (int i = x; i < nrec && row; i += 8) {
+      const float4 head = __ldcg(reinterpret_cast<const float4*>(rec + i * next));
+      held = fmaf(exp2f(head.x - m), (head.y + head.z) + (head.w + __ldcg(rec + i * next + 4)), held);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      held += __shfl_xor_sync(0xffffffffu, held, o);
+    }
+    l += held;
+    if (x == 0) {
+      srow[r] = make_float4(m, held, row ? 1.f / l : 0.f, 0.f);
+      if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (m + log2f(l)) * kLn2;
+    }
+  }
+  __syncthreads();
+  // ---- latent sums of the records, relative to M, in two bf16 parts
+  const int cols = J.a_pitch - 8, per = cols / 4;
+  for (int i = tid; i < kRows * per; i += kJoinThreads) {
+    const int r = i / per, c = (i - r * per) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < nr && c < a.r_v) {
+      const float m = srow[r].x;
+      const float* rec = recs + r * stride;
+      for (int k = 0; k < nrec; ++k, rec += next) {
+        const float f = exp2f(__ldcg(rec) - m);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(rec + kTreeHead + c));
+        x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y); x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
+      }
+    }
+    const uint32_t h0 = pack_bf16(x.x, x.y), h1 = pack_bf16(x.z, x.w);
+    const uint32_t l0 = pack_bf16(x.x - __uint_as_float(h0 << 16), x.y - __uint_as_float(h0 & 0xFFFF0000u));
+    const uint32_t l1 = pack_bf16(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xFFFF0000u));
+    *reinterpret_cast<uint2*>(sa + r * J.a_pitch + c) = make_uint2(h0, h1);
+    *reinterpret_cast<uint2*>(sa + (kRows + r) * J.a_pitch + c) = make_uint2(l0, l1);
+  }
+  __syncthreads();
+
+  // ---- A W^T + P V: this warp's 16 nodes, 128 / kSplit dimensions
+  float acc[kTiles][4];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+  const int e0 = part * (kHeadDim / kSplit);
+  const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + e0 + g) * a.r_v;
+  for (int c = 0; c < cols && nrec > 0; c += 32) {
+    const __nv_bfloat16* ah = sa + (16 * rt + g) * J.a_pitch + c + 8 * q;
+    const __nv_bfloat16* al = ah + kRows * J.a_pitch;
+    const uint4 h0 = *reinterpret_cast<const uint4*>(ah), h1 = *reinterpret_cast<const uint4*>(ah + 8 * J.a_pitch);
+    const uint4 l0 = *reinterpret_cast<const uint4*>(al), l1 = *reinterpret_cast<const uint4*>(al + 8 * J.a_pitch);
+    uint4 x[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+      x[t] = c + 8 * q < a.r_v ? __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(8 * t) * a.r_v + c + 8 * q)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      mma_k32(acc[t], h0, h1, x[t]);
+      mma_k32(acc[t], l0, l1, x[t]);
+    }
+  }
+  for (int k = 0; k < nk16; k += 16) {
+    const __nv_bfloat16* p = sp + (16 * rt + g) * J.p_pitch + k + 2 * q;
+    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(p), a1 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch);
+    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(p + 8), a3 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch + 8);
+#pragma unroll
+    for (int t = 0; t < kTiles; t += 2) {
+      uint32_t b0, b1, b2, b3;
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                   : "r"(smem_u32(sv + (k + (lane & 15)) * (kHeadDim + 8) + e0 + 8 * t + 8 * (lane >> 4)))
+                   : "memory");
+      mma16816(acc[t], a0, a1, a2, a3, b0, b1);
+      mma16816(acc[t + 1], a0, a1, a2, a3, b2, b3);
+    }
+  }
+  // ---- means, division, one rounding
+  const float4 r0 = srow[16 * rt + g], r1 = srow[16 * rt + g + 8];
+  const int n0 = 16 * rt + g, n1 = n0 + 8;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((static_cast<int64_t>(first) + row0) * a.H + h) * kHeadDim;
+  const float* mu = a.mu_v + h * a.mu_hstride;
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int e = e0 + 8 * t + 2 * q;
+    float2 m = make_float2(0.f, 0.f);
+    if (nrec > 0) m = __ldg(reinterpret_cast<const float2*>(mu + e));
+    if (n0 < nr)
+      *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(n0) * a.H * kHeadDim + e) =
+          __floats2bfloat162_rn(fmaf(r0.y, m.x, acc[t][0]) * r0.z, fmaf(r0.y, m.y, acc[t][1]) * r0.z);
+    if (n1 < nr)
+      *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(n1) * a.H * kHeadDim + e) =
+          __floats2bfloat162_rn(fmaf(r1.y, m.x, acc[t][2]) * r1.z, fmaf(r1.y, m.y, acc[t][3]) * r1.z);
+  }
+}
+
 }  // namespace
 
 bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
@@ -930,10 +1216,18 @@ static cudaError_t launch_tiles(const TreeArgs& a, const TreeMaps& maps, cudaStr
 }
 
 cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H * a.groups + a.H + 1), dim3(kPrepThreads), 0, s, a);
+  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H * a.groups + a.B + a.H + 1), dim3(kPrepThreads), 0, s, a);
   if (e != cudaSuccess) return e;
-  if (!a.block_table) return launch_tiles<0>(a, maps, s);
-  return a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s) : launch_tiles<2>(a, maps, s);
+  const cudaError_t t = !a.block_table              ? launch_tiles<0>(a, maps, s)
+                        : a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s)
+                                                   : launch_tiles<2>(a, maps, s);
+  if (t != cudaSuccess) return t;
+  auto join = a.rows == 16 ? tree_join_kernel<4> : a.rows == 32 ? tree_join_kernel<2> : tree_join_kernel<1>;
+  // (the most any shape takes, at every call)
+  const cudaError_t c = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             join_plan(kTreeGroup, kTreeMaxNodes, kMaxRankPerHead).bytes);
+  if (c != cudaSuccess) return c;
+  return launch_pdl(join, dim3(a.B * a.H, a.groups), dim3(kJoinThreads), join_plan(a.rows, a.max_nodes, a.r_v).bytes, s, a);
 }
 
 }  // namespace lla
