@@ -958,12 +958,13 @@ __device__ __forceinline__ void mma_k32(float (&acc)[4], const uint4& lo, const 
 // Shared memory of a join block (bytes): V rows of the keys, scores or the two parts of the latent
 // sums, weights, per row {reference, cached sum, 1 / sum}.
 struct JoinPlan {
-  int rows, keys, s_pitch, p_pitch, a_pitch;         // pitches in elements
+  int keys, s_pitch, p_pitch, a_pitch;               // pitches in elements
   int v, s, p, row, bytes;
 };
-__host__ __device__ inline JoinPlan join_plan(int rows, int max_nodes, int r_v) {
+constexpr int kJoinRows = 16;           // nodes of a join block
+__host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
+  constexpr int rows = kJoinRows;
   JoinPlan j{};
-  j.rows = rows;
   j.keys = (max_nodes + 15) / 16 * 16;
   j.s_pitch = j.keys + 4;
   j.p_pitch = j.keys + 8;
@@ -977,31 +978,28 @@ __host__ __device__ inline JoinPlan join_plan(int rows, int max_nodes, int r_v) 
   return j;
 }
 
-// Block = (unit): up to 16, 32 or 64 nodes of a (sequence, head), 4 warps = row tiles of 16 nodes x kSplit
-// parts of the output's dimensions (of the keys, for the scores).
+// Block = 16 nodes of a (sequence, head); its four warps split the keys, then the output's dimensions.
 //   S = Q^ K^^T over the nodes' keys, masked to each node's path; reference M over S and the records
 //   P = 2^(S - M), A = sum of the records' latent sums times 2^(m - M) (in two bf16 parts, 16 bits)
 //   out = (A W_up,v^T + P V + held mu_v) / l
 // by warp-level products whose operands come straight from global memory (L2) where they are read
-// along K.  Bound by the latency of its few steps.
-template <int kSplit>
+// along K.  Bound by the latency of its few steps; blocks are small so that many run at a time.  The
+// scores need nothing of the tile kernel, so they are made before the wait for it (its blocks let this
+// grid start only once they have seen the preparation complete).
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ uint4 shared[];
-  constexpr int kRows = 64 / kSplit, kTiles = 16 / kSplit;      // nodes of the block; 8-dimension tiles of a warp
+  constexpr int kSplit = kJoinThreads / 32, kRows = kJoinRows, kTiles = 16 / kSplit;      // 8-dimension tiles of a warp
   uint8_t* sm = reinterpret_cast<uint8_t*>(shared);
-  const JoinPlan J = join_plan(kRows, a.max_nodes, a.r_v);
+  const JoinPlan J = join_plan(a.max_nodes, a.r_v);
   __nv_bfloat16* sv = reinterpret_cast<__nv_bfloat16*>(sm + J.v);
   float* ss = reinterpret_cast<float*>(sm + J.s);
   __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(sm + J.s);          // (over the scores once they are weights)
   __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
   float4* srow = reinterpret_cast<float4*>(sm + J.row);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int rt = warp / kSplit, part = warp % kSplit;
-  const int64_t bh = blockIdx.x;
-  const int b = static_cast<int>(bh / a.H), h = static_cast<int>(bh - static_cast<int64_t>(b) * a.H), grp = blockIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, part = tid >> 5, g = lane >> 2, q = lane & 3;
+  const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, row0 = blockIdx.y * kRows, grp = row0 / kTreeGroup;
   int first;
-  const int n = tree_nodes(a, b, first, false), row0 = grp * kTreeGroup;
+  const int n = tree_nodes(a, b, first, false);
   if (row0 >= n) return;
   const int nr = min(kRows, n - row0), nk = min(n, row0 + kRows), nk16 = (nk + 15) & ~15;
 
@@ -1014,18 +1012,19 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   }
   // ---- scores of this warp's 16 nodes against every kSplit-th tile of eight keys
   {
-    const uint8_t* img = a.qimg + (bh * a.groups + grp) * (kRows * 256);
+    const uint8_t* img = a.qimg + (static_cast<int64_t>(bh) * a.groups + grp) * (a.rows * 256);
+    const int ir = row0 - grp * kTreeGroup + g;       // row of the image
     uint4 lo[4], hi[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {                     // K values 32 c + 8 q .. of chunk c / 2
       const uint32_t o = (c & 1) * 64 + q * 16;
-      const uint8_t* chunk = img + (c >> 1) * kRows * 128;
-      lo[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((16 * rt + g) * 128 + o, 128)));
-      hi[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((16 * rt + g + 8) * 128 + o, 128)));
+      const uint8_t* chunk = img + (c >> 1) * a.rows * 128;
+      lo[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset(ir * 128 + o, 128)));
+      hi[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((ir + 8) * 128 + o, 128)));
     }
-    const uint8_t* keys = a.khat + bh * a.max_nodes * 256;
+    const uint8_t* keys = a.khat + static_cast<int64_t>(bh) * a.max_nodes * 256;
     uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
-    const int r0 = row0 + 16 * rt + g;
+    const int r0 = row0 + g;
     if (r0 < n) m0 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0);
     if (r0 + 8 < n) m1 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0 + 8);
     for (int kt = part; kt < nk16 / 8; kt += kSplit) {
@@ -1039,7 +1038,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       const int col = 8 * kt + 2 * q, wd = col >> 5, bit = col & 31;
       const uint32_t b0 = (wd == 0 ? m0.x : wd == 1 ? m0.y : wd == 2 ? m0.z : m0.w) >> bit;
       const uint32_t b1 = (wd == 0 ? m1.x : wd == 1 ? m1.y : wd == 2 ? m1.z : m1.w) >> bit;
-      float* s0 = ss + (16 * rt + g) * J.s_pitch + col;
+      float* s0 = ss + g * J.s_pitch + col;
       float* s1 = s0 + 8 * J.s_pitch;
       s0[0] = b0 & 1 ? acc[0] : -INFINITY;
       s0[1] = b0 & 2 ? acc[1] : -INFINITY;
@@ -1047,20 +1046,21 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       s1[1] = b1 & 2 ? acc[3] : -INFINITY;
     }
   }
-  // the unit's records: consecutive
+  // ---- the unit's records: consecutive
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ng = (n + kTreeGroup - 1) / kTreeGroup, stride = a.r_v + kTreeHead;
-  const int64_t t0 = __ldcg(a.tile_start + b), nb = (__ldcg(a.tile_start + b + 1) - t0) / ng;
-  const int64_t share = max(static_cast<int64_t>(1), (static_cast<int64_t>(__ldcg(a.tile_start + a.B)) * a.H + a.grid - 1) / a.grid);
-  const int64_t f0 = t0 * a.H + (h * ng + grp) * nb;
-  const int64_t c0 = f0 / share;
+  const uint32_t t0 = __ldcg(a.tile_start + b), nb = (__ldcg(a.tile_start + b + 1) - t0) / ng;
+  const uint32_t total = static_cast<uint32_t>(__ldcg(a.tile_start + a.B)) * a.H;     // (below 2^31)
+  const uint32_t share = max(1u, (total + a.grid - 1) / a.grid);
+  const uint32_t f0 = t0 * a.H + (h * ng + grp) * nb, c0 = f0 / share;
   const int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
   const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
-  const float* recs = a.records + (bh * a.groups + grp + c0) * next;
+  const float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * kTreeGroup) * stride;
   __syncthreads();
 
   // ---- reference, weights and sums: eight lanes a row
-  for (int r = tid >> 3; r < kRows; r += kJoinThreads / 8) {
-    const int x = tid & 7;
+  {
+    const int r = tid >> 3, x = tid & 7;
     const bool row = r < nr;
     const float* rec = recs + r * stride;
     float m = -INFINITY;
@@ -1098,6 +1098,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     if (r < nr && c < a.r_v) {
       const float m = srow[r].x;
       const float* rec = recs + r * stride;
+#pragma unroll 2
       for (int k = 0; k < nrec; ++k, rec += next) {
         const float f = exp2f(__ldcg(rec) - m);
         const float4 y = __ldcg(reinterpret_cast<const float4*>(rec + kTreeHead + c));
@@ -1119,7 +1120,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   const int e0 = part * (kHeadDim / kSplit);
   const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + e0 + g) * a.r_v;
   for (int c = 0; c < cols && nrec > 0; c += 32) {
-    const __nv_bfloat16* ah = sa + (16 * rt + g) * J.a_pitch + c + 8 * q;
+    const __nv_bfloat16* ah = sa + g * J.a_pitch + c + 8 * q;
     const __nv_bfloat16* al = ah + kRows * J.a_pitch;
     const uint4 h0 = *reinterpret_cast<const uint4*>(ah), h1 = *reinterpret_cast<const uint4*>(ah + 8 * J.a_pitch);
     const uint4 l0 = *reinterpret_cast<const uint4*>(al), l1 = *reinterpret_cast<const uint4*>(al + 8 * J.a_pitch);
@@ -1134,7 +1135,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     }
   }
   for (int k = 0; k < nk16; k += 16) {
-    const __nv_bfloat16* p = sp + (16 * rt + g) * J.p_pitch + k + 2 * q;
+    const __nv_bfloat16* p = sp + g * J.p_pitch + k + 2 * q;
     const uint32_t a0 = *reinterpret_cast<const uint32_t*>(p), a1 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch);
     const uint32_t a2 = *reinterpret_cast<const uint32_t*>(p + 8), a3 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch + 8);
 #pragma unroll
@@ -1149,8 +1150,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     }
   }
   // ---- means, division, one rounding
-  const float4 r0 = srow[16 * rt + g], r1 = srow[16 * rt + g + 8];
-  const int n0 = 16 * rt + g, n1 = n0 + 8;
+  const float4 r0 = srow[g], r1 = srow[g + 8];
+  const int n0 = g, n1 = g + 8;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((static_cast<int64_t>(first) + row0) * a.H + h) * kHeadDim;
   const float* mu = a.mu_v + h * a.mu_hstride;
 #pragma unroll
@@ -1222,12 +1223,12 @@ cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStre
                         : a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s)
                                                    : launch_tiles<2>(a, maps, s);
   if (t != cudaSuccess) return t;
-  auto join = a.rows == 16 ? tree_join_kernel<4> : a.rows == 32 ? tree_join_kernel<2> : tree_join_kernel<1>;
   // (the most any shape takes, at every call)
-  const cudaError_t c = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             join_plan(kTreeGroup, kTreeMaxNodes, kMaxRankPerHead).bytes);
+  const cudaError_t c = cudaFuncSetAttribute(tree_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             join_plan(kTreeMaxNodes, kMaxRankPerHead).bytes);
   if (c != cudaSuccess) return c;
-  return launch_pdl(join, dim3(a.B * a.H, a.groups), dim3(kJoinThreads), join_plan(a.rows, a.max_nodes, a.r_v).bytes, s, a);
+  return launch_pdl(tree_join_kernel, dim3(a.B * a.H, (a.max_nodes + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads),
+                    join_plan(a.max_nodes, a.r_v).bytes, s, a);
 }
 
 }  // namespace lla
