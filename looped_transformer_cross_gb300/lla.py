@@ -656,30 +656,37 @@ def tree_workspace(dm: Dims, tree: DraftTree, L_max: int) -> torch.Tensor:
 
 def _node_vectors(name: str, t, dtype, dev: int, shape):
     """Address and token stride of q, k or v [n_tok][H][d], each token's [H][d] contiguous."""
-    _need(isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape,
-          "%s must be %s of shape %s on cuda:%d" % (name, dtype, tuple(shape), dev))
     n, H, d = shape
-    st = t.stride()
-    _need((d <= 1 or st[2] == 1) and (H <= 1 or st[1] == d), "each token's vectors of %s must be contiguous" % name)
-    # (torch leaves the stride of a single token open)
-    return t.data_ptr(), st[0] if n > 1 else H * d
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and (s1 == d or H == 1):
+                # (torch leaves the stride of a single token open)
+                return t.data_ptr(), s0 if n > 1 else H * d
+    except AttributeError:
+        pass
+    raise ValueError("%s must be %s of shape %s on cuda:%d, each token's vectors contiguous" % (name, dtype, shape, dev))
 
 
 def _tree_attn(what, f, dm, loop_t, tree, q, k, v, cache, B, seq_lens, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin,
                out, lse, workspace, stream):
-    dev, sd, T, H, d, f32 = tree.dev, _storage(dm), dm.T, dm.H, dm.d_head, torch.float32
-    _need(tree.pos is not None, "the tree has no positions")
-    _need(B == tree.B, "the cache is for %d sequences, the tree for %d" % (B, tree.B))
-    vec, table = (tree.n_tok, H, d), rope_cos.shape
-    _need(len(table) == 2 and table[1] == d // 2, "rope_cos must be [rope_len][%d]" % (d // 2))
+    dev, sd, T, H, d, f32, n = tree.dev, _storage(dm), dm.T, dm.H, dm.d_head, torch.float32, tree.n_tok
+    if tree.pos is None or B != tree.B:
+        raise ValueError("the tree has no positions" if tree.pos is None else
+                         "the cache is for %d sequences, the tree for %d" % (B, tree.B))
+    vec, table, mu = (n, H, d), rope_cos.shape, (H, T * d)
+    if len(table) != 2 or table[1] != d // 2:
+        raise ValueError("rope_cos must be [rope_len][%d]" % (d // 2))
+    qp, qs = _node_vectors("q", q, sd, dev, vec)
+    kp, ks = _node_vectors("k", k, sd, dev, vec)
+    vp, vs = _node_vectors("v", v, sd, dev, vec)
     ws, wb = _space(workspace, dev)
-    _run(what, f, dev, stream, ctypes.byref(dm), loop_t, tree.ref, *_node_vectors("q", q, sd, dev, vec),
-         *_node_vectors("k", k, sd, dev, vec), *_node_vectors("v", v, sd, dev, vec), cache,
+    _run(what, f, dev, stream, ctypes.byref(dm), loop_t, tree.ref, qp, qs, kp, ks, vp, vs, cache,
          _arg("seq_lens", seq_lens, torch.int32, dev, (B,)), _arg("w_up_k", w_up_k, sd, dev, (T, H, d, dm.r_k)),
-         _arg("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)), _arg("mu_k", mu_k, f32, dev, (H, T * d)),
-         _arg("mu_v", mu_v, f32, dev, (H, T * d)), _arg("rope_cos", rope_cos, f32, dev, table),
+         _arg("w_up_v", w_up_v, sd, dev, (T, H, d, dm.r_v)), _arg("mu_k", mu_k, f32, dev, mu),
+         _arg("mu_v", mu_v, f32, dev, mu), _arg("rope_cos", rope_cos, f32, dev, table),
          _arg("rope_sin", rope_sin, f32, dev, table), table[0], _arg("out", out, sd, dev, vec),
-         None if lse is None else _arg("lse", lse, f32, dev, (tree.n_tok, H)), ws, wb)
+         None if lse is None else _arg("lse", lse, f32, dev, (n, H)), ws, wb)
 
 
 def tree_attn(dm: Dims, loop_t: int, tree: DraftTree, q, k, v, cache_k, cache_v, seq_lens, w_up_k, w_up_v, mu_k, mu_v,
@@ -687,11 +694,12 @@ def tree_attn(dm: Dims, loop_t: int, tree: DraftTree, q, k, v, cache_k, cache_v,
     """lla_tree_attn: every node of ``tree`` attends to its sequence's cached latents and to the nodes
     on its path.  q, k, v [n_tok][H][d] (token stride free) of loop ``loop_t``, before RoPE; ``out``
     [n_tok][H][d] (storage dtype), ``lse`` [n_tok][H] (fp32) or None."""
-    sd, dev = _storage(dm), tree.dev
-    _need(cache_k.dim() == 4, "cache_k must be [B][H][L_max][r_k]")
-    B, L_max = cache_k.shape[0], cache_k.shape[2]
-    cache = Cache(_arg("cache_k", cache_k, sd, dev, (B, dm.H, L_max, dm.r_k)),
-                  _arg("cache_v", cache_v, sd, dev, (B, dm.H, L_max, dm.r_v)), B, L_max)
+    sd, dev, shape = _storage(dm), tree.dev, cache_k.shape
+    if len(shape) != 4:
+        raise ValueError("cache_k must be [B][H][L_max][r_k]")
+    B, L_max, H = shape[0], shape[2], dm.H
+    cache = Cache(_arg("cache_k", cache_k, sd, dev, (B, H, L_max, dm.r_k)),
+                  _arg("cache_v", cache_v, sd, dev, (B, H, L_max, dm.r_v)), B, L_max)
     _tree_attn("lla_tree_attn", lib().lla_tree_attn, dm, loop_t, tree, q, k, v, cache, B, seq_lens, w_up_k, w_up_v, mu_k,
                mu_v, rope_cos, rope_sin, out, lse, workspace, stream)
 
@@ -700,12 +708,12 @@ def tree_attn_paged(dm: Dims, loop_t: int, tree: DraftTree, q, k, v, pool_k, poo
                     seq_lens, w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, out, lse, workspace, stream=None):
     """lla_tree_attn_paged: tree_attn over pools [num_pages][H][page_size][r] and a block table
     [B][max_pages]."""
-    sd, dev = _storage(dm), tree.dev
-    _need(pool_k.dim() == 4 and pool_k.shape[2] == page_size, "pool_k must be [num_pages][H][%d][r_k]" % page_size)
-    num, table = pool_k.shape[0], block_table.shape
-    _need(len(table) == 2, "block_table must be [B][max_pages]")
-    cache = PagedCache(_arg("pool_k", pool_k, sd, dev, (num, dm.H, page_size, dm.r_k)),
-                       _arg("pool_v", pool_v, sd, dev, (num, dm.H, page_size, dm.r_v)),
+    sd, dev, H, table = _storage(dm), tree.dev, dm.H, block_table.shape
+    if len(pool_k.shape) != 4 or len(table) != 2:
+        raise ValueError("pools must be [num_pages][H][page_size][r], block_table [B][max_pages]")
+    num = pool_k.shape[0]
+    cache = PagedCache(_arg("pool_k", pool_k, sd, dev, (num, H, page_size, dm.r_k)),
+                       _arg("pool_v", pool_v, sd, dev, (num, H, page_size, dm.r_v)),
                        _arg("block_table", block_table, torch.int32, dev, table), table[0], table[1], page_size, num)
     _tree_attn("lla_tree_attn_paged", lib().lla_tree_attn_paged, dm, loop_t, tree, q, k, v, cache, table[0], seq_lens,
                w_up_k, w_up_v, mu_k, mu_v, rope_cos, rope_sin, out, lse, workspace, stream)
@@ -769,23 +777,25 @@ def logits_adjust(tree: DraftTree, token, logits, rules: LogitRules, out=None, b
     and its log-sum-exp into ``lse`` [n_tok] (fp32); at least one of the three.  ``token`` [n_tok]
     (int32) are the nodes' tokens."""
     dev, n = tree.dev, tree.n_tok
-    _need(isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.shape[0] == n and logits.get_device() == dev,
-          "logits must be [%d][vocab] on cuda:%d" % (n, dev))
-    dtype, V = logits.dtype, logits.shape[1]
-    _need(dtype in _LOGIT_TYPES, "logits must be bfloat16 or float32, not %s" % (dtype,))
-    _need(V <= 1 or logits.stride(1) == 1, "each row of logits must be contiguous")
-    if out is not None:
-        _need(out.dtype is dtype and out.get_device() == dev and out.shape == logits.shape and
-              (V <= 1 or out.stride(1) == 1), "out must be like logits")
-    _need(rules.dev in (None, dev), "the rules are on cuda:%s, not on cuda:%d" % (rules.dev, dev))
-    _need(rules.B in (None, tree.B), "the rules are for %s sequences, the tree for %d" % (rules.B, tree.B))
-    _need(rules.n_tok in (None, n), "allowed_row has %s entries, the tree %d" % (rules.n_tok, n))
-    _need(rules.words in (None, (V + 31) // 32), "a mask has %s words, %d tokens need %d" % (rules.words, V, (V + 31) // 32))
-    row = lambda t: t.stride(0) if n > 1 else V  # noqa: E731
+    shape, dtype = logits.shape, logits.dtype
+    if len(shape) != 2 or shape[0] != n or logits.get_device() != dev or dtype not in _LOGIT_TYPES:
+        raise ValueError("logits must be bfloat16 or float32 [%d][vocab] on cuda:%d" % (n, dev))
+    V = shape[1]
+    xs, os = logits.stride(), (V, 1) if out is None else out.stride()
+    if not (out is None or out.dtype is dtype and out.get_device() == dev and out.shape == shape):
+        raise ValueError("out must be like logits")
+    if V > 1 and (xs[1] != 1 or os[1] != 1):
+        raise ValueError("each row of logits and out must be contiguous")
+    if rules.dev not in (None, dev) or rules.B not in (None, tree.B) or rules.n_tok not in (None, n) or \
+            rules.words not in (None, (V + 31) // 32):
+        raise ValueError("the rules are for %s sequences, %s tokens and masks of %s words on cuda:%s; the call has %d, %d, %d "
+                         "and cuda:%d" % (rules.B, rules.n_tok, rules.words, rules.dev, tree.B, n, (V + 31) // 32, dev))
+    # (torch leaves the stride of a single row open)
     ws, wb = _space(workspace, dev)
     _run("lla_logits_adjust", lib().lla_logits_adjust, dev, stream, tree.ref, _arg("token", token, torch.int32, dev, (n,)),
-         _LOGIT_TYPES[dtype], logits.data_ptr(), row(logits), V, rules.ref, None if out is None else out.data_ptr(),
-         0 if out is None else row(out), None if best is None else _arg("best", best, torch.int32, dev, (n,)),
+         _LOGIT_TYPES[dtype], logits.data_ptr(), xs[0] if n > 1 else V, V, rules.ref,
+         None if out is None else out.data_ptr(), os[0] if n > 1 else V,
+         None if best is None else _arg("best", best, torch.int32, dev, (n,)),
          None if lse is None else _arg("lse", lse, torch.float32, dev, (n,)), ws, wb)
 
 
