@@ -2,12 +2,14 @@
 // every node under its request's rules (lla_logits_adjust) and the walk down the tree along the
 // chosen tokens (lla_tree_accept).
 //
-// Logits: one pass.  A block takes a slice of the vocabulary of one sequence and up to `group` of
-// its nodes: the slice's counts (output part of the history) and prompt marks are made once in
-// shared memory, each node adds the tokens on its own path and takes them away again, and only
-// stretches of 64 tokens in which anything is counted or biased look at them.  Best token and
-// log-sum-exp come out of the same pass, a partial result per (node, slice) that a second launch
-// merges in a fixed order.  Memory-bound: each logit is read and written once.
+// Logits: one pass.  A block takes a slice of the vocabulary of one sequence and some of its nodes; each of
+// its warps owns a window of the slice, for all of these nodes, and never waits for another while it
+// goes through them.  What the history and the biases touch is counted once per block in shared memory and
+// listed per window: a node's pass streams the window's logits, leaving out the listed tokens by a bitmap, and
+// then takes the listed ones one by one through the whole formula.  The tokens on a node's path join the
+// window's counts and list for that node and leave them again.  Best token and log-sum-exp come out of the
+// same pass, a partial result per (node, slice) that a second launch merges in a fixed order.
+// Memory-bound: each logit is read and written once.
 #include <algorithm>
 
 #include "lla_kernels.h"
@@ -20,15 +22,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxNodes = LLA_TREE_MAX_NODES;
 constexpr int kSlice = 4096;            // tokens of a slice
 constexpr int kLogitThreads = 256;
-constexpr int kStretch = 64;            // tokens a warp takes at a time
-constexpr int kSteps = kSlice / (kLogitThreads / 32 * kStretch);
-constexpr uint32_t kPrompt = 0x80000000u;   // mark of a token of the prompt part; the rest is the count
+constexpr int kLogitWarps = kLogitThreads / 32;
+constexpr int kWindow = kSlice / kLogitWarps;          // tokens of a warp
+constexpr int kPerLane = kWindow / 32;
+constexpr int kGroup = 16;              // most nodes of a block
+// marks in a token's count: it occurs in the prompt part; it has a bias
+constexpr uint32_t kPrompt = 0x80000000u, kBiased = 0x40000000u, kTimes = kBiased - 1;
 constexpr int kMaxVocab = 1 << 22;
 
 struct Partial {
   float m, s;      // largest value; sum of exp(x - ref(m))
   int32_t best;    // its lowest index, -1: none
-  int32_t pad;
 };
 
 struct LogitArgs {
@@ -77,65 +81,105 @@ __device__ __forceinline__ void warp_merge(float& m, float& s, int& best) {
   m = mw;
 }
 
-// Two neighbouring tokens' logits (or, unpaired, tokens 32 apart).
-template <typename T, bool kPair>
-__device__ __forceinline__ float2 load2(const T* p, int lane, int left) {
-  float2 v = make_float2(-INFINITY, -INFINITY);
-  if constexpr (kPair) {
-    // (a row of an odd vocabulary ends within a pair)
-    const int i = 2 * lane;
-    if constexpr (sizeof(T) == 2) {
-      if (i + 1 < left) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(p + i);
-        v = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-      } else if (i < left) {
-        v.x = __bfloat162float(p[i]);
+// Which of a window's tokens a lane takes: 16 of them, in rising order.  Rows that start on 16 bytes
+// (kVec): stretches of 16 bytes; others: every 32nd token.
+template <typename T, bool kVec>
+struct Lanes {
+  static constexpr int kRun = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;   // neighbouring tokens
+  __device__ static int token(int lane, int e) { return (e / kRun) * 32 * kRun + lane * kRun + e % kRun; }
+  // Bits of the lane's tokens out of a bitmap of the window (`words` of its words exist).
+  __device__ static uint32_t bits(const uint32_t* map, int lane, int words) {
+    uint32_t r = 0;
+    if constexpr (kVec) {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kRun; ++v) {
+        const int bit = v * 32 * kRun + lane * kRun, w = bit >> 5;
+        if (w < words) r |= ((map[w] >> (bit & 31)) & ((1u << kRun) - 1u)) << (v * kRun);
       }
     } else {
-      if (i + 1 < left) v = *reinterpret_cast<const float2*>(p + i);
-      else if (i < left) v.x = p[i];
+#pragma unroll 4
+      for (int e = 0; e < kPerLane; ++e)
+        if (e < words) r |= ((map[e] >> lane) & 1u) << e;
     }
-  } else {
-    if constexpr (sizeof(T) == 2) {
-      if (lane < left) v.x = __bfloat162float(p[lane]);
-      if (lane + 32 < left) v.y = __bfloat162float(p[lane + 32]);
+    return r;
+  }
+  // The lane's logits; -inf past `left`.
+  __device__ static void load(const T* p, int lane, int left, float (&x)[kPerLane]) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kRun; ++v) {
+        const int i = v * 32 * kRun + lane * kRun;
+        if (i + kRun <= left) {
+          const uint4 w = *reinterpret_cast<const uint4*>(p + i);
+          if constexpr (sizeof(T) == 2) {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              x[v * kRun + 2 * k] = __uint_as_float(u[k] << 16);
+              x[v * kRun + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+            }
+          } else {
+            x[v * kRun] = __uint_as_float(w.x);
+            x[v * kRun + 1] = __uint_as_float(w.y);
+            x[v * kRun + 2] = __uint_as_float(w.z);
+            x[v * kRun + 3] = __uint_as_float(w.w);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kRun; ++k) x[v * kRun + k] = i + k < left ? static_cast<float>(p[i + k]) : -INFINITY;
+        }
+      }
     } else {
-      if (lane < left) v.x = p[lane];
-      if (lane + 32 < left) v.y = p[lane + 32];
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = 32 * e + lane < left ? static_cast<float>(p[32 * e + lane]) : -INFINITY;
     }
   }
-  return v;
-}
-
-template <typename T, bool kPair>
-__device__ __forceinline__ void store2(T* p, int lane, int left, float2 v) {
-  const int i0 = kPair ? 2 * lane : lane, i1 = kPair ? 2 * lane + 1 : lane + 32;
-  if constexpr (sizeof(T) == 2) {
-    if (kPair && i1 < left) {
-      *reinterpret_cast<__nv_bfloat162*>(p + i0) = __floats2bfloat162_rn(v.x, v.y);
+  __device__ static void store(T* p, int lane, int left, const float (&x)[kPerLane]) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kRun; ++v) {
+        const int i = v * 32 * kRun + lane * kRun;
+        if (i + kRun <= left) {
+          uint4 w;
+          if constexpr (sizeof(T) == 2) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x[v * kRun + 2 * k], x[v * kRun + 2 * k + 1]);
+              u[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            w = make_uint4(u[0], u[1], u[2], u[3]);
+          } else {
+            w = make_uint4(__float_as_uint(x[v * kRun]), __float_as_uint(x[v * kRun + 1]), __float_as_uint(x[v * kRun + 2]),
+                           __float_as_uint(x[v * kRun + 3]));
+          }
+          *reinterpret_cast<uint4*>(p + i) = w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < kRun; ++k)
+            if (i + k < left) p[i + k] = static_cast<T>(x[v * kRun + k]);
+        }
+      }
     } else {
-      if (i0 < left) p[i0] = __float2bfloat16_rn(v.x);
-      if (i1 < left) p[i1] = __float2bfloat16_rn(v.y);
-    }
-  } else {
-    if (kPair && i1 < left) {
-      *reinterpret_cast<float2*>(p + i0) = v;
-    } else {
-      if (i0 < left) p[i0] = v.x;
-      if (i1 < left) p[i1] = v.y;
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e)
+        if (32 * e + lane < left) p[32 * e + lane] = static_cast<T>(x[e]);
     }
   }
-}
+};
 
-template <typename T, bool kPair>
+template <typename T, bool kVec>
 __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_constant__ LogitArgs a) {
-  __shared__ uint32_t cnt[kSlice];
+  __shared__ uint32_t cnt[kSlice];                  // occurrences and marks
   __shared__ float bias[kSlice];
-  __shared__ uint32_t touched[kSlice / kStretch];
+  __shared__ uint16_t list[kSlice];                 // per window: its touched tokens
+  __shared__ uint32_t touched[kSlice / 32];         // the same as bits
   __shared__ int32_t tok[kMaxNodes];
   __shared__ int32_t jump[2][kMaxNodes];
   __shared__ uint32_t path[2][kMaxNodes][kMaxNodes / 32];
-  __shared__ Partial red[2][kLogitThreads / 32];
+  __shared__ Partial part[kGroup][kLogitWarps];
+  __shared__ int again;                             // a token has more than one bias
+  using L = Lanes<T, kVec>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.slices, slice = blockIdx.x - b * a.slices;
   int first;
@@ -145,8 +189,8 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_cons
   const bool flag = slice == 0 && blockIdx.y == 0;      // the block that reports what it skips
   const int lo = slice * kSlice, width = min(kSlice, a.vocab - lo);
 
-  for (int i = tid; i < kSlice; i += kLogitThreads) { cnt[i] = 0; bias[i] = 0.f; }
-  if (tid < kSlice / kStretch) touched[tid] = 0;
+  for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) again = 0;
   for (int i = tid; i < n; i += kLogitThreads) {
     const int t = __ldg(a.token + first + i);
     int p = __ldg(a.parent + first + i);
@@ -182,12 +226,12 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_cons
       pl = min(max(pl, 0), hl);
     }
     const int32_t* hist = a.r.history + static_cast<int64_t>(b) * a.r.max_history;
+#pragma unroll 4
     for (int i = tid; i < hl; i += kLogitThreads) {
       const int t = __ldg(hist + i);
       if (t >= lo && t < lo + width) {
         if (i < pl) atomicOr(&cnt[t - lo], kPrompt);
         else atomicAdd(&cnt[t - lo], 1u);
-        touched[(t - lo) / kStretch] = 1;
       } else if (flag && (t < 0 || t >= a.vocab)) {
         record_status(a.status, LLA_ERR_DEVICE_ARG);
       }
@@ -199,107 +243,159 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_cons
     for (int i = tid; i < a.r.max_bias; i += kLogitThreads) {
       const int t = __ldg(bt + i);
       if (t >= lo && t < lo + width) {
-        // the first entry of a token adds up all of them, in list order
-        bool again = false;
-        for (int j = 0; j < i; ++j) again |= __ldg(bt + j) == t;
-        if (!again) {
-          float sum = __ldg(bv + i);
-          for (int j = i + 1; j < a.r.max_bias; ++j)
-            if (__ldg(bt + j) == t) sum += __ldg(bv + j);
-          bias[t - lo] = sum;
-          touched[(t - lo) / kStretch] = 1;
-        }
+        if (atomicOr(&cnt[t - lo], kBiased) & kBiased) again = 1;
+        else bias[t - lo] = __ldg(bv + i);
       } else if (flag && t >= a.vocab) {
         record_status(a.status, LLA_ERR_DEVICE_ARG);
       }
     }
+    __syncthreads();
+    if (again) {
+      // the first entry of a token adds up all of them, in list order
+      for (int i = tid; i < a.r.max_bias; i += kLogitThreads) {
+        const int t = __ldg(bt + i);
+        if (t < lo || t >= lo + width) continue;
+        bool later = false;
+        for (int j = 0; j < i; ++j) later |= __ldg(bt + j) == t;
+        if (later) continue;
+        float sum = __ldg(bv + i);
+        for (int j = i + 1; j < a.r.max_bias; ++j)
+          if (__ldg(bt + j) == t) sum += __ldg(bv + j);
+        bias[t - lo] = sum;
+      }
+    }
   }
+  __syncthreads();
+
+  // ---- from here on a warp is on its own with its window
+  const int w0 = warp * kWindow, left = width - w0;
+  uint16_t* mine = list + w0;
+  uint32_t* map = touched + w0 / 32;
+  int listed = 0;
+#pragma unroll 4
+  for (int k = 0; k < kPerLane; ++k) {
+    const uint32_t m = __ballot_sync(0xffffffffu, cnt[w0 + 32 * k + lane] != 0);
+    if (lane == 0) map[k] = m;
+    if (m >> lane & 1u) mine[listed + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(w0 + 32 * k + lane);
+    listed += __popc(m);
+  }
+  __syncwarp();
   const float rep = a.r.repetition ? __ldg(a.r.repetition + b) : 1.f;
   const float pres = a.r.presence ? __ldg(a.r.presence + b) : 0.f;
   const float freq = a.r.frequency ? __ldg(a.r.frequency + b) : 0.f;
+  const int row1 = min(n, row0 + a.group), words = left > 0 ? min(kPerLane, (left + 31) / 32) : 0;
 
-  const int row1 = min(n, row0 + a.group);
-  for (int row = row0; row < row1; ++row) {
-    // ---- this node's path joins the counts
-    auto on_path = [&]() {
-      return tid < n && (path[cur][row][tid >> 5] >> (tid & 31) & 1u) && tok[tid] >= lo && tok[tid] < lo + width;
-    };
-    // (the counts of the history, or the undoing of the node before, may still be under way in
-    // other warps: additions commute, and the barrier below comes before any is read)
-    if (on_path()) {
-      atomicAdd(&cnt[tok[tid] - lo], 1u);
-      touched[(tok[tid] - lo) / kStretch] = 1;
-    }
-    __syncthreads();
+  for (int row = row0; row < row1 && left > 0; ++row) {
     const int64_t at = first + row;
-    const T* src = static_cast<const T*>(a.logits) + at * a.row_stride + lo;
-    T* dst = a.out ? static_cast<T*>(a.out) + at * a.out_stride + lo : nullptr;
-    float2 x[kSteps];
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int g = (k * (kLogitThreads / 32) + warp) * kStretch;
-      x[k] = load2<T, kPair>(src + g, lane, width - g);
-    }
+    const T* src = static_cast<const T*>(a.logits) + at * a.row_stride + lo + w0;
+    T* dst = a.out ? static_cast<T*>(a.out) + at * a.out_stride + lo + w0 : nullptr;
+    float x[kPerLane];
+    L::load(src, lane, left, x);
     const uint32_t* mask = nullptr;
     if (a.r.n_masks > 0) {
       const int mr = __ldg(a.r.allowed_row + at);
       if (mr >= a.r.n_masks) {
         if (slice == 0 && tid == 0) record_status(a.status, LLA_ERR_DEVICE_ARG);
       } else if (mr >= 0) {
-        mask = a.r.allowed + static_cast<int64_t>(mr) * a.mask_words + lo / 32;
+        mask = a.r.allowed + static_cast<int64_t>(mr) * a.mask_words + (lo + w0) / 32;
       }
     }
-    float m = -INFINITY;
+    // ---- this node's path joins the counts, the list and the bitmap
+    int more = 0;
+    uint32_t fresh = 0, on = 0;                     // of the lane's four nodes: listed just now; in the window
+#pragma unroll
+    for (int k = 0; k < kMaxNodes / 32; ++k) {
+      const int i = 32 * k + lane, t = i < n ? tok[i] - lo - w0 : -1;
+      const bool here = t >= 0 && t < min(left, kWindow) && (path[cur][row][k] >> lane & 1u);
+      if (!__any_sync(0xffffffffu, here)) continue;
+      const bool first_of = here && atomicAdd(&cnt[w0 + t], 1u) == 0;
+      const uint32_t f = __ballot_sync(0xffffffffu, first_of);
+      if (here) on |= 1u << k;
+      if (first_of) {
+        fresh |= 1u << k;
+        mine[listed + more + __popc(f & ((1u << lane) - 1u))] = static_cast<uint16_t>(w0 + t);
+        atomicOr(&map[t >> 5], 1u << (t & 31));
+      }
+      more += __popc(f);
+      __syncwarp();
+    }
+    // ---- what nothing touches
+    if (mask) {
+      const uint32_t allowed = L::bits(mask, lane, words);
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e)
+        if (!(allowed >> e & 1u)) x[e] = -INFINITY;
+    }
+    // (in place and without a mask these logits stay as they are)
+    if (dst && (mask || static_cast<const void*>(dst) != src)) L::store(dst, lane, left, x);
+    if (listed + more > 0) {
+      const uint32_t skip = L::bits(map, lane, words);
+      if (skip) {
+#pragma unroll
+        for (int e = 0; e < kPerLane; ++e)
+          if (skip >> e & 1u) x[e] = -INFINITY;
+      }
+    }
+    float m = x[0];
+#pragma unroll
+    for (int e = 1; e < kPerLane; ++e) m = fmaxf(m, x[e]);
+    if (m != m) m = -INFINITY;                      // nothing but NaN
+    float ref = ref_of(m), s = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPerLane; ++e) s += exp2f((x[e] - ref) * kLog2e);
     int best = -1;
+    if (m == warp_max(m) && m > -INFINITY) {        // (only a lane that may hold the warp's best looks for it)
+      uint32_t eq = 0;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int g = (k * (kLogitThreads / 32) + warp) * kStretch;
-      const int i0 = g + (kPair ? 2 * lane : lane), i1 = g + (kPair ? 2 * lane + 1 : lane + 32);
-      if (touched[g / kStretch]) {
-        float* v = &x[k].x;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = e == 0 ? i0 : i1;
-          const uint32_t c = cnt[i];
-          // each step rounded by itself, as the formulas are written
-          if (c != 0) {
-            const uint32_t times = c & ~kPrompt;
-            v[e] = v[e] > 0.f ? __fdiv_rn(v[e], rep) : __fmul_rn(v[e], rep);
-            v[e] = __fsub_rn(v[e], __fmul_rn(freq, static_cast<float>(times)));
-            if (times) v[e] = __fsub_rn(v[e], pres);
-          }
-          if (a.r.max_bias > 0) v[e] = __fadd_rn(v[e], bias[i]);
-        }
-      }
-      if (mask && g < width) {
-        const uint32_t w0 = __ldg(mask + g / 32), w1 = g + 32 < width ? __ldg(mask + g / 32 + 1) : 0u;
-        const uint32_t bits = kPair ? (lane < 16 ? w0 : w1) >> ((2 * lane) & 31) : (w0 >> lane & 1u) | (w1 >> lane & 1u) << 1;
-        if (!(bits & 1u)) x[k].x = -INFINITY;
-        if (!(bits & 2u)) x[k].y = -INFINITY;
-      }
-      if (dst) store2<T, kPair>(dst + g, lane, width - g, x[k]);
-      // (tokens past the end of the vocabulary take no part, whatever was added to them)
-      if (i0 >= width) x[k].x = -INFINITY;
-      if (i1 >= width) x[k].y = -INFINITY;
-      if (x[k].x > m) { m = x[k].x; best = lo + i0; }
-      if (x[k].y > m) { m = x[k].y; best = lo + i1; }
+      for (int e = 0; e < kPerLane; ++e) eq |= (x[e] == m ? 1u : 0u) << e;
+      best = lo + w0 + L::token(lane, __ffs(eq) - 1);
     }
-    const float ref = ref_of(m);
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) s += exp2f((x[k].x - ref) * kLog2e) + exp2f((x[k].y - ref) * kLog2e);
+    // ---- what the history, the biases or the path touch: each step rounded by itself, as the formulas are written
+    __syncwarp();
+    for (int j = lane; j < listed + more; j += 32) {
+      const int i = mine[j];
+      const uint32_t c = cnt[i], times = c & kTimes;
+      float v = static_cast<float>(src[i - w0]);    // (in place: as it was, or -inf where it is masked)
+      if (c & ~kBiased) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+      if (times) v = __fsub_rn(__fsub_rn(v, __fmul_rn(freq, static_cast<float>(times))), pres);
+      if (c & kBiased) v = __fadd_rn(v, bias[i]);
+      if (mask && !(__ldg(mask + (i - w0) / 32) >> (i & 31) & 1u)) v = -INFINITY;
+      if (dst) dst[i - w0] = static_cast<T>(v);
+      const int id = lo + i;
+      if (v > m || (v == m && v > -INFINITY && (best < 0 || id < best))) best = id;
+      const float m2 = fmaxf(m, v), r2 = ref_of(m2);
+      s = rebase(s, ref, r2) + exp2f((v - r2) * kLog2e);
+      m = m2;
+      ref = r2;
+    }
     warp_merge(m, s, best);
-    if (lane == 0) red[row & 1][warp] = Partial{m, s, best, 0};
-    __syncthreads();
-    if (warp == 0) {
-      const Partial p = lane < kLogitThreads / 32 ? red[row & 1][lane] : Partial{-INFINITY, 0.f, -1, 0};
-      m = p.m;
-      s = p.s;
-      best = p.best;
-      warp_merge(m, s, best);
-      if (lane == 0) a.partials[at * a.slices + slice] = Partial{m, s, best, 0};
+    if (lane == 0) part[row - row0][warp] = Partial{m, s, best};
+    // ---- and the path leaves them again
+    if (more > 0 || __any_sync(0xffffffffu, on != 0)) {
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kMaxNodes / 32; ++k) {
+        if (!(on >> k & 1u)) continue;
+        const int t = tok[32 * k + lane] - lo - w0;
+        atomicSub(&cnt[w0 + t], 1u);
+        if (fresh >> k & 1u) atomicAnd(&map[t >> 5], ~(1u << (t & 31)));
+      }
+      __syncwarp();
     }
-    if (on_path()) atomicSub(&cnt[tok[tid] - lo], 1u);
+  }
+  __syncthreads();
+  // ---- the windows of each node, in order
+  const int windows = (width + kWindow - 1) / kWindow;
+  for (int r = tid; r < row1 - row0; r += kLogitThreads) {
+    Partial p = part[r][0];
+    for (int w = 1; w < windows; ++w) {
+      const Partial y = part[r][w];
+      const float m2 = fmaxf(p.m, y.m), r2 = ref_of(m2);
+      p.s = rebase(p.s, ref_of(p.m), r2) + rebase(y.s, ref_of(y.m), r2);
+      if (y.m > p.m) p.best = y.best;
+      p.m = m2;
+    }
+    a.partials[(first + row0 + r) * static_cast<int64_t>(a.slices) + slice] = p;
   }
 }
 
@@ -474,7 +570,7 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
   a.vocab = vocab;
   a.slices = slices;
   // nodes a block: as many as leave eight blocks an SM, so that a slice's counts are made once for them
-  a.group = static_cast<int>(std::min<int64_t>(tree->max_nodes, std::max<int64_t>(1, static_cast<int64_t>(tree->n_tok) * slices / (8 * sms))));
+  a.group = static_cast<int>(std::min<int64_t>(std::min(tree->max_nodes, kGroup), std::max<int64_t>(1, static_cast<int64_t>(tree->n_tok) * slices / (8 * sms))));
   a.tok_start = tree->tok_start;
   a.parent = tree->parent;
   a.token = token;
@@ -490,15 +586,15 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid(static_cast<unsigned>(tree->B) * slices, (tree->max_nodes + a.group - 1) / a.group);
-  // a thread takes two neighbouring tokens at once where every row starts on a pair
-  const uintptr_t pair = 2 * es;
-  const bool paired = reinterpret_cast<uintptr_t>(logits) % pair == 0 && row_stride % 2 == 0 &&
-                      (!out || (reinterpret_cast<uintptr_t>(out) % pair == 0 && out_stride % 2 == 0));
+  // a lane takes 16 bytes of neighbouring tokens at once where every row starts on 16 bytes
+  const int64_t run = 16 / static_cast<int64_t>(es);
+  const bool vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && row_stride % run == 0 &&
+                   (!out || (reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_stride % run == 0));
   if (dtype == LLA_BF16) {
-    if (paired) logits_kernel<__nv_bfloat16, true><<<grid, kLogitThreads, 0, s>>>(a);
+    if (vec) logits_kernel<__nv_bfloat16, true><<<grid, kLogitThreads, 0, s>>>(a);
     else logits_kernel<__nv_bfloat16, false><<<grid, kLogitThreads, 0, s>>>(a);
   } else {
-    if (paired) logits_kernel<float, true><<<grid, kLogitThreads, 0, s>>>(a);
+    if (vec) logits_kernel<float, true><<<grid, kLogitThreads, 0, s>>>(a);
     else logits_kernel<float, false><<<grid, kLogitThreads, 0, s>>>(a);
   }
   if (cudaGetLastError() != cudaSuccess) return LLA_ERR_CUDA;
