@@ -4,11 +4,11 @@
 //
 // Logits: one pass.  A block takes a slice of the vocabulary of one sequence and some of its nodes; each of
 // its warps owns a window of the slice, for all of these nodes, and never waits for another while it
-// goes through them.  What the history and the biases touch is counted once per block in shared memory and
-// listed per window: a node's pass streams the window's logits, leaving out the listed tokens by a bitmap, and
-// then takes the listed ones one by one through the whole formula.  The tokens on a node's path join the
-// window's counts and list for that node and leave them again.  Best token and log-sum-exp come out of the
-// same pass, a partial result per (node, slice) that a second launch merges in a fixed order.
+// goes through them.  What the history and the biases touch is counted once per block in shared memory,
+// and listed per window; a node's pass streams the window's logits and takes the listed ones through the whole
+// formula.  The tokens on a node's path join the window's counts and list for that node and leave them
+// again.  Best token and log-sum-exp come out of the same pass, a partial result per (node, slice) that a
+// second launch merges in a fixed order.
 // Memory-bound: each logit is read and written once.
 #include <algorithm>
 
@@ -26,8 +26,7 @@ constexpr int kLogitWarps = kLogitThreads / 32;
 constexpr int kWindow = kSlice / kLogitWarps;          // tokens of a warp
 constexpr int kPerLane = kWindow / 32;
 constexpr int kGroup = 16;              // most nodes of a block
-// marks in a token's count: it occurs in the prompt part; it has a bias
-constexpr uint32_t kPrompt = 0x80000000u, kBiased = 0x40000000u, kTimes = kBiased - 1;
+constexpr int kHeldBiases = 256;        // biases of a slice that shared memory has room for
 constexpr int kMaxVocab = 1 << 22;
 
 struct Partial {
@@ -66,14 +65,27 @@ __device__ __forceinline__ int nodes_of(const int32_t* tok_start, int b, int n_t
 // infinite (so that infinities give sums of 0 and infinity, not NaN).
 __device__ __forceinline__ float ref_of(float m) { return fabsf(m) == INFINITY ? 0.f : m; }
 
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+// 2^x (sums of logits' exponentials: an error of 2^-22 a term).
+__device__ __forceinline__ float exp2_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // A sum relative to `from`, relative to `to`.
 __device__ __forceinline__ float rebase(float s, float from, float to) {
-  return s == 0.f ? 0.f : s * exp2f((from - to) * kLog2e);
+  return s == 0.f ? 0.f : s * exp2_of((from - to) * kLog2e);
 }
 
 // Maximum, its lowest index and the sum over a warp.
 __device__ __forceinline__ void warp_merge(float& m, float& s, int& best) {
-  const float mw = warp_max(m);
+  const float mw = warp_max_redux(m);
   s = warp_sum(rebase(s, ref_of(m), ref_of(mw)));
   const uint32_t i = m == mw && best >= 0 ? static_cast<uint32_t>(best) : 0x7FFFFFFFu;
   const uint32_t lo = __reduce_min_sync(0xffffffffu, i);
@@ -87,6 +99,13 @@ template <typename T, bool kVec>
 struct Lanes {
   static constexpr int kRun = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;   // neighbouring tokens
   __device__ static int token(int lane, int e) { return (e / kRun) * 32 * kRun + lane * kRun + e % kRun; }
+  // Where a lane's logit e, or a token's, lies in shared memory: lane by lane, so that neither side's
+  // accesses meet in a bank more often than they have to.
+  __device__ static int place(int lane, int e) { return 32 * e + lane; }
+  __device__ static int place_of(int t) {
+    const int run = t / kRun, e = (run / 32) * kRun + t % kRun;
+    return 32 * e + run % 32;
+  }
   // Bits of the lane's tokens out of a bitmap of the window (`words` of its words exist).
   __device__ static uint32_t bits(const uint32_t* map, int lane, int words) {
     uint32_t r = 0;
@@ -103,35 +122,49 @@ struct Lanes {
     }
     return r;
   }
-  // The lane's logits; -inf past `left`.
-  __device__ static void load(const T* p, int lane, int left, float (&x)[kPerLane]) {
+  // The lane's logits as they lie in memory (a node's are requested while the one before it is worked on).
+  struct Raw {
+    uint4 v[kVec ? kPerLane / kRun : 1];
+    T one[kVec ? 1 : kPerLane];
+  };
+  __device__ static T nothing() { return static_cast<T>(-INFINITY); }
+  __device__ static void fetch(const T* p, int lane, int left, Raw& r) {
     if constexpr (kVec) {
 #pragma unroll
       for (int v = 0; v < kPerLane / kRun; ++v) {
         const int i = v * 32 * kRun + lane * kRun;
         if (i + kRun <= left) {
-          const uint4 w = *reinterpret_cast<const uint4*>(p + i);
-          if constexpr (sizeof(T) == 2) {
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+          r.v[v] = *reinterpret_cast<const uint4*>(p + i);
+        } else {                                    // -inf past the end
+          T t[kRun];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[v * kRun + 2 * k] = __uint_as_float(u[k] << 16);
-              x[v * kRun + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-            }
-          } else {
-            x[v * kRun] = __uint_as_float(w.x);
-            x[v * kRun + 1] = __uint_as_float(w.y);
-            x[v * kRun + 2] = __uint_as_float(w.z);
-            x[v * kRun + 3] = __uint_as_float(w.w);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < kRun; ++k) x[v * kRun + k] = i + k < left ? static_cast<float>(p[i + k]) : -INFINITY;
+          for (int k = 0; k < kRun; ++k) t[k] = i + k < left ? p[i + k] : nothing();
+          r.v[v] = *reinterpret_cast<const uint4*>(t);
         }
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < kPerLane; ++e) x[e] = 32 * e + lane < left ? static_cast<float>(p[32 * e + lane]) : -INFINITY;
+      for (int e = 0; e < kPerLane; ++e) r.one[e] = 32 * e + lane < left ? p[32 * e + lane] : nothing();
+    }
+  }
+  __device__ static void unpack(const Raw& r, float (&x)[kPerLane]) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int v = 0; v < kPerLane / kRun; ++v) {
+        const uint32_t u[4] = {r.v[v].x, r.v[v].y, r.v[v].z, r.v[v].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(T) == 2) {
+            x[v * kRun + 2 * k] = __uint_as_float(u[k] << 16);
+            x[v * kRun + 2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+          } else {
+            x[v * kRun + k] = __uint_as_float(u[k]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = static_cast<float>(r.one[e]);
     }
   }
   __device__ static void store(T* p, int lane, int left, const float (&x)[kPerLane]) {
@@ -168,29 +201,93 @@ struct Lanes {
   }
 };
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_constant__ LogitArgs a) {
-  __shared__ uint32_t cnt[kSlice];                  // occurrences and marks
-  __shared__ float bias[kSlice];
-  __shared__ uint16_t list[kSlice];                 // per window: its touched tokens
-  __shared__ uint32_t touched[kSlice / 32];         // the same as bits
-  __shared__ int32_t tok[kMaxNodes];
-  __shared__ int32_t jump[2][kMaxNodes];
-  __shared__ uint32_t path[2][kMaxNodes][kMaxNodes / 32];
-  __shared__ Partial part[kGroup][kLogitWarps];
-  __shared__ int again;                             // a token has more than one bias
+// Occurrences of a slice's tokens, with two marks (in the prompt part, has a bias) above them: 16 bits a token
+// where no history is longer than 14 bits can count, else 32.
+template <int kBits>
+struct Counts {
+  static constexpr uint32_t kPrompt = 1u << (kBits - 1), kBiased = 1u << (kBits - 2), kTimes = kBiased - 1;
+  static constexpr int kPer = 32 / kBits;           // tokens of a word
+  uint32_t word[kSlice / kPer];
+  __device__ uint32_t get(int i) const { return kPer == 1 ? word[i] : (word[i >> 1] >> (16 * (i & 1))) & 0xFFFFu; }
+  __device__ uint32_t mark(int i, uint32_t m) {     // the count before
+    return kPer == 1 ? atomicOr(&word[i], m) : (atomicOr(&word[i >> 1], m << (16 * (i & 1))) >> (16 * (i & 1))) & 0xFFFFu;
+  }
+  __device__ uint32_t add(int i) {
+    return kPer == 1 ? atomicAdd(&word[i], 1u) : (atomicAdd(&word[i >> 1], 1u << (16 * (i & 1))) >> (16 * (i & 1))) & 0xFFFFu;
+  }
+  __device__ void take(int i) {
+    if (kPer == 1) atomicSub(&word[i], 1u);
+    else atomicSub(&word[i >> 1], 1u << (16 * (i & 1)));
+  }
+};
+constexpr int kMaxTimes16 = (1 << 14) - 1;
+
+template <int kBits>
+struct LogitShared {
+  Counts<kBits> cnt;
+  uint32_t touched[kSlice / 32];                    // tokens with a count or a mark, as bits
+  int32_t tok[kMaxNodes];
+  uint32_t path[kMaxNodes][kMaxNodes / 32];         // the nodes on each node's path, as bits
+  Partial part[kGroup][kLogitWarps];
+  uint16_t list[kSlice];                            // per window: its touched tokens
+  union {
+    float stage[kLogitWarps][kWindow];              // a window's logits while they are worked on
+    struct {                                        // before that, steps of the paths' doubling
+      int32_t jump[2][kMaxNodes];
+      uint32_t path[2][kMaxNodes][kMaxNodes / 32];
+    } walk;
+  };
+  int biases;                                       // of the slice
+  int16_t bias_at[kHeldBiases];                     // their tokens
+  int32_t bias_entry[kHeldBiases];                  // and entries of the list
+};
+
+template <typename T, bool kVec, int kBits>
+__global__ void __launch_bounds__(kLogitThreads, 4) logits_kernel(const __grid_constant__ LogitArgs a) {
+  __shared__ LogitShared<kBits> sh;
+  using C = Counts<kBits>;
+  C& cnt = sh.cnt;
+  uint32_t* touched = sh.touched;
+  int32_t* tok = sh.tok;
+  auto& jump = sh.walk.jump;
+  auto& path = sh.walk.path;
+  auto& part = sh.part;
   using L = Lanes<T, kVec>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.slices, slice = blockIdx.x - b * a.slices;
+  // (the chain of loads below is what a block with one node takes: everything is requested as early as it can be)
+  const int lo = slice * kSlice, width = min(kSlice, a.vocab - lo);
+  const int w0 = warp * kWindow, left = width - w0, row0 = blockIdx.y * a.group;
+  int hl = 0, pl = 0;
+  constexpr int kEarly = 8;
+  int hist_early[kEarly], bias_early = -1;
+  const int32_t* hist = a.r.history + static_cast<int64_t>(b) * a.r.max_history;
+  const int32_t* bt = a.r.bias_token + static_cast<int64_t>(b) * a.r.max_bias;
+  const float* bv = a.r.bias + static_cast<int64_t>(b) * a.r.max_bias;
+  if (a.r.max_history > 0) {
+    hl = __ldg(a.r.hist_len + b);
+    pl = a.r.prompt_len ? __ldg(a.r.prompt_len + b) : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const int i = tid + k * kLogitThreads;
+    hist_early[k] = i < a.r.max_history ? __ldg(hist + i) : -1;
+  }
+  if (tid < a.r.max_bias) bias_early = __ldg(bt + tid);
+  const float rep = a.r.repetition ? __ldg(a.r.repetition + b) : 1.f;
+  const float pres = a.r.presence ? __ldg(a.r.presence + b) : 0.f;
+  const float freq = a.r.frequency ? __ldg(a.r.frequency + b) : 0.f;
   int first;
   const int n = nodes_of(a.tok_start, b, a.n_tok, a.max_nodes, first, a.status);
-  const int row0 = blockIdx.y * a.group;
   if (row0 >= n) return;
   const bool flag = slice == 0 && blockIdx.y == 0;      // the block that reports what it skips
-  const int lo = slice * kSlice, width = min(kSlice, a.vocab - lo);
+  const T* src = static_cast<const T*>(a.logits) + (static_cast<int64_t>(first) + row0) * a.row_stride + lo + w0;
+  typename L::Raw raw;
+  if (left > 0) L::fetch(src, lane, left, raw);
 
-  for (int i = tid; i < kSlice / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
-  if (tid == 0) again = 0;
+  for (int i = tid; i < kSlice / C::kPer / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt.word)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < kSlice / 32) touched[tid] = 0;
+  if (tid == 0) sh.biases = 0;
   for (int i = tid; i < n; i += kLogitThreads) {
     const int t = __ldg(a.token + first + i);
     int p = __ldg(a.parent + first + i);
@@ -216,81 +313,101 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_cons
     }
     __syncthreads();
   }
-  // ---- counts of the history and biases
-  if (a.r.max_history > 0) {
-    int hl = __ldg(a.r.hist_len + b);
-    int pl = a.r.prompt_len ? __ldg(a.r.prompt_len + b) : 0;
-    if (hl < 0 || hl > a.r.max_history || pl < 0 || pl > hl) {
-      if (flag) record_status(a.status, LLA_ERR_DEVICE_ARG);
-      hl = min(max(hl, 0), a.r.max_history);
-      pl = min(max(pl, 0), hl);
-    }
-    const int32_t* hist = a.r.history + static_cast<int64_t>(b) * a.r.max_history;
-#pragma unroll 4
-    for (int i = tid; i < hl; i += kLogitThreads) {
-      const int t = __ldg(hist + i);
-      if (t >= lo && t < lo + width) {
-        if (i < pl) atomicOr(&cnt[t - lo], kPrompt);
-        else atomicAdd(&cnt[t - lo], 1u);
-      } else if (flag && (t < 0 || t >= a.vocab)) {
-        record_status(a.status, LLA_ERR_DEVICE_ARG);
-      }
-    }
+  if (tid < n) {
+#pragma unroll
+    for (int w = 0; w < kMaxNodes / 32; ++w) sh.path[tid][w] = path[cur][tid][w];
   }
+  // ---- counts of the history and biases
+  if (hl < 0 || hl > a.r.max_history || pl < 0 || pl > hl) {
+    if (flag) record_status(a.status, LLA_ERR_DEVICE_ARG);
+    hl = min(max(hl, 0), a.r.max_history);
+    pl = min(max(pl, 0), hl);
+  }
+  auto count = [&](int i, int t) {
+    if (t >= lo && t < lo + width) {
+      const int at = t - lo;
+      if ((i < pl ? cnt.mark(at, C::kPrompt) : cnt.add(at)) == 0) atomicOr(&touched[at >> 5], 1u << (at & 31));
+    } else if (flag && (t < 0 || t >= a.vocab)) {
+      record_status(a.status, LLA_ERR_DEVICE_ARG);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (tid + k * kLogitThreads < hl) count(tid + k * kLogitThreads, hist_early[k]);
+#pragma unroll 4
+  for (int i = tid + kEarly * kLogitThreads; i < hl; i += kLogitThreads) count(i, __ldg(hist + i));
   if (a.r.max_bias > 0) {
-    const int32_t* bt = a.r.bias_token + static_cast<int64_t>(b) * a.r.max_bias;
-    const float* bv = a.r.bias + static_cast<int64_t>(b) * a.r.max_bias;
     for (int i = tid; i < a.r.max_bias; i += kLogitThreads) {
-      const int t = __ldg(bt + i);
+      const int t = i < kLogitThreads ? bias_early : __ldg(bt + i);
       if (t >= lo && t < lo + width) {
-        if (atomicOr(&cnt[t - lo], kBiased) & kBiased) again = 1;
-        else bias[t - lo] = __ldg(bv + i);
+        const int at = t - lo;
+        if (cnt.mark(at, C::kBiased) == 0) atomicOr(&touched[at >> 5], 1u << (at & 31));
+        const int k = atomicAdd(&sh.biases, 1);
+        if (k < kHeldBiases) {
+          sh.bias_at[k] = static_cast<int16_t>(at);
+          sh.bias_entry[k] = i;
+        }
       } else if (flag && t >= a.vocab) {
         record_status(a.status, LLA_ERR_DEVICE_ARG);
       }
     }
-    __syncthreads();
-    if (again) {
-      // the first entry of a token adds up all of them, in list order
-      for (int i = tid; i < a.r.max_bias; i += kLogitThreads) {
-        const int t = __ldg(bt + i);
-        if (t < lo || t >= lo + width) continue;
-        bool later = false;
-        for (int j = 0; j < i; ++j) later |= __ldg(bt + j) == t;
-        if (later) continue;
-        float sum = __ldg(bv + i);
-        for (int j = i + 1; j < a.r.max_bias; ++j)
-          if (__ldg(bt + j) == t) sum += __ldg(bv + j);
-        bias[t - lo] = sum;
-      }
-    }
   }
   __syncthreads();
+  // The bias of a token: the sum of its entries in list order (found by their index, as the order in
+  // which they came into shared memory is open).
+  auto bias_of = [&](int at) {
+    float sum = 0.f;
+    if (sh.biases <= kHeldBiases) {
+      for (int last = -1;;) {
+        int next = INT32_MAX;
+        for (int k = 0; k < sh.biases; ++k)
+          if (sh.bias_at[k] == at && sh.bias_entry[k] > last) next = min(next, sh.bias_entry[k]);
+        if (next == INT32_MAX) break;
+        sum = last < 0 ? __ldg(bv + next) : __fadd_rn(sum, __ldg(bv + next));
+        last = next;
+      }
+    } else {
+      bool any = false;
+      for (int k = 0; k < a.r.max_bias; ++k)
+        if (__ldg(bt + k) == lo + at) {
+          sum = any ? __fadd_rn(sum, __ldg(bv + k)) : __ldg(bv + k);
+          any = true;
+        }
+    }
+    return sum;
+  };
 
   // ---- from here on a warp is on its own with its window
-  const int w0 = warp * kWindow, left = width - w0;
-  uint16_t* mine = list + w0;
   uint32_t* map = touched + w0 / 32;
+  // its touched tokens: sixteen neighbouring bits a lane, places by a scan
+  uint16_t* list = sh.list + w0;
   int listed = 0;
-#pragma unroll 4
-  for (int k = 0; k < kPerLane; ++k) {
-    const uint32_t m = __ballot_sync(0xffffffffu, cnt[w0 + 32 * k + lane] != 0);
-    if (lane == 0) map[k] = m;
-    if (m >> lane & 1u) mine[listed + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(w0 + 32 * k + lane);
-    listed += __popc(m);
+  {
+    uint32_t bits = (map[lane >> 1] >> (16 * (lane & 1))) & 0xFFFFu;
+    int end = __popc(bits);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += v;
+    }
+    listed = __shfl_sync(0xffffffffu, end, 31);
+    for (int k = end - __popc(bits); bits; bits &= bits - 1) list[k++] = static_cast<uint16_t>(16 * lane + __ffs(bits) - 1);
+    __syncwarp();
   }
-  __syncwarp();
-  const float rep = a.r.repetition ? __ldg(a.r.repetition + b) : 1.f;
-  const float pres = a.r.presence ? __ldg(a.r.presence + b) : 0.f;
-  const float freq = a.r.frequency ? __ldg(a.r.frequency + b) : 0.f;
+  uint32_t here[kMaxNodes / 32];                    // nodes whose token lies in the window
+#pragma unroll
+  for (int k = 0; k < kMaxNodes / 32; ++k) {
+    const int t = 32 * k + lane < n ? tok[32 * k + lane] - lo - w0 : -1;
+    here[k] = __ballot_sync(0xffffffffu, t >= 0 && t < min(left, kWindow));
+  }
   const int row1 = min(n, row0 + a.group), words = left > 0 ? min(kPerLane, (left + 31) / 32) : 0;
 
-  for (int row = row0; row < row1 && left > 0; ++row) {
+  for (int row = row0; row < row1 && left > 0; ++row, src += a.row_stride) {
     const int64_t at = first + row;
-    const T* src = static_cast<const T*>(a.logits) + at * a.row_stride + lo + w0;
     T* dst = a.out ? static_cast<T*>(a.out) + at * a.out_stride + lo + w0 : nullptr;
     float x[kPerLane];
-    L::load(src, lane, left, x);
+    L::unpack(raw, x);
+    if (row + 1 < row1) L::fetch(src + a.row_stride, lane, left, raw);
     const uint32_t* mask = nullptr;
     if (a.r.n_masks > 0) {
       const int mr = __ldg(a.r.allowed_row + at);
@@ -300,88 +417,91 @@ __global__ void __launch_bounds__(kLogitThreads) logits_kernel(const __grid_cons
         mask = a.r.allowed + static_cast<int64_t>(mr) * a.mask_words + (lo + w0) / 32;
       }
     }
-    // ---- this node's path joins the counts, the list and the bitmap
+    // ---- this node's path joins the counts and the list
+    uint32_t on = 0;                                // of the lane's four nodes: in the window
     int more = 0;
-    uint32_t fresh = 0, on = 0;                     // of the lane's four nodes: listed just now; in the window
 #pragma unroll
     for (int k = 0; k < kMaxNodes / 32; ++k) {
-      const int i = 32 * k + lane, t = i < n ? tok[i] - lo - w0 : -1;
-      const bool here = t >= 0 && t < min(left, kWindow) && (path[cur][row][k] >> lane & 1u);
-      if (!__any_sync(0xffffffffu, here)) continue;
-      const bool first_of = here && atomicAdd(&cnt[w0 + t], 1u) == 0;
-      const uint32_t f = __ballot_sync(0xffffffffu, first_of);
-      if (here) on |= 1u << k;
-      if (first_of) {
-        fresh |= 1u << k;
-        mine[listed + more + __popc(f & ((1u << lane) - 1u))] = static_cast<uint16_t>(w0 + t);
-        atomicOr(&map[t >> 5], 1u << (t & 31));
-      }
+      const uint32_t nodes = here[k] & sh.path[row][k];
+      if (nodes == 0) continue;
+      const bool in = nodes >> lane & 1u;
+      const int t = in ? tok[32 * k + lane] - lo - w0 : 0;
+      const bool fresh = in && cnt.add(w0 + t) == 0;
+      const uint32_t f = __ballot_sync(0xffffffffu, fresh);
+      if (in) on |= 1u << k;
+      if (fresh) list[listed + more + __popc(f & ((1u << lane) - 1u))] = static_cast<uint16_t>(t);
       more += __popc(f);
       __syncwarp();
     }
-    // ---- what nothing touches
+    // ---- tokens that the history, the biases or the path touch: each step rounded by itself, as the formulas
+    // are written.  The window goes through shared memory, where a lane takes every 32nd of the list.
+    const int work = listed + more;
+    if (work > 0) {
+      float* stage = sh.stage[warp];
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) stage[L::place(lane, e)] = x[e];
+      __syncwarp();
+#pragma unroll 1
+      for (int j = lane; j < work; j += 32) {
+        const int t = list[j], at_t = L::place_of(t);
+        const uint32_t c = cnt.get(w0 + t), times = c & C::kTimes;
+        float v = stage[at_t];
+        if (c & ~C::kBiased) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+        if (times) v = __fsub_rn(__fsub_rn(v, __fmul_rn(freq, static_cast<float>(times))), pres);
+        if (c & C::kBiased) v = __fadd_rn(v, bias_of(w0 + t));
+        stage[at_t] = v;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < kPerLane; ++e) x[e] = stage[L::place(lane, e)];
+      // the path leaves the counts again
+#pragma unroll
+      for (int k = 0; k < kMaxNodes / 32; ++k)
+        if (on >> k & 1u) cnt.take(tok[32 * k + lane] - lo);
+      __syncwarp();
+    }
     if (mask) {
       const uint32_t allowed = L::bits(mask, lane, words);
 #pragma unroll
       for (int e = 0; e < kPerLane; ++e)
         if (!(allowed >> e & 1u)) x[e] = -INFINITY;
     }
-    // (in place and without a mask these logits stay as they are)
-    if (dst && (mask || static_cast<const void*>(dst) != src)) L::store(dst, lane, left, x);
-    if (listed + more > 0) {
-      const uint32_t skip = L::bits(map, lane, words);
-      if (skip) {
-#pragma unroll
-        for (int e = 0; e < kPerLane; ++e)
-          if (skip >> e & 1u) x[e] = -INFINITY;
-      }
-    }
+    // (in place, a window that nothing changes stays as it is)
+    if (dst && (mask || work > 0 || static_cast<const void*>(dst) != src)) L::store(dst, lane, left, x);
     float m = x[0];
 #pragma unroll
     for (int e = 1; e < kPerLane; ++e) m = fmaxf(m, x[e]);
     if (m != m) m = -INFINITY;                      // nothing but NaN
-    float ref = ref_of(m), s = 0.f;
+    // (the difference first: it is exact where it matters, at any size of the logits)
+    const float ref = ref_of(m);
+    float s;
+    {
+      const uint64_t scale = pair2(kLog2e, kLog2e), off = pair2(-ref, -ref);
+      uint64_t sum = 0;
 #pragma unroll
-    for (int e = 0; e < kPerLane; ++e) s += exp2f((x[e] - ref) * kLog2e);
-    int best = -1;
-    if (m == warp_max(m) && m > -INFINITY) {        // (only a lane that may hold the warp's best looks for it)
-      uint32_t eq = 0;
-#pragma unroll
-      for (int e = 0; e < kPerLane; ++e) eq |= (x[e] == m ? 1u : 0u) << e;
-      best = lo + w0 + L::token(lane, __ffs(eq) - 1);
+      for (int e = 0; e < kPerLane; e += 2) {
+        uint64_t d = pair2(x[e], x[e + 1]);
+        float d0, d1;
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(off));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(scale));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(pair2(exp2_of(d0), exp2_of(d1))));
+      }
+      float s0, s1;
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum));
+      s = s0 + s1;
     }
-    // ---- what the history, the biases or the path touch: each step rounded by itself, as the formulas are written
-    __syncwarp();
-    for (int j = lane; j < listed + more; j += 32) {
-      const int i = mine[j];
-      const uint32_t c = cnt[i], times = c & kTimes;
-      float v = static_cast<float>(src[i - w0]);    // (in place: as it was, or -inf where it is masked)
-      if (c & ~kBiased) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-      if (times) v = __fsub_rn(__fsub_rn(v, __fmul_rn(freq, static_cast<float>(times))), pres);
-      if (c & kBiased) v = __fadd_rn(v, bias[i]);
-      if (mask && !(__ldg(mask + (i - w0) / 32) >> (i & 31) & 1u)) v = -INFINITY;
-      if (dst) dst[i - w0] = static_cast<T>(v);
-      const int id = lo + i;
-      if (v > m || (v == m && v > -INFINITY && (best < 0 || id < best))) best = id;
-      const float m2 = fmaxf(m, v), r2 = ref_of(m2);
-      s = rebase(s, ref, r2) + exp2f((v - r2) * kLog2e);
-      m = m2;
-      ref = r2;
+    int best = -1;
+    if (m == warp_max_redux(m) && m > -INFINITY) {  // (only a lane that may hold the warp's best looks for it)
+      int at_e = 0;
+#pragma unroll
+      for (int e = kPerLane - 1; e > 0; --e)
+        if (x[e] == m) at_e = e;
+      if (x[0] == m) at_e = 0;
+      best = lo + w0 + L::token(lane, at_e);
     }
     warp_merge(m, s, best);
     if (lane == 0) part[row - row0][warp] = Partial{m, s, best};
-    // ---- and the path leaves them again
-    if (more > 0 || __any_sync(0xffffffffu, on != 0)) {
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < kMaxNodes / 32; ++k) {
-        if (!(on >> k & 1u)) continue;
-        const int t = tok[32 * k + lane] - lo - w0;
-        atomicSub(&cnt[w0 + t], 1u);
-        if (fresh >> k & 1u) atomicAnd(&map[t >> 5], ~(1u << (t & 31)));
-      }
-      __syncwarp();
-    }
   }
   __syncthreads();
   // ---- the windows of each node, in order
@@ -590,12 +710,14 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
   const int64_t run = 16 / static_cast<int64_t>(es);
   const bool vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && row_stride % run == 0 &&
                    (!out || (reinterpret_cast<uintptr_t>(out) % 16 == 0 && out_stride % run == 0));
-  if (dtype == LLA_BF16) {
-    if (vec) logits_kernel<__nv_bfloat16, true><<<grid, kLogitThreads, 0, s>>>(a);
-    else logits_kernel<__nv_bfloat16, false><<<grid, kLogitThreads, 0, s>>>(a);
+  if (r.max_history + kMaxNodes <= kMaxTimes16) {
+    auto kern = dtype == LLA_BF16 ? (vec ? logits_kernel<__nv_bfloat16, true, 16> : logits_kernel<__nv_bfloat16, false, 16>)
+                                  : (vec ? logits_kernel<float, true, 16> : logits_kernel<float, false, 16>);
+    kern<<<grid, kLogitThreads, 0, s>>>(a);
   } else {
-    if (vec) logits_kernel<float, true><<<grid, kLogitThreads, 0, s>>>(a);
-    else logits_kernel<float, false><<<grid, kLogitThreads, 0, s>>>(a);
+    auto kern = dtype == LLA_BF16 ? (vec ? logits_kernel<__nv_bfloat16, true, 32> : logits_kernel<__nv_bfloat16, false, 32>)
+                                  : (vec ? logits_kernel<float, true, 32> : logits_kernel<float, false, 32>);
+    kern<<<grid, kLogitThreads, 0, s>>>(a);
   }
   if (cudaGetLastError() != cudaSuccess) return LLA_ERR_CUDA;
   if (!best && !lse) return LLA_OK;

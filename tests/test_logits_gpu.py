@@ -154,6 +154,21 @@ def test_in_place_and_strides(dtype, stride):
     assert (out[:, 4999:] == 55.0).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_histories_and_many_biases(dtype):
+    """Counts past 14 bits, and more biases of one stretch of the vocabulary than shared memory holds."""
+    c = make([3, 2], 6000, dtype, hist=20000, max_bias=400)
+    c["history"][0, :17000] = 5                       # one token 17,000 times
+    c["prompt_len"][0] = 100
+    c["bias_token"][0] = torch.arange(400) % 390      # some of them twice, all below 4096
+    c["freq"] *= 1e-3
+    x, best, lse = expected(c)
+    out = torch.full_like(c["logits"], 55.0)
+    ws = run(c, out)
+    assert lla.device_status(ws) == lla.LLA_OK
+    compare(c, x, best, lse, out)
+
+
 def test_parts_on_their_own():
     """No rule at all, one rule at a time, and outputs one at a time."""
     c = make([6, 2], 3000, "f32", hist=20, max_bias=0, masks=0)
