@@ -342,9 +342,6 @@ struct View {
   int64_t num_pages;
 };
 
-// Pages that the tensor-core kernel's copies take (0: dense).
-bool tensor_pages(int page_size) { return page_size == 0 || (page_size >= 8 && tile_kernel_page_size(page_size)); }
-
 // Shapes of the tensor-core kernel: those whose operands fit for any number of nodes.
 bool tensor_path(const lla_dims* d) {
   TreePlan p;
@@ -409,8 +406,9 @@ bool tree_maps(const TreeArgs& a, TreeMaps* m) {
   // rows of one (sequence or page, head): L_max or page_size of them
   const uint64_t rows = static_cast<uint64_t>(a.block_table ? a.page_size : a.L_max);
   const uint64_t outer = static_cast<uint64_t>(a.block_table ? a.num_pages : a.B) * a.H;
-  const uint32_t box_rows = a.block_table && a.page_size < kTile ? a.page_size : kTile;
+  const uint32_t box_rows = a.block_table ? a.piece : kTile;
   const uint64_t rk = a.r_k, rv = a.r_v;
+  const bool copies = !a.block_table || a.piece >= 8;       // else row by row, without a map
   auto latents = [&](CUtensorMap* map, const void* base, uint64_t r, uint32_t width) {
     const uint64_t d[3] = {r, rows, outer}, st[2] = {2 * r, 2 * r * rows};
     const uint32_t box[3] = {width, box_rows, 1};
@@ -419,13 +417,14 @@ bool tree_maps(const TreeArgs& a, TreeMaps* m) {
   for (int c = 0; c < a.plan.kplan.n; ++c) {
     const uint32_t width = a.plan.kplan.width[c];
     const int i = chunk_map_index(width);
-    if (!latents(&m->k[i], a.cache_k, rk, width)) return false;
+    if (copies && !latents(&m->k[i], a.cache_k, rk, width)) return false;
     // row pair_index of member 0 or 1: f and f + 64, or 2 f and 2 f + 1
     const uint64_t step = a.rope_style == 0 ? 1 : 2, member = a.rope_style == 0 ? 64 : 1;
     const uint64_t d[4] = {rk, 64, 2, static_cast<uint64_t>(a.H)}, st[3] = {2 * rk * step, 2 * rk * member, 2 * rk * kHeadDim};
     const uint32_t box[4] = {width, 64, 2, 1};
     if (!map_4d(&m->w[i], a.w_up_k, 4, d, st, box)) return false;
   }
+  if (!copies) return true;
   if (rv % 32 == 0) {
     const uint64_t d[4] = {32, rows, rv / 32, outer}, st[3] = {2 * rv, 64, 2 * rv * rows};
     const uint32_t box[4] = {32, box_rows, static_cast<uint32_t>(rv / 32), 1};
@@ -470,8 +469,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
   TreeArgs a{};
-  const bool tensor = tensor_path(dims) && tensor_pages(cache.page_size) &&
-                      make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes), &a.plan);
+  const bool tensor = tensor_path(dims) && make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes), &a.plan);
   const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms, tensor);
   if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   a.B = tree->B;
@@ -500,6 +498,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   a.page_size = cache.page_size;
   a.max_pages = cache.max_pages;
   a.num_pages = cache.num_pages;
+  a.piece = std::min(kTile, cache.page_size & -cache.page_size);
   a.w_up_k = static_cast<const uint8_t*>(w_up_k) + static_cast<size_t>(loop_t) * width * dims->r_k * es;
   a.w_up_v = static_cast<const uint8_t*>(w_up_v) + static_cast<size_t>(loop_t) * width * dims->r_v * es;
   a.mu_k = mu_k + static_cast<size_t>(loop_t) * kHeadDim;
@@ -542,16 +541,14 @@ extern "C" {
 
 const char* lla_tree_kernel(const lla_dims* dims, int page_size) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || page_size < 0) return nullptr;
-  return tensor_path(dims) && tensor_pages(page_size) ? "tensor" : "plain";
+  return tensor_path(dims) ? "tensor" : "plain";
 }
 
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max) {
   if (checked_dims(dims) != LLA_OK || dims->variant != LLA_PER_HEAD || B < 0 || max_nodes < 1 ||
       max_nodes > kTreeMaxNodes || L_max < 0)
     return 0;
-  // either kernel: which one a call takes depends on its page size too
-  const int sms = std::max(1, device_sm_count());
-  return std::max(tree_ws(dims, B, max_nodes, L_max, sms, false).total, tensor_path(dims) ? tree_ws(dims, B, max_nodes, L_max, sms, true).total : 0);
+  return tree_ws(dims, B, max_nodes, L_max, std::max(1, device_sm_count()), tensor_path(dims)).total;
 }
 
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,

@@ -43,6 +43,8 @@ struct TreeArgs {
   const void* cache_v;
   const int32_t* block_table;        // [B][max_pages], or nullptr (dense)
   int page_size, max_pages;
+  int piece;                         // tokens of a tile that lie in one page wherever it starts: the largest power
+                                     // of two that divides page_size, at most 128
   int64_t num_pages;
   const void* w_up_k;                // loop-t slice [H][128][r_k]
   const void* w_up_v;                // loop-t slice [H][128][r_v]

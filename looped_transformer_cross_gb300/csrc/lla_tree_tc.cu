@@ -161,13 +161,13 @@ struct Chunk {
   int off, start, row, map;          // byte offset in a tile, first column, bytes of a row, tensor map
 };
 
-// Where the latents of a tile lie: the lane's page (pages of 8..64 tokens: lane mod pages of a tile) or
-// the sequence, as the maps' outer coordinate, and the first row in it.
+// Where the latents of a tile lie: the sequence or the tile's page or, with pieces, the lane's piece's page, as the
+// maps' outer coordinate, and the first row in it.
 struct Place {
   int y, z;
 };
 template <int kPage>
-__device__ __forceinline__ Place place_of(const TreeArgs& a, const Walk& w, int my_page) {
+__device__ __forceinline__ Place place_of(const TreeArgs& a, const Walk& w, int my_piece) {
   Place p{w.t * kTile, w.b * a.H + w.h};
   if constexpr (kPage == 1) {
     const int lp = p.y / a.page_size;
@@ -175,28 +175,50 @@ __device__ __forceinline__ Place place_of(const TreeArgs& a, const Walk& w, int 
     p.y -= lp * a.page_size;
   }
   if constexpr (kPage == 2) {
-    const int lp = w.t * (kTile / a.page_size) + my_page;
-    p.z = lp * a.page_size < w.L ? page_at(a, w.b, lp) * a.H + w.h : 0;
-    p.y = 0;
+    p.y += my_piece * a.piece;
+    const int lp = p.y < w.L ? p.y / a.page_size : 0;
+    p.z = p.y < w.L ? page_at(a, w.b, lp) * a.H + w.h : 0;
+    p.y -= lp * a.page_size;
   }
   return p;
 }
 
 // One latent tile into dst, completing on fb (the whole warp calls it).  A lane issues the boxes of one
-// page (pages of 8..64 tokens, those that hold tokens) or of the tile, every `every`-th chunk from its first on.
+// piece (those that hold tokens) or of the tile, every `every`-th chunk from its first on.
 template <int kPage>
 __device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32_t dst, uint32_t fb, const Chunk* chunks, int n, int bytes,
-                                          const CUtensorMap* maps, int page_size, int my_page, int first, int every) {
+                                          const CUtensorMap* maps, int piece, int my_piece, int first, int every) {
   int np = 1;
-  if constexpr (kPage == 2) np = (min(kTile, w.L - w.t * kTile) + page_size - 1) / page_size;
-  if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(fb, kPage == 2 ? bytes / kTile * page_size * np : bytes);
+  if constexpr (kPage == 2) np = (min(kTile, w.L - w.t * kTile) + piece - 1) / piece;
+  if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(fb, kPage == 2 ? bytes / kTile * piece * np : bytes);
   __syncwarp();
-  if (my_page < np) {
+  if (my_piece < np) {
     for (int c = first; c < n; c += every) {
       const Chunk k = chunks[c];
-      tma_load_3d(dst + k.off + (kPage == 2 ? my_page * page_size * k.row : 0), maps + k.map, fb, k.start, at.y, at.z);
+      tma_load_3d(dst + k.off + (kPage == 2 ? my_piece * piece * k.row : 0), maps + k.map, fb, k.start, at.y, at.z);
     }
   }
+}
+
+// Rows of one latent (width r) of a tile, token by token through the block table, into dst: 16 bytes a lane
+// and step, to where the tile's chunks (n of them) have them; they complete on fb, on which every lane arrives.
+// `rows` holds the pool row of the tile's tokens lane, lane + 32, ..; tokens past the sequence's end are left out.
+__device__ __forceinline__ void gather_tile(const void* pool, int r, const int64_t (&rows)[4], int valid, uint8_t* dst, uint32_t fb,
+                                            const Chunk* chunks, int n) {
+  const int lane = threadIdx.x & 31, g = min(lane, (r >> 3) - 1);             // (a row is 32 pieces of 16 bytes at most)
+  int c = 0;
+  while (c + 1 < n && 8 * g >= chunks[c + 1].start) ++c;
+  const Chunk k = chunks[c];
+  const uint32_t to = smem_u32(dst + k.off), col = (8 * g - k.start) * 2;
+  const uint8_t* from = static_cast<const uint8_t*>(pool) + 16 * g;
+#pragma unroll 4
+  for (int t = 0; t < valid; ++t) {
+    const int64_t q = t < 32 ? rows[0] : t < 64 ? rows[1] : t < 96 ? rows[2] : rows[3];
+    const uint8_t* src = from + __shfl_sync(0xffffffffu, q, t & 31) * (2 * r);
+    const uint32_t o = swizzle_offset(t * k.row + col, k.row);
+    if (lane == g) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + o), "l"(src) : "memory");
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(fb) : "memory");
 }
 
 // ---------------------------------------------------------------- preparation
@@ -392,8 +414,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
 
 // ---------------------------------------------------------------- the cached tokens
 
-// kPage: 0 dense, 1 pages of a multiple of 128 tokens, 2 pages of 8..64 tokens.  kRows: nodes that S
-// and D have room for (16, 32 or 64).
+// kPage: 0 dense, 1 pages of a multiple of 128 tokens, 2 tiles in pieces of 8..64 tokens, each within a page, 3
+// any page size, row by row.  kRows: nodes that S and D have room for (16, 32 or 64).
 template <int kPage, int kRows>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
@@ -416,8 +438,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     misc->over[0] = misc->over[1] = 0;
     for (int s = 0; s < 4; ++s) mbar_init(bar(misc->bfull[s]), 1);
     for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(bar(misc->kfull[s]), 1); mbar_init(bar(misc->kempty[s]), 1);
-      mbar_init(bar(misc->vfull[s]), 1); mbar_init(bar(misc->vempty[s]), 1);
+      mbar_init(bar(misc->kfull[s]), kPage == 3 ? 32 : 1); mbar_init(bar(misc->kempty[s]), 1);
+      mbar_init(bar(misc->vfull[s]), kPage == 3 ? 32 : 1); mbar_init(bar(misc->vempty[s]), 1);
     }
     mbar_init(bar(misc->wfull), 1); mbar_init(bar(misc->wfree), 1);
     mbar_init(bar(misc->qfull), 1); mbar_init(bar(misc->qfree), 1);
@@ -480,8 +502,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== K and V tiles
     // V tile i - 1 after K tile i: it is needed only once tile i - 1 has weights.  Page ids are read one
     // tile ahead.  (A copy costs this warp some hundred cycles: the fewer the better.)
-    const int page_size = a.page_size, pages = kPage == 2 ? kTile / page_size : 1;
-    const int my_page = lane % pages, first = lane / pages, every = 32 / pages;
+    const int piece = a.piece, pieces = kPage == 2 ? kTile / piece : 1;
+    const int my_piece = lane % pieces, first = lane / pieces, every = 32 / pieces;
     const Chunk* kc = reinterpret_cast<const Chunk*>(sm + P.chunks);
     const Chunk* vc = kc + 8;
     const int SK = P.SK, SV = P.SV, nk = P.kplan.n, nv = P.vplan.n, k_bytes = P.kplan.bytes, v_bytes = P.vplan.bytes;
@@ -492,29 +514,47 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     Ring kr, vr;
     int issued_k = 0, issued_v = 0;
     Place at = {}, at_v = {};
-    if (count > 0) at = place_of<kPage>(a, w, my_page);
+    if (count > 0) at = place_of<kPage>(a, w, my_piece);
+    // (row by row: the pool rows of this tile's tokens and of the one before it)
+    int64_t rows[4] = {}, rows_v[4] = {};
+    auto find_rows = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = w.t * kTile + 32 * k + lane, lp = j / a.page_size;
+        rows[k] = j < w.L ? (static_cast<int64_t>(page_at(a, w.b, lp)) * a.H + w.h) * a.page_size + (j - lp * a.page_size) : 0;
+      }
+    };
     for (int i = 0; i <= count && count > 0; ++i) {
       const Walk wt = w;
       Place at_k = at;
       if (i < count) {
         if (!wait(misc->kempty[kr.slot], kr.phase ^ 1u)) break;
-        load_tile<kPage>(w, at, k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, page_size, my_page,
-                         first, every);
+        if constexpr (kPage == 3) {
+          find_rows();
+          gather_tile(a.cache_k, a.r_k, rows, w.L - w.t * kTile < kTile ? w.L - w.t * kTile : kTile, sm + P.k_ring + kr.slot * k_stage,
+                      bar(misc->kfull[kr.slot]), kc, nk);
+        } else {
+          load_tile<kPage>(w, at, k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, piece, my_piece,
+                           first, every);
+        }
         issued_k = i + 1;
         kr.next(SK);
         walk_next(w, a);
-        if (i + 1 < count) at = place_of<kPage>(a, w, my_page);
+        if (i + 1 < count) at = place_of<kPage>(a, w, my_piece);
       }
       if (i > 0) {
         if (!wait(misc->vempty[vr.slot], vr.phase ^ 1u)) break;
-        if (v_whole) {                                // all of a tile's, or a page's, columns in one copy
-          const int np = kPage == 2 ? (min(kTile, wv.L - wv.t * kTile) + page_size - 1) / page_size : 1;
-          const uint32_t vb = bar(misc->vfull[vr.slot]), region = kPage == 2 ? page_size * nv * 64 : v_bytes;
+        if constexpr (kPage == 3) {
+          gather_tile(a.cache_v, a.r_v, rows_v, min(kTile, wv.L - wv.t * kTile), sm + P.v_ring + vr.slot * v_stage,
+                      bar(misc->vfull[vr.slot]), vc, nv);
+        } else if (v_whole) {                         // all of a tile's, or a piece's, columns in one copy
+          const int np = kPage == 2 ? (min(kTile, wv.L - wv.t * kTile) + piece - 1) / piece : 1;
+          const uint32_t vb = bar(misc->vfull[vr.slot]), region = kPage == 2 ? piece * nv * 64 : v_bytes;
           if (lane == 0) mbar_arrive_expect_tx(vb, region * np);
           __syncwarp();
           if (lane < np) tma_load_4d(v_ring + vr.slot * v_stage + lane * region, &maps.v4, vb, 0, at_v.y, 0, at_v.z);
         } else {
-          load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, page_size, my_page,
+          load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, piece, my_piece,
                            first, every);
         }
         issued_v = i;
@@ -522,6 +562,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       wv = wt;
       at_v = at_k;
+      if constexpr (kPage == 3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) rows_v[k] = rows[k];
+      }
     }
     if (lane == 0) {
       for (int i = max(0, issued_k - P.SK); i < issued_k; ++i) landed(misc->kfull[i % P.SK], i / P.SK);
@@ -555,6 +599,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!wait(misc->wfull, unit)) break;
       }
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
+      if constexpr (kPage == 3) fence_proxy_async_smem();       // (plain copies, read by the products)
       if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
       // (chunks of 64 columns, then one of 32, then one of 16)
@@ -635,10 +680,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // (two blocks of 128 rows of r_v; rows past r_v read whatever follows the tile in shared memory and
     // are not looked at)
     const uint32_t idesc = umma_idesc_bf16(128, kRows, true, true);
-    // V: chunks of 32 columns, their 128 token rows of 64 bytes one after the other; with pages of 8..64
-    // tokens and one copy per page, page by page, each [chunk][page_size rows]
-    const bool by_page = kPage == 2 && a.v_whole;
-    const int nv = P.vplan.n, rows = by_page ? a.page_size : kTile;          // rows of a chunk that lie together
+    // V: chunks of 32 columns, their 128 token rows of 64 bytes one after the other; with one copy per piece of
+    // 8..64 tokens, piece by piece, each [chunk][piece rows]
+    const bool by_piece = kPage == 2 && a.v_whole;
+    const int nv = P.vplan.n, rows = by_piece ? a.piece : kTile;             // rows of a chunk that lie together
     const uint32_t region = rows * nv * 64;
     const uint64_t d_v = umma_desc(sbase + P.v_ring, rows * 64, rows >= 16 ? 512 : region, kSw64);
     const uint32_t block_step = 4 * rows * 64 / 16;
@@ -649,6 +694,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     Ring vr;
     for (int j = 0; j < count; ++j, vr.next(SV)) {
       if (!wait(misc->vfull[vr.slot], vr.phase)) break;
+      if constexpr (kPage == 3) fence_proxy_async_smem();
       // rows past the sequence's end: whole steps of 16 tokens are left out, the rest of a partial step
       // is zeroed (it may hold anything; its weights are 0 and 0 * x stays 0)
       const int valid = min(kTile, w.L - w.t * kTile);
@@ -1221,7 +1267,8 @@ cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStre
   if (e != cudaSuccess) return e;
   const cudaError_t t = !a.block_table              ? launch_tiles<0>(a, maps, s)
                         : a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s)
-                                                   : launch_tiles<2>(a, maps, s);
+                        : a.piece >= 8             ? launch_tiles<2>(a, maps, s)
+                                                   : launch_tiles<3>(a, maps, s);
   if (t != cudaSuccess) return t;
   // (the most any shape takes, at every call)
   const cudaError_t c = cudaFuncSetAttribute(tree_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -67,8 +67,7 @@ def test_kernel_names(L):
     assert lla.tree_kernel(lla.dims(4, 2, 96, 160, dtype=lla.LLA_F32)) == "plain"
     assert lla.tree_kernel(lla.dims(4, 2, 96, 160, variant=lla.LLA_2D)) is None
     bf = lla.dims(4, 2, 96, 160)
-    assert all(lla.tree_kernel(bf, p) == "tensor" for p in (0, 8, 16, 32, 64, 128, 256))
-    assert all(lla.tree_kernel(bf, p) == "plain" for p in (1, 4, 24, 100, 192))
+    assert all(lla.tree_kernel(bf, p) == "tensor" for p in (0, 1, 4, 8, 16, 24, 32, 64, 100, 128, 192, 256))
     assert lla.tree_kernel(lla.dims(4, 2, 256, 256)) == "plain" and lla.tree_kernel(lla.dims(4, 2, 16, 256)) == "tensor"
     assert lla.tree_kernel(lla.dims(4, 2, 100, 160)) is None and lla.tree_kernel(lla.dims(4, 2, 96, 160), -1) is None
 

@@ -153,6 +153,12 @@ CASES = [
     ([301, 64], [5, 6], 2, 96, 160, 100),
     ([301, 600], [17, 6], 2, 96, 160, 128),
     ([301, 600], [17, 6], 2, 80, 48, 256),
+    ([500, 131], [9, 40], 2, 96, 160, 48),
+    ([500, 131], [9, 40], 2, 80, 112, 40),
+    ([333, 260], [70, 3], 3, 64, 80, 192),
+    ([333, 260], [70, 3], 3, 48, 128, 6),
+    ([700, 20], [5, 31], 2, 192, 192, 2),
+    ([513, 256], [100, 64], 2, 16, 240, 20),
     ([301], [40], 2, 112, 112, 0),
     ([140], [6], 2, 256, 256, 0),
     ([140], [6], 1, 240, 16, 64),
