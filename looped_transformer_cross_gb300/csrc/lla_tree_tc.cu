@@ -200,23 +200,32 @@ __device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32
   }
 }
 
-// Rows of one latent (width r) of a tile, token by token through the block table, into dst: 16 bytes a lane
-// and step, to where the tile's chunks (n of them) have them; they complete on fb, on which every lane arrives.
-// `rows` holds the pool row of the tile's tokens lane, lane + 32, ..; tokens past the sequence's end are left out.
+// Rows of one latent (width r) of a tile through the block table, into dst: 16 bytes a lane and step, as many
+// rows at a time as a warp covers, to where the tile's chunks (n of them) have them; they complete on fb, on
+// which every lane arrives.  `rows` holds the pool row of the tile's tokens lane, lane + 32, ..; tokens past the
+// sequence's end are left out.
 __device__ __forceinline__ void gather_tile(const void* pool, int r, const int64_t (&rows)[4], int valid, uint8_t* dst, uint32_t fb,
                                             const Chunk* chunks, int n) {
-  const int lane = threadIdx.x & 31, g = min(lane, (r >> 3) - 1);             // (a row is 32 pieces of 16 bytes at most)
+  const int lane = threadIdx.x & 31, gran = r >> 3, at_once = 32 / gran;      // (a row is 32 pieces of 16 bytes at most)
+  const int sub = lane / gran, g = lane - sub * gran;
   int c = 0;
   while (c + 1 < n && 8 * g >= chunks[c + 1].start) ++c;
   const Chunk k = chunks[c];
-  const uint32_t to = smem_u32(dst + k.off), col = (8 * g - k.start) * 2;
+  const uint32_t to = smem_u32(dst + k.off) + sub * k.row, col = (8 * g - k.start) * 2;
+  const uint32_t mask = k.row == 128 ? 7u : k.row == 64 ? 3u : 1u, shift = k.row == 128 ? 0u : k.row == 64 ? 1u : 2u;
   const uint8_t* from = static_cast<const uint8_t*>(pool) + 16 * g;
-#pragma unroll 4
-  for (int t = 0; t < valid; ++t) {
-    const int64_t q = t < 32 ? rows[0] : t < 64 ? rows[1] : t < 96 ? rows[2] : rows[3];
-    const uint8_t* src = from + __shfl_sync(0xffffffffu, q, t & 31) * (2 * r);
-    const uint32_t o = swizzle_offset(t * k.row + col, k.row);
-    if (lane == g) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + o), "l"(src) : "memory");
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int64_t mine = rows[b] * (2 * r);
+    const int m = min(32, valid - 32 * b);
+#pragma unroll 2
+    for (int t = 0; t < m; t += at_once) {
+      const uint8_t* src = from + __shfl_sync(0xffffffffu, mine, (t + sub) & 31);
+      const uint32_t row = 32 * b + t + sub;        // (its place in the swizzle: 16-byte pieces exchanged by rows)
+      if (sub < at_once && t + sub < m)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (32 * b + t) * k.row + (col ^ (((row >> shift) & mask) << 4))), "l"(src)
+                     : "memory");
+    }
   }
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(fb) : "memory");
 }
