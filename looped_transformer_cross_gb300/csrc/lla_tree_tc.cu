@@ -15,8 +15,8 @@
 // fp32 sums have the range); the softmax warps vote on that for every tile, and a tile that breaks it
 // moves the references and rescales D.
 //
-// Roles: warp 0 copies K and V tiles, warp 1 issues U (and copies W), warp 2 issues S
-// (and copies Q^ and RoPE rows), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
+// Roles: warp 0 copies K and V tiles, warp 1 issues U (and copies W and RoPE rows), warp 2 issues S
+// (and copies Q^), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
 // each, one token per lane), warps 12..15 do the softmax, one token per lane.  cos/sin of a token's
 // angle are the angle sum of the tile's base row (shared memory) and the lane's own row (registers).
 // The roles' loops are kept short on purpose: with bodies unrolled all the way, instruction fetch took
@@ -42,9 +42,8 @@ constexpr int kKhatCol = 256;                       // TMEM columns: U 0..255 (t
 
 struct alignas(16) TreeMisc {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages];
-  uint64_t bfull[4];                                // a tile's base row of the RoPE table
   uint64_t wfull, wfree, qfull, qfree;              // the unit's W and bias; its queries
-  uint64_t ufull[2], ufree[2];                      // U computed; read by the rotating warps
+  uint64_t ufull[2], ufree[2];                      // U computed and the tile's base RoPE row written; both read
   uint64_t rfull[2];                                // K^ written
   uint64_t sfull[2], sfree[2];                      // S computed (and K^ read); S read
   uint64_t pfull[2], vdone[2];                      // P written; D += C_v^T P done
@@ -164,29 +163,31 @@ struct Chunk {
 // Where the latents of a tile lie: the sequence or the tile's page or, with pieces, the lane's piece's page, as the
 // maps' outer coordinate, and the first row in it.
 struct Place {
-  int y, z;
+  int y, page;                       // (the table's entry as it was read: what depends on it waits for the load)
 };
 template <int kPage>
 __device__ __forceinline__ Place place_of(const TreeArgs& a, const Walk& w, int my_piece) {
-  Place p{w.t * kTile, w.b * a.H + w.h};
-  if constexpr (kPage == 1) {
-    const int lp = p.y / a.page_size;
-    p.z = page_at(a, w.b, lp) * a.H + w.h;
-    p.y -= lp * a.page_size;
-  }
-  if constexpr (kPage == 2) {
-    p.y += my_piece * a.piece;
-    const int lp = p.y < w.L ? p.y / a.page_size : 0;
-    p.z = p.y < w.L ? page_at(a, w.b, lp) * a.H + w.h : 0;
-    p.y -= lp * a.page_size;
+  Place p{w.t * kTile, 0};
+  if constexpr (kPage == 1 || kPage == 2) {
+    if (kPage == 2) p.y += my_piece * a.piece;
+    if (kPage == 1 || p.y < w.L) {
+      const int lp = p.y / a.page_size;
+      p.page = __ldg(a.block_table + static_cast<int64_t>(w.b) * a.max_pages + lp);
+      p.y -= lp * a.page_size;
+    }
   }
   return p;
+}
+template <int kPage>
+__device__ __forceinline__ int outer_of(const TreeArgs& a, const Walk& w, const Place& p) {
+  if constexpr (kPage == 1 || kPage == 2) return min(max(p.page, 0), static_cast<int>(a.num_pages) - 1) * a.H + w.h;
+  return w.b * a.H + w.h;
 }
 
 // One latent tile into dst, completing on fb (the whole warp calls it).  A lane issues the boxes of one
 // piece (those that hold tokens) or of the tile, every `every`-th chunk from its first on.
 template <int kPage>
-__device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32_t dst, uint32_t fb, const Chunk* chunks, int n, int bytes,
+__device__ __forceinline__ void load_tile(const Walk& w, int y, int z, uint32_t dst, uint32_t fb, const Chunk* chunks, int n, int bytes,
                                           const CUtensorMap* maps, int piece, int my_piece, int first, int every) {
   int np = 1;
   if constexpr (kPage == 2) np = (min(kTile, w.L - w.t * kTile) + piece - 1) / piece;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void load_tile(const Walk& w, const Place& at, uint32
   if (my_piece < np) {
     for (int c = first; c < n; c += every) {
       const Chunk k = chunks[c];
-      tma_load_3d(dst + k.off + (kPage == 2 ? my_piece * piece * k.row : 0), maps + k.map, fb, k.start, at.y, at.z);
+      tma_load_3d(dst + k.off + (kPage == 2 ? my_piece * piece * k.row : 0), maps + k.map, fb, k.start, y, z);
     }
   }
 }
@@ -445,7 +446,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   if (tid == 0) {
     misc->abort = 0;
     misc->over[0] = misc->over[1] = 0;
-    for (int s = 0; s < 4; ++s) mbar_init(bar(misc->bfull[s]), 1);
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(bar(misc->kfull[s]), kPage == 3 ? 32 : 1); mbar_init(bar(misc->kempty[s]), 1);
       mbar_init(bar(misc->vfull[s]), kPage == 3 ? 32 : 1); mbar_init(bar(misc->vempty[s]), 1);
@@ -453,7 +453,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     mbar_init(bar(misc->wfull), 1); mbar_init(bar(misc->wfree), 1);
     mbar_init(bar(misc->qfull), 1); mbar_init(bar(misc->qfree), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(misc->ufull[s]), 1); mbar_init(bar(misc->ufree[s]), kRotWarps);
+      mbar_init(bar(misc->ufull[s]), 2); mbar_init(bar(misc->ufree[s]), kRotWarps);
       mbar_init(bar(misc->rfull[s]), kRotWarps);
       mbar_init(bar(misc->sfull[s]), 1); mbar_init(bar(misc->sfree[s]), 4);
       mbar_init(bar(misc->pfull[s]), 4); mbar_init(bar(misc->vdone[s]), 1);
@@ -543,7 +543,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           gather_tile(a.cache_k, a.r_k, rows, w.L - w.t * kTile < kTile ? w.L - w.t * kTile : kTile, sm + P.k_ring + kr.slot * k_stage,
                       bar(misc->kfull[kr.slot]), kc, nk);
         } else {
-          load_tile<kPage>(w, at, k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, piece, my_piece,
+          load_tile<kPage>(w, at.y, outer_of<kPage>(a, w, at), k_ring + kr.slot * k_stage, bar(misc->kfull[kr.slot]), kc, nk, k_bytes, maps.k, piece, my_piece,
                            first, every);
         }
         issued_k = i + 1;
@@ -561,9 +561,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           const uint32_t vb = bar(misc->vfull[vr.slot]), region = kPage == 2 ? piece * nv * 64 : v_bytes;
           if (lane == 0) mbar_arrive_expect_tx(vb, region * np);
           __syncwarp();
-          if (lane < np) tma_load_4d(v_ring + vr.slot * v_stage + lane * region, &maps.v4, vb, 0, at_v.y, 0, at_v.z);
+          if (lane < np) tma_load_4d(v_ring + vr.slot * v_stage + lane * region, &maps.v4, vb, 0, at_v.y, 0, outer_of<kPage>(a, wv, at_v));
         } else {
-          load_tile<kPage>(wv, at_v, v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, piece, my_piece,
+          load_tile<kPage>(wv, at_v.y, outer_of<kPage>(a, wv, at_v), v_ring + vr.slot * v_stage, bar(misc->vfull[vr.slot]), vc, nv, v_bytes, &maps.v, piece, my_piece,
                            first, every);
         }
         issued_v = i;
@@ -593,6 +593,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const int SK = P.SK;
     Ring kr;
     int unit = -1;
+    // the tile's base row of the RoPE table too: a lane takes four cosines or sines, read one tile ahead
+    const float* table = lane < 16 ? a.rope_cos + 4 * lane : a.rope_sin + 4 * (lane - 16);
+    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto fetch = [&]() { ahead = __ldg(reinterpret_cast<const float4*>(table + static_cast<int64_t>(w.t) * kTile * 64)); };
+    if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
@@ -609,8 +614,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
       if constexpr (kPage == 3) fence_proxy_async_smem();       // (plain copies, read by the products)
-      if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;
+      if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;      // (and the row's place with U's)
+      // where K^ has two buffers, S(i - 2) has read the one that U(i) becomes: one wait here instead of one for
+      // each rotating warp
+      if (kBuf == 2 && i >= 2 && !wait(misc->sfull[i & 1], (i - 2) >> 1)) break;
+      reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = ahead;
       tc_fence_after();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(misc->ufull[i & 1]));
       // (chunks of 64 columns, then one of 32, then one of 16)
       const uint32_t d = tmem + (i & 1) * 128, so = kr.slot * kst;
       umma_bf16_warp(d, d_ones, d_mu, idesc, 0);
@@ -630,6 +641,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
       kr.next(SK);
       walk_next(w, a);
+      if (i + 1 < count) fetch();
     }
     products_done(misc->done[0]);
     landed(misc->wfull, unit);
@@ -638,28 +650,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint32_t idesc = umma_idesc_bf16(128, kRows, false, false);
     const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128);
     int unit = -1;
-    // The tiles' base rows of the RoPE table too: a lane takes four cosines or sines, read three tiles
-    // ahead and stored two ahead, to slot i mod 4 (K^(i - 1), and with it every reader of the slot's last
-    // row, is done before tile i + 2's is stored).
-    Walk wr = w;
-    const float* table = lane < 16 ? a.rope_cos + 4 * lane : a.rope_sin + 4 * (lane - 16);
-    float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto fetch = [&]() { ahead = __ldg(reinterpret_cast<const float4*>(table + static_cast<int64_t>(wr.t) * kTile * 64)); };
-    auto store = [&](int i) {
-      reinterpret_cast<float4*>(sm + P.base + (i & 3) * 512)[lane] = ahead;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(misc->bfull[i & 3]));
-      walk_next(wr, a);
-      if (i + 1 < count) fetch();
-    };
-    if (count > 0) {
-      fetch();
-      store(0);
-    }
-    if (count > 1) store(1);
     for (int i = 0; i < count; ++i) {
       const int sb = i % kBuf;
-      if (i + 2 < count) store(i + 2);
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->qfree, unit)) break;
         ++unit;
@@ -673,6 +665,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       if (!wait(misc->rfull[sb], i / kBuf)) break;
       if (i >= kBuf && !wait(misc->sfree[sb], (i - kBuf) / kBuf)) break;
+      // the weights of tile i - 2 have been read: those of S(i) take their place (one wait here instead of one for
+      // each softmax warp)
+      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int k = 0; k < 8; ++k)
@@ -753,10 +748,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     for (int i = 0; i < count; ++i) {
       const int kb = i % kBuf;
       const uint32_t t_u = lanes + (i & 1) * 128 + f0, t_k = lanes + kKhatCol + kb * 64 + f0 / 2;
-      const float* base = rows + (i & 3) * 128;       // cos, then sin
-      if (!wait(misc->bfull[i & 3], i >> 2)) break;
+      const float* base = rows + (i & 1) * 128;       // cos, then sin
       if (!wait(misc->ufull[i & 1], i >> 1)) break;
-      if (i >= kBuf && !wait(misc->sfull[kb], (i - kBuf) / kBuf)) break;   // the buffer's last K^ has been read
+      if (kBuf == 1 && i >= 1 && !wait(misc->sfull[0], i - 1)) break;      // the last K^ has been read
       tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -885,8 +879,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (i == count || !wait(misc->sfull[sb], i / kBuf)) break;
       tc_fence_after();
       const bool live = w.t * kTile + row < w.L, partial = (w.t + 1) * kTile > w.L;
-      // the buffer's last weights have been read
-      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
       if (fresh) {
         if (!move(t_s, live, true)) break;
@@ -1235,7 +1227,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->v_stage = al(p->vplan.bytes);
   // queries, W, two 4 KB bias operands, two buffers of weights, references, barriers, alignment
   const int refs = 16 * rows * 4;
-  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 2048 + 256 + 768 + 1024;
+  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 1024 + 256 + 768 + 1024;
   auto fits = [&](int sk, int sv) { return fixed + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
@@ -1255,7 +1247,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->ones = off;   off += 4096;
   p->mu = off;     off += 4096;
   p->refs = off;   off += refs;
-  p->base = off;   off += 2048;
+  p->base = off;   off += 1024;
   p->chunks = off; off += 256;
   p->misc = off;   off += 768;
   p->bytes = off + 1024;
