@@ -22,7 +22,6 @@ constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
 constexpr int kPlainThreads = 256;
 constexpr int kKeyStride = kHeadDim + 4;            // floats between rows of keys and queries in shared memory
 constexpr int kFinishThreads = 128;
-constexpr int kFinishRows = 8;                      // nodes of a finish block
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -48,17 +47,42 @@ __device__ __forceinline__ int64_t node_pos(const TreeArgs& a, int entry, bool f
   return p < 0 ? 0 : a.rope_len - 1;
 }
 
-// Block = (unit, split of the cache) x 32 nodes.  32 tokens at a time: their K latents in
-// shared memory, keys by a thread per (dimension, 16 tokens), rotated in place, then eight
-// threads a node take its scores, its softmax and r_v / 8 columns of its latent sum each.
+// W_up,k of the loop in fp32 as [H][r_k][128], dimensions in the paired layout: the plain kernel's threads
+// read neighbouring dimensions of one column (from L1; in shared memory it left room for one block an SM).
+// Block = 32 columns of a head.
+template <typename T>
+__global__ void __launch_bounds__(kPlainThreads) tree_turn_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ float t[32][kHeadDim + 1];
+  const int h = blockIdx.x, c0 = blockIdx.y * 32, cols = min(32, a.r_k - c0);
+  const T* W = static_cast<const T*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * a.r_k + c0;
+  const int c = threadIdx.x & 31, e0 = threadIdx.x >> 5;
+  if (c < cols) {
+    float x[kHeadDim * 32 / kPlainThreads];           // every load under way before the first is used
+#pragma unroll
+    for (int k = 0; k < kHeadDim * 32 / kPlainThreads; ++k) {
+      const int e = e0 + k * (kPlainThreads / 32);
+      x[k] = to_f(W[static_cast<int64_t>(e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64)) * a.r_k + c]);
+    }
+#pragma unroll
+    for (int k = 0; k < kHeadDim * 32 / kPlainThreads; ++k) t[c][e0 + k * (kPlainThreads / 32)] = x[k];
+  }
+  __syncthreads();
+  float* out = a.w_turned + (static_cast<int64_t>(h) * a.r_k + c0) * kHeadDim;
+  for (int i = threadIdx.x; i < kHeadDim * cols; i += kPlainThreads) out[i] = t[i >> 7][i & 127];
+}
+
+// Block = (unit, split of the cache) x 32 nodes.  32 tokens at a time: their K latents transposed in shared
+// memory, keys by a thread per 4 tokens x 4 dimensions, rotated in place, then eight threads a node take
+// its scores, its softmax and a share of its latent sum.
 // Bound by its multiply-adds (2 * 128 * r_k a token for the keys, repeated for every 32 nodes).
 template <typename T>
-__global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kPlainThreads, 2) tree_plain_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ float4 sh4[];
+  constexpr int kTokStride = kTreePlainTile + 4;
   float* qs = reinterpret_cast<float*>(sh4);                    // [32][kKeyStride]
   float* ks = qs + kTreePlainRows * kKeyStride;                 // [32][kKeyStride]
-  float* cs = ks + kTreePlainTile * kKeyStride;                 // [32][r_k]
-  float* vs = cs + kTreePlainTile * a.r_k;                      // [32][r_v]
+  float* ct = ks + kTreePlainTile * kKeyStride;                 // [r_k][kTokStride]: latents transposed
+  float* vs = ct + a.r_k * kTokStride;                          // [32][r_v]
   float* ps = vs + kTreePlainTile * a.r_v;                      // [32][33]
   const int tid = threadIdx.x;
   const int64_t unit = blockIdx.x / a.splits;
@@ -91,56 +115,89 @@ __global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_
   }
 
   const int row = tid >> 3, part = tid & 7;     // eight threads a node
-  const int nv = a.r_v >> 3;                    // columns of its latent sum a thread keeps
-  float acc[kMaxRankPerHead / 8];
+  // its latent sum: columns 4 part .. of every 32
+  float4 acc[kMaxRankPerHead / 32];
 #pragma unroll
-  for (int i = 0; i < kMaxRankPerHead / 8; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kMaxRankPerHead / 32; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
-  const T* W = static_cast<const T*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * a.r_k;
-  const int e = tid & 127, half = tid >> 7;     // key dimension and token half of a thread
-  // dimension e of the paired layout is dimension src of W and mu
-  const int src = e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64);
-  const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
-
+  const float* W = a.w_turned + static_cast<int64_t>(h) * a.r_k * kHeadDim;
+  const int tg = tid >> 5, dg = tid & 31;       // keys: tokens 4 tg .., dimensions 4 dg .. (paired layout)
+  float mu[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    const int e = 4 * dg + d;
+    mu[d] = __ldg(a.mu_k + h * a.mu_hstride + (e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64)));
+  }
   for (int64_t t0 = j0; t0 < j1; t0 += kTreePlainTile) {
     const int cnt = static_cast<int>(min(static_cast<int64_t>(kTreePlainTile), j1 - t0));
     __syncthreads();
-    // ---- latents of the tile; zeros past its last token
-    const int gk = a.r_k >> 2, gv = a.r_v >> 2, g = gk + gv;
-    for (int i = tid; i < kTreePlainTile * g; i += kPlainThreads) {
-      const int t = i / g, c = i - t * g;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < cnt) {
-        const int64_t at = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, t0 + t, a.status);
-        x = c < gk ? ld4(static_cast<const T*>(a.cache_k) + at * a.r_k + 4 * c)
-                   : ld4(static_cast<const T*>(a.cache_v) + at * a.r_v + 4 * (c - gk));
+    // ---- latents of the tile, four tokens a warp, their loads together; zeros past its last token
+    const int gk = a.r_k >> 2, gv = a.r_v >> 2;
+    {
+      int64_t at[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int t = 4 * tg + u;
+        at[u] = t < cnt ? latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, t0 + t, a.status) : 0;
       }
-      *reinterpret_cast<float4*>(c < gk ? cs + t * a.r_k + 4 * c : vs + t * a.r_v + 4 * (c - gk)) = x;
+      for (int c = dg; c < gk + gv; c += 32) {
+        float4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          x[u] = c < gk ? ld4(static_cast<const T*>(a.cache_k) + at[u] * a.r_k + 4 * c)
+                        : ld4(static_cast<const T*>(a.cache_v) + at[u] * a.r_v + 4 * (c - gk));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (4 * tg + u >= cnt) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < gk) {
+          float* to = ct + 4 * c * kTokStride + 4 * tg;
+          *reinterpret_cast<float4*>(to) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
+          *reinterpret_cast<float4*>(to + kTokStride) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
+          *reinterpret_cast<float4*>(to + 2 * kTokStride) = make_float4(x[0].z, x[1].z, x[2].z, x[3].z);
+          *reinterpret_cast<float4*>(to + 3 * kTokStride) = make_float4(x[0].w, x[1].w, x[2].w, x[3].w);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) *reinterpret_cast<float4*>(vs + (4 * tg + u) * a.r_v + 4 * (c - gk)) = x[u];
+        }
+      }
     }
-    __syncthreads();
     // ---- keys before rotation
-    float k[16];
+    float k[4][4];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) k[t] = mu;
-    for (int r = 0; r < a.r_k; r += 4) {
-      const float4 w = ld4(W + static_cast<int64_t>(src) * a.r_k + r);
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
-        const float4 c = *reinterpret_cast<const float4*>(cs + (16 * half + t) * a.r_k + r);
-        k[t] = fmaf(w.x, c.x, fmaf(w.y, c.y, fmaf(w.z, c.z, fmaf(w.w, c.w, k[t]))));
-      }
+      for (int d = 0; d < 4; ++d) k[t][d] = mu[d];
+    __syncthreads();
+#pragma unroll 8
+    for (int r = 0; r < a.r_k; ++r) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(W + r * kHeadDim + 4 * dg));
+      const float4 c = *reinterpret_cast<const float4*>(ct + r * kTokStride + 4 * tg);
+      const float wv[4] = {w.x, w.y, w.z, w.w}, cv[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) k[t][d] = fmaf(cv[t], wv[d], k[t][d]);
     }
 #pragma unroll
-    for (int t = 0; t < 16; ++t) ks[(16 * half + t) * kKeyStride + e] = k[t];
+    for (int t = 0; t < 4; ++t)
+      *reinterpret_cast<float4*>(ks + (4 * tg + t) * kKeyStride + 4 * dg) = make_float4(k[t][0], k[t][1], k[t][2], k[t][3]);
     __syncthreads();
-    // ---- rotation by each token's row of the table
-    for (int i = tid; i < kTreePlainTile * 64; i += kPlainThreads) {
-      const int t = i >> 6, f = i & 63;
-      if (t < cnt) {
-        const float c = __ldg(a.rope_cos + (t0 + t) * 64 + f), s = __ldg(a.rope_sin + (t0 + t) * 64 + f);
-        const float x0 = ks[t * kKeyStride + f], x1 = ks[t * kKeyStride + 64 + f];
-        ks[t * kKeyStride + f] = x0 * c - x1 * s;
-        ks[t * kKeyStride + 64 + f] = x0 * s + x1 * c;
+    // ---- rotation by each token's row of the table: frequency tid mod 64 of every fourth token
+    {
+      const int f = tid & 63, t1 = tid >> 6;
+      float c[8], sn[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int64_t at = (t0 + min(t1 + 4 * u, cnt - 1)) * 64 + f;
+        c[u] = __ldg(a.rope_cos + at);
+        sn[u] = __ldg(a.rope_sin + at);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        float* kk = ks + (t1 + 4 * u) * kKeyStride + f;
+        const float x0 = kk[0], x1 = kk[64];
+        kk[0] = x0 * c[u] - x1 * sn[u];
+        kk[64] = x0 * sn[u] + x1 * c[u];
       }
     }
     __syncthreads();
@@ -176,13 +233,21 @@ __global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_
     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     l = l * alpha + sum;
     __syncwarp();
-    // ---- latent sum: columns part, part + 8, ..
+    // ---- latent sum
 #pragma unroll
-    for (int i = 0; i < kMaxRankPerHead / 8; ++i) {
-      if (i < nv) {
-        float x = acc[i] * alpha;
-        for (int t = 0; t < kTreePlainTile; ++t) x = fmaf(ps[row * 33 + t], vs[t * a.r_v + part + 8 * i], x);
-        acc[i] = x;
+    for (int i = 0; i < kMaxRankPerHead / 32; ++i) {
+      if (32 * i < a.r_v) { acc[i].x *= alpha; acc[i].y *= alpha; acc[i].z *= alpha; acc[i].w *= alpha; }
+    }
+#pragma unroll 2
+    for (int t = 0; t < kTreePlainTile; ++t) {
+      const float p = ps[row * 33 + t];
+#pragma unroll
+      for (int i = 0; i < kMaxRankPerHead / 32; ++i) {
+        if (32 * i + 4 * part < a.r_v) {
+          const float4 v = *reinterpret_cast<const float4*>(vs + t * a.r_v + 32 * i + 4 * part);
+          acc[i].x = fmaf(p, v.x, acc[i].x); acc[i].y = fmaf(p, v.y, acc[i].y);
+          acc[i].z = fmaf(p, v.z, acc[i].z); acc[i].w = fmaf(p, v.w, acc[i].w);
+        }
       }
     }
   }
@@ -190,12 +255,12 @@ __global__ void __launch_bounds__(kPlainThreads) tree_plain_kernel(const __grid_
     float* rec = a.records + ((unit * a.splits + split) * a.rec_rows + row0 + row) * (a.r_v + kTreeHead);
     if (part == 0) { rec[0] = m; rec[1] = l; rec[2] = rec[3] = rec[4] = 0.f; }
 #pragma unroll
-    for (int i = 0; i < kMaxRankPerHead / 8; ++i)
-      if (i < nv) rec[kTreeHead + part + 8 * i] = acc[i];
+    for (int i = 0; i < kMaxRankPerHead / 32; ++i)
+      if (32 * i + 4 * part < a.r_v) *reinterpret_cast<float4*>(rec + kTreeHead + 32 * i + 4 * part) = acc[i];
   }
 }
 
-// Block = (unit, eight nodes), one node at a time: scores of the nodes on its path (a warp each),
+// Block = (unit, a few nodes), one node at a time: scores of the nodes on its path (a warp each),
 // merge of the unit's records, then thread e forms out_e = (W_e . A + mu_e P + sum_a p_a v_a,e) / l.
 template <typename T>
 __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __grid_constant__ TreeArgs a) {
@@ -212,7 +277,7 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
   int first;
   const int n = tree_nodes(a, b, first, flag);
   const int L = tree_cached(a, b, flag);
-  if (blockIdx.y * kFinishRows >= n) return;
+  if (blockIdx.y * a.finish_rows >= n) return;
   for (int i = tid; i < n; i += kFinishThreads) {
     int p = __ldg(a.parent + first + i);
     if (p < -1 || p >= i) {
@@ -223,11 +288,11 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     if (flag) node_pos(a, first + i, true);
   }
   __syncthreads();
-  const int row_first = blockIdx.y * kFinishRows;
+  const int row_first = blockIdx.y * a.finish_rows;
   const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
   const int stride = a.r_v + kTreeHead;
 
-  for (int row = row_first; row < min(n, row_first + kFinishRows); ++row) {
+  for (int row = row_first; row < min(n, row_first + a.finish_rows); ++row) {
     const int entry = first + row;
     __syncthreads();
     if (tid == 0) {
@@ -298,7 +363,8 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
 }
 
 size_t plain_smem(int r_k, int r_v) {
-  return sizeof(float) * ((kTreePlainRows + kTreePlainTile) * kKeyStride + kTreePlainTile * (r_k + r_v) + kTreePlainRows * 33);
+  return sizeof(float) * ((kTreePlainRows + kTreePlainTile) * kKeyStride + (kTreePlainTile + 4) * r_k + kTreePlainTile * r_v +
+                          kTreePlainRows * 33);
 }
 
 }  // namespace
@@ -311,12 +377,14 @@ cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(plain_smem(kMaxRankPerHead, kMaxRankPerHead)));
   if (e != cudaSuccess) return e;
+  auto turn = bf16 ? tree_turn_kernel<__nv_bfloat16> : tree_turn_kernel<float>;
+  turn<<<dim3(a.H, (a.r_k + 31) / 32), kPlainThreads, 0, s>>>(a);
   kern<<<grid, kPlainThreads, plain_smem(a.r_k, a.r_v), s>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_tree_finish(const TreeArgs& a, bool bf16, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H), (a.max_nodes + kFinishRows - 1) / kFinishRows);
+  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(a.B) * a.H), (a.max_nodes + a.finish_rows - 1) / a.finish_rows);
   if (bf16) tree_finish_kernel<__nv_bfloat16><<<grid, kFinishThreads, 0, s>>>(a);
   else tree_finish_kernel<float><<<grid, kFinishThreads, 0, s>>>(a);
   return cudaGetLastError();
@@ -352,7 +420,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t tile_start, cta_start, bias, qimg, khat, paths, records, total;
+  size_t turned, tile_start, cta_start, bias, qimg, khat, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -380,8 +448,9 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
   const int64_t per = (tiles + want - 1) / want;
   w.chunk = per * kTreePlainTile;
   w.splits = static_cast<int>((tiles + per - 1) / per);
-  w.records = 256;
-  w.total = 256 + static_cast<size_t>(units) * w.splits * rec;
+  w.turned = 256;
+  w.records = 256 + static_cast<size_t>(d->H) * d->r_k * kHeadDim * 4;
+  w.total = w.records + static_cast<size_t>(units) * w.splits * rec;
   return w;
 }
 
@@ -511,6 +580,8 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   a.records = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.records);
   a.rec_rows = a.max_nodes;
   a.splits = w.splits;
+  // nodes of a finish block: few enough that there are four blocks an SM, at most eight (which share W_up,v in L1)
+  a.finish_rows = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, static_cast<int64_t>(tree->n_tok) * dims->H / (4 * sms))));
   a.chunk = w.chunk;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dims->dtype == LLA_BF16;
@@ -531,6 +602,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     if (!tree_maps(a, &maps)) return LLA_ERR_CUDA;
     return launch_tree_tensor(a, maps, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
   }
+  a.w_turned = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.turned);
   if (launch_tree_plain(a, bf16, s) != cudaSuccess || launch_tree_finish(a, bf16, s) != cudaSuccess) return LLA_ERR_CUDA;
   return LLA_OK;
 }

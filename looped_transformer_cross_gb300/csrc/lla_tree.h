@@ -58,8 +58,9 @@ struct TreeArgs {
   // Partial results of the cached tokens: a record holds rec_rows rows of {m, l's, acc[r_v]}, acc and
   // l relative to 2^m.  Plain kernel: record (b H + h) * splits + s covers tokens s * chunk ..
   float* records;
-  int rec_rows, splits;
+  int rec_rows, splits, finish_rows;
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
+  float* w_turned;                   // plain kernel: [H][r_k][128]
   // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of 64 nodes, and record
   // unit + CTA belongs to every (unit, CTA) that share a tile
   int v_whole;                       // r_v a multiple of 32: V by maps.v4
