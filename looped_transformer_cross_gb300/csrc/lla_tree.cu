@@ -420,7 +420,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t turned, tile_start, cta_start, bias, qimg, khat, paths, records, total;
+  size_t turned, tile_start, cta_start, bias, qimg, qback, khat, kback, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -436,8 +436,10 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
     w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
-    w.khat = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 256;
-    w.paths = w.khat + static_cast<size_t>(units) * max_nodes * 256;
+    w.qback = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 512;
+    w.khat = al(w.qback + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 4);
+    w.kback = w.khat + static_cast<size_t>(units) * max_nodes * 512;
+    w.paths = al(w.kback + static_cast<size_t>(units) * max_nodes * 4);
     w.records = al(w.paths + static_cast<size_t>(std::max(B, 1)) * max_nodes * 16);
     w.total = w.records + static_cast<size_t>(units * groups + w.grid) * rec;
     return w;
@@ -596,7 +598,9 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
     a.bias = ws + w.bias;
     a.qimg = ws + w.qimg;
+    a.qback = reinterpret_cast<float*>(ws + w.qback);
     a.khat = ws + w.khat;
+    a.kback = reinterpret_cast<float*>(ws + w.kback);
     a.paths = reinterpret_cast<uint4*>(ws + w.paths);
     TreeMaps maps;
     if (!tree_maps(a, &maps)) return LLA_ERR_CUDA;

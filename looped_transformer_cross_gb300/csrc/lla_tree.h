@@ -67,8 +67,10 @@ struct TreeArgs {
   int groups, rows, grid;            // blocks of nodes a sequence may have, nodes S has room for, CTAs
   int32_t* tile_start;               // [B + 1]: tiles of one head before sequence b
   int4* cta_start;                   // [grid]: first (sequence, head, tile), number of tiles
-  uint8_t* qimg;                     // [units][rows * 256] query operands
-  uint8_t* khat;                     // [B H][max_nodes][256] rotated keys of the nodes
+  uint8_t* qimg;                     // [units][rows * 512] query operands, rows scaled by powers of two
+  float* qback;                      // [units][rows] what undoes that
+  uint8_t* khat;                     // [B H][max_nodes][512] rotated keys of the nodes, scaled likewise
+  float* kback;                      // [B H][max_nodes]
   uint4* paths;                      // [B][max_nodes] nodes on each node's path, as bits
   uint8_t* bias;                     // [H][4096] mu operands
   TreePlan plan;

@@ -5,9 +5,14 @@
 // cut into equal contiguous ranges, one persistent CTA per SM.  Per tile, three matrix products,
 // tokens in the rows of the first two:
 //   U = C_k W^T + mu          128 tokens x 128 dimensions, latents by TMA
-//   S = K^ Q^^T               128 tokens x nodes: K^ is U rotated and rounded to bf16 by the warps below,
-//                             read from TMEM; Q^ (rotated, scaled to log2 units) from tree_prepare_kernel
+//   S = K^ Q^^T               128 tokens x nodes: K^ is U rotated by the warps below, over U in TMEM; Q^
+//                             (rotated, scaled to log2 units) from tree_prepare_kernel
 //   D += C_v^T P              r_v x nodes, both operands MN-major from shared memory
+// K^, Q^ and P are each the sum of two 16-bit parts: one rounding to bf16 of each made the log-sum-exp 1e-3
+// off and an output 1.5 times as far off as its own rounding.  K^ and Q^ are f16 + f16 (22 bits; products
+// high x high, high x low, low x high; a row of Q^ is scaled by a power of two to 1..2 first, K^ is not: a
+// component of a cached key beyond 65504 has no f16 part, and its sequence's results are NaN), P is
+// bf16 + bf16 (16 bits at any size).
 // so a key is reconstructed and rotated once for all nodes of its sequence, V never is, and the
 // products and exponentials of S and D are made for 16, 32 or 64 nodes, not for a full 128 rows.
 // Weights are 2^(s - ref) with one reference per node and unit: the largest score of the unit's first
@@ -24,6 +29,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cuda_fp16.h>
+
 #include "lla_tree.h"
 
 namespace lla {
@@ -38,13 +45,13 @@ constexpr int kPrepThreads = 256;
 constexpr int kRotWarps = 8;
 constexpr int kSoftWarp0 = 4 + kRotWarps;
 constexpr int kTreeThreads = 32 * (kSoftWarp0 + 4);
-constexpr int kKhatCol = 256;                       // TMEM columns: U 0..255 (two), K^, S, D
+constexpr int kSCol = 256;                          // TMEM columns: U, then K^ in its place 0..255 (two), S (two), D
 
 struct alignas(16) TreeMisc {
   uint64_t kfull[kMaxStages], kempty[kMaxStages], vfull[kMaxStages], vempty[kMaxStages];
   uint64_t wfull, wfree, qfull, qfree;              // the unit's W and bias; its queries
-  uint64_t ufull[2], ufree[2];                      // U computed and the tile's base RoPE row written; both read
-  uint64_t rfull[2];                                // K^ written
+  uint64_t ufull[2];                                // U computed and the tile's base RoPE row written
+  uint64_t rfull[2];                                // K^ written over U, the base row read
   uint64_t sfull[2], sfree[2];                      // S computed (and K^ read); S read
   uint64_t pfull[2], vdone[2];                      // P written; D += C_v^T P done
   uint64_t vote;                                    // the four softmax warps
@@ -114,6 +121,7 @@ __device__ __forceinline__ uint64_t pair2(float lo, float hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
+__device__ __forceinline__ void unpack2(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
 __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -124,11 +132,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
   return r;
 }
-// The two lanes rounded to bf16, the lower one in the low half.
-__device__ __forceinline__ uint32_t pack2(uint64_t x) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-  return pack_bf16(lo, hi);
+// x = hi + lo in f16: hi with x's first 11 bits, lo with the next 11 (both lanes).
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void split2(uint64_t x, uint64_t minus, uint32_t& hi, uint32_t& lo) {
+  float x0, x1;
+  unpack2(x, x0, x1);
+  hi = pack_f16(x0, x1);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  unpack2(fma2(pair2(h.x, h.y), minus, x), x0, x1);
+  lo = pack_f16(x0, x1);
+}
+__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16(x0, x1);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = pack_f16(x0 - h.x, x1 - h.y);
+}
+// x = hi + lo in bf16 (16 bits).
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -250,27 +275,24 @@ __device__ __forceinline__ void load_pairs8(const __nv_bfloat16* v, int style, i
   }
 }
 
-// The pairs rotated, times `scale`, in bf16.
+// The pairs rotated, times `scale`: first members, then second members.
 __device__ __forceinline__ void turn_pairs8(const float (&x0)[8], const float (&x1)[8], const float* c, const float* s, float scale,
-                                            uint4& y0, uint4& y1) {
-  float z0[8], z1[8];
+                                            float (&z)[16]) {
 #pragma unroll
   for (int k = 0; k < 8; k += 4) {
     const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + k)), s4 = __ldg(reinterpret_cast<const float4*>(s + k));
     const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      z0[k + e] = (x0[k + e] * cc[e] - x1[k + e] * ss[e]) * scale;
-      z1[k + e] = (x0[k + e] * ss[e] + x1[k + e] * cc[e]) * scale;
+      z[k + e] = (x0[k + e] * cc[e] - x1[k + e] * ss[e]) * scale;
+      z[8 + k + e] = (x0[k + e] * ss[e] + x1[k + e] * cc[e]) * scale;
     }
   }
-  y0 = make_uint4(pack_bf16(z0[0], z0[1]), pack_bf16(z0[2], z0[3]), pack_bf16(z0[4], z0[5]), pack_bf16(z0[6], z0[7]));
-  y1 = make_uint4(pack_bf16(z1[0], z1[1]), pack_bf16(z1[2], z1[3]), pack_bf16(z1[4], z1[5]), pack_bf16(z1[6], z1[7]));
 }
 
-// Blocks 0 .. units-1: the unit's query operand, RoPE(q, pos) log2(e)/sqrt(d) in bf16, as the
+// Blocks 0 .. units-1: the unit's query operand, RoPE(q, pos) log2(e)/sqrt(d) as two f16 parts, each the
 // shared-memory image (two chunks of 64 columns, 128-byte rows, swizzled), and its drafted keys, RoPE(k, pos)
-// in bf16, row by row; dimensions in the order first members of the pairs, then second members, as U's.
+// likewise, row by row; dimensions in the order first members of the pairs, then second members, as U's.
 // Then B blocks: the nodes on each node's path as bits, and the checks of a sequence's values.  Then H
 // blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits).  The last
 // block: tiles per sequence, and every CTA's first tile.
@@ -286,12 +308,16 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     const int n = tree_nodes(a, b, first, false) - g * kTreeGroup;
     if (n <= 0) return;
     first += g * kTreeGroup;
-    uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 256;
-    uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup) * 256;
-    for (int i = tid; i < a.rows * 16; i += kPrepThreads) {
+    uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 512;
+    float* back_q = a.qback + static_cast<int64_t>(blockIdx.x) * a.rows;
+    uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup) * 512;
+    float* back_k = a.kback + static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup;
+    for (int i = tid; i < a.rows * 16; i += kPrepThreads) {      // (whole warps: rows is a multiple of 16)
       const bool key = i >= a.rows * 8;
       const int it = key ? i - a.rows * 8 : i, r = it >> 3, f0 = (it & 7) * 8;
-      uint4 y0 = make_uint4(0, 0, 0, 0), y1 = y0;
+      float z[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) z[k] = 0.f;
       if (r < n) {
         const int64_t entry = first + r;
         const __nv_bfloat16* v = key ? static_cast<const __nv_bfloat16*>(a.k) + entry * a.k_stride
@@ -301,15 +327,35 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
         int p = __ldg(a.pos + entry);
         p = p < 0 ? 0 : (p >= a.rope_len ? static_cast<int>(a.rope_len - 1) : p);
         const int64_t at = static_cast<int64_t>(p) * 64 + f0;
-        turn_pairs8(x0, x1, a.rope_cos + at, a.rope_sin + at, key ? 1.f : kLog2e * kInvSqrtD, y0, y1);
+        turn_pairs8(x0, x1, a.rope_cos + at, a.rope_sin + at, key ? 1.f : kLog2e * kInvSqrtD, z);
       }
+      // the row times the power of two that brings its largest value to 1..2 (eight lanes hold a row)
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(z[k]));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+      const float scale = __uint_as_float((254u - e) << 23);
+      uint32_t hi[8], lo[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) split_f16(z[2 * k] * scale, z[2 * k + 1] * scale, hi[k], lo[k]);
+      const uint4 h0 = make_uint4(hi[0], hi[1], hi[2], hi[3]), h1 = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+      const uint4 l0 = make_uint4(lo[0], lo[1], lo[2], lo[3]), l1 = make_uint4(lo[4], lo[5], lo[6], lo[7]);
       if (!key) {
         const uint32_t o = swizzle_offset(r * 128 + f0 * 2, 128);
-        *reinterpret_cast<uint4*>(img + o) = y0;
-        *reinterpret_cast<uint4*>(img + a.rows * 128 + o) = y1;
+        *reinterpret_cast<uint4*>(img + o) = h0;
+        *reinterpret_cast<uint4*>(img + a.rows * 128 + o) = h1;
+        *reinterpret_cast<uint4*>(img + a.rows * 256 + o) = l0;
+        *reinterpret_cast<uint4*>(img + a.rows * 384 + o) = l1;
+        if (f0 == 0) back_q[r] = __uint_as_float(e << 23);
       } else if (r < n) {
-        *reinterpret_cast<uint4*>(keys + r * 256 + f0 * 2) = y0;
-        *reinterpret_cast<uint4*>(keys + r * 256 + 128 + f0 * 2) = y1;
+        uint8_t* to = keys + r * 512 + f0 * 2;
+        *reinterpret_cast<uint4*>(to) = h0;
+        *reinterpret_cast<uint4*>(to + 128) = h1;
+        *reinterpret_cast<uint4*>(to + 256) = l0;
+        *reinterpret_cast<uint4*>(to + 384) = l1;
+        if (f0 == 0) back_k[r] = __uint_as_float(e << 23);
       }
     }
     return;
@@ -429,10 +475,15 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
 template <int kPage, int kRows>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
-  constexpr int kBuf = kRows <= 32 ? 2 : 1;           // buffers of K^ and of S (TMEM has 512 columns)
-  constexpr int kSCol = kKhatCol + 64 * kBuf, kDCol = kSCol + kRows * kBuf;
-  static_assert(kDCol + 2 * kRows <= 512, "TMEM columns");
-  constexpr uint32_t kPRow = kRows * 2;               // bytes of a token's weights
+  // The two parts of the weights: up to 32 nodes side by side in a token's row, one product for both (into columns
+  // of their own); 64 nodes one tile after the other, two products into the same columns, and one buffer of
+  // both (shared memory, TMEM)
+  constexpr bool kBoth = kRows <= 32;
+  constexpr int kPBuf = kBoth ? 2 : 1, kDCols = kBoth ? 2 * kRows : kRows;
+  constexpr int kDCol = kSCol + 2 * kRows;
+  static_assert(kDCol + 2 * kDCols <= 512, "TMEM columns");
+  constexpr uint32_t kPRow = kDCols * 2;              // bytes of a token's weights
+  constexpr uint32_t kPTile = kTile * kPRow * (kBoth ? 1 : 2), kLow = kBoth ? kRows * 2 : kTile * kPRow;     // (the lower parts' place)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const TreePlan& P = a.plan;
@@ -453,7 +504,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     mbar_init(bar(misc->wfull), 1); mbar_init(bar(misc->wfree), 1);
     mbar_init(bar(misc->qfull), 1); mbar_init(bar(misc->qfree), 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(misc->ufull[s]), 2); mbar_init(bar(misc->ufree[s]), kRotWarps);
+      mbar_init(bar(misc->ufull[s]), 2);
       mbar_init(bar(misc->rfull[s]), kRotWarps);
       mbar_init(bar(misc->sfull[s]), 1); mbar_init(bar(misc->sfree[s]), 4);
       mbar_init(bar(misc->pfull[s]), 4); mbar_init(bar(misc->vdone[s]), 1);
@@ -472,10 +523,12 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     tmem_alloc(smem_u32(&misc->tmem_base), 512);
   }
   if (warp >= kSoftWarp0) {
-    // ones that meet the three parts of mu
+    // ones that meet the three parts of mu: eight rows, the same for every eight tokens
     const int r = tid - 32 * kSoftWarp0;
-    *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32, 32)) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
-    *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32 + 16, 32)) = make_uint4(0, 0, 0, 0);
+    if (r < 8) {
+      *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32, 32)) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
+      *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32 + 16, 32)) = make_uint4(0, 0, 0, 0);
+    }
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -583,7 +636,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   } else if (warp == 1) {
     // ======================================================== U = C_k W^T + mu
     const uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
-    const uint64_t d_ones = umma_desc(sbase + P.ones, 16, 256, kSw32), d_mu = umma_desc(sbase + P.mu, 16, 256, kSw32);
+    const uint64_t d_ones = umma_desc(sbase + P.ones, 16, 0, kSw32), d_mu = umma_desc(sbase + P.mu, 16, 256, kSw32);
     const int r_k = a.r_k, n64 = r_k / 64, k32 = r_k & 32, k16 = r_k & 16;
     const int o32 = r_k / 64 * 16384, o16 = o32 + (r_k & 32) * 256;
     const uint32_t k_ring = sbase + P.k_ring, wb = sbase + P.w, kst = static_cast<uint32_t>(P.k_stage) >> 4;
@@ -614,10 +667,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
       if constexpr (kPage == 3) fence_proxy_async_smem();       // (plain copies, read by the products)
-      if (i >= 2 && !wait(misc->ufree[i & 1], (i - 2) >> 1)) break;      // (and the row's place with U's)
-      // where K^ has two buffers, S(i - 2) has read the one that U(i) becomes: one wait here instead of one for
-      // each rotating warp
-      if (kBuf == 2 && i >= 2 && !wait(misc->sfull[i & 1], (i - 2) >> 1)) break;
+      if (i >= 2 && !wait(misc->sfull[i & 1], (i - 2) >> 1)) break;      // S(i - 2) has read the K^ in U(i)'s place
       reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = ahead;
       tc_fence_after();
       __syncwarp();
@@ -647,32 +697,36 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     landed(misc->wfull, unit);
   } else if (warp == 2) {
     // ======================================================== S = K^ Q^^T
-    const uint32_t idesc = umma_idesc_bf16(128, kRows, false, false);
+    const uint32_t idesc = umma_idesc_f16(128, kRows);
     const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128);
     int unit = -1;
     for (int i = 0; i < count; ++i) {
-      const int sb = i % kBuf;
+      const int sb = i & 1;
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->qfree, unit)) break;
         ++unit;
         if (lane == 0) {
           const uint32_t qf = bar(misc->qfull);
-          mbar_arrive_expect_tx(qf, kRows * 256);
-          bulk_load(sbase + P.q, a.qimg + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * (kRows * 256), kRows * 256, qf);
+          mbar_arrive_expect_tx(qf, kRows * 512);
+          bulk_load(sbase + P.q, a.qimg + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * (kRows * 512), kRows * 512, qf);
         }
         __syncwarp();
         if (!wait(misc->qfull, unit)) break;
       }
-      if (!wait(misc->rfull[sb], i / kBuf)) break;
-      if (i >= kBuf && !wait(misc->sfree[sb], (i - kBuf) / kBuf)) break;
+      if (!wait(misc->rfull[sb], i >> 1)) break;
+      if (i >= 2 && !wait(misc->sfree[sb], (i - 2) >> 1)) break;
       // the weights of tile i - 2 have been read: those of S(i) take their place (one wait here instead of one for
       // each softmax warp)
-      if (i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
+      if (kPBuf == 2 && i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int k = 0; k < 8; ++k)
-        umma_bf16_ts_warp(tmem + kSCol + sb * kRows, tmem + kKhatCol + sb * 64 + 8 * k, d_q + (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2,
-                          idesc, k > 0);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t d = tmem + kSCol + sb * kRows, high = tmem + sb * 128 + 16 * k;
+        const uint64_t q_high = d_q + (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2;
+        umma_bf16_ts_warp(d, high, q_high, idesc, k > 0);
+        umma_bf16_ts_warp(d, high, q_high + kRows * 256 / 16, idesc, 1);
+        umma_bf16_ts_warp(d, high + 8, q_high, idesc, 1);
+      }
       umma_commit_warp(bar(misc->sfull[sb]));
       if (w.t == w.nb - 1) umma_commit_warp(bar(misc->qfree));
       walk_next(w, a);
@@ -683,7 +737,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== D += C_v^T P
     // (two blocks of 128 rows of r_v; rows past r_v read whatever follows the tile in shared memory and
     // are not looked at)
-    const uint32_t idesc = umma_idesc_bf16(128, kRows, true, true);
+    const uint32_t idesc = umma_idesc_bf16(128, kDCols, true, true);
     // V: chunks of 32 columns, their 128 token rows of 64 bytes one after the other; with one copy per piece of
     // 8..64 tokens, piece by piece, each [chunk][piece rows]
     const bool by_piece = kPage == 2 && a.v_whole;
@@ -716,7 +770,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       }
       if (!wait(misc->pfull[j & 1], j >> 1)) break;
       tc_fence_after();
-      const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j & 1) * (kTile * kPRow / 16);
+      const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j % kPBuf) * (kPTile / 16);
       const uint32_t sum = !(j == 0 || w.t == 0);     // a unit's first product starts the sum
 #pragma unroll 1
       for (int blk = 0; blk < blocks; ++blk)
@@ -724,7 +778,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         for (int k = 0; k < steps; ++k) {
           // (rows is a power of two; a whole tile is one region)
           const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
-          umma_bf16_warp(tmem + kDCol + blk * kRows, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
+          umma_bf16_warp(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
+          if (!kBoth) umma_bf16_warp(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + kLow / 16 + k * kPRow, idesc, 1);
         }
       umma_commit_warp(bar(misc->vdone[j & 1]));
       umma_commit_warp(bar(misc->vempty[vr.slot]));
@@ -746,11 +801,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint64_t minus = pair2(-1.f, -1.f);
     const float* rows = reinterpret_cast<const float*>(sm + P.base) + f0;
     for (int i = 0; i < count; ++i) {
-      const int kb = i % kBuf;
-      const uint32_t t_u = lanes + (i & 1) * 128 + f0, t_k = lanes + kKhatCol + kb * 64 + f0 / 2;
+      const uint32_t t_u = lanes + (i & 1) * 128 + f0;
       const float* base = rows + (i & 1) * 128;       // cos, then sin
       if (!wait(misc->ufull[i & 1], i >> 1)) break;
-      if (kBuf == 1 && i >= 1 && !wait(misc->sfull[0], i - 1)) break;      // the last K^ has been read
       tc_fence_after();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -758,7 +811,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         tmem_ld_x16(t_u + 16 * g, u0);
         tmem_ld_x16(t_u + 64 + 16 * g, u1);
         tmem_wait_ld();
-        uint32_t y0[8], y1[8];
+        uint32_t y0[16], y1[16];                      // (higher parts, then lower)
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
           const float4 c4 = *reinterpret_cast<const float4*>(base + 16 * g + 2 * k);
@@ -769,30 +822,32 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             const int f = 8 * g + k + e;
             const uint64_t c = fma2(mul2(sb, sl[f]), minus, mul2(cb, cl[f])), sn = fma2(sb, cl[f], mul2(cb, sl[f]));
             const uint64_t x0 = pair2(u0[2 * (k + e)], u0[2 * (k + e) + 1]), x1 = pair2(u1[2 * (k + e)], u1[2 * (k + e) + 1]);
-            y0[k + e] = pack2(fma2(mul2(x1, sn), minus, mul2(x0, c)));
-            y1[k + e] = pack2(fma2(x0, sn, mul2(x1, c)));
+            split2(fma2(mul2(x1, sn), minus, mul2(x0, c)), minus, y0[k + e], y0[8 + k + e]);
+            split2(fma2(x0, sn, mul2(x1, c)), minus, y1[k + e], y1[8 + k + e]);
           }
         }
-        tmem_st_x8(t_k + 8 * g, y0);
-        tmem_st_x8(t_k + 32 + 8 * g, y1);
+        tmem_st_x16(t_u + 16 * g, y0);
+        tmem_st_x16(t_u + 64 + 16 * g, y1);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(misc->rfull[kb]));
-        mbar_arrive(bar(misc->ufree[i & 1]));
-      }
+      if (lane == 0) mbar_arrive(bar(misc->rfull[i & 1]));
     }
   } else {
     // ======================================================== softmax: S -> P, records
     const int quad = warp & 3, row = 32 * quad + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    // references of this unit (each warp its own copy) and what they were multiplied by when they moved;
-    // the warps' maxima (two sets in turn)
-    float* ref = reinterpret_cast<float*>(sm + P.refs) + quad * kRows;
-    float* factor = reinterpret_cast<float*>(sm + P.refs) + (4 + quad) * kRows;
-    float* maxima = reinterpret_cast<float*>(sm + P.refs) + 8 * kRows;
+    // Of this unit's nodes: what brings a score to log2 units, minus the reference, and what the sums were
+    // multiplied by when the references moved.  A lane holds the first two of nodes lane and lane + 32; for
+    // all lanes they are in shared memory, where all four warps write the same values after a vote.  The
+    // warps' maxima (two sets in turn).
+    constexpr int kMine = (kRows + 31) / 32;
+    float back[kMine], refs[kMine];
+    float* scale = reinterpret_cast<float*>(sm + P.refs);
+    float* minus_ref = scale + kRows;
+    float* factor = minus_ref + kRows;
+    float* maxima = factor + kRows;
     const int blocks = P.blocks;
     int votes = 0, moves = 0;
     auto vote = [&]() {
@@ -823,13 +878,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (lane < 16) mine[c + lane] = keep;
       }
       if (!vote()) return false;
-      for (int c = lane; c < kRows; c += 32) {
+#pragma unroll
+      for (int j = 0; j < kMine; ++j) {
+        const int c = lane + 32 * j;
+        if (c >= kRows) break;
         const float* m = maxima + (moves & 1) * 4 * kRows + c;
-        float top = fmaxf(fmaxf(m[0], m[kRows]), fmaxf(m[2 * kRows], m[3 * kRows]));
+        float top = fmaxf(fmaxf(m[0], m[kRows]), fmaxf(m[2 * kRows], m[3 * kRows])) * back[j];
         if (fresh) top = top == -INFINITY ? 0.f : top;
-        else top = fmaxf(top, ref[c]);
-        factor[c] = exp2f(ref[c] - top);               // (not looked at for a new unit)
-        ref[c] = top;
+        else top = fmaxf(top, refs[j]);
+        factor[c] = exp2f(refs[j] - top);              // (not looked at for a new unit)
+        refs[j] = top;
+        minus_ref[c] = -top;
+        scale[c] = back[j];
       }
       ++moves;
       __syncwarp();
@@ -844,8 +904,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       const int64_t slot = (static_cast<int64_t>(cur_b) * a.H + cur_h) * a.groups + cur_g + blockIdx.x;
       const int stride = a.r_v + kTreeHead;
       float* rec = a.records + slot * a.rec_rows * stride;
-      for (int c = lane; c < n; c += 32)
-        if (quad == 0) rec[c * stride] = ref[c];
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        if (quad == 0 && lane + 32 * j < n) rec[(lane + 32 * j) * stride] = refs[j];
 #pragma unroll
       for (int t = 0; t < kRows / 8; ++t)
 #pragma unroll
@@ -858,8 +919,16 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll 1
         for (int c = 0; c < n; c += 16) {
           float v[16];
-          tmem_ld_x16(lanes + kDCol + blk * kRows + c, v);
-          tmem_wait_ld();
+          tmem_ld_x16(lanes + kDCol + blk * kDCols + c, v);
+          if constexpr (kBoth) {
+            float low[16];
+            tmem_ld_x16(lanes + kDCol + blk * kDCols + kRows + c, low);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] += low[k];
+          } else {
+            tmem_wait_ld();
+          }
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             if (c + k < n && r < a.r_v) rec[(c + k) * stride + kTreeHead + r] = v[k];
@@ -869,23 +938,29 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return true;
     };
     for (int i = 0; i <= count && count > 0; ++i) {
-      const int sb = i % kBuf;
+      const int sb = i & 1;
       const uint32_t t_s = lanes + kSCol + sb * kRows;
       const bool fresh = i == 0 || w.t == 0;
+      if (fresh && i < count) {
+        const float* from = a.qback + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * kRows;
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) back[j] = lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f;
+      }
       if (i > 0 && (fresh || i == count)) {
         if (!finish(i - 1)) break;
         cur_b = w.b; cur_h = w.h; cur_g = w.g;
       }
-      if (i == count || !wait(misc->sfull[sb], i / kBuf)) break;
+      if (i == count || !wait(misc->sfull[sb], i >> 1)) break;
       tc_fence_after();
       const bool live = w.t * kTile + row < w.L, partial = (w.t + 1) * kTile > w.L;
-      uint8_t* p = sm + P.p + (i & 1) * (kTile * kPRow);
+      uint8_t* p = sm + P.p + (i % kPBuf) * kPTile;
       if (fresh) {
         if (!move(t_s, live, true)) break;
 #pragma unroll
         for (int t = 0; t < kRows / 8; ++t) l[t][0] = l[t][1] = l[t][2] = l[t][3] = 0.f;
       }
-      // Weights, in bf16 as the product takes them (a token past the end has none).  Where a score is too
+      if (kPBuf == 1 && i > 0 && !wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;     // the last weights have been read
+      // Weights, in two bf16 parts as the product takes them (a token past the end has none).  Where a score is too
       // far above its reference, the references move and the weights are made again.
       bool settled = fresh, ok = true;
       while (true) {
@@ -897,28 +972,36 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           if constexpr (kCols == 32) tmem_ld_x32(t_s + c, s);
           else tmem_ld_x16(t_s + c, s);
           tmem_wait_ld();
-          uint32_t x[kCols / 2];
+          uint32_t x[kCols / 2], y[kCols / 2];
 #pragma unroll
           for (int k = 0; k < kCols / 2; k += 2) {
-            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(ref + c + 2 * k);
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + c + 2 * k);
+            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(minus_ref + c + 2 * k);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float d0, d1;
-              asm("mov.b64 {%0, %1}, %2;"
-                  : "=f"(d0), "=f"(d1)
-                  : "l"(fma2(e == 0 ? m.x : m.y, minus, pair2(s[2 * (k + e)], s[2 * (k + e) + 1]))));
+              unpack2(fma2(pair2(s[2 * (k + e)], s[2 * (k + e) + 1]), e == 0 ? f.x : f.y, e == 0 ? m.x : m.y), d0, d1);
               top = fmaxf(top, fmaxf(d0, d1));
-              x[k + e] = pack_bf16(exp2_fast(d0), exp2_fast(d1));
+              const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
+              const uint32_t h = pack_bf16(p0, p1);
+              x[k + e] = h;
+              unpack2(fma2(pair2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)), minus, pair2(p0, p1)), d0, d1);
+              y[k + e] = pack_bf16(d0, d1);
             }
           }
 #pragma unroll
-          for (int k = 0; k < kCols / 2; k += 4)
+          for (int k = 0; k < kCols / 2; k += 4) {
             *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + (c + 2 * k) * 2, kPRow)) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + (c + 2 * k) * 2 + kLow, kPRow)) =
+                make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+          }
         }
         if (partial && !live) {
 #pragma unroll 1
-          for (int c = 0; c < kRows; c += 8)
+          for (int c = 0; c < kRows; c += 8) {
             *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + kLow, kPRow)) = make_uint4(0, 0, 0, 0);
+          }
         }
         if (settled) break;
         if (__any_sync(0xffffffffu, live && top > kHeadroom) && lane == 0) misc->over[i & 1] = i + 1;
@@ -930,7 +1013,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < blocks * kRows; c += 8) {
+        for (int c = 0; c < blocks * kDCols; c += 8) {
           float v[8];
           tmem_ld_x8(lanes + kDCol + c, v);
           tmem_wait_ld();
@@ -955,20 +1038,20 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         mbar_arrive(bar(misc->pfull[i & 1]));
         mbar_arrive(bar(misc->sfree[sb]));
       }
-      // the sums add up what was rounded, once the products have it
+      // the sums add up both parts, once the products have them
 #pragma unroll
-      for (int t = 0; t < kRows / 16; ++t)
+      for (int t = 0; t < kRows / 8; ++t)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // four 8 x 8 blocks: tokens 0..7 and 8..15 of 16 by nodes 0..7 and 8..15, lane = block * 8 + token
-          const int tok = 32 * quad + 16 * half + (lane & 15), col = 16 * t + 8 * (lane >> 4);
+          const int tok = 32 * quad + 16 * half + (lane & 15), col = 16 * (t % (kRows / 16)) + 8 * (lane >> 4);
           uint32_t b0, b1, b2, b3;
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                        : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
-                       : "r"(smem_u32(p) + swizzle_offset(tok * kPRow + col * 2, kPRow))
+                       : "r"(smem_u32(p) + swizzle_offset(tok * kPRow + col * 2 + (t < kRows / 16 ? 0 : kLow), kPRow))
                        : "memory");
-          add_columns(l[2 * t], b0, b1);
-          add_columns(l[2 * t + 1], b2, b3);
+          add_columns(l[2 * (t % (kRows / 16))], b0, b1);
+          add_columns(l[2 * (t % (kRows / 16)) + 1], b2, b3);
         }
       walk_next(w, a);
     }
@@ -1002,11 +1085,21 @@ __device__ __forceinline__ void mma_k32(float (&acc)[4], const uint4& lo, const 
   mma16816(acc, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
+__device__ __forceinline__ void mma16816_f16(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_k32_f16(float (&acc)[4], const uint4& lo, const uint4& hi, const uint4& b) {
+  mma16816_f16(acc, lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+  mma16816_f16(acc, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+}
+
 // Shared memory of a join block (bytes): V rows of the keys, scores or the two parts of the latent
 // sums, weights, per row {reference, cached sum, 1 / sum}.
 struct JoinPlan {
   int keys, s_pitch, p_pitch, a_pitch;               // pitches in elements
-  int v, s, p, row, bytes;
+  int v, s, p, row, bytes;       // (p: the weights in two bf16 parts)
 };
 constexpr int kJoinRows = 16;           // nodes of a join block
 __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
@@ -1019,7 +1112,7 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
   int off = 0;
   j.v = off;   off += j.keys * (kHeadDim + 8) * 2;
   j.s = off;   off += rows * j.s_pitch * 4 > 2 * rows * j.a_pitch * 2 ? rows * j.s_pitch * 4 : 2 * rows * j.a_pitch * 2;
-  j.p = off;   off += rows * j.p_pitch * 2;
+  j.p = off;   off += 2 * rows * j.p_pitch * 2;
   j.row = off; off += rows * 16;
   j.bytes = off;
   return j;
@@ -1059,38 +1152,46 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   }
   // ---- scores of this warp's 16 nodes against every kSplit-th tile of eight keys
   {
-    const uint8_t* img = a.qimg + (static_cast<int64_t>(bh) * a.groups + grp) * (a.rows * 256);
+    const int64_t unit = static_cast<int64_t>(bh) * a.groups + grp;
+    const uint8_t* img = a.qimg + unit * (a.rows * 512);
     const int ir = row0 - grp * kTreeGroup + g;       // row of the image
-    uint4 lo[4], hi[4];
+    uint4 x0[2][4], x1[2][4];                         // rows ir and ir + 8, both parts
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {                     // K values 32 c + 8 q .. of chunk c / 2
+    for (int c = 0; c < 8; ++c) {                     // K values 32 c + 8 q .. of chunk c / 2
       const uint32_t o = (c & 1) * 64 + q * 16;
       const uint8_t* chunk = img + (c >> 1) * a.rows * 128;
-      lo[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset(ir * 128 + o, 128)));
-      hi[c] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((ir + 8) * 128 + o, 128)));
+      x0[c >> 2][c & 3] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset(ir * 128 + o, 128)));
+      x1[c >> 2][c & 3] = __ldcg(reinterpret_cast<const uint4*>(chunk + swizzle_offset((ir + 8) * 128 + o, 128)));
     }
-    const uint8_t* keys = a.khat + static_cast<int64_t>(bh) * a.max_nodes * 256;
+    const float f0 = __ldcg(a.qback + unit * a.rows + ir), f1 = __ldcg(a.qback + unit * a.rows + ir + 8);
+    const uint8_t* keys = a.khat + static_cast<int64_t>(bh) * a.max_nodes * 512;
+    const float* back = a.kback + static_cast<int64_t>(bh) * a.max_nodes;
     uint4 m0 = make_uint4(0, 0, 0, 0), m1 = m0;
     const int r0 = row0 + g;
     if (r0 < n) m0 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0);
     if (r0 + 8 < n) m1 = __ldcg(a.paths + static_cast<int64_t>(b) * a.max_nodes + r0 + 8);
     for (int kt = part; kt < nk16 / 8; kt += kSplit) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      uint4 x[4];
+      uint4 y[2][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        x[c] = 8 * kt + g < nk ? __ldcg(reinterpret_cast<const uint4*>(keys + (8 * kt + g) * 256 + c * 64 + q * 16)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) mma_k32(acc, lo[c], hi[c], x[c]);
+      for (int c = 0; c < 8; ++c)
+        y[c >> 2][c & 3] = 8 * kt + g < nk ? __ldcg(reinterpret_cast<const uint4*>(keys + (8 * kt + g) * 512 + c * 64 + q * 16)) : make_uint4(0, 0, 0, 0);
       const int col = 8 * kt + 2 * q, wd = col >> 5, bit = col & 31;
+      const float k0 = col < nk ? __ldcg(back + col) : 0.f, k1 = col + 1 < nk ? __ldcg(back + col + 1) : 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mma_k32_f16(acc, x0[0][c], x1[0][c], y[0][c]);
+        mma_k32_f16(acc, x0[0][c], x1[0][c], y[1][c]);
+        mma_k32_f16(acc, x0[1][c], x1[1][c], y[0][c]);
+      }
       const uint32_t b0 = (wd == 0 ? m0.x : wd == 1 ? m0.y : wd == 2 ? m0.z : m0.w) >> bit;
       const uint32_t b1 = (wd == 0 ? m1.x : wd == 1 ? m1.y : wd == 2 ? m1.z : m1.w) >> bit;
       float* s0 = ss + g * J.s_pitch + col;
       float* s1 = s0 + 8 * J.s_pitch;
-      s0[0] = b0 & 1 ? acc[0] : -INFINITY;
-      s0[1] = b0 & 2 ? acc[1] : -INFINITY;
-      s1[0] = b1 & 1 ? acc[2] : -INFINITY;
-      s1[1] = b1 & 2 ? acc[3] : -INFINITY;
+      s0[0] = b0 & 1 ? acc[0] * f0 * k0 : -INFINITY;
+      s0[1] = b0 & 2 ? acc[1] * f0 * k1 : -INFINITY;
+      s1[0] = b1 & 1 ? acc[2] * f1 * k0 : -INFINITY;
+      s1[1] = b1 & 2 ? acc[3] * f1 * k1 : -INFINITY;
     }
   }
   // ---- the unit's records: consecutive
@@ -1117,9 +1218,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f, held = 0.f;
     for (int c = x; c < nk16; c += 8) {
-      const __nv_bfloat16 p = __float2bfloat16_rn(row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f);
+      const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f;
+      const __nv_bfloat16 p = __float2bfloat16_rn(w);
       sp[r * J.p_pitch + c] = p;
-      l += __bfloat162float(p);
+      sp[(kRows + r) * J.p_pitch + c] = __float2bfloat16_rn(w - __bfloat162float(p));
+      l += w;
     }
     for (int i = x; i < nrec && row; i += 8) {
       const float4 head = __ldcg(reinterpret_cast<const float4*>(rec + i * next));
@@ -1152,9 +1255,9 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y); x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
       }
     }
-    const uint32_t h0 = pack_bf16(x.x, x.y), h1 = pack_bf16(x.z, x.w);
-    const uint32_t l0 = pack_bf16(x.x - __uint_as_float(h0 << 16), x.y - __uint_as_float(h0 & 0xFFFF0000u));
-    const uint32_t l1 = pack_bf16(x.z - __uint_as_float(h1 << 16), x.w - __uint_as_float(h1 & 0xFFFF0000u));
+    uint32_t h0, h1, l0, l1;
+    split_bf16(x.x, x.y, h0, l0);
+    split_bf16(x.z, x.w, h1, l1);
     *reinterpret_cast<uint2*>(sa + r * J.a_pitch + c) = make_uint2(h0, h1);
     *reinterpret_cast<uint2*>(sa + (kRows + r) * J.a_pitch + c) = make_uint2(l0, l1);
   }
@@ -1182,9 +1285,15 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
     }
   }
   for (int k = 0; k < nk16; k += 16) {
-    const __nv_bfloat16* p = sp + g * J.p_pitch + k + 2 * q;
-    const uint32_t a0 = *reinterpret_cast<const uint32_t*>(p), a1 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch);
-    const uint32_t a2 = *reinterpret_cast<const uint32_t*>(p + 8), a3 = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch + 8);
+    uint32_t x[2][4];                                 // (both parts of the weights)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const __nv_bfloat16* p = sp + (e * kRows + g) * J.p_pitch + k + 2 * q;
+      x[e][0] = *reinterpret_cast<const uint32_t*>(p);
+      x[e][1] = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch);
+      x[e][2] = *reinterpret_cast<const uint32_t*>(p + 8);
+      x[e][3] = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch + 8);
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; t += 2) {
       uint32_t b0, b1, b2, b3;
@@ -1192,8 +1301,11 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
                    : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
                    : "r"(smem_u32(sv + (k + (lane & 15)) * (kHeadDim + 8) + e0 + 8 * t + 8 * (lane >> 4)))
                    : "memory");
-      mma16816(acc[t], a0, a1, a2, a3, b0, b1);
-      mma16816(acc[t + 1], a0, a1, a2, a3, b2, b3);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mma16816(acc[t], x[e][0], x[e][1], x[e][2], x[e][3], b0, b1);
+        mma16816(acc[t + 1], x[e][0], x[e][1], x[e][2], x[e][3], b2, b3);
+      }
     }
   }
   // ---- means, division, one rounding
@@ -1225,9 +1337,9 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   auto al = [](int x) { return (x + 1023) / 1024 * 1024; };
   p->k_stage = al(p->kplan.bytes);
   p->v_stage = al(p->vplan.bytes);
-  // queries, W, two 4 KB bias operands, two buffers of weights, references, barriers, alignment
-  const int refs = 16 * rows * 4;
-  const int fixed = rows * 256 + al(p->kplan.bytes) + 8192 + 2 * kTile * rows * 2 + refs + 1024 + 256 + 768 + 1024;
+  // weights in two parts (two buffers of them for up to 32 nodes); queries (two parts), W, bias, ones
+  const int weights = kTile * rows * 2 * 2 * (rows <= 32 ? 2 : 1), refs = 11 * rows * 4;
+  const int fixed = rows * 512 + al(p->kplan.bytes) + weights + 4096 + 256 + refs + 1024 + 256 + 768 + 1024;
   auto fits = [&](int sk, int sv) { return fixed + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
@@ -1242,10 +1354,10 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->v_ring = off; off += p->SV * p->v_stage;
   p->k_ring = off; off += p->SK * p->k_stage;
   p->w = off;      off += al(p->kplan.bytes);
-  p->q = off;      off += rows * 256;
-  p->p = off;      off += 2 * kTile * rows * 2;
-  p->ones = off;   off += 4096;
+  p->q = off;      off += rows * 512;
+  p->p = off;      off += weights;
   p->mu = off;     off += 4096;
+  p->ones = off;   off += 256;
   p->refs = off;   off += refs;
   p->base = off;   off += 1024;
   p->chunks = off; off += 256;
