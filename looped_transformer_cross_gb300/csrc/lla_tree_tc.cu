@@ -110,6 +110,14 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, volatil
   return wait_on(bar, parity, abort, status);
 }
 
+// True in one lane of the warp, the same at every call.  Products are issued from a block that only this lane
+// enters: one takes 24..110 cycles there (M 128, N 16..128) and 110..145 where the whole warp runs along with
+// the instruction predicated, or where the lane is chosen by its number.
+__device__ __forceinline__ bool elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -674,21 +682,24 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (lane == 0) mbar_arrive(bar(misc->ufull[i & 1]));
       // (chunks of 64 columns, then one of 32, then one of 16)
       const uint32_t d = tmem + (i & 1) * 128, so = kr.slot * kst;
-      umma_bf16_warp(d, d_ones, d_mu, idesc, 0);
+      if (elected()) {
+        umma_bf16(d, d_ones, d_mu, idesc, 0);
 #pragma unroll 1
-      for (int c = 0; c < n64; ++c) {
-        const uint64_t ac = a64 + so + c * 1024, bc = b64 + c * 1024;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) umma_bf16_warp(d, ac + 2 * k, bc + 2 * k, idesc, 1);
+        for (int c = 0; c < n64; ++c) {
+          const uint64_t ac = a64 + so + c * 1024, bc = b64 + c * 1024;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_bf16(d, ac + 2 * k, bc + 2 * k, idesc, 1);
+        }
+        if (k32) {
+          umma_bf16(d, a32 + so, b32, idesc, 1);
+          umma_bf16(d, a32 + so + 2, b32 + 2, idesc, 1);
+        }
+        if (k16) umma_bf16(d, a16 + so, b16, idesc, 1);
+        umma_commit(bar(misc->ufull[i & 1]));
+        umma_commit(bar(misc->kempty[kr.slot]));
+        if (w.t == w.nb - 1) umma_commit(bar(misc->wfree));
       }
-      if (k32) {
-        umma_bf16_warp(d, a32 + so, b32, idesc, 1);
-        umma_bf16_warp(d, a32 + so + 2, b32 + 2, idesc, 1);
-      }
-      if (k16) umma_bf16_warp(d, a16 + so, b16, idesc, 1);
-      umma_commit_warp(bar(misc->ufull[i & 1]));
-      umma_commit_warp(bar(misc->kempty[kr.slot]));
-      if (w.t == w.nb - 1) umma_commit_warp(bar(misc->wfree));
+      __syncwarp();
       kr.next(SK);
       walk_next(w, a);
       if (i + 1 < count) fetch();
@@ -719,16 +730,21 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       // each softmax warp)
       if (kPBuf == 2 && i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
+      if (elected()) {
+        const uint32_t d = tmem + kSCol + sb * kRows, high = tmem + sb * 128;
 #pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t d = tmem + kSCol + sb * kRows, high = tmem + sb * 128 + 16 * k;
-        const uint64_t q_high = d_q + (k >> 2) * (kRows * 128 / 16) + (k & 3) * 2;
-        umma_bf16_ts_warp(d, high, q_high, idesc, k > 0);
-        umma_bf16_ts_warp(d, high, q_high + kRows * 256 / 16, idesc, 1);
-        umma_bf16_ts_warp(d, high + 8, q_high, idesc, 1);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t q_high = d_q + c * (kRows * 128 / 16) + k * 2;
+            umma_bf16_ts(d, high + 64 * c + 16 * k, q_high, idesc, c + k > 0);
+            umma_bf16_ts(d, high + 64 * c + 16 * k, q_high + kRows * 256 / 16, idesc, 1);
+            umma_bf16_ts(d, high + 64 * c + 16 * k + 8, q_high, idesc, 1);
+          }
+        umma_commit(bar(misc->sfull[sb]));
+        if (w.t == w.nb - 1) umma_commit(bar(misc->qfree));
       }
-      umma_commit_warp(bar(misc->sfull[sb]));
-      if (w.t == w.nb - 1) umma_commit_warp(bar(misc->qfree));
+      __syncwarp();
       walk_next(w, a);
     }
     products_done(misc->done[1]);
@@ -772,17 +788,20 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       tc_fence_after();
       const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j % kPBuf) * (kPTile / 16);
       const uint32_t sum = !(j == 0 || w.t == 0);     // a unit's first product starts the sum
+      if (elected()) {
 #pragma unroll 1
-      for (int blk = 0; blk < blocks; ++blk)
-#pragma unroll 1
-        for (int k = 0; k < steps; ++k) {
-          // (rows is a power of two; a whole tile is one region)
-          const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
-          umma_bf16_warp(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
-          if (!kBoth) umma_bf16_warp(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + kLow / 16 + k * kPRow, idesc, 1);
-        }
-      umma_commit_warp(bar(misc->vdone[j & 1]));
-      umma_commit_warp(bar(misc->vempty[vr.slot]));
+        for (int blk = 0; blk < blocks; ++blk)
+#pragma unroll 2
+          for (int k = 0; k < steps; ++k) {
+            // (rows is a power of two; a whole tile is one region)
+            const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
+            umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
+            if (!kBoth) umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + kLow / 16 + k * kPRow, idesc, 1);
+          }
+        umma_commit(bar(misc->vdone[j & 1]));
+        umma_commit(bar(misc->vempty[vr.slot]));
+      }
+      __syncwarp();
       walk_next(w, a);
     }
     products_done(misc->done[2]);
