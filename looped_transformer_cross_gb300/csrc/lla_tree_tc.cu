@@ -145,12 +145,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ void split2(uint64_t x, uint64_t minus, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& hi, uint32_t& lo) {
   float x0, x1;
   unpack2(x, x0, x1);
   hi = pack_f16(x0, x1);
-  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  unpack2(fma2(pair2(h.x, h.y), minus, x), x0, x1);
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.f16 %0, l, %5, %3;\n\tfma.rn.f32.f16 %1, h, %5, %4;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "r"(hi), "f"(x0), "f"(x1), "h"(static_cast<unsigned short>(0xBC00)));
   lo = pack_f16(x0, x1);
 }
 __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
@@ -841,8 +842,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             const int f = 8 * g + k + e;
             const uint64_t c = fma2(mul2(sb, sl[f]), minus, mul2(cb, cl[f])), sn = fma2(sb, cl[f], mul2(cb, sl[f]));
             const uint64_t x0 = pair2(u0[2 * (k + e)], u0[2 * (k + e) + 1]), x1 = pair2(u1[2 * (k + e)], u1[2 * (k + e) + 1]);
-            split2(fma2(mul2(x1, sn), minus, mul2(x0, c)), minus, y0[k + e], y0[8 + k + e]);
-            split2(fma2(x0, sn, mul2(x1, c)), minus, y1[k + e], y1[8 + k + e]);
+            split2(fma2(mul2(x1, sn), minus, mul2(x0, c)), y0[k + e], y0[8 + k + e]);
+            split2(fma2(x0, sn, mul2(x1, c)), y1[k + e], y1[8 + k + e]);
           }
         }
         tmem_st_x16(t_u + 16 * g, y0);
@@ -1004,7 +1005,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
               const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
               const uint32_t h = pack_bf16(p0, p1);
               x[k + e] = h;
-              unpack2(fma2(pair2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)), minus, pair2(p0, p1)), d0, d1);
+              asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %5, %3;\n\tfma.rn.f32.bf16 %1, h, %5, %4;\n\t}"
+                  : "=f"(d0), "=f"(d1)
+                  : "r"(h), "f"(p0), "f"(p1), "h"(static_cast<unsigned short>(0xBF80)));
               y[k + e] = pack_bf16(d0, d1);
             }
           }
