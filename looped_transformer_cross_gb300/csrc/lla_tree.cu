@@ -413,7 +413,7 @@ struct View {
 // Shapes of the tensor-core kernel: those whose operands fit for any number of nodes.
 bool tensor_path(const lla_dims* d) {
   TreePlan p;
-  return d->dtype == LLA_BF16 && make_tree_plan(d->r_k, d->r_v, kTreeGroup, &p);
+  return d->dtype == LLA_BF16 && make_tree_plan(d->r_k, d->r_v, tree_group(d->r_v), &p);
 }
 
 // Workspace: status word; tensor-core kernel: the plan, the mu and the query operands; the records.
@@ -426,8 +426,8 @@ struct TreeWs {
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
   TreeWs w{};
   const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(B) * d->H);
-  const int groups = (max_nodes + kTreeGroup - 1) / kTreeGroup;
-  const size_t rec = static_cast<size_t>(tensor ? std::min(max_nodes, kTreeGroup) : max_nodes) * (d->r_v + kTreeHead) * 4;
+  const int group = tree_group(d->r_v), groups = (max_nodes + group - 1) / group;
+  const size_t rec = static_cast<size_t>(tensor ? std::min(max_nodes, group) : max_nodes) * (d->r_v + kTreeHead) * 4;
   auto al = [](size_t x) { return (x + 255) / 256 * 256; };
   if (tensor) {
     const int64_t most = units * groups * std::max<int64_t>(1, (L_max + kTile - 1) / kTile);
@@ -436,8 +436,8 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
     w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
-    w.qback = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 512;
-    w.khat = al(w.qback + static_cast<size_t>(units * groups) * tree_rows(max_nodes) * 4);
+    w.qback = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 512;
+    w.khat = al(w.qback + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 4);
     w.kback = w.khat + static_cast<size_t>(units) * max_nodes * 512;
     w.paths = al(w.kback + static_cast<size_t>(units) * max_nodes * 4);
     w.records = al(w.paths + static_cast<size_t>(std::max(B, 1)) * max_nodes * 16);
@@ -540,7 +540,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
   TreeArgs a{};
-  const bool tensor = tensor_path(dims) && make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes), &a.plan);
+  const bool tensor = tensor_path(dims) && make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes, dims->r_v), &a.plan);
   const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms, tensor);
   if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
   a.B = tree->B;
@@ -589,10 +589,11 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   const bool bf16 = dims->dtype == LLA_BF16;
   if (tensor) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.groups = (a.max_nodes + kTreeGroup - 1) / kTreeGroup;
-    a.rows = tree_rows(a.max_nodes);
+    a.group = tree_group(a.r_v);
+    a.groups = (a.max_nodes + a.group - 1) / a.group;
+    a.rows = tree_rows(a.max_nodes, a.r_v);
     a.v_whole = a.r_v % 32 == 0;
-    a.rec_rows = std::min(a.max_nodes, kTreeGroup);
+    a.rec_rows = std::min(a.max_nodes, a.group);
     a.grid = w.grid;
     a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);

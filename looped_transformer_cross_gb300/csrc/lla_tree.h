@@ -8,7 +8,6 @@
 namespace lla {
 
 constexpr int kTreeMaxNodes = LLA_TREE_MAX_NODES;
-constexpr int kTreeGroup = 64;          // nodes of a unit of the tensor-core kernel
 constexpr int kTreeHead = 8;            // a record row: {reference, up to four sums, -, -, -, acc[r_v]}
 constexpr int kTreePlainRows = 32;      // nodes of a plain block
 constexpr int kTreePlainTile = 32;      // cached tokens it takes at a time
@@ -61,10 +60,10 @@ struct TreeArgs {
   int rec_rows, splits, finish_rows;
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
   float* w_turned;                   // plain kernel: [H][r_k][128]
-  // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of 64 nodes, and record
+  // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of `group` nodes, and record
   // unit + CTA belongs to every (unit, CTA) that share a tile
   int v_whole;                       // r_v a multiple of 32: V by maps.v4
-  int groups, rows, grid;            // blocks of nodes a sequence may have, nodes S has room for, CTAs
+  int group, groups, rows, grid;     // nodes of a block, blocks a sequence may have, nodes S has room for, CTAs
   int32_t* tile_start;               // [B + 1]: tiles of one head before sequence b
   int4* cta_start;                   // [grid]: first (sequence, head, tile), number of tiles
   uint8_t* qimg;                     // [units][rows * 512] query operands, rows scaled by powers of two
@@ -95,8 +94,10 @@ __device__ __forceinline__ int tree_cached(const TreeArgs& a, int b, bool flag) 
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
-// Nodes that S has room for in calls of up to max_nodes a sequence.
-inline int tree_rows(int max_nodes) { return max_nodes <= 16 ? 16 : max_nodes <= 32 ? 32 : 64; }
+// The most nodes of a unit (TMEM has 192 columns left for the sums of 64 nodes), and the nodes that S has room
+// for in calls of up to max_nodes a sequence.
+inline int tree_group(int r_v) { return r_v <= 192 ? 64 : 32; }
+inline int tree_rows(int max_nodes, int r_v) { return max_nodes <= 16 ? 16 : max_nodes <= 32 ? 32 : tree_group(r_v); }
 // False where the operands do not fit in shared memory.
 bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p);
 cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s);

@@ -71,7 +71,7 @@ __device__ __forceinline__ void walk_load(Walk& w, const TreeArgs& a) {
   int first;
   const int n = tree_nodes(a, w.b, first, false);
   w.L = tree_cached(a, w.b, false);
-  w.ng = (n + kTreeGroup - 1) / kTreeGroup;
+  w.ng = (n + a.group - 1) / a.group;
   w.nb = n > 0 ? (w.L + kTile - 1) / kTile : 0;
 }
 
@@ -169,12 +169,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// acc += ones (16 x 16) times a 16 x 8 block of bf16 values: every row of acc gets the columns' sums.
-__device__ __forceinline__ void add_columns(float (&acc)[4], uint32_t b0, uint32_t b1) {
+// acc += a 16 x 16 block of bf16 values times ones (16 x 8): every column of acc gets the rows' sums.
+__device__ __forceinline__ void add_rows(float (&acc)[4], const uint32_t (&x)[4]) {
   const uint32_t ones = 0x3F803F80u;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %4, %4, %4}, {%5, %6}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %8}, {%0, %1, %2, %3};"
       : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
-      : "r"(ones), "r"(b0), "r"(b1));
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(ones));
 }
 // Store 8 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -314,13 +314,13 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     const int bh = blockIdx.x / a.groups, g = blockIdx.x - bh * a.groups;
     const int b = bh / a.H, h = bh - b * a.H;
     int first;
-    const int n = tree_nodes(a, b, first, false) - g * kTreeGroup;
+    const int n = tree_nodes(a, b, first, false) - g * a.group;
     if (n <= 0) return;
-    first += g * kTreeGroup;
+    first += g * a.group;
     uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 512;
     float* back_q = a.qback + static_cast<int64_t>(blockIdx.x) * a.rows;
-    uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup) * 512;
-    float* back_k = a.kback + static_cast<int64_t>(bh) * a.max_nodes + g * kTreeGroup;
+    uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * a.group) * 512;
+    float* back_k = a.kback + static_cast<int64_t>(bh) * a.max_nodes + g * a.group;
     for (int i = tid; i < a.rows * 16; i += kPrepThreads) {      // (whole warps: rows is a multiple of 16)
       const bool key = i >= a.rows * 8;
       const int it = key ? i - a.rows * 8 : i, r = it >> 3, f0 = (it & 7) * 8;
@@ -484,15 +484,16 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
 template <int kPage, int kRows>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ TreeMaps maps) {
-  // The two parts of the weights: up to 32 nodes side by side in a token's row, one product for both (into columns
-  // of their own); 64 nodes one tile after the other, two products into the same columns, and one buffer of
-  // both (shared memory, TMEM)
+  // Up to 32 nodes (kBoth): D is r_v x nodes in blocks of 128 rows, B = P with the two parts side by side in a
+  // token's row, into columns of their own.  64 nodes: D is its transpose, A = P^T with both parts' nodes one below
+  // the other, 128 rows (8 products a tile where the other form takes 16 of N = 128 or 32 of N = 64, with
+  // 109 and 78 cycles each against 46 + r_v / 2), and there is one buffer of P (shared memory) and of S (TMEM).
   constexpr bool kBoth = kRows <= 32;
-  constexpr int kPBuf = kBoth ? 2 : 1, kDCols = kBoth ? 2 * kRows : kRows;
-  constexpr int kDCol = kSCol + 2 * kRows;
-  static_assert(kDCol + 2 * kDCols <= 512, "TMEM columns");
-  constexpr uint32_t kPRow = kDCols * 2;              // bytes of a token's weights
-  constexpr uint32_t kPTile = kTile * kPRow * (kBoth ? 1 : 2), kLow = kBoth ? kRows * 2 : kTile * kPRow;     // (the lower parts' place)
+  constexpr int kSBuf = kBoth ? 2 : 1, kPBuf = kBoth ? 2 : 1, kDCols = 2 * kRows;
+  constexpr int kDCol = kSCol + kSBuf * kRows;        // (64 nodes: r_v columns, up to 192)
+  static_assert(kDCol + (kBoth ? 2 * kDCols : 192) <= 512, "TMEM columns");
+  constexpr uint32_t kPRow = kBoth ? kRows * 4 : kRows * 2;        // bytes of a token's weights
+  constexpr uint32_t kPTile = kTile * kRows * 4, kLow = kBoth ? kRows * 2 : kTile * kPRow;     // (the lower parts' place)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const TreePlan& P = a.plan;
@@ -713,7 +714,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint64_t d_q = umma_desc(sbase + P.q, 16, 1024, kSw128);
     int unit = -1;
     for (int i = 0; i < count; ++i) {
-      const int sb = i & 1;
+      const int sb = i % kSBuf;
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->qfree, unit)) break;
         ++unit;
@@ -725,14 +726,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         __syncwarp();
         if (!wait(misc->qfull, unit)) break;
       }
-      if (!wait(misc->rfull[sb], i >> 1)) break;
-      if (i >= 2 && !wait(misc->sfree[sb], (i - 2) >> 1)) break;
+      if (!wait(misc->rfull[i & 1], i >> 1)) break;
+      if (i >= kSBuf && !wait(misc->sfree[(i - kSBuf) & 1], (i - kSBuf) >> 1)) break;
       // the weights of tile i - 2 have been read: those of S(i) take their place (one wait here instead of one for
       // each softmax warp)
       if (kPBuf == 2 && i >= 2 && !wait(misc->vdone[i & 1], (i - 2) >> 1)) break;
       tc_fence_after();
       if (elected()) {
-        const uint32_t d = tmem + kSCol + sb * kRows, high = tmem + sb * 128;
+        const uint32_t d = tmem + kSCol + sb * kRows, high = tmem + (i & 1) * 128;
 #pragma unroll 1
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -742,7 +743,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             umma_bf16_ts(d, high + 64 * c + 16 * k, q_high + kRows * 256 / 16, idesc, 1);
             umma_bf16_ts(d, high + 64 * c + 16 * k + 8, q_high, idesc, 1);
           }
-        umma_commit(bar(misc->sfull[sb]));
+        umma_commit(bar(misc->sfull[i & 1]));
         if (w.t == w.nb - 1) umma_commit(bar(misc->qfree));
       }
       __syncwarp();
@@ -754,7 +755,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== D += C_v^T P
     // (two blocks of 128 rows of r_v; rows past r_v read whatever follows the tile in shared memory and
     // are not looked at)
-    const uint32_t idesc = umma_idesc_bf16(128, kDCols, true, true);
+    const uint32_t idesc = umma_idesc_bf16(128, kBoth ? kDCols : a.r_v, true, true);
     // V: chunks of 32 columns, their 128 token rows of 64 bytes one after the other; with one copy per piece of
     // 8..64 tokens, piece by piece, each [chunk][piece rows]
     const bool by_piece = kPage == 2 && a.v_whole;
@@ -763,9 +764,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint64_t d_v = umma_desc(sbase + P.v_ring, rows * 64, rows >= 16 ? 512 : region, kSw64);
     const uint32_t block_step = 4 * rows * 64 / 16;
     const int log_rows = 31 - __clz(rows);
-    const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));
+    const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));     // (64 nodes: lower parts a tile on)
     const uint32_t vst = static_cast<uint32_t>(P.v_stage) >> 4;
-    const int SV = P.SV, blocks = P.blocks;
+    const int SV = P.SV, blocks = kBoth ? P.blocks : 1;
     Ring vr;
     for (int j = 0; j < count; ++j, vr.next(SV)) {
       if (!wait(misc->vfull[vr.slot], vr.phase)) break;
@@ -796,8 +797,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           for (int k = 0; k < steps; ++k) {
             // (rows is a power of two; a whole tile is one region)
             const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
-            umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
-            if (!kBoth) umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + kLow / 16 + k * kPRow, idesc, 1);
+            if (kBoth) umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
+            else umma_bf16(tmem + kDCol, b0 + k * kPRow, a0 + o, idesc, k > 0 || sum);
           }
         umma_commit(bar(misc->vdone[j & 1]));
         umma_commit(bar(misc->vempty[vr.slot]));
@@ -868,7 +869,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     float* minus_ref = scale + kRows;
     float* factor = minus_ref + kRows;
     float* maxima = factor + kRows;
-    const int blocks = P.blocks;
     int votes = 0, moves = 0;
     auto vote = [&]() {
       __syncwarp();
@@ -876,9 +876,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return wait(misc->vote, votes++);
     };
     const uint64_t minus = pair2(-1.f, -1.f);
-    // sums of the weights over this warp's tokens, as the accumulators of ones (16 x 16) times P (16 tokens x
-    // 8 nodes): l[t][0..1] is nodes 8 t + 2 (lane mod 4) and the next
-    float l[kRows / 8][4];
+    // sums of the weights over this warp's tokens, as the accumulators of P^T (16 nodes x 16 tokens) times
+    // ones: l[t][0] is node 16 t + lane / 4, l[t][2] the eighth after it
+    float l[kRows / 16][4];
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
     // is higher, or if it is the unit's first
@@ -920,7 +920,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!wait(misc->vdone[last & 1], last >> 1)) return false;
       tc_fence_after();
       int first;
-      const int n = min(kTreeGroup, tree_nodes(a, cur_b, first, false) - cur_g * kTreeGroup);
+      const int n = min(a.group, tree_nodes(a, cur_b, first, false) - cur_g * a.group);
       const int64_t slot = (static_cast<int64_t>(cur_b) * a.H + cur_h) * a.groups + cur_g + blockIdx.x;
       const int stride = a.r_v + kTreeHead;
       float* rec = a.records + slot * a.rec_rows * stride;
@@ -928,38 +928,54 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       for (int j = 0; j < kMine; ++j)
         if (quad == 0 && lane + 32 * j < n) rec[(lane + 32 * j) * stride] = refs[j];
 #pragma unroll
-      for (int t = 0; t < kRows / 8; ++t)
+      for (int t = 0; t < kRows / 16; ++t)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int c = 8 * t + 2 * (lane & 3) + e;
-          if (lane < 4 && c < n) rec[c * stride + 1 + quad] = l[t][e];
+          const int c = 16 * t + 8 * e + (lane >> 2);
+          if ((lane & 3) == 0 && c < n) rec[c * stride + 1 + quad] = l[t][2 * e];
         }
-      for (int blk = 0; blk < blocks; ++blk) {
-        const int r = blk * 128 + row;
+      if constexpr (kBoth) {
+        for (int blk = 0; blk < P.blocks; ++blk) {
+          const int r = blk * 128 + row;
 #pragma unroll 1
-        for (int c = 0; c < n; c += 16) {
-          float v[16];
-          tmem_ld_x16(lanes + kDCol + blk * kDCols + c, v);
-          if constexpr (kBoth) {
-            float low[16];
+          for (int c = 0; c < n; c += 16) {
+            float v[16], low[16];
+            tmem_ld_x16(lanes + kDCol + blk * kDCols + c, v);
             tmem_ld_x16(lanes + kDCol + blk * kDCols + kRows + c, low);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] += low[k];
-          } else {
-            tmem_wait_ld();
+            for (int k = 0; k < 16; ++k)
+              if (c + k < n && r < a.r_v) rec[(c + k) * stride + kTreeHead + r] = v[k] + low[k];
           }
+        }
+      } else {
+        // lanes are nodes: the lower parts' sums reach the upper parts' warps through the weights' memory, which
+        // has been read, 16 columns at a time
+        float* pass = reinterpret_cast<float*>(sm + P.p) + (row & 63) * 20;
+#pragma unroll 1
+        for (int c = 0; c < a.r_v; c += 16) {
+          float v[16];
+          tmem_ld_x16(lanes + kDCol + c, v);
+          tmem_wait_ld();
+          if (quad >= 2) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (c + k < n && r < a.r_v) rec[(c + k) * stride + kTreeHead + r] = v[k];
+            for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(pass + (c & 16) * 80 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+          }
+          if (!vote()) return false;                   // (two places in turn: one vote a step keeps them apart)
+          if (quad < 2 && row < n) {
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 y = *reinterpret_cast<const float4*>(pass + (c & 16) * 80 + k);
+              *reinterpret_cast<float4*>(rec + row * stride + kTreeHead + c + k) = make_float4(v[k] + y.x, v[k + 1] + y.y, v[k + 2] + y.z, v[k + 3] + y.w);
+            }
+          }
         }
       }
       tc_fence_before();
       return true;
     };
     for (int i = 0; i <= count && count > 0; ++i) {
-      const int sb = i & 1;
-      const uint32_t t_s = lanes + kSCol + sb * kRows;
+      const uint32_t t_s = lanes + kSCol + i % kSBuf * kRows;
       const bool fresh = i == 0 || w.t == 0;
       if (fresh && i < count) {
         const float* from = a.qback + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * kRows;
@@ -970,29 +986,28 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!finish(i - 1)) break;
         cur_b = w.b; cur_h = w.h; cur_g = w.g;
       }
-      if (i == count || !wait(misc->sfull[sb], i >> 1)) break;
+      if (i == count || !wait(misc->sfull[i & 1], i >> 1)) break;
       tc_fence_after();
       const bool live = w.t * kTile + row < w.L, partial = (w.t + 1) * kTile > w.L;
       uint8_t* p = sm + P.p + (i % kPBuf) * kPTile;
       if (fresh) {
         if (!move(t_s, live, true)) break;
 #pragma unroll
-        for (int t = 0; t < kRows / 8; ++t) l[t][0] = l[t][1] = l[t][2] = l[t][3] = 0.f;
+        for (int t = 0; t < kRows / 16; ++t) l[t][0] = l[t][1] = l[t][2] = l[t][3] = 0.f;
       }
-      if (kPBuf == 1 && i > 0 && !wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;     // the last weights have been read
-      // Weights, in two bf16 parts as the product takes them (a token past the end has none).  Where a score is too
-      // far above its reference, the references move and the weights are made again.
+      // Weights, in two bf16 parts as the product takes them.  Where a score is too far above its reference, the
+      // references move and the weights are made again.
       bool settled = fresh, ok = true;
+      uint32_t x[kRows / 2], y[kRows / 2];
       while (true) {
         float top = -INFINITY;
-        constexpr int kCols = kRows < 32 ? kRows : 32;  // columns at a time
+        constexpr int kCols = kRows == 32 ? 32 : 16;    // columns at a time (64 nodes: registers)
 #pragma unroll
         for (int c = 0; c < kRows; c += kCols) {
           float s[kCols];
           if constexpr (kCols == 32) tmem_ld_x32(t_s + c, s);
           else tmem_ld_x16(t_s + c, s);
           tmem_wait_ld();
-          uint32_t x[kCols / 2], y[kCols / 2];
 #pragma unroll
           for (int k = 0; k < kCols / 2; k += 2) {
             const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + c + 2 * k);
@@ -1004,25 +1019,12 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
               top = fmaxf(top, fmaxf(d0, d1));
               const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
               const uint32_t h = pack_bf16(p0, p1);
-              x[k + e] = h;
+              x[c / 2 + k + e] = h;
               asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %5, %3;\n\tfma.rn.f32.bf16 %1, h, %5, %4;\n\t}"
                   : "=f"(d0), "=f"(d1)
                   : "r"(h), "f"(p0), "f"(p1), "h"(static_cast<unsigned short>(0xBF80)));
-              y[k + e] = pack_bf16(d0, d1);
+              y[c / 2 + k + e] = pack_bf16(d0, d1);
             }
-          }
-#pragma unroll
-          for (int k = 0; k < kCols / 2; k += 4) {
-            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + (c + 2 * k) * 2, kPRow)) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + (c + 2 * k) * 2 + kLow, kPRow)) =
-                make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-          }
-        }
-        if (partial && !live) {
-#pragma unroll 1
-          for (int c = 0; c < kRows; c += 8) {
-            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2, kPRow)) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + c * 2 + kLow, kPRow)) = make_uint4(0, 0, 0, 0);
           }
         }
         if (settled) break;
@@ -1034,46 +1036,63 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         ok = move(t_s, live, false) && wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1);
         if (!ok) break;
         tc_fence_after();
+        const int columns = kBoth ? P.blocks * kDCols : a.r_v;
 #pragma unroll 1
-        for (int c = 0; c < blocks * kDCols; c += 8) {
+        for (int c = 0; c < columns; c += 8) {
           float v[8];
           tmem_ld_x8(lanes + kDCol + c, v);
           tmem_wait_ld();
-          uint32_t x[8];
+          uint32_t z[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(v[k] * factor[(c + k) % kRows]);
-          tmem_st_x8(lanes + kDCol + c, x);
+          for (int k = 0; k < 8; ++k) z[k] = __float_as_uint(v[k] * factor[(kBoth ? c + k : row) % kRows]);
+          tmem_st_x8(lanes + kDCol + c, z);
         }
         tmem_wait_st();
 #pragma unroll
-        for (int t = 0; t < kRows / 8; ++t) {
-          const float2 f = *reinterpret_cast<const float2*>(factor + 8 * t + 2 * (lane & 3));
-          l[t][0] *= f.x;
-          l[t][1] *= f.y;
+        for (int t = 0; t < kRows / 16; ++t) {
+          l[t][0] *= factor[16 * t + (lane >> 2)];
+          l[t][2] *= factor[16 * t + 8 + (lane >> 2)];
         }
       }
       if (!ok) break;
+      if constexpr (kPBuf == 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(misc->sfree[i & 1]));
+        if (i > 0 && !wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;     // the last weights have been read
+      }
+      if (partial) {                                    // a token past the end has none
+#pragma unroll
+        for (int k = 0; k < kRows / 2; ++k) {
+          x[k] = live ? x[k] : 0u;
+          y[k] = live ? y[k] : 0u;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kRows / 2; k += 4) {
+        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + 4 * k, kPRow)) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + 4 * k + kLow, kPRow)) = make_uint4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+      }
       tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(misc->pfull[i & 1]));
-        mbar_arrive(bar(misc->sfree[sb]));
+        if (kPBuf == 2) mbar_arrive(bar(misc->sfree[i & 1]));
       }
       // the sums add up both parts, once the products have them
 #pragma unroll
       for (int t = 0; t < kRows / 8; ++t)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          // four 8 x 8 blocks: tokens 0..7 and 8..15 of 16 by nodes 0..7 and 8..15, lane = block * 8 + token
-          const int tok = 32 * quad + 16 * half + (lane & 15), col = 16 * (t % (kRows / 16)) + 8 * (lane >> 4);
-          uint32_t b0, b1, b2, b3;
+          // four 8 x 8 blocks: nodes 0..7 and 8..15 by tokens 0..7, then by tokens 8..15, lane = block * 8 + token
+          const int tok = 32 * quad + 16 * half + (lane & 7) + 8 * (lane >> 4), col = 16 * (t % (kRows / 16)) + (lane & 8);
+          uint32_t z[4];
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                       : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3])
                        : "r"(smem_u32(p) + swizzle_offset(tok * kPRow + col * 2 + (t < kRows / 16 ? 0 : kLow), kPRow))
                        : "memory");
-          add_columns(l[2 * (t % (kRows / 16))], b0, b1);
-          add_columns(l[2 * (t % (kRows / 16)) + 1], b2, b3);
+          add_rows(l[t % (kRows / 16)], z);
         }
       walk_next(w, a);
     }
@@ -1159,7 +1178,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
   float4* srow = reinterpret_cast<float4*>(sm + J.row);
   const int tid = threadIdx.x, lane = tid & 31, part = tid >> 5, g = lane >> 2, q = lane & 3;
-  const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, row0 = blockIdx.y * kRows, grp = row0 / kTreeGroup;
+  const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, row0 = blockIdx.y * kRows, grp = row0 / a.group;
   int first;
   const int n = tree_nodes(a, b, first, false);
   if (row0 >= n) return;
@@ -1176,7 +1195,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   {
     const int64_t unit = static_cast<int64_t>(bh) * a.groups + grp;
     const uint8_t* img = a.qimg + unit * (a.rows * 512);
-    const int ir = row0 - grp * kTreeGroup + g;       // row of the image
+    const int ir = row0 - grp * a.group + g;       // row of the image
     uint4 x0[2][4], x1[2][4];                         // rows ir and ir + 8, both parts
 #pragma unroll
     for (int c = 0; c < 8; ++c) {                     // K values 32 c + 8 q .. of chunk c / 2
@@ -1218,14 +1237,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   }
   // ---- the unit's records: consecutive
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int ng = (n + kTreeGroup - 1) / kTreeGroup, stride = a.r_v + kTreeHead;
+  const int ng = (n + a.group - 1) / a.group, stride = a.r_v + kTreeHead;
   const uint32_t t0 = __ldcg(a.tile_start + b), nb = (__ldcg(a.tile_start + b + 1) - t0) / ng;
   const uint32_t total = static_cast<uint32_t>(__ldcg(a.tile_start + a.B)) * a.H;     // (below 2^31)
   const uint32_t share = max(1u, (total + a.grid - 1) / a.grid);
   const uint32_t f0 = t0 * a.H + (h * ng + grp) * nb, c0 = f0 / share;
   const int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
   const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
-  const float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * kTreeGroup) * stride;
+  const float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * a.group) * stride;
   __syncthreads();
 
   // ---- reference, weights and sums: eight lanes a row
