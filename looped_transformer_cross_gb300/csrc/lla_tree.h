@@ -94,9 +94,9 @@ __device__ __forceinline__ int tree_cached(const TreeArgs& a, int b, bool flag) 
   return L < 0 ? 0 : (L > a.L_max ? static_cast<int>(a.L_max) : L);
 }
 
-// The most nodes of a unit (TMEM has 192 columns left for the sums of 64 nodes), and the nodes that S has room
+// The most nodes of a unit (TMEM has 192 columns left for the sums of 64 nodes, 16 of them for the weights'), and the nodes that S has room
 // for in calls of up to max_nodes a sequence.
-inline int tree_group(int r_v) { return r_v <= 192 ? 64 : 32; }
+inline int tree_group(int r_v) { return r_v <= 176 ? 64 : 32; }
 inline int tree_rows(int max_nodes, int r_v) { return max_nodes <= 16 ? 16 : max_nodes <= 32 ? 32 : tree_group(r_v); }
 // False where the operands do not fit in shared memory.
 bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p);

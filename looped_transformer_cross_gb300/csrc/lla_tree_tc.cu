@@ -130,6 +130,11 @@ __device__ __forceinline__ uint64_t pair2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ void unpack2(uint64_t x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x)); }
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -168,13 +173,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-// acc += a 16 x 16 block of bf16 values times ones (16 x 8): every column of acc gets the rows' sums.
-__device__ __forceinline__ void add_rows(float (&acc)[4], const uint32_t (&x)[4]) {
-  const uint32_t ones = 0x3F803F80u;
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %8}, {%0, %1, %2, %3};"
-      : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
-      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(ones));
 }
 // Store 8 consecutive 32-bit columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
@@ -490,7 +488,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
   // 109 and 78 cycles each against 46 + r_v / 2), and there is one buffer of P (shared memory) and of S (TMEM).
   constexpr bool kBoth = kRows <= 32;
   constexpr int kSBuf = kBoth ? 2 : 1, kPBuf = kBoth ? 2 : 1, kDCols = 2 * kRows;
-  constexpr int kDCol = kSCol + kSBuf * kRows;        // (64 nodes: r_v columns, up to 192)
+  constexpr int kDCol = kSCol + kSBuf * kRows;        // (64 nodes: r_v columns, up to 176, and 16 of the weights' sums)
   static_assert(kDCol + (kBoth ? 2 * kDCols : 192) <= 512, "TMEM columns");
   constexpr uint32_t kPRow = kBoth ? kRows * 4 : kRows * 2;        // bytes of a token's weights
   constexpr uint32_t kPTile = kTile * kRows * 4, kLow = kBoth ? kRows * 2 : kTile * kPRow;     // (the lower parts' place)
@@ -539,6 +537,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32, 32)) = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
       *reinterpret_cast<uint4*>(sm + P.ones + swizzle_offset(r * 32 + 16, 32)) = make_uint4(0, 0, 0, 0);
     }
+    // and ones that sum weights
+    if (!kBoth && r < 16) *reinterpret_cast<uint4*>(sm + P.ones + 256 + r * 16) = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -763,6 +763,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const uint32_t region = rows * nv * 64;
     const uint64_t d_v = umma_desc(sbase + P.v_ring, rows * 64, rows >= 16 ? 512 : region, kSw64);
     const uint32_t block_step = 4 * rows * 64 / 16;
+    const uint32_t idesc_sum = umma_idesc_bf16(128, 16, true, false);
+    const uint64_t d_sum = umma_desc(sbase + P.ones + 256, 16, 0, kSw32);
     const int log_rows = 31 - __clz(rows);
     const uint64_t d_p = umma_desc(sbase + P.p, kTile * kPRow, 8 * kPRow, sw_mode_for_row_bytes(kPRow));     // (64 nodes: lower parts a tile on)
     const uint32_t vst = static_cast<uint32_t>(P.v_stage) >> 4;
@@ -798,7 +800,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             // (rows is a power of two; a whole tile is one region)
             const uint32_t o = (16 * k >> log_rows) * (region / 16) + (16 * k & (rows - 1)) * 4;
             if (kBoth) umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
-            else umma_bf16(tmem + kDCol, b0 + k * kPRow, a0 + o, idesc, k > 0 || sum);
+            else {
+              umma_bf16(tmem + kDCol, b0 + k * kPRow, a0 + o, idesc, k > 0 || sum);
+              umma_bf16(tmem + kDCol + a.r_v, b0 + k * kPRow, d_sum, idesc_sum, k > 0 || sum);
+            }
           }
         umma_commit(bar(misc->vdone[j & 1]));
         umma_commit(bar(misc->vempty[vr.slot]));
@@ -876,9 +881,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return wait(misc->vote, votes++);
     };
     const uint64_t minus = pair2(-1.f, -1.f);
-    // sums of the weights over this warp's tokens, as the accumulators of P^T (16 nodes x 16 tokens) times
-    // ones: l[t][0] is node 16 t + lane / 4, l[t][2] the eighth after it
-    float l[kRows / 16][4];
+    // sums of the weights of this lane's tokens, nodes by twos (64 nodes: D has them)
+    uint64_t l[kBoth ? kRows / 2 : 1];
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
     // is higher, or if it is the unit's first
@@ -927,14 +931,23 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
       for (int j = 0; j < kMine; ++j)
         if (quad == 0 && lane + 32 * j < n) rec[(lane + 32 * j) * stride] = refs[j];
-#pragma unroll
-      for (int t = 0; t < kRows / 16; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = 16 * t + 8 * e + (lane >> 2);
-          if ((lane & 3) == 0 && c < n) rec[c * stride + 1 + quad] = l[t][2 * e];
-        }
       if constexpr (kBoth) {
+        // the lanes' sums through the warp's own rows of the weights, which have been read
+        float* own = reinterpret_cast<float*>(sm + P.p + (last % kPBuf) * kPTile + quad * (32 * kPRow));
+#pragma unroll
+        for (int k = 0; k < kRows / 2; ++k) {
+          float l0, l1;
+          unpack2(l[k], l0, l1);
+          own[64 * k + lane] = l0;
+          own[64 * k + 32 + lane] = l1;
+        }
+        __syncwarp();
+        if (lane < n) {
+          float sum = 0.f;
+#pragma unroll 4
+          for (int k = 0; k < 32; ++k) sum += own[32 * lane + ((k + lane) & 31)];
+          rec[lane * stride + 1 + quad] = sum;
+        }
         for (int blk = 0; blk < P.blocks; ++blk) {
           const int r = blk * 128 + row;
 #pragma unroll 1
@@ -953,7 +966,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         // has been read, 16 columns at a time
         float* pass = reinterpret_cast<float*>(sm + P.p) + (row & 63) * 20;
 #pragma unroll 1
-        for (int c = 0; c < a.r_v; c += 16) {
+        for (int c = 0; c <= a.r_v; c += 16) {
           float v[16];
           tmem_ld_x16(lanes + kDCol + c, v);
           tmem_wait_ld();
@@ -966,7 +979,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
             for (int k = 0; k < 16; k += 4) {
               const float4 y = *reinterpret_cast<const float4*>(pass + (c & 16) * 80 + k);
-              *reinterpret_cast<float4*>(rec + row * stride + kTreeHead + c + k) = make_float4(v[k] + y.x, v[k + 1] + y.y, v[k + 2] + y.z, v[k + 3] + y.w);
+              const float4 z = make_float4(v[k] + y.x, v[k + 1] + y.y, v[k + 2] + y.z, v[k + 3] + y.w);
+              if (c < a.r_v) *reinterpret_cast<float4*>(rec + row * stride + kTreeHead + c + k) = z;
+              else rec[row * stride + 1 + k / 4] = k == 0 ? z.x : 0.f;
             }
           }
         }
@@ -993,12 +1008,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (fresh) {
         if (!move(t_s, live, true)) break;
 #pragma unroll
-        for (int t = 0; t < kRows / 16; ++t) l[t][0] = l[t][1] = l[t][2] = l[t][3] = 0.f;
+        for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = 0;
       }
       // Weights, in two bf16 parts as the product takes them.  Where a score is too far above its reference, the
       // references move and the weights are made again.
       bool settled = fresh, ok = true;
       uint32_t x[kRows / 2], y[kRows / 2];
+      uint64_t pp[kBoth ? kRows / 2 : 1];
       while (true) {
         float top = -INFINITY;
         constexpr int kCols = kRows == 32 ? 32 : 16;    // columns at a time (64 nodes: registers)
@@ -1019,6 +1035,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
               top = fmaxf(top, fmaxf(d0, d1));
               const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
               const uint32_t h = pack_bf16(p0, p1);
+              if (kBoth) pp[c / 2 + k + e] = pair2(p0, p1);
               x[c / 2 + k + e] = h;
               asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %5, %3;\n\tfma.rn.f32.bf16 %1, h, %5, %4;\n\t}"
                   : "=f"(d0), "=f"(d1)
@@ -1036,7 +1053,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         ok = move(t_s, live, false) && wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1);
         if (!ok) break;
         tc_fence_after();
-        const int columns = kBoth ? P.blocks * kDCols : a.r_v;
+        const int columns = kBoth ? P.blocks * kDCols : a.r_v + 16;
 #pragma unroll 1
         for (int c = 0; c < columns; c += 8) {
           float v[8];
@@ -1049,10 +1066,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         }
         tmem_wait_st();
 #pragma unroll
-        for (int t = 0; t < kRows / 16; ++t) {
-          l[t][0] *= factor[16 * t + (lane >> 2)];
-          l[t][2] *= factor[16 * t + 8 + (lane >> 2)];
-        }
+        for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
       }
       if (!ok) break;
       if constexpr (kPBuf == 1) {
@@ -1066,8 +1080,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         for (int k = 0; k < kRows / 2; ++k) {
           x[k] = live ? x[k] : 0u;
           y[k] = live ? y[k] : 0u;
+          if (kBoth) pp[k] = live ? pp[k] : 0;
         }
       }
+#pragma unroll
+      for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = add2(l[k], pp[k]);
 #pragma unroll
       for (int k = 0; k < kRows / 2; k += 4) {
         *reinterpret_cast<uint4*>(p + swizzle_offset(row * kPRow + 4 * k, kPRow)) = make_uint4(x[k], x[k + 1], x[k + 2], x[k + 3]);
@@ -1080,20 +1097,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         mbar_arrive(bar(misc->pfull[i & 1]));
         if (kPBuf == 2) mbar_arrive(bar(misc->sfree[i & 1]));
       }
-      // the sums add up both parts, once the products have them
-#pragma unroll
-      for (int t = 0; t < kRows / 8; ++t)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          // four 8 x 8 blocks: nodes 0..7 and 8..15 by tokens 0..7, then by tokens 8..15, lane = block * 8 + token
-          const int tok = 32 * quad + 16 * half + (lane & 7) + 8 * (lane >> 4), col = 16 * (t % (kRows / 16)) + (lane & 8);
-          uint32_t z[4];
-          asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(z[0]), "=r"(z[1]), "=r"(z[2]), "=r"(z[3])
-                       : "r"(smem_u32(p) + swizzle_offset(tok * kPRow + col * 2 + (t < kRows / 16 ? 0 : kLow), kPRow))
-                       : "memory");
-          add_rows(l[t % (kRows / 16)], z);
-        }
       walk_next(w, a);
     }
   }
@@ -1380,7 +1383,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->v_stage = al(p->vplan.bytes);
   // weights in two parts (two buffers of them for up to 32 nodes); queries (two parts), W, bias, ones
   const int weights = kTile * rows * 2 * 2 * (rows <= 32 ? 2 : 1), refs = 11 * rows * 4;
-  const int fixed = rows * 512 + al(p->kplan.bytes) + weights + 4096 + 256 + refs + 1024 + 256 + 768 + 1024;
+  const int fixed = rows * 512 + al(p->kplan.bytes) + weights + 4096 + 512 + refs + 1024 + 256 + 768 + 1024;
   auto fits = [&](int sk, int sv) { return fixed + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
   p->SK = p->SV = 1;
@@ -1398,7 +1401,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->q = off;      off += rows * 512;
   p->p = off;      off += weights;
   p->mu = off;     off += 4096;
-  p->ones = off;   off += 256;
+  p->ones = off;   off += 512;
   p->refs = off;   off += refs;
   p->base = off;   off += 1024;
   p->chunks = off; off += 256;
