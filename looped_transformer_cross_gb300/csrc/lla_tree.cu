@@ -420,7 +420,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t turned, tile_start, cta_start, bias, qimg, qback, khat, kback, paths, records, total;
+  size_t turned, tile_start, cta_start, head_scale, bias, qimg, qback, khat, kback, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -434,7 +434,8 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
     w.grid = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxGrid), most));
     w.tile_start = 256;
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
-    w.bias = al(w.cta_start + static_cast<size_t>(w.grid) * 16);
+    w.head_scale = w.cta_start + static_cast<size_t>(w.grid) * 16;
+    w.bias = al(w.head_scale + static_cast<size_t>(d->H) * 8);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
     w.qback = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 512;
     w.khat = al(w.qback + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 4);
@@ -597,6 +598,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     a.grid = w.grid;
     a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
+    a.head_scale = reinterpret_cast<float2*>(ws + w.head_scale);
     a.bias = ws + w.bias;
     a.qimg = ws + w.qimg;
     a.qback = reinterpret_cast<float*>(ws + w.qback);

@@ -72,6 +72,7 @@ struct TreeArgs {
   float* kback;                      // [B H][max_nodes]
   uint4* paths;                      // [B][max_nodes] nodes on each node's path, as bits
   uint8_t* bias;                     // [H][4096] mu operands
+  float2* head_scale;                // [H] powers of two: what cached keys are scaled by, and what undoes it
   TreePlan plan;
 };
 

@@ -10,8 +10,9 @@
 //   D += C_v^T P              r_v x nodes, both operands MN-major from shared memory
 // K^, Q^ and P are each the sum of two 16-bit parts: one rounding to bf16 of each made the log-sum-exp 1e-3
 // off and an output 1.5 times as far off as its own rounding.  K^ and Q^ are f16 + f16 (22 bits; products
-// high x high, high x low, low x high; a row of Q^ is scaled by a power of two to 1..2 first, K^ is not: a
-// component of a cached key beyond 65504 has no f16 part, and its sequence's results are NaN), P is
+// high x high, high x low, low x high), scaled by powers of two first: a row of Q^ to 1..2, a head's keys by
+// what brings the largest row sum of |W| and |mu| to 16..32.  So latents up to 2^11 have keys in range at any
+// weights; keys beyond make the sums NaN, and the join then takes the cached tokens again in fp32.  P is
 // bf16 + bf16 (16 bits at any size).
 // so a key is reconstructed and rotated once for all nodes of its sequence, V never is, and the
 // products and exponentials of S and D are made for 16, 32 or 64 nodes, not for a full 128 rows.
@@ -301,7 +302,8 @@ __device__ __forceinline__ void turn_pairs8(const float (&x0)[8], const float (&
 // shared-memory image (two chunks of 64 columns, 128-byte rows, swizzled), and its drafted keys, RoPE(k, pos)
 // likewise, row by row; dimensions in the order first members of the pairs, then second members, as U's.
 // Then B blocks: the nodes on each node's path as bits, and the checks of a sequence's values.  Then H
-// blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits).  The last
+// blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits), and the power of two that the
+// head's cached keys are scaled by.  The last
 // block: tiles per sequence, and every CTA's first tile.
 __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid_constant__ TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -411,6 +413,21 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
   }
   if (blockIdx.x < units + a.B + a.H) {
     const int h = blockIdx.x - units - a.B;
+    __shared__ float most[kPrepThreads / 32];
+    // the largest sum of a row's |W| and |mu|, two threads a row
+    const int dim = tid >> 1;
+    const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + (static_cast<int64_t>(h) * kHeadDim + dim) * a.r_k;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int c = (tid & 1) * 8; c < a.r_k; c += 16) {
+      float x[8];
+      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + c)), x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += fabsf(x[k]);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1) + fabsf(__ldg(a.mu_k + h * a.mu_hstride + dim));
+    sum = warp_max(sum);
+    if ((tid & 31) == 0) most[tid >> 5] = sum;
     if (tid < kHeadDim) {
       const int src = tid < 64 ? (a.rope_style == 0 ? tid : 2 * tid) : (a.rope_style == 0 ? tid : 2 * (tid - 64) + 1);
       const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
@@ -419,6 +436,14 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
       uint8_t* ab = a.bias + h * 4096;
       *reinterpret_cast<uint4*>(ab + swizzle_offset(tid * 32, 32)) = make_uint4(pack_bf16(hi, mid), pack_bf16(mu - hi - mid, 0.f), 0, 0);
       *reinterpret_cast<uint4*>(ab + swizzle_offset(tid * 32 + 16, 32)) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      float top = most[0];
+      for (int k = 1; k < kPrepThreads / 32; ++k) top = fmaxf(top, most[k]);
+      // to 16..32, within what products of these powers with others leave finite
+      const int power = min(60, max(-60, 131 - static_cast<int>(__float_as_uint(top) >> 23)));
+      a.head_scale[h] = make_float2(__int_as_float((127 + power) << 23), __int_as_float((127 - power) << 23));
     }
     return;
   }
@@ -660,11 +685,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const float* table = lane < 16 ? a.rope_cos + 4 * lane : a.rope_sin + 4 * (lane - 16);
     float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
     auto fetch = [&]() { ahead = __ldg(reinterpret_cast<const float4*>(table + static_cast<int64_t>(w.t) * kTile * 64)); };
+    float scale = 1.f;                                // (of the unit's keys, which the base row brings to them)
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
         ++unit;
+        scale = __ldcg(&a.head_scale[w.h]).x;
         if (lane == 0) {
           const uint32_t wf = bar(misc->wfull);
           mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
@@ -678,7 +705,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
       if constexpr (kPage == 3) fence_proxy_async_smem();       // (plain copies, read by the products)
       if (i >= 2 && !wait(misc->sfull[i & 1], (i - 2) >> 1)) break;      // S(i - 2) has read the K^ in U(i)'s place
-      reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = ahead;
+      reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = make_float4(ahead.x * scale, ahead.y * scale, ahead.z * scale, ahead.w * scale);
       tc_fence_after();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(misc->ufull[i & 1]));
@@ -995,7 +1022,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (fresh && i < count) {
         const float* from = a.qback + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * kRows;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) back[j] = lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f;
+        for (int j = 0; j < kMine; ++j) back[j] = (lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f) * __ldcg(&a.head_scale[w.h]).y;
       }
       if (i > 0 && (fresh || i == count)) {
         if (!finish(i - 1)) break;
@@ -1162,6 +1189,104 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
   return j;
 }
 
+// The cached tokens of a join block's nodes once more, in fp32 and token by token: for sums that are NaN, which a
+// component of a scaled cached key beyond the range of f16 makes them (and NaN and infinite inputs, whose
+// results stay NaN).  Leaves weights, reference, sums and latent sums as the usual way does.  Eight lanes a row; a
+// thread makes one component of each key.
+__device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const JoinPlan& J, int b, int h, int first, int row0, int nr, int nk) {
+  __shared__ float u[kHeadDim];
+  float* ss = reinterpret_cast<float*>(sm + J.s);
+  __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(sm + J.s);
+  __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
+  const int tid = threadIdx.x, r = tid >> 3, x = tid & 7, nk16 = (nk + 15) & ~15;
+  const int L = tree_cached(a, b, false);
+  const int64_t unit = (static_cast<int64_t>(b) * a.H + h) * a.groups + row0 / a.group;
+  const int ir = row0 % a.group + r;
+  float q[16];                                        // components 16 x ..
+  const float back = __ldcg(a.qback + unit * a.rows + ir);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint8_t* chunk = a.qimg + unit * (a.rows * 512) + (x >> 2) * a.rows * 128 + swizzle_offset(ir * 128 + (x & 3) * 32 + c * 16, 128);
+    const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(chunk)), lo = __ldcg(reinterpret_cast<const uint4*>(chunk + a.rows * 256));
+    const __half2* y = reinterpret_cast<const __half2*>(&hi);
+    const __half2* z = reinterpret_cast<const __half2*>(&lo);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = __half22float2(y[k]), w = __half22float2(z[k]);
+      q[8 * c + 2 * k] = (v.x + w.x) * back;
+      q[8 * c + 2 * k + 1] = (v.y + w.y) * back;
+    }
+  }
+  const int src = a.rope_style == 0 ? tid : tid < 64 ? 2 * tid : 2 * (tid - 64) + 1;
+  const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + (static_cast<int64_t>(h) * kHeadDim + src) * a.r_k;
+  const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
+  float m = -INFINITY, held = 0.f, acc[kMaxRankPerHead / 8];
+#pragma unroll
+  for (int k = 0; k < kMaxRankPerHead / 8; ++k) acc[k] = 0.f;
+  for (int t = 0; t < L; ++t) {
+    const int64_t at = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, t, a.status);
+    const __nv_bfloat16* ck = static_cast<const __nv_bfloat16*>(a.cache_k) + at * a.r_k;
+    const __nv_bfloat16* cv = static_cast<const __nv_bfloat16*>(a.cache_v) + at * a.r_v;
+    float key = mu;
+    for (int c = 0; c < a.r_k; c += 8) {
+      float y[8], z[8];
+      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + c)), y);
+      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(ck + c)), z);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) key = fmaf(y[k], z[k], key);
+    }
+    __syncthreads();
+    u[tid] = key;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int f = (16 * x + k) & 63;
+      const float c = __ldg(a.rope_cos + static_cast<int64_t>(t) * 64 + f), sn = __ldg(a.rope_sin + static_cast<int64_t>(t) * 64 + f);
+      s = fmaf(q[k], x < 4 ? u[f] * c - u[f + 64] * sn : u[f] * sn + u[f + 64] * c, s);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float top = fmaxf(m, s), f = exp2f(m - top), p = exp2f(s - top);
+    m = top;
+    held = fmaf(held, f, p);
+#pragma unroll
+    for (int k = 0; k < kMaxRankPerHead / 8; ++k)
+      if (x + 8 * k < a.r_v) acc[k] = fmaf(acc[k], f, p * __bfloat162float(cv[x + 8 * k]));
+  }
+  const bool row = r < nr;
+  float top = m, l = 0.f;
+  for (int c = x; c < nk && row; c += 8) top = fmaxf(top, ss[r * J.s_pitch + c]);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int c = x; c < nk16; c += 8) {
+    const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - top) : 0.f;
+    const __nv_bfloat16 p = __float2bfloat16_rn(w);
+    sp[r * J.p_pitch + c] = p;
+    sp[(kJoinRows + r) * J.p_pitch + c] = __float2bfloat16_rn(w - __bfloat162float(p));
+    l += w;
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float f = row ? exp2f(m - top) : 0.f;
+  held *= f;
+  l += held;
+  if (x == 0) {
+    reinterpret_cast<float4*>(sm + J.row)[r] = make_float4(top, held, row ? 1.f / l : 0.f, 0.f);
+    if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (top + log2f(l)) * kLn2;
+  }
+  __syncthreads();                                    // (the scores have been read)
+#pragma unroll
+  for (int k = 0; k < kMaxRankPerHead / 8; ++k) {
+    const int c = x + 8 * k;
+    if (c >= J.a_pitch - 8) break;
+    const float y = row ? acc[k] * f : 0.f;
+    const __nv_bfloat16 hi = __float2bfloat16_rn(y);
+    sa[r * J.a_pitch + c] = hi;
+    sa[(kJoinRows + r) * J.a_pitch + c] = __float2bfloat16_rn(y - __bfloat162float(hi));
+  }
+}
+
 // Block = 16 nodes of a (sequence, head); its four warps split the keys, then the output's dimensions.
 //   S = Q^ K^^T over the nodes' keys, masked to each node's path; reference M over S and the records
 //   P = 2^(S - M), A = sum of the records' latent sums times 2^(m - M) (in two bf16 parts, 16 bits)
@@ -1170,7 +1295,7 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
 // along K.  Bound by the latency of its few steps; blocks are small so that many run at a time.  The
 // scores need nothing of the tile kernel, so they are made before the wait for it (its blocks let this
 // grid start only once they have seen the preparation complete).
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ uint4 shared[];
   constexpr int kSplit = kJoinThreads / 32, kRows = kJoinRows, kTiles = 16 / kSplit;      // 8-dimension tiles of a warp
   uint8_t* sm = reinterpret_cast<uint8_t*>(shared);
@@ -1251,6 +1376,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
   __syncthreads();
 
   // ---- reference, weights and sums: eight lanes a row
+  bool lost = false;
   {
     const int r = tid >> 3, x = tid & 7;
     const bool row = r < nr;
@@ -1278,15 +1404,17 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
       held += __shfl_xor_sync(0xffffffffu, held, o);
     }
     l += held;
+    lost = row && held != held;
     if (x == 0) {
       srow[r] = make_float4(m, held, row ? 1.f / l : 0.f, 0.f);
       if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (m + log2f(l)) * kLn2;
     }
   }
-  __syncthreads();
   // ---- latent sums of the records, relative to M, in two bf16 parts
   const int cols = J.a_pitch - 8, per = cols / 4;
-  for (int i = tid; i < kRows * per; i += kJoinThreads) {
+  const bool again = __syncthreads_or(lost);
+  if (again) join_again(a, sm, J, b, h, first, row0, nr, nk);
+  for (int i = tid; i < kRows * per && !again; i += kJoinThreads) {
     const int r = i / per, c = (i - r * per) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr && c < a.r_v) {

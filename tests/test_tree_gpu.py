@@ -304,3 +304,74 @@ def test_shared_pages(dtype):
     c = make([128, 128], [3, 4], 2, 96, 160, 64, 0, dtype)
     c["table"][1] = c["table"][0]
     check(c, call(c))
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("lens,nodes,rk,rv,page", [([300, 7, 0, 129], [9, 3, 4, 1], 96, 160, 0), ([200, 140], [40, 128], 64, 128, 24),
+                                                   ([130, 33], [20, 2], 16, 240, 64)])
+def test_keys_beyond_half_precision(lens, nodes, rk, rv, page, style):
+    """Cached keys with components up to 1e6 (and some tokens' far below), queries small enough that the scores
+    are ordinary ones."""
+    c = make(lens, nodes, 2, rk, rv, page, style, "bf16")
+    c["ck"].mul_(2.0 ** 18)
+    c["wk"][:, :, :64].mul_(2.0 ** -3)
+    c["mk"].mul_(2.0 ** 10)
+    c["qkv"][:, :2].mul_(2.0 ** -18)
+    ws = call(c)
+    check(c, ws)
+    assert np.abs(widen(c["ck"])[np.isfinite(widen(c["ck"]))]).max() > 65504
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -20, 2.0 ** -6, 2.0 ** 12])
+def test_log_sum_exp_is_as_exact_as_fp32(scale):
+    """bf16 storage, the log-sum-exp of fp32 arithmetic: keys and queries of 22 bits (scores up to 6 with an
+    error of 6 * 2^-20), weights of 16 (2^-17 of a sum each, independent); key sizes far from 1, the queries'
+    the other way."""
+    for lens, nodes in (([1, 2, 5, 0], [1, 3, 2, 4]), ([130, 700], [16, 2]), ([260], [33]), ([140, 90], [128, 65])):
+        c = make(lens, nodes, 2, 96, 160, 0, 0, "bf16")
+        if scale != 1.0:
+            c["wk"].mul_(scale), c["mk"].mul_(scale)
+            c["qkv"][:, :2].div_(scale)
+            c["qkv"][:, 2:4].mul_(scale)
+        ws = call(c)
+        check(c, ws)
+        o, s, _, _ = want(c)
+        n = sum(nodes)
+        assert np.abs(widen(c["lse"])[:n] - s[:n]).max() <= 2e-5
+
+
+@pytest.mark.parametrize("nodes", [3, 20, 64])
+def test_keys_that_grow(nodes):
+    """Cached keys that grow 2^18-fold after the first 128 tokens."""
+    c = make([400, 129, 128], [nodes, 2, 1], 2, 96, 160, 0, 0, "bf16")
+    c["ck"][:, :, :128].mul_(2.0 ** -18)
+    c["mk"].mul_(2.0 ** -18)
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("nodes,page,style", [(3, 0, 0), (40, 24, 1), (128, 64, 0)])
+def test_latents_far_above_their_weights(nodes, page, style):
+    """Latents of 2^26 in one of three sequences: its keys leave the range that their weights suggest."""
+    c = make([300, 150, 77], [5, nodes, 2], 2, 96, 160, page, style, "bf16")
+    if page:
+        used = c["table"][1, :(150 + page - 1) // page].long()
+        c["ck"][used] *= 2.0 ** 26
+    else:
+        c["ck"][1] *= 2.0 ** 26
+    c["qkv"][5:5 + nodes, :2] *= 2.0 ** -26
+    check(c, call(c))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_in_one_sequence(dtype):
+    """A NaN among a sequence's cached latents makes its own results NaN and no other's."""
+    c = make([300, 150, 77], [5, 20, 2], 2, 96, 160, 0, 0, dtype)
+    c["ck"][1, :, 70, 3] = float("nan")
+    ws = call(c)
+    assert lla.device_status(ws) == lla.LLA_OK
+    assert torch.isnan(c["out"][5:25].float()).all() and torch.isnan(c["lse"][5:25]).all()
+    o, s, tol, tol_s = want(c)
+    keep = [*range(5), 25, 26]
+    err = np.abs(widen(c["out"])[keep] - o[keep])
+    assert (err <= tol[keep] + 2.0 ** -8 * np.abs(o[keep]) + 1e-4 * np.abs(o[keep]).max()).all()
+    assert (np.abs(widen(c["lse"])[keep] - s[keep]) <= 2e-5).all()
