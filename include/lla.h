@@ -526,11 +526,12 @@ typedef struct {
  *                     max_pages * page_size), the first 256 zero
  * cache.B is the tree's B.  seq_lens, w_up, mu, rope tables and the paged cache as for
  * lla_decode_attn and lla_decode_attn_paged; rope_len >= max(L_max, 128) and past every pos.
- * bf16 storage, shapes and pages that lla_tree_kernel names "tensor": fp32 sums; keys (after
- * their rotation), queries (after rotation and scale) and weights are rounded to bf16 for the
- * matrix instructions, as exact attention over a bf16 cache of keys does, and the table's rows
- * have to be those of a plain rotation, cos and sin of j theta_f (rows of any scaling; no factor
- * on them).  Otherwise ("plain") fp32 arithmetic throughout.  LLA_ERR_UNSUPPORTED: LLA-2D.
+ * fp32 arithmetic, or ("tensor" of lla_tree_kernel) matrix instructions on operands that keep 22
+ * bits of keys and queries and 16 of weights, with fp32 sums: lse is as exact as fp32 makes it,
+ * out within its own rounding.  There the table's rows have to be those of a plain rotation, cos
+ * and sin of j theta_f (rows of any scaling; no factor on them), and a sequence whose latents are
+ * beyond 2^11 in size may take a slower way to the same result.  A NaN or an infinity among a
+ * sequence's inputs reaches the results of that sequence only.  LLA_ERR_UNSUPPORTED: LLA-2D.
  */
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max);
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,
@@ -669,10 +670,9 @@ const char* lla_decode_kernel(const lla_dims* dims);
 const char* lla_decoupled_kernel(const lla_dims* dims, int d_rope);
 
 /* Name of the kernel family lla_tree_attn (page_size 0) or lla_tree_attn_paged runs for
- * `dims` (host-only, no launch): "tensor" (LLA_BF16 whose operands fit in shared memory, dense or
- * with pages of a multiple of 128 tokens or of 8, 16, 32 or 64), "plain" (LLA_F32, larger
- * ranks, other page sizes: fp32 arithmetic, not tuned for bf16), or NULL for invalid or
- * unsupported dims (LLA_2D). */
+ * `dims` (host-only, no launch), the same for every page size: "tensor" (LLA_BF16 whose operands
+ * fit in shared memory: r_k up to 208 with any r_v, larger ones with smaller r_v), "plain" (others: fp32
+ * arithmetic, not tuned for bf16), or NULL for invalid or unsupported dims (LLA_2D). */
 const char* lla_tree_kernel(const lla_dims* dims, int page_size);
 
 /* Workspace bytes for calls with at most B sequences of L_max slots and
