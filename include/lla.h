@@ -530,8 +530,9 @@ typedef struct {
  * bits of keys and queries and 16 of weights, with fp32 sums: lse is as exact as fp32 makes it,
  * out within its own rounding.  There the table's rows have to be those of a plain rotation, cos
  * and sin of j theta_f (rows of any scaling; no factor on them), and a sequence whose latents are
- * beyond 2^11 in size may take a slower way to the same result.  A NaN or an infinity among a
- * sequence's inputs reaches the results of that sequence only.  LLA_ERR_UNSUPPORTED: LLA-2D.
+ * beyond 2^11 in size may take a slower way to the same result.  A NaN or an infinity reaches the
+ * nodes that see it and no others: a cached latent's its sequence's nodes, a node's key and value
+ * the nodes below it, a query its own node.  LLA_ERR_UNSUPPORTED: LLA-2D.
  */
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max);
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,

@@ -22,6 +22,7 @@ constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
 constexpr int kPlainThreads = 256;
 constexpr int kKeyStride = kHeadDim + 4;            // floats between rows of keys and queries in shared memory
 constexpr int kFinishThreads = 128;
+constexpr int kFinishRows = 8;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -47,27 +48,29 @@ __device__ __forceinline__ int64_t node_pos(const TreeArgs& a, int entry, bool f
   return p < 0 ? 0 : a.rope_len - 1;
 }
 
-// W_up,k of the loop in fp32 as [H][r_k][128], dimensions in the paired layout: the plain kernel's threads
-// read neighbouring dimensions of one column (from L1; in shared memory it left room for one block an SM).
-// Block = 32 columns of a head.
+// W_up,k of the loop in fp32 as [H][r_k][128], dimensions in the paired layout, and W_up,v as [H][r_v][128]: the
+// other kernels' threads read neighbouring dimensions of one column (from L1; in shared memory the first left
+// room for one block an SM).  Block = 32 columns of a head.
 template <typename T>
 __global__ void __launch_bounds__(kPlainThreads) tree_turn_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ float t[32][kHeadDim + 1];
-  const int h = blockIdx.x, c0 = blockIdx.y * 32, cols = min(32, a.r_k - c0);
-  const T* W = static_cast<const T*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * a.r_k + c0;
+  const int k_tiles = (a.r_k + 31) / 32;
+  const bool key = blockIdx.y < k_tiles;
+  const int r = key ? a.r_k : a.r_v, h = blockIdx.x, c0 = (key ? blockIdx.y : blockIdx.y - k_tiles) * 32, cols = min(32, r - c0);
+  const T* W = static_cast<const T*>(key ? a.w_up_k : a.w_up_v) + static_cast<int64_t>(h) * kHeadDim * r + c0;
   const int c = threadIdx.x & 31, e0 = threadIdx.x >> 5;
   if (c < cols) {
     float x[kHeadDim * 32 / kPlainThreads];           // every load under way before the first is used
 #pragma unroll
     for (int k = 0; k < kHeadDim * 32 / kPlainThreads; ++k) {
       const int e = e0 + k * (kPlainThreads / 32);
-      x[k] = to_f(W[static_cast<int64_t>(e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64)) * a.r_k + c]);
+      x[k] = to_f(W[static_cast<int64_t>(!key ? e : e < 64 ? pair0(a.rope_style, e) : pair1(a.rope_style, e - 64)) * r + c]);
     }
 #pragma unroll
     for (int k = 0; k < kHeadDim * 32 / kPlainThreads; ++k) t[c][e0 + k * (kPlainThreads / 32)] = x[k];
   }
   __syncthreads();
-  float* out = a.w_turned + (static_cast<int64_t>(h) * a.r_k + c0) * kHeadDim;
+  float* out = (key ? a.w_turned : a.v_turned) + (static_cast<int64_t>(h) * r + c0) * kHeadDim;
   for (int i = threadIdx.x; i < kHeadDim * cols; i += kPlainThreads) out[i] = t[i >> 7][i & 127];
 }
 
@@ -260,16 +263,21 @@ __global__ void __launch_bounds__(kPlainThreads, 2) tree_plain_kernel(const __gr
   }
 }
 
-// Block = (unit, a few nodes), one node at a time: scores of the nodes on its path (a warp each),
-// merge of the unit's records, then thread e forms out_e = (W_e . A + mu_e P + sum_a p_a v_a,e) / l.
+// Block = (unit, up to eight nodes).  A warp takes a key at a time, rotates it and has its products with all
+// nodes; sixteen threads a node make its softmax over its path and the records; thread e then forms
+// out_e = (W_e . A + mu_e P + sum_a p_a v_a,e) / l of all nodes, so that a key, a value and a weight are read
+// once for eight.  Bound by the latency of its steps.  16 sequences of 12 heads with 35 nodes each over 76 tokens
+// 48 us, 128 nodes of 16 heads over 1000 tokens 59, 4 x 16 nodes of 16 heads over 2000 38 (one node at a time, rows of
+// W_up,v read as they lie by the threads: 177, 130, 31).
 template <typename T>
-__global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kFinishThreads, 5) tree_finish_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ int32_t par[kTreeMaxNodes];
-  __shared__ int32_t chain[kTreeMaxNodes];
-  __shared__ int depth;
-  __shared__ float sc[kTreeMaxNodes];
-  __shared__ float qrow[kHeadDim];
-  __shared__ float A[kMaxRankPerHead];
+  __shared__ uint32_t path[kFinishRows][4], used[4];
+  __shared__ __align__(16) float sc[kTreeMaxNodes][kFinishRows];       // scores, then weights
+  __shared__ __align__(16) float A[kMaxRankPerHead][kFinishRows];
+  __shared__ float q[kFinishRows][kHeadDim];
+  __shared__ float factor[16][kFinishRows];
+  __shared__ float4 stat[kFinishRows];                // {reference, cached sum, sum, -}
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t unit = blockIdx.x;
   const int b = static_cast<int>(unit / a.H), h = static_cast<int>(unit - static_cast<int64_t>(b) * a.H);
@@ -277,7 +285,11 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
   int first;
   const int n = tree_nodes(a, b, first, flag);
   const int L = tree_cached(a, b, flag);
-  if (blockIdx.y * a.finish_rows >= n) return;
+  constexpr int kMost = kFinishRows * kMaxRankPerHead / 4 / kFinishThreads;     // quads of latent sums a thread holds
+  const int row0 = blockIdx.y * a.finish_rows;
+  if (row0 >= n) return;
+  const int rows = min(a.finish_rows, n - row0), nk = row0 + rows;
+  const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk), stride = a.r_v + kTreeHead;
   for (int i = tid; i < n; i += kFinishThreads) {
     int p = __ldg(a.parent + first + i);
     if (p < -1 || p >= i) {
@@ -287,78 +299,195 @@ __global__ void __launch_bounds__(kFinishThreads) tree_finish_kernel(const __gri
     par[i] = p;
     if (flag) node_pos(a, first + i, true);
   }
-  __syncthreads();
-  const int row_first = blockIdx.y * a.finish_rows;
-  const int nsplit = static_cast<int>((L + a.chunk - 1) / a.chunk);
-  const int stride = a.r_v + kTreeHead;
-
-  for (int row = row_first; row < min(n, row_first + a.finish_rows); ++row) {
-    const int entry = first + row;
-    __syncthreads();
-    if (tid == 0) {
-      int d = 0;
-      for (int i = row; i >= 0; i = par[i]) chain[d++] = i;
-      depth = d;
-    }
-    if (tid < 64) {
+  for (int i = tid; i < kFinishRows * 64; i += kFinishThreads) {
+    const int r = i >> 6, f = i & 63;
+    float y0 = 0.f, y1 = 0.f;
+    if (r < rows) {
+      const int entry = first + row0 + r;
       const T* qv = static_cast<const T*>(a.q) + entry * a.q_stride + h * kHeadDim;
       const int64_t p = node_pos(a, entry, false);
-      const float c = __ldg(a.rope_cos + p * 64 + tid), s = __ldg(a.rope_sin + p * 64 + tid);
-      const float x0 = to_f(qv[pair0(a.rope_style, tid)]), x1 = to_f(qv[pair1(a.rope_style, tid)]);
-      qrow[tid] = (x0 * c - x1 * s) * (kLog2e * kInvSqrtD);
-      qrow[64 + tid] = (x0 * s + x1 * c) * (kLog2e * kInvSqrtD);
+      const float c = __ldg(a.rope_cos + p * 64 + f), s = __ldg(a.rope_sin + p * 64 + f);
+      const float x0 = to_f(qv[pair0(a.rope_style, f)]), x1 = to_f(qv[pair1(a.rope_style, f)]);
+      y0 = (x0 * c - x1 * s) * (kLog2e * kInvSqrtD);
+      y1 = (x0 * s + x1 * c) * (kLog2e * kInvSqrtD);
     }
-    __syncthreads();
-    const int nd = depth;
-    for (int i = warp; i < nd; i += kFinishThreads / 32) {
-      const int ke = first + chain[i];
-      const T* kv = static_cast<const T*>(a.k) + ke * a.k_stride + h * kHeadDim;
-      const int64_t p = node_pos(a, ke, false);
-      float dot = 0.f;
+    q[r][f] = y0;
+    q[r][64 + f] = y1;
+  }
+  if (tid < 4) used[tid] = 0;
+  __syncthreads();
+  // ---- the nodes on each node's path, as bits
+  if (tid < kFinishRows) {
+    uint32_t on[4] = {0, 0, 0, 0};
+    if (tid < rows) {
+      for (int i = row0 + tid; i >= 0; i = par[i]) {
 #pragma unroll
-      for (int f = lane; f < 64; f += 32) {
+        for (int k = 0; k < 4; ++k) on[k] |= (i >> 5) == k ? 1u << (i & 31) : 0u;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      path[tid][k] = on[k];
+      if (on[k]) atomicOr(&used[k], on[k]);
+    }
+  }
+  __syncthreads();
+  // ---- scores: four keys of a warp at a time, their loads under way together
+  constexpr int kWarps = kFinishThreads / 32, kAtOnce = 4;
+  for (int j0 = warp; j0 < nk; j0 += kWarps * kAtOnce) {
+    float y0[kAtOnce][2], y1[kAtOnce][2];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = min(j0 + i * kWarps, nk - 1);
+      const T* kv = static_cast<const T*>(a.k) + (first + j) * a.k_stride + h * kHeadDim;
+      const int64_t p = node_pos(a, first + j, false);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int f = lane + 32 * k;
         const float c = __ldg(a.rope_cos + p * 64 + f), s = __ldg(a.rope_sin + p * 64 + f);
         const float x0 = to_f(kv[pair0(a.rope_style, f)]), x1 = to_f(kv[pair1(a.rope_style, f)]);
-        dot = fmaf(qrow[f], x0 * c - x1 * s, fmaf(qrow[64 + f], x0 * s + x1 * c, dot));
+        y0[i][k] = x0 * c - x1 * s;
+        y1[i][k] = x0 * s + x1 * c;
       }
-      dot = warp_sum(dot);
-      if (lane == 0) sc[i] = dot;
     }
-    __syncthreads();
-    // the largest of the path's scores and of the records' maxima
-    float m = -INFINITY;
-    for (int i = 0; i < nd; ++i) m = fmaxf(m, sc[i]);
-    const float* rec0 = a.records + (unit * a.splits * a.rec_rows + row) * stride;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const int j = j0 + i * kWarps;
+      if (j >= nk || !(used[j >> 5] >> (j & 31) & 1)) continue;
+      float d[kFinishRows];
+#pragma unroll
+      for (int r = 0; r < kFinishRows; ++r) d[r] = q[r][lane] * y0[i][0];
+#pragma unroll
+      for (int r = 0; r < kFinishRows; ++r)
+        d[r] = fmaf(q[r][lane + 32], y0[i][1], fmaf(q[r][lane + 64], y1[i][0], fmaf(q[r][lane + 96], y1[i][1], d[r])));
+      // the eight sums over the lanes: half of them go on in half of the lanes, three times
+      float x[4], y[2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float give = __shfl_xor_sync(0xffffffffu, lane & 16 ? d[r] : d[r + 4], 16);
+        x[r] = (lane & 16 ? d[r + 4] : d[r]) + give;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float give = __shfl_xor_sync(0xffffffffu, lane & 8 ? x[r] : x[r + 2], 8);
+        y[r] = (lane & 8 ? x[r + 2] : x[r]) + give;
+      }
+      const float give = __shfl_xor_sync(0xffffffffu, lane & 4 ? y[0] : y[1], 4);
+      float z = (lane & 4 ? y[1] : y[0]) + give;
+      z += __shfl_xor_sync(0xffffffffu, z, 2);
+      z += __shfl_xor_sync(0xffffffffu, z, 1);
+      if ((lane & 3) == 0) sc[j][(lane >> 4) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1)] = z;
+    }
+  }
+  __syncthreads();
+  // ---- softmax over the path and the records: sixteen threads a node
+  {
+    const int r = tid >> 4, x = tid & 15;
+    const float* rec0 = a.records + (unit * a.splits * a.rec_rows + row0 + r) * stride;
     const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
-    for (int i = 0; i < nsplit; ++i) m = fmaxf(m, rec0[i * next]);
-    float held = 0.f;
-    for (int i = 0; i < nsplit; ++i) {
-      const float* r = rec0 + i * next;
-      held = fmaf(exp2f(r[0] - m), (r[1] + r[2]) + (r[3] + r[4]), held);
-    }
-    for (int c = tid; c < a.r_v; c += kFinishThreads) {
-      float x = 0.f;
-      for (int i = 0; i < nsplit; ++i) x = fmaf(exp2f(rec0[i * next] - m), rec0[i * next + kTreeHead + c], x);
-      A[c] = x;
-    }
-    __syncthreads();
-    float l = held, o = held * __ldg(a.mu_v + h * a.mu_hstride + tid);
-    if (nsplit == 0) o = 0.f;
-    for (int i = 0; i < nd; ++i) {
-      const float p = exp2f(sc[i] - m);
+    const int held_by = r < rows ? nsplit : 0;
+    float m = -INFINITY;
+    for (int j = x; j < nk; j += 16)
+      if (path[r][j >> 5] >> (j & 31) & 1) m = fmaxf(m, sc[j][r]);
+    for (int i = x; i < held_by; i += 16) m = fmaxf(m, rec0[i * next]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f, held = 0.f;
+    for (int j = x; j < nk; j += 16) {
+      const float p = path[r][j >> 5] >> (j & 31) & 1 ? exp2f(sc[j][r] - m) : 0.f;
+      sc[j][r] = p;
       l += p;
-      o = fmaf(p, to_f(static_cast<const T*>(a.v)[(first + chain[i]) * a.v_stride + h * kHeadDim + tid]), o);
     }
-    if (nsplit > 0) {
-      const T* wrow = static_cast<const T*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + tid) * a.r_v;
-      for (int r = 0; r < a.r_v; r += 4) {
-        const float4 w = ld4(wrow + r);
-        o = fmaf(w.x, A[r], fmaf(w.y, A[r + 1], fmaf(w.z, A[r + 2], fmaf(w.w, A[r + 3], o))));
+    for (int i = x; i < held_by; i += 16) {
+      const float* rec = rec0 + i * next;
+      held = fmaf(exp2f(rec[0] - m), (rec[1] + rec[2]) + (rec[3] + rec[4]), held);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      held += __shfl_xor_sync(0xffffffffu, held, o);
+    }
+    if (x == 0) stat[r] = make_float4(m, held, l + held, 0.f);
+  }
+  __syncthreads();
+  // ---- the records' latent sums, sixteen records' factors at a time
+  if (nsplit > 0) {
+    const float* rec0 = a.records + (unit * a.splits * a.rec_rows + row0) * stride;
+    const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
+    const int quads = a.r_v / 4;
+    float4 sum[kMost];
+#pragma unroll
+    for (int e = 0; e < kMost; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < nsplit; s0 += 16) {
+      const int r = tid & 7, k = tid >> 3, parts = min(16, nsplit - s0);
+      __syncthreads();
+      factor[k][r] = r < rows && k < parts ? exp2f(rec0[(s0 + k) * next + r * stride] - stat[r].x) : 0.f;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kMost; ++e) {
+        const int i = tid + e * kFinishThreads, row = i / quads;
+        if (row >= rows) break;
+        const float* at = rec0 + s0 * next + row * stride + kTreeHead + 4 * (i - row * quads);
+#pragma unroll 8
+        for (int x = 0; x < parts; ++x, at += next) {
+          const float4 y = ld4(at);
+          const float f = factor[x][row];
+          sum[e].x = fmaf(f, y.x, sum[e].x); sum[e].y = fmaf(f, y.y, sum[e].y);
+          sum[e].z = fmaf(f, y.z, sum[e].z); sum[e].w = fmaf(f, y.w, sum[e].w);
+        }
       }
     }
-    const int64_t at = static_cast<int64_t>(entry) * a.H + h;
-    from_f(o / l, static_cast<T*>(a.out) + at * kHeadDim + tid);
-    if (tid == 0 && a.lse) a.lse[at] = (m + log2f(l)) * kLn2;
+#pragma unroll
+    for (int e = 0; e < kMost; ++e) {
+      const int i = tid + e * kFinishThreads, row = i / quads, c = 4 * (i - row * quads);
+      if (row >= kFinishRows) break;
+      A[c][row] = sum[e].x; A[c + 1][row] = sum[e].y; A[c + 2][row] = sum[e].z; A[c + 3][row] = sum[e].w;
+    }
+  }
+  __syncthreads();
+  // ---- dimension tid of every node
+  float o[kFinishRows];
+  auto add = [&](const float (&by)[kFinishRows], float w) {
+    const float4 lo = *reinterpret_cast<const float4*>(by), hi = *reinterpret_cast<const float4*>(by + 4);
+    o[0] = fmaf(lo.x, w, o[0]); o[1] = fmaf(lo.y, w, o[1]); o[2] = fmaf(lo.z, w, o[2]); o[3] = fmaf(lo.w, w, o[3]);
+    o[4] = fmaf(hi.x, w, o[4]); o[5] = fmaf(hi.y, w, o[5]); o[6] = fmaf(hi.z, w, o[6]); o[7] = fmaf(hi.w, w, o[7]);
+  };
+  const float mu = nsplit > 0 ? __ldg(a.mu_v + h * a.mu_hstride + tid) : 0.f;
+#pragma unroll
+  for (int r = 0; r < kFinishRows; ++r) o[r] = stat[r].y * mu;
+  for (int j0 = 0; j0 < nk; j0 += 8) {                // (eight values under way together)
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f(static_cast<const T*>(a.v)[(first + min(j0 + i, nk - 1)) * a.v_stride + h * kHeadDim + tid]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = j0 + i;
+      if (j >= nk || !(used[j >> 5] >> (j & 31) & 1)) continue;
+      if (isfinite(v[i])) {
+        add(sc[j], v[i]);
+      } else {                                        // (0 times it is not 0 where the node is not on the path)
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r)
+          if (path[r][j >> 5] >> (j & 31) & 1) {
+            const float x = sc[j][r] * v[i];
+#pragma unroll
+            for (int k = 0; k < kFinishRows; ++k) o[k] += k == r ? x : 0.f;
+          }
+      }
+    }
+  }
+  if (nsplit > 0) {
+    const float* w = a.v_turned + static_cast<int64_t>(h) * a.r_v * kHeadDim + tid;
+#pragma unroll 16
+    for (int c = 0; c < a.r_v; ++c) add(A[c], __ldg(w + c * kHeadDim));
+  }
+#pragma unroll
+  for (int r = 0; r < kFinishRows; ++r) {
+    if (r >= rows) break;
+    const int64_t at = (static_cast<int64_t>(first) + row0 + r) * a.H + h;
+    const float4 st = stat[r];
+    from_f(o[r] / st.z, static_cast<T*>(a.out) + at * kHeadDim + tid);
+    if (tid == 0 && a.lse) a.lse[at] = (st.x + log2f(st.z)) * kLn2;
   }
 }
 
@@ -378,7 +507,7 @@ cudaError_t launch_tree_plain(const TreeArgs& a, bool bf16, cudaStream_t s) {
                                              static_cast<int>(plain_smem(kMaxRankPerHead, kMaxRankPerHead)));
   if (e != cudaSuccess) return e;
   auto turn = bf16 ? tree_turn_kernel<__nv_bfloat16> : tree_turn_kernel<float>;
-  turn<<<dim3(a.H, (a.r_k + 31) / 32), kPlainThreads, 0, s>>>(a);
+  turn<<<dim3(a.H, (a.r_k + 31) / 32 + (a.r_v + 31) / 32), kPlainThreads, 0, s>>>(a);
   kern<<<grid, kPlainThreads, plain_smem(a.r_k, a.r_v), s>>>(a);
   return cudaGetLastError();
 }
@@ -420,7 +549,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t turned, tile_start, cta_start, head_scale, bias, qimg, qback, khat, kback, paths, records, total;
+  size_t turned, v_turned, tile_start, cta_start, head_scale, bias, qimg, qback, khat, kback, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -452,7 +581,8 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
   w.chunk = per * kTreePlainTile;
   w.splits = static_cast<int>((tiles + per - 1) / per);
   w.turned = 256;
-  w.records = 256 + static_cast<size_t>(d->H) * d->r_k * kHeadDim * 4;
+  w.v_turned = 256 + static_cast<size_t>(d->H) * d->r_k * kHeadDim * 4;
+  w.records = w.v_turned + static_cast<size_t>(d->H) * d->r_v * kHeadDim * 4;
   w.total = w.records + static_cast<size_t>(units) * w.splits * rec;
   return w;
 }
@@ -610,6 +740,7 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     return launch_tree_tensor(a, maps, s) == cudaSuccess ? LLA_OK : LLA_ERR_CUDA;
   }
   a.w_turned = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.turned);
+  a.v_turned = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.v_turned);
   if (launch_tree_plain(a, bf16, s) != cudaSuccess || launch_tree_finish(a, bf16, s) != cudaSuccess) return LLA_ERR_CUDA;
   return LLA_OK;
 }

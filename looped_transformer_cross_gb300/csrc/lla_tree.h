@@ -60,6 +60,7 @@ struct TreeArgs {
   int rec_rows, splits, finish_rows;
   int64_t chunk;                     // cached tokens of a split, a multiple of kTreePlainTile
   float* w_turned;                   // plain kernel: [H][r_k][128]
+  float* v_turned;                   // finish kernel: [H][r_v][128]
   // Tensor-core kernel (groups > 0): a unit is (b H + h) * groups + block of `group` nodes, and record
   // unit + CTA belongs to every (unit, CTA) that share a tile
   int v_whole;                       // r_v a multiple of 32: V by maps.v4

@@ -1166,6 +1166,13 @@ __device__ __forceinline__ void mma_k32_f16(float (&acc)[4], const uint4& lo, co
   mma16816_f16(acc, lo.z, hi.z, lo.w, hi.w, b.z, b.w);
 }
 
+// Of two bf16 values, those that are not finite become 0; whether there was one.
+__device__ __forceinline__ bool drop_odd(uint32_t& x) {
+  const uint32_t hi = (x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u, lo = (x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
+  x &= ~(hi | lo);
+  return (hi | lo) != 0;
+}
+
 // Shared memory of a join block (bytes): V rows of the keys, scores or the two parts of the latent
 // sums, weights, per row {reference, cached sum, 1 / sum}.
 struct JoinPlan {
@@ -1312,11 +1319,14 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   if (row0 >= n) return;
   const int nr = min(kRows, n - row0), nk = min(n, row0 + kRows), nk16 = (nk + 15) & ~15;
 
-  // ---- values of the keys
+  // ---- values of the keys; NaN and infinities are left out (0 times them is not 0 for the nodes that do not have
+  // the key on their path) and added at the end
+  bool odd = false;
   for (int i = tid; i < nk16 * 16; i += kJoinThreads) {
     const int r = i >> 4, c = (i & 15) * 8;
     uint4 x = make_uint4(0, 0, 0, 0);
     if (r < nk) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + (first + r) * a.v_stride + h * kHeadDim + c));
+    odd |= drop_odd(x.x) | drop_odd(x.y) | drop_odd(x.z) | drop_odd(x.w);
     *reinterpret_cast<uint4*>(sv + r * (kHeadDim + 8) + c) = x;
   }
   // ---- scores of this warp's 16 nodes against every kSplit-th tile of eight keys
@@ -1373,7 +1383,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
   const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
   const float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * a.group) * stride;
-  __syncthreads();
+  odd = __syncthreads_or(odd);
 
   // ---- reference, weights and sums: eight lanes a row
   bool lost = false;
@@ -1477,6 +1487,24 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
       for (int e = 0; e < 2; ++e) {
         mma16816(acc[t], x[e][0], x[e][1], x[e][2], x[e][3], b0, b1);
         mma16816(acc[t + 1], x[e][0], x[e][1], x[e][2], x[e][3], b2, b3);
+      }
+    }
+  }
+  if (odd) {
+    for (int j = 0; j < nk; ++j) {
+      const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v) + (first + j) * a.v_stride + h * kHeadDim + e0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        if (row >= nr || !(__ldcg(reinterpret_cast<const uint32_t*>(a.paths + static_cast<int64_t>(b) * a.max_nodes + row0 + row) + (j >> 5)) >> (j & 31) & 1)) continue;
+        const float p = __bfloat162float(sp[row * J.p_pitch + j]) + __bfloat162float(sp[(kRows + row) * J.p_pitch + j]);
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float y = __bfloat162float(v[8 * t + 2 * q + k]);
+            if (!isfinite(y)) acc[t][2 * r + k] = fmaf(p, y, acc[t][2 * r + k]);
+          }
       }
     }
   }

@@ -375,3 +375,34 @@ def test_nan_in_one_sequence(dtype):
     err = np.abs(widen(c["out"])[keep] - o[keep])
     assert (err <= tol[keep] + 2.0 ** -8 * np.abs(o[keep]) + 1e-4 * np.abs(o[keep]).max()).all()
     assert (np.abs(widen(c["lse"])[keep] - s[keep]) <= 2e-5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("L", [0, 200])
+def test_nan_and_infinity_off_the_path(dtype, what, L):
+    """A node's key and value that are not finite reach the nodes below it and no others, and a query its own node."""
+    c = make([L, L], [40, 9], 2, 96, 160, 0, 0, dtype)
+    parent = c["parent"].tolist()
+    for node, part in ((7, 1), (30, 2), (12, 0)):
+        c["qkv"][node, 2 * part:2 * part + 2, 5] = what
+    below = set()
+    for i in range(40):
+        if any(a in (7, 30) for a in otree.path_of(parent[:40], i)) or i == 12:
+            below.add(i)
+    ws = call(c)
+    assert lla.device_status(ws) == lla.LLA_OK
+    c["qkv"] = torch.nan_to_num(c["qkv"], 0.0, 0.0, 0.0)
+    o, s, tol, tol_s = want(c)
+    keep = [i for i in range(49) if i not in below]
+    assert len(keep) >= 10
+    err = np.abs(widen(c["out"])[keep] - o[keep])
+    assert (err <= (0 if dtype == "f32" else tol[keep] + 2.0 ** -8 * np.abs(o[keep])) + 1e-4 * np.abs(o[keep]).max()).all()
+    assert (np.abs(widen(c["lse"])[keep] - s[keep]) <= 2e-5).all()
+    got = c["out"].float()
+    if what == what:
+        # an infinite value: infinite in its component where the weights are above 0, finite in the others
+        chain = [i for i in range(40) if 30 in otree.path_of(parent[:40], i) and 7 not in otree.path_of(parent[:40], i) and i != 12]
+        assert (got[chain][:, :, 5] == what).all() and torch.isfinite(got[chain][:, :, 6:]).all() if chain else True
+    else:
+        assert torch.isnan(got[30, :, 5]).all() and torch.isnan(got[12]).all()
