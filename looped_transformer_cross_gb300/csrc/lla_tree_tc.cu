@@ -29,6 +29,7 @@
 // more time than anything else.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -248,19 +249,29 @@ __device__ __forceinline__ void gather_tile(const void* pool, int r, const int64
   const uint32_t to = smem_u32(dst + k.off) + sub * k.row, col = (8 * g - k.start) * 2;
   const uint32_t mask = k.row == 128 ? 7u : k.row == 64 ? 3u : 1u, shift = k.row == 128 ? 0u : k.row == 64 ? 1u : 2u;
   const uint8_t* from = static_cast<const uint8_t*>(pool) + 16 * g;
+  // (steps without a branch between them, so that their shuffles overlap; eight where a step is a few rows: 32 x 4096
+  // tokens one a page 864 us, 1148 with a branch, 1395 two at a time; at the small ranks four, 1342 and 1473)
+  auto steps = [&](auto most) {
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int64_t mine = rows[b] * (2 * r);
-    const int m = min(32, valid - 32 * b);
-#pragma unroll 2
-    for (int t = 0; t < m; t += at_once) {
-      const uint8_t* src = from + __shfl_sync(0xffffffffu, mine, (t + sub) & 31);
-      const uint32_t row = 32 * b + t + sub;        // (its place in the swizzle: 16-byte pieces exchanged by rows)
-      if (sub < at_once && t + sub < m)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (32 * b + t) * k.row + (col ^ (((row >> shift) & mask) << 4))), "l"(src)
-                     : "memory");
+    for (int b = 0; b < 4; ++b) {
+      const int64_t mine = rows[b] * (2 * r);
+      const int m = min(32, valid - 32 * b);
+#pragma unroll 1
+      for (int t0 = 0; t0 < m; t0 += most * at_once) {
+#pragma unroll
+        for (int i = 0; i < most; ++i) {
+          const int t = t0 + i * at_once;
+          const uint8_t* src = from + __shfl_sync(0xffffffffu, mine, (t + sub) & 31);
+          const uint32_t row = 32 * b + t + sub;      // (its place in the swizzle: 16-byte pieces exchanged by rows)
+          if (sub < at_once && t + sub < m)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (32 * b + t) * k.row + (col ^ (((row >> shift) & mask) << 4))), "l"(src)
+                         : "memory");
+        }
+      }
     }
-  }
+  };
+  if (at_once < 8) steps(std::integral_constant<int, 8>{});
+  else steps(std::integral_constant<int, 4>{});
   asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(fb) : "memory");
 }
 
