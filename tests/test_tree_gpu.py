@@ -406,3 +406,109 @@ def test_nan_and_infinity_off_the_path(dtype, what, L):
         assert (got[chain][:, :, 5] == what).all() and torch.isfinite(got[chain][:, :, 6:]).all() if chain else True
     else:
         assert torch.isnan(got[30, :, 5]).all() and torch.isnan(got[12]).all()
+
+
+@pytest.mark.parametrize("lens,nodes,rk,rv,page", [([300, 7, 0, 129], [9, 3, 4, 1], 96, 160, 0), ([700, 140], [40, 128], 64, 128, 24),
+                                                   ([130, 1300], [20, 30], 16, 240, 64), ([2, 1, 5], [1, 2, 16], 192, 192, 1)])
+def test_out_is_rounded_once(lens, nodes, rk, rv, page):
+    """bf16 storage: an output is off by half a step of its own, 2^-8 of its value, and by what parts of 16
+    bits leave out: weights and latent sums 2^-17 each, weights by scores of up to 8 with 22 bits 2^-18 more:
+    2^-15 of a sum of |p v| of up to twice the largest value, taken as 2^-14 of that value."""
+    c = make(lens, nodes, 2, rk, rv, page, 0, "bf16")
+    ws = call(c)
+    assert lla.device_status(ws) == lla.LLA_OK
+    o = want(c)[0]
+    n = sum(nodes)
+    err = np.abs(widen(c["out"])[:n] - o[:n])
+    tol = 2.0 ** -8 * np.abs(o[:n]) + 2.0 ** -14 * np.abs(o[:n]).max(-1, keepdims=True)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_two_streams_at_once(dtype):
+    """Calls on two streams with a workspace each, under way together."""
+    cases = [make([900, 333], [20, 5], 3, 96, 160, 64, 0, dtype), make([500, 40, 77], [64, 1, 9], 2, 32, 64, 0, 1, dtype)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [lla.tree_workspace(c["dm"], tree_of(c), c["cap"]) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, ws in zip(cases, streams, spaces):
+            call(c, ws, stream=s)
+    torch.cuda.synchronize()
+    for c, ws in zip(cases, spaces):
+        check(c, ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_graphs_that_share_a_workspace(dtype):
+    """Two captured calls of different shapes over one workspace, whose contents are whatever was there before."""
+    cases = [make([900, 333], [20, 5], 3, 96, 160, 64, 0, dtype), make([500, 40, 77], [64, 1, 9], 2, 32, 64, 0, 1, dtype)]
+    trees = [tree_of(c) for c in cases]
+    size = max(lla.tree_workspace(c["dm"], t, c["cap"]).numel() for c, t in zip(cases, trees))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    graphs = []
+    for c, t in zip(cases, trees):
+        call(c, ws, t)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call(c, ws, t)
+    for _ in range(3):
+        for c, g in zip(cases, graphs):
+            c["out"].fill_(77.0), c["lse"].fill_(77.0)
+            g.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        check(c, ws)
+
+
+@pytest.mark.parametrize("dtype,page", [("bf16", 64), ("bf16", 12), ("f32", 64)])
+def test_pages_far_into_a_pool(dtype, page):
+    """Pages whose elements lie beyond 2^32 in their pools."""
+    c = make([150, 70], [3, 6], 16, 96, 160, page, 0, dtype)
+    num = (1 << 32) // (16 * page * 96) + 50
+    if torch.cuda.mem_get_info()[0] < 2 * num * 16 * page * 256 * c["ck"].element_size():
+        pytest.skip("not enough memory")
+    for name in ("ck", "cv"):
+        small = c[name]
+        c[name] = torch.empty((num, *small.shape[1:]), dtype=small.dtype, device="cuda")
+        c[name][num - small.shape[0]:] = small
+    small = {k: c[k][num - len(small):].clone() for k in ("ck", "cv")}
+    table = c["table"].clone()
+    c["table"] = torch.where(table >= 0, table + (num - len(small["ck"])), table)
+    ws = call(c)
+    c.update(small, table=table)
+    check(c, ws)
+
+
+def test_tree_binding_refusals():
+    c = make([40, 20], [4, 3], 2, 96, 160, 0, 0, "bf16")
+    ws = lla.tree_workspace(c["dm"], tree_of(c), c["cap"])
+    good = dict(c)
+
+    def refused(error, **over):
+        bad = dict(good, **over)
+        with pytest.raises(error):
+            call(bad, over.get("ws", ws), over.get("tree"))
+
+    refused(ValueError, qkv=good["qkv"].float())
+    refused(ValueError, qkv=good["qkv"][:-1])
+    refused(ValueError, qkv=good["qkv"].cpu())
+    refused(ValueError, ck=good["ck"][:1])
+    refused(ValueError, ck=good["ck"].transpose(1, 2))
+    refused(ValueError, seq_lens=good["seq_lens"].long())
+    refused(ValueError, wk=good["wk"][:1])
+    refused(ValueError, mk=good["mk"].bfloat16())
+    refused(ValueError, cos=good["cos"][:, :32].contiguous())
+    refused(ValueError, sin=good["sin"][:-1])
+    refused(ValueError, out=good["out"].float())
+    refused(ValueError, lse=good["lse"][:-1])
+    refused(ValueError, tree=lla.DraftTree(good["tok_start"], good["parent"], 4))              # no positions
+    refused(ValueError, tree=lla.DraftTree(good["tok_start"][:2].contiguous(), good["parent"], 4, pos=good["pos"]))
+    refused(lla.LLAError, ws=ws[:-4096].contiguous())
+    refused(lla.LLAError, out=good["qkv"].view(-1)[:good["out"].numel()].view(good["out"].shape))     # over its inputs
+    with pytest.raises(ValueError):
+        lla.DraftTree(good["tok_start"], good["parent"], lla.LLA_TREE_MAX_NODES + 1, pos=good["pos"])
+    call(c, ws)
+    check(c, ws)
