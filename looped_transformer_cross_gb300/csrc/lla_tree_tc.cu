@@ -854,13 +854,30 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // ======================================================== rotation: U -> K^
     const int quad = warp & 3, row = 32 * quad + lane, f0 = 32 * ((warp - 4) >> 2);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
-    uint64_t cl[16], sl[16];                          // the lane's own row of the table, by twos
+    // the lane's own row of the table, by twos: in registers, or, where TMEM has room for it (up to 16 nodes), there,
+    // and the loop over the frequencies stays rolled
+    constexpr bool kTable = kRows == 16;
+    constexpr int kTabCol = kDCol + 2 * kDCols;
+    uint64_t cl[kTable ? 8 : 16], sl[kTable ? 8 : 16];
+    if constexpr (kTable) {
+      uint4 x[16];                                    // cosines, then sines
 #pragma unroll
-    for (int f = 0; f < 16; f += 2) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + row * 64 + f0 + 2 * f));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(a.rope_sin + row * 64 + f0 + 2 * f));
-      cl[f] = pair2(c.x, c.y); cl[f + 1] = pair2(c.z, c.w);
-      sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
+      for (int k = 0; k < 16; ++k) x[k] = __ldg(reinterpret_cast<const uint4*>((k < 8 ? a.rope_cos : a.rope_sin) + row * 64 + f0 + 4 * (k & 7)));
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const uint32_t y[16] = {x[c].x, x[c].y, x[c].z, x[c].w, x[c + 1].x, x[c + 1].y, x[c + 1].z, x[c + 1].w,
+                                x[c + 2].x, x[c + 2].y, x[c + 2].z, x[c + 2].w, x[c + 3].x, x[c + 3].y, x[c + 3].z, x[c + 3].w};
+        tmem_st_x16(lanes + kTabCol + (c >> 3) * 64 + f0 + (c & 7) * 4, y);
+      }
+      tmem_wait_st();
+    } else {
+#pragma unroll
+      for (int f = 0; f < 16; f += 2) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(a.rope_cos + row * 64 + f0 + 2 * f));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(a.rope_sin + row * 64 + f0 + 2 * f));
+        cl[f] = pair2(c.x, c.y); cl[f + 1] = pair2(c.z, c.w);
+        sl[f] = pair2(s.x, s.y); sl[f + 1] = pair2(s.z, s.w);
+      }
     }
     const uint64_t minus = pair2(-1.f, -1.f);
     const float* rows = reinterpret_cast<const float*>(sm + P.base) + f0;
@@ -869,12 +886,24 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       const float* base = rows + (i & 1) * 128;       // cos, then sin
       if (!wait(misc->ufull[i & 1], i >> 1)) break;
       tc_fence_after();
-#pragma unroll
+#pragma unroll(kTable ? 1 : 2)
       for (int g = 0; g < 2; ++g) {
         float u0[16], u1[16];
         tmem_ld_x16(t_u + 16 * g, u0);
         tmem_ld_x16(t_u + 64 + 16 * g, u1);
-        tmem_wait_ld();
+        if constexpr (kTable) {
+          float c[16], sn[16];
+          tmem_ld_x16(lanes + kTabCol + f0 + 16 * g, c);
+          tmem_ld_x16(lanes + kTabCol + 64 + f0 + 16 * g, sn);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            cl[k] = pair2(c[2 * k], c[2 * k + 1]);
+            sl[k] = pair2(sn[2 * k], sn[2 * k + 1]);
+          }
+        } else {
+          tmem_wait_ld();
+        }
         uint32_t y0[16], y1[16];                      // (higher parts, then lower)
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -883,7 +912,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint64_t cb = e == 0 ? pair2(c4.x, c4.y) : pair2(c4.z, c4.w), sb = e == 0 ? pair2(s4.x, s4.y) : pair2(s4.z, s4.w);
-            const int f = 8 * g + k + e;
+            const int f = (kTable ? 0 : 8 * g) + k + e;
             const uint64_t c = fma2(mul2(sb, sl[f]), minus, mul2(cb, cl[f])), sn = fma2(sb, cl[f], mul2(cb, sl[f]));
             const uint64_t x0 = pair2(u0[2 * (k + e)], u0[2 * (k + e) + 1]), x1 = pair2(u1[2 * (k + e)], u1[2 * (k + e) + 1]);
             split2(fma2(mul2(x1, sn), minus, mul2(x0, c)), y0[k + e], y0[8 + k + e]);
