@@ -29,7 +29,7 @@
 // unrolled all the way, instruction fetch took more time than anything else.
 //
 // Measured (the whole call, 16 heads; bytes of the latents over the time): 32 x 4096 tokens at (96, 160) with up to
-// 16 nodes 185 us, 5.5 TB/s of the 6.8 that a copy reaches; 8 x 16384 in 64-token pages with up to 64 nodes 245 us,
+// 16 nodes 184 us, 5.5 TB/s of the 6.8 that a copy reaches; 8 x 16384 in 64-token pages with up to 64 nodes 241 us,
 // 4.3 TB/s, where the softmax warps and 2,900 cycles of products a tile bound it; 128 x 4096 at (16, 32) with up to 8
 // nodes 445 us, 1.4 TB/s: a tile's fixed part, 2,600 cycles, most of them the rotation's.
 #include <algorithm>
@@ -1089,31 +1089,29 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       uint64_t pp[kBoth ? kRows / 2 : 1];
       while (true) {
         float top = -INFINITY;
-        constexpr int kCols = kRows == 32 ? 32 : 16;    // columns at a time (64 nodes: registers)
+        // (all of the lane's scores at once: the waits of one chain hide behind the others)
+        float s[kRows];
+        if constexpr (kRows == 16) tmem_ld_x16(t_s, s);
+        else tmem_ld_x32(t_s, *reinterpret_cast<float(*)[32]>(s));
+        if constexpr (kRows == 64) tmem_ld_x32(t_s + 32, *reinterpret_cast<float(*)[32]>(s + 32));
+        tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < kRows; c += kCols) {
-          float s[kCols];
-          if constexpr (kCols == 32) tmem_ld_x32(t_s + c, s);
-          else tmem_ld_x16(t_s + c, s);
-          tmem_wait_ld();
+        for (int k = 0; k < kRows / 2; k += 2) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + 2 * k);
+          const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(minus_ref + 2 * k);
 #pragma unroll
-          for (int k = 0; k < kCols / 2; k += 2) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scale + c + 2 * k);
-            const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(minus_ref + c + 2 * k);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float d0, d1;
-              unpack2(fma2(pair2(s[2 * (k + e)], s[2 * (k + e) + 1]), e == 0 ? f.x : f.y, e == 0 ? m.x : m.y), d0, d1);
-              top = fmaxf(top, fmaxf(d0, d1));
-              const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
-              const uint32_t h = pack_bf16(p0, p1);
-              if (kBoth) pp[c / 2 + k + e] = pair2(p0, p1);
-              x[c / 2 + k + e] = h;
-              asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %5, %3;\n\tfma.rn.f32.bf16 %1, h, %5, %4;\n\t}"
-                  : "=f"(d0), "=f"(d1)
-                  : "r"(h), "f"(p0), "f"(p1), "h"(static_cast<unsigned short>(0xBF80)));
-              y[c / 2 + k + e] = pack_bf16(d0, d1);
-            }
+          for (int e = 0; e < 2; ++e) {
+            float d0, d1;
+            unpack2(fma2(pair2(s[2 * (k + e)], s[2 * (k + e) + 1]), e == 0 ? f.x : f.y, e == 0 ? m.x : m.y), d0, d1);
+            top = fmaxf(top, fmaxf(d0, d1));
+            const float p0 = exp2_fast(d0), p1 = exp2_fast(d1);
+            const uint32_t h = pack_bf16(p0, p1);
+            if (kBoth) pp[k + e] = pair2(p0, p1);
+            x[k + e] = h;
+            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %5, %3;\n\tfma.rn.f32.bf16 %1, h, %5, %4;\n\t}"
+                : "=f"(d0), "=f"(d1)
+                : "r"(h), "f"(p0), "f"(p1), "h"(static_cast<unsigned short>(0xBF80)));
+            y[k + e] = pack_bf16(d0, d1);
           }
         }
         if (settled) break;
