@@ -512,3 +512,12 @@ def test_tree_binding_refusals():
         lla.DraftTree(good["tok_start"], good["parent"], lla.LLA_TREE_MAX_NODES + 1, pos=good["pos"])
     call(c, ws)
     check(c, ws)
+
+
+def test_many_sequences_without_work():
+    """Long runs of sequences without nodes or without cached tokens between others."""
+    lens, nodes = [0] * 200, [0] * 200
+    for b, L, n in ((3, 300, 2), (4, 90, 0), (70, 129, 3), (140, 0, 4), (199, 260, 1)):
+        lens[b], nodes[b] = L, n
+    c = make(lens, nodes, 2, 32, 64, 0, 0, "bf16")
+    check(c, call(c))
