@@ -171,10 +171,13 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   lo = pack_f16(x0 - h.x, x1 - h.y);
 }
-// x = hi + lo in bf16 (16 bits).
-__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+// x = hi + mid + lo in bf16: 24 bits, all that fp32 has (both lanes).
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16(x0, x1);
-  lo = pack_bf16(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xFFFF0000u));
+  x0 -= __uint_as_float(hi << 16);
+  x1 -= __uint_as_float(hi & 0xFFFF0000u);
+  mid = pack_bf16(x0, x1);
+  lo = pack_bf16(x0 - __uint_as_float(mid << 16), x1 - __uint_as_float(mid & 0xFFFF0000u));
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -1216,11 +1219,11 @@ __device__ __forceinline__ bool drop_odd(uint32_t& x) {
   return (hi | lo) != 0;
 }
 
-// Shared memory of a join block (bytes): V rows of the keys, scores or the two parts of the latent
-// sums, weights, per row {reference, cached sum, 1 / sum}.
+// Shared memory of a join block (bytes): V rows of the keys, scores and then weights, latent sums, per row
+// {reference, cached sum, 1 / sum}.
 struct JoinPlan {
-  int keys, s_pitch, p_pitch, a_pitch;               // pitches in elements
-  int v, s, p, row, bytes;       // (p: the weights in two bf16 parts)
+  int keys, s_pitch, a_pitch;                        // pitches in elements
+  int v, s, a, row, bytes;
 };
 constexpr int kJoinRows = 16;           // nodes of a join block
 __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
@@ -1228,12 +1231,11 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
   JoinPlan j{};
   j.keys = (max_nodes + 15) / 16 * 16;
   j.s_pitch = j.keys + 4;
-  j.p_pitch = j.keys + 8;
-  j.a_pitch = (r_v + 31) / 32 * 32 + 8;
+  j.a_pitch = (r_v + 31) / 32 * 32 + 4;
   int off = 0;
   j.v = off;   off += j.keys * (kHeadDim + 8) * 2;
-  j.s = off;   off += rows * j.s_pitch * 4 > 2 * rows * j.a_pitch * 2 ? rows * j.s_pitch * 4 : 2 * rows * j.a_pitch * 2;
-  j.p = off;   off += 2 * rows * j.p_pitch * 2;
+  j.s = off;   off += rows * j.s_pitch * 4;
+  j.a = off;   off += rows * j.a_pitch * 4;
   j.row = off; off += rows * 16;
   j.bytes = off;
   return j;
@@ -1246,8 +1248,7 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
 __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const JoinPlan& J, int b, int h, int first, int row0, int nr, int nk) {
   __shared__ float u[kHeadDim];
   float* ss = reinterpret_cast<float*>(sm + J.s);
-  __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(sm + J.s);
-  __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
+  float* sa = reinterpret_cast<float*>(sm + J.a);
   const int tid = threadIdx.x, r = tid >> 3, x = tid & 7, nk16 = (nk + 15) & ~15;
   const int L = tree_cached(a, b, false);
   const int64_t unit = (static_cast<int64_t>(b) * a.H + h) * a.groups + row0 / a.group;
@@ -1311,9 +1312,7 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const Jo
   for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   for (int c = x; c < nk16; c += 8) {
     const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - top) : 0.f;
-    const __nv_bfloat16 p = __float2bfloat16_rn(w);
-    sp[r * J.p_pitch + c] = p;
-    sp[(kJoinRows + r) * J.p_pitch + c] = __float2bfloat16_rn(w - __bfloat162float(p));
+    ss[r * J.s_pitch + c] = w;
     l += w;
   }
 #pragma unroll
@@ -1325,24 +1324,21 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const Jo
     reinterpret_cast<float4*>(sm + J.row)[r] = make_float4(top, held, row ? 1.f / l : 0.f, 0.f);
     if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (top + log2f(l)) * kLn2;
   }
-  __syncthreads();                                    // (the scores have been read)
 #pragma unroll
   for (int k = 0; k < kMaxRankPerHead / 8; ++k) {
     const int c = x + 8 * k;
-    if (c >= J.a_pitch - 8) break;
-    const float y = row ? acc[k] * f : 0.f;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(y);
-    sa[r * J.a_pitch + c] = hi;
-    sa[(kJoinRows + r) * J.a_pitch + c] = __float2bfloat16_rn(y - __bfloat162float(hi));
+    if (c >= J.a_pitch - 4) break;
+    sa[r * J.a_pitch + c] = row ? acc[k] * f : 0.f;
   }
 }
 
 // Block = 16 nodes of a (sequence, head); its four warps split the keys, then the output's dimensions.
 //   S = Q^ K^^T over the nodes' keys, masked to each node's path; reference M over S and the records
-//   P = 2^(S - M), A = sum of the records' latent sums times 2^(m - M) (in two bf16 parts, 16 bits)
+//   P = 2^(S - M), A = sum of the records' latent sums times 2^(m - M), both fp32
 //   out = (A W_up,v^T + P V + held mu_v) / l
 // by warp-level products whose operands come straight from global memory (L2) where they are read
-// along K (Q^ and K^ in two f16 parts, P and A in two bf16 parts).  Bound by the latency of its few steps; blocks are
+// along K (Q^ and K^ in two f16 parts; P and A as the three bf16 parts that hold an fp32 value, split where a
+// product takes them: with two parts, 16 bits, one output in 500 took the other neighbour in its rounding).  Bound by the latency of its few steps; blocks are
 // small so that many run at a time: 16 us for 512 blocks, 65 for 2048 with 128 keys (80 registers and six blocks an
 // SM instead of four, with half of the values held at a time: no faster).  The
 // scores need nothing of the tile kernel, so they are made before the wait for it (its blocks let this
@@ -1354,8 +1350,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const JoinPlan J = join_plan(a.max_nodes, a.r_v);
   __nv_bfloat16* sv = reinterpret_cast<__nv_bfloat16*>(sm + J.v);
   float* ss = reinterpret_cast<float*>(sm + J.s);
-  __nv_bfloat16* sa = reinterpret_cast<__nv_bfloat16*>(sm + J.s);          // (over the scores once they are weights)
-  __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(sm + J.p);
+  float* sa = reinterpret_cast<float*>(sm + J.a);
   float4* srow = reinterpret_cast<float4*>(sm + J.row);
   const int tid = threadIdx.x, lane = tid & 31, part = tid >> 5, g = lane >> 2, q = lane & 3;
   const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, row0 = blockIdx.y * kRows, grp = row0 / a.group;
@@ -1432,6 +1427,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 
   // ---- reference, weights and sums: eight lanes a row
   bool lost = false;
+  float p[kTreeMaxNodes / 8];
   {
     const int r = tid >> 3, x = tid & 7;
     const bool row = r < nr;
@@ -1442,12 +1438,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f, held = 0.f;
-    for (int c = x; c < nk16; c += 8) {
-      const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f;
-      const __nv_bfloat16 p = __float2bfloat16_rn(w);
-      sp[r * J.p_pitch + c] = p;
-      sp[(kRows + r) * J.p_pitch + c] = __float2bfloat16_rn(w - __bfloat162float(p));
-      l += w;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxNodes / 8; ++k) {
+      if (8 * k >= nk16) break;
+      const int c = x + 8 * k;
+      p[k] = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f;
+      l += p[k];
     }
     for (int i = x; i < nrec && row; i += 8) {
       const float4 head = __ldcg(reinterpret_cast<const float4*>(rec + i * next));
@@ -1465,10 +1461,18 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
       if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (m + log2f(l)) * kLn2;
     }
   }
-  // ---- latent sums of the records, relative to M, in two bf16 parts
-  const int cols = J.a_pitch - 8, per = cols / 4;
+  // ---- weights over the scores (which join_again reads); latent sums of the records, relative to M
+  const int cols = J.a_pitch - 4, per = cols / 4;
   const bool again = __syncthreads_or(lost);
-  if (again) join_again(a, sm, J, b, h, first, row0, nr, nk);
+  if (again) {
+    join_again(a, sm, J, b, h, first, row0, nr, nk);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kTreeMaxNodes / 8; ++k) {
+      if (8 * k >= nk16) break;
+      ss[(tid >> 3) * J.s_pitch + (tid & 7) + 8 * k] = p[k];
+    }
+  }
   for (int i = tid; i < kRows * per && !again; i += kJoinThreads) {
     const int r = i / per, c = (i - r * per) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1482,11 +1486,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
         x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y); x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
       }
     }
-    uint32_t h0, h1, l0, l1;
-    split_bf16(x.x, x.y, h0, l0);
-    split_bf16(x.z, x.w, h1, l1);
-    *reinterpret_cast<uint2*>(sa + r * J.a_pitch + c) = make_uint2(h0, h1);
-    *reinterpret_cast<uint2*>(sa + (kRows + r) * J.a_pitch + c) = make_uint2(l0, l1);
+    *reinterpret_cast<float4*>(sa + r * J.a_pitch + c) = x;
   }
   __syncthreads();
 
@@ -1497,29 +1497,30 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const int e0 = part * (kHeadDim / kSplit);
   const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_v) + (static_cast<int64_t>(h) * kHeadDim + e0 + g) * a.r_v;
   for (int c = 0; c < cols && nrec > 0; c += 32) {
-    const __nv_bfloat16* ah = sa + g * J.a_pitch + c + 8 * q;
-    const __nv_bfloat16* al = ah + kRows * J.a_pitch;
-    const uint4 h0 = *reinterpret_cast<const uint4*>(ah), h1 = *reinterpret_cast<const uint4*>(ah + 8 * J.a_pitch);
-    const uint4 l0 = *reinterpret_cast<const uint4*>(al), l1 = *reinterpret_cast<const uint4*>(al + 8 * J.a_pitch);
-    uint4 x[kTiles];
+    uint4 x[kTiles], y[2][3];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
       x[t] = c + 8 * q < a.r_v ? __ldg(reinterpret_cast<const uint4*>(W + static_cast<int64_t>(8 * t) * a.r_v + c + 8 * q)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      mma_k32(acc[t], h0, h1, x[t]);
-      mma_k32(acc[t], l0, l1, x[t]);
+    for (int r = 0; r < 2; ++r) {                     // rows g and g + 8
+      const float* from = sa + (g + 8 * r) * J.a_pitch + c + 8 * q;
+      const float4 u = *reinterpret_cast<const float4*>(from), v = *reinterpret_cast<const float4*>(from + 4);
+      split_bf16(u.x, u.y, y[r][0].x, y[r][1].x, y[r][2].x);
+      split_bf16(u.z, u.w, y[r][0].y, y[r][1].y, y[r][2].y);
+      split_bf16(v.x, v.y, y[r][0].z, y[r][1].z, y[r][2].z);
+      split_bf16(v.z, v.w, y[r][0].w, y[r][1].w, y[r][2].w);
     }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) mma_k32(acc[t], y[0][e], y[1][e], x[t]);
   }
   for (int k = 0; k < nk16; k += 16) {
-    uint32_t x[2][4];                                 // (both parts of the weights)
+    uint32_t x[4][3];                                 // (all parts of the weights: rows g and g + 8, keys 2 q and 2 q + 8)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const __nv_bfloat16* p = sp + (e * kRows + g) * J.p_pitch + k + 2 * q;
-      x[e][0] = *reinterpret_cast<const uint32_t*>(p);
-      x[e][1] = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch);
-      x[e][2] = *reinterpret_cast<const uint32_t*>(p + 8);
-      x[e][3] = *reinterpret_cast<const uint32_t*>(p + 8 * J.p_pitch + 8);
+    for (int e = 0; e < 4; ++e) {
+      const float2 u = *reinterpret_cast<const float2*>(ss + (g + 8 * (e & 1)) * J.s_pitch + k + 2 * q + 8 * (e >> 1));
+      split_bf16(u.x, u.y, x[e][0], x[e][1], x[e][2]);
     }
 #pragma unroll
     for (int t = 0; t < kTiles; t += 2) {
@@ -1529,9 +1530,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
                    : "r"(smem_u32(sv + (k + (lane & 15)) * (kHeadDim + 8) + e0 + 8 * t + 8 * (lane >> 4)))
                    : "memory");
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mma16816(acc[t], x[e][0], x[e][1], x[e][2], x[e][3], b0, b1);
-        mma16816(acc[t + 1], x[e][0], x[e][1], x[e][2], x[e][3], b2, b3);
+      for (int e = 0; e < 3; ++e) {
+        mma16816(acc[t], x[0][e], x[1][e], x[2][e], x[3][e], b0, b1);
+        mma16816(acc[t + 1], x[0][e], x[1][e], x[2][e], x[3][e], b2, b3);
       }
     }
   }
@@ -1542,13 +1543,13 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
       for (int r = 0; r < 2; ++r) {
         const int row = g + 8 * r;
         if (row >= nr || !(__ldcg(reinterpret_cast<const uint32_t*>(a.paths + static_cast<int64_t>(b) * a.max_nodes + row0 + row) + (j >> 5)) >> (j & 31) & 1)) continue;
-        const float p = __bfloat162float(sp[row * J.p_pitch + j]) + __bfloat162float(sp[(kRows + row) * J.p_pitch + j]);
+        const float w = ss[row * J.s_pitch + j];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float y = __bfloat162float(v[8 * t + 2 * q + k]);
-            if (!isfinite(y)) acc[t][2 * r + k] = fmaf(p, y, acc[t][2 * r + k]);
+            if (!isfinite(y)) acc[t][2 * r + k] = fmaf(w, y, acc[t][2 * r + k]);
           }
       }
     }

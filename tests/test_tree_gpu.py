@@ -521,3 +521,52 @@ def test_many_sequences_without_work():
         lens[b], nodes[b] = L, n
     c = make(lens, nodes, 2, 32, 64, 0, 0, "bf16")
     check(c, call(c))
+
+
+def _half_step(o):
+    """Half a step of bf16 at values o."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(o), 1e-30))) - 8)
+
+
+def test_drafted_weights_are_not_rounded():
+    """bf16 storage, two nodes and no cached tokens, scores that keys and queries of 22 bits give exactly but for
+    2^-22 of at most 0.4: an output is off by half a step and, relative to the sum of |p v|, by the exponential's two units
+    (2^-22), the score (2^-24), three products' sums (2^-23 each), sum, division and scaling (2^-24 each): below 2^-20."""
+    B, H = 256, 16
+    c = make([0] * B, [2] * B, H, 16, 16, dtype="bf16", pad=0, branch=1)
+    c["pos"].zero_()
+    c["qkv"][:, :2 * H, 1:] = 0.0
+    c["qkv"][:, :H, 0] = 1.0
+    ws = call(c)
+    assert lla.device_status(ws) == lla.LLA_OK
+    x = widen(c["qkv"]).reshape(B, 2, 3, H, D)
+    s = x[:, :, 1, :, 0] / np.sqrt(D)
+    p = np.exp(s - s.max(1, keepdims=True))[..., None]
+    o, mass = (p * x[:, :, 2]).sum(1) / p.sum(1), (p * np.abs(x[:, :, 2])).sum(1) / p.sum(1)
+    err = np.abs(widen(c["out"]).reshape(B, 2, H, D)[:, 1] - o)
+    assert (err <= _half_step(o) + 2.0 ** -20 * mass).all(), int((err > _half_step(o) + 2.0 ** -20 * mass).sum())
+
+
+@pytest.mark.parametrize("nodes,page", [(1, 0), (20, 24), (40, 0)])
+def test_latent_sums_are_not_rounded(nodes, page):
+    """bf16 storage, equal weights (queries of 0) and latents of one component: out = W sum(c) / l, where the sum, in
+    24 bits, is off by 2^-24 a cached token, and three products' sums (2^-23 each), division and scaling (2^-24 each) follow:
+    below 2^-20 of the value, beside half a step."""
+    B, H, L = 64, 16, 5
+    c = make([L] * B, [nodes] * B, H, 16, 32, page, dtype="bf16", pad=0, branch=1)
+    c["qkv"][:, :H] = 0.0
+    c["qkv"][:, 2 * H:] = 0.0
+    c["mv"].zero_()
+    c["cv"].nan_to_num_(0.0)
+    c["cv"][..., :3] = 0.0
+    c["cv"][..., 4:] = 0.0
+    c["cv"] *= (2.0 ** (-3.0 * torch.arange(c["cv"].shape[2], device="cuda")))[:, None].bfloat16()     # (sums of 20 bits)
+    ws = call(c)
+    assert lla.device_status(ws) == lla.LLA_OK
+    cv = widen(c["cv"])[..., 3]
+    total = cv[:, :, :L].sum(-1) if not page else cv[c["table"][:, 0].cpu().numpy()][:, :, :L].sum(-1)      # [B][H]
+    got = widen(c["out"]).reshape(B, nodes, H, D)
+    depth = np.arange(1, nodes + 1)[None, :, None, None]                                               # (chains)
+    o = total[:, None, :, None] * widen(c["wv"])[c["t"]][None, None, :, :, 3] / (L + depth)
+    err, tol = np.abs(got - o), _half_step(o) + 2.0 ** -20 * np.abs(o)
+    assert (err <= tol).all(), int((err > tol).sum())
