@@ -48,6 +48,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
 constexpr float kHeadroom = 32.f;                   // a score this far above its reference (log2 units) moves it
+// The tensor core cuts its sums off at 24 bits: up to 2^-23 of a sum is lost with every 16 tokens, always downwards
+// (65536 tokens in one sum: log-sum-exp 1e-4 off, outputs 5e-4).  So a unit's latent sums go to its record, and
+// start anew, every 64 tiles (512 steps, 2^-14 at most), and the sums of weights of 64 nodes to a register every 8.
+constexpr int kSumTiles = 64, kWeightTiles = 8;
 constexpr int kPrepThreads = 256;
 constexpr int kRotWarps = 8;
 constexpr int kSoftWarp0 = 4 + kRotWarps;
@@ -837,7 +841,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!wait(misc->pfull[j & 1], j >> 1)) break;
       tc_fence_after();
       const uint64_t a0 = d_v + vr.slot * vst, b0 = d_p + (j % kPBuf) * (kPTile / 16);
-      const uint32_t sum = !(j == 0 || w.t == 0);     // a unit's first product starts the sum
+      // a unit's first product starts the sums, and every kSumTiles-th or kWeightTiles-th does again
+      const uint32_t sum = j > 0 && w.t % kSumTiles != 0, sum_w = j > 0 && w.t % kWeightTiles != 0;
       if (elected()) {
 #pragma unroll 1
         for (int blk = 0; blk < blocks; ++blk)
@@ -848,7 +853,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             if (kBoth) umma_bf16(tmem + kDCol + blk * kDCols, a0 + blk * block_step + o, b0 + k * kPRow, idesc, k > 0 || sum);
             else {
               umma_bf16(tmem + kDCol, b0 + k * kPRow, a0 + o, idesc, k > 0 || sum);
-              umma_bf16(tmem + kDCol + a.r_v, b0 + k * kPRow, d_sum, idesc_sum, k > 0 || sum);
+              umma_bf16(tmem + kDCol + a.r_v, b0 + k * kPRow, d_sum, idesc_sum, k > 0 || sum_w);
             }
           }
         umma_commit(bar(misc->vdone[j & 1]));
@@ -956,8 +961,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return wait(misc->vote, votes++);
     };
     const uint64_t minus = pair2(-1.f, -1.f);
-    // sums of the weights of this lane's tokens, nodes by twos (64 nodes: D has them)
+    // sums of the weights of this lane's tokens, nodes by twos (64 nodes: D has them, and the lane's node here what
+    // has left it)
     uint64_t l[kBoth ? kRows / 2 : 1];
+    float l_node = 0.f;
+    // whether the record has latent sums of this unit, and what they are relative to
+    bool held = false;
+    float held_ref[kMine];
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
     // is higher, or if it is the unit's first
@@ -994,8 +1004,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       __syncwarp();
       return true;
     };
-    // the finished unit's sums (its last product was tile `last`): D's lanes are columns of the latent
-    auto finish = [&](int last) -> bool {
+    // the unit's sums (the last product was tile `last`) into its record; `whole`: it is finished.  D's lanes are
+    // columns of the latent
+    auto finish = [&](int last, bool whole) -> bool {
       if (!wait(misc->vdone[last & 1], last >> 1)) return false;
       tc_fence_after();
       int first;
@@ -1004,24 +1015,30 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       const int stride = a.r_v + kTreeHead;
       float* rec = a.records + slot * a.rec_rows * stride;
 #pragma unroll
-      for (int j = 0; j < kMine; ++j)
+      for (int j = 0; j < kMine; ++j) {
         if (quad == 0 && lane + 32 * j < n) rec[(lane + 32 * j) * stride] = refs[j];
+        if (lane + 32 * j < kRows) factor[lane + 32 * j] = exp2f(held_ref[j] - refs[j]);       // (all four warps the same)
+        held_ref[j] = refs[j];
+      }
+      __syncwarp();
       if constexpr (kBoth) {
         // the lanes' sums through the warp's own rows of the weights, which have been read
-        float* own = reinterpret_cast<float*>(sm + P.p + (last % kPBuf) * kPTile + quad * (32 * kPRow));
+        if (whole) {
+          float* own = reinterpret_cast<float*>(sm + P.p + (last % kPBuf) * kPTile + quad * (32 * kPRow));
 #pragma unroll
-        for (int k = 0; k < kRows / 2; ++k) {
-          float l0, l1;
-          unpack2(l[k], l0, l1);
-          own[64 * k + lane] = l0;
-          own[64 * k + 32 + lane] = l1;
-        }
-        __syncwarp();
-        if (lane < n) {
-          float sum = 0.f;
+          for (int k = 0; k < kRows / 2; ++k) {
+            float l0, l1;
+            unpack2(l[k], l0, l1);
+            own[64 * k + lane] = l0;
+            own[64 * k + 32 + lane] = l1;
+          }
+          __syncwarp();
+          if (lane < n) {
+            float sum = 0.f;
 #pragma unroll 4
-          for (int k = 0; k < 32; ++k) sum += own[32 * lane + ((k + lane) & 31)];
-          rec[lane * stride + 1 + quad] = sum;
+            for (int k = 0; k < 32; ++k) sum += own[32 * lane + ((k + lane) & 31)];
+            rec[lane * stride + 1 + quad] = sum;
+          }
         }
         for (int blk = 0; blk < P.blocks; ++blk) {
           const int r = blk * 128 + row;
@@ -1031,9 +1048,17 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             tmem_ld_x16(lanes + kDCol + blk * kDCols + c, v);
             tmem_ld_x16(lanes + kDCol + blk * kDCols + kRows + c, low);
             tmem_wait_ld();
+            float* to = rec + c * stride + kTreeHead + r;
+            if (held) {
+              float before[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) before[k] = c + k < n && r < a.r_v ? to[k * stride] : 0.f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) low[k] = fmaf(before[k], factor[c + k], low[k]);
+            }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              if (c + k < n && r < a.r_v) rec[(c + k) * stride + kTreeHead + r] = v[k] + low[k];
+              if (c + k < n && r < a.r_v) to[k * stride] = v[k] + low[k];
           }
         }
       } else {
@@ -1041,10 +1066,16 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         // has been read, 16 columns at a time
         float* pass = reinterpret_cast<float*>(sm + P.p) + (row & 63) * 20;
 #pragma unroll 1
-        for (int c = 0; c <= a.r_v; c += 16) {
+        for (int c = 0; whole ? c <= a.r_v : c < a.r_v; c += 16) {
           float v[16];
+          float4 before[4];
+          float* to = rec + row * stride + kTreeHead + c;
+          const bool more = held && quad < 2 && row < n && c < a.r_v;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) before[k] = more ? *reinterpret_cast<const float4*>(to + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
           tmem_ld_x16(lanes + kDCol + c, v);
           tmem_wait_ld();
+          if (c == a.r_v) v[0] += l_node;
           if (quad >= 2) {
 #pragma unroll
             for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(pass + (c & 16) * 80 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
@@ -1054,14 +1085,18 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
             for (int k = 0; k < 16; k += 4) {
               const float4 y = *reinterpret_cast<const float4*>(pass + (c & 16) * 80 + k);
-              const float4 z = make_float4(v[k] + y.x, v[k + 1] + y.y, v[k + 2] + y.z, v[k + 3] + y.w);
-              if (c < a.r_v) *reinterpret_cast<float4*>(rec + row * stride + kTreeHead + c + k) = z;
+              const float f = more ? factor[row & 63] : 0.f;
+              const float4 o = before[k / 4];
+              const float4 z = make_float4(v[k] + fmaf(o.x, f, y.x), v[k + 1] + fmaf(o.y, f, y.y), v[k + 2] + fmaf(o.z, f, y.z),
+                                           v[k + 3] + fmaf(o.w, f, y.w));
+              if (c < a.r_v) *reinterpret_cast<float4*>(to + k) = z;
               else rec[row * stride + 1 + k / 4] = k == 0 ? z.x : 0.f;
             }
           }
         }
       }
       tc_fence_before();
+      held = !whole;
       return true;
     };
     for (int i = 0; i <= count && count > 0; ++i) {
@@ -1072,8 +1107,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
         for (int j = 0; j < kMine; ++j) back[j] = (lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f) * __ldcg(&a.head_scale[w.h]).y;
       }
-      if (i > 0 && (fresh || i == count)) {
-        if (!finish(i - 1)) break;
+      if (i > 0 && (i == count || w.t % kSumTiles == 0)) {
+        if (!finish(i - 1, fresh || i == count)) break;
         cur_b = w.b; cur_h = w.h; cur_g = w.g;
       }
       if (i == count || !wait(misc->sfull[i & 1], i >> 1)) break;
@@ -1084,6 +1119,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!move(t_s, live, true)) break;
 #pragma unroll
         for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = 0;
+        l_node = 0.f;
       }
       // Weights, in two bf16 parts as the product takes them.  Where a score is too far above its reference, the
       // references move and the weights are made again.
@@ -1138,6 +1174,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           tmem_st_x8(lanes + kDCol + c, z);
         }
         tmem_wait_st();
+        if (!kBoth) l_node *= factor[row % kRows];
 #pragma unroll
         for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
       }
@@ -1147,6 +1184,13 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(misc->sfree[i & 1]));
         if (i > 0 && !wait(misc->vdone[(i - 1) & 1], (i - 1) >> 1)) break;     // the last weights have been read
+        if (!fresh && w.t % kWeightTiles == 0) {      // (their sum starts anew with this tile's)
+          float v[8];
+          tc_fence_after();
+          tmem_ld_x8(lanes + kDCol + a.r_v, v);
+          tmem_wait_ld();
+          l_node += v[0];
+        }
       }
       if (partial) {                                    // a token past the end has none
 #pragma unroll

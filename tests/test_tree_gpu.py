@@ -570,3 +570,40 @@ def test_latent_sums_are_not_rounded(nodes, page):
     o = total[:, None, :, None] * widen(c["wv"])[c["t"]][None, None, :, :, 3] / (L + depth)
     err, tol = np.abs(got - o), _half_step(o) + 2.0 ** -20 * np.abs(o)
     assert (err <= tol).all(), int((err > tol).sum())
+
+
+@pytest.mark.parametrize("nodes,B,std", [(64, 10, 1.0), (64, 10, 3.0), (128, 5, 1.0), (24, 10, 1.0), (10, 10, 3.0)])
+def test_long_sums(nodes, B, std):
+    """65536 cached tokens, a unit's in one block's sums, values that do not cancel.  The log-sum-exp as exact as fp32 makes
+    it (2e-5: scores of up to 15 with 22 bits, 2^-18, and sums cut off for 64 steps, 2^-17); outputs off by half a step
+    and by sums cut off for 512 steps of 2^-23 (2^-14 of the sum, all its terms being positive), parts of 16 bits and those scores."""
+    H, L, rk, rv = 16, 65536, 16, 32
+    g = torch.Generator(device="cuda").manual_seed(nodes)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dm, n = lla.dims(1, H, rk, rv), B * nodes
+    qkv = rnd(n, 3 * H, D).bfloat16()
+    qkv[:, :H] *= std
+    ck, cv = rnd(B, H, L, rk).bfloat16(), (1 + 0.1 * rnd(B, H, L, rv)).bfloat16()
+    wk, wv = (rnd(1, H, D, rk) / 4).bfloat16(), (rnd(1, H, D, rv).abs() / 6).bfloat16()
+    zero = torch.zeros(H, D, device="cuda")
+    ang = torch.arange(L + 1, dtype=torch.float64, device="cuda")[:, None] * 10000.0 ** (-2.0 * torch.arange(64, dtype=torch.float64, device="cuda") / D)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    tree = lla.DraftTree(i32([nodes * b for b in range(B + 1)]), i32([-1] * n), nodes, pos=i32([L] * n))
+    out, lse = torch.zeros(n, H, D, device="cuda", dtype=torch.bfloat16), torch.zeros(n, H, device="cuda")
+    ws = lla.tree_workspace(dm, tree, L)
+    lla.tree_attn(dm, 0, tree, qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:], ck, cv, i32([L] * B), wk, wv, zero, zero, cos, sin, out, lse, ws)
+    assert lla.device_status(ws) == lla.LLA_OK
+    turn = lambda x, at: torch.cat((x[..., :64] * cos[at].double() - x[..., 64:] * sin[at].double(),  # noqa: E731
+                                    x[..., :64] * sin[at].double() + x[..., 64:] * cos[at].double()), -1)
+    for b, h in ((0, 0), (B // 2, 7), (B - 1, 15)):
+        own = slice(b * nodes, (b + 1) * nodes)
+        q, kd = turn(qkv[own, h].double(), L), turn(qkv[own, H + h].double(), L)
+        k = turn(ck[b, h].double() @ wk[0, h].double().T, slice(0, L))
+        s = torch.cat((q @ k.T, (q * kd).sum(-1, keepdim=True)), -1) / D ** 0.5
+        assert (lse[own, h].double() - torch.logsumexp(s, -1)).abs().max() <= 2e-5
+        p = torch.softmax(s, -1)
+        cached = (p[:, :L] @ cv[b, h].double()) @ wv[0, h].double().T
+        o = (cached + p[:, L:] * qkv[own, 2 * H + h].double()).cpu().numpy()
+        err = np.abs(widen(out[own, h]) - o)
+        assert (err <= _half_step(o) + 2.0 ** -13 * np.abs(cached.cpu().numpy())).all()
