@@ -961,13 +961,14 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       return wait(misc->vote, votes++);
     };
     const uint64_t minus = pair2(-1.f, -1.f);
-    // sums of the weights of this lane's tokens, nodes by twos (64 nodes: D has them, and the lane's node here what
-    // has left it)
+    // sums of the weights of this lane's tokens, nodes by twos (64 nodes: D has them, and the lane's node in shared
+    // memory, where only this lane reads, what has left it)
     uint64_t l[kBoth ? kRows / 2 : 1];
-    float l_node = 0.f;
-    // whether the record has latent sums of this unit, and what they are relative to
+    float* l_node = maxima + 8 * kRows + row;
+    // whether the record has latent sums of this unit, and what they are relative to (each warp has its own
+    // copy; of 64 nodes there is one, written after all four have read it)
     bool held = false;
-    float held_ref[kMine];
+    float* held_ref = maxima + 8 * kRows + (kBoth ? quad * kRows : kTile);
     int cur_b = w.b, cur_h = w.h, cur_g = w.g;
     // the largest score of every node in tile S (t_s), over the four warps, becomes its reference if that
     // is higher, or if it is the unit's first
@@ -1017,8 +1018,11 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
 #pragma unroll
       for (int j = 0; j < kMine; ++j) {
         if (quad == 0 && lane + 32 * j < n) rec[(lane + 32 * j) * stride] = refs[j];
-        if (lane + 32 * j < kRows) factor[lane + 32 * j] = exp2f(held_ref[j] - refs[j]);       // (all four warps the same)
-        held_ref[j] = refs[j];
+        const int c = lane + 32 * j;
+        if (c < kRows) {
+          if (held) factor[c] = exp2f(held_ref[c] - refs[j]);
+          if (kBoth && !whole) held_ref[c] = refs[j];
+        }
       }
       __syncwarp();
       if constexpr (kBoth) {
@@ -1075,7 +1079,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           for (int k = 0; k < 4; ++k) before[k] = more ? *reinterpret_cast<const float4*>(to + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
           tmem_ld_x16(lanes + kDCol + c, v);
           tmem_wait_ld();
-          if (c == a.r_v) v[0] += l_node;
+          if (c == a.r_v) v[0] += *l_node;
           if (quad >= 2) {
 #pragma unroll
             for (int k = 0; k < 16; k += 4) *reinterpret_cast<float4*>(pass + (c & 16) * 80 + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
@@ -1094,6 +1098,10 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
             }
           }
         }
+      }
+      if (!kBoth && !whole && quad == 0) {            // (votes lie between)
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) held_ref[lane + 32 * j] = refs[j];
       }
       tc_fence_before();
       held = !whole;
@@ -1119,7 +1127,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (!move(t_s, live, true)) break;
 #pragma unroll
         for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = 0;
-        l_node = 0.f;
+        if (!kBoth) *l_node = 0.f;
       }
       // Weights, in two bf16 parts as the product takes them.  Where a score is too far above its reference, the
       // references move and the weights are made again.
@@ -1174,7 +1182,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           tmem_st_x8(lanes + kDCol + c, z);
         }
         tmem_wait_st();
-        if (!kBoth) l_node *= factor[row % kRows];
+        if (!kBoth) *l_node *= factor[row % kRows];
 #pragma unroll
         for (int k = 0; k < (kBoth ? kRows / 2 : 0); ++k) l[k] = mul2(l[k], *reinterpret_cast<const uint64_t*>(factor + 2 * k));
       }
@@ -1189,7 +1197,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           tc_fence_after();
           tmem_ld_x8(lanes + kDCol + a.r_v, v);
           tmem_wait_ld();
-          l_node += v[0];
+          *l_node += v[0];
         }
       }
       if (partial) {                                    // a token past the end has none
@@ -1628,7 +1636,7 @@ bool make_tree_plan(int r_k, int r_v, int rows, TreePlan* p) {
   p->k_stage = al(p->kplan.bytes);
   p->v_stage = al(p->vplan.bytes);
   // weights in two parts (two buffers of them for up to 32 nodes); queries (two parts), W, bias, ones
-  const int weights = kTile * rows * 2 * 2 * (rows <= 32 ? 2 : 1), refs = 11 * rows * 4;
+  const int weights = kTile * rows * 2 * 2 * (rows <= 32 ? 2 : 1), refs = rows <= 32 ? 15 * rows * 4 : 12 * rows * 4 + kTile * 4;
   const int fixed = rows * 512 + al(p->kplan.bytes) + weights + 4096 + 512 + refs + 1024 + 256 + 768 + 1024;
   auto fits = [&](int sk, int sv) { return fixed + sk * p->k_stage + sv * p->v_stage <= kSmemLimit; };
   if (!fits(1, 1)) return false;
