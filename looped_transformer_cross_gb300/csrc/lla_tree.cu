@@ -550,7 +550,7 @@ bool tensor_path(const lla_dims* d) {
 struct TreeWs {
   int64_t chunk;
   int splits, grid;
-  size_t turned, v_turned, tile_start, cta_start, head_scale, bias, qimg, qback, khat, kback, paths, records, total;
+  size_t turned, v_turned, tile_start, cta_start, head_top, unit_top, bias, qimg, qback, khat, kback, paths, records, total;
 };
 
 TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, bool tensor) {
@@ -564,8 +564,9 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
     w.grid = static_cast<int>(std::min<int64_t>(std::min(sms, kMaxGrid), most));
     w.tile_start = 256;
     w.cta_start = al(w.tile_start + (static_cast<size_t>(B) + 1) * 4);
-    w.head_scale = w.cta_start + static_cast<size_t>(w.grid) * 16;
-    w.bias = al(w.head_scale + static_cast<size_t>(d->H) * 8);
+    w.head_top = w.cta_start + static_cast<size_t>(w.grid) * 16;
+    w.unit_top = w.head_top + static_cast<size_t>(d->H) * 8;
+    w.bias = al(w.unit_top + static_cast<size_t>(units) * 4);
     w.qimg = w.bias + static_cast<size_t>(d->H) * 4096;
     w.qback = w.qimg + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 512;
     w.khat = al(w.qback + static_cast<size_t>(units * groups) * tree_rows(max_nodes, d->r_v) * 4);
@@ -729,7 +730,8 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
     a.grid = w.grid;
     a.tile_start = reinterpret_cast<int32_t*>(ws + w.tile_start);
     a.cta_start = reinterpret_cast<int4*>(ws + w.cta_start);
-    a.head_scale = reinterpret_cast<float2*>(ws + w.head_scale);
+    a.head_top = reinterpret_cast<float2*>(ws + w.head_top);
+    a.unit_top = reinterpret_cast<float*>(ws + w.unit_top);
     a.bias = ws + w.bias;
     a.qimg = ws + w.qimg;
     a.qback = reinterpret_cast<float*>(ws + w.qback);

@@ -73,7 +73,8 @@ struct TreeArgs {
   float* kback;                      // [B H][max_nodes]
   uint4* paths;                      // [B][max_nodes] nodes on each node's path, as bits
   uint8_t* bias;                     // [H][4096] mu operands
-  float2* head_scale;                // [H] powers of two: what cached keys are scaled by, and what undoes it
+  float2* head_top;                  // [H] largest row sum of |W_up,k|, largest |mu_k|
+  float* unit_top;                   // [B H] the size of its K latents: the quartile of some tokens' largest values
   TreePlan plan;
 };
 

@@ -10,9 +10,11 @@
 //   D += C_v^T P              r_v x nodes, both operands MN-major from shared memory
 // K^, Q^ and P are each the sum of two 16-bit parts: one rounding to bf16 of each made the log-sum-exp 1e-3
 // off and an output 1.5 times as far off as its own rounding.  K^ and Q^ are f16 + f16 (22 bits; products
-// high x high, high x low, low x high), scaled by powers of two first: a row of Q^ to 1..2, a head's keys by
-// what brings the largest row sum of |W| and |mu| to 16..32.  So latents up to 2^11 have keys in range at any
-// weights; keys beyond make the sums NaN, and the join then takes the cached tokens again in fp32.  P is
+// high x high, high x low, low x high), scaled by powers of two first: a row of Q^ to 1..2, a unit's keys by
+// what brings a bound of them (row sums of |W| times a latent's largest value, and |mu|) to 16..32 at the upper
+// quartile of 16 of its tokens.  A component is then off by 2^-22 of itself, or of 2^-8 of that bound where it is
+// smaller, at any sizes of latents and weights; keys 2^11 times beyond the bound make the sums NaN, and the join then
+// takes the cached tokens again in fp32.  P is
 // bf16 + bf16 (16 bits at any size).
 // A key is reconstructed and rotated once for all nodes of its block, V never is, and the
 // products and exponentials of S and D are made for 16, 32 or 64 nodes, not for a full 128 rows.
@@ -52,7 +54,7 @@ constexpr float kHeadroom = 32.f;                   // a score this far above it
 // (65536 tokens in one sum: log-sum-exp 1e-4 off, outputs 5e-4).  So a unit's latent sums go to its record, and
 // start anew, every 64 tiles (512 steps, 2^-14 at most), and the sums of weights of 64 nodes to a register every 8.
 constexpr int kSumTiles = 64, kWeightTiles = 8;
-constexpr int kPrepThreads = 256;
+constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 constexpr int kRotWarps = 8;
 constexpr int kSoftWarp0 = 4 + kRotWarps;
 constexpr int kTreeThreads = 32 * (kSoftWarp0 + 4);
@@ -195,6 +197,15 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8
                : "memory");
 }
 
+// What the cached keys of a (sequence, head) are scaled by, and what undoes it: the power of two that brings the
+// bound of its keys (see above) to 16..32, within what products of these powers with others leave finite.
+__device__ __forceinline__ float2 key_scale(const TreeArgs& a, int b, int h) {
+  const float2 top = __ldcg(&a.head_top[h]);
+  const float bound = fmaf(top.x, __ldcg(a.unit_top + b * a.H + h), top.y);
+  const int power = min(60, max(-60, 131 - static_cast<int>((__float_as_uint(bound) >> 23) & 255u)));
+  return make_float2(__int_as_float((127 + power) << 23), __int_as_float((127 - power) << 23));
+}
+
 __device__ __forceinline__ int page_at(const TreeArgs& a, int b, int lp) {
   const int pg = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_pages + lp);
   return min(max(pg, 0), static_cast<int>(a.num_pages) - 1);
@@ -321,27 +332,68 @@ __device__ __forceinline__ void turn_pairs8(const float (&x0)[8], const float (&
   }
 }
 
-// Blocks 0 .. units-1: the unit's query operand, RoPE(q, pos) log2(e)/sqrt(d) as two f16 parts, each the
+// First a warp a (sequence, head): the size of its K latents, by which its cached keys are scaled.  Then a block a
+// unit: its query operand, RoPE(q, pos) log2(e)/sqrt(d) as two f16 parts, each the
 // shared-memory image (two chunks of 64 columns, 128-byte rows, swizzled), and its drafted keys, RoPE(k, pos)
 // likewise, row by row; dimensions in the order first members of the pairs, then second members, as U's.
 // Then B blocks: the nodes on each node's path as bits, and the checks of a sequence's values.  Then H
-// blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits), and the power of two that the
-// head's cached keys are scaled by.  The last
+// blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits), and the largest row sum of
+// |W_up,k| and |mu|.  The last
 // block: tiles per sequence, and every CTA's first tile.
 __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid_constant__ TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   const int units = a.B * a.H * a.groups;
-  if (blockIdx.x < units) {
-    const int bh = blockIdx.x / a.groups, g = blockIdx.x - bh * a.groups;
+  const int sized = (a.B * a.H + kPrepWarps - 1) / kPrepWarps;
+  if (blockIdx.x < sized) {
+    // a warp a (sequence, head): the largest values of the K latents of 16 tokens from the first to the last, 16 bytes
+    // a lane, and their upper quartile, without zeros
+    constexpr int kSampled = 16, kAtOnce = 4;
+    __shared__ uint32_t most[kPrepWarps][kSampled];
+    const int warp = tid >> 5, lane = tid & 31, bh = blockIdx.x * kPrepWarps + warp;
+    if (bh >= a.B * a.H) return;
+    const int b = bh / a.H, h = bh - b * a.H, L = tree_cached(a, b, false), gran = a.r_k >> 3, pieces = L > 0 ? kSampled * gran : 0;
+    if (lane < kSampled) most[warp][lane] = 0;
+    __syncwarp();
+    for (int i0 = lane; i0 < pieces; i0 += 32 * kAtOnce) {
+      uint4 x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = min(i0 + 32 * k, pieces - 1), s = i / gran;
+        const int64_t at = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h,
+                                      static_cast<int64_t>(L - 1) * s / (kSampled - 1), a.status);
+        x[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.cache_k) + at * a.r_k + 8 * (i - s * gran)));
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        float y[8], m = 0.f;
+        unpack_bf16x8(x[k], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+        atomicMax(&most[warp][min(i0 + 32 * k, pieces - 1) / gran], __float_as_uint(m));
+      }
+    }
+    __syncwarp();
+    const uint32_t m = lane < kSampled ? most[warp][lane] : 0u;
+    int below = 0;
+#pragma unroll
+    for (int k = 0; k < kSampled; ++k) below += most[warp][k] < m || (most[warp][k] == m && k < lane) ? 1 : 0;
+    const int zeros = __popc(__ballot_sync(0xffffffffu, lane < kSampled && m == 0));
+    const bool pick = zeros == kSampled ? lane == 0 : below == zeros + 3 * (kSampled - 1 - zeros) / 4;
+    if (lane < kSampled && pick) a.unit_top[bh] = __uint_as_float(m);
+    return;
+  }
+  const int block = blockIdx.x - sized;
+  if (block < units) {
+    const int bh = block / a.groups, g = block - bh * a.groups;
     const int b = bh / a.H, h = bh - b * a.H;
     int first;
     const int n = tree_nodes(a, b, first, false) - g * a.group;
     if (n <= 0) return;
     first += g * a.group;
-    uint8_t* img = a.qimg + static_cast<int64_t>(blockIdx.x) * a.rows * 512;
-    float* back_q = a.qback + static_cast<int64_t>(blockIdx.x) * a.rows;
+    uint8_t* img = a.qimg + static_cast<int64_t>(block) * a.rows * 512;
+    float* back_q = a.qback + static_cast<int64_t>(block) * a.rows;
     uint8_t* keys = a.khat + (static_cast<int64_t>(bh) * a.max_nodes + g * a.group) * 512;
     float* back_k = a.kback + static_cast<int64_t>(bh) * a.max_nodes + g * a.group;
     for (int i = tid; i < a.rows * 16; i += kPrepThreads) {      // (whole warps: rows is a multiple of 16)
@@ -392,8 +444,8 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     }
     return;
   }
-  if (blockIdx.x < units + a.B) {
-    const int b = blockIdx.x - units;
+  if (block < units + a.B) {
+    const int b = block - units;
     __shared__ int32_t jump[2][kTreeMaxNodes];
     __shared__ uint4 path[2][kTreeMaxNodes];
     int first;
@@ -434,10 +486,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     if (tid < n) a.paths[static_cast<int64_t>(b) * a.max_nodes + tid] = path[cur][tid];
     return;
   }
-  if (blockIdx.x < units + a.B + a.H) {
-    const int h = blockIdx.x - units - a.B;
-    __shared__ float most[kPrepThreads / 32];
-    // the largest sum of a row's |W| and |mu|, two threads a row
+  if (block < units + a.B + a.H) {
+    const int h = block - units - a.B;
+    __shared__ float2 most[kPrepThreads / 32];
+    // the largest sum of a row's |W|, and |mu|, two threads a row
     const int dim = tid >> 1;
     const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + (static_cast<int64_t>(h) * kHeadDim + dim) * a.r_k;
     float sum = 0.f;
@@ -448,9 +500,10 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum += fabsf(x[k]);
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1) + fabsf(__ldg(a.mu_k + h * a.mu_hstride + dim));
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum = warp_max(sum);
-    if ((tid & 31) == 0) most[tid >> 5] = sum;
+    const float mean = warp_max(fabsf(__ldg(a.mu_k + h * a.mu_hstride + dim)));
+    if ((tid & 31) == 0) most[tid >> 5] = make_float2(sum, mean);
     if (tid < kHeadDim) {
       const int src = tid < 64 ? (a.rope_style == 0 ? tid : 2 * tid) : (a.rope_style == 0 ? tid : 2 * (tid - 64) + 1);
       const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
@@ -462,11 +515,9 @@ __global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid
     }
     __syncthreads();
     if (tid == 0) {
-      float top = most[0];
-      for (int k = 1; k < kPrepThreads / 32; ++k) top = fmaxf(top, most[k]);
-      // to 16..32, within what products of these powers with others leave finite
-      const int power = min(60, max(-60, 131 - static_cast<int>(__float_as_uint(top) >> 23)));
-      a.head_scale[h] = make_float2(__int_as_float((127 + power) << 23), __int_as_float((127 - power) << 23));
+      float2 top = most[0];
+      for (int k = 1; k < kPrepThreads / 32; ++k) top = make_float2(fmaxf(top.x, most[k].x), fmaxf(top.y, most[k].y));
+      a.head_top[h] = top;
     }
     return;
   }
@@ -714,7 +765,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
         ++unit;
-        scale = __ldcg(&a.head_scale[w.h]).x;
+        scale = key_scale(a, w.b, w.h).x;
         if (lane == 0) {
           const uint32_t wf = bar(misc->wfull);
           mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
@@ -1112,8 +1163,9 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       const bool fresh = i == 0 || w.t == 0;
       if (fresh && i < count) {
         const float* from = a.qback + (static_cast<int64_t>(w.b * a.H + w.h) * a.groups + w.g) * kRows;
+        const float undo = key_scale(a, w.b, w.h).y;
 #pragma unroll
-        for (int j = 0; j < kMine; ++j) back[j] = (lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f) * __ldcg(&a.head_scale[w.h]).y;
+        for (int j = 0; j < kMine; ++j) back[j] = (lane + 32 * j < kRows ? __ldcg(from + lane + 32 * j) : 1.f) * undo;
       }
       if (i > 0 && (i == count || w.t % kSumTiles == 0)) {
         if (!finish(i - 1, fresh || i == count)) break;
@@ -1674,7 +1726,7 @@ static cudaError_t launch_tiles(const TreeArgs& a, const TreeMaps& maps, cudaStr
 }
 
 cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H * a.groups + a.B + a.H + 1), dim3(kPrepThreads), 0, s, a);
+  const cudaError_t e = launch_pdl(tree_prepare_kernel, dim3(a.B * a.H * a.groups + a.B + (a.B * a.H + kPrepWarps - 1) / kPrepWarps + a.H + 1), dim3(kPrepThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   const cudaError_t t = !a.block_table              ? launch_tiles<0>(a, maps, s)
                         : a.page_size % kTile == 0 ? launch_tiles<1>(a, maps, s)

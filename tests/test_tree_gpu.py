@@ -607,3 +607,28 @@ def test_long_sums(nodes, B, std):
         o = (cached + p[:, L:] * qkv[own, 2 * H + h].double()).cpu().numpy()
         err = np.abs(widen(out[own, h]) - o)
         assert (err <= _half_step(o) + 2.0 ** -13 * np.abs(cached.cpu().numpy())).all()
+
+
+@pytest.mark.parametrize("e", [8, 12, 16, 24, -20])
+@pytest.mark.parametrize("lens,nodes,page", [([1, 2, 5, 0], [1, 3, 2, 4], 0), ([130, 700], [16, 2], 24), ([260, 1], [33, 40], 0), ([140, 90], [128, 65], 64)])
+def test_scale_between_latents_and_weights(lens, nodes, page, e):
+    """The same keys from latents 2^-e as large and weights 2^e as large: the same log-sum-exp."""
+    c = make(lens, nodes, 2, 96, 160, page, 0, "bf16")
+    c["ck"].mul_(2.0 ** -e), c["wk"].mul_(2.0 ** e)
+    check(c, call(c))
+    n = sum(nodes)
+    assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 2e-5
+
+
+@pytest.mark.parametrize("nodes", [2, 40])
+@pytest.mark.parametrize("which,by", [(slice(0, 250), 2.0 ** -14), (slice(0, 12), 0.0), (slice(0, 250), 0.0), (slice(0, 1), 2.0 ** 10),
+                                      (slice(10, 14), 2.0 ** 14)])
+def test_sizes_of_latents_that_differ(which, by, nodes):
+    """Tokens whose latents are far smaller or far larger than the others', or zero."""
+    c = make([400, 300], [nodes, 3], 2, 96, 160, 0, 0, "bf16")
+    c["ck"][:, :, which] *= by
+    if by > 1:      # (their keys small enough in the end that others keep some weight)
+        c["qkv"][:, :2] *= 1.0 / by
+    check(c, call(c))
+    n = nodes + 3
+    assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 2e-5
