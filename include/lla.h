@@ -528,9 +528,10 @@ typedef struct {
  * lla_decode_attn and lla_decode_attn_paged; rope_len >= max(L_max, 128) and past every pos.
  * fp32 arithmetic, or ("tensor" of lla_tree_kernel) matrix instructions on operands that keep 22
  * bits of keys and queries and 16 of weights, with fp32 sums: lse is as exact as fp32 makes it,
- * out within its own rounding.  There the table's rows have to be those of a plain rotation, cos
- * and sin of j theta_f (rows of any scaling; no factor on them), and a sequence with keys 2^11 times
- * above most others' may take a slower way to the same result.  A NaN or an infinity reaches the
+ * out within its own rounding.  There the table's rows have to be cos and sin of j theta_f (those of
+ * any scaling), in both paths times an attention factor if there is one, the same in every row, which
+ * then multiplies queries and keys.  A sequence with keys 2^11 times above most of its others' may
+ * take a slower way to the same result.  A NaN or an infinity reaches the
  * nodes that see it and no others: a cached latent's its sequence's nodes, a node's key and value
  * the nodes below it, a query its own node.  LLA_ERR_UNSUPPORTED: LLA-2D.
  */

@@ -26,7 +26,8 @@
 // Roles: warp 0 copies K and V tiles, warp 1 issues U (and copies W and RoPE rows), warp 2 issues S
 // (and copies Q^), warp 3 issues D; warps 4..11 rotate (two per TMEM lane quadrant, 32 frequencies
 // each, one token per lane), warps 12..15 do the softmax, one token per lane.  cos/sin of a token's
-// angle are the angle sum of the tile's base row (shared memory) and the lane's own row (registers, or TMEM
+// angle are the angle sum of the tile's base row (shared memory, without a factor that the table's rows may
+// have) and the lane's own row (registers, or TMEM
 // for up to 16 nodes: 185 us for 194 at 32 x 4096).  The roles' loops are kept short on purpose: with bodies
 // unrolled all the way, instruction fetch took more time than anything else.
 //
@@ -759,13 +760,17 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     const float* table = lane < 16 ? a.rope_cos + 4 * lane : a.rope_sin + 4 * (lane - 16);
     float4 ahead = make_float4(0.f, 0.f, 0.f, 0.f);
     auto fetch = [&]() { ahead = __ldg(reinterpret_cast<const float4*>(table + static_cast<int64_t>(w.t) * kTile * 64)); };
-    float scale = 1.f;                                // (of the unit's keys, which the base row brings to them)
+    // what the base row is multiplied by: the scale of the unit's keys, and what undoes the factor on the table's rows
+    // (the cosines of row 0), which the lanes' own rows bring once already
+    const float4 on_rows = __ldg(reinterpret_cast<const float4*>(a.rope_cos + 4 * (lane & 15)));
+    float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
         ++unit;
-        scale = key_scale(a, w.b, w.h).x;
+        const float keys = key_scale(a, w.b, w.h).x;
+        scale = make_float4(keys / on_rows.x, keys / on_rows.y, keys / on_rows.z, keys / on_rows.w);
         if (lane == 0) {
           const uint32_t wf = bar(misc->wfull);
           mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
@@ -779,7 +784,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
       if constexpr (kPage == 3) fence_proxy_async_smem();       // (plain copies, read by the products)
       if (i >= 2 && !wait(misc->sfull[i & 1], (i - 2) >> 1)) break;      // S(i - 2) has read the K^ in U(i)'s place
-      reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = make_float4(ahead.x * scale, ahead.y * scale, ahead.z * scale, ahead.w * scale);
+      reinterpret_cast<float4*>(sm + P.base + (i & 1) * 512)[lane] = make_float4(ahead.x * scale.x, ahead.y * scale.y, ahead.z * scale.z, ahead.w * scale.w);
       tc_fence_after();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(misc->ufull[i & 1]));

@@ -632,3 +632,15 @@ def test_sizes_of_latents_that_differ(which, by, nodes):
     check(c, call(c))
     n = nodes + 3
     assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 2e-5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factor", [1.25, 0.1 * np.log(32.0) + 1.0, 0.5])
+@pytest.mark.parametrize("lens,nodes,page,style", [([300, 40], [4, 9], 0, 0), ([520], [50], 64, 1), ([130, 7], [20, 1], 24, 0)])
+def test_tables_with_an_attention_factor(lens, nodes, page, style, factor, dtype):
+    """A factor on the table's rows multiplies queries and keys, cached and drafted, once each."""
+    c = make(lens, nodes, 2, 96, 160, page, style, dtype)
+    c["cos"].mul_(factor), c["sin"].mul_(factor)
+    check(c, call(c))
+    n = sum(nodes)
+    assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 2e-5
