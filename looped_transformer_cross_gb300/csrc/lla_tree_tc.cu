@@ -1335,7 +1335,8 @@ struct JoinPlan {
   int v, s, a, row, bytes;
 };
 constexpr int kJoinRows = 16;           // nodes of a join block
-__host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
+constexpr int kAgainStep = 8;           // cached tokens that join_again takes at a time
+__host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_k, int r_v) {
   constexpr int rows = kJoinRows;
   JoinPlan j{};
   j.keys = (max_nodes + 15) / 16 * 16;
@@ -1344,76 +1345,173 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_v) {
   int off = 0;
   j.v = off;   off += j.keys * (kHeadDim + 8) * 2;
   j.s = off;   off += rows * j.s_pitch * 4;
-  j.a = off;   off += rows * j.a_pitch * 4;
+  j.a = off;   off += rows * j.a_pitch * 4 > kAgainStep * (r_k + r_v) * 2 ? rows * j.a_pitch * 4 : kAgainStep * (r_k + r_v) * 2;
   j.row = off; off += rows * 16;
   j.bytes = off;
   return j;
 }
 
-// The cached tokens of a join block's nodes once more, in fp32 and token by token: for sums that are NaN, which a
-// component of a scaled cached key beyond the range of f16 makes them (and NaN and infinite inputs, whose
-// results stay NaN).  Leaves weights, reference, sums and latent sums as the usual way does.  Eight lanes a row; a
-// thread makes one component of each key.
+// The cached tokens of a join block's nodes once more, in fp32, eight at a time: for sums that are NaN, which a
+// component of a scaled cached key beyond the range of f16 makes them (and NaN and infinities in the cache, whose
+// results stay NaN: it stops once every row's is).  Leaves weights, reference, sums and latent sums as the usual way
+// does, and the keys' values to be read again (their place holds the step's keys).  Keys by warp-level products of the bf16
+// latents and weights (exact, fp32 sums), then eight lanes a row.  One block goes through its whole sequence, 0.75 us a token
+// (rank 96, bound by the latency of a step's few dependent parts: 3653 tokens 2.6 ms, 15393 11.6 ms).
 __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const JoinPlan& J, int b, int h, int first, int row0, int nr, int nk) {
-  __shared__ float u[kHeadDim];
+  constexpr int kStep = kAgainStep, kPitch = kHeadDim + 8;       // (16 rows of values are eight of keys)
+  float* u = reinterpret_cast<float*>(sm + J.v);
   float* ss = reinterpret_cast<float*>(sm + J.s);
   float* sa = reinterpret_cast<float*>(sm + J.a);
-  const int tid = threadIdx.x, r = tid >> 3, x = tid & 7, nk16 = (nk + 15) & ~15;
+  const int tid = threadIdx.x, lane = tid & 31, r = tid >> 3, x = tid & 7, nk16 = (nk + 15) & ~15;
   const int L = tree_cached(a, b, false);
+  // (what the loops need of the arguments, read once: they lie in memory here, which the loops' stores might change)
+  const int H = a.H, r_k = a.r_k, r_v = a.r_v, page_size = a.page_size, max_pages = a.max_pages;
+  const int64_t num_pages = a.num_pages, L_max = a.L_max;
+  const int32_t* block_table = a.block_table;
+  const __nv_bfloat16* cache_k = static_cast<const __nv_bfloat16*>(a.cache_k);
+  const __nv_bfloat16* cache_v = static_cast<const __nv_bfloat16*>(a.cache_v);
+  const float* rope_cos = a.rope_cos;
+  const float* rope_sin = a.rope_sin;
+  uint32_t* status = a.status;
   const int64_t unit = (static_cast<int64_t>(b) * a.H + h) * a.groups + row0 / a.group;
   const int ir = row0 % a.group + r;
-  float q[16];                                        // components 16 x ..
+  float q[16];                                        // components 4 x .. of every 32
   const float back = __ldcg(a.qback + unit * a.rows + ir);
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint8_t* chunk = a.qimg + unit * (a.rows * 512) + (x >> 2) * a.rows * 128 + swizzle_offset(ir * 128 + (x & 3) * 32 + c * 16, 128);
-    const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(chunk)), lo = __ldcg(reinterpret_cast<const uint4*>(chunk + a.rows * 256));
+  for (int c = 0; c < 4; ++c) {
+    const uint8_t* chunk = a.qimg + unit * (a.rows * 512) + (c >> 1) * a.rows * 128 + swizzle_offset(ir * 128 + (c & 1) * 64 + x * 8, 128);
+    const uint2 hi = __ldcg(reinterpret_cast<const uint2*>(chunk)), lo = __ldcg(reinterpret_cast<const uint2*>(chunk + a.rows * 256));
     const __half2* y = reinterpret_cast<const __half2*>(&hi);
     const __half2* z = reinterpret_cast<const __half2*>(&lo);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const float2 v = __half22float2(y[k]), w = __half22float2(z[k]);
-      q[8 * c + 2 * k] = (v.x + w.x) * back;
-      q[8 * c + 2 * k + 1] = (v.y + w.y) * back;
+      q[4 * c + 2 * k] = (v.x + w.x) * back;
+      q[4 * c + 2 * k + 1] = (v.y + w.y) * back;
     }
   }
-  const int src = a.rope_style == 0 ? tid : tid < 64 ? 2 * tid : 2 * (tid - 64) + 1;
-  const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + (static_cast<int64_t>(h) * kHeadDim + src) * a.r_k;
-  const float mu = __ldg(a.mu_k + h * a.mu_hstride + src);
-  float m = -INFINITY, held = 0.f, acc[kMaxRankPerHead / 8];
+  // keys: a warp makes 32 components (8 i + .. of its own), the step's tokens in the first eight rows of its products
+  constexpr int kWarps = kJoinThreads / 32, kTiles = 16 / kWarps;
+  const int g = lane >> 2, k8 = 8 * (lane & 3), e0 = (tid >> 5) * (kHeadDim / kWarps);
+  auto source = [&](int e) { return a.rope_style == 0 ? e : e < 64 ? 2 * e : 2 * (e - 64) + 1; };
+  const __nv_bfloat16* W = static_cast<const __nv_bfloat16*>(a.w_up_k) + static_cast<int64_t>(h) * kHeadDim * r_k + k8;
+  float mu[kTiles][2];
+  int w_row[kTiles];
 #pragma unroll
-  for (int k = 0; k < kMaxRankPerHead / 8; ++k) acc[k] = 0.f;
-  for (int t = 0; t < L; ++t) {
-    const int64_t at = latent_row(a.block_table, a.page_size, a.max_pages, a.num_pages, a.L_max, a.H, b, h, t, a.status);
-    const __nv_bfloat16* ck = static_cast<const __nv_bfloat16*>(a.cache_k) + at * a.r_k;
-    const __nv_bfloat16* cv = static_cast<const __nv_bfloat16*>(a.cache_v) + at * a.r_v;
-    float key = mu;
-    for (int c = 0; c < a.r_k; c += 8) {
-      float y[8], z[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(W + c)), y);
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(ck + c)), z);
+  for (int i = 0; i < kTiles; ++i) {
+    w_row[i] = source(e0 + 8 * i + g) * r_k;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) key = fmaf(y[k], z[k], key);
+    for (int k = 0; k < 2; ++k) mu[i][k] = __ldg(a.mu_k + h * a.mu_hstride + source(e0 + 8 * i + (k8 >> 2) + k));
+  }
+  float m = -INFINITY, held = 0.f, acc[4][8];         // columns 8 x .. of every 64
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+  // a step's latents, K then V of a token, 16 bytes a piece: read one step ahead, and where the latent sums go in the
+  // end (past the sequence's end: the last token, whose weight is then 0)
+  constexpr int kPieces = kStep * 2 * kMaxRankPerHead / 8 / kJoinThreads;
+  const int gk = r_k >> 3, gran = gk + (r_v >> 3);
+  uint4* held_rows = reinterpret_cast<uint4*>(sa);
+  uint4 ahead[kPieces];
+  float turn[kStep];                                  // and cosine and sine of frequency tid mod 64 of every other token
+  auto read = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int i = tid + k * kJoinThreads, t = i / gran, c = i - t * gran;
+      if (t < kStep) {
+        const int64_t at = latent_row(block_table, page_size, max_pages, num_pages, L_max, H, b, h, min(t0 + t, L - 1), status);
+        ahead[k] = __ldg(reinterpret_cast<const uint4*>(c < gk ? cache_k + at * r_k + 8 * c
+                                                               : cache_v + at * r_v + 8 * (c - gk)));
+      }
     }
-    __syncthreads();
-    u[tid] = key;
-    __syncthreads();
-    float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int f = (16 * x + k) & 63;
-      const float c = __ldg(a.rope_cos + static_cast<int64_t>(t) * 64 + f), sn = __ldg(a.rope_sin + static_cast<int64_t>(t) * 64 + f);
-      s = fmaf(q[k], x < 4 ? u[f] * c - u[f + 64] * sn : u[f] * sn + u[f + 64] * c, s);
+    for (int k = 0; k < kStep; k += 2) {
+      const int64_t at = static_cast<int64_t>(min(t0 + k + (tid >> 6), L - 1)) * 64 + (tid & 63);
+      turn[k] = __ldg(rope_cos + at);
+      turn[k + 1] = __ldg(rope_sin + at);
+    }
+  };
+  if (L > 0) read(0);
+  for (int t0 = 0; t0 < L; t0 += kStep) {
+    if (__syncthreads_and(r >= nr || held != held)) break;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+      if (tid + k * kJoinThreads < kStep * gran) held_rows[tid + k * kJoinThreads] = ahead[k];
+    __syncthreads();
+    float key[kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) { key[i][0] = mu[i][0]; key[i][1] = mu[i][1]; key[i][2] = key[i][3] = 0.f; }
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+    for (int c = 0; c < r_k; c += 32) {
+      const bool in = c + k8 < r_k;
+      const uint4 y = in ? held_rows[g * gran + ((c + k8) >> 3)] : none;
+      uint4 w[kTiles];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) w[i] = in ? __ldg(reinterpret_cast<const uint4*>(W + w_row[i] + c)) : none;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) mma_k32(key[i], y, none, w[i]);
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float top = fmaxf(m, s), f = exp2f(m - top), p = exp2f(s - top);
+    for (int i = 0; i < kTiles; ++i) *reinterpret_cast<float2*>(u + g * kPitch + e0 + 8 * i + (k8 >> 2)) = make_float2(key[i][0], key[i][1]);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kStep; k += 2) {
+      float* y = u + (k + (tid >> 6)) * kPitch + (tid & 63);
+      const float x0 = y[0], x1 = y[64];
+      y[0] = x0 * turn[k] - x1 * turn[k + 1];
+      y[64] = x0 * turn[k + 1] + x1 * turn[k];
+    }
+    if (t0 + kStep < L) read(t0 + kStep);
+    __syncthreads();
+    float s[kStep];
+#pragma unroll
+    for (int t = 0; t < kStep; ++t) {
+      s[t] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float4 y = *reinterpret_cast<const float4*>(u + t * kPitch + 32 * c + 4 * x);
+        s[t] = fmaf(q[4 * c], y.x, fmaf(q[4 * c + 1], y.y, fmaf(q[4 * c + 2], y.z, fmaf(q[4 * c + 3], y.w, s[t]))));
+      }
+    }
+    // the eight sums over a row's lanes: half of them go on in half of the lanes, three times; lane x has token x
+    float s4[4], s2[2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s4[t] = (x & 4 ? s[t + 4] : s[t]) + __shfl_xor_sync(0xffffffffu, x & 4 ? s[t] : s[t + 4], 4);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) s2[t] = (x & 2 ? s4[t + 2] : s4[t]) + __shfl_xor_sync(0xffffffffu, x & 2 ? s4[t] : s4[t + 2], 2);
+    float mine = (x & 1 ? s2[1] : s2[0]) + __shfl_xor_sync(0xffffffffu, x & 1 ? s2[0] : s2[1], 1);
+    if (t0 + x >= L) mine = -INFINITY;
+    float top = fmaxf(m, mine);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m - ref), p = t0 + x < L ? exp2f(mine - ref) : 0.f;
+    float sum = p;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     m = top;
-    held = fmaf(held, f, p);
+    held = fmaf(held, f, sum);
 #pragma unroll
-    for (int k = 0; k < kMaxRankPerHead / 8; ++k)
-      if (x + 8 * k < a.r_v) acc[k] = fmaf(acc[k], f, p * __bfloat162float(cv[x + 8 * k]));
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[k][e] *= f;
+#pragma unroll 1
+    for (int t = 0; t < kStep; ++t) {                 // (rolled: a long body waits for its instructions)
+      const float w = __shfl_sync(0xffffffffu, p, (lane & 24) + t);
+      const uint4* from = held_rows + t * gran + gk + x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (64 * k + 8 * x >= r_v) break;
+        float v[8];
+        unpack_bf16x8(from[8 * k], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] = fmaf(w, v[e], acc[k][e]);
+      }
+      __syncwarp();
+    }
   }
+  __syncthreads();                                    // (the last step's latents have been read)
   const bool row = r < nr;
   float top = m, l = 0.f;
   for (int c = x; c < nk && row; c += 8) top = fmaxf(top, ss[r * J.s_pitch + c]);
@@ -1434,10 +1532,12 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const Jo
     if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (top + log2f(l)) * kLn2;
   }
 #pragma unroll
-  for (int k = 0; k < kMaxRankPerHead / 8; ++k) {
-    const int c = x + 8 * k;
+  for (int k = 0; k < 4; ++k) {
+    const int c = 8 * x + 64 * k;
     if (c >= J.a_pitch - 4) break;
-    sa[r * J.a_pitch + c] = row ? acc[k] * f : 0.f;
+    float* to = sa + r * J.a_pitch + c;
+    *reinterpret_cast<float4*>(to) = row ? make_float4(acc[k][0] * f, acc[k][1] * f, acc[k][2] * f, acc[k][3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(to + 4) = row ? make_float4(acc[k][4] * f, acc[k][5] * f, acc[k][6] * f, acc[k][7] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
@@ -1456,7 +1556,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   extern __shared__ uint4 shared[];
   constexpr int kSplit = kJoinThreads / 32, kRows = kJoinRows, kTiles = 16 / kSplit;      // 8-dimension tiles of a warp
   uint8_t* sm = reinterpret_cast<uint8_t*>(shared);
-  const JoinPlan J = join_plan(a.max_nodes, a.r_v);
+  const JoinPlan J = join_plan(a.max_nodes, a.r_k, a.r_v);
   __nv_bfloat16* sv = reinterpret_cast<__nv_bfloat16*>(sm + J.v);
   float* ss = reinterpret_cast<float*>(sm + J.s);
   float* sa = reinterpret_cast<float*>(sm + J.a);
@@ -1471,13 +1571,16 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   // ---- values of the keys; NaN and infinities are left out (0 times them is not 0 for the nodes that do not have
   // the key on their path) and added at the end
   bool odd = false;
-  for (int i = tid; i < nk16 * 16; i += kJoinThreads) {
-    const int r = i >> 4, c = (i & 15) * 8;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < nk) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + (first + r) * a.v_stride + h * kHeadDim + c));
-    odd |= drop_odd(x.x) | drop_odd(x.y) | drop_odd(x.z) | drop_odd(x.w);
-    *reinterpret_cast<uint4*>(sv + r * (kHeadDim + 8) + c) = x;
-  }
+  auto read_values = [&]() {
+    for (int i = tid; i < nk16 * 16; i += kJoinThreads) {
+      const int r = i >> 4, c = (i & 15) * 8;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < nk) x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + (first + r) * a.v_stride + h * kHeadDim + c));
+      odd |= drop_odd(x.x) | drop_odd(x.y) | drop_odd(x.z) | drop_odd(x.w);
+      *reinterpret_cast<uint4*>(sv + r * (kHeadDim + 8) + c) = x;
+    }
+  };
+  read_values();
   // ---- scores of this warp's 16 nodes against every kSplit-th tile of eight keys
   {
     const int64_t unit = static_cast<int64_t>(bh) * a.groups + grp;
@@ -1563,8 +1666,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
       l += __shfl_xor_sync(0xffffffffu, l, o);
       held += __shfl_xor_sync(0xffffffffu, held, o);
     }
+    lost = row && held != held && l == l;             // (where the path's part is NaN, nothing can mend it)
     l += held;
-    lost = row && held != held;
     if (x == 0) {
       srow[r] = make_float4(m, held, row ? 1.f / l : 0.f, 0.f);
       if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (m + log2f(l)) * kLn2;
@@ -1575,6 +1678,8 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const bool again = __syncthreads_or(lost);
   if (again) {
     join_again(a, sm, J, b, h, first, row0, nr, nk);
+    __syncthreads();
+    read_values();
   } else {
 #pragma unroll
     for (int k = 0; k < kTreeMaxNodes / 8; ++k) {
@@ -1740,10 +1845,10 @@ cudaError_t launch_tree_tensor(const TreeArgs& a, const TreeMaps& maps, cudaStre
   if (t != cudaSuccess) return t;
   // (the most any shape takes, at every call)
   const cudaError_t c = cudaFuncSetAttribute(tree_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             join_plan(kTreeMaxNodes, kMaxRankPerHead).bytes);
+                                             join_plan(kTreeMaxNodes, kMaxRankPerHead, kMaxRankPerHead).bytes);
   if (c != cudaSuccess) return c;
   return launch_pdl(tree_join_kernel, dim3(a.B * a.H, (a.max_nodes + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads),
-                    join_plan(a.max_nodes, a.r_v).bytes, s, a);
+                    join_plan(a.max_nodes, a.r_k, a.r_v).bytes, s, a);
 }
 
 }  // namespace lla

@@ -644,3 +644,52 @@ def test_tables_with_an_attention_factor(lens, nodes, page, style, factor, dtype
     check(c, call(c))
     n = sum(nodes)
     assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 2e-5
+
+
+@pytest.mark.parametrize("nodes,page", [(3, 0), (20, 24), (70, 64)])
+def test_keys_beyond_half_precision_in_a_long_cache(nodes, page):
+    """A few of 16389 tokens with keys 2^20 times the others', in one of two sequences; weights that make up the sums
+    from all of them.  A score is off by a share of |q| |k| / sqrt d (22 bits of queries, fp32 keys), which is 2^20 2^-18 = 4
+    times that of ordinary queries and keys, for which 2e-5 stands: 8e-5."""
+    c = make([16389, 300], [nodes, 2], 1, 96, 160, page, 0, "bf16")
+    for t in (5, 4000, 16388):
+        if page:
+            c["ck"][int(c["table"][0, t // page]), :, t % page] *= 2.0 ** 20
+        else:
+            c["ck"][0, :, t] *= 2.0 ** 20
+    c["qkv"][:nodes, 0] *= 2.0 ** -18
+    check(c, call(c))
+    n = nodes + 2
+    assert np.abs(widen(c["lse"])[:n] - want(c)[1][:n]).max() <= 8e-5
+
+
+def test_a_nan_does_not_hold_up_the_step():
+    """A NaN query, or a NaN early in a cache, beside long sequences: its own results are NaN and the call takes about as
+    long as any other (ten times as long would be a walk over the cache)."""
+    c = make([16384, 16384], [20, 9], 2, 96, 160, 0, 0, "bf16")
+    tree = tree_of(c)
+    ws = call(c, tree=tree)
+
+    def took():
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(5):
+            call(c, ws, tree)
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b)
+
+    took()
+    ordinary = took()
+    first = c["out"].clone()
+    c["qkv"][3, 0, 7] = float("nan")
+    assert took() < 10 * ordinary
+    assert torch.isnan(c["out"][3, 0].float()).all()
+    rest = torch.ones(29, 2, dtype=torch.bool)
+    rest[3, 0] = False
+    assert torch.equal(c["out"][:29][rest], first[:29][rest])
+    c["qkv"][3, 0, 7] = 0.0
+    c["ck"][1, 1, 100, 5] = float("nan")
+    assert took() < 10 * ordinary
+    assert torch.isnan(c["out"][20:29, 1].float()).all() and torch.isfinite(c["out"][:20].float()).all()
