@@ -531,7 +531,7 @@ typedef struct {
  * out within its own rounding.  There the table's rows have to be cos and sin of j theta_f (those of
  * any scaling), in both paths times an attention factor if there is one, the same in every row, which
  * then multiplies queries and keys.  A sequence with keys 2^11 times above most of its others' may
- * take a slower way to the same result (0.75 us for each of its cached tokens).  A NaN or an infinity reaches the
+ * take a slower way to the same result (0.9 us for each of its cached tokens).  A NaN or an infinity reaches the
  * nodes that see it and no others: a cached latent's its sequence's nodes, a node's key and value
  * the nodes below it, a query its own node.  LLA_ERR_UNSUPPORTED: LLA-2D.
  */

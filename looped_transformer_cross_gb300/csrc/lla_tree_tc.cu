@@ -179,12 +179,17 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   lo = pack_f16(x0 - h.x, x1 - h.y);
 }
 // x = hi + mid + lo in bf16: 24 bits, all that fp32 has (both lanes).
+__device__ __forceinline__ void less_bf16(uint32_t part, float& x0, float& x1) {       // x minus the part
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tfma.rn.f32.bf16 %0, l, %3, %0;\n\tfma.rn.f32.bf16 %1, h, %3, %1;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "r"(part), "h"(static_cast<unsigned short>(0xBF80)));
+}
 __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16(x0, x1);
-  x0 -= __uint_as_float(hi << 16);
-  x1 -= __uint_as_float(hi & 0xFFFF0000u);
+  less_bf16(hi, x0, x1);
   mid = pack_bf16(x0, x1);
-  lo = pack_bf16(x0 - __uint_as_float(mid << 16), x1 - __uint_as_float(mid & 0xFFFF0000u));
+  less_bf16(mid, x0, x1);
+  lo = pack_bf16(x0, x1);
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -763,6 +768,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // what the base row is multiplied by: the scale of the unit's keys, and what undoes the factor on the table's rows
     // (the cosines of row 0), which the lanes' own rows bring once already
     const float4 on_rows = __ldg(reinterpret_cast<const float4*>(a.rope_cos + 4 * (lane & 15)));
+    const float4 undo = make_float4(__fdividef(1.f, on_rows.x), __fdividef(1.f, on_rows.y), __fdividef(1.f, on_rows.z), __fdividef(1.f, on_rows.w));
     float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
@@ -770,7 +776,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
         ++unit;
         const float keys = key_scale(a, w.b, w.h).x;
-        scale = make_float4(keys / on_rows.x, keys / on_rows.y, keys / on_rows.z, keys / on_rows.w);
+        scale = make_float4(keys * undo.x, keys * undo.y, keys * undo.z, keys * undo.w);
         if (lane == 0) {
           const uint32_t wf = bar(misc->wfull);
           mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
@@ -1353,16 +1359,15 @@ __host__ __device__ inline JoinPlan join_plan(int max_nodes, int r_k, int r_v) {
 
 // The cached tokens of a join block's nodes once more, in fp32, eight at a time: for sums that are NaN, which a
 // component of a scaled cached key beyond the range of f16 makes them (and NaN and infinities in the cache, whose
-// results stay NaN: it stops once every row's is).  Leaves weights, reference, sums and latent sums as the usual way
-// does, and the keys' values to be read again (their place holds the step's keys).  Keys by warp-level products of the bf16
-// latents and weights (exact, fp32 sums), then eight lanes a row.  One block goes through its whole sequence, 0.75 us a token
-// (rank 96, bound by the latency of a step's few dependent parts: 3653 tokens 2.6 ms, 15393 11.6 ms).
-__device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const JoinPlan& J, int b, int h, int first, int row0, int nr, int nk) {
+// results stay NaN: it stops once every row's is).  Leaves them in rec, the block's rows of the unit's first record, as
+// the one record there is, and the keys' values to be read again (their place holds the step's keys).  Keys by warp-level products of the bf16
+// latents and weights (exact, fp32 sums), then eight lanes a row.  One block goes through its whole sequence, 0.9 us a token
+// (rank 96, bound by the latency of the few dependent parts of a step: 3653 tokens 3.2 ms, 15393 14.0 ms).
+__device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, int b, int h, int row0, int nr, float* rec) {
   constexpr int kStep = kAgainStep, kPitch = kHeadDim + 8;       // (16 rows of values are eight of keys)
+  const JoinPlan J = join_plan(a.max_nodes, a.r_k, a.r_v);
   float* u = reinterpret_cast<float*>(sm + J.v);
-  float* ss = reinterpret_cast<float*>(sm + J.s);
-  float* sa = reinterpret_cast<float*>(sm + J.a);
-  const int tid = threadIdx.x, lane = tid & 31, r = tid >> 3, x = tid & 7, nk16 = (nk + 15) & ~15;
+  const int tid = threadIdx.x, lane = tid & 31, r = tid >> 3, x = tid & 7;
   const int L = tree_cached(a, b, false);
   // (what the loops need of the arguments, read once: they lie in memory here, which the loops' stores might change)
   const int H = a.H, r_k = a.r_k, r_v = a.r_v, page_size = a.page_size, max_pages = a.max_pages;
@@ -1412,7 +1417,7 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const Jo
   // end (past the sequence's end: the last token, whose weight is then 0)
   constexpr int kPieces = kStep * 2 * kMaxRankPerHead / 8 / kJoinThreads;
   const int gk = r_k >> 3, gran = gk + (r_v >> 3);
-  uint4* held_rows = reinterpret_cast<uint4*>(sa);
+  uint4* held_rows = reinterpret_cast<uint4*>(sm + J.a);
   uint4 ahead[kPieces];
   float turn[kStep];                                  // and cosine and sine of frequency tid mod 64 of every other token
   auto read = [&](int t0) {
@@ -1511,33 +1516,19 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, const Jo
       __syncwarp();
     }
   }
-  __syncthreads();                                    // (the last step's latents have been read)
-  const bool row = r < nr;
-  float top = m, l = 0.f;
-  for (int c = x; c < nk && row; c += 8) top = fmaxf(top, ss[r * J.s_pitch + c]);
+  if (r < nr) {
+    float* to = rec + static_cast<int64_t>(r) * (r_v + kTreeHead);
+    if (x == 0) {
+      *reinterpret_cast<float4*>(to) = make_float4(m, held, 0.f, 0.f);
+      to[4] = 0.f;
+    }
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  for (int c = x; c < nk16; c += 8) {
-    const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - top) : 0.f;
-    ss[r * J.s_pitch + c] = w;
-    l += w;
-  }
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float f = row ? exp2f(m - top) : 0.f;
-  held *= f;
-  l += held;
-  if (x == 0) {
-    reinterpret_cast<float4*>(sm + J.row)[r] = make_float4(top, held, row ? 1.f / l : 0.f, 0.f);
-    if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (top + log2f(l)) * kLn2;
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = 8 * x + 64 * k;
-    if (c >= J.a_pitch - 4) break;
-    float* to = sa + r * J.a_pitch + c;
-    *reinterpret_cast<float4*>(to) = row ? make_float4(acc[k][0] * f, acc[k][1] * f, acc[k][2] * f, acc[k][3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<float4*>(to + 4) = row ? make_float4(acc[k][4] * f, acc[k][5] * f, acc[k][6] * f, acc[k][7] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < 4; ++k) {
+      const int c = 8 * x + 64 * k;
+      if (c >= r_v) break;
+      *reinterpret_cast<float4*>(to + kTreeHead + c) = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+      *reinterpret_cast<float4*>(to + kTreeHead + c + 4) = make_float4(acc[k][4], acc[k][5], acc[k][6], acc[k][7]);
+    }
   }
 }
 
@@ -1632,62 +1623,67 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const uint32_t total = static_cast<uint32_t>(__ldcg(a.tile_start + a.B)) * a.H;     // (below 2^31)
   const uint32_t share = max(1u, (total + a.grid - 1) / a.grid);
   const uint32_t f0 = t0 * a.H + (h * ng + grp) * nb, c0 = f0 / share;
-  const int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
+  int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
   const int64_t next = static_cast<int64_t>(a.rec_rows) * stride;
-  const float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * a.group) * stride;
-  odd = __syncthreads_or(odd);
-
-  // ---- reference, weights and sums: eight lanes a row
-  bool lost = false;
-  float p[kTreeMaxNodes / 8];
+  float* recs = a.records + (static_cast<int64_t>(bh) * a.groups + grp + c0) * next + (row0 - grp * a.group) * stride;
+  // ---- their references and sums: eight lanes a row
+  float top, held;
+  auto read_records = [&]() {
+    const int r = tid >> 3, x = tid & 7;
+    const float* rec = recs + r * stride;
+    top = -INFINITY;
+    held = 0.f;
+    for (int i = x; i < nrec && r < nr; i += 8) top = fmaxf(top, __ldcg(rec + i * next));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = x; i < nrec && r < nr; i += 8) {
+      const float4 head = __ldcg(reinterpret_cast<const float4*>(rec + i * next));
+      held = fmaf(exp2f(head.x - top), (head.y + head.z) + (head.w + __ldcg(rec + i * next + 4)), held);
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) held += __shfl_xor_sync(0xffffffffu, held, o);
+  };
+  read_records();
+  if (__syncthreads_or(odd || held != held)) {
+    odd = __syncthreads_or(odd);
+    // (a node whose score of itself is NaN has a result that nothing mends)
+    const int r = tid >> 3;
+    const float own = r < nr ? ss[r * J.s_pitch + row0 + r] : 0.f;
+    if (__syncthreads_or(r < nr && held != held && own == own)) {
+      join_again(a, sm, b, h, row0, nr, recs);
+      nrec = 1;
+      __syncthreads();
+      read_values();
+      read_records();
+    }
+  }
+  // ---- reference, weights (over the scores) and sums
   {
     const int r = tid >> 3, x = tid & 7;
     const bool row = r < nr;
-    const float* rec = recs + r * stride;
-    float m = -INFINITY;
+    float m = top;
     for (int c = x; c < nk && row; c += 8) m = fmaxf(m, ss[r * J.s_pitch + c]);
-    for (int i = x; i < nrec && row; i += 8) m = fmaxf(m, __ldcg(rec + i * next));
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f, held = 0.f;
-#pragma unroll
-    for (int k = 0; k < kTreeMaxNodes / 8; ++k) {
-      if (8 * k >= nk16) break;
-      const int c = x + 8 * k;
-      p[k] = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f;
-      l += p[k];
-    }
-    for (int i = x; i < nrec && row; i += 8) {
-      const float4 head = __ldcg(reinterpret_cast<const float4*>(rec + i * next));
-      held = fmaf(exp2f(head.x - m), (head.y + head.z) + (head.w + __ldcg(rec + i * next + 4)), held);
+    float l = 0.f;
+    for (int c = x; c < nk16; c += 8) {
+      const float w = row && c < nk ? exp2f(ss[r * J.s_pitch + c] - m) : 0.f;
+      ss[r * J.s_pitch + c] = w;
+      l += w;
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      held += __shfl_xor_sync(0xffffffffu, held, o);
-    }
-    lost = row && held != held && l == l;             // (where the path's part is NaN, nothing can mend it)
+    for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (nrec > 0) held *= exp2f(top - m);
     l += held;
     if (x == 0) {
       srow[r] = make_float4(m, held, row ? 1.f / l : 0.f, 0.f);
       if (row && a.lse) a.lse[(static_cast<int64_t>(first) + row0 + r) * a.H + h] = (m + log2f(l)) * kLn2;
     }
   }
-  // ---- weights over the scores (which join_again reads); latent sums of the records, relative to M
+  __syncthreads();
+  // ---- latent sums of the records, relative to M
   const int cols = J.a_pitch - 4, per = cols / 4;
-  const bool again = __syncthreads_or(lost);
-  if (again) {
-    join_again(a, sm, J, b, h, first, row0, nr, nk);
-    __syncthreads();
-    read_values();
-  } else {
-#pragma unroll
-    for (int k = 0; k < kTreeMaxNodes / 8; ++k) {
-      if (8 * k >= nk16) break;
-      ss[(tid >> 3) * J.s_pitch + (tid & 7) + 8 * k] = p[k];
-    }
-  }
-  for (int i = tid; i < kRows * per && !again; i += kJoinThreads) {
+  for (int i = tid; i < kRows * per; i += kJoinThreads) {
     const int r = i / per, c = (i - r * per) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < nr && c < a.r_v) {
