@@ -1556,7 +1556,12 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H, row0 = blockIdx.y * kRows, grp = row0 / a.group;
   int first;
   const int n = tree_nodes(a, b, first, false);
-  if (row0 >= n) return;
+  if (row0 >= n) {
+    // (where no block has nodes too, this grid has to end after the tile kernel: the next call waits for it alone
+    // before it writes the plan that the tile kernel reads)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int nr = min(kRows, n - row0), nk = min(n, row0 + kRows), nk16 = (nk + 15) & ~15;
 
   // ---- values of the keys; NaN and infinities are left out (0 times them is not 0 for the nodes that do not have

@@ -693,3 +693,19 @@ def test_a_nan_does_not_hold_up_the_step():
     c["ck"][1, 1, 100, 5] = float("nan")
     assert took() < 10 * ordinary
     assert torch.isnan(c["out"][20:29, 1].float()).all() and torch.isfinite(c["out"][:20].float()).all()
+
+
+def test_calls_without_nodes_between_others():
+    """Steps in which no sequence has nodes, and ordinary ones, in turn over one workspace and without a wait."""
+    c = make([900, 333], [20, 5], 3, 96, 160, 64, 0, "bf16")
+    tree, ws = tree_of(c), None
+    none = lla.DraftTree(torch.zeros(3, dtype=torch.int32, device="cuda"), c["parent"], c["max_nodes"], pos=c["pos"])
+    for _ in range(50):
+        ws = call(c, ws, none)
+        ws = call(c, ws, tree)
+        ws = call(c, ws, none)
+    check(c, ws)
+    c["out"].fill_(77.0), c["lse"].fill_(77.0)
+    call(c, ws, none)
+    assert lla.device_status(ws) == lla.LLA_OK
+    assert (c["out"] == 77.0).all() and (c["lse"] == 77.0).all()
