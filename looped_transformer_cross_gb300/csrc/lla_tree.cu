@@ -585,7 +585,8 @@ TreeWs tree_ws(const lla_dims* d, int B, int max_nodes, int64_t L_max, int sms, 
   w.turned = 256;
   w.v_turned = 256 + static_cast<size_t>(d->H) * d->r_k * kHeadDim * 4;
   w.records = w.v_turned + static_cast<size_t>(d->H) * d->r_v * kHeadDim * 4;
-  w.total = w.records + static_cast<size_t>(units) * w.splits * rec;
+  // (units x splits is at most max(units, 4 sms), a bound that does not fall as the batch grows)
+  w.total = w.records + static_cast<size_t>(std::min(units * tiles, std::max<int64_t>(units, 4 * sms))) * rec;
   return w;
 }
 

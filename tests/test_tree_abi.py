@@ -209,3 +209,23 @@ def test_oracle_logits():
     np.testing.assert_allclose(y[0], [1.0, -2.0 - 0.75 - 0.5, 2.5, 3.0])
     np.testing.assert_allclose(y[1], [0.5, 0.5 - 0.75 - 0.5, -np.inf, -np.inf])
     assert list(best) == [3, 0] and abs(lse[0] - math.log(sum(math.exp(t) for t in y[0]))) < 1e-12
+
+
+@pytest.mark.parametrize("d", [lla.dims(4, 1, 96, 160, dtype=lla.LLA_F32), lla.dims(4, 1, 256, 256), lla.dims(4, 3, 96, 160),
+                               lla.dims(4, 2, 16, 240)])
+def test_sizes_do_not_fall(L, d):
+    """A workspace for a larger batch, cache or tree does for a smaller one."""
+    size = lambda B, N, cap: L.lla_tree_workspace_size(ctypes.byref(d), B, N, cap)  # noqa: E731
+    sizes = [1, 2, 3, 4, 5, 7, 8, 31, 32, 33, 127, 128]
+    lengths = [0, 1, 31, 32, 33, 64, 95, 96, 97, 128, 129, 1000, 4096, 5000]
+    for N in sizes:
+        for cap in lengths:
+            by_batch = [size(B, N, cap) for B in range(1, 40)]
+            assert by_batch == sorted(by_batch)
+    for B in (1, 2, 3, 5, 20):
+        for N in sizes:
+            by_length = [size(B, N, cap) for cap in lengths]
+            assert by_length == sorted(by_length)
+        for cap in lengths:
+            by_nodes = [size(B, N, cap) for N in sizes]
+            assert by_nodes == sorted(by_nodes)
