@@ -646,10 +646,12 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   if (!tree || loop_t < 0 || loop_t >= dims->T || tree->B < 0 || tree->n_tok < 0 || tree->max_nodes < 1 ||
       cache.B != tree->B || cache.L_max < 1)
     return LLA_ERR_INVALID_ARG;
+  // (tiles: of every block of nodes, which the tensor-core kernels count in 32 bits)
+  const int64_t blocks = tensor_path(dims) ? (tree->max_nodes + tree_group(dims->r_v) - 1) / tree_group(dims->r_v) : 1;
   if (tree->max_nodes > kTreeMaxNodes || cache.L_max > (int64_t(1) << 30) ||
       static_cast<int64_t>(tree->B) * dims->H > (int64_t(1) << 24) ||
       static_cast<int64_t>(tree->n_tok) * dims->H >= (int64_t(1) << 31) ||
-      static_cast<int64_t>(tree->B) * dims->H * ((cache.L_max + kTile - 1) / kTile) >= (int64_t(1) << 30))
+      static_cast<int64_t>(tree->B) * dims->H * blocks * ((cache.L_max + kTile - 1) / kTile) >= (int64_t(1) << 30))
     return LLA_ERR_UNSUPPORTED;
   if (tree->B == 0 || tree->n_tok == 0) return LLA_OK;
   if (rope_len < cache.L_max || rope_len < kTile) return LLA_ERR_INVALID_ARG;

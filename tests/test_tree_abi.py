@@ -229,3 +229,16 @@ def test_sizes_do_not_fall(L, d):
         for cap in lengths:
             by_nodes = [size(B, N, cap) for N in sizes]
             assert by_nodes == sorted(by_nodes)
+
+
+@pytest.mark.parametrize("rv,nodes,B,ok", [(192, 128, 32, False), (192, 128, 31, True), (192, 33, 64, False), (160, 128, 64, False),
+                                           (160, 64, 127, True), (160, 1, 128, False)])
+def test_tiles_of_all_blocks_of_nodes_are_counted(L, mem, rv, nodes, B, ok):
+    """2^23 tiles of 128 tokens a sequence and head, through a table that names its pages again and again: once for each
+    block of nodes, 2^30 of them are refused (others here for their workspace)."""
+    d = lla.dims(1, 1, 96, rv)
+    p = mem()
+    tr = lla.Tree(B, 4, nodes, p, p, p)
+    st = L.lla_tree_attn_paged(ctypes.byref(d), 0, ctypes.byref(tr), mem(32768), 128, mem(32768), 128, mem(32768), 128,
+                               lla.PagedCache(p, p, p, B, 1 << 23, 128, 4), p, p, p, p, p, p, p, 1 << 30, p, None, p, 255, None)
+    assert (st == INV) if ok else (st == UNS)
