@@ -520,8 +520,9 @@ typedef struct {
  *   q, k, v   device  [n_tok][H][d] of loop t, before RoPE, storage dtype: element (n, h, e)
  *                     at n*stride + h*d + e (strides in elements, multiples of 16 bytes of
  *                     at least H*d: slices of one fused projection are taken as they are)
- *   out       device  [n_tok][H][d] in the storage dtype, rounded once; no input may overlap it
- *   lse       device  fp32 [n_tok][H] or NULL
+ *   out       device  [n_tok][H][d] in the storage dtype, rounded once
+ *   lse       device  fp32 [n_tok][H] or NULL; no output, the workspace among them, may overlap an
+ *                     input or another output (LLA_ERR_INVALID_ARG)
  *   workspace device  >= lla_tree_workspace_size() bytes (L_max: that of the cache, or
  *                     max_pages * page_size), the first 256 zero
  * cache.B is the tree's B.  seq_lens, w_up, mu, rope tables and the paged cache as for
@@ -564,7 +565,8 @@ lla_status lla_tree_attn_paged(const lla_dims* dims, int loop_t, const lla_tree*
  *   logits      device [n_tok] rows of `vocab` elements, row n at n*row_stride elements; dtype
  *                                      LLA_BF16 or LLA_F32, aligned to an element
  *   out         the same layout with out_stride, rounded once; out == logits with equal strides
- *               is in place, any other overlap LLA_ERR_INVALID_ARG; NULL: not written
+ *               is in place, any other overlap of an output or the workspace with an input or
+ *               another output LLA_ERR_INVALID_ARG; NULL: not written
  *   best        device int32 [n_tok] or NULL: from x before `out` rounds it
  *   lse         device fp32 [n_tok] or NULL; at least one of out, best, lse
  *   workspace   device, >= lla_logits_workspace_size() bytes, the first 256 zero
@@ -609,7 +611,8 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
  *                                        them in node order (every entry has a slot of its own; what
  *                                        lies behind seq_lens is overwritten by the next step)
  *   workspace      device, >= 256 bytes: the status word
- * A negative ctx_lens counts as 0 and records LLA_ERR_DEVICE_ARG.  No output may overlap an input.
+ * A negative ctx_lens counts as 0 and records LLA_ERR_DEVICE_ARG.  No output may overlap an input or
+ * another output (LLA_ERR_INVALID_ARG).
  */
 lla_status lla_tree_accept(const lla_tree* tree, const int32_t* token, const int32_t* chosen,
                            const int32_t* ctx_lens, int32_t* count, int32_t* next_token, int32_t* seq_lens,

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 #include <cstdint>
+#include <initializer_list>
 
 #include "lla_sm103.cuh"
 
@@ -375,6 +376,42 @@ struct FastDiv {
 };
 
 // ----------------------------------------------------------------- host checks
+// A range of memory that a call reads or writes (nullptr or 0 bytes: none), for checks of overlap.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// A product of sizes, none of them negative, that stops at the largest value.
+inline int64_t product(std::initializer_list<int64_t> factors) {
+  int64_t r = 1;
+  for (int64_t f : factors) {
+    if (f == 0) return 0;
+    r = r > INT64_MAX / f ? INT64_MAX : r * f;
+  }
+  return r;
+}
+// n rows of `row` elements, `stride` apart.
+inline int64_t row_bytes(int64_t n, int64_t stride, int64_t row, int64_t elem) {
+  const int64_t before = n > 0 ? product({n - 1, stride}) : 0;
+  return n > 0 ? product({before > INT64_MAX - row ? INT64_MAX : before + row, elem}) : 0;
+}
+inline bool meet(const Span& x, const Span& y) {
+  if (!x.p || !y.p || x.bytes <= 0 || y.bytes <= 0) return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return a < b ? b - a < static_cast<uintptr_t>(x.bytes) : a - b < static_cast<uintptr_t>(y.bytes);
+}
+// Whether an output overlaps an input or another output.
+template <int kOut, int kIn>
+bool outputs_meet(const Span (&out)[kOut], const Span (&in)[kIn]) {
+  for (int o = 0; o < kOut; ++o) {
+    for (const Span& i : in)
+      if (meet(out[o], i)) return true;
+    for (int k = 0; k < o; ++k)
+      if (meet(out[o], out[k])) return true;
+  }
+  return false;
+}
+
 // (lla_api.cu) the checks of dims that every call makes, and the current device's SM count
 lla_status checked_dims(const lla_dims* dims);
 int device_sm_count();

@@ -666,19 +666,24 @@ lla_status tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, con
   for (const void* p : words)
     if (!at4(p)) return LLA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(lse) & 3u) || ws_bytes < 256) return LLA_ERR_INVALID_ARG;
-  // blocks read q, k and v of other nodes while they write out: no overlap
-  const uintptr_t o0 = reinterpret_cast<uintptr_t>(out), o1 = o0 + tree->n_tok * width * es;
-  const void* in[] = {q, k, v};
-  for (int i = 0; i < 3; ++i) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(in[i]);
-    if (p < o1 && o0 < p + ((tree->n_tok - 1) * strides[i] + width) * es) return LLA_ERR_INVALID_ARG;
-  }
   const int sms = device_sm_count();
-  if (sms <= 0) return LLA_ERR_CUDA;
   TreeArgs a{};
   const bool tensor = tensor_path(dims) && make_tree_plan(dims->r_k, dims->r_v, tree_rows(tree->max_nodes, dims->r_v), &a.plan);
-  const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, sms, tensor);
+  const TreeWs w = tree_ws(dims, tree->B, tree->max_nodes, cache.L_max, std::max(1, sms), tensor);
   if (ws_bytes < w.total) return LLA_ERR_INVALID_ARG;
+  // (blocks read what belongs to other nodes while they write)
+  const int64_t n = tree->n_tok, H = dims->H, TH = static_cast<int64_t>(dims->T) * H;
+  const int64_t rows = cache.bt ? product({cache.num_pages, H, cache.page_size}) : product({cache.B, H, cache.L_max});
+  const Span outs[] = {{out, product({n, width, es})}, {lse, product({n, H, 4})}, {workspace, static_cast<int64_t>(w.total)}};
+  const Span ins[] = {{q, row_bytes(n, q_stride, width, es)}, {k, row_bytes(n, k_stride, width, es)}, {v, row_bytes(n, v_stride, width, es)},
+                      {cache.k, product({rows, dims->r_k, es})}, {cache.v, product({rows, dims->r_v, es})},
+                      {w_up_k, product({TH, kHeadDim, dims->r_k, es})}, {w_up_v, product({TH, kHeadDim, dims->r_v, es})},
+                      {mu_k, product({TH, kHeadDim, 4})}, {mu_v, product({TH, kHeadDim, 4})},
+                      {rope_cos, product({rope_len, kHeadDim / 2, 4})}, {rope_sin, product({rope_len, kHeadDim / 2, 4})},
+                      {seq_lens, product({tree->B, 4})}, {tree->tok_start, product({tree->B, 4}) + 4}, {tree->parent, n * 4}, {tree->pos, n * 4},
+                      {cache.bt, product({cache.B, cache.max_pages, 4})}};
+  if (outputs_meet(outs, ins)) return LLA_ERR_INVALID_ARG;
+  if (sms <= 0) return LLA_ERR_CUDA;
   a.B = tree->B;
   a.H = dims->H;
   a.r_k = dims->r_k;

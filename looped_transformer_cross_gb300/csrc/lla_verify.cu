@@ -638,12 +638,6 @@ bool at4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool opt4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 int slices_of(int vocab) { return (vocab + kSlice - 1) / kSlice; }
 
-struct Range { const void* p; int64_t bytes; };
-bool overlap(const Range& x, const Range& y) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-  return x.p && y.p && a < b + y.bytes && b < a + x.bytes;
-}
-
 }  // namespace
 
 extern "C" {
@@ -678,10 +672,20 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
   if (r.n_masks > 0 && (!at4(r.allowed) || !at4(r.allowed_row))) return LLA_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) || ws_bytes < lla_logits_workspace_size(tree->n_tok, vocab))
     return LLA_ERR_INVALID_ARG;
-  if (out && !(out == logits && out_stride == row_stride) &&
-      overlap({logits, static_cast<int64_t>(((tree->n_tok - 1) * row_stride + vocab) * es)},
-              {out, static_cast<int64_t>(((tree->n_tok - 1) * out_stride + vocab) * es)}))
-    return LLA_ERR_INVALID_ARG;
+  const int64_t n = tree->n_tok, B4 = product({tree->B, 4});
+  const bool in_place = out == logits && out_stride == row_stride;
+  const Span outs[] = {{out, row_bytes(n, out_stride, vocab, es)}, {best, n * 4}, {lse, n * 4},
+                       {workspace, static_cast<int64_t>(lla_logits_workspace_size(tree->n_tok, vocab))},
+                       {in_place ? nullptr : logits, row_bytes(n, row_stride, vocab, es)}};      // (no output may lie over it either)
+  const Span ins[] = {{token, n * 4}, {tree->tok_start, B4 + 4}, {tree->parent, n * 4},
+                      {r.max_history > 0 ? r.history : nullptr, product({tree->B, r.max_history, 4})},
+                      {r.max_history > 0 ? r.hist_len : nullptr, B4}, {r.max_history > 0 ? r.prompt_len : nullptr, B4},
+                      {r.repetition, B4}, {r.presence, B4}, {r.frequency, B4},
+                      {r.max_bias > 0 ? r.bias_token : nullptr, product({tree->B, r.max_bias, 4})},
+                      {r.max_bias > 0 ? r.bias : nullptr, product({tree->B, r.max_bias, 4})},
+                      {r.n_masks > 0 ? r.allowed : nullptr, product({r.n_masks, (vocab + 31) / 32, 4})},
+                      {r.n_masks > 0 ? r.allowed_row : nullptr, n * 4}};
+  if (outputs_meet(outs, ins)) return LLA_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LLA_ERR_CUDA;
   LogitArgs a{};
@@ -741,11 +745,9 @@ lla_status lla_tree_accept(const lla_tree* tree, const int32_t* token, const int
     if (tree->n_tok > 0 ? !at4(p) : !opt4(p)) return LLA_ERR_INVALID_ARG;
   // warps read while others write: no output may be an input
   const int64_t b4 = static_cast<int64_t>(tree->B) * 4, t4 = static_cast<int64_t>(tree->n_tok) * 4;
-  const Range in[] = {{tree->tok_start, b4 + 4}, {tree->parent, t4}, {token, t4}, {chosen, t4}, {ctx_lens, b4}};
-  const Range outs[] = {{count, b4}, {next_token, b4}, {seq_lens, b4}, {path, t4}, {seq_idx, t4}, {pos, t4}};
-  for (const Range& o : outs)
-    for (const Range& i : in)
-      if (overlap(o, i)) return LLA_ERR_INVALID_ARG;
+  const Span in[] = {{tree->tok_start, b4 + 4}, {tree->parent, t4}, {token, t4}, {chosen, t4}, {ctx_lens, b4}};
+  const Span outs[] = {{count, b4}, {next_token, b4}, {seq_lens, b4}, {path, t4}, {seq_idx, t4}, {pos, t4}, {workspace, 256}};
+  if (outputs_meet(outs, in)) return LLA_ERR_INVALID_ARG;
   AcceptArgs a{tree->B, tree->n_tok, tree->max_nodes, tree->tok_start, tree->parent, token, chosen, ctx_lens, count,
                next_token, seq_lens, path, seq_idx, pos, static_cast<uint32_t*>(workspace)};
   tree_accept_kernel<<<(tree->B + kAcceptWarps - 1) / kAcceptWarps, 32 * kAcceptWarps, 0, static_cast<cudaStream_t>(stream)>>>(a);

@@ -242,3 +242,77 @@ def test_tiles_of_all_blocks_of_nodes_are_counted(L, mem, rv, nodes, B, ok):
     st = L.lla_tree_attn_paged(ctypes.byref(d), 0, ctypes.byref(tr), mem(32768), 128, mem(32768), 128, mem(32768), 128,
                                lla.PagedCache(p, p, p, B, 1 << 23, 128, 4), p, p, p, p, p, p, p, 1 << 30, p, None, p, 255, None)
     assert (st == INV) if ok else (st == UNS)
+
+
+@pytest.fixture(scope="module")
+def room():
+    """Megabytes of a host buffer, cut into pieces that stand in for device pointers."""
+    buf = (ctypes.c_char * (16 << 20))()
+    base = ctypes.addressof(buf)
+    base += -base % 256
+    yield lambda k: base + k * (1 << 18)
+    del buf
+
+
+def _refuses_overlaps(call, base, outs):
+    """Every output over the start and the inside of every input and of every other output."""
+    for o in outs:
+        for other in (x for x in base if x != o):
+            for off in (0, 4 if other in ("best", "lse", "count", "next", "seq_lens", "path", "seq_idx", "pos_out") else 16):
+                if (o not in ("out", "ws") or off % 16 == 0) and off % 16 in (0, 4):
+                    assert call(**{o: base[other] + off}) == INV, (o, other, off)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_tree_attn_overlaps(L, room, paged):
+    d = lla.dims(2, 2, 16, 32, dtype=lla.LLA_F32)
+    names = ["out", "lse", "ws", "q", "k", "v", "ck", "cv", "wk", "wv", "mk", "mv", "cos", "sin", "lens", "start", "parent", "pos"]
+    base = {n: room(i) for i, n in enumerate(names + ["table"] * paged)}
+
+    def call(**over):
+        a = {n: ctypes.c_void_p(x) for n, x in dict(base, **over).items()}
+        tr = lla.Tree(5, 6, 4, a["start"], a["parent"], a["pos"])
+        head = [ctypes.byref(d), 1, ctypes.byref(tr), a["q"], 256, a["k"], 256, a["v"], 256]
+        tail = [a["lens"], a["wk"], a["wv"], a["mk"], a["mv"], a["cos"], a["sin"], 128, a["out"], a["lse"], a["ws"], 1 << 24, None]
+        if paged:
+            return L.lla_tree_attn_paged(*head, lla.PagedCache(a["ck"], a["cv"], a["table"], 5, 4, 32, 8), *tail)
+        return L.lla_tree_attn(*head, lla.Cache(a["ck"], a["cv"], 5, 128), *tail)
+
+    _refuses_overlaps(call, base, names[:3])
+    # an output whose end lies inside an input
+    assert call(q=base["out"] + 6 * 256 * 4 - 16) == INV and call(lens=base["lse"] + 6 * 2 * 4 - 4) == INV
+
+
+def test_logits_overlaps(L, room):
+    names = ["out", "best", "lse", "ws", "logits", "token", "start", "parent", "history", "hist_len", "prompt_len", "rep", "pres", "freq",
+             "bias_token", "bias", "allowed", "allowed_row"]
+    base = {n: room(i) for i, n in enumerate(names)}
+
+    def call(**over):
+        a = {n: ctypes.c_void_p(x) for n, x in dict(base, **over).items()}
+        tr = lla.Tree(5, 6, 4, a["start"], a["parent"], None)
+        r = lla.LogitRulesC(a["history"], a["hist_len"], a["prompt_len"], 9, a["rep"], a["pres"], a["freq"], a["bias_token"], a["bias"], 6,
+                            a["allowed"], a["allowed_row"], 3)
+        return L.lla_logits_adjust(ctypes.byref(tr), a["token"], lla.LLA_F32, a["logits"], 1000, 1000, ctypes.byref(r), a["out"], 1000,
+                                   a["best"], a["lse"], a["ws"], 1 << 20, None)
+
+    base_of = {n: x for n, x in base.items() if n != "logits"}
+    _refuses_overlaps(call, base_of, names[:4])
+    for o in names[1:4]:
+        assert call(**{o: base["logits"] + 48}) == INV
+    assert call(out=base["logits"] + 16) == INV and call(token=base["out"] + 24000 - 4) == INV
+    # in place it is an input and an output, which nothing else may lie over
+    assert call(out=base["logits"], best=base["logits"] + 48) == INV
+
+
+def test_accept_overlaps(L, room):
+    names = ["count", "next", "seq_lens", "path", "seq_idx", "pos_out", "ws", "start", "parent", "token", "chosen", "ctx"]
+    base = {n: room(i) for i, n in enumerate(names)}
+
+    def call(**over):
+        a = {n: ctypes.c_void_p(x) for n, x in dict(base, **over).items()}
+        tr = lla.Tree(5, 6, 4, a["start"], a["parent"], None)
+        return L.lla_tree_accept(ctypes.byref(tr), a["token"], a["chosen"], a["ctx"], a["count"], a["next"], a["seq_lens"], a["path"],
+                                 a["seq_idx"], a["pos_out"], a["ws"], 256, None)
+
+    _refuses_overlaps(call, base, names[:7])
