@@ -609,7 +609,10 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
  *   seq_idx, pos   device int32 [n_tok]  out: as lla_encode takes them: accepted nodes go to slots
  *                                        ctx_lens .. seq_lens-1 in path order, the others behind
  *                                        them in node order (every entry has a slot of its own; what
- *                                        lies behind seq_lens is overwritten by the next step)
+ *                                        lies behind seq_lens is overwritten by the next step).
+ *                                        Entries of no sequence keep what they held, a call before
+ *                                        perhaps: where all n_tok go to lla_encode, set seq_idx to -1
+ *                                        first (it skips and flags those, as lla_page_plan's)
  *   workspace      device, >= 256 bytes: the status word
  * A negative ctx_lens counts as 0 and records LLA_ERR_DEVICE_ARG.  No output may overlap an input or
  * another output (LLA_ERR_INVALID_ARG).

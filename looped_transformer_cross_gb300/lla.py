@@ -803,18 +803,29 @@ class TreeAccept:
     """Output arrays and status word of lla_tree_accept for ``tree``; calling it walks down the tree.
 
     ``count``, ``next_token``, ``seq_lens`` [B], ``path``, ``seq_idx``, ``pos`` [n_tok] (int32; the
-    last two as lla_encode takes them)."""
+    last two as lla_encode takes them, which skips entries of -1).
 
-    def __init__(self, tree: DraftTree):
+    Entries of no sequence (behind tok_start[B], or of a sequence that does not fit) are -1 at first, and a call leaves
+    them as they are: after one with more nodes they name its slots.  With ``clear`` every call sets them to -1 before it
+    walks, as a step needs that hands all n_tok entries on and whose number of nodes varies (a captured one)."""
+
+    def __init__(self, tree: DraftTree, clear: bool = False):
         i32 = dict(dtype=torch.int32, device=tree.tok_start.device)
-        self.tree = tree
+        self.tree, self.clear = tree, bool(clear)
         self.count, self.next_token, self.seq_lens = (torch.empty(tree.B, **i32) for _ in range(3))
-        self.path, self.seq_idx, self.pos = (torch.empty(tree.n_tok, **i32) for _ in range(3))
+        self._entries = torch.full((3, (tree.n_tok + 63) // 64 * 64), -1, **i32)        # (rows on 256 bytes)
+        self.path, self.seq_idx, self.pos = self._entries[:, :tree.n_tok].unbind()
         self.workspace = torch.zeros(256, dtype=torch.uint8, device=tree.tok_start.device)
 
     def __call__(self, token, chosen, ctx_lens, stream=None):
         t, i32 = self.tree, torch.int32
         one = (t.n_tok,)
+        if self.clear:
+            if stream is None:
+                self._entries.fill_(-1)
+            else:
+                with torch.cuda.stream(stream):
+                    self._entries.fill_(-1)
         _run("lla_tree_accept", lib().lla_tree_accept, t.dev, stream, t.ref, _arg("token", token, i32, t.dev, one),
              _arg("chosen", chosen, i32, t.dev, one), _arg("ctx_lens", ctx_lens, i32, t.dev, (t.B,)),
              self.count.data_ptr(), self.next_token.data_ptr(), self.seq_lens.data_ptr(), self.path.data_ptr(),

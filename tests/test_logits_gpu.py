@@ -413,3 +413,50 @@ def test_a_verification_step(page):
     c["tok_start"], c["parent"], c["pos"] = i32([0, 1, 2]), i32([-1, -1]), walk.seq_lens.clone()
     c["qkv"], c["out"], c["lse"] = c["qkv"][:2].contiguous(), c["out"][:2].contiguous(), c["lse"][:2].contiguous()
     tg.check(c, tg.call(c))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_all_entries_of_a_step_go_to_encode(captured, own_stream):
+    """Steps of fewer and fewer nodes over the same arrays, all entries handed on to lla_encode: only the slots of the
+    step's own nodes are written, though the host never knows how many there are."""
+    import test_tree_gpu as tg
+    c = tg.make([20, 9], [6, 5], 2, 16, 16, 0, 0, "bf16", cap=60, pad=4)
+    tree, n_tok, T = tg.tree_of(c), c["parent"].shape[0], 2
+    dirty = [torch.zeros(n_tok, dtype=torch.int32, device="cuda") for _ in range(8)]
+    del dirty                                        # (memory that new tensors take over holds zeros, a slot)
+    walk = lla.TreeAccept(tree, clear=True)
+    assert (walk.seq_idx == -1).all() and (lla.TreeAccept(tree).seq_idx == -1).all()
+    g = torch.Generator().manual_seed(3)
+    x = [torch.randn(n_tok, 2, T * 128, generator=g).bfloat16().cuda() for _ in range(2)]
+    wd = [torch.randn(2, T * 128, 16, generator=g).div(16).bfloat16().cuda() for _ in range(2)]
+    token, chosen = (torch.zeros(n_tok, dtype=torch.int32, device="cuda") for _ in range(2))
+    ctx, ws = c["seq_lens"].clone(), lla.make_workspace(c["dm"], 2, 60, n_tok)
+    stream = torch.cuda.Stream() if own_stream else None
+    torch.cuda.synchronize()
+
+    def step(s):
+        walk(token, chosen, ctx, stream=s)
+        lla.encode(c["dm"], *x, walk.seq_idx, walk.pos, *wd, c["mk"], c["mv"], c["ck"], c["cv"], ws, stream=s)
+
+    graph = None
+    if captured:
+        step(stream)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(None)
+    for sizes in ([6, 5], [2, 3], [0, 1], [0, 0], [1, 0]):
+        tree.tok_start.copy_(i32([0, sizes[0], sum(sizes)]))
+        c["ck"].fill_(float("nan")), c["cv"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        if graph is not None:
+            graph.replay()
+        else:
+            step(stream)
+        torch.cuda.synchronize()
+        for b, L in enumerate(ctx.tolist()):
+            there = torch.isfinite(c["ck"][b, 0, :, 0].float()).nonzero().flatten().tolist()
+            assert there == list(range(L, L + sizes[b]))
+    for part in (walk.path, walk.seq_idx, walk.pos):
+        assert (part[1:] == -1).all()
