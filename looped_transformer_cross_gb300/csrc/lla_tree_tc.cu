@@ -346,7 +346,7 @@ __device__ __forceinline__ void turn_pairs8(const float (&x0)[8], const float (&
 // blocks: mu of a head as an operand that ones multiply, in three bf16 parts (24 bits), and the largest row sum of
 // |W_up,k| and |mu|.  The last
 // block: tiles per sequence, and every CTA's first tile.
-__global__ void __launch_bounds__(kPrepThreads) tree_prepare_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, 5) tree_prepare_kernel(const __grid_constant__ TreeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
@@ -775,8 +775,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
       if (i == 0 || w.t == 0) {
         if (unit >= 0 && !wait(misc->wfree, unit)) break;
         ++unit;
-        const float keys = key_scale(a, w.b, w.h).x;
-        scale = make_float4(keys * undo.x, keys * undo.y, keys * undo.z, keys * undo.w);
         if (lane == 0) {
           const uint32_t wf = bar(misc->wfull);
           mbar_arrive_expect_tx(wf, P.kplan.bytes + 4096);
@@ -785,6 +783,8 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
           bulk_load(sbase + P.mu, a.bias + static_cast<int64_t>(w.h) * 4096, 4096, wf);
         }
         __syncwarp();
+        const float keys = key_scale(a, w.b, w.h).x;  // (with the copies under way)
+        scale = make_float4(keys * undo.x, keys * undo.y, keys * undo.z, keys * undo.w);
         if (!wait(misc->wfull, unit)) break;
       }
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
