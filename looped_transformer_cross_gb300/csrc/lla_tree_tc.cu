@@ -359,7 +359,9 @@ __global__ void __launch_bounds__(kPrepThreads, 5) tree_prepare_kernel(const __g
     __shared__ uint32_t most[kPrepWarps][kSampled];
     const int warp = tid >> 5, lane = tid & 31, bh = blockIdx.x * kPrepWarps + warp;
     if (bh >= a.B * a.H) return;
-    const int b = bh / a.H, h = bh - b * a.H, L = tree_cached(a, b, false), gran = a.r_k >> 3, pieces = L > 0 ? kSampled * gran : 0;
+    int first;
+    const int b = bh / a.H, h = bh - b * a.H, L = tree_cached(a, b, false), gran = a.r_k >> 3;
+    const int pieces = L > 0 && tree_nodes(a, b, first, false) > 0 ? kSampled * gran : 0;    // (none of a sequence without nodes is read)
     if (lane < kSampled) most[warp][lane] = 0;
     __syncwarp();
     for (int i0 = lane; i0 < pieces; i0 += 32 * kAtOnce) {

@@ -709,3 +709,11 @@ def test_calls_without_nodes_between_others():
     call(c, ws, none)
     assert lla.device_status(ws) == lla.LLA_OK
     assert (c["out"] == 77.0).all() and (c["lse"] == 77.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_caches_of_sequences_without_nodes_are_left_alone(dtype):
+    """A sequence without nodes may have a table that names no pages: nothing of it is read, and nothing recorded."""
+    c = make([200, 300, 0], [5, 0, 2], 2, 96, 160, 64, 0, dtype)
+    c["table"][1].fill_(-1)
+    check(c, call(c))
