@@ -717,3 +717,43 @@ def test_caches_of_sequences_without_nodes_are_left_alone(dtype):
     c = make([200, 300, 0], [5, 0, 2], 2, 96, 160, 64, 0, dtype)
     c["table"][1].fill_(-1)
     check(c, call(c))
+
+
+@pytest.mark.parametrize("nodes", [3, 24, 64, 100])
+def test_scores_that_rise_in_long_sums(nodes):
+    """20000 cached tokens whose keys grow along the cache, a unit's in one block: references move after sums have left
+    the accumulators.  Queries 12 times as large: the log-sum-exp to 12 x 2e-5; a weight is then off by 2^-11 at most, and an
+    output by that share of its values beside half a step."""
+    H, L, rk, rv, B = 16, 20000, 16, 32, 10
+    g = torch.Generator(device="cuda").manual_seed(nodes)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dm, n = lla.dims(1, H, rk, rv), B * nodes
+    qkv = rnd(n, 3 * H, D).bfloat16()
+    qkv[:, :H] *= 12.0
+    qkv[:, H:2 * H] *= 0.1
+    size = torch.full((L, 1), 1.0, device="cuda")
+    size[:8192], size[8192:9000], size[9000:16384] = 0.02, 0.3, 0.1
+    ck, cv = (rnd(B, H, L, rk) * size).bfloat16(), (1 + 0.1 * rnd(B, H, L, rv)).bfloat16()
+    wk, wv = (rnd(1, H, D, rk) / 4).bfloat16(), (rnd(1, H, D, rv).abs() / 6).bfloat16()
+    zero = torch.zeros(H, D, device="cuda")
+    ang = torch.arange(L + 1, dtype=torch.float64, device="cuda")[:, None] * 10000.0 ** (-2.0 * torch.arange(64, dtype=torch.float64, device="cuda") / D)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    lens = [L, 9000, 8192, 8193, 16384, 12000, L, L, L, L]
+    tree = lla.DraftTree(i32([nodes * b for b in range(B + 1)]), i32([-1] * n), nodes, pos=i32([x for x in lens for _ in range(nodes)]))
+    out, lse = torch.zeros(n, H, D, device="cuda", dtype=torch.bfloat16), torch.zeros(n, H, device="cuda")
+    ws = lla.tree_workspace(dm, tree, L)
+    lla.tree_attn(dm, 0, tree, qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:], ck, cv, i32(lens), wk, wv, zero, zero, cos, sin, out, lse, ws)
+    assert lla.device_status(ws) == lla.LLA_OK
+    turn = lambda x, at: torch.cat((x[..., :64] * cos[at].double() - x[..., 64:] * sin[at].double(),  # noqa: E731
+                                    x[..., :64] * sin[at].double() + x[..., 64:] * cos[at].double()), -1)
+    for b, h in ((0, 0), (1, 3), (2, 5), (3, 9), (4, 2), (5, 7), (9, 15)):
+        own, m = slice(b * nodes, (b + 1) * nodes), lens[b]
+        q, kd = turn(qkv[own, h].double(), m), turn(qkv[own, H + h].double(), m)
+        k = turn(ck[b, h, :m].double() @ wk[0, h].double().T, slice(0, m))
+        s = torch.cat((q @ k.T, (q * kd).sum(-1, keepdim=True)), -1) / D ** 0.5
+        assert (lse[own, h].double() - torch.logsumexp(s, -1)).abs().max() <= 12 * 2e-5
+        p = torch.softmax(s, -1)
+        o = ((p[:, :m] @ cv[b, h, :m].double()) @ wv[0, h].double().T + p[:, m:] * qkv[own, 2 * H + h].double()).cpu().numpy()
+        err = np.abs(widen(out[own, h]) - o)
+        assert (err <= _half_step(o) + 2.0 ** -11 * np.abs(o).max() + 2.0 ** -13 * np.abs(o)).all()
