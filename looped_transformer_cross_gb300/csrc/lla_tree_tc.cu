@@ -28,13 +28,14 @@
 // each, one token per lane), warps 12..15 do the softmax, one token per lane.  cos/sin of a token's
 // angle are the angle sum of the tile's base row (shared memory, without a factor that the table's rows may
 // have) and the lane's own row (registers, or TMEM
-// for up to 16 nodes: 185 us for 194 at 32 x 4096).  The roles' loops are kept short on purpose: with bodies
+// for up to 16 nodes: 5 % of the call at 32 x 4096; those kernels do not spill, those for 32 nodes 104 bytes a
+// thread, those for 64 48).  The roles' loops are kept short on purpose: with bodies
 // unrolled all the way, instruction fetch took more time than anything else.
 //
 // Measured (the whole call, 16 heads; bytes of the latents over the time): 32 x 4096 tokens at (96, 160) with up to
-// 16 nodes 184 us, 5.5 TB/s of the 6.8 that a copy reaches; 8 x 16384 in 64-token pages with up to 64 nodes 241 us,
-// 4.3 TB/s, where the softmax warps and 2,900 cycles of products a tile bound it; 128 x 4096 at (16, 32) with up to 8
-// nodes 445 us, 1.4 TB/s: a tile's fixed part, 2,600 cycles, most of them the rotation's.
+// 16 nodes 187 us, 5.4 TB/s of the 6.8 that a copy reaches; 8 x 16384 in 64-token pages with up to 64 nodes 265 us,
+// 3.9 TB/s, where the softmax warps and 2,900 cycles of products a tile bound it; 128 x 4096 at (16, 32) with up to 8
+// nodes 455 us, 1.4 TB/s: a tile's fixed part, 2,600 cycles, most of them the rotation's.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -53,7 +54,8 @@ constexpr float kInvSqrtD = 0.08838834764831845f;   // 1/sqrt(128)
 constexpr float kHeadroom = 32.f;                   // a score this far above its reference (log2 units) moves it
 // The tensor core cuts its sums off at 24 bits: up to 2^-23 of a sum is lost with every 16 tokens, always downwards
 // (65536 tokens in one sum: log-sum-exp 1e-4 off, outputs 5e-4).  So a unit's latent sums go to its record, and
-// start anew, every 64 tiles (512 steps, 2^-14 at most), and the sums of weights of 64 nodes to a register every 8.
+// start anew, every 64 tiles (512 steps, 2^-14 at most), and the sums of weights of 64 nodes to shared memory every 8
+// (8 x 16384 with 64 nodes: 8 us of 259).
 constexpr int kSumTiles = 64, kWeightTiles = 8;
 constexpr int kPrepThreads = 256, kPrepWarps = kPrepThreads / 32;
 constexpr int kRotWarps = 8;
@@ -279,7 +281,7 @@ __device__ __forceinline__ void gather_tile(const void* pool, int r, const int64
   const uint32_t mask = k.row == 128 ? 7u : k.row == 64 ? 3u : 1u, shift = k.row == 128 ? 0u : k.row == 64 ? 1u : 2u;
   const uint8_t* from = static_cast<const uint8_t*>(pool) + 16 * g;
   // (steps without a branch between them, so that their shuffles overlap; eight where a step is a few rows: 32 x 4096
-  // tokens one a page 864 us, 1148 with a branch, 1395 two at a time; at the small ranks four, 1342 and 1473)
+  // tokens one a page 864 us, 1148 with a branch, 1395 two at a time; at the small ranks four, 1342 and 1473; both with what else there was then)
   auto steps = [&](auto most) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -770,7 +772,6 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
     // what the base row is multiplied by: the scale of the unit's keys, and what undoes the factor on the table's rows
     // (the cosines of row 0), which the lanes' own rows bring once already
     const float4 on_rows = __ldg(reinterpret_cast<const float4*>(a.rope_cos + 4 * (lane & 15)));
-    const float4 undo = make_float4(__fdividef(1.f, on_rows.x), __fdividef(1.f, on_rows.y), __fdividef(1.f, on_rows.z), __fdividef(1.f, on_rows.w));
     float4 scale = make_float4(1.f, 1.f, 1.f, 1.f);
     if (count > 0) fetch();
     for (int i = 0; i < count; ++i) {
@@ -786,7 +787,7 @@ tree_tile_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ Tre
         }
         __syncwarp();
         const float keys = key_scale(a, w.b, w.h).x;  // (with the copies under way)
-        scale = make_float4(keys * undo.x, keys * undo.y, keys * undo.z, keys * undo.w);
+        scale = make_float4(__fdividef(keys, on_rows.x), __fdividef(keys, on_rows.y), __fdividef(keys, on_rows.z), __fdividef(keys, on_rows.w));
         if (!wait(misc->wfull, unit)) break;
       }
       if (!wait(misc->kfull[kr.slot], kr.phase)) break;
@@ -1540,11 +1541,11 @@ __device__ __noinline__ void join_again(const TreeArgs& a, uint8_t* sm, int b, i
 //   out = (A W_up,v^T + P V + held mu_v) / l
 // by warp-level products whose operands come straight from global memory (L2) where they are read
 // along K (Q^ and K^ in two f16 parts; P and A as the three bf16 parts that hold an fp32 value, split where a
-// product takes them: with two parts, 16 bits, one output in 500 took the other neighbour in its rounding).  Bound by the latency of its few steps; blocks are
-// small so that many run at a time: 16 us for 512 blocks, 65 for 2048 with 128 keys (80 registers and six blocks an
+// product takes them: with two parts, 16 bits, one output in 500 took the other neighbour in its rounding).  Bound by
+// the latency of its few steps; blocks are small so that many run at a time: 17 us for 512 blocks, 75 for 2048 with 128 keys (of which the third parts 7) (80 registers and six blocks an
 // SM instead of four, with half of the values held at a time: no faster).  The
 // scores need nothing of the tile kernel, so they are made before the wait for it (its blocks let this
-// grid start only once they have seen the preparation complete).
+// grid start only once they have seen the preparation complete, and leave room for it as they end).
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeArgs a) {
   extern __shared__ uint4 shared[];
   constexpr int kSplit = kJoinThreads / 32, kRows = kJoinRows, kTiles = 16 / kSplit;      // 8-dimension tiles of a warp
@@ -1627,7 +1628,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int ng = (n + a.group - 1) / a.group, stride = a.r_v + kTreeHead;
   const uint32_t t0 = __ldcg(a.tile_start + b), nb = (__ldcg(a.tile_start + b + 1) - t0) / ng;
-  const uint32_t total = static_cast<uint32_t>(__ldcg(a.tile_start + a.B)) * a.H;     // (below 2^31)
+  const uint32_t total = static_cast<uint32_t>(__ldcg(a.tile_start + a.B)) * a.H;     // (below 2^30)
   const uint32_t share = max(1u, (total + a.grid - 1) / a.grid);
   const uint32_t f0 = t0 * a.H + (h * ng + grp) * nb, c0 = f0 / share;
   int nrec = nb > 0 ? static_cast<int>((f0 + nb - 1) / share + 1 - c0) : 0;
