@@ -528,13 +528,15 @@ typedef struct {
  * cache.B is the tree's B.  seq_lens, w_up, mu, rope tables and the paged cache as for
  * lla_decode_attn and lla_decode_attn_paged; rope_len >= max(L_max, 128) and past every pos.
  * fp32 arithmetic, or ("tensor" of lla_tree_kernel) matrix instructions on operands that keep 22
- * bits of keys and queries and 16 of weights, with fp32 sums: lse is as exact as fp32 makes it,
- * out within its own rounding.  There the table's rows have to be cos and sin of j theta_f (those of
- * any scaling), in both paths times an attention factor if there is one, the same in every row, which
- * then multiplies queries and keys.  A sequence with keys 2^11 times above most of its others' may
- * take a slower way to the same result (0.9 us for each of its cached tokens).  A NaN or an infinity reaches the
- * nodes that see it and no others: a cached latent's its sequence's nodes, a node's key and value
- * the nodes below it, a query its own node.  LLA_ERR_UNSUPPORTED: LLA-2D.
+ * bits of keys and queries, 16 of the cached tokens' weights and 24 of the drafted ones' and of the
+ * latent sums, with fp32 sums: lse is off by some 2^-20 of |q| |k| / sqrt(d) (2e-5 at most for scores
+ * of ordinary size, at any length), out by its own rounding and 2^-13 of a sum of its terms' sizes.
+ * There the table's rows have to be cos and sin of j theta_f (those of any scaling), in both paths
+ * times an attention factor if there is one, the same in every row, which then multiplies queries
+ * and keys.  A sequence with keys 2^11 times above most of its others' may take a slower way to the
+ * same result (0.9 us for each of its cached tokens).  A NaN or an infinity reaches the nodes that
+ * see it and no others: a cached latent's its sequence's nodes, a node's key and value the nodes
+ * below it, a query its own node.  LLA_ERR_UNSUPPORTED: LLA-2D.
  */
 size_t lla_tree_workspace_size(const lla_dims* dims, int B, int max_nodes, int64_t L_max);
 lla_status lla_tree_attn(const lla_dims* dims, int loop_t, const lla_tree* tree, const void* q, int64_t q_stride,
@@ -678,9 +680,10 @@ const char* lla_decode_kernel(const lla_dims* dims);
 const char* lla_decoupled_kernel(const lla_dims* dims, int d_rope);
 
 /* Name of the kernel family lla_tree_attn (page_size 0) or lla_tree_attn_paged runs for
- * `dims` (host-only, no launch), the same for every page size: "tensor" (LLA_BF16 whose operands
- * fit in shared memory: r_k up to 208 with any r_v, larger ones with smaller r_v), "plain" (others: fp32
- * arithmetic, not tuned for bf16), or NULL for invalid or unsupported dims (LLA_2D). */
+ * `dims` (host-only, no launch), the same for every page size and number of nodes: "tensor" (LLA_BF16
+ * whose operands fit in shared memory beside the largest block of nodes, 64 for r_v up to 176 and 32
+ * above: r_k up to 208 with any r_v; r_k 224 but for r_v 176, 240 and 256; r_k 240 with r_v up to 128
+ * or 192; r_k 256 with r_v up to 96), "plain" (others: fp32 arithmetic, not tuned for bf16), or NULL for invalid or unsupported dims (LLA_2D). */
 const char* lla_tree_kernel(const lla_dims* dims, int page_size);
 
 /* Workspace bytes for calls with at most B sequences of L_max slots and
