@@ -675,9 +675,8 @@ lla_status lla_logits_adjust(const lla_tree* tree, const int32_t* token, int dty
   const int64_t n = tree->n_tok, B4 = product({tree->B, 4});
   const bool in_place = out == logits && out_stride == row_stride;
   const Span outs[] = {{out, row_bytes(n, out_stride, vocab, es)}, {best, n * 4}, {lse, n * 4},
-                       {workspace, static_cast<int64_t>(lla_logits_workspace_size(tree->n_tok, vocab))},
-                       {in_place ? nullptr : logits, row_bytes(n, row_stride, vocab, es)}};      // (no output may lie over it either)
-  const Span ins[] = {{token, n * 4}, {tree->tok_start, B4 + 4}, {tree->parent, n * 4},
+                       {workspace, static_cast<int64_t>(lla_logits_workspace_size(tree->n_tok, vocab))}};
+  const Span ins[] = {{in_place ? nullptr : logits, row_bytes(n, row_stride, vocab, es)}, {token, n * 4}, {tree->tok_start, B4 + 4}, {tree->parent, n * 4},
                       {r.max_history > 0 ? r.history : nullptr, product({tree->B, r.max_history, 4})},
                       {r.max_history > 0 ? r.hist_len : nullptr, B4}, {r.max_history > 0 ? r.prompt_len : nullptr, B4},
                       {r.repetition, B4}, {r.presence, B4}, {r.frequency, B4},
